@@ -175,6 +175,35 @@ int attn_fwd_masked(const void* q, const void* k, const void* v, void* out, floa
                     int Nq, int Nk, int D, float scale, int causal, int dtype, void* stream);
 
 /*
+ * Forward with a sliding window and sinks: causal attention in which each query
+ * sees the last `window` positions up to its own and, wherever it stands, the
+ * first `sinks` positions.  The Nq queries are the last Nq positions of the Nk
+ * (query i stands at position p = i + Nk - Nq; Nq <= Nk), and key j is visible
+ * when j <= p and (j > p - window or j < sinks).  window >= 1 (a query always
+ * sees itself) and sinks >= 0; either may exceed Nk.  The forward never
+ * loads the key tiles between the sinks and a window, so its cost grows with
+ * window + sinks instead of Nk.  lse is over the visible keys.  (The pages
+ * have no counterpart; "Other areas where this could be useful" patches every
+ * SDPA call, and long-context models call it with such masks.)
+ *
+ * workspace: attn_fwd_window_workspace_size() bytes, 16-byte aligned (may be
+ * NULL when that is 0): the fp16 copy of v that attn_fwd_ws also makes (bf16,
+ * Nq > 256; only its visible tiles), and the partial results of a grid under
+ * one wave, whose key tiles are cut into ranges and merged like
+ * attn_fwd_splitkv's.  Other arguments, layouts and errors are attn_fwd's.
+ * Like the causal forwards it multiplies hidden keys' values by zero, so a
+ * value tile that holds an infinity or NaN spoils the rows that meet it.
+ */
+int attn_fwd_window(const void* q, const void* k, const void* v, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq,
+                    int Nk, int D, float scale, int window, int sinks, int dtype, void* stream);
+
+/* Workspace bytes attn_fwd_window needs on the current device (0: none, or
+ * invalid sizes).  Host-only apart from the SM count. */
+size_t attn_fwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window,
+                                      int sinks, int dtype);
+
+/*
  * Split-key forward for short query blocks against long key sequences (LLM
  * decode against a KV cache, the workload of the forum post's table "PyTorch
  * LLM Inference -- Qwen 2.5 0.5B (GQA, FP16)").  attn_fwd runs one CTA per KV
@@ -272,6 +301,26 @@ int attn_bwd_masked(const void* q, const void* k, const void* v, const void* out
                     long long mask_stride_b, long long mask_stride_h, long long mask_stride_q,
                     int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int causal,
                     int dtype, void* stream);
+
+/*
+ * Backward of attn_fwd_window: the same window, sinks and positions (Nq <= Nk).
+ * dk and dv of keys that no query sees are zero.  workspace:
+ * attn_bwd_window_workspace_size() bytes (ATTN_ERR_WORKSPACE if smaller): the
+ * per-row statistics, each head's rows padded to a multiple of 128, and the
+ * fp32 partial sums of dK and dV -- always for the sink tiles, whose many query
+ * tiles are cut into ranges, for the others when they leave SMs idle -- which a
+ * last kernel adds in a fixed order (deterministic).  Other arguments, layouts
+ * and errors are attn_bwd's.
+ */
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* out,
+                    const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                    void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq,
+                    int Nk, int D, float scale, int window, int sinks, int dtype, void* stream);
+
+/* Workspace bytes attn_bwd_window needs on the current device; 0 for invalid
+ * sizes.  Host-only apart from the SM count. */
+size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int D, int window,
+                                      int sinks, int dtype);
 
 /*
  * attn_bwd without a workspace argument, for callers that cannot allocate

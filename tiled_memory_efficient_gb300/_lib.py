@@ -48,6 +48,12 @@ _SIGNATURES = {
     "attn_fwd_masked": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, ctypes.c_longlong, ctypes.c_longlong,
                          ctypes.c_longlong, _i, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _vp],
                         _i),
+    "attn_fwd_window": ([_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _i, _i, _i, _i, _i, _i,
+                         ctypes.c_float, _i, _i, _i, _vp], _i),
+    "attn_fwd_window_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _i, _i], ctypes.c_size_t),
+    "attn_bwd_window": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                         _i, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i, _i, _vp], _i),
+    "attn_bwd_window_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _i, _i], ctypes.c_size_t),
     "attn_fwd_splitkv": ([_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _i, _i, _i, _i, _i, _i,
                           ctypes.c_float, _i, _i, _i, _vp], _i),
     "attn_fwd_splitkv_workspace_size": ([_i, _i, _i, _i, _i, _i, _i], ctypes.c_size_t),
@@ -336,6 +342,121 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
     return out, lse
 
 
+def _same_device(first, *others):
+    """Every tensor lives on the device of the first."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+
+
+class _on_device:
+    """Makes a tensor's device current for a call (nothing to do when it is)."""
+    __slots__ = ("index", "prev")
+
+    def __init__(self, t):
+        self.index = t.device.index
+
+    def __enter__(self):
+        import torch
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.prev != self.index:
+            import torch
+            torch.cuda.set_device(self.prev)
+
+
+def _check_like(name, t, shape, dtype):
+    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+
+
+def _check_workspace(t):
+    if t is not None and not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+
+
+def _window_args(q, k, v, window, sinks, scale):
+    _check(q, k, v)
+    _same_device(q, k, v)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[3])
+    # the C ABI takes 32-bit counts; either may exceed the keys
+    return min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff), float(scale)
+
+
+def attn_fwd_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None,
+                    lse=None, workspace=None):
+    """Sliding-window attention with sinks: query i stands at position
+    p = i + Nk - Nq and sees keys j <= p with j > p - window or j < sinks.
+    Returns (out, lse) as attn_fwd does; workspace (allocated here when not
+    given) as in include/attn.h."""
+    import torch
+    window, sinks, scale = _window_args(q, k, v, window, sinks, scale)
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    dt = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like("out", out, q.shape, q.dtype)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+    else:
+        _check_like("lse", lse, (B, Hq, Nq), torch.float32)
+    _same_device(q, out, lse, workspace)
+    _check_workspace(workspace)
+    lib = load()
+    with _on_device(q):
+        if workspace is None:
+            n = lib.attn_fwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, dt)
+            if n > 0:
+                workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
+        rc = lib.attn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), _ptr(workspace), _nbytes(workspace), B, Hq, Hkv,
+                                 Nq, Nk, D, scale, window, sinks, dt, _stream_handle(q.device))
+    if rc != ATTN_OK:
+        raise AttnError("attn_fwd_window", rc)
+    return out, lse
+
+
+def attn_bwd_window(q, k, v, out, dout, lse, window: int, sinks: int = 0,
+                    scale: float | None = None, dq=None, dk=None, dv=None, workspace=None):
+    """dq, dk, dv of attn_fwd_window (dk, dv summed over each GQA group)."""
+    import torch
+    window, sinks, scale = _window_args(q, k, v, window, sinks, scale)
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    dt = _dtype_code(q)
+    _check_like("out", out, q.shape, q.dtype)
+    _check_like("dout", dout, q.shape, q.dtype)
+    _check_like("lse", lse, (B, Hq, Nq), torch.float32)
+    grads = []
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is None:
+            g = torch.empty_like(like)
+        else:
+            _check_like(name, g, like.shape, like.dtype)
+        grads.append(g)
+    _same_device(q, out, dout, lse, workspace, *grads)
+    _check_workspace(workspace)
+    lib = load()
+    with _on_device(q):
+        if workspace is None:
+            n = lib.attn_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, dt)
+            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+        rc = lib.attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                 dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(),
+                                 grads[1].data_ptr(), grads[2].data_ptr(), workspace.data_ptr(),
+                                 _nbytes(workspace), B, Hq, Hkv, Nq, Nk, D, scale, window, sinks,
+                                 dt, _stream_handle(q.device))
+    if rc != ATTN_OK:
+        raise AttnError("attn_bwd_window", rc)
+    return tuple(grads)
+
+
 def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None = None,
              dq=None, dk=None, dv=None, workspace=None, mask=None):
     """dq, dk, dv of attn_fwd (dk, dv summed over each GQA group); with the
@@ -384,6 +505,10 @@ def sync_status(device=None) -> int:
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def ffn_forward(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4096, out=None,

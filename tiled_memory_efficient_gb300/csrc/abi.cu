@@ -522,6 +522,143 @@ extern "C" int attn_fwd_masked(const void* q, const void* k, const void* v, void
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+namespace tme {
+namespace {
+
+// Launch plan of the sliding-window forward.  A query block of more than 256
+// positions runs one query head per group: its Q tiles then never span two
+// heads, whose windows lie far apart.  A shorter one (a decode step, a draft)
+// flattens the group's heads onto its KV head like the other forwards.
+struct WindowPlan {
+    bool per_head = false;
+    int64_t groups = 0, pairs = 0, rows = 0;   // rows per group
+    int splits = 1, tps = 0;                   // key ranges of the tile list
+    int skip0 = 0, skip1 = 0;                  // key tiles no query sees
+};
+
+WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks, int sms) {
+    WindowPlan w;
+    w.per_head = Nq > 256;
+    w.groups = static_cast<int64_t>(B) * (w.per_head ? Hq : Hkv);
+    w.rows = w.per_head ? Nq : static_cast<int64_t>(Hq / Hkv) * Nq;
+    w.pairs = (w.rows + 255) / 256;
+    const int64_t lo = static_cast<int64_t>(Nk) - Nq - window + 1;   // first key in any window
+    const int64_t lo_tile = lo > 0 ? lo / 128 : 0;
+    int64_t n_sink = (static_cast<int64_t>(sinks) + 127) / 128;
+    if (n_sink > lo_tile) n_sink = lo_tile;
+    w.skip0 = static_cast<int>(n_sink);
+    w.skip1 = static_cast<int>(lo_tile);
+    // the longest key-tile list of a pair (the pairs of a head see min(Nq, 256)
+    // positions, a flattened block all Nq of them)
+    const int64_t span = (Nq < 256 || !w.per_head ? Nq : 256) + static_cast<int64_t>(window) - 1;
+    int64_t tiles = (span + 127) / 128 + 1 + (static_cast<int64_t>(sinks) + 127) / 128;
+    if (tiles > key_tiles(Nk)) tiles = key_tiles(Nk);
+    w.tps = static_cast<int>(tiles);
+    const int64_t units = w.groups * w.pairs;
+    if (sms <= 0) sms = device_sms();
+    if (sms <= 0 || units >= sms) return w;
+    // Under one wave: cut the list into as many ranges as fill the SMs, of at
+    // least kWindowRangeTiles key tiles each.
+    constexpr int64_t kWindowRangeTiles = 4;
+    int64_t want = sms / units;
+    if (want > tiles / kWindowRangeTiles) want = tiles / kWindowRangeTiles;
+    if (want > kMaxSplits) want = kMaxSplits;
+    if (want < 2) return w;
+    w.tps = static_cast<int>((tiles + want - 1) / want);
+    w.splits = static_cast<int>((tiles + w.tps - 1) / w.tps);
+    return w;
+}
+
+int check_window(int Nq, int Nk, int window, int sinks) {
+    return window >= 1 && sinks >= 0 && Nq <= Nk ? ATTN_OK : ATTN_ERR_INVALID;
+}
+
+// Bytes of the fp16 copy of V and its flags (bf16, long query blocks).
+size_t window_v_bytes(const WindowPlan& w, int B, int Hkv, int Nk, int D, int dtype) {
+    if (dtype != ATTN_BF16 || !w.per_head) return 0;
+    const size_t groups = static_cast<size_t>(B) * Hkv;
+    return pad256(groups * Nk * D * 2) + pad256(groups * static_cast<size_t>(key_tiles(Nk)));
+}
+
+size_t window_part_bytes(const WindowPlan& w, int D) {
+    if (w.splits < 2) return 0;
+    const size_t rows = static_cast<size_t>(w.groups) * w.rows;
+    return pad256(w.splits * rows * D * sizeof(float)) + pad256(w.splits * rows * sizeof(float));
+}
+
+}  // namespace
+}  // namespace tme
+
+extern "C" size_t attn_fwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int D,
+                                                 int window, int sinks, int dtype) {
+    if (check_shape(B, Hq, Hkv, Nq, Nk, D, 1.0f, dtype) != ATTN_OK) return 0;
+    if (check_window(Nq, Nk, window, sinks) != ATTN_OK) return 0;
+    if (window > Nk) window = Nk;
+    if (sinks > Nk) sinks = Nk;
+    const WindowPlan w = window_plan(B, Hq, Hkv, Nq, Nk, window, sinks, 0);
+    return window_v_bytes(w, B, Hkv, Nk, D, dtype) + window_part_bytes(w, D);
+}
+
+extern "C" int attn_fwd_window(const void* q, const void* k, const void* v, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                               int Nq, int Nk, int D, float scale, int window, int sinks,
+                               int dtype, void* stream) {
+    int rc = check_shape(B, Hq, Hkv, Nq, Nk, D, scale, dtype);
+    if (rc != ATTN_OK) return rc;
+    rc = check_window(Nq, Nk, window, sinks);
+    if (rc != ATTN_OK) return rc;
+    // a window or sinks past the sequence see all of it
+    if (window > Nk) window = Nk;
+    if (sinks > Nk) sinks = Nk;
+    const WindowPlan w = window_plan(B, Hq, Hkv, Nq, Nk, window, sinks, 0);
+    if (w.groups * w.pairs * w.splits > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    const size_t v_bytes = window_v_bytes(w, B, Hkv, Nk, D, dtype);
+    const size_t need = v_bytes + window_part_bytes(w, D);
+    if (need > 0) {
+        if (!workspace) return ATTN_ERR_INVALID;
+        if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+        if (workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    }
+    CUtensorMap tmQ, tmK, tmV, tmV16;
+    FwdParams p;
+    rc = fwd_prepare(q, k, v, out, lse, B, Hq, Hkv, Nq, Nk, D, scale, ATTN_CAUSAL_BOTTOM_RIGHT,
+                     dtype, &tmQ, &tmK, &tmV, &p);
+    if (rc != ATTN_OK) return rc;
+    const bool bf16 = dtype == ATTN_BF16;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t kv_groups = static_cast<int64_t>(B) * Hkv;
+    p.window = window;
+    p.sinks = sinks;
+    p.kv_div = 1;
+    if (w.per_head) {
+        if (make_map(&tmQ, q, bf16, D, Nq, w.groups) != ATTN_OK) return ATTN_ERR_CUDA;
+        p.kv_div = Hq / Hkv;
+        p.n_groups = static_cast<int>(w.groups);
+        p.rows_per_group = w.rows;
+        p.n_pairs = static_cast<int>(w.pairs);
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (w.splits > 1) {
+        p.n_splits = w.splits;
+        p.tiles_per_split = w.tps;
+        p.o_part = reinterpret_cast<float*>(ws + v_bytes);
+        p.lse_part = reinterpret_cast<float*>(
+            ws + v_bytes + pad256(static_cast<size_t>(w.splits) * p.total_rows * D * sizeof(float)));
+    }
+    cudaError_t e = cudaSuccess;
+    if (v_bytes > 0) {
+        if (make_map(&tmV16, ws, false, D, Nk, kv_groups) != ATTN_OK) return ATTN_ERR_CUDA;
+        uint8_t* vflags = ws + pad256(static_cast<size_t>(kv_groups) * Nk * D * 2);
+        p.vflags = vflags;
+        p.n_ktiles = static_cast<int>(key_tiles(Nk));
+        e = launch_v_to_f16(D, v, ws, vflags, kv_groups, Nk, st, w.skip0, w.skip1);
+    }
+    if (e == cudaSuccess)
+        e = launch_fwd(D, bf16, true, tmQ, tmK, tmV, p, st, v_bytes > 0 ? &tmV16 : nullptr);
+    if (e == cudaSuccess && w.splits > 1) e = launch_splitkv_merge(D, bf16, p, st);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 extern "C" int attn_fwd_num_splits(int B, int Hq, int Hkv, int Nq, int Nk, int D, int num_sms) {
     if (check_shape(B, Hq, Hkv, Nq, Nk, D, 1.0f, ATTN_F16) != ATTN_OK) return 1;
     if (num_sms <= 0) {
@@ -788,6 +925,158 @@ extern "C" int attn_bwd_masked(const void* q, const void* k, const void* v, cons
     return bwd_run(q, k, v, out, dout, lse, dq, dk, dv, workspace, workspace_bytes, B, Hq, Hkv, Nq,
                    Nk, D, scale, causal, dtype, mask, mask_kind, mask_stride_b, mask_stride_h,
                    mask_stride_q, stream);
+}
+
+namespace tme {
+namespace {
+
+// Query ranges of the sliding-window dK/dV.  A key tile past the sinks meets
+// about (window + 127) / 128 + 1 query tiles of each of its G heads; a sink tile
+// meets every later one, so its list is cut into ranges of about one other
+// tile's work (its CTAs would otherwise outlast the grid).  When the other
+// tiles alone leave SMs idle, they are cut too.  Ranges hold at least
+// kWindowMinTiles query tiles.
+struct WindowBwdPlan {
+    int64_t n_qtiles = 0, n_ktiles = 0;
+    int sink_tiles = 0;
+    int splits[2] = {1, 1};
+    int keys[2] = {0, 0};
+};
+constexpr int64_t kWindowMinTiles = 4;
+
+WindowBwdPlan window_bwd_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks,
+                              int sms) {
+    WindowBwdPlan w;
+    const int64_t groups = static_cast<int64_t>(B) * Hkv, G = Hq / Hkv;
+    w.n_qtiles = (static_cast<int64_t>(Nq) + 127) / 128;
+    w.n_ktiles = key_tiles(Nk);
+    w.sink_tiles = static_cast<int>((static_cast<int64_t>(sinks) + 127) / 128);
+    w.keys[0] = static_cast<int>(w.sink_tiles * 128LL < Nk ? w.sink_tiles * 128LL : Nk);
+    w.keys[1] = Nk - w.keys[0];
+    if (sms <= 0) sms = device_sms();
+    if (sms <= 0) return w;
+    int64_t per = (static_cast<int64_t>(window) + 127) / 128 + 1;
+    if (per > w.n_qtiles) per = w.n_qtiles;
+    per *= G;
+    const int64_t units = groups * (w.n_ktiles - w.sink_tiles);
+    if (units > 0 && units < sms) {
+        int64_t want = (sms + units - 1) / units;
+        if (want > per / kWindowMinTiles) want = per / kWindowMinTiles;
+        if (want > 32) want = 32;
+        if (want > 1) w.splits[1] = static_cast<int>(want);
+    }
+    if (w.sink_tiles > 0) {
+        int64_t target = (per + w.splits[1] - 1) / w.splits[1];
+        if (target < kWindowMinTiles) target = kWindowMinTiles;
+        int64_t want = (G * w.n_qtiles + target - 1) / target;
+        // many sink tiles fill the device by themselves
+        const int64_t most = (4LL * sms + groups * w.sink_tiles - 1) / (groups * w.sink_tiles);
+        if (want > most) want = most;
+        if (want > 256) want = 256;
+        w.splits[0] = static_cast<int>(want);
+    }
+    return w;
+}
+
+size_t window_stats_bytes(const WindowBwdPlan& w, int B, int Hq) {
+    return pad256(2 * static_cast<size_t>(B) * Hq * w.n_qtiles * 128 * sizeof(float));
+}
+size_t window_range_bytes(const WindowBwdPlan& w, int r, int B, int Hkv, int D) {
+    if (w.splits[r] < 2) return 0;
+    return pad256(static_cast<size_t>(w.splits[r]) * B * Hkv * w.keys[r] * D * sizeof(float));
+}
+
+}  // namespace
+}  // namespace tme
+
+extern "C" size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int D,
+                                                 int window, int sinks, int dtype) {
+    if (check_shape(B, Hq, Hkv, Nq, Nk, D, 1.0f, dtype) != ATTN_OK) return 0;
+    if (check_window(Nq, Nk, window, sinks) != ATTN_OK) return 0;
+    if (window > Nk) window = Nk;
+    if (sinks > Nk) sinks = Nk;
+    const WindowBwdPlan w = window_bwd_plan(B, Hq, Hkv, Nq, Nk, window, sinks, 0);
+    return window_stats_bytes(w, B, Hq) + 2 * window_range_bytes(w, 0, B, Hkv, D) +
+           2 * window_range_bytes(w, 1, B, Hkv, D);
+}
+
+extern "C" int attn_bwd_window(const void* q, const void* k, const void* v, const void* out,
+                               const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                               void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                               int Nq, int Nk, int D, float scale, int window, int sinks,
+                               int dtype, void* stream) {
+    if (!q || !k || !v || !out || !dout || !lse || !dq || !dk || !dv || !workspace)
+        return ATTN_ERR_INVALID;
+    int rc = check_shape(B, Hq, Hkv, Nq, Nk, D, scale, dtype);
+    if (rc != ATTN_OK) return rc;
+    rc = check_window(Nq, Nk, window, sinks);
+    if (rc != ATTN_OK) return rc;
+    const void* ptrs[] = {q, k, v, out, dout, lse, dq, dk, dv, workspace};
+    for (const void* ptr : ptrs)
+        if (!aligned16(ptr)) return ATTN_ERR_ALIGN;
+    if (window > Nk) window = Nk;
+    if (sinks > Nk) sinks = Nk;
+    const WindowBwdPlan w = window_bwd_plan(B, Hq, Hkv, Nq, Nk, window, sinks, 0);
+    if (workspace_bytes <
+        attn_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, dtype))
+        return ATTN_ERR_WORKSPACE;
+    const int64_t groups = static_cast<int64_t>(B) * Hkv;
+    const int64_t heads = static_cast<int64_t>(B) * Hq;
+    if (heads * w.n_qtiles > 0x7fffffffll ||
+        groups * (w.sink_tiles * static_cast<int64_t>(w.splits[0]) +
+                  (w.n_ktiles - w.sink_tiles) * w.splits[1]) > 0x7fffffffll)
+        return ATTN_ERR_UNSUPPORTED;
+    unsigned int* status = nullptr;
+    rc = device_setup(&status);
+    if (rc != ATTN_OK) return rc;
+    const bool bf16 = dtype == ATTN_BF16;
+    CUtensorMap tmQ, tmK, tmV, tmDO;
+    if (make_map(&tmQ, q, bf16, D, Nq, heads) != ATTN_OK ||
+        make_map(&tmDO, dout, bf16, D, Nq, heads) != ATTN_OK ||
+        make_map(&tmK, k, bf16, D, Nk, groups) != ATTN_OK ||
+        make_map(&tmV, v, bf16, D, Nk, groups) != ATTN_OK)
+        return ATTN_ERR_CUDA;
+    BwdParams p{};
+    p.out = out;
+    p.dout = dout;
+    p.lse = lse;
+    p.nlse2 = static_cast<float*>(workspace);
+    p.ndelta = p.nlse2 + heads * w.n_qtiles * 128;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.status = status;
+    p.rows_per_group = Nq;
+    p.rows_pad = w.n_qtiles * 128;
+    p.total_rows = heads * Nq;
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.n_groups = static_cast<int>(groups);
+    p.n_qtiles = static_cast<int>(w.n_qtiles);
+    p.n_ktiles = static_cast<int>(w.n_ktiles);
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.kv_splits = 1;
+    p.window = window;
+    p.sinks = sinks;
+    p.causal_off = Nk - Nq;
+    p.kv_div = p.G;
+    p.n_sink_tiles = w.sink_tiles;
+    char* part = static_cast<char*>(workspace) + window_stats_bytes(w, B, Hq);
+    for (int r = 0; r < 2; ++r) {
+        const size_t bytes = window_range_bytes(w, r, B, Hkv, D);
+        p.wr[r].key0 = r == 0 ? 0 : w.keys[0];
+        p.wr[r].keys = w.keys[r];
+        p.wr[r].splits = w.splits[r];
+        p.wr[r].dv_part = reinterpret_cast<float*>(part);
+        p.wr[r].dk_part = reinterpret_cast<float*>(part + bytes);
+        part += 2 * bytes;
+    }
+    const cudaError_t e =
+        launch_bwd(D, bf16, true, tmQ, tmK, tmV, tmDO, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" int attn_sync_status(void* stream) {

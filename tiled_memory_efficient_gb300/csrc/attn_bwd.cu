@@ -27,6 +27,7 @@
 #include "attn_internal.h"
 #include "bias.cuh"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace tme {
 namespace {
@@ -263,7 +264,10 @@ struct BwdCfg {
 // its P^T / dS^T are in TMEM, then S^T / dP^T of half u of tile n+1 into the
 // same columns (the tensor pipe runs in order, so the products of tile n have
 // read them first).
-template <int D, bool BF16, bool CAUSAL, bool MASK>
+// WIN: the key tile meets query tiles [qa, qb] of each of its G heads (window and
+// sinks, BwdParams); entry it of that list is tile qa + it % (qb - qa + 1) of
+// head it / (qb - qa + 1).  Without it the list is the group's flattened tiles.
+template <int D, bool BF16, bool CAUSAL, bool MASK, bool WIN = false>
 __global__ void __launch_bounds__(kKvThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmDO,
@@ -295,17 +299,52 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     // Heaviest first: under the causal mask low key tiles meet the most queries.
     // CTA (group, key tile kt, query range sp): consecutive CTAs share a key
     // tile; range sp takes query tiles [qi0, qi1).
-    const int unit = static_cast<int>(blockIdx.x / p.kv_splits);
-    const int sp = static_cast<int>(blockIdx.x % p.kv_splits);
-    const int group = unit / p.n_ktiles;
-    const int kt = unit % p.n_ktiles;
+    // With a window the sink tiles' CTAs come first, then the others'.
+    const int n_sink_ctas = WIN ? p.n_groups * p.n_sink_tiles * p.wr[0].splits : 0;
+    const int region = WIN && static_cast<int>(blockIdx.x) >= n_sink_ctas ? 1 : 0;
+    const int kv_splits = WIN ? p.wr[region].splits : p.kv_splits;
+    const int cta = static_cast<int>(blockIdx.x) - (region ? n_sink_ctas : 0);
+    const int unit = cta / kv_splits;
+    const int sp = cta % kv_splits;
+    const int region_tiles = !WIN ? p.n_ktiles : region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
+    const int group = unit / region_tiles;
+    const int kt = unit % region_tiles + (region ? p.n_sink_tiles : 0);
     const int key0 = kt * kRows;
-    const int qi0 = sp * p.qtiles_per_split;
-    const int qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
-    // head (within the group) and position of the first row of query tile qi0
-    const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
-    const int head_0 = static_cast<int>(r0 / p.Nq);
-    const int pos_0 = static_cast<int>(r0 % p.Nq);
+    int qi0 = 0, qi1 = 0;          // list entries [qi0, qi1)
+    int qa = 0, q_cnt = 1;         // WIN: first query tile, tiles per head
+    int head_0 = 0, pos_0 = 0;     // head and position of the first row of entry qi0
+    if constexpr (WIN) {
+        // positions of a head that see some key of the tile
+        const int i_min = max(0, key0 - p.causal_off);
+        int64_t i_max = p.Nq - 1;
+        if (key0 >= p.sinks)
+            i_max = min(i_max, static_cast<int64_t>(key0) + kRows - 2 + p.window - p.causal_off);
+        qa = i_min / kRows;
+        q_cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
+        const int64_t total = static_cast<int64_t>(p.G) * q_cnt;
+        qi0 = static_cast<int>(total * sp / kv_splits);
+        qi1 = static_cast<int>(total * (sp + 1) / kv_splits);
+        head_0 = q_cnt > 0 ? qi0 / q_cnt : 0;
+        pos_0 = q_cnt > 0 ? (qa + qi0 % q_cnt) * kRows : 0;
+    } else {
+        qi0 = sp * p.qtiles_per_split;
+        qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
+        const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
+        head_0 = static_cast<int>(r0 / p.Nq);
+        pos_0 = static_cast<int>(r0 % p.Nq);
+    }
+    // head and position of the next entry's first row
+    auto next_entry = [&](int& pos, int& head) {
+        if constexpr (WIN) {
+            pos += kRows;
+            if (pos >= (qa + q_cnt) * kRows) {
+                pos = qa * kRows;
+                ++head;
+            }
+        } else {
+            next_tile(pos, head, p.Nq);
+        }
+    };
     // Query tile qi (first-row position pos) meets this key tile.
     // A boolean mask that depends on the key alone (one row of keep bytes per
     // KV group, as a padding mask is) may remove every key of this tile: then
@@ -320,7 +359,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
     bool any_kept = true;   // set after the set-up barrier
     auto visit = [&](int qi, int pos) {
-        return any_kept && (!CAUSAL || tile_max_pos_at(qi, pos, p) >= key0);
+        return any_kept && (WIN || !CAUSAL || tile_max_pos_at(qi, pos, p) >= key0);
     };
 
     if (threadIdx.x == 0) {
@@ -352,18 +391,27 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 tma_load_3d(&tmV, kv_full, sV + kb * (kRows * 128), kb * 64, key0, group);
             }
             int n = 0;
-            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq)) {
-                if (!visit(qi, pos)) continue;
+            int head = head_0;
+            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi) {
+                if (!visit(qi, pos)) {
+                    pos = next_tile_pos(pos, p.Nq);
+                    continue;
+                }
+                // first row of the tile within its group (WIN: its head) and that group
+                const int row0 = WIN ? pos : qi * kRows;
+                const int q_group = WIN ? group * p.G + head : group;
+                if constexpr (WIN) next_entry(pos, head);
+                else pos = next_tile_pos(pos, p.Nq);
                 const int slot = n % QS;
                 if (!mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status)) break;
                 mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
-                                qi * kRows, group);
+                                row0, q_group);
                     tma_load_3d(&tmDO, &q_full[slot], sDO + slot * TB + kb * (kRows * 128),
-                                kb * 64, qi * kRows, group);
+                                kb * 64, row0, q_group);
                 }
-                const int64_t w0 = static_cast<int64_t>(group) * p.rows_pad + qi * kRows;
+                const int64_t w0 = static_cast<int64_t>(q_group) * p.rows_pad + row0;
                 bulk_load(sL + slot * kRows, p.nlse2 + w0, kRows * 4, &q_full[slot]);
                 bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
                 ++n;
@@ -401,8 +449,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             mma_commit_elect(&s_full[u]);
         };
         int n_vis = 0;   // query tiles this key tile meets (the producer loads them in order)
-        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq))
-            n_vis += visit(qi, pos) ? 1 : 0;
+        if constexpr (WIN) {
+            n_vis = qi1 - qi0;
+        } else {
+            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq))
+                n_vis += visit(qi, pos) ? 1 : 0;
+        }
         warp_wait(kv_full, 0, abort_flag, p.status);
         if (n_vis > 0) {
             warp_wait(&q_full[0], 0, abort_flag, p.status);
@@ -457,7 +509,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int head0 = MASK ? (group % p.Hkv) * p.G : 0;
         int n = 0;
         int head = head_0;   // head within the group of the current tile's first row
-        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, next_tile(pos, head, p.Nq)) {
+        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, next_entry(pos, head)) {
             if (!visit(qi, pos)) continue;
             const int slot = n % QS;
             // This chunk's bias column, requested before the waits for the
@@ -489,7 +541,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             uint32_t sv[32], dp[32];
             tmem_ld32(tS, sv);
             tmem_ld32(tDP, dp);
-            const int64_t row0 = static_cast<int64_t>(qi) * kRows;
+            const int64_t row0 = WIN ? pos : static_cast<int64_t>(qi) * kRows;
             const int base = pos;
             const float* L = sL + slot * kRows + c * 32;
             const float* Dl = sDl + slot * kRows + c * 32;
@@ -499,7 +551,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             const int wkey_last = key0 + quad * 32 + 31;
             const int q_first = c * 32;
             bool fast = (row0 + q_first + 32 <= p.rows_per_group) && (wkey_last < p.Nk);
-            if (CAUSAL)
+            // WIN: key position of the chunk's first query, the last sees 31 more
+            const int kq_first = base + q_first + p.causal_off;
+            if (WIN)
+                fast = fast && !window_edge(wkey_last - 31, wkey_last, kq_first, kq_first + 31,
+                                            p.window, p.sinks);
+            else if (CAUSAL)
                 fast = fast && (base + q_first + 32 <= p.Nq) && (wkey_last <= base + q_first);
             const uint64_t sl22 = f2(sc, sc);
             tmem_wait_ld();
@@ -535,7 +592,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                     for (int u = 0; u < 2; ++u) {
                         const int q = q_first + i + u;
                         bool ok = (row0 + q < p.rows_per_group) && (key < p.Nk);
-                        if (CAUSAL) ok = ok && key <= tile_pos(base, q, p.Nq);
+                        if (WIN) {
+                            const int kq = base + q + p.causal_off;   // key position of the query
+                            ok = ok && window_sees(key, kq + 1, kq - p.window, p.sinks);
+                        } else if (CAUSAL) {
+                            ok = ok && key <= tile_pos(base, q, p.Nq);
+                        }
                         const float pr = ex2_ftz(fmaf(__uint_as_float(sv[i + u]), sc, L[i + u]));
                         pp[u] = ok ? pr : 0.0f;
                         dd[u] = ok ? pr * (__uint_as_float(dp[i + u]) + Dl[i + u]) : 0.0f;
@@ -578,10 +640,18 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
                 for (int i = 0; i < CW; ++i) a[i] = 0u;
             }
-            if (ok && key < p.Nk && p.kv_splits > 1) {
+            if (ok && key < p.Nk && kv_splits > 1) {
                 // this query range's fp32 partial sum (dK unscaled)
-                float* dst = (which ? p.dk_part : p.dv_part) +
-                             (static_cast<int64_t>(sp) * p.n_groups * p.Nk + grow) * D + col0;
+                float* dst;
+                if constexpr (WIN) {
+                    const BwdParams::WindowRanges& w = p.wr[region];
+                    dst = (which ? w.dk_part : w.dv_part) +
+                          ((static_cast<int64_t>(sp) * p.n_groups + group) * w.keys + key - w.key0) * D +
+                          col0;
+                } else {
+                    dst = (which ? p.dk_part : p.dv_part) +
+                          (static_cast<int64_t>(sp) * p.n_groups * p.Nk + grow) * D + col0;
+                }
 #pragma unroll
                 for (int i = 0; i < CW / 4; ++i)
                     reinterpret_cast<float4*>(dst)[i] =
@@ -717,7 +787,8 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
     // MK: 0 no mask, 1 a general bias, 2 a boolean mask that depends on the
     // key alone (the same keep bytes for every row: read directly, served to
     // the whole warp at once).
-    constexpr bool MASK = MK != 0, STAGE = MK == 1;
+    // 3 a sliding window with sinks (one query head per group).
+    constexpr bool MASK = MK == 1 || MK == 2, STAGE = MK == 1, WIN = MK == 3;
     // K lives from S_j to dQ_j, V only until dP_j: separate rings, K deeper.
     // A general mask stages each warp's next 32 x 64 bias block in shared
     // memory (8 warps x 4 KB); at D = 128 the K ring gives a stage for it.
@@ -756,10 +827,18 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
     const int qi = p.n_qtiles - 1 - static_cast<int>(blockIdx.x % p.n_qtiles);
     const int64_t row0 = static_cast<int64_t>(qi) * kRows;
     int nkv = (p.Nk + kRows - 1) / kRows;
-    if (CAUSAL) {
+    KeyList kl;
+    if constexpr (WIN) {
+        kl = key_list(row0 + p.causal_off, p.window, p.sinks);
+        const int64_t keys =
+            min(min(row0 + kRows, p.rows_per_group) + p.causal_off, static_cast<int64_t>(p.Nk));
+        nkv = static_cast<int>((keys + kRows - 1) / kRows) - kl.skip;
+    } else if (CAUSAL) {
         const int keys = min(tile_max_pos(row0, p) + 1, p.Nk);
         nkv = (keys + kRows - 1) / kRows;
     }
+    auto ktile = [&](int j) { return WIN ? kl.tile(j) : j; };
+    const int kv_group = WIN ? group / p.kv_div : group;
     // A boolean mask that depends on the key alone: the key tiles past its last
     // kept key contribute nothing to dQ (at least one tile is kept, so rows with
     // no kept key still end with dQ = 0).
@@ -818,13 +897,13 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
                 mbar_arrive_expect_tx(&k_full[ks], TB);
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(&tmK, &k_full[ks], sK + ks * TB + kb * (kRows * 128), kb * 64,
-                                j * kRows, group);
+                                ktile(j) * kRows, kv_group);
                 ++nk;
                 if (!mbar_wait(&v_empty[vs], ((j / VS) & 1) ^ 1, abort_flag, p.status)) break;
                 mbar_arrive_expect_tx(&v_full[vs], TB);
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(&tmV, &v_full[vs], sV + vs * TB + kb * (kRows * 128), kb * 64,
-                                j * kRows, group);
+                                ktile(j) * kRows, kv_group);
                 ++nv;
             }
             mbar_wait_bounded(q_full, 0, p.status);
@@ -888,13 +967,16 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         warp_wait(q_full, 0, abort_flag, p.status);
         const float nl = sL[quad * 32 + lane];   // -lse2 of this row
         const float nd = sDl[quad * 32 + lane];  // -delta of this row
-        const int lim = CAUSAL ? min(p.Nk, pos + 1) : p.Nk;  // keys [0, lim) allowed
+        const int off = WIN ? p.causal_off : 0;
+        const int lim = CAUSAL ? min(p.Nk, pos + off + 1) : p.Nk;  // keys [0, lim) allowed
+        const int low = WIN ? pos + off - p.window : 0;            // WIN: above it, or sinks
         // Smallest position among this warp's rows: key tiles past it (or past
         // Nk) need the mask.  Rows past the group only feed their own dQ rows,
         // which are never stored, so they need none.
         const int64_t wr0 = row0 + quad * 32;
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
         const int warp_min_pos = (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
+        const int warp_max_pos = static_cast<int>(wr1 % p.Nq);   // WIN: one head per group
         // scale still to apply to the scores read below: an additive bias
         // leaves natural-log logits (log2 e), a boolean one raw scores
         const float sc = (MASK && p.mask_kind == 2) ? kLog2e : sl2;
@@ -924,10 +1006,14 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         if constexpr (STAGE)
             if (nkv > 0 && staged(0)) prefetch(32 * CPW * hq);
         for (int j = 0; j < nkv; ++j) {
-            const int k0 = j * kRows;
+            const int k0 = ktile(j) * kRows;
             warp_wait(s_full, j & 1, abort_flag, p.status);
             tc_fence_after();
-            const bool need_mask = (k0 + kRows > p.Nk) || (CAUSAL && k0 + kRows - 1 > warp_min_pos);
+            const bool need_mask =
+                (k0 + kRows > p.Nk) ||
+                (WIN ? window_edge(k0, k0 + kRows - 1, warp_min_pos + off, warp_max_pos + off,
+                                   p.window, p.sinks)
+                     : CAUSAL && k0 + kRows - 1 > warp_min_pos);
             uint32_t sv[CPW][32], dp[CPW][32];
 #pragma unroll
             for (int cc = 0; cc < CPW; ++cc) {
@@ -980,8 +1066,13 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
                     float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
                     if (need_mask) {
                         const int kk = k0 + c * 32 + i;
-                        p0 = kk < lim ? p0 : 0.0f;
-                        p1 = kk + 1 < lim ? p1 : 0.0f;
+                        if constexpr (WIN) {
+                            p0 = window_sees(kk, lim, low, p.sinks) ? p0 : 0.0f;
+                            p1 = window_sees(kk + 1, lim, low, p.sinks) ? p1 : 0.0f;
+                        } else {
+                            p0 = kk < lim ? p0 : 0.0f;
+                            p1 = kk + 1 < lim ? p1 : 0.0f;
+                        }
                     }
                     const uint64_t dd = fmul2(
                         f2(p0, p1),
@@ -1096,6 +1187,75 @@ cudaError_t launch_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
     return launch_dependent(kern, ctas, dq_threads<MK, D>(), smem, stream, tmQ, tmDO, tmK, tmV, p);
 }
 
+// The same sums for a sliding window's backward: regions of keys with their own
+// numbers of ranges (BwdParams::wr), n8[r] = 8-element runs of region r that
+// have partials.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+    bwd_window_reduce_kernel(const BwdParams p, int64_t n8_0, int64_t n8_1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n8_0 + n8_1) return;
+    const BwdParams::WindowRanges w = p.wr[i < n8_0 ? 0 : 1];
+    if (i >= n8_0) i -= n8_0;
+    const int64_t stride = static_cast<int64_t>(p.n_groups) * w.keys * D;   // elements per range
+    const int64_t row = i / (D / 8);
+    const int64_t group = row / w.keys, key = w.key0 + row % w.keys;
+    const int64_t dst = (group * p.Nk + key) * (D / 8) + i % (D / 8);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const float* src = (which ? w.dk_part : w.dv_part) + i * 8;
+        float4 a = reinterpret_cast<const float4*>(src)[0];
+        float4 b = reinterpret_cast<const float4*>(src)[1];
+        for (int s = 1; s < w.splits; ++s) {
+            const float4 c = reinterpret_cast<const float4*>(src + s * stride)[0];
+            const float4 d = reinterpret_cast<const float4*>(src + s * stride)[1];
+            a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+            b = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+        }
+        const float sc = which ? p.scale : 1.0f;
+        reinterpret_cast<uint4*>(which ? p.dk : p.dv)[dst] =
+            make_uint4(pack2<BF16>(a.x * sc, a.y * sc), pack2<BF16>(a.z * sc, a.w * sc),
+                       pack2<BF16>(b.x * sc, b.y * sc), pack2<BF16>(b.z * sc, b.w * sc));
+    }
+}
+
+// Sliding window: the same chain of kernels; the Q side runs one query head per
+// group (tmQ, tmDO and p are laid out so).
+template <int D, bool BF16>
+cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          const CUtensorMap& tmDO, const BwdParams& p, cudaStream_t stream) {
+    const int64_t threads = p.total_rows * (D / 8);
+    cudaError_t e = launch_kernel(bwd_stats_kernel<D, BF16>,
+                                  dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0,
+                                  stream, p);
+    if (e != cudaSuccess) return e;
+    auto dq = bwd_dq_kernel<D, BF16, true, 3>;
+    constexpr int dq_bytes = dq_smem<D, false>();
+    e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(dq, static_cast<long long>(p.n_groups) * p.G * p.n_qtiles,
+                         dq_threads<3, D>(), dq_bytes, stream, tmQ, tmDO, tmK, tmV, p);
+    if (e != cudaSuccess) return e;
+    auto kv = bwd_dkdv_kernel<D, BF16, true, false, true>;
+    constexpr int kv_bytes = dkdv_smem<D>();
+    e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
+    if (e != cudaSuccess) return e;
+    const long long ctas =
+        static_cast<long long>(p.n_groups) *
+        (static_cast<long long>(p.n_sink_tiles) * p.wr[0].splits +
+         static_cast<long long>(p.n_ktiles - p.n_sink_tiles) * p.wr[1].splits);
+    e = launch_dependent(kv, ctas, kKvThreads, kv_bytes, stream, tmQ, tmDO, tmK, tmV, p);
+    if (e != cudaSuccess) return e;
+    int64_t n8[2];
+    for (int r = 0; r < 2; ++r)
+        n8[r] = p.wr[r].splits > 1 ? static_cast<int64_t>(p.n_groups) * p.wr[r].keys * (D / 8) : 0;
+    if (n8[0] + n8[1] > 0)
+        e = launch_dependent(bwd_window_reduce_kernel<D, BF16>, (n8[0] + n8[1] + 255) / 256, 256, 0,
+                             stream, p, n8[0], n8[1]);
+    return e;
+}
+
 template <int D, bool BF16, bool CAUSAL, bool MASK>
 cudaError_t launch_one(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmDO, const BwdParams& p, cudaStream_t stream) {
@@ -1139,6 +1299,16 @@ cudaError_t launch_bwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmDO,
                        const BwdParams& p, cudaStream_t stream) {
     const bool mask = p.mask != nullptr;
+    if (p.window > 0) {
+        if (mask || !causal) return cudaErrorInvalidValue;
+        if (D == 64)
+            return bf16 ? launch_window<64, true>(tmQ, tmK, tmV, tmDO, p, stream)
+                        : launch_window<64, false>(tmQ, tmK, tmV, tmDO, p, stream);
+        if (D == 128)
+            return bf16 ? launch_window<128, true>(tmQ, tmK, tmV, tmDO, p, stream)
+                        : launch_window<128, false>(tmQ, tmK, tmV, tmDO, p, stream);
+        return cudaErrorInvalidValue;
+    }
 #define TME_CASE(d, b, c, m)                              \
     if (D == d && bf16 == b && causal == c && mask == m)  \
         return launch_one<d, b, c, m>(tmQ, tmK, tmV, tmDO, p, stream);

@@ -34,6 +34,7 @@
 #include "attn_internal.h"
 #include "bias.cuh"
 #include "ptx.cuh"
+#include "window.cuh"
 
 namespace tme {
 namespace {
@@ -46,7 +47,8 @@ constexpr float kRescaleThreshold = 8.0f;
 
 // MK: 0 no mask; 1 a general attention bias (boolean or additive, any
 // broadcast); 2 a boolean keep-mask that depends on the key alone (a padding
-// mask, [B,1,1,Nk] or per head when G = 1), applied in the split layout.
+// mask, [B,1,1,Nk] or per head when G = 1), applied in the split layout; 3 a
+// sliding window with sinks (always causal; window.cuh).
 // BF16: bf16 inputs, whose value tiles the PV product takes as fp16: converted
 // in shared memory by converter warps, or (VPRE) read from an fp16 copy that
 // the caller's workspace holds.
@@ -245,6 +247,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     using C = FwdCfg<D, MK, BF16, VPRE>;
     constexpr bool MASK = MK == 1;      // general bias
     constexpr bool KEYMASK = MK == 2;   // key-only keep-mask (split layout)
+    constexpr bool WIN = MK == 3;       // sliding window with sinks
+    static_assert(!WIN || CAUSAL, "a sliding window is causal");
     constexpr int KS = C::kKStages, VS = C::kVStages;
     constexpr int kProducerWarp = C::kProducerWarp;
     constexpr int kMmaWarp0 = C::kMmaWarp0;
@@ -301,7 +305,12 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     }
     int group, pair;
     int only = -1;   // >= 0: the one Q tile of the pair this CTA runs
-    if (CAUSAL && p.Nq % (2 * kRows) == 0) {
+    if (WIN) {
+        // Units of equal work but for the first positions of a head (shorter
+        // lists): those last.  Consecutive CTAs share most of their key tiles.
+        group = unit / p.n_pairs;
+        pair = p.n_pairs - 1 - unit % p.n_pairs;
+    } else if (CAUSAL && p.Nq % (2 * kRows) == 0) {
         const int m = p.Nq / (2 * kRows);        // pairs per head (n_pairs = G * m)
         const int heads = p.n_groups * p.G;      // (group, head) combinations
         // The n_half_pos heaviest positions run as two CTAs per pair, one per
@@ -336,8 +345,19 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     const int64_t row_base = static_cast<int64_t>(pair) * (2 * kRows);
     const int kt0 = split >= 0 ? split * p.tiles_per_split : 0;
     const int tps = split >= 0 ? p.tiles_per_split : 0x7fffffff - kt0;
-    int n0 = tiles_in_range(kv_tiles_for(row_base, p, CAUSAL), kt0, tps);
-    int n1 = tiles_in_range(kv_tiles_for(row_base + kRows, p, CAUSAL), kt0, tps);
+    KeyList kl;
+    if constexpr (WIN) {
+        const int64_t last = min(row_base + 2 * kRows, p.rows_per_group) - 1;
+        // a pair that spans heads holds position 0
+        const int64_t min_pos = row_base / p.Nq == last / p.Nq ? row_base % p.Nq : 0;
+        kl = key_list(min_pos + p.causal_off, p.window, p.sinks);
+    }
+    // key tile of this CTA's step j, and its K/V group (a window's units may be
+    // query heads: FwdParams)
+    auto ktile = [&](int j) { return WIN ? kl.tile(kt0 + j) : kt0 + j; };
+    const int kv_group = WIN ? group / p.kv_div : group;
+    int n0 = tiles_in_range(kv_tiles_for(row_base, p, CAUSAL) - kl.skip, kt0, tps);
+    int n1 = tiles_in_range(kv_tiles_for(row_base + kRows, p, CAUSAL) - kl.skip, kt0, tps);
     if (only == 0) n1 = 0;
     if (only == 1) n0 = 0;
     int nmax = n0 > n1 ? n0 : n1;
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     // the whole CTA, as a padding mask is) removes every key tile past its
     // last kept key: the CTA stops there (keeping at least one tile, so rows
     // with no kept key still end with O = 0 and LSE = -inf).
-    const bool key_only = MK != 0 && p.mask_kind == 1 && p.msq == 0 && (p.msh == 0 || p.G == 1);
+    const bool key_only = (MK == 1 || MK == 2) && p.mask_kind == 1 && p.msq == 0 && (p.msh == 0 || p.G == 1);
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -379,9 +399,9 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         // The CTA reads the fp16 copy of V only if the copy holds every one of
         // its key tiles (flag 0); otherwise all of them come from the bf16 V.
         if (warp == 0) {
-            const uint8_t* fl = p.vflags + static_cast<int64_t>(group) * p.n_ktiles + kt0;
+            const uint8_t* fl = p.vflags + static_cast<int64_t>(kv_group) * p.n_ktiles;
             bool wide = false;
-            for (int i = lane; i < nmax; i += 32) wide |= fl[i] != 0;
+            for (int i = lane; i < nmax; i += 32) wide |= fl[ktile(i)] != 0;
             wide = __any_sync(0xffffffffu, wide);
             if (lane == 0) *cta_v16 = wide ? 0 : 1;
         }
@@ -430,7 +450,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(&tmK, &k_full[ks], sK + ks * C::kTileBytes + kb * (kRows * 128),
-                                kb * 64, (kt0 + j) * kRows, group);
+                                kb * 64, ktile(j) * kRows, kv_group);
                 ++nk;
                 const int vs = j % VS;
                 for (int t = 0; okp && t < 2; ++t)
@@ -441,7 +461,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 const CUtensorMap* mv = (VPRE && *cta_v16) ? &tmV16 : &tmV;
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(mv, &v_full[vs], sV + vs * C::kTileBytes + kb * (kRows * 128),
-                                kb * 64, (kt0 + j) * kRows, group);
+                                kb * 64, ktile(j) * kRows, kv_group);
                 ++nv;
             }
             // Never leave a copy in flight into shared memory we are about to give up.
@@ -623,6 +643,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
         const int warp_min_pos =
             (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
+        const int warp_max_pos =   // for a window's lower edge
+            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
         // General bias (MK = 1): this row's bias row (query head hkv*G +
         // row/Nq of batch group/Hkv), staged one key tile ahead: this warp's
         // 32 rows x 64 keys, nvalid rows real.  A half-tile is staged when its
@@ -706,7 +728,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 warp_wait(&p_full[t], j & 1, abort_flag, p.status);
                 continue;
             }
-            const int key0 = (kt0 + j) * kRows + 64 * h;
+            const int key0 = ktile(j) * kRows + 64 * h;
             uint4 kcur = make_uint4(0u, 0u, 0u, 0u);
             if constexpr (KEYMASK) kcur = kload(j);
             warp_wait(&s_full[t], j & 1, abort_flag, p.status);
@@ -762,7 +784,20 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                     }
                 }
             }
-            if (j >= j_mask) {
+            if constexpr (WIN) {
+                if (key0 + 64 > p.Nk ||
+                    window_edge(key0, key0 + 63, warp_min_pos + p.causal_off,
+                                warp_max_pos + p.causal_off, p.window, p.sinks)) {
+                    const int lim = min(p.Nk, pos + p.causal_off + 1);
+                    const int low = pos + p.causal_off - p.window;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!window_sees(key0 + c * 32 + i, lim, low, p.sinks))
+                                sr[c][i] = __float_as_uint(-INFINITY);
+                }
+            } else if (j >= j_mask) {
                 // keys [0, lim) allowed
                 const int lim = CAUSAL ? min(p.Nk, pos + p.causal_off + 1) : p.Nk;
 #pragma unroll
@@ -890,6 +925,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
         const int warp_min_pos =
             (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
+        const int warp_max_pos =   // for a window's lower edge
+            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
         // Staged bias (kBiasSmem): this warp's 32 rows, nvalid of them real.
         // A key tile is staged when it lies inside [0, Nk) and the warp has a
         // real row; the ragged last tile reads its bias directly.
@@ -921,7 +958,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 warp_wait(&p_full[t], j & 1, abort_flag, p.status);
                 continue;
             }
-            const int key0 = (kt0 + j) * kRows;
+            const int key0 = ktile(j) * kRows;
             // D = 128 with a general mask: the first bias chunk is requested
             // before the wait for S, each later one a chunk ahead.
             const bool bfull = MASK && row_valid && key0 + kRows <= p.Nk;
@@ -981,7 +1018,20 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
             const float sc = MASK ? 1.0f : sl2;   // scale still to apply to sr
             const bool need_mask =
                 (key0 + kRows > p.Nk) || (CAUSAL && key0 + kRows - 1 > warp_min_pos + p.causal_off);
-            if (need_mask) {
+            if constexpr (WIN) {
+                if (key0 + kRows > p.Nk ||
+                    window_edge(key0, key0 + kRows - 1, warp_min_pos + p.causal_off,
+                                warp_max_pos + p.causal_off, p.window, p.sinks)) {
+                    const int lim = min(p.Nk, pos + p.causal_off + 1);
+                    const int low = pos + p.causal_off - p.window;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!window_sees(key0 + c * 32 + i, lim, low, p.sinks))
+                                sr[c][i] = __float_as_uint(-INFINITY);
+                }
+            } else if (need_mask) {
                 // keys [0, lim) allowed
                 const int lim = CAUSAL ? min(p.Nk, pos + p.causal_off + 1) : p.Nk;
 #pragma unroll
@@ -1125,10 +1175,18 @@ cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
         const bool key_only = p.mask_kind == 1 && p.msq == 0 && (p.msh == 0 || p.G == 1);
         mk = (D == 64 && key_only && !bf16) ? 2 : 1;
     }
+    if (p.window > 0) {
+        if (mk != 0 || !causal) return cudaErrorInvalidValue;
+        mk = 3;
+    }
     // bf16 without a mask, given the fp16 copy of V (p.vflags and tmV16):
     // the instantiation without converter warps.
     if (tmV16 != nullptr) {
-        if (!bf16 || mk != 0 || p.vflags == nullptr) return cudaErrorInvalidValue;
+        if (!bf16 || (mk != 0 && mk != 3) || p.vflags == nullptr) return cudaErrorInvalidValue;
+        if (mk == 3)
+            return D == 64    ? launch_one<64, true, true, 3, true>(tmQ, tmK, tmV, *tmV16, p, stream)
+                   : D == 128 ? launch_one<128, true, true, 3, true>(tmQ, tmK, tmV, *tmV16, p, stream)
+                              : cudaErrorInvalidValue;
         if (D == 64 && !causal) return launch_one<64, true, false, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);
         if (D == 64 && causal) return launch_one<64, true, true, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);
         if (D == 128 && !causal) return launch_one<128, true, false, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);
@@ -1151,6 +1209,10 @@ cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
     TME_CASES(1)
     TME_CASE(64, false, false, 2)
     TME_CASE(64, false, true, 2)
+    TME_CASE(64, false, true, 3)
+    TME_CASE(64, true, true, 3)
+    TME_CASE(128, false, true, 3)
+    TME_CASE(128, true, true, 3)
 #undef TME_CASES
 #undef TME_CASE
     return cudaErrorInvalidValue;

@@ -64,19 +64,27 @@ struct FwdParams {
     // n_half_pos heaviest pair positions of every head run as two CTAs per
     // pair, one per Q tile (n_groups * G * n_half_pos more CTAs); 0: none.
     int n_half_pos;
+    // Sliding window (0: none; with it the causal mask): the key at position j
+    // <= i + causal_off is visible when it is one of the last `window` up to
+    // there or j < sinks.  Long query blocks then run one query head per
+    // "group" (rows_per_group = Nq, n_groups = B * Hq), so that no Q tile spans
+    // two heads' windows; a group's K/V are those of KV group group / kv_div.
+    int window, sinks, kv_div;
 };
 
 // Launches the forward kernel for one (D, dtype, causal) instantiation.
 // p.mask != nullptr selects the masked instantiation; tmV16 (with p.vflags)
-// the bf16 instantiation that reads the fp16 copy of V where it exists.
+// the bf16 instantiation that reads the fp16 copy of V where it exists;
+// p.window > 0 (causal, no mask) the sliding-window one.
 cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const FwdParams& p,
                        cudaStream_t stream, const CUtensorMap* tmV16 = nullptr);
 
 // Writes the fp16 copy of a bf16 value tensor [groups][Nk][D] and one flag
-// byte per (group, 128-key tile) (vconv.cu).
+// byte per (group, 128-key tile) (vconv.cu).  Key tiles [skip0, skip1) are left
+// out (those a sliding window never visits).
 cudaError_t launch_v_to_f16(int D, const void* v, void* v16, uint8_t* flags, int64_t groups,
-                            int Nk, cudaStream_t stream);
+                            int Nk, cudaStream_t stream, int skip0 = 0, int skip1 = 0);
 
 // Combines the n_splits partial results of a split forward into out / lse.
 cudaError_t launch_splitkv_merge(int D, bool bf16, const FwdParams& p, cudaStream_t stream);
@@ -119,6 +127,20 @@ struct BwdParams {
     int qtiles_per_split;
     float* dv_part;
     float* dk_part;
+    // Sliding window (0: none; with it the causal mask), as in FwdParams.  The
+    // Q side then runs one query head per group: rows_per_group = Nq, rows_pad
+    // and n_qtiles per head, statistics [B * Hq][rows_pad].  Key tile kt meets
+    // the same query tiles of each of its G heads; the sink tiles [0,
+    // n_sink_tiles), which meet all later ones, and the others are cut into
+    // their own numbers of ranges (wr[0], wr[1]).
+    int window, sinks, causal_off, kv_div;
+    int n_sink_tiles;
+    struct WindowRanges {
+        int key0, keys;    // keys [key0, key0 + keys) of every group
+        int splits;        // query ranges; > 1: fp32 partials [splits][n_groups][keys][D]
+        float* dv_part;
+        float* dk_part;
+    } wr[2];
 };
 
 // Workspace bytes of the backward without the split of dK/dV (the per-row
@@ -127,7 +149,8 @@ size_t bwd_stats_bytes(int B, int Hq, int Hkv, int Nq);
 size_t bwd_split_bytes(int B, int Hkv, int Nk, int D, int splits);
 
 // Launches the three backward kernels (statistics, dK/dV, dQ) in order;
-// p.mask != nullptr selects the masked instantiations.
+// p.mask != nullptr selects the masked instantiations, p.window > 0 the
+// sliding-window ones.
 cudaError_t launch_bwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmDO,
                        const BwdParams& p, cudaStream_t stream);

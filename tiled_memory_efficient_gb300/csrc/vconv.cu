@@ -29,10 +29,11 @@ template <int D>
 __global__ void __launch_bounds__(kConvThreads) v_to_f16_kernel(const uint16_t* __restrict__ v,
                                                                uint16_t* __restrict__ v16,
                                                                uint8_t* __restrict__ flags, int Nk,
-                                                               int n_ktiles) {
+                                                               int n_ktiles, int skip0, int skip1) {
     constexpr int kPer = 128 * D / 8 / kConvThreads;  // 16-byte chunks per thread (4 or 8)
     const int group = static_cast<int>(blockIdx.x / n_ktiles);
     const int kt = static_cast<int>(blockIdx.x % n_ktiles);
+    if (kt >= skip0 && kt < skip1) return;   // no query sees this tile
     const int rows = min(128, Nk - kt * 128);
     const int chunks = rows * (D / 8);
     const int64_t off = (static_cast<int64_t>(group) * Nk + static_cast<int64_t>(kt) * 128) * D;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kConvThreads) v_to_f16_kernel(const uint16_t* 
 }  // namespace
 
 cudaError_t launch_v_to_f16(int D, const void* v, void* v16, uint8_t* flags, int64_t groups, int Nk,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, int skip0, int skip1) {
     const int n_ktiles = (Nk + 127) / 128;
     const long long blocks = groups * n_ktiles;
     if (blocks <= 0 || blocks > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -80,10 +81,12 @@ cudaError_t launch_v_to_f16(int D, const void* v, void* v16, uint8_t* flags, int
     uint16_t* dst = static_cast<uint16_t*>(v16);
     if (D == 128)
         return launch_kernel(v_to_f16_kernel<128>, dim3(static_cast<unsigned>(blocks)),
-                             dim3(kConvThreads), 0, stream, src, dst, flags, Nk, n_ktiles);
+                             dim3(kConvThreads), 0, stream, src, dst, flags, Nk, n_ktiles, skip0,
+                             skip1);
     if (D == 64)
         return launch_kernel(v_to_f16_kernel<64>, dim3(static_cast<unsigned>(blocks)),
-                             dim3(kConvThreads), 0, stream, src, dst, flags, Nk, n_ktiles);
+                             dim3(kConvThreads), 0, stream, src, dst, flags, Nk, n_ktiles, skip0,
+                             skip1);
     return cudaErrorInvalidValue;
 }
 

@@ -10,6 +10,8 @@ for training.  This module provides that surface on GB300:
   the library's kernels;
 * ``scaled_dot_product_attention(...)`` -- the SDPA signature, accepting the
   arguments the kernels implement and raising for the rest;
+* ``window_attention(q, k, v, window, sinks=0, scale=None)`` -- the same for a
+  sliding window whose first tokens stay visible;
 * ``patch()`` / ``unpatch()`` -- opt-in replacement of
   ``torch.nn.functional.scaled_dot_product_attention``.
 
@@ -25,7 +27,7 @@ import torch
 
 from . import _lib
 
-__all__ = ["attention", "scaled_dot_product_attention", "patch", "unpatch", "is_patched"]
+__all__ = ["attention", "window_attention", "scaled_dot_product_attention", "patch", "unpatch", "is_patched"]
 
 _SUPPORTED_D = (64, 128)
 _original_sdpa = None
@@ -79,6 +81,23 @@ class _TiledAttention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
+class _WindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks, scale):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        out, lse = _lib.attn_fwd_window(q, k, v, window, sinks, scale=scale)
+        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.window, ctx.sinks, ctx.scale = window, sinks, scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse = ctx.saved_tensors
+        dq, dk, dv = _lib.attn_bwd_window(q, k, v, out, dout.contiguous(), lse, ctx.window,
+                                          ctx.sinks, scale=ctx.scale)
+        return dq, dk, dv, None, None, None
+
+
 def _validate(q, k, v):
     for name, t in (("query", q), ("key", k), ("value", v)):
         if not isinstance(t, torch.Tensor):
@@ -106,6 +125,21 @@ def attention(q, k, v, is_causal: bool = False, scale: float | None = None, attn
     if attn_mask is not None:
         return _TiledAttentionMasked.apply(q, k, v, attn_mask, bool(is_causal), float(scale))
     return _TiledAttention.apply(q, k, v, bool(is_causal), float(scale))
+
+
+def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None = None):
+    """Differentiable causal attention with a sliding window and sinks.  The Nq
+    queries are the last Nq of the Nk positions; each sees the last `window`
+    positions up to its own and the first `sinks` ones (Nq <= Nk, window >= 1,
+    sinks >= 0).  Layouts, dtypes and GQA as in ``attention``."""
+    _validate(q, k, v)
+    if q.shape[2] > k.shape[2]:
+        raise ValueError(f"{q.shape[2]} queries are more than the {k.shape[2]} positions")
+    if int(window) < 1 or int(sinks) < 0:
+        raise ValueError(f"window must be >= 1 and sinks >= 0, got {window} and {sinks}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return _WindowAttention.apply(q, k, v, int(window), int(sinks), float(scale))
 
 
 def scaled_dot_product_attention(query, key, value, attn_mask=None, dropout_p=0.0,
