@@ -64,7 +64,9 @@ typedef enum {
     ATTN_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed */
     ATTN_ERR_TIMEOUT = 5,     /* a device wait gave up (reported by attn_sync_status) */
     ATTN_ERR_WORKSPACE = 6,   /* workspace too small */
-    ATTN_ERR_MISMATCH = 7     /* a run-time check found two results that must agree differ (ffn.h) */
+    ATTN_ERR_MISMATCH = 7,    /* a run-time check found two results that must agree differ (ffn.h) */
+    ATTN_ERR_PAGE = 8,        /* a page id, length or parent outside the cache met on the device (kvcache.h) */
+    ATTN_ERR_POOL = 9         /* too few free pages, found on the device (kvcache.h) */
 } attn_status_t;
 
 /*
@@ -350,7 +352,8 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* ou
 /*
  * Synchronises `stream`, then returns and clears the device status word of the
  * current device: ATTN_ERR_TIMEOUT if any kernel's bounded wait gave up since
- * the last call, ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
+ * the last call, else ATTN_ERR_PAGE or ATTN_ERR_POOL if a cache call (kvcache.h)
+ * recorded one, ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
  */
 int attn_sync_status(void* stream);
 

@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/attn.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/attn.h, ffn.h and kvcache.h (argument
+marshalling only).
 
 Every step of the computation runs in libattn.so's CUDA kernels; torch is used
 only to own device memory and to name the current stream.  There is no CPU
@@ -16,7 +17,8 @@ import threading
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libattn.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
-HEADERS = [os.path.join(INCLUDE, "attn.h"), os.path.join(INCLUDE, "ffn.h")]
+HEADERS = [os.path.join(INCLUDE, "attn.h"), os.path.join(INCLUDE, "ffn.h"),
+           os.path.join(INCLUDE, "kvcache.h")]
 
 ATTN_OK = 0
 ATTN_ERR_INVALID = 1
@@ -26,6 +28,8 @@ ATTN_ERR_CUDA = 4
 ATTN_ERR_TIMEOUT = 5
 ATTN_ERR_WORKSPACE = 6
 ATTN_ERR_MISMATCH = 7
+ATTN_ERR_PAGE = 8
+ATTN_ERR_POOL = 9
 FFN_ACTS = {"none": 0, "relu": 1, "gelu_tanh": 2, "silu": 3, "swiglu": 4}
 ATTN_F16 = 0
 ATTN_BF16 = 1
@@ -78,6 +82,14 @@ _SIGNATURES = {
                      _vp], _i),
     "ffn_check_chunking": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
                             ctypes.c_size_t, _i, _vp], _i),
+    "kv8_append": ([_vp] * 9 + [_i] * 7 + [ctypes.c_longlong] * 3 + [_i, _vp], _i),
+    "kv8_attn": ([_vp] * 10 + [ctypes.c_size_t] + [_i] * 8 + [ctypes.c_float, _i, _i, _i, _vp], _i),
+    "kv8_attn_workspace_size": ([_i] * 5, ctypes.c_size_t),
+    "kv8_copy_pages": ([_vp] * 7 + [_i] * 6 + [_vp], _i),
+    "kvp_reserve": ([_vp] * 4 + [_i] * 6 + [_vp, _vp, ctypes.c_size_t, _vp], _i),
+    "kvp_reassign": ([_vp] * 4 + [_i] * 4 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
+    "kvp_compact": ([_vp] * 4 + [_i] * 3 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
+    "kvp_workspace_size": ([_i] * 3, ctypes.c_size_t),
     "attn_selftest_timeout": ([ctypes.c_ulonglong, _vp], _i),
     "attn_strerror": ([_i], ctypes.c_char_p),
     "attn_version": ([], _i),
@@ -91,11 +103,11 @@ class AttnError(RuntimeError):
 
 
 def declared_functions() -> list:
-    """Names of the functions include/attn.h and include/ffn.h declare."""
+    """Names of the functions include/attn.h, ffn.h and kvcache.h declare."""
     names = set()
     for h in HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
-        names.update(re.findall(r"\b((?:attn|ffn)_[a-z0-9_]+)\s*\(", text))
+        names.update(re.findall(r"\b((?:attn|ffn|kv8|kvp)_[a-z0-9_]+)\s*\(", text))
     return sorted(names)
 
 
@@ -553,3 +565,208 @@ def ffn_check_chunking(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4
     if rc not in (ATTN_OK, ATTN_ERR_MISMATCH):
         raise AttnError("ffn_check_chunking", rc)
     return y, rc == ATTN_OK
+
+
+# ------------------------------------------------------------------ paged 8-bit KV cache
+
+_BYTE_TYPES = ("torch.float8_e4m3fn", "torch.uint8", "torch.int8")
+
+
+def _check_pages(k_pages, v_pages, k_scale, v_scale, layers=False):
+    """(n_layers, n_pages, Hkv, page, D) of a cache's pools."""
+    dims = 5 if layers and k_pages.dim() == 5 else 4
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not t.is_cuda or not t.is_contiguous() or t.dim() != dims or \
+                str(t.dtype) not in _BYTE_TYPES:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of 8-bit values "
+                             "[n_pages, Hkv, page, D]")
+    if v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
+    import torch
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check_like(name, t, k_pages.shape[:dims - 2], torch.float32)
+    _same_device(k_pages, v_pages, k_scale, v_scale)
+    shape = tuple(k_pages.shape)
+    return shape if dims == 5 else (1,) + shape
+
+
+def _check_ints(like, **tensors):
+    """Contiguous int32 tensors of the given shapes on the device of `like`."""
+    import torch
+    for name, (t, shape) in tensors.items():
+        _check_like(name, t, shape, torch.int32)
+        _same_device(like, t)
+
+
+def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None):
+    """Quantises new keys and values [B, Hkv, T, D] (any strides that are multiples
+    of 8 with dense rows) into the paged cache (include/kvcache.h).  lens [B] are
+    the lengths after the call; n_new [B] how many of the T tokens each sequence
+    takes (None: all T)."""
+    _, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale)
+    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != Hkv \
+            or k.shape[3] != D:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, {Hkv}, T, {D}]")
+    if not k.is_cuda or not v.is_cuda:
+        raise ValueError("k and v must be CUDA tensors")
+    B, _, T, _ = k.shape
+    strides = [tuple(0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3]))
+               for t in (k, v)]
+    if strides[0] != strides[1] or k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("k and v must have the same strides and dense rows")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages]")
+    max_pages = table.shape[1]
+    _check_ints(k, table=(table, (B, max_pages)), lens=(lens, (B,)))
+    if n_new is not None:
+        _check_ints(k, n_new=(n_new, (B,)))
+    _same_device(k, v, k_pages)
+    with _on_device(k):
+        rc = load().kv8_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                               k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                               lens.data_ptr(), _ptr(n_new), B, Hkv, T, D, page, n_pages, max_pages,
+                               *strides[0], _dtype_code(k), _stream_handle(k.device))
+    if rc != ATTN_OK:
+        raise AttnError("kv8_append", rc)
+
+
+def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,
+             window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None):
+    """Attention of the newest Nq positions of each sequence, q [B, Hq, Nq, D], over
+    the paged cache (include/kvcache.h); returns (out, lse)."""
+    import torch
+    _, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale)
+    if q.dim() != 4 or not q.is_cuda or not q.is_contiguous() or q.shape[3] != D:
+        raise ValueError(f"q must be a contiguous CUDA tensor [B, Hq, Nq, {D}]")
+    B, Hq, Nq, _ = q.shape
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages]")
+    max_pages = table.shape[1]
+    _check_ints(q, table=(table, (B, max_pages)), lens=(lens, (B,)))
+    dt = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like("out", out, q.shape, q.dtype)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+    else:
+        _check_like("lse", lse, (B, Hq, Nq), torch.float32)
+    _same_device(q, k_pages, out, lse, workspace)
+    _check_workspace(workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    lib = load()
+    with _on_device(q):
+        if workspace is None:
+            n = lib.kv8_attn_workspace_size(B, Hq, Hkv, Nq, D)
+            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+        rc = lib.kv8_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                          v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+                          lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace), B, Hq, Hkv, Nq,
+                          D, page, n_pages, max_pages, float(scale), min(int(window), 0x7fffffff),
+                          min(int(sinks), 0x7fffffff), dt, _stream_handle(q.device))
+    if rc != ATTN_OK:
+        raise AttnError("kv8_attn", rc)
+    return out, lse
+
+
+def kv8_copy_pages(k_pages, v_pages, k_scale, v_scale, src, dst, count, max_count: int | None = None):
+    """Copies pages src[i] to dst[i] for i < min(count[0], max_count) in every layer
+    of the pools ([n_layers, n_pages, Hkv, page, D], or without layers)."""
+    import torch
+    L, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale, layers=True)
+    _check_ints(k_pages, src=(src, src.shape), dst=(dst, dst.shape))
+    if count.dtype != torch.int32 or count.numel() < 1 or not count.is_cuda:
+        raise ValueError("count must be a CUDA int32 tensor")
+    _same_device(k_pages, count)
+    room = min(src.numel(), dst.numel())
+    max_count = room if max_count is None else int(max_count)
+    if max_count > room:
+        raise ValueError(f"max_count {max_count} is past the {room} listed pairs")
+    with _on_device(k_pages):
+        rc = load().kv8_copy_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                                   v_scale.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                   count.data_ptr(), max_count, L, Hkv, page, D, n_pages,
+                                   _stream_handle(k_pages.device))
+    if rc != ATTN_OK:
+        raise AttnError("kv8_copy_pages", rc)
+
+
+def kvp_workspace_size(n_seqs: int, max_pages: int, n_pages: int) -> int:
+    """Bytes of workspace the page bookkeeping calls need."""
+    return load().kvp_workspace_size(n_seqs, max_pages, n_pages)
+
+
+def _page_args(table, refs, info, workspace):
+    import torch
+    if table.dim() != 2:
+        raise ValueError("table must be [n_seqs, max_pages]")
+    if refs.dim() != 1:
+        raise ValueError("refs must be [n_pages]")
+    n_seqs, max_pages = table.shape
+    _check_ints(table, table=(table, table.shape), refs=(refs, refs.shape), info=(info, (4,)))
+    _check_workspace(workspace)
+    _same_device(table, workspace)
+    if workspace is None:
+        n = kvp_workspace_size(n_seqs, max_pages, refs.numel())
+        workspace = torch.empty(max(n, 16), device=table.device, dtype=torch.uint8)
+    return n_seqs, max_pages, refs.numel(), workspace
+
+
+def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sinks: int = 0,
+                workspace=None):
+    """Adds n_new [n_seqs] tokens to the sequences' lengths and pages for them to
+    their tables; with a window first gives back the pages it has left behind
+    (include/kvcache.h).  info [4] int32 receives (done, taken, given back, free)."""
+    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
+    _check_ints(table, lens=(lens, (n_seqs,)), n_new=(n_new, (n_seqs,)))
+    with _on_device(table):
+        rc = load().kvp_reserve(table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                                n_new.data_ptr(), n_seqs, max_pages, n_pages, int(page),
+                                min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff),
+                                info.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                                _stream_handle(table.device))
+    if rc != ATTN_OK:
+        raise AttnError("kvp_reserve", rc)
+
+
+def kvp_reassign(table, lens, refs, parents, page: int, copy_src, copy_dst, info, workspace=None):
+    """Sequence c becomes what parents[c] was (c: kept, -1: freed); the pairs of
+    pages to copy go to copy_src / copy_dst, info [4] int32 receives (done, pairs,
+    given back, free) (include/kvcache.h)."""
+    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
+    _check_ints(table, lens=(lens, (n_seqs,)), parents=(parents, (n_seqs,)),
+                copy_src=(copy_src, copy_src.shape), copy_dst=(copy_dst, copy_dst.shape))
+    if copy_src.numel() < n_seqs or copy_dst.numel() < n_seqs:
+        raise ValueError(f"copy_src and copy_dst need {n_seqs} entries")
+    with _on_device(table):
+        rc = load().kvp_reassign(table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                                 parents.data_ptr(), n_seqs, max_pages, n_pages, int(page),
+                                 copy_src.data_ptr(), copy_dst.data_ptr(), info.data_ptr(),
+                                 workspace.data_ptr(), _nbytes(workspace),
+                                 _stream_handle(table.device))
+    if rc != ATTN_OK:
+        raise AttnError("kvp_reassign", rc)
+
+
+def kvp_compact(table, refs, move_src, move_dst, info, table_out=None, refs_out=None,
+                workspace=None):
+    """Renumbers the held pages to the front of the pool (in place without table_out
+    and refs_out); the moves go to move_src / move_dst, info [4] int32 receives (1,
+    moves, held, free) (include/kvcache.h)."""
+    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
+    table_out = table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    _check_ints(table, table_out=(table_out, table.shape), refs_out=(refs_out, refs.shape),
+                move_src=(move_src, move_src.shape), move_dst=(move_dst, move_dst.shape))
+    if min(move_src.numel(), move_dst.numel()) < n_pages // 2:
+        raise ValueError(f"move_src and move_dst need {n_pages // 2} entries")
+    with _on_device(table):
+        rc = load().kvp_compact(table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
+                                refs_out.data_ptr(), n_seqs, max_pages, n_pages,
+                                move_src.data_ptr(), move_dst.data_ptr(), info.data_ptr(),
+                                workspace.data_ptr(), _nbytes(workspace),
+                                _stream_handle(table.device))
+    if rc != ATTN_OK:
+        raise AttnError("kvp_compact", rc)

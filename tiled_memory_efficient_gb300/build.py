@@ -19,7 +19,7 @@ LIB = os.path.join(BUILD, "libattn.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["abi.cu", "attn_fwd.cu", "attn_bwd.cu", "bwd_noalloc.cu", "splitkv.cu", "ffn.cu",
-           "vconv.cu"]
+           "vconv.cu", "kv8.cu", "kvp.cu"]
 HEADERS = ["ptx.cuh", "attn_internal.h", "bias.cuh", "window.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,7 +36,7 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h")]
+    files += [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h", "kvcache.h")]
     return max(os.path.getmtime(f) for f in files)
 
 

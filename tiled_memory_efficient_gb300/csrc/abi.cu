@@ -132,8 +132,24 @@ __global__ void selftest_timeout_kernel(unsigned long long wait_ns, unsigned int
 
 }  // namespace
 
-// For the other translation units of the library (ffn.cu).
+// For the other translation units of the library (ffn.cu, kv8.cu, kvp.cu).
 int device_setup_public(unsigned int** status) { return device_setup(status); }
+// 3-D map over [groups][rows][D] bytes, boxes of D columns x box_rows rows x 1
+// group, swizzled over the row (D = 64 or 128 bytes), zero fill outside.
+int make_byte_map_public(CUtensorMap* map, const void* base, int D, int rows, int64_t groups,
+                         int box_rows) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows) * D};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r =
+        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
 int make_map_public(CUtensorMap* map, const void* base, bool bf16, int cols, int64_t rows,
                     int64_t groups) {
     return make_map(map, base, bf16, cols, rows, groups);
@@ -1093,7 +1109,10 @@ extern "C" int attn_sync_status(void* stream) {
         if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
             return ATTN_ERR_CUDA;
     }
-    return (word & kStatusTimeout) ? ATTN_ERR_TIMEOUT : ATTN_OK;
+    return (word & kStatusTimeout) ? ATTN_ERR_TIMEOUT
+           : (word & kStatusPage)  ? ATTN_ERR_PAGE
+           : (word & kStatusPool)  ? ATTN_ERR_POOL
+                                   : ATTN_OK;
 }
 
 extern "C" int attn_selftest_timeout(unsigned long long wait_ns, void* stream) {
@@ -1118,6 +1137,8 @@ extern "C" const char* attn_strerror(int status) {
         case ATTN_ERR_TIMEOUT: return "a device-side wait timed out";
         case ATTN_ERR_WORKSPACE: return "workspace too small";
         case ATTN_ERR_MISMATCH: return "results that must agree differ";
+        case ATTN_ERR_PAGE: return "a page id, length or parent outside the cache";
+        case ATTN_ERR_POOL: return "too few free pages";
         default: return "unknown status";
     }
 }

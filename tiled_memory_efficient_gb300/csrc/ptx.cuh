@@ -14,7 +14,11 @@ namespace tme {
 
 // Device status word (one per library, passed to every kernel):
 // bit 0 = an mbarrier wait timed out.
+// bit 1 = a page id, length, count or parent that does not fit the cache;
+// bit 2 = a page pool with too few free pages.
 constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusPage = 2u;
+constexpr unsigned kStatusPool = 4u;
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 
