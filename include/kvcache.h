@@ -75,7 +75,7 @@ int kv8_append(const void* k, const void* v, void* k_pages, void* v_pages, float
  * on the device from lens, so mixed lengths are balanced without the host.
  * The keys' part of the arithmetic is exact in fp16 (e4m3 fits), scores, softmax
  * statistics and sums are fp32, the softmax terms of the value product fp16.
- * B <= 2048.  workspace: kv8_attn_workspace_size() bytes.
+ * B <= 1024.  workspace: kv8_attn_workspace_size() bytes.
  */
 int kv8_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
              const float* v_scale, const int* table, const int* lens, void* out, float* lse,

@@ -35,7 +35,7 @@ ATTN = dict(q=P, kp=P, vp=P, ks=P, vs=P, table=P, lens=P, out=P, lse=P, ws=P, n=
     ({"q": 0}, 1), ({"vs": 0}, 1), ({"ws": 0}, 1), ({"B": 0}, 1), ({"Hq": 3}, 1), ({"Nq": 0}, 1),
     ({"D": 96}, 2), ({"page": 48}, 2), ({"page": 0}, 1), ({"n_pages": 0}, 1), ({"max_pages": 0}, 1),
     ({"scale": 0.0}, 1), ({"scale": float("inf")}, 1), ({"window": -1}, 1), ({"sinks": -1}, 1),
-    ({"dtype": 3}, 1), ({"kp": P + 8}, 3), ({"lens": P + 2}, 3), ({"n": 16}, 6), ({"B": 2049}, 2),
+    ({"dtype": 3}, 1), ({"kp": P + 8}, 3), ({"lens": P + 2}, 3), ({"n": 16}, 6), ({"B": 1025}, 2),
     ({"max_pages": 1 << 25}, 2), ({"n_pages": 1 << 30}, 2),
 ])
 def test_attention_refusals(lib, change, code):

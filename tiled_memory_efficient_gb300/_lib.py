@@ -9,6 +9,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -354,19 +355,12 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
     return out, lse
 
 
-def _same_device(first, *others):
-    """Every tensor lives on the device of the first."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
-
-
 class _on_device:
-    """Makes a tensor's device current for a call (nothing to do when it is)."""
+    """Makes a device current for a call (nothing to do when it is)."""
     __slots__ = ("index", "prev")
 
-    def __init__(self, t):
-        self.index = t.device.index
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
         import torch
@@ -380,23 +374,70 @@ class _on_device:
             torch.cuda.set_device(self.prev)
 
 
-def _check_like(name, t, shape, dtype):
-    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+def _call(fn: str, dev: int, *args):
+    """lib.fn(*args, current stream) with device `dev` current; raises on an error.
+    (The calls below take a few microseconds on the GPU for a decoding step, so
+    this side is kept short: one test per tensor, and only one that fails is
+    looked at again to say why.)"""
+    import torch
+    f = getattr(_lib or load(), fn)
+    try:
+        stream = torch._C._cuda_getCurrentRawStream(dev)   # what current_stream() wraps
+    except AttributeError:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, stream)
+    else:
+        with _on_device(dev):
+            rc = f(*args, stream)
+    if rc != ATTN_OK:
+        raise AttnError(fn, rc)
 
 
-def _check_workspace(t):
-    if t is not None and not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+def _fits(t, shape, dtype, dev) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _need(name, t, shape, dtype, dev):
+    """Raises unless t is a contiguous tensor of that shape and dtype on CUDA device dev."""
+    if not _fits(t, shape, dtype, dev):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"CUDA device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _workspace(workspace, size: int, dev: int):
+    """The caller's workspace after a look at it, or a new one (None: none needed)."""
+    import torch
+    if workspace is None:
+        return torch.empty(size, device=dev, dtype=torch.uint8) if size > 0 else None
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
+    return workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _size_on(dev: int, fn: str, *args) -> int:
+    """A workspace size (a function of the sizes and the device alone)."""
+    with _on_device(dev):
+        return getattr(load(), fn)(*args)
 
 
 def _window_args(q, k, v, window, sinks, scale):
-    _check(q, k, v)
-    _same_device(q, k, v)
+    """Device, dtype code, sizes and clamped window of a sliding-window call."""
+    dev, dt = q.get_device(), q.dtype
+    if not (dev >= 0 and q.dim() == 4 and k.dim() == 4 and k.dtype is dt and v.dtype is dt
+            and v.shape == k.shape and k.shape[0] == q.shape[0] and k.shape[3] == q.shape[3]
+            and k.get_device() == dev and v.get_device() == dev and q.is_contiguous()
+            and k.is_contiguous() and v.is_contiguous()):
+        _check(q, k, v)
+        raise ValueError(f"tensors on {q.device}, {k.device} and {v.device}: one device is needed")
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
     if scale is None:
-        scale = 1.0 / math.sqrt(q.shape[3])
+        scale = 1.0 / math.sqrt(D)
     # the C ABI takes 32-bit counts; either may exceed the keys
-    return min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff), float(scale)
+    return (dev, _dtype_code(q), (B, Hq, Hkv, Nq, Nk, D), float(scale),
+            min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff))
 
 
 def attn_fwd_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None,
@@ -406,31 +447,19 @@ def attn_fwd_window(q, k, v, window: int, sinks: int = 0, scale: float | None = 
     Returns (out, lse) as attn_fwd does; workspace (allocated here when not
     given) as in include/attn.h."""
     import torch
-    window, sinks, scale = _window_args(q, k, v, window, sinks, scale)
-    B, Hq, Nq, D = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    dt = _dtype_code(q)
+    dev, dt, sizes, scale, window, sinks = _window_args(q, k, v, window, sinks, scale)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_like("out", out, q.shape, q.dtype)
+        _need("out", out, q.shape, q.dtype, dev)
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+        lse = torch.empty(q.shape[:3], device=dev, dtype=torch.float32)
     else:
-        _check_like("lse", lse, (B, Hq, Nq), torch.float32)
-    _same_device(q, out, lse, workspace)
-    _check_workspace(workspace)
-    lib = load()
-    with _on_device(q):
-        if workspace is None:
-            n = lib.attn_fwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, dt)
-            if n > 0:
-                workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
-        rc = lib.attn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), _ptr(workspace), _nbytes(workspace), B, Hq, Hkv,
-                                 Nq, Nk, D, scale, window, sinks, dt, _stream_handle(q.device))
-    if rc != ATTN_OK:
-        raise AttnError("attn_fwd_window", rc)
+        _need("lse", lse, q.shape[:3], torch.float32, dev)
+    ws = _workspace(workspace, _size_on(dev, "attn_fwd_window_workspace_size", *sizes, window, sinks,
+                                        dt), dev)
+    _call("attn_fwd_window", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), _ptr(ws), _nbytes(ws), *sizes, scale, window, sinks, dt)
     return out, lse
 
 
@@ -438,34 +467,22 @@ def attn_bwd_window(q, k, v, out, dout, lse, window: int, sinks: int = 0,
                     scale: float | None = None, dq=None, dk=None, dv=None, workspace=None):
     """dq, dk, dv of attn_fwd_window (dk, dv summed over each GQA group)."""
     import torch
-    window, sinks, scale = _window_args(q, k, v, window, sinks, scale)
-    B, Hq, Nq, D = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    dt = _dtype_code(q)
-    _check_like("out", out, q.shape, q.dtype)
-    _check_like("dout", dout, q.shape, q.dtype)
-    _check_like("lse", lse, (B, Hq, Nq), torch.float32)
+    dev, dt, sizes, scale, window, sinks = _window_args(q, k, v, window, sinks, scale)
+    _need("out", out, q.shape, q.dtype, dev)
+    _need("dout", dout, q.shape, q.dtype, dev)
+    _need("lse", lse, q.shape[:3], torch.float32, dev)
     grads = []
     for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if g is None:
             g = torch.empty_like(like)
         else:
-            _check_like(name, g, like.shape, like.dtype)
+            _need(name, g, like.shape, like.dtype, dev)
         grads.append(g)
-    _same_device(q, out, dout, lse, workspace, *grads)
-    _check_workspace(workspace)
-    lib = load()
-    with _on_device(q):
-        if workspace is None:
-            n = lib.attn_bwd_window_workspace_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, dt)
-            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-        rc = lib.attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(),
-                                 grads[1].data_ptr(), grads[2].data_ptr(), workspace.data_ptr(),
-                                 _nbytes(workspace), B, Hq, Hkv, Nq, Nk, D, scale, window, sinks,
-                                 dt, _stream_handle(q.device))
-    if rc != ATTN_OK:
-        raise AttnError("attn_bwd_window", rc)
+    ws = _workspace(workspace, max(16, _size_on(dev, "attn_bwd_window_workspace_size", *sizes, window,
+                                                sinks, dt)), dev)
+    _call("attn_bwd_window", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
+          grads[2].data_ptr(), ws.data_ptr(), _nbytes(ws), *sizes, scale, window, sinks, dt)
     return tuple(grads)
 
 
@@ -569,33 +586,25 @@ def ffn_check_chunking(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4
 
 # ------------------------------------------------------------------ paged 8-bit KV cache
 
-_BYTE_TYPES = ("torch.float8_e4m3fn", "torch.uint8", "torch.int8")
-
-
-def _check_pages(k_pages, v_pages, k_scale, v_scale, layers=False):
-    """(n_layers, n_pages, Hkv, page, D) of a cache's pools."""
-    dims = 5 if layers and k_pages.dim() == 5 else 4
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not t.is_cuda or not t.is_contiguous() or t.dim() != dims or \
-                str(t.dtype) not in _BYTE_TYPES:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of 8-bit values "
-                             "[n_pages, Hkv, page, D]")
-    if v_pages.shape != k_pages.shape:
-        raise ValueError(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
+def _pools(k_pages, v_pages, k_scale, v_scale, dev):
+    """Looks a cache's pools over: [n_pages, Hkv, page, D], or with a leading layer
+    dimension, 8-bit; scales of all but the last two."""
     import torch
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check_like(name, t, k_pages.shape[:dims - 2], torch.float32)
-    _same_device(k_pages, v_pages, k_scale, v_scale)
-    shape = tuple(k_pages.shape)
-    return shape if dims == 5 else (1,) + shape
+    shape, dt = k_pages.shape, k_pages.dtype
+    if not (len(shape) in (4, 5) and dt in (torch.float8_e4m3fn, torch.uint8, torch.int8)
+            and k_pages.get_device() == dev >= 0 and k_pages.is_contiguous()):
+        raise ValueError("k_pages must be a contiguous tensor of 8-bit values [n_pages, Hkv, page, D] "
+                         f"on CUDA device {dev}, not {dt} {tuple(shape)} on {k_pages.device}")
+    _need("v_pages", v_pages, shape, dt, dev)
+    _need("k_scale", k_scale, shape[:-2], torch.float32, dev)
+    _need("v_scale", v_scale, shape[:-2], torch.float32, dev)
+    return shape
 
 
-def _check_ints(like, **tensors):
-    """Contiguous int32 tensors of the given shapes on the device of `like`."""
-    import torch
-    for name, (t, shape) in tensors.items():
-        _check_like(name, t, shape, torch.int32)
-        _same_device(like, t)
+def _layer(shape):
+    if len(shape) != 4:
+        raise ValueError(f"the pools {tuple(shape)} must be one layer's [n_pages, Hkv, page, D]")
+    return shape
 
 
 def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None):
@@ -603,31 +612,36 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
     of 8 with dense rows) into the paged cache (include/kvcache.h).  lens [B] are
     the lengths after the call; n_new [B] how many of the T tokens each sequence
     takes (None: all T)."""
-    _, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale)
-    if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != Hkv \
-            or k.shape[3] != D:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, {Hkv}, T, {D}]")
-    if not k.is_cuda or not v.is_cuda:
-        raise ValueError("k and v must be CUDA tensors")
+    import torch
+    dev = k.get_device()
+    n_pages, Hkv, page, D = _layer(_pools(k_pages, v_pages, k_scale, v_scale, dev))
+    if not (k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and k.shape[1] == Hkv
+            and k.shape[3] == D and v.get_device() == dev):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, {Hkv}, T, {D}] on "
+                         "one device")
     B, _, T, _ = k.shape
-    strides = [tuple(0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3]))
-               for t in (k, v)]
-    if strides[0] != strides[1] or k.stride(3) != 1 or v.stride(3) != 1:
-        raise ValueError("k and v must have the same strides and dense rows")
+    sb, sh, st, sd = k.stride()
+    if v.stride() != (sb, sh, st, sd) or sd != 1:
+        # strides of dimensions of size 1 do not matter
+        strides = [tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride())) for t in (k, v)]
+        if strides[0] != strides[1] or sd != 1 or v.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and dense rows")
+    if B == 1:
+        sb = 0
+    if Hkv == 1:
+        sh = 0
+    if T == 1:
+        st = 0
     if table.dim() != 2:
         raise ValueError("table must be [B, max_pages]")
     max_pages = table.shape[1]
-    _check_ints(k, table=(table, (B, max_pages)), lens=(lens, (B,)))
+    _need("table", table, (B, max_pages), torch.int32, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
     if n_new is not None:
-        _check_ints(k, n_new=(n_new, (B,)))
-    _same_device(k, v, k_pages)
-    with _on_device(k):
-        rc = load().kv8_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                               k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
-                               lens.data_ptr(), _ptr(n_new), B, Hkv, T, D, page, n_pages, max_pages,
-                               *strides[0], _dtype_code(k), _stream_handle(k.device))
-    if rc != ATTN_OK:
-        raise AttnError("kv8_append", rc)
+        _need("n_new", n_new, (B,), torch.int32, dev)
+    _call("kv8_append", dev, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(n_new), B,
+          Hkv, T, D, page, n_pages, max_pages, sb, sh, st, _dtype_code(k))
 
 
 def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,
@@ -635,39 +649,32 @@ def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | 
     """Attention of the newest Nq positions of each sequence, q [B, Hq, Nq, D], over
     the paged cache (include/kvcache.h); returns (out, lse)."""
     import torch
-    _, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale)
-    if q.dim() != 4 or not q.is_cuda or not q.is_contiguous() or q.shape[3] != D:
+    dev = q.get_device()
+    n_pages, Hkv, page, D = _layer(_pools(k_pages, v_pages, k_scale, v_scale, dev))
+    if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous CUDA tensor [B, Hq, Nq, {D}]")
     B, Hq, Nq, _ = q.shape
     if table.dim() != 2:
         raise ValueError("table must be [B, max_pages]")
     max_pages = table.shape[1]
-    _check_ints(q, table=(table, (B, max_pages)), lens=(lens, (B,)))
+    _need("table", table, (B, max_pages), torch.int32, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
     dt = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_like("out", out, q.shape, q.dtype)
+        _need("out", out, q.shape, q.dtype, dev)
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+        lse = torch.empty(q.shape[:3], device=dev, dtype=torch.float32)
     else:
-        _check_like("lse", lse, (B, Hq, Nq), torch.float32)
-    _same_device(q, k_pages, out, lse, workspace)
-    _check_workspace(workspace)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    lib = load()
-    with _on_device(q):
-        if workspace is None:
-            n = lib.kv8_attn_workspace_size(B, Hq, Hkv, Nq, D)
-            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-        rc = lib.kv8_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-                          v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
-                          lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace), B, Hq, Hkv, Nq,
-                          D, page, n_pages, max_pages, float(scale), min(int(window), 0x7fffffff),
-                          min(int(sinks), 0x7fffffff), dt, _stream_handle(q.device))
-    if rc != ATTN_OK:
-        raise AttnError("kv8_attn", rc)
+        _need("lse", lse, q.shape[:3], torch.float32, dev)
+    ws = _workspace(workspace, max(16, _size_on(dev, "kv8_attn_workspace_size", B, Hq, Hkv, Nq, D)),
+                    dev)
+    _call("kv8_attn", dev, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          ws.data_ptr(), _nbytes(ws), B, Hq, Hkv, Nq, D, page, n_pages, max_pages,
+          1.0 / math.sqrt(D) if scale is None else float(scale), min(int(window), 0x7fffffff),
+          min(int(sinks), 0x7fffffff), dt)
     return out, lse
 
 
@@ -675,22 +682,20 @@ def kv8_copy_pages(k_pages, v_pages, k_scale, v_scale, src, dst, count, max_coun
     """Copies pages src[i] to dst[i] for i < min(count[0], max_count) in every layer
     of the pools ([n_layers, n_pages, Hkv, page, D], or without layers)."""
     import torch
-    L, n_pages, Hkv, page, D = _check_pages(k_pages, v_pages, k_scale, v_scale, layers=True)
-    _check_ints(k_pages, src=(src, src.shape), dst=(dst, dst.shape))
-    if count.dtype != torch.int32 or count.numel() < 1 or not count.is_cuda:
-        raise ValueError("count must be a CUDA int32 tensor")
-    _same_device(k_pages, count)
+    dev = k_pages.get_device()
+    shape = _pools(k_pages, v_pages, k_scale, v_scale, dev)
+    n_pages, Hkv, page, D = shape[-4:]
+    _need("src", src, src.shape, torch.int32, dev)
+    _need("dst", dst, dst.shape, torch.int32, dev)
+    if count.dtype is not torch.int32 or count.numel() < 1 or count.get_device() != dev:
+        raise ValueError(f"count must be an int32 tensor on CUDA device {dev}")
     room = min(src.numel(), dst.numel())
     max_count = room if max_count is None else int(max_count)
     if max_count > room:
         raise ValueError(f"max_count {max_count} is past the {room} listed pairs")
-    with _on_device(k_pages):
-        rc = load().kv8_copy_pages(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-                                   v_scale.data_ptr(), src.data_ptr(), dst.data_ptr(),
-                                   count.data_ptr(), max_count, L, Hkv, page, D, n_pages,
-                                   _stream_handle(k_pages.device))
-    if rc != ATTN_OK:
-        raise AttnError("kv8_copy_pages", rc)
+    _call("kv8_copy_pages", dev, k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), src.data_ptr(), dst.data_ptr(), count.data_ptr(), max_count,
+          shape[0] if len(shape) == 5 else 1, Hkv, page, D, n_pages)
 
 
 def kvp_workspace_size(n_seqs: int, max_pages: int, n_pages: int) -> int:
@@ -699,19 +704,21 @@ def kvp_workspace_size(n_seqs: int, max_pages: int, n_pages: int) -> int:
 
 
 def _page_args(table, refs, info, workspace):
+    """Device, sizes and workspace of a bookkeeping call."""
     import torch
-    if table.dim() != 2:
-        raise ValueError("table must be [n_seqs, max_pages]")
-    if refs.dim() != 1:
-        raise ValueError("refs must be [n_pages]")
+    dev = table.get_device()
+    if table.dim() != 2 or refs.dim() != 1 or dev < 0:
+        raise ValueError("table must be a CUDA tensor [n_seqs, max_pages], refs [n_pages]")
     n_seqs, max_pages = table.shape
-    _check_ints(table, table=(table, table.shape), refs=(refs, refs.shape), info=(info, (4,)))
-    _check_workspace(workspace)
-    _same_device(table, workspace)
+    n_pages = refs.shape[0]
+    _need("table", table, table.shape, torch.int32, dev)
+    _need("refs", refs, refs.shape, torch.int32, dev)
+    _need("info", info, (4,), torch.int32, dev)
     if workspace is None:
-        n = kvp_workspace_size(n_seqs, max_pages, refs.numel())
-        workspace = torch.empty(max(n, 16), device=table.device, dtype=torch.uint8)
-    return n_seqs, max_pages, refs.numel(), workspace
+        size = max(16, kvp_workspace_size(n_seqs, max_pages, n_pages))
+    else:
+        size = 0
+    return dev, n_seqs, max_pages, n_pages, _workspace(workspace, size, dev)
 
 
 def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sinks: int = 0,
@@ -719,35 +726,30 @@ def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sink
     """Adds n_new [n_seqs] tokens to the sequences' lengths and pages for them to
     their tables; with a window first gives back the pages it has left behind
     (include/kvcache.h).  info [4] int32 receives (done, taken, given back, free)."""
-    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
-    _check_ints(table, lens=(lens, (n_seqs,)), n_new=(n_new, (n_seqs,)))
-    with _on_device(table):
-        rc = load().kvp_reserve(table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-                                n_new.data_ptr(), n_seqs, max_pages, n_pages, int(page),
-                                min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff),
-                                info.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-                                _stream_handle(table.device))
-    if rc != ATTN_OK:
-        raise AttnError("kvp_reserve", rc)
+    import torch
+    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
+    _need("lens", lens, (n_seqs,), torch.int32, dev)
+    _need("n_new", n_new, (n_seqs,), torch.int32, dev)
+    _call("kvp_reserve", dev, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), n_new.data_ptr(),
+          n_seqs, max_pages, n_pages, int(page), min(int(window), 0x7fffffff),
+          min(int(sinks), 0x7fffffff), info.data_ptr(), ws.data_ptr(), _nbytes(ws))
 
 
 def kvp_reassign(table, lens, refs, parents, page: int, copy_src, copy_dst, info, workspace=None):
     """Sequence c becomes what parents[c] was (c: kept, -1: freed); the pairs of
     pages to copy go to copy_src / copy_dst, info [4] int32 receives (done, pairs,
     given back, free) (include/kvcache.h)."""
-    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
-    _check_ints(table, lens=(lens, (n_seqs,)), parents=(parents, (n_seqs,)),
-                copy_src=(copy_src, copy_src.shape), copy_dst=(copy_dst, copy_dst.shape))
+    import torch
+    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
+    _need("lens", lens, (n_seqs,), torch.int32, dev)
+    _need("parents", parents, (n_seqs,), torch.int32, dev)
+    _need("copy_src", copy_src, copy_src.shape, torch.int32, dev)
+    _need("copy_dst", copy_dst, copy_dst.shape, torch.int32, dev)
     if copy_src.numel() < n_seqs or copy_dst.numel() < n_seqs:
         raise ValueError(f"copy_src and copy_dst need {n_seqs} entries")
-    with _on_device(table):
-        rc = load().kvp_reassign(table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-                                 parents.data_ptr(), n_seqs, max_pages, n_pages, int(page),
-                                 copy_src.data_ptr(), copy_dst.data_ptr(), info.data_ptr(),
-                                 workspace.data_ptr(), _nbytes(workspace),
-                                 _stream_handle(table.device))
-    if rc != ATTN_OK:
-        raise AttnError("kvp_reassign", rc)
+    _call("kvp_reassign", dev, table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+          parents.data_ptr(), n_seqs, max_pages, n_pages, int(page), copy_src.data_ptr(),
+          copy_dst.data_ptr(), info.data_ptr(), ws.data_ptr(), _nbytes(ws))
 
 
 def kvp_compact(table, refs, move_src, move_dst, info, table_out=None, refs_out=None,
@@ -755,18 +757,16 @@ def kvp_compact(table, refs, move_src, move_dst, info, table_out=None, refs_out=
     """Renumbers the held pages to the front of the pool (in place without table_out
     and refs_out); the moves go to move_src / move_dst, info [4] int32 receives (1,
     moves, held, free) (include/kvcache.h)."""
-    n_seqs, max_pages, n_pages, workspace = _page_args(table, refs, info, workspace)
+    import torch
+    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
-    _check_ints(table, table_out=(table_out, table.shape), refs_out=(refs_out, refs.shape),
-                move_src=(move_src, move_src.shape), move_dst=(move_dst, move_dst.shape))
+    _need("table_out", table_out, table.shape, torch.int32, dev)
+    _need("refs_out", refs_out, refs.shape, torch.int32, dev)
+    _need("move_src", move_src, move_src.shape, torch.int32, dev)
+    _need("move_dst", move_dst, move_dst.shape, torch.int32, dev)
     if min(move_src.numel(), move_dst.numel()) < n_pages // 2:
         raise ValueError(f"move_src and move_dst need {n_pages // 2} entries")
-    with _on_device(table):
-        rc = load().kvp_compact(table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
-                                refs_out.data_ptr(), n_seqs, max_pages, n_pages,
-                                move_src.data_ptr(), move_dst.data_ptr(), info.data_ptr(),
-                                workspace.data_ptr(), _nbytes(workspace),
-                                _stream_handle(table.device))
-    if rc != ATTN_OK:
-        raise AttnError("kvp_compact", rc)
+    _call("kvp_compact", dev, table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
+          refs_out.data_ptr(), n_seqs, max_pages, n_pages, move_src.data_ptr(),
+          move_dst.data_ptr(), info.data_ptr(), ws.data_ptr(), _nbytes(ws))

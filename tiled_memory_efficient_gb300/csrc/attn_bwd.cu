@@ -1157,25 +1157,6 @@ __global__ void __launch_bounds__(256) bwd_dkdv_reduce_kernel(const BwdParams p,
     }
 }
 
-// Launch as a programmatic dependent of the previous kernel in the stream:
-// the grid may start before that kernel has ended, and waits for it on the
-// device (griddepcontrol.wait) where it needs its results.
-template <typename Kern, typename... Args>
-cudaError_t launch_dependent(Kern kern, long long ctas, int threads, int smem,
-                             cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, bool BF16, bool CAUSAL, int MK>
 cudaError_t launch_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                       const CUtensorMap& tmDO, const BwdParams& p, cudaStream_t stream) {

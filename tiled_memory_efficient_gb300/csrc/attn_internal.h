@@ -18,6 +18,25 @@ inline cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block,
     return cudaLaunchKernel(reinterpret_cast<const void*>(kern), grid, block, ptrs, smem, stream);
 }
 
+// Launch as a programmatic dependent of the previous kernel in the stream:
+// the grid may start before that kernel has ended, and waits for it on the
+// device (griddepcontrol.wait) where it needs its results.
+template <typename Kern, typename... Args>
+inline cudaError_t launch_dependent(Kern kern, long long ctas, int threads, int smem,
+                             cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Forward launch parameters (everything the kernel needs besides the three
 // tensor maps).  Row indices are "flattened": within KV group g of batch b the
 // G query heads that share that KV head form G*Nq consecutive rows, head-major.

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     constexpr int NV = PAGE * D / 8 / kAppendThreads;
     static_assert(NV >= 1, "a thread holds at least one vector");
     constexpr int VPT = D / 8;   // vectors per token
+    asm volatile("griddepcontrol.launch_dependents;");   // the attention may set up meanwhile
     int64_t id = blockIdx.x;
     const int which = static_cast<int>(id & 1);
     id >>= 1;
@@ -205,7 +206,7 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 
 // ------------------------------------------------------------------ attention
 //
-// Work is counted in tiles of 32 tokens: sequence b has n_b visible ones (its sink
+// Work is counted in tiles of 32 or 64 tokens: sequence b has n_b visible ones (its sink
 // tiles and then its window's, or all) for each of its U = Hkv * row blocks
 // units.  The CTAs of one wave cut the concatenation of all (sequence, unit)
 // lists into equal shares, so the balance does not depend on the lengths; a unit
@@ -215,21 +216,23 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 // Inside a CTA every warp works on its own: tiles w, w + 8, ... of the share,
 // through a ring of kStages (K, V) slots that it alone fills (TMA, an mbarrier
 // each) and empties, so warps meet only where a unit ends.  Lane s owns slot s:
-// it follows the slot's tiles through the table and issues their copies.
+// it follows the slot's tiles through the table, a tile ahead of the copies it
+// issues, so that no copy waits for its page id.
 //
 // Products run on mma.sync m16n8k16 with the tokens (scores) or the head
 // dimensions (output) as its 16 rows and up to 8 query rows as its columns:
 // S^T = K Q^T, O^T += V^T P^T.  The tensor core is not what bounds this kernel (a
 // tile of 32 tokens is 8 KB at D = 128, about 180 cycles of one SM's share of the
 // memory, and 32 small products), and registers hold P between the two products.
+// With 32 query rows Q comes from shared memory instead of registers, which the
+// accumulators fill.
 // K and V become fp16 exactly (e4m3x2 -> f16x2); the dimensions of a K row and
 // the tokens of a V column may meet the product in any order that its other
 // operand shares, which is how 16-byte shared loads feed both (kTok below).
 
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr int kTile = 32;         // tokens per tile
-constexpr int kMaxBatch = 2048;   // sequences per call (their tile counts live in shared memory)
+constexpr int kMaxBatch = 1024;   // sequences per call (their tile counts live in shared memory)
 constexpr int kMinShare = kWarps; // tiles per CTA, at least (one per warp)
 
 struct AttnParams {
@@ -244,8 +247,8 @@ struct AttnParams {
     float* part_lse;   // [2 * ctas][rows of a block], log2 domain
     unsigned int* status;
     int B, Hkv, rows, n_rb;   // rows = G * Nq of a KV head, row blocks
-    int Nq, page, n_pages, max_pages;
-    int window, sinks, ctas;
+    int Nq, page_shift, n_pages, max_pages;
+    int window, sinks, ctas, tile_shift;
     float scale_log2;
 };
 
@@ -257,17 +260,18 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const AttnParams& p, int len) {
     Seq s;
-    s.len = min(max(len, 0), p.max_pages * p.page);
+    const int up = (1 << p.tile_shift) - 1;
+    s.len = min(max(len, 0), p.max_pages << p.page_shift);
     s.first = s.len - p.Nq;
     s.lo = p.window > 0 ? max(s.first - p.window + 1, 0) : 0;
-    const int lo_tile = s.lo / kTile;
-    s.n_sink = min((p.sinks + kTile - 1) / kTile, lo_tile);
+    const int lo_tile = s.lo >> p.tile_shift;
+    s.n_sink = min((p.sinks + up) >> p.tile_shift, lo_tile);
     s.skip = lo_tile - s.n_sink;
-    s.n = (s.len + kTile - 1) / kTile - s.skip;
+    s.n = ((s.len + up) >> p.tile_shift) - s.skip;
     return s;
 }
-__device__ __forceinline__ int seq_token(const Seq& s, int v) {   // first token of tile v of the list
-    return (v < s.n_sink ? v : v + s.skip) * kTile;
+__device__ __forceinline__ int seq_tile(const Seq& s, int v) {   // tile v of the list
+    return v < s.n_sink ? v : v + s.skip;
 }
 
 // Shares: CTA c takes [c T / n, (c + 1) T / n) of the T tiles, n CTAs.
@@ -313,26 +317,57 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return r;
 }
 
-template <int D>
+// 4-byte asynchronous copy global -> shared, and an arrival on a barrier once this
+// thread's copies so far have landed (the barrier counts it).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// What a slot's lane leaves beside its tile: the scales and page ids of its 16-token
+// quarters' boxes (up to 4), and which boxes hold nothing readable.
+struct SlotInfo {
+    float ks[4], vs[4];
+    int pid[4];   // of the lane's next tile
+    int bad;      // bit i: box i
+    int pad[3];
+};
+
+// Tokens of a tile: 8 KB of keys and values (a warp's share of the loop's fixed work
+// is then the same for both head dimensions), 4 KB where 32 rows' scores leave no
+// registers for more.
+template <int D, int NR>
+constexpr int tile_tokens() { return D == 64 && NR < 4 ? 64 : 32; }
+
+template <int D, int NR>
 struct AttnCfg {
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kTile = tile_tokens<D, NR>();
+    static constexpr int kStages = D * kTile == 4096 ? 3 : 6;
     static constexpr int kHalf = kTile * D;         // bytes of K (or V) of a tile
+    static constexpr bool kQSmem = NR == 4;
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kRing = kWarps * kStages * kSlot;          // 192 KB
     static constexpr int kMergeOff = kRing;                         // 8 warps x 8 rows x 64 fp32
     static constexpr int kLseOff = kMergeOff + kWarps * 8 * 64 * 4;
-    static constexpr int kBarOff = kLseOff + kWarps * 8 * 4;
+    static constexpr int kInfoOff = kLseOff + kWarps * 8 * 4;       // a slot each
+    static constexpr int kQOff = kInfoOff + kWarps * kStages * static_cast<int>(sizeof(SlotInfo));
+    static constexpr int kBarOff = kQOff + (kQSmem ? NR * 8 * D * 2 + NR * 8 * 4 : 0);
     static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kPreOff = kMiscOff + 64;                   // B + 1 ints
-    static int smem_bytes(int B) { return kPreOff + (B + 1) * 4 + 1024; }
+    static constexpr int kPreOff = kMiscOff + 64;                   // B + 1 ints, then B
+    static int smem_bytes(int B) { return kPreOff + (2 * B + 1) * 4 + 1024; }
 };
 
 template <int D, bool BF16, int NR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnParams p) {
-    using C = AttnCfg<D>;
-    constexpr int ST = C::kStages;
+    using C = AttnCfg<D, NR>;
+    constexpr int ST = C::kStages, kTile = C::kTile;
+    constexpr int NQ = kTile / 16;     // 16-token quarters of a tile (2 or 4)
     constexpr int KC = D / 64;         // 16-byte chunks of a K row per lane
     constexpr int MT = D / 16;         // 16-dimension tiles of O^T
     constexpr int VB = D / 8;          // bytes of a V row per lane (16 or 8)
@@ -344,15 +379,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
     int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 16);    // [8]
-    int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1]
+    int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
+    int* s_len = s_pre + p.B + 1;                                     // [B]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * ST; ++i) mbar_init(&bars[i], 1);
+        // a slot's phase: its copies' bytes, and its lane's small copies
+        for (int i = 0; i < kWarps * ST; ++i) mbar_init(&bars[i], 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
+    // Launched as a programmatic dependent of the kernel before it (an append, as
+    // a rule), whose writes it reads from here on; the merge may set up already.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     // exclusive prefix sums of the sequences' tile counts
     int carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
@@ -360,7 +401,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         int len = 0;
         if (b < p.B) {
             len = p.lens[b];
-            if (blockIdx.x == 0 && (len < 0 || len > p.max_pages * p.page))
+            if (blockIdx.x == 0 && (len < 0 || len > p.max_pages << p.page_shift))
                 atomicOr(p.status, kStatusPage);
         }
         const int n = b < p.B ? seq_of(p, len).n : 0;
@@ -378,7 +419,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (i < warp) before += s_warp[i];
             all += s_warp[i];
         }
-        if (b < p.B) s_pre[b] = before + x - n;
+        if (b < p.B) {
+            s_pre[b] = before + x - n;
+            s_len[b] = len;
+        }
         carry = all;
         __syncthreads();
     }
@@ -391,63 +435,107 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (c >= n_cta) return;   // nothing in flight, no barrier left
     const int64_t g0 = c * T / n_cta, g1 = (c + 1) * T / n_cta;
 
-    // (sequence, unit, tile) of a position in the concatenated lists; b moves forward only
+    // (sequence, unit, tile) of a position in the concatenated lists
     auto locate = [&](int64_t x, int& b, int& u, int& v) {
-        while (x >= static_cast<int64_t>(s_pre[b + 1]) * U) ++b;
+        int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before x and is not empty
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (static_cast<int64_t>(s_pre[mid]) * U <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo;
         const int n = s_pre[b + 1] - s_pre[b];
         const int64_t r = x - static_cast<int64_t>(s_pre[b]) * U;
         u = static_cast<int>(r / n);
         v = static_cast<int>(r - static_cast<int64_t>(u) * n);
     };
 
-    // ---- this lane's slot (lanes 0 .. ST - 1)
+    // ---- this lane's slot (lanes 0 .. ST - 1).  Page ids and scales travel by
+    // asynchronous copies into the slot's SlotInfo: a load into a register would
+    // hold up every lane that reads its own copy of that register.
     uint8_t* ring = smem + warp * (ST * C::kSlot);
     uint64_t* full = bars + warp * ST;
-    const int box = min(p.page, kTile);    // tokens per TMA box
-    const int boxes = kTile / box;         // 1, or 2 of 16 tokens
-    int64_t next = g0 + warp + kWarps * lane;   // next tile of this lane's slot
-    int nb = 0;                                 // its sequence
-    // scales of the tile in the slot: pages of its two 16-token halves
-    float ks0 = 0.0f, ks1 = 0.0f, vs0 = 0.0f, vs1 = 0.0f;
-    int bad = 0;                                // bit i: half i has no readable page
+    SlotInfo* infos = reinterpret_cast<SlotInfo*>(smem + C::kInfoOff) + warp * ST;
+    const int box_shift = min(p.page_shift, p.tile_shift);   // tokens per TMA box
+    const int boxes = kTile >> box_shift;                    // 1 to 4
+    int64_t next = g0 + warp + kWarps * lane;   // the tile `fetch` has looked up
+    int nb = 0, nu = 0, nv = 0, nh = 0, nn = 0; // its sequence, unit, list index; KV head; list length
+    Seq ns{};
+    int ntok = 0, nseen = 0;                    // its first token; boxes some query sees
     int issued = 0;
-    auto issue = [&]() {
+    auto enter = [&]() {   // a new sequence
+        nn = s_pre[nb + 1] - s_pre[nb];
+        ns = seq_of(p, s_len[nb]);
+    };
+    // Page ids of tile `next`; a box no query sees need not have a page.
+    auto fetch = [&]() {
         if (next >= g1) return;
-        int u, v;
-        locate(next, nb, u, v);
-        next += kWarps * ST;
-        const Seq s = seq_of(p, p.lens[nb]);
-        const int tok = seq_token(s, v);
-        const int h = u / p.n_rb;
-        uint8_t* dst = ring + lane * C::kSlot;
-        mbar_arrive_expect_tx(&full[lane], C::kSlot);
-        bad = 0;
-        ++issued;
-        for (int i = 0; i < boxes; ++i) {
-            const int x = tok + i * box;
-            // a box no query sees need not have a page
-            const bool seen = x < s.len && (x + box > s.lo || x < p.sinks);
-            int pid = -1;
-            if (seen) pid = p.table[static_cast<int64_t>(nb) * p.max_pages + x / p.page];
-            const bool ok = pid >= 0 && pid < p.n_pages;
-            if (seen && !ok) atomicOr(p.status, kStatusPage);
-            if (!ok) bad |= boxes == 1 ? 3 : 1 << i;
-            // past the pool the copy fills zeros
-            const int z = ok ? pid * p.Hkv + h : p.n_pages * p.Hkv;
-            tma_load_3d(&tmK, &full[lane], dst + i * 16 * D, 0, x % p.page, z);
-            tma_load_3d(&tmV, &full[lane], dst + C::kHalf + i * 16 * D, 0, x % p.page, z);
-            const float a = ok ? p.k_scale[z] : 1.0f, e = ok ? p.v_scale[z] : 1.0f;
-            if (i == 0) {
-                ks0 = a;
-                vs0 = e;
+        while (nv >= nn) {
+            nv -= nn;
+            if (++nu == U) {
+                nu = 0;
+                do ++nb;
+                while (s_pre[nb + 1] == s_pre[nb]);
+                enter();
             }
-            if (i == 1 || boxes == 1) {
-                ks1 = a;
-                vs1 = e;
+            nh = nu / p.n_rb;
+        }
+        ntok = seq_tile(ns, nv) << p.tile_shift;
+        const int* row = p.table + static_cast<int64_t>(nb) * p.max_pages;
+        nseen = 0;
+        for (int i = 0; i < boxes; ++i) {
+            const int x = ntok + (i << box_shift);
+            if (x < ns.len && (x + (1 << box_shift) > ns.lo || x < p.sinks)) {
+                nseen |= 1 << i;
+                cp_async4(&infos[lane].pid[i], row + (x >> p.page_shift));
             }
         }
+        cp_async_commit();
     };
-    if (lane < ST) issue();
+    auto issue = [&]() {
+        if (next >= g1) return;
+        uint8_t* dst = ring + lane * C::kSlot;
+        SlotInfo* in = infos + lane;
+        cp_async_wait_all();   // the ids, asked for a whole turn of the ring ago
+        const volatile int* pids = in->pid;
+        int bad = 0;
+        for (int i = 0; i < boxes; ++i) {
+            const int pid = (nseen >> i) & 1 ? pids[i] : -1;
+            if (pid < 0 || pid >= p.n_pages) {
+                bad |= 1 << i;
+                in->ks[i] = in->vs[i] = 1.0f;
+                if ((nseen >> i) & 1) atomicOr(p.status, kStatusPage);
+            }
+        }
+        in->bad = bad;
+        ++issued;
+        mbar_arrive_expect_tx(&full[lane], C::kSlot);   // releases the stores above, too
+        for (int i = 0; i < boxes; ++i) {
+            const bool ok = !((bad >> i) & 1);
+            const int y = (ntok + (i << box_shift)) & ((1 << p.page_shift) - 1);
+            // past the pool the copy fills zeros
+            const int z = ok ? pids[i] * p.Hkv + nh : p.n_pages * p.Hkv;
+            tma_load_3d(&tmK, &full[lane], dst + (i << box_shift) * D, 0, y, z);
+            tma_load_3d(&tmV, &full[lane], dst + C::kHalf + (i << box_shift) * D, 0, y, z);
+            if (ok) {
+                cp_async4(&in->ks[i], p.k_scale + z);
+                cp_async4(&in->vs[i], p.v_scale + z);
+            }
+        }
+        cp_async_arrive(&full[lane]);
+        next += kWarps * ST;
+        nv += kWarps * ST;
+        fetch();
+    };
+    if (lane < ST) {
+        if (next < g1) {
+            locate(next, nb, nu, nv);
+            nh = nu / p.n_rb;
+            enter();
+        }
+        fetch();
+        issue();
+    }
 
     // ---- fragment addresses (the same in every tile)
     uint32_t k_at[2][KC], v_at[2];   // K: token rows g / g + 8, chunks t (+ 4); V: rows 2t, 2t + 1
@@ -469,12 +557,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---- the share, unit by unit
     int64_t mine = g0 + warp;   // this warp's next tile
     int it = 0;                 // tiles this warp has done
+    int slot = 0;               // it % ST
+    uint32_t phase = 0;         // (it / ST) & 1
     int b = 0, u, v;
     locate(g0, b, u, v);
     int64_t unit0 = g0 - v;     // the unit's first tile in the concatenated lists
     while (unit0 < g1) {
         while (s_pre[b + 1] == s_pre[b]) ++b;   // empty sequences
-        const Seq s = seq_of(p, p.lens[b]);
+        const Seq s = seq_of(p, s_len[b]);
         const int h = u / p.n_rb, rb = u % p.n_rb;
         const int64_t unit1 = unit0 + s.n;
         const int64_t end = unit1 < g1 ? unit1 : g1;
@@ -484,11 +574,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // Q as fp16 B fragments: lane (g, t) holds dimensions 16 (t + 4 cc) .. + 15 of row g.
         // bf16 rows are scaled by a power of two first (their largest magnitude
         // to [2^14, 2^15)), which the scores take back: fp16 then holds every
-        // value down to 2^-28 of the row's largest exactly.
-        uint32_t qf[NR][KC][8];
+        // value down to 2^-28 of the row's largest exactly.  In registers, or
+        // (kQSmem) warp w prepares the 8 rows w and leaves them in shared memory
+        // as [row tile][word pair][lane], and the factors behind them.
+        uint32_t qf[C::kQSmem ? 1 : NR][KC][8];
         float f_row[NR][2];   // softmax scale of this lane's score columns 2t, 2t + 1
+        uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::kQOff);
+        float* s_f = reinterpret_cast<float*>(smem + C::kQOff + NR * 8 * D * 2);
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
+            if (C::kQSmem && nt != warp) continue;
             const int r = row0 + nt * 8 + g;
             uint32_t w[KC][8];
 #pragma unroll
@@ -522,13 +617,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         w[cc][i] = pack2<false>(x.x * up, x.y * up);
                     }
             }
+            if constexpr (C::kQSmem) {
 #pragma unroll
-            for (int cc = 0; cc < KC; ++cc)
+                for (int cc = 0; cc < KC; ++cc)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) qf[nt][cc][i] = w[cc][i];
-            // lane 8t (row 2t) and lane 8t + 4 (row 2t + 1) know this lane's columns' shifts
-            f_row[nt][0] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t));
-            f_row[nt][1] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t + 4));
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint2*>(s_q + ((nt * KC + cc) * 4 + i) * 64 + 2 * lane) =
+                            make_uint2(w[cc][2 * i], w[cc][2 * i + 1]);
+                if (t == 0) s_f[nt * 8 + g] = p.scale_log2 * exp2i(-shift);
+            } else {
+#pragma unroll
+                for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) qf[nt][cc][i] = w[cc][i];
+                // lane 8t (row 2t) and lane 8t + 4 (row 2t + 1) know this lane's columns' shifts
+                f_row[nt][0] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t));
+                f_row[nt][1] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t + 4));
+            }
+        }
+        if constexpr (C::kQSmem) {
+            __syncthreads();   // (the previous unit's last barrier came after its last read)
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt) {
+                f_row[nt][0] = s_f[nt * 8 + 2 * t];
+                f_row[nt][1] = s_f[nt * 8 + 2 * t + 1];
+            }
         }
 
         // running state of this lane's columns (rows 2t, 2t + 1 of each 8): m the
@@ -550,47 +663,70 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
 
         for (; mine < end; mine += kWarps, ++it) {
-            const int slot = it % ST;
-            const int tok = seq_token(s, static_cast<int>(mine - unit0));
-            // scales of the two 16-token halves, from the slot's lane
-            const float fk[2] = {__shfl_sync(0xffffffffu, ks0, slot), __shfl_sync(0xffffffffu, ks1, slot)};
-            const float lv[2] = {
-                static_cast<float>(scale_exp(__shfl_sync(0xffffffffu, vs0, slot))),
-                static_cast<float>(scale_exp(__shfl_sync(0xffffffffu, vs1, slot)))};
-            const int bad_t = __shfl_sync(0xffffffffu, bad, slot);
-            warp_wait(&full[slot], (it / ST) & 1, abort_flag, p.status);
+            const int tok = seq_tile(s, static_cast<int>(mine - unit0)) * kTile;
+            warp_wait(&full[slot], phase, abort_flag, p.status);
             const uint32_t sk = smem_u32(ring + slot * C::kSlot), sv = sk + C::kHalf;
-
-            // S^T: 2 halves of 16 tokens
-            float sc[2][NR][4];
+            const volatile SlotInfo* in = infos + slot;
+            const int bad = in->bad;
+            float fk[NQ], lv[NQ];   // of each quarter: key scale, log2 of the value scale
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < NQ; ++hf) {
+                const int i = (16 * hf) >> box_shift;
+                fk[hf] = in->ks[i];
+                lv[hf] = static_cast<float>(scale_exp(in->vs[i]));
+            }
+
+            // S^T of the tile's quarters
+            float sc[NQ][NR][4];
+#pragma unroll
+            for (int hf = 0; hf < NQ; ++hf)
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[hf][nt][e] = 0.0f;
 #pragma unroll
-                for (int cc = 0; cc < KC; ++cc) {
-                    const uint4 r0 = lds128(sk + hf * 16 * D + k_at[0][cc]);
-                    const uint4 r1 = lds128(sk + hf * 16 * D + k_at[1][cc]);
-                    const uint32_t x0[4] = {r0.x, r0.y, r0.z, r0.w}, x1[4] = {r1.x, r1.y, r1.z, r1.w};
+            for (int cc = 0; cc < KC; ++cc) {
+                uint4 x[NQ][2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = e4m3x2_to_f16x2(x0[i]), a2 = e4m3x2_hi_to_f16x2(x0[i]);
-                        const uint32_t a1 = e4m3x2_to_f16x2(x1[i]), a3 = e4m3x2_hi_to_f16x2(x1[i]);
+                for (int hf = 0; hf < NQ; ++hf) {
+                    x[hf][0] = lds128(sk + hf * 16 * D + k_at[0][cc]);
+                    x[hf][1] = lds128(sk + hf * 16 * D + k_at[1][cc]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint2 qv[NR];
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt) {
+                        if constexpr (C::kQSmem)
+                            qv[nt] = lds64(smem_u32(s_q + ((nt * KC + cc) * 4 + i) * 64 + 2 * lane));
+                        else
+                            qv[nt] = make_uint2(qf[nt][cc][2 * i], qf[nt][cc][2 * i + 1]);
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < NQ; ++hf) {
+                        const uint32_t x0 = i == 0   ? x[hf][0].x
+                                            : i == 1 ? x[hf][0].y
+                                            : i == 2 ? x[hf][0].z
+                                                     : x[hf][0].w;
+                        const uint32_t x1 = i == 0   ? x[hf][1].x
+                                            : i == 1 ? x[hf][1].y
+                                            : i == 2 ? x[hf][1].z
+                                                     : x[hf][1].w;
+                        const uint32_t a0 = e4m3x2_to_f16x2(x0), a2 = e4m3x2_hi_to_f16x2(x0);
+                        const uint32_t a1 = e4m3x2_to_f16x2(x1), a3 = e4m3x2_hi_to_f16x2(x1);
 #pragma unroll
                         for (int nt = 0; nt < NR; ++nt)
-                            mma16816(sc[hf][nt], a0, a1, a2, a3, qf[nt][cc][2 * i], qf[nt][cc][2 * i + 1]);
+                            mma16816(sc[hf][nt], a0, a1, a2, a3, qv[nt].x, qv[nt].y);
                     }
                 }
             }
             // scores in log2 units; edge tiles hide what a row does not see
-            const bool edge = bad_t != 0 || tok + kTile - 1 > s.first ||
+            const bool edge = bad != 0 || tok + kTile - 1 > s.first ||
                               (p.window > 0 && tok <= s.len - 1 - p.window && tok + kTile > p.sinks);
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int hf = 0; hf < NQ; ++hf) {
                     const float f0 = f_row[nt][0] * fk[hf], f1 = f_row[nt][1] * fk[hf];
                     sc[hf][nt][0] *= f0;
                     sc[hf][nt][1] *= f1;
@@ -604,9 +740,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const int pos = s.first + (row0 + nt * 8 + 2 * t + (e & 1)) % p.Nq;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
+                        for (int hf = 0; hf < NQ; ++hf) {
                             const int key = tok + hf * 16 + tok_a + 8 * (e >> 1);
-                            const bool see = !((bad_t >> hf) & 1) && key <= pos &&
+                            const bool see = !((bad >> ((16 * hf) >> box_shift)) & 1) && key <= pos &&
                                              (p.window <= 0 || key > pos - p.window || key < p.sinks);
                             if (!see) sc[hf][nt][e] = -INFINITY;
                         }
@@ -619,11 +755,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float h0 = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
-                    const float h1 = fmaxf(sc[1][nt][e], sc[1][nt][e + 2]);
-                    mx[nt][e] = fmaxf(h0, h1);
-                    ax[nt][e] = fmaxf(h0 + lv[0], h1 + lv[1]);
-                    grow = grow || mx[nt][e] > m[nt][e] || ax[nt][e] > R[nt][e];
+                    float a = -INFINITY, x = -INFINITY;
+#pragma unroll
+                    for (int hf = 0; hf < NQ; ++hf) {
+                        const float y = fmaxf(sc[hf][nt][e], sc[hf][nt][e + 2]);
+                        a = fmaxf(a, y);
+                        x = fmaxf(x, y + lv[hf]);
+                    }
+                    mx[nt][e] = a;
+                    ax[nt][e] = x;
+                    grow = grow || a > m[nt][e] || x > R[nt][e];
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -652,24 +793,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // p = 2^(s - m) into l; P^T = 2^(s + log2 vs - R), fp16 (at most 1: rounded by
             // 2^-11 of itself, and 2^-25 of the largest at the far end)
-            uint32_t pf[2][NR][2];
+            uint32_t pf[NQ][NR][2];
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt) {
-                float nm[2], nR[2][2];
+                float nm[2], nr[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     nm[e] = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-                    const float r = R[nt][e] == -INFINITY ? 0.0f : R[nt][e];
-                    nR[0][e] = lv[0] - r;
-                    nR[1][e] = lv[1] - r;
+                    nr[e] = R[nt][e] == -INFINITY ? 0.0f : R[nt][e];
                 }
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int hf = 0; hf < NQ; ++hf) {
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         l[nt][e & 1] += ex2_ftz(sc[hf][nt][e] - nm[e & 1]);
-                        w[e] = ex2_ftz(sc[hf][nt][e] + nR[hf][e & 1]);
+                        w[e] = ex2_ftz(sc[hf][nt][e] + (lv[hf] - nr[e & 1]));
                     }
                     pf[hf][nt][0] = movmatrix_trans(pack2<false>(w[0], w[1]));
                     pf[hf][nt][1] = movmatrix_trans(pack2<false>(w[2], w[3]));
@@ -677,7 +816,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // O^T += V^T P^T
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < NQ; ++hf) {
                 uint32_t r[4][VB / 4];   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -695,7 +834,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = tok + hf * 16 + (i >> 1) * 8 + ((i & 1) ? tok_v1 : tok_v0);
-                        if (((bad_t >> hf) & 1) || key >= s.len || (key < s.lo && key >= p.sinks)) {
+                        if (((bad >> ((16 * hf) >> box_shift)) & 1) || key >= s.len ||
+                            (key < s.lo && key >= p.sinks)) {
 #pragma unroll
                             for (int j = 0; j < VB / 4; ++j) r[i][j] = 0u;
                         }
@@ -721,6 +861,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             __syncwarp();   // every lane has read the slot
             if (lane == slot) issue();
+            if (++slot == ST) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
 
         // ---- the unit ends here for this CTA: combine the 8 warps
@@ -821,98 +965,119 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_wait_bounded(&full[lane], (issued - 1) & 1, p.status);
 }
 
-// Combines the partial results of the units that lie in several CTAs, one CTA per
-// (sequence, unit); empty sequences get out = 0 and lse = -inf here.
+// Combines the partial results of the units that lie in several CTAs: a warp per
+// row, kMergeRows rows of one (sequence, unit) per CTA.  Lanes hold the CTAs' LSEs,
+// 32 at a time, so the loads of the partial outputs depend on nothing but each
+// other's sum.  Empty sequences get out = 0 and lse = -inf here.
+constexpr int kMergeRows = 4;
+
 template <int D, bool BF16, int NR>
-__global__ void __launch_bounds__(256) kv8_merge_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnParams p) {
+    constexpr int V = D / 32, kThreads = kMergeRows * 32;
     const int U = p.Hkv * p.n_rb;
-    const int b = static_cast<int>(blockIdx.x / U), u = static_cast<int>(blockIdx.x % U);
+    const int chunks = (min(8 * NR, p.rows) + kMergeRows - 1) / kMergeRows;   // of a row block
+    const int unit = static_cast<int>(blockIdx.x / chunks);
+    const int b = unit / U, u = unit % U;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // tiles of all sequences, and of those before b
+    // Launched as a programmatic dependent of the attention kernel, whose results
+    // (and, through it, the lengths) it reads from here on.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // tiles of all sequences, and of those before b: each warp for itself, or
+    // (many sequences) the CTA together
+    const bool alone = p.B <= 128;
     int all = 0, before = 0;
-    for (int i = threadIdx.x; i < p.B; i += 256) {
+    for (int i = alone ? lane : threadIdx.x; i < p.B; i += alone ? 32 : kThreads) {
         const int n = seq_of(p, p.lens[i]).n;
         all += n;
         if (i < b) before += n;
     }
     all = __reduce_add_sync(0xffffffffu, all);
     before = __reduce_add_sync(0xffffffffu, before);
-    __shared__ int s_sum[2][8];
-    if (lane == 0) {
-        s_sum[0][warp] = all;
-        s_sum[1][warp] = before;
-    }
-    __syncthreads();
-    all = before = 0;
+    if (!alone) {
+        __shared__ int s_sum[2][kMergeRows];
+        if (lane == 0) {
+            s_sum[0][warp] = all;
+            s_sum[1][warp] = before;
+        }
+        __syncthreads();
+        all = before = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        all += s_sum[0][i];
-        before += s_sum[1][i];
+        for (int i = 0; i < kMergeRows; ++i) {
+            all += s_sum[0][i];
+            before += s_sum[1][i];
+        }
     }
-    const Seq s = seq_of(p, p.lens[b]);
+    const int row0 = u % p.n_rb * (8 * NR);
+    const int r = static_cast<int>(blockIdx.x % chunks) * kMergeRows + warp;   // within the block
+    if (r >= min(8 * NR, p.rows - row0)) return;
+    const int n = seq_of(p, p.lens[b]).n;
     const int64_t T = static_cast<int64_t>(all) * U;
     const int n_cta = shares(T, p.ctas);
-    const int64_t first = static_cast<int64_t>(before) * U + static_cast<int64_t>(u) * s.n;
-    const int h = u / p.n_rb, row0 = u % p.n_rb * (8 * NR);
-    const int64_t head_row = (static_cast<int64_t>(b) * p.Hkv + h) * p.rows;
-    const int rows = min(8 * NR, p.rows - row0);
-    // Launched as a programmatic dependent of the attention kernel: what follows
-    // reads its partial results.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int c0 = 0, c1 = -1;   // the CTAs that hold part of it
-    if (s.n > 0) {
+    const int64_t first = static_cast<int64_t>(before) * U + static_cast<int64_t>(u) * n;
+    int c0 = 0, c1 = -1;   // the CTAs that hold part of the unit
+    if (n > 0) {
         c0 = static_cast<int>(((first + 1) * n_cta - 1) / T);
-        c1 = static_cast<int>(((first + s.n) * n_cta - 1) / T);
+        c1 = static_cast<int>(((first + n) * n_cta - 1) / T);
         if (c0 == c1) return;   // written by that CTA
     }
-    constexpr int V = D / 32;
-    for (int r = warp; r < rows; r += 8) {
-        float M = -INFINITY, sum = 0.0f, acc[V] = {};
-        for (int cta = c0; cta <= c1; ++cta) {
-            const int slot = 2 * cta + (cta == c0 && first > c0 * T / n_cta ? 1 : 0);
-            const int64_t pr = static_cast<int64_t>(slot) * (8 * NR) + r;
-            const float L = p.part_lse[pr];
+    const int second = n > 0 && first > c0 * T / n_cta ? 1 : 0;   // slot of c0's part
+    auto part_row = [&](int cta) {
+        return static_cast<int64_t>(2 * cta + (cta == c0 ? second : 0)) * (8 * NR) + r;
+    };
+    float M = -INFINITY, sum = 0.0f, acc[V] = {};
+    for (int base = c0; base <= c1; base += 32) {
+        const int cnt = min(32, c1 + 1 - base);
+        const float L = lane < cnt ? p.part_lse[part_row(base + lane)] : -INFINITY;
+        float M1 = fmaxf(M, L);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, d));
+        const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - M1);
+        const float w = L == -INFINITY ? 0.0f : ex2_ftz(L - M1);
+        M = M1;
+        sum *= al;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= al;
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* src = p.part_o + part_row(base + k) * D + lane * V;
             float x[V];
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[0] = y.x, x[1] = y.y;
+            }
+            sum += wk;
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = p.part_o[pr * D + lane * V + i];
-            if (L == -INFINITY) continue;
-            const float M1 = fmaxf(M, L), al = ex2_ftz(M - M1), w = ex2_ftz(L - M1);
-            sum = sum * al + w;
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = acc[i] * al + w * x[i];
-            M = M1;
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, x[i], acc[i]);
         }
-        const float n = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint16_t* out = static_cast<uint16_t*>(p.out) + (head_row + row0 + r) * D + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; i += 2)
-            *reinterpret_cast<uint32_t*>(out + i) = pack2<BF16>(acc[i] * n, acc[i + 1] * n);
-        if (lane == 0)
-            p.lse[head_row + row0 + r] =
-                sum == 0.0f ? -INFINITY : (M + lg2_approx(sum)) * 0.6931471805599453f;
     }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t row = (static_cast<int64_t>(b) * p.Hkv + u / p.n_rb) * p.rows + row0 + r;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + row * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t*>(out + i) = pack2<BF16>(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0)
+        p.lse[row] = sum == 0.0f ? -INFINITY : (M + lg2_approx(sum)) * 0.6931471805599453f;
 }
 
 template <int D, bool BF16, int NR>
-cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p,
+cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnParams p,
                         cudaStream_t stream) {
     auto kern = kv8_attn_kernel<D, BF16, NR>;
-    const int smem = AttnCfg<D>::smem_bytes(p.B);
+    p.tile_shift = AttnCfg<D, NR>::kTile == 64 ? 6 : 5;
+    const int smem = AttnCfg<D, NR>::smem_bytes(p.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kAttnThreads), smem, stream,
-                      tmK, tmV, p);
+    e = launch_dependent(kern, p.ctas, kAttnThreads, smem, stream, tmK, tmV, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * p.n_rb);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, BF16, NR>, p);
+    const int rows = 8 * NR < p.rows ? 8 * NR : p.rows;
+    const int64_t ctas = static_cast<int64_t>(p.B) * p.Hkv * p.n_rb *
+                         ((rows + kMergeRows - 1) / kMergeRows);
+    return launch_dependent(kv8_merge_kernel<D, BF16, NR>, ctas, kMergeRows * 32, 0, stream, p);
 }
 
 // ------------------------------------------------------------------ page copies
@@ -928,32 +1093,37 @@ struct CopyParams {
     int vecs;   // 16-byte vectors of a page (all heads)
 };
 
-// One CTA per (pair, layer, keys or values), 4 vectors in flight a thread.
-__global__ void __launch_bounds__(256) kv8_copy_kernel(const CopyParams p) {
-    const int64_t id = blockIdx.x;
-    const int which = static_cast<int>(id & 1);
-    const int layer = static_cast<int>((id >> 1) % p.n_layers);
-    const int i = static_cast<int>((id >> 1) / p.n_layers);
-    if (i >= min(*p.count, p.max_count)) return;
-    const int a = p.src[i], b = p.dst[i];
-    if (a < 0 || a >= p.n_pages || b < 0 || b >= p.n_pages) {
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
-        return;
-    }
-    const int64_t base = static_cast<int64_t>(layer) * p.n_pages;
-    const uint4* from = reinterpret_cast<const uint4*>(p.pages[which]) + (base + a) * p.vecs;
-    uint4* to = reinterpret_cast<uint4*>(p.pages[which]) + (base + b) * p.vecs;
-    for (int x = threadIdx.x; x < p.vecs; x += 1024) {
-        uint4 w[4];
+// CTAs take (pair, layer, keys or values) items in turn, as many as the device
+// holds: the count of pairs is only known there.  4 vectors in flight a thread.
+constexpr int kCopyThreads = 256, kCopyCtasPerSm = 8;
+__global__ void __launch_bounds__(kCopyThreads) kv8_copy_kernel(const CopyParams p) {
+    // Launched as a programmatic dependent of the kernel that lists the pairs.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t items = 2 * static_cast<int64_t>(min(*p.count, p.max_count)) * p.n_layers;
+    for (int64_t id = blockIdx.x; id < items; id += gridDim.x) {
+        const int which = static_cast<int>(id & 1);
+        const int layer = static_cast<int>((id >> 1) % p.n_layers);
+        const int i = static_cast<int>((id >> 1) / p.n_layers);
+        const int a = p.src[i], b = p.dst[i];
+        if (a < 0 || a >= p.n_pages || b < 0 || b >= p.n_pages) {
+            if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
+            continue;
+        }
+        const int64_t base = static_cast<int64_t>(layer) * p.n_pages;
+        const uint4* from = reinterpret_cast<const uint4*>(p.pages[which]) + (base + a) * p.vecs;
+        uint4* to = reinterpret_cast<uint4*>(p.pages[which]) + (base + b) * p.vecs;
+        for (int x = threadIdx.x; x < p.vecs; x += 4 * kCopyThreads) {
+            uint4 w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (x + 256 * k < p.vecs) w[k] = from[x + 256 * k];
+            for (int k = 0; k < 4; ++k)
+                if (x + kCopyThreads * k < p.vecs) w[k] = from[x + kCopyThreads * k];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (x + 256 * k < p.vecs) to[x + 256 * k] = w[k];
+            for (int k = 0; k < 4; ++k)
+                if (x + kCopyThreads * k < p.vecs) to[x + kCopyThreads * k] = w[k];
+        }
+        for (int x = threadIdx.x; x < p.Hkv; x += kCopyThreads)
+            p.scales[which][(base + b) * p.Hkv + x] = p.scales[which][(base + a) * p.Hkv + x];
     }
-    for (int x = threadIdx.x; x < p.Hkv; x += 256)
-        p.scales[which][(base + b) * p.Hkv + x] = p.scales[which][(base + a) * p.Hkv + x];
 }
 
 // ------------------------------------------------------------------ host
@@ -999,9 +1169,10 @@ size_t part_bytes(int64_t rows, int D, int ctas) {
     return pad256(n * D * sizeof(float)) + pad256(n * sizeof(float));
 }
 
-// The [n_pages * Hkv][page][D] bytes of a pool, boxes of min(page, 32) tokens.
-int make_page_map(CUtensorMap* map, const void* base, int D, int page, int64_t pages) {
-    return make_byte_map_public(map, base, D, page, pages, page < kTile ? page : kTile);
+// The [n_pages * Hkv][page][D] bytes of a pool, boxes of at most a tile's tokens.
+int make_page_map(CUtensorMap* map, const void* base, int D, int page, int64_t pages, int nr) {
+    const int tile = D == 64 && nr < 4 ? tile_tokens<64, 1>() : tile_tokens<128, 1>();
+    return make_byte_map_public(map, base, D, page, pages, page < tile ? page : tile);
 }
 
 }  // namespace
@@ -1111,11 +1282,11 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     if (sms <= 0) return ATTN_ERR_CUDA;
     CUtensorMap tmK, tmV;
     const int64_t pages = static_cast<int64_t>(n_pages) * Hkv;
-    if (make_page_map(&tmK, k_pages, D, page, pages) != ATTN_OK ||
-        make_page_map(&tmV, v_pages, D, page, pages) != ATTN_OK)
-        return ATTN_ERR_CUDA;
     const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
     const int nr = row_tiles(rows);
+    if (make_page_map(&tmK, k_pages, D, page, pages, nr) != ATTN_OK ||
+        make_page_map(&tmV, v_pages, D, page, pages, nr) != ATTN_OK)
+        return ATTN_ERR_CUDA;
     p.q = q;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
@@ -1133,7 +1304,7 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     p.rows = static_cast<int>(rows);
     p.n_rb = static_cast<int>((rows + 8 * nr - 1) / (8 * nr));
     p.Nq = Nq;
-    p.page = page;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     p.n_pages = n_pages;
     p.max_pages = max_pages;
     // no position is past max_pages * page <= 2^30: larger ones mean all
@@ -1192,9 +1363,11 @@ extern "C" int kv8_copy_pages(void* k_pages, void* v_pages, float* k_scale, floa
     p.n_pages = n_pages;
     p.Hkv = Hkv;
     p.vecs = Hkv * page * D / 16;
-    const unsigned ctas = static_cast<unsigned>(max_count) * n_layers * 2;
-    return launch_kernel(kv8_copy_kernel, dim3(ctas), dim3(256), 0, static_cast<cudaStream_t>(stream),
-                         p) == cudaSuccess
+    const int sms = device_sms();
+    const int64_t items = static_cast<int64_t>(max_count) * n_layers * 2;
+    const int64_t most = static_cast<int64_t>(sms > 0 ? sms : 1) * kCopyCtasPerSm;
+    return launch_dependent(kv8_copy_kernel, items < most ? items : most, kCopyThreads, 0,
+                            static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
 }

@@ -17,6 +17,16 @@ int device_setup_public(unsigned int** status);   // abi.cu
 namespace {
 
 constexpr int kThreads = 1024;   // the planning kernels run as one CTA
+constexpr int kWarps = kThreads / 32;
+// The planning's steps depend on one another through the pages' counts, the list of
+// free ids and a few numbers per sequence, and each step costs a round trip of the
+// memory those are in: they live in shared memory up to this many bytes (2 ints a
+// page, 5 a sequence), in the workspace past it.  reassign of 64 sequences over
+// 2049 pages: @SH us against @WS us.
+constexpr size_t kSharedBytes = 200 * 1024;
+// Table entries that compact's planning CTA renumbers itself; more take a second
+// kernel.
+constexpr int64_t kRemapEntries = 16 * 1024;
 
 struct PageParams {
     int* table;
@@ -27,16 +37,40 @@ struct PageParams {
     int* dst;
     int* info;
     unsigned int* status;
-    int* refs2;            // workspace: refs after the call [n_pages]
-    int* ids;              // workspace: free ids, lowest first [n_pages]; compact: new id of a page
-    int* keeper;           // workspace [n_seqs]
-    int* base;             // workspace [n_seqs]
-    int* tail;             // workspace [n_seqs]
-    int* new_len;          // workspace [n_seqs]
+    int* scratch;          // workspace: scratch_ints() (when not in shared memory)
+    int* ids;              // workspace: new id of each page (compact's second kernel)
     int* table2;           // workspace [n_seqs][max_pages]
     const int* table_in;   // compact
     const int* refs_in;
     int n_seqs, max_pages, n_pages, page, window, sinks;
+};
+
+size_t scratch_ints(int n_seqs, int n_pages) {
+    return 2 * static_cast<size_t>(n_pages) + 5 * static_cast<size_t>(n_seqs);
+}
+
+// The planning's working arrays.
+template <bool SHARED>
+struct Scratch {
+    int* count;    // [n_pages] holders of each page after the call
+    int* ids;      // [n_pages] free ids, lowest first; compact: new ids
+    int* len;      // [n_seqs]
+    int* arg;      // [n_seqs] tokens to add, or parent
+    int* keeper;   // [n_seqs]
+    int* base;     // [n_seqs]
+    int* tail;     // [n_seqs]
+    __device__ __forceinline__ explicit Scratch(const PageParams& p) {
+        extern __shared__ int s_scratch[];
+        count = SHARED ? s_scratch : p.scratch;
+        ids = count + p.n_pages;
+        len = ids + p.n_pages;
+        arg = len + p.n_seqs;
+        keeper = arg + p.n_seqs;
+        base = keeper + p.n_seqs;
+        tail = base + p.n_seqs;
+    }
+    // What atomics of this CTA change is read past the first-level cache.
+    __device__ __forceinline__ static int get(const int* p) { return SHARED ? *p : __ldcg(p); }
 };
 
 // Exclusive prefix sum of one value per thread over the CTA, and the total.
@@ -63,51 +97,70 @@ __device__ __forceinline__ int block_scan(int x, int* total) {
     return __shfl_sync(0xffffffffu, winc - w, warp) + inc - x;
 }
 
-__device__ __forceinline__ int block_sum(int x) {
-    int total;
-    block_scan(x, &total);
-    return total;
-}
-
-// Counters that atomics of this CTA change are read past the first-level cache.
-__device__ __forceinline__ int counter(const int* p) { return __ldcg(p); }
-
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Lists the free ids (refs2 = 0) in order; returns how many there are.
-__device__ int list_free(const PageParams& p) {
-    int count = 0;
-    for (int i0 = 0; i0 < p.n_pages; i0 += kThreads) {
-        const int i = i0 + static_cast<int>(threadIdx.x);
-        const bool free = i < p.n_pages && counter(p.refs2 + i) == 0;
-        int total;
-        const int at = block_scan(free ? 1 : 0, &total);
-        if (free) p.ids[count + at] = i;
-        count += total;
-    }
-    __syncthreads();
-    return count;
-}
 
 __device__ __forceinline__ bool in_pool(const PageParams& p, int id) {
     return id >= 0 && id < p.n_pages;
 }
 
+// Loads the counts; returns how many pages are free (after a barrier).
+template <bool SHARED>
+__device__ int load_counts(const PageParams& p, const Scratch<SHARED>& m, const int* refs) {
+    int free = 0;
+    for (int i = threadIdx.x; i < p.n_pages; i += kThreads) {
+        const int r = refs[i];
+        m.count[i] = r;
+        free += r == 0;
+    }
+    int total;
+    block_scan(free, &total);
+    return total;
+}
+
+// Lists the free ids in order; returns how many there are.  4 pages a thread and step.
+template <bool SHARED>
+__device__ int list_free(const PageParams& p, const Scratch<SHARED>& m) {
+    int n = 0;
+    for (int i0 = 0; i0 < p.n_pages; i0 += 4 * kThreads) {
+        const int i = i0 + 4 * static_cast<int>(threadIdx.x);
+        bool free[4];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            free[k] = i + k < p.n_pages && m.get(m.count + i + k) == 0;
+            mine += free[k];
+        }
+        int total;
+        int at = n + block_scan(mine, &total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (free[k]) m.ids[at++] = i + k;
+        n += total;
+    }
+    __syncthreads();
+    return n;
+}
+
+template <bool SHARED>
 __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams p) {
+    const Scratch<SHARED> m(p);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __shared__ int s_bad;
     if (tid == 0) s_bad = 0;
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs2[i] = p.refs[i];
-    __syncthreads();
-    // pages each sequence needs; those its window leaves behind are released
+    for (int c = tid; c < p.n_seqs; c += kThreads) {
+        m.len[c] = p.lens[c];
+        m.arg[c] = p.arg[c];
+    }
+    const int before = load_counts(p, m, p.refs);
+    // pages each sequence needs
     const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page;
     int need = 0;
     for (int c0 = 0; c0 < p.n_seqs; c0 += kThreads) {
         const int c = c0 + tid;
         int want = 0;
         if (c < p.n_seqs) {
-            const int len = p.lens[c];
-            int n = p.arg[c];
+            const int len = m.len[c];
+            int n = m.arg[c];
             if (n < 0 || len < 0) {
                 atomicOr(p.status, kStatusPage);
                 n = 0;
@@ -116,34 +169,31 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
                 s_bad = 1;
                 n = 0;
             }
+            m.arg[c] = n;
             want = n > 0 ? ceil_div(len + n, p.page) - ceil_div(len, p.page) : 0;
         }
         int total;
         const int at = block_scan(want, &total);
-        if (c < p.n_seqs) p.base[c] = need + at;
+        if (c < p.n_seqs) m.base[c] = need + at;
         need += total;
     }
-    auto evicted = [&](int c, int* j0, int* j1) {   // columns [j0, j1) no later query sees
-        const int len = p.lens[c];
-        *j0 = *j1 = 0;
-        if (p.window <= 0 || p.arg[c] <= 0 || len < 0) return;
-        *j0 = ceil_div(p.sinks, p.page);
-        const int past = len - p.window + 1;   // first position a new query sees
-        *j1 = min(past > 0 ? past / p.page : 0, p.max_pages);
-    };
-    for (int c = warp; c < p.n_seqs; c += kThreads / 32) {
-        int j0, j1;
-        evicted(c, &j0, &j1);
-        for (int j = j0 + lane; j < j1; j += 32) {
-            const int id = p.table[static_cast<int64_t>(c) * p.max_pages + j];
-            if (in_pool(p, id)) atomicSub(p.refs2 + id, 1);
-        }
-    }
     __syncthreads();
-    int before = 0;
-    for (int i = tid; i < p.n_pages; i += kThreads) before += p.refs[i] == 0;
-    before = block_sum(before);
-    const int free = list_free(p);
+    // pages that windows leave behind: columns [j0, j1), which no later query sees
+    const int j0 = ceil_div(p.sinks, p.page);
+    auto past = [&](int c) {
+        if (p.window <= 0 || m.arg[c] <= 0) return 0;
+        const int first = m.len[c] - p.window + 1;   // first position a new query sees
+        return min(first > 0 ? first / p.page : 0, p.max_pages);
+    };
+    if (p.window > 0) {
+        for (int c = warp; c < p.n_seqs; c += kWarps) {
+            const int* row = p.table + static_cast<int64_t>(c) * p.max_pages;
+            for (int j = j0 + lane; j < past(c); j += 32)
+                if (in_pool(p, row[j])) atomicSub(m.count + row[j], 1);
+        }
+        __syncthreads();
+    }
+    const int free = list_free(p, m);
     const bool done = s_bad == 0 && need <= free;
     if (tid == 0) {
         p.info[0] = done;
@@ -153,41 +203,44 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
         if (!done) atomicOr(p.status, kStatusPool);
     }
     if (!done) return;
-    for (int c = warp; c < p.n_seqs; c += kThreads / 32) {
-        int j0, j1;
-        evicted(c, &j0, &j1);
+    for (int c = warp; c < p.n_seqs; c += kWarps) {
         int* row = p.table + static_cast<int64_t>(c) * p.max_pages;
-        for (int j = j0 + lane; j < j1; j += 32) row[j] = -1;
-        const int len = p.lens[c], n = p.arg[c];
-        if (n > 0 && len >= 0) {
+        for (int j = j0 + lane; j < past(c); j += 32) row[j] = -1;
+        const int len = m.len[c], n = m.arg[c];
+        if (n > 0) {
             const int first = ceil_div(len, p.page), want = ceil_div(len + n, p.page) - first;
             for (int k = lane; k < want; k += 32) {
-                const int id = p.ids[p.base[c] + k];
+                const int id = m.ids[m.base[c] + k];
                 row[first + k] = id;
-                atomicExch(p.refs2 + id, 1);
+                atomicExch(m.count + id, 1);
             }
-            __syncwarp();
             if (lane == 0) p.lens[c] = len + n;
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = counter(p.refs2 + i);
+    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = m.get(m.count + i);
 }
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");   // the copies may set up meanwhile
+    const Scratch<SHARED> m(p);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs2[i] = p.refs[i];
-    for (int c = tid; c < p.n_seqs; c += kThreads) p.keeper[c] = 0x7fffffff;
-    __syncthreads();
-    auto parent = [&](int c) {   // a bad one keeps the sequence
-        const int q = p.arg[c];
-        return q < -1 || q >= p.n_seqs ? c : q;
-    };
-    auto length = [&](int c) { return c < 0 ? 0 : min(max(p.lens[c], 0), p.max_pages * p.page); };
+    const int cap = p.max_pages * p.page;
     for (int c = tid; c < p.n_seqs; c += kThreads) {
-        const int q = parent(c);
-        if (q != p.arg[c]) atomicOr(p.status, kStatusPage);
-        if (q >= 0) atomicMin(p.keeper + q, q == c ? -1 : c);
+        int q = p.arg[c];
+        if (q < -1 || q >= p.n_seqs) {   // a bad parent keeps the sequence
+            atomicOr(p.status, kStatusPage);
+            q = c;
+        }
+        m.arg[c] = q;
+        m.len[c] = min(max(p.lens[c], 0), cap);
+        m.keeper[c] = 0x7fffffff;
+    }
+    const int before = load_counts(p, m, p.refs);
+    for (int c = tid; c < p.n_seqs; c += kThreads) {
+        const int q = m.arg[c];
+        if (q >= 0) atomicMin(m.keeper + q, q == c ? -1 : c);
     }
     __syncthreads();
     // Children that do not keep their parent's partly filled last page copy it.
@@ -196,44 +249,44 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
         const int c = c0 + tid;
         int tail = -1;
         if (c < p.n_seqs) {
-            const int q = parent(c), len = length(q);
-            if (q >= 0 && q != c && len % p.page != 0 && counter(p.keeper + q) != c &&
-                in_pool(p, p.table[static_cast<int64_t>(q) * p.max_pages + len / p.page]))
-                tail = len / p.page;
-            p.tail[c] = tail;
-            p.new_len[c] = q == c ? p.lens[c] : len;
+            const int q = m.arg[c];
+            if (q >= 0 && q != c && m.len[q] % p.page != 0 && m.get(m.keeper + q) != c) {
+                const int j = m.len[q] / p.page;
+                if (in_pool(p, p.table[static_cast<int64_t>(q) * p.max_pages + j])) tail = j;
+            }
+            m.tail[c] = tail;
         }
         int total;
         const int at = block_scan(tail >= 0 ? 1 : 0, &total);
-        if (c < p.n_seqs) p.base[c] = n_copy + at;
+        if (c < p.n_seqs) m.base[c] = n_copy + at;
         n_copy += total;
     }
     __syncthreads();
     // New rows of the changed sequences aside, and the counts they leave.
-    auto columns = [&](int c, int q) {
-        return max(ceil_div(length(c), p.page), ceil_div(length(q), p.page));
+    auto columns = [&](int c, int* had, int* has) {
+        const int q = m.arg[c];
+        *had = ceil_div(m.len[c], p.page);
+        *has = q >= 0 ? ceil_div(m.len[q], p.page) : 0;
+        return max(*had, *has);
     };
-    for (int c = warp; c < p.n_seqs; c += kThreads / 32) {
-        const int q = parent(c);
+    for (int c = warp; c < p.n_seqs; c += kWarps) {
+        const int q = m.arg[c];
         if (q == c) continue;
+        int had, has;
+        const int cols = columns(c, &had, &has);
+        const int tail = m.tail[c];
         const int64_t row = static_cast<int64_t>(c) * p.max_pages;
-        const int had = ceil_div(length(c), p.page), has = ceil_div(length(q), p.page);
-        const int tail = p.tail[c];
-        for (int j = lane; j < columns(c, q); j += 32) {
-            if (j < had && in_pool(p, p.table[row + j])) atomicSub(p.refs2 + p.table[row + j], 1);
-            int id = -1;
-            if (j < has) {
-                id = p.table[static_cast<int64_t>(q) * p.max_pages + j];
-                if (in_pool(p, id) && j != tail) atomicAdd(p.refs2 + id, 1);
-            }
+        const int64_t from = static_cast<int64_t>(q) * p.max_pages;
+        for (int j = lane; j < cols; j += 32) {
+            const int old = j < had ? p.table[row + j] : -1;
+            const int id = j < has ? p.table[from + j] : -1;
+            if (in_pool(p, old)) atomicSub(m.count + old, 1);
+            if (in_pool(p, id) && j != tail) atomicAdd(m.count + id, 1);
             p.table2[row + j] = id;
         }
     }
     __syncthreads();
-    int before = 0;
-    for (int i = tid; i < p.n_pages; i += kThreads) before += p.refs[i] == 0;
-    before = block_sum(before);
-    const int free = list_free(p);
+    const int free = list_free(p, m);
     const bool done = n_copy <= free;
     if (tid == 0) {
         p.info[0] = done;
@@ -243,60 +296,80 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
         if (!done) atomicOr(p.status, kStatusPool);
     }
     if (!done) return;
-    for (int c = warp; c < p.n_seqs; c += kThreads / 32) {
-        const int q = parent(c);
+    for (int c = warp; c < p.n_seqs; c += kWarps) {
+        const int q = m.arg[c];
         if (q == c) continue;
+        int had, has;
+        const int cols = columns(c, &had, &has);
+        const int tail = m.tail[c], at = m.base[c];
         const int64_t row = static_cast<int64_t>(c) * p.max_pages;
-        const int tail = p.tail[c], at = p.base[c];
-        const int cols = max(ceil_div(length(c), p.page), ceil_div(p.new_len[c], p.page));
         for (int j = lane; j < cols; j += 32) {
-            int id = p.table2[row + j];
+            int id = p.table2[row + j];   // this lane wrote it
             if (j == tail) {
                 p.src[at] = id;
-                id = p.ids[at];
+                id = m.ids[at];
                 p.dst[at] = id;
-                atomicExch(p.refs2 + id, 1);
+                atomicExch(m.count + id, 1);
             }
             p.table[row + j] = id;
         }
+        if (lane == 0) p.lens[c] = q >= 0 ? m.len[q] : 0;
     }
     __syncthreads();
-    for (int c = tid; c < p.n_seqs; c += kThreads) p.lens[c] = p.new_len[c];
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = counter(p.refs2 + i);
+    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = m.get(m.count + i);
 }
 
-// New ids of the held pages: ids[i] = -1 (not held), i, or the free id it moves
-// to; refs_out and the moves.
-__global__ void __launch_bounds__(kThreads) kvp_compact_kernel(const PageParams p) {
+// New ids of the held pages (ids: -1 not held, the page itself, or the free id it
+// moves to), refs_out, the moves and, for a small table, table_out.
+template <bool SHARED>
+__global__ void __launch_bounds__(kThreads) kvp_compact_kernel(const PageParams p, int64_t entries) {
+    asm volatile("griddepcontrol.launch_dependents;");   // what follows may set up meanwhile
+    const Scratch<SHARED> m(p);
     const int tid = threadIdx.x;
     int held = 0;
-    for (int i = tid; i < p.n_pages; i += kThreads) held += p.refs_in[i] > 0;
-    held = block_sum(held);
+    for (int i = tid; i < p.n_pages; i += kThreads) {
+        const int r = p.refs_in[i];
+        m.count[i] = r;
+        held += r > 0;
+    }
+    int total;
+    block_scan(held, &total);
+    held = total;
+    // holes below `held` and pages past it, each in order; both counts of a step
+    // travel in one scan (at most 4 * 1024 each, 16 bits)
     int holes = 0, movers = 0;
-    for (int i0 = 0; i0 < p.n_pages; i0 += kThreads) {
-        const int i = i0 + tid;
-        const int r = i < p.n_pages ? p.refs_in[i] : 0;
-        const bool hole = i < held && r <= 0, mover = i >= held && i < p.n_pages && r > 0;
-        int n_hole, n_mover;
-        const int a = block_scan(hole ? 1 : 0, &n_hole), b = block_scan(mover ? 1 : 0, &n_mover);
-        if (hole) p.dst[holes + a] = i;
-        if (mover) {
-            p.src[movers + b] = i;
-            p.refs2[movers + b] = r;   // refs_out may be refs
+    for (int i0 = 0; i0 < p.n_pages; i0 += 4 * kThreads) {
+        const int i = i0 + 4 * tid;
+        int kind[4], mine = 0;   // 0, 1 a hole, 1 << 16 a mover
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool in = i + k < p.n_pages;
+            const int r = in ? m.count[i + k] : 0;
+            kind[k] = !in ? 0 : i + k < held ? (r > 0 ? 0 : 1) : (r > 0 ? 1 << 16 : 0);
+            mine += kind[k];
         }
-        if (i < p.n_pages) p.ids[i] = r > 0 ? i : -1;
-        holes += n_hole;
-        movers += n_mover;
+        int both;
+        const int at = block_scan(mine, &both);
+        int h = holes + (at & 0xffff), v = movers + (at >> 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (kind[k] == 1) p.dst[h++] = i + k;
+            if (kind[k] > 1) p.src[v++] = i + k;
+        }
+        holes += both & 0xffff;
+        movers += both >> 16;
     }
     __syncthreads();
     for (int i = tid; i < p.n_pages; i += kThreads) {
-        const int r = p.refs_in[i];
+        const int r = m.count[i];
+        m.ids[i] = r > 0 ? i : -1;
         p.refs[i] = i < held && r > 0 ? r : 0;
     }
     __syncthreads();
     for (int k = tid; k < movers; k += kThreads) {   // as many holes as movers
-        p.ids[p.src[k]] = p.dst[k];
-        p.refs[p.dst[k]] = p.refs2[k];
+        const int from = p.src[k], to = p.dst[k];
+        m.ids[from] = to;
+        p.refs[to] = m.count[from];
     }
     if (tid == 0) {
         p.info[0] = 1;
@@ -304,9 +377,19 @@ __global__ void __launch_bounds__(kThreads) kvp_compact_kernel(const PageParams 
         p.info[2] = held;
         p.info[3] = p.n_pages - held;
     }
+    __syncthreads();
+    if (entries <= kRemapEntries) {
+        for (int i = tid; i < static_cast<int>(entries); i += kThreads) {
+            const int id = p.table_in[i];
+            p.table[i] = in_pool(p, id) ? m.ids[id] : id;
+        }
+    } else {
+        for (int i = tid; i < p.n_pages; i += kThreads) p.ids[i] = m.ids[i];
+    }
 }
 
 __global__ void __launch_bounds__(256) kvp_remap_kernel(const PageParams p, int64_t n) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n) return;
     const int id = p.table_in[i];
@@ -332,14 +415,22 @@ size_t lay_out(PageParams* p, void* ws, int n_seqs, int max_pages, int n_pages) 
         *ptr = ws ? reinterpret_cast<int*>(at + off) : nullptr;
         off += pad256(n * sizeof(int));
     };
-    take(&p->refs2, n_pages);
+    take(&p->scratch, scratch_ints(n_seqs, n_pages));
     take(&p->ids, n_pages);
-    take(&p->keeper, n_seqs);
-    take(&p->base, n_seqs);
-    take(&p->tail, n_seqs);
-    take(&p->new_len, n_seqs);
     take(&p->table2, static_cast<size_t>(n_seqs) * max_pages);
     return off;
+}
+
+// Launches a planning kernel: `shared` when its working arrays fit shared memory.
+template <typename... Args>
+cudaError_t launch_plan(void (*shared)(Args...), void (*global)(Args...), const PageParams& p,
+                        cudaStream_t stream, Args... args) {
+    const size_t bytes = scratch_ints(p.n_seqs, p.n_pages) * sizeof(int);
+    if (bytes > kSharedBytes) return launch_kernel(global, dim3(1), dim3(kThreads), 0, stream, args...);
+    const cudaError_t e = cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSharedBytes));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(shared, dim3(1), dim3(kThreads), bytes, stream, args...);
 }
 
 int prepare(PageParams* p, void* ws, size_t bytes, int n_seqs, int max_pages, int n_pages) {
@@ -389,8 +480,8 @@ extern "C" int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, i
     // no position is past 2^30: larger ones mean all of them
     p.window = window > (1 << 30) ? 1 << 30 : window;
     p.sinks = sinks > (1 << 30) ? 1 << 30 : sinks;
-    return launch_kernel(kvp_reserve_kernel, dim3(1), dim3(kThreads), 0,
-                         static_cast<cudaStream_t>(stream), p) == cudaSuccess
+    return launch_plan(kvp_reserve_kernel<true>, kvp_reserve_kernel<false>, p,
+                       static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
 }
@@ -416,8 +507,8 @@ extern "C" int kvp_reassign(int* table, int* lens, int* refs, const int* parents
     p.dst = copy_dst;
     p.info = info;
     p.page = page;
-    return launch_kernel(kvp_reassign_kernel, dim3(1), dim3(kThreads), 0,
-                         static_cast<cudaStream_t>(stream), p) == cudaSuccess
+    return launch_plan(kvp_reassign_kernel<true>, kvp_reassign_kernel<false>, p,
+                       static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
 }
@@ -441,10 +532,9 @@ extern "C" int kvp_compact(const int* table, const int* refs, int* table_out, in
     p.dst = move_dst;
     p.info = info;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_kernel(kvp_compact_kernel, dim3(1), dim3(kThreads), 0, st, p);
     const int64_t n = static_cast<int64_t>(n_seqs) * max_pages;
-    if (e == cudaSuccess)
-        e = launch_kernel(kvp_remap_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
-                          st, p, n);
+    cudaError_t e = launch_plan(kvp_compact_kernel<true>, kvp_compact_kernel<false>, p, st, p, n);
+    if (e == cudaSuccess && n > kRemapEntries)
+        e = launch_dependent(kvp_remap_kernel, (n + 255) / 256, 256, 0, st, p, n);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
