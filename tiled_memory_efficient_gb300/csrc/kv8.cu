@@ -213,7 +213,7 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 // that lies in one CTA is written out directly, the others leave fp32 partial
 // results that kv8_merge_kernel combines.
 //
-// Inside a CTA every warp works on its own: tiles w, w + 8, ... of the share,
+// Inside a CTA every warp works on its own: tiles w, w + W, ... of the share (W warps),
 // through a ring of kStages (K, V) slots that it alone fills (TMA, an mbarrier
 // each) and empties, so warps meet only where a unit ends.  Lane s owns slot s:
 // it follows the slot's tiles through the table, a tile ahead of the copies it
@@ -230,10 +230,8 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 // the tokens of a V column may meet the product in any order that its other
 // operand shares, which is how 16-byte shared loads feed both (kTok below).
 
-constexpr int kWarps = 8;
-constexpr int kAttnThreads = kWarps * 32;
+constexpr int kMinShare = 4;      // tiles per CTA, at least
 constexpr int kMaxBatch = 1024;   // sequences per call (their tile counts live in shared memory)
-constexpr int kMinShare = kWarps; // tiles per CTA, at least (one per warp)
 
 struct AttnParams {
     const void* q;
@@ -249,6 +247,7 @@ struct AttnParams {
     int B, Hkv, rows, n_rb;   // rows = G * Nq of a KV head, row blocks
     int Nq, page_shift, n_pages, max_pages;
     int window, sinks, ctas, tile_shift;
+    int min_share;     // tiles per CTA, at least
     float scale_log2;
 };
 
@@ -274,11 +273,21 @@ __device__ __forceinline__ int seq_tile(const Seq& s, int v) {   // tile v of th
     return v < s.n_sink ? v : v + s.skip;
 }
 
-// Shares: CTA c takes [c T / n, (c + 1) T / n) of the T tiles, n CTAs.
-__device__ __forceinline__ int shares(int64_t T, int ctas) {
-    const int64_t n = (T + kMinShare - 1) / kMinShare;
-    return static_cast<int>(n < ctas ? n : ctas);
-}
+// Shares: the T tiles are cut into n runs of q or q + 1 tiles (the first rem of them).
+// T < 2^31 (checked on the host).
+struct Shares {
+    int n, q, rem;
+    __device__ __forceinline__ Shares(int T, const AttnParams& p) {
+        n = min((T + p.min_share - 1) / p.min_share, p.ctas);
+        q = n > 0 ? T / n : 0;
+        rem = T - q * n;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int owner(int x) const {   // CTA that holds tile x
+        const int big = rem * (q + 1);
+        return x < big ? x / (q + 1) : rem + (x - big) / q;
+    }
+};
 
 // Token that row m of a 16-token product tile stands for (both halves of 8
 // alike).  The 16-byte shared loads of K (lanes g = m, chunk t) and of V (lanes
@@ -294,26 +303,24 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 r;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "r"(a)
-                 : "memory");
+                 : "r"(a));
     return r;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -342,62 +349,70 @@ struct SlotInfo {
 // registers for more.
 template <int D, int NR>
 constexpr int tile_tokens() { return D == 64 && NR < 4 ? 64 : 32; }
+template <int D, int NR>
+constexpr int attn_warps() { return NR == 1 ? 12 : 8; }
 
 template <int D, int NR>
 struct AttnCfg {
+    static constexpr int kWarps = attn_warps<D, NR>();
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = tile_tokens<D, NR>();
-    static constexpr int kStages = D * kTile == 4096 ? 3 : 6;
+    static constexpr int kStages = 24 * 1024 * 8 / kWarps / (2 * D * kTile);
     static constexpr int kHalf = kTile * D;         // bytes of K (or V) of a tile
     static constexpr bool kQSmem = NR == 4;
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kRing = kWarps * kStages * kSlot;          // 192 KB
-    static constexpr int kMergeOff = kRing;                         // 8 warps x 8 rows x 64 fp32
+    static constexpr int kMergeOff = kRing;                         // [warp][8 rows][64] fp32
     static constexpr int kLseOff = kMergeOff + kWarps * 8 * 64 * 4;
-    static constexpr int kInfoOff = kLseOff + kWarps * 8 * 4;       // a slot each
+    static constexpr int kInfoOff = kLseOff + kWarps * NR * 8 * 4;  // a slot each
     static constexpr int kQOff = kInfoOff + kWarps * kStages * static_cast<int>(sizeof(SlotInfo));
     static constexpr int kBarOff = kQOff + (kQSmem ? NR * 8 * D * 2 + NR * 8 * 4 : 0);
     static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kPreOff = kMiscOff + 64;                   // B + 1 ints, then B
-    static int smem_bytes(int B) { return kPreOff + (2 * B + 1) * 4 + 1024; }
+    static constexpr int kPreOff = kMiscOff + 8 * kWarps;                   // B + 1 ints, then B
+    static constexpr int smem_bytes(int B) { return kPreOff + (2 * B + 1) * 4; }
+    static_assert(smem_bytes(kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
 };
 
-template <int D, bool BF16, int NR>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+// ONE: a tile lies in one page (page >= the tile's tokens); else it takes 2 or 4 boxes.
+template <int D, bool BF16, int NR, bool ONE>
+__global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnParams p) {
     using C = AttnCfg<D, NR>;
-    constexpr int ST = C::kStages, kTile = C::kTile;
+    constexpr int ST = C::kStages, kTile = C::kTile, kWarps = C::kWarps;
     constexpr int NQ = kTile / 16;     // 16-token quarters of a tile (2 or 4)
     constexpr int KC = D / 64;         // 16-byte chunks of a K row per lane
     constexpr int MT = D / 16;         // 16-dimension tiles of O^T
     constexpr int VB = D / 8;          // bytes of a V row per lane (16 or 8)
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     float* s_merge = reinterpret_cast<float*>(smem + C::kMergeOff);   // [warp][8 rows][64]
-    float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);       // [warp][8 rows]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
-    int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 16);    // [8]
-    int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
-    int* s_len = s_pre + p.B + 1;                                     // [B]
+    float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);       // [warp][8 NR rows]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * ST;   // this warp's slots
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff) + warp;
+    int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 4 * kWarps);   // [kWarps]
+    int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
+    int* s_len = s_pre + p.B + 1;                                     // [B]
 
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         // a slot's phase: its copies' bytes, and its lane's small copies
-        for (int i = 0; i < kWarps * ST; ++i) mbar_init(&bars[i], 2);
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 2);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
     // Launched as a programmatic dependent of the kernel before it (an append, as
     // a rule), whose writes it reads from here on; the merge may set up already.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    // exclusive prefix sums of the sequences' tile counts
+    // Exclusive prefix sums of the sequences' tile counts: up to 32 sequences each
+    // warp makes them for itself (all write the same), more are made together.
     int carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
-        const int b = b0 + static_cast<int>(threadIdx.x);
+    const bool few = p.B <= 32;
+    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
+        const int b = few ? lane : b0 + static_cast<int>(threadIdx.x);
         int len = 0;
         if (b < p.B) {
             len = p.lens[b];
@@ -411,125 +426,249 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += y;
         }
-        if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
         int before = carry, all = carry;
+        if (few) {
+            all = __shfl_sync(0xffffffffu, x, 31);
+        } else {
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += s_warp[i];
-            all += s_warp[i];
+            for (int i = 0; i < kWarps; ++i) {
+                if (i < warp) before += s_warp[i];
+                all += s_warp[i];
+            }
         }
         if (b < p.B) {
             s_pre[b] = before + x - n;
             s_len[b] = len;
         }
         carry = all;
-        __syncthreads();
+        if (!few) __syncthreads();
     }
-    if (threadIdx.x == 0) s_pre[p.B] = carry;
-    __syncthreads();
+    if (lane == 0) s_pre[p.B] = carry;
+    if (few) __syncwarp();
+    else __syncthreads();
     const int U = p.Hkv * p.n_rb;
-    const int64_t T = static_cast<int64_t>(carry) * U;
-    const int n_cta = shares(T, p.ctas);
+    const Shares sh(carry * U, p);
     const int c = static_cast<int>(blockIdx.x);
-    if (c >= n_cta) return;   // nothing in flight, no barrier left
-    const int64_t g0 = c * T / n_cta, g1 = (c + 1) * T / n_cta;
+    if (c >= sh.n) return;   // nothing in flight, no barrier left
+    const int g0 = sh.begin(c), g1 = sh.begin(c + 1);
 
     // (sequence, unit, tile) of a position in the concatenated lists
-    auto locate = [&](int64_t x, int& b, int& u, int& v) {
+    auto locate = [&](int x, int& b, int& u, int& v) {
         int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before x and is not empty
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (static_cast<int64_t>(s_pre[mid]) * U <= x) lo = mid;
+            if (s_pre[mid] * U <= x) lo = mid;
             else hi = mid - 1;
         }
         b = lo;
         const int n = s_pre[b + 1] - s_pre[b];
-        const int64_t r = x - static_cast<int64_t>(s_pre[b]) * U;
-        u = static_cast<int>(r / n);
-        v = static_cast<int>(r - static_cast<int64_t>(u) * n);
+        const int r = x - s_pre[b] * U;
+        u = r / n;
+        v = r - u * n;
     };
+
+    // ---- the first unit, and Q of a unit as B fragments: lane (g, t) holds
+    // dimensions 16 (t + 4 cc) .. + 15 of row g of each 8.  The raw rows are asked
+    // for ahead of their unit; make_q makes them fp16.  bf16 rows are scaled by a
+    // power of two first (their largest magnitude to [2^14, 2^15)), which the
+    // scores take back: fp16 then holds every value down to 2^-28 of the row's
+    // largest exactly.  They stay in registers, or (kQSmem) warp w prepares the 8
+    // rows w and leaves them in shared memory as [row tile][word pair][lane], and
+    // the factors behind them.
+    int b, u, v;
+    locate(g0, b, u, v);
+    int unit0 = g0 - v;         // the unit's first tile in the concatenated lists
+    constexpr int QN = C::kQSmem ? 1 : NR;
+    uint32_t qf[QN][KC][8];
+    float f_row[NR][2];   // softmax scale of this lane's score columns 2t, 2t + 1
+    uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::kQOff);
+    float* s_f = reinterpret_cast<float*>(smem + C::kQOff + NR * 8 * D * 2);
+    auto load_q = [&](int b_, int u_) {
+        const int h_ = u_ / p.n_rb;
+        const int64_t head = (static_cast<int64_t>(b_) * p.Hkv + h_) * p.rows;
+#pragma unroll
+        for (int nt = 0; nt < QN; ++nt) {
+            if (C::kQSmem && warp >= NR) continue;
+            const int r = (u_ - h_ * p.n_rb) * (8 * NR) + (C::kQSmem ? warp : nt) * 8 + g;
+#pragma unroll
+            for (int cc = 0; cc < KC; ++cc) {
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.q) + (head + r) * D + 16 * (t + 4 * cc));
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 lo = r < p.rows ? src[0] : z, hi = r < p.rows ? src[1] : z;
+                uint32_t* w = qf[nt][cc];
+                w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+                w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+            }
+        }
+    };
+    auto make_q = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < QN; ++nt) {
+            if (C::kQSmem && warp >= NR) continue;
+            int shift = 0;   // the row is scaled by 2^shift
+            if constexpr (BF16) {
+                uint32_t ex = 0u;   // largest finite bf16 exponent field
+#pragma unroll
+                for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t x = qf[nt][cc][i];
+                        const uint32_t a = (x >> 7) & 0xffu, e = (x >> 23) & 0xffu;
+                        ex = max(ex, max(a < 255u ? a : 0u, e < 255u ? e : 0u));
+                    }
+                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 1));
+                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 2));
+                shift = ex == 0u ? 0 : min(14 + 127 - static_cast<int>(ex), 126);
+                const float up = exp2i(shift);
+#pragma unroll
+                for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 x = unpack16<true>(qf[nt][cc][i]);
+                        qf[nt][cc][i] = pack2<false>(x.x * up, x.y * up);
+                    }
+            }
+            if constexpr (C::kQSmem) {
+#pragma unroll
+                for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint2*>(s_q + ((warp * KC + cc) * 4 + i) * 64 + 2 * lane) =
+                            make_uint2(qf[0][cc][2 * i], qf[0][cc][2 * i + 1]);
+                if (t == 0) s_f[warp * 8 + g] = p.scale_log2 * exp2i(-shift);
+            } else {
+                // lane 8t (row 2t) and lane 8t + 4 (row 2t + 1) know this lane's columns' shifts
+                f_row[nt][0] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t));
+                f_row[nt][1] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t + 4));
+            }
+        }
+        if constexpr (C::kQSmem) {
+            __syncthreads();   // (barriers of the previous unit's end came after its last read)
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt) {
+                f_row[nt][0] = s_f[nt * 8 + 2 * t];
+                f_row[nt][1] = s_f[nt * 8 + 2 * t + 1];
+            }
+        }
+    };
+    load_q(b, u);
 
     // ---- this lane's slot (lanes 0 .. ST - 1).  Page ids and scales travel by
     // asynchronous copies into the slot's SlotInfo: a load into a register would
     // hold up every lane that reads its own copy of that register.
     uint8_t* ring = smem + warp * (ST * C::kSlot);
-    uint64_t* full = bars + warp * ST;
     SlotInfo* infos = reinterpret_cast<SlotInfo*>(smem + C::kInfoOff) + warp * ST;
-    const int box_shift = min(p.page_shift, p.tile_shift);   // tokens per TMA box
-    const int boxes = kTile >> box_shift;                    // 1 to 4
-    int64_t next = g0 + warp + kWarps * lane;   // the tile `fetch` has looked up
-    int nb = 0, nu = 0, nv = 0, nh = 0, nn = 0; // its sequence, unit, list index; KV head; list length
-    Seq ns{};
+    const int box_shift = ONE ? p.tile_shift : p.page_shift;   // tokens per TMA box
+    const int boxes = ONE ? 1 : kTile >> box_shift;
+    // quarters that a box covers: quarter hf lies in box hf >> q_shift
+    const int q_shift = box_shift - 4;
+    int left = 0;                               // tiles of this lane not issued yet
+    int nb = 0, nu = 0, nv = 0, nh = 0, nn = 0; // the next one: sequence, unit, list index; KV head; list length
+    int n_sink = 0, n_skip = 0, n_len = 0, n_lo = 0;   // of its sequence (Seq)
+    const int* nrow = nullptr;                  // and its table row
     int ntok = 0, nseen = 0;                    // its first token; boxes some query sees
     int issued = 0;
     auto enter = [&]() {   // a new sequence
-        nn = s_pre[nb + 1] - s_pre[nb];
-        ns = seq_of(p, s_len[nb]);
+        const Seq x = seq_of(p, s_len[nb]);
+        nn = x.n;
+        n_sink = x.n_sink;
+        n_skip = x.skip;
+        n_len = x.len;
+        n_lo = x.lo;
+        nrow = p.table + static_cast<int64_t>(nb) * p.max_pages;
     };
-    // Page ids of tile `next`; a box no query sees need not have a page.
+    // Asks for the page ids of the next tile; a box no query sees need not have a page.
     auto fetch = [&]() {
-        if (next >= g1) return;
-        while (nv >= nn) {
-            nv -= nn;
-            if (++nu == U) {
-                nu = 0;
-                do ++nb;
-                while (s_pre[nb + 1] == s_pre[nb]);
-                enter();
-            }
+        if (left == 0) return;
+        if (nv >= nn) {
+            do {
+                nv -= nn;
+                if (++nu == U) {
+                    nu = 0;
+                    do ++nb;
+                    while (s_pre[nb + 1] == s_pre[nb]);
+                    enter();
+                }
+            } while (nv >= nn);
             nh = nu / p.n_rb;
         }
-        ntok = seq_tile(ns, nv) << p.tile_shift;
-        const int* row = p.table + static_cast<int64_t>(nb) * p.max_pages;
-        nseen = 0;
-        for (int i = 0; i < boxes; ++i) {
-            const int x = ntok + (i << box_shift);
-            if (x < ns.len && (x + (1 << box_shift) > ns.lo || x < p.sinks)) {
-                nseen |= 1 << i;
-                cp_async4(&infos[lane].pid[i], row + (x >> p.page_shift));
+        ntok = (nv < n_sink ? nv : nv + n_skip) << p.tile_shift;
+        if constexpr (ONE) {
+            cp_async4(&infos[lane].pid[0], nrow + (ntok >> p.page_shift));
+        } else {
+            nseen = 0;
+            for (int i = 0; i < boxes; ++i) {
+                const int x = ntok + (i << box_shift);
+                if (x < n_len && (x + (1 << box_shift) > n_lo || x < p.sinks)) {
+                    nseen |= 1 << i;
+                    cp_async4(&infos[lane].pid[i], nrow + (x >> p.page_shift));
+                }
             }
         }
         cp_async_commit();
     };
+    const int n_heads = p.n_pages * p.Hkv;   // past the pool copies fill zeros
+    const uint32_t dst0 = smem_u32(ring + lane * C::kSlot);
     auto issue = [&]() {
-        if (next >= g1) return;
-        uint8_t* dst = ring + lane * C::kSlot;
+        if (left == 0) return;
+        --left;
         SlotInfo* in = infos + lane;
         cp_async_wait_all();   // the ids, asked for a whole turn of the ring ago
         const volatile int* pids = in->pid;
         int bad = 0;
-        for (int i = 0; i < boxes; ++i) {
-            const int pid = (nseen >> i) & 1 ? pids[i] : -1;
+        if constexpr (ONE) {
+            const int pid = pids[0];
             if (pid < 0 || pid >= p.n_pages) {
-                bad |= 1 << i;
-                in->ks[i] = in->vs[i] = 1.0f;
-                if ((nseen >> i) & 1) atomicOr(p.status, kStatusPage);
+                bad = 1;
+                in->ks[0] = in->vs[0] = 1.0f;
+                atomicOr(p.status, kStatusPage);
             }
-        }
-        in->bad = bad;
-        ++issued;
-        mbar_arrive_expect_tx(&full[lane], C::kSlot);   // releases the stores above, too
-        for (int i = 0; i < boxes; ++i) {
-            const bool ok = !((bad >> i) & 1);
-            const int y = (ntok + (i << box_shift)) & ((1 << p.page_shift) - 1);
-            // past the pool the copy fills zeros
-            const int z = ok ? pids[i] * p.Hkv + nh : p.n_pages * p.Hkv;
-            tma_load_3d(&tmK, &full[lane], dst + (i << box_shift) * D, 0, y, z);
-            tma_load_3d(&tmV, &full[lane], dst + C::kHalf + (i << box_shift) * D, 0, y, z);
-            if (ok) {
-                cp_async4(&in->ks[i], p.k_scale + z);
-                cp_async4(&in->vs[i], p.v_scale + z);
+            in->bad = bad;
+            mbar_arrive_expect_tx(&full[lane], C::kSlot);   // releases the stores above, too
+            const int y = ntok & ((1 << p.page_shift) - 1);
+            const int z = bad ? n_heads : pid * p.Hkv + nh;
+            tma_load_3d_at(&tmK, &full[lane], dst0, 0, y, z);
+            tma_load_3d_at(&tmV, &full[lane], dst0 + C::kHalf, 0, y, z);
+            if (!bad) {
+                cp_async4(&in->ks[0], p.k_scale + z);
+                cp_async4(&in->vs[0], p.v_scale + z);
+            }
+        } else {
+            for (int i = 0; i < boxes; ++i) {
+                const int pid = (nseen >> i) & 1 ? pids[i] : -1;
+                if (pid < 0 || pid >= p.n_pages) {
+                    bad |= 1 << i;
+                    in->ks[i] = in->vs[i] = 1.0f;
+                    if ((nseen >> i) & 1) atomicOr(p.status, kStatusPage);
+                }
+            }
+            in->bad = bad;
+            mbar_arrive_expect_tx(&full[lane], C::kSlot);
+            for (int i = 0; i < boxes; ++i) {
+                const bool ok = !((bad >> i) & 1);
+                const int z = ok ? pids[i] * p.Hkv + nh : n_heads;
+                const uint32_t at = dst0 + (i << box_shift) * D;   // a box is a page: row 0
+                tma_load_3d_at(&tmK, &full[lane], at, 0, 0, z);
+                tma_load_3d_at(&tmV, &full[lane], at + C::kHalf, 0, 0, z);
+                if (ok) {
+                    cp_async4(&in->ks[i], p.k_scale + z);
+                    cp_async4(&in->vs[i], p.v_scale + z);
+                }
             }
         }
         cp_async_arrive(&full[lane]);
-        next += kWarps * ST;
+        ++issued;
         nv += kWarps * ST;
         fetch();
     };
     if (lane < ST) {
-        if (next < g1) {
-            locate(next, nb, nu, nv);
+        const int first = g0 + warp + kWarps * lane;
+        if (first < g1) {
+            left = (g1 - first + kWarps * ST - 1) / (kWarps * ST);
+            locate(first, nb, nu, nv);
             nh = nu / p.n_rb;
             enter();
         }
@@ -555,94 +694,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int tok_v0 = tok8<D>(2 * t), tok_v1 = tok8<D>(2 * t + 1);
 
     // ---- the share, unit by unit
-    int64_t mine = g0 + warp;   // this warp's next tile
-    int it = 0;                 // tiles this warp has done
-    int slot = 0;               // it % ST
-    uint32_t phase = 0;         // (it / ST) & 1
-    int b = 0, u, v;
-    locate(g0, b, u, v);
-    int64_t unit0 = g0 - v;     // the unit's first tile in the concatenated lists
+    int mine = g0 + warp;       // this warp's next tile
+    int slot = 0;               // of that tile
+    uint32_t phase = 0;         // and its turn of the ring
     while (unit0 < g1) {
-        while (s_pre[b + 1] == s_pre[b]) ++b;   // empty sequences
         const Seq s = seq_of(p, s_len[b]);
-        const int h = u / p.n_rb, rb = u % p.n_rb;
-        const int64_t unit1 = unit0 + s.n;
-        const int64_t end = unit1 < g1 ? unit1 : g1;
-        const int row0 = rb * (8 * NR);
+        const int h = u / p.n_rb, row0 = (u - h * p.n_rb) * (8 * NR);
+        const int unit1 = unit0 + s.n, end = min(unit1, g1);
         const int64_t head_row = (static_cast<int64_t>(b) * p.Hkv + h) * p.rows;   // of q, out, lse
-
-        // Q as fp16 B fragments: lane (g, t) holds dimensions 16 (t + 4 cc) .. + 15 of row g.
-        // bf16 rows are scaled by a power of two first (their largest magnitude
-        // to [2^14, 2^15)), which the scores take back: fp16 then holds every
-        // value down to 2^-28 of the row's largest exactly.  In registers, or
-        // (kQSmem) warp w prepares the 8 rows w and leaves them in shared memory
-        // as [row tile][word pair][lane], and the factors behind them.
-        uint32_t qf[C::kQSmem ? 1 : NR][KC][8];
-        float f_row[NR][2];   // softmax scale of this lane's score columns 2t, 2t + 1
-        uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::kQOff);
-        float* s_f = reinterpret_cast<float*>(smem + C::kQOff + NR * 8 * D * 2);
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt) {
-            if (C::kQSmem && nt != warp) continue;
-            const int r = row0 + nt * 8 + g;
-            uint32_t w[KC][8];
-#pragma unroll
-            for (int cc = 0; cc < KC; ++cc) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) + (head_row + r) * D + 16 * (t + 4 * cc));
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                const uint4 lo = r < p.rows ? src[0] : z, hi = r < p.rows ? src[1] : z;
-                w[cc][0] = lo.x, w[cc][1] = lo.y, w[cc][2] = lo.z, w[cc][3] = lo.w;
-                w[cc][4] = hi.x, w[cc][5] = hi.y, w[cc][6] = hi.z, w[cc][7] = hi.w;
-            }
-            int shift = 0;   // the row is scaled by 2^shift
-            if constexpr (BF16) {
-                uint32_t ex = 0u;   // largest finite bf16 exponent field
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t a = (w[cc][i] >> 7) & 0xffu, e = (w[cc][i] >> 23) & 0xffu;
-                        ex = max(ex, max(a < 255u ? a : 0u, e < 255u ? e : 0u));
-                    }
-                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 1));
-                ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, 2));
-                shift = ex == 0u ? 0 : min(14 + 127 - static_cast<int>(ex), 126);
-                const float up = exp2i(shift);
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 x = unpack16<true>(w[cc][i]);
-                        w[cc][i] = pack2<false>(x.x * up, x.y * up);
-                    }
-            }
-            if constexpr (C::kQSmem) {
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint2*>(s_q + ((nt * KC + cc) * 4 + i) * 64 + 2 * lane) =
-                            make_uint2(w[cc][2 * i], w[cc][2 * i + 1]);
-                if (t == 0) s_f[nt * 8 + g] = p.scale_log2 * exp2i(-shift);
-            } else {
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) qf[nt][cc][i] = w[cc][i];
-                // lane 8t (row 2t) and lane 8t + 4 (row 2t + 1) know this lane's columns' shifts
-                f_row[nt][0] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t));
-                f_row[nt][1] = p.scale_log2 * exp2i(-__shfl_sync(0xffffffffu, shift, 8 * t + 4));
-            }
-        }
-        if constexpr (C::kQSmem) {
-            __syncthreads();   // (the previous unit's last barrier came after its last read)
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt) {
-                f_row[nt][0] = s_f[nt * 8 + 2 * t];
-                f_row[nt][1] = s_f[nt * 8 + 2 * t + 1];
-            }
-        }
+        make_q();
 
         // running state of this lane's columns (rows 2t, 2t + 1 of each 8): m the
         // largest score, l the sum of 2^(score - m) over this lane's tokens, R
@@ -662,19 +722,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
         }
 
-        for (; mine < end; mine += kWarps, ++it) {
-            const int tok = seq_tile(s, static_cast<int>(mine - unit0)) * kTile;
+        for (; mine < end; mine += kWarps) {
+            const int tok = seq_tile(s, mine - unit0) * kTile;
             warp_wait(&full[slot], phase, abort_flag, p.status);
             const uint32_t sk = smem_u32(ring + slot * C::kSlot), sv = sk + C::kHalf;
             const volatile SlotInfo* in = infos + slot;
             const int bad = in->bad;
             float fk[NQ], lv[NQ];   // of each quarter: key scale, log2 of the value scale
+            if constexpr (ONE) {
+                const float a = in->ks[0], e = static_cast<float>(scale_exp(in->vs[0]));
 #pragma unroll
-            for (int hf = 0; hf < NQ; ++hf) {
-                const int i = (16 * hf) >> box_shift;
-                fk[hf] = in->ks[i];
-                lv[hf] = static_cast<float>(scale_exp(in->vs[i]));
+                for (int hf = 0; hf < NQ; ++hf) {
+                    fk[hf] = a;
+                    lv[hf] = e;
+                }
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < NQ; ++hf) {
+                    fk[hf] = in->ks[hf >> q_shift];
+                    lv[hf] = static_cast<float>(scale_exp(in->vs[hf >> q_shift]));
+                }
             }
+            // bit hf: the quarter has no readable page
+            auto bad_quarter = [&](int hf) { return ONE ? bad != 0 : ((bad >> (hf >> q_shift)) & 1) != 0; };
 
             // S^T of the tile's quarters
             float sc[NQ][NR][4];
@@ -742,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int hf = 0; hf < NQ; ++hf) {
                             const int key = tok + hf * 16 + tok_a + 8 * (e >> 1);
-                            const bool see = !((bad >> ((16 * hf) >> box_shift)) & 1) && key <= pos &&
+                            const bool see = !bad_quarter(hf) && key <= pos &&
                                              (p.window <= 0 || key > pos - p.window || key < p.sinks);
                             if (!see) sc[hf][nt][e] = -INFINITY;
                         }
@@ -834,8 +904,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = tok + hf * 16 + (i >> 1) * 8 + ((i & 1) ? tok_v1 : tok_v0);
-                        if (((bad >> ((16 * hf) >> box_shift)) & 1) || key >= s.len ||
-                            (key < s.lo && key >= p.sinks)) {
+                        if (bad_quarter(hf) || key >= s.len || (key < s.lo && key >= p.sinks)) {
 #pragma unroll
                             for (int j = 0; j < VB / 4; ++j) r[i][j] = 0u;
                         }
@@ -867,96 +936,91 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         }
 
-        // ---- the unit ends here for this CTA: combine the 8 warps
+        // ---- the unit ends here for this CTA: combine the warps.  The next unit's Q
+        // is asked for first.
         const bool whole = unit0 >= g0 && unit1 <= g1;
         const int part = 2 * c + (unit0 <= g0 ? 0 : 1);
-#pragma unroll 1
-        for (int nt = 0; nt < NR; ++nt) {
-            if (row0 + nt * 8 >= p.rows) break;
-            float inv[2], lse2[2];
-            // (nt is a run-time index here: pick the registers)
-            float mm[2], ll[2], RR[2], oo[MT][4];
-#pragma unroll
-            for (int k = 0; k < NR; ++k)
-                if (k == nt) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        mm[e] = m[k][e];
-                        ll[e] = l[k][e];
-                        RR[e] = R[k][e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) oo[i][e] = o[k][i][e];
-                }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = ll[e];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                lse2[e] = x == 0.0f ? -INFINITY : mm[e] + lg2_approx(x);   // a NaN stays one
-                inv[e] = x == 0.0f ? 0.0f : ex2_ftz(RR[e] - mm[e]) / x;
-            }
-            if (g == 0) {
-                s_lse[warp * 8 + 2 * t] = lse2[0];
-                s_lse[warp * 8 + 2 * t + 1] = lse2[1];
-            }
-#pragma unroll 1
-            for (int half = 0; half < D / 64; ++half) {
-                // dimensions VB g + 8 half .. + 7 of rows 2t, 2t + 1 (64 columns in all)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[4];
-#pragma unroll
-                    for (int k = 0; k < D / 64; ++k)
-                        if (k == half) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = oo[4 * k + i][e] * inv[e & 1];
-                        }
-                    float* at = s_merge + (warp * 8 + 2 * t) * 64 + 8 * g + 2 * i;
-                    *reinterpret_cast<float2*>(at) = make_float2(x[0], x[2]);
-                    *reinterpret_cast<float2*>(at + 64) = make_float2(x[1], x[3]);
-                }
-                __syncthreads();
-                // 256 threads: row threadIdx / 32, two columns each
-                const int r = warp, row = row0 + nt * 8 + r;
-                float M = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) M = fmaxf(M, s_lse[k * 8 + r]);
-                float sum = 0.0f, ox = 0.0f, oy = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float L = s_lse[k * 8 + r];
-                    const float wk = L == -INFINITY ? 0.0f : ex2_ftz(L - M);
-                    const float2 x = *reinterpret_cast<const float2*>(s_merge + (k * 8 + r) * 64 + 2 * lane);
-                    sum += wk;
-                    ox = fmaf(wk, x.x, ox);
-                    oy = fmaf(wk, x.y, oy);
-                }
-                const float n = sum == 0.0f ? 0.0f : 1.0f / sum;
-                // column 2 lane of this half: dimension VB (lane / 4) + 8 half + 2 (lane % 4)
-                const int dim = VB * g + 8 * half + 2 * t;
-                const float L = sum == 0.0f ? -INFINITY : M + lg2_approx(sum);
-                if (row < p.rows) {
-                    if (whole) {
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-                                                     (head_row + row) * D + dim) =
-                            pack2<BF16>(ox * n, oy * n);
-                        if (half == 0 && lane == 0) p.lse[head_row + row] = L * 0.6931471805599453f;
-                    } else {
-                        const int64_t pr = static_cast<int64_t>(part) * (8 * NR) + nt * 8 + r;
-                        *reinterpret_cast<float2*>(p.part_o + pr * D + dim) = make_float2(ox * n, oy * n);
-                        if (half == 0 && lane == 0) p.part_lse[pr] = L;
-                    }
-                }
-                __syncthreads();
-            }
-        }
         unit0 = unit1;
         if (++u == U) {
             u = 0;
-            ++b;
+            do ++b;
+            while (unit0 < g1 && s_pre[b + 1] == s_pre[b]);   // empty sequences
+        }
+        if (unit0 < g1) load_q(b, u);
+        // every warp's LSE of each row; this lane's columns: rows 2t, 2t + 1 of each 8
+        float up[NR][2];   // brings O^T to real units, then to the warp's share of the row
+        float own[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[nt][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                own[nt][e] = x == 0.0f ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
+                up[nt][e] = x == 0.0f ? 0.0f : ex2_ftz(R[nt][e] - m[nt][e]) / x;
+                if (g == 0) s_lse[(warp * NR + nt) * 8 + 2 * t + e] = own[nt][e];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // lanes g take warps g and g + 8
+                const int at = nt * 8 + 2 * t + e;
+                const float a = s_lse[g * NR * 8 + at];
+                const float z = kWarps > 8 && g + 8 < kWarps ? s_lse[(g + 8) * NR * 8 + at] : -INFINITY;
+                float M = fmaxf(a, z);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                float sum = (a == -INFINITY ? 0.0f : ex2_ftz(a - M)) + (z == -INFINITY ? 0.0f : ex2_ftz(z - M));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                up[nt][e] *= sum == 0.0f || own[nt][e] == -INFINITY ? 0.0f : ex2_ftz(own[nt][e] - M) / sum;
+                const int row = row0 + at;
+                if (warp == 0 && g == 0 && row < p.rows) {
+                    const float L = sum == 0.0f ? -INFINITY : M + lg2_approx(sum);
+                    if (whole) p.lse[head_row + row] = L * 0.6931471805599453f;
+                    else p.part_lse[static_cast<int64_t>(part) * (8 * NR) + at] = L;
+                }
+            }
+        // the warps' shares of O, 8 rows and 64 dimensions at a time: per lane the
+        // next 8 of its dimensions
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+            if (row0 + nt * 8 >= p.rows) break;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                if (nt + half > 0) __syncthreads();   // the previous step's sums are made
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float(&x)[4] = o[nt][4 * half + i];
+                    float* at = s_merge + (warp * 8 + 2 * t) * 64 + 8 * g + 2 * i;
+                    *reinterpret_cast<float2*>(at) = make_float2(x[0] * up[nt][0], x[2] * up[nt][0]);
+                    *reinterpret_cast<float2*>(at + 64) = make_float2(x[1] * up[nt][1], x[3] * up[nt][1]);
+                }
+                __syncthreads();
+                // warp r < 8 takes row r, two columns a lane
+                const int row = row0 + nt * 8 + warp;
+                if (warp < 8 && row < p.rows) {
+                    float ox = 0.0f, oy = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const float2 x =
+                            *reinterpret_cast<const float2*>(s_merge + (k * 8 + warp) * 64 + 2 * lane);
+                        ox += x.x;
+                        oy += x.y;
+                    }
+                    const int dim = VB * g + 8 * half + 2 * t;   // of column 2 lane
+                    if (whole)
+                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                     (head_row + row) * D + dim) = pack2<BF16>(ox, oy);
+                    else
+                        *reinterpret_cast<float2*>(
+                            p.part_o + (static_cast<int64_t>(part) * (8 * NR) + nt * 8 + warp) * D + dim) =
+                            make_float2(ox, oy);
+                }
+            }
         }
     }
     // After a wait that gave up, copies may still be on their way into this
@@ -979,9 +1043,10 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnPa
     const int unit = static_cast<int>(blockIdx.x / chunks);
     const int b = unit / U, u = unit % U;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Launched as a programmatic dependent of the attention kernel, whose results
-    // (and, through it, the lengths) it reads from here on.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");   // the next kernel may set up
+    // Launched as a programmatic dependent of the attention kernel, which lets this
+    // one start after its own wait: the lengths are complete here, the partial
+    // results after the wait below.
     // tiles of all sequences, and of those before b: each warp for itself, or
     // (many sequences) the CTA together
     const bool alone = p.B <= 128;
@@ -1009,18 +1074,17 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnPa
     }
     const int row0 = u % p.n_rb * (8 * NR);
     const int r = static_cast<int>(blockIdx.x % chunks) * kMergeRows + warp;   // within the block
-    if (r >= min(8 * NR, p.rows - row0)) return;
     const int n = seq_of(p, p.lens[b]).n;
-    const int64_t T = static_cast<int64_t>(all) * U;
-    const int n_cta = shares(T, p.ctas);
-    const int64_t first = static_cast<int64_t>(before) * U + static_cast<int64_t>(u) * n;
+    const Shares sh(all * U, p);
+    const int first = before * U + u * n;
     int c0 = 0, c1 = -1;   // the CTAs that hold part of the unit
     if (n > 0) {
-        c0 = static_cast<int>(((first + 1) * n_cta - 1) / T);
-        c1 = static_cast<int>(((first + n) * n_cta - 1) / T);
-        if (c0 == c1) return;   // written by that CTA
+        c0 = sh.owner(first);
+        c1 = sh.owner(first + n - 1);
     }
-    const int second = n > 0 && first > c0 * T / n_cta ? 1 : 0;   // slot of c0's part
+    const int second = n > 0 && first > sh.begin(c0) ? 1 : 0;   // slot of c0's part
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // in every thread: this grid ends after that one
+    if (r >= min(8 * NR, p.rows - row0) || c0 == c1) return;   // c0 == c1: written by that CTA
     auto part_row = [&](int cta) {
         return static_cast<int64_t>(2 * cta + (cta == c0 ? second : 0)) * (8 * NR) + r;
     };
@@ -1064,15 +1128,16 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnPa
         p.lse[row] = sum == 0.0f ? -INFINITY : (M + lg2_approx(sum)) * 0.6931471805599453f;
 }
 
-template <int D, bool BF16, int NR>
+template <int D, bool BF16, int NR, bool ONE>
 cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnParams p,
                         cudaStream_t stream) {
-    auto kern = kv8_attn_kernel<D, BF16, NR>;
+    auto kern = kv8_attn_kernel<D, BF16, NR, ONE>;
     p.tile_shift = AttnCfg<D, NR>::kTile == 64 ? 6 : 5;
+    p.min_share = kMinShare;
     const int smem = AttnCfg<D, NR>::smem_bytes(p.B);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, p.ctas, kAttnThreads, smem, stream, tmK, tmV, p);
+    e = launch_dependent(kern, p.ctas, AttnCfg<D, NR>::kThreads, smem, stream, tmK, tmV, p);
     if (e != cudaSuccess) return e;
     const int rows = 8 * NR < p.rows ? 8 * NR : p.rows;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.Hkv * p.n_rb *
@@ -1275,6 +1340,10 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     const void* words[] = {k_scale, v_scale, table, lens};
     if (!aligned(ptrs, 16) || !aligned(words, 4)) return ATTN_ERR_ALIGN;
     if (workspace_bytes < kv8_attn_workspace_size(B, Hq, Hkv, Nq, D)) return ATTN_ERR_WORKSPACE;
+    // the kernels count tiles of all sequences' table capacity in 32 bits
+    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Hq / Hkv) * Nq + 31) / 32 + 1) *
+            ((static_cast<int64_t>(max_pages) * page + 31) / 32 + 1) > 0x7fffffffll)
+        return ATTN_ERR_UNSUPPORTED;
     AttnParams p{};
     rc = device_setup_public(&p.status);
     if (rc != ATTN_OK) return rc;
@@ -1316,7 +1385,9 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
 #define TME_ATTN(d, b, n) \
-    if (D == d && bf16 == b && nr == n) e = launch_attn<d, b, n>(tmK, tmV, p, st);
+    if (D == d && bf16 == b && nr == n)                                              \
+        e = page >= tile_tokens<d, n>() ? launch_attn<d, b, n, true>(tmK, tmV, p, st) \
+                                        : launch_attn<d, b, n, false>(tmK, tmV, p, st);
     TME_ATTN(64, false, 1)
     TME_ATTN(64, false, 2)
     TME_ATTN(64, false, 4)
