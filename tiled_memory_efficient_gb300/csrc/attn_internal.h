@@ -2,6 +2,7 @@
 // translation units (not part of the public C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -17,6 +18,23 @@ inline cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block,
     void* ptrs[] = {static_cast<void*>(&args)...};
     return cudaLaunchKernel(reinterpret_cast<const void*>(kern), grid, block, ptrs, smem, stream);
 }
+
+// Raises a kernel's shared-memory limit the first time it is launched on each
+// device (one static object per kernel; the setting lasts as long as the context).
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};   // bit per device
+    template <typename Kern>
+    cudaError_t raise(Kern kern, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Launch as a programmatic dependent of the previous kernel in the stream:
 // the grid may start before that kernel has ended, and waits for it on the

@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -95,23 +96,58 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 128;
 
+// Largest finite magnitude of n packed pairs, as fp32 bits.  Magnitudes order like
+// their bits, so the pairs' maximum is taken on the 16-bit fields; only where it
+// is an infinity or NaN are those left out one by one.
+template <bool BF16, int N>
+__device__ __forceinline__ uint32_t amax_bits(const uint4 (&w)[N]) {
+    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+    uint32_t u = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        u = __vmaxu2(u, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                 __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+    uint32_t top = max(u & 0xffffu, u >> 16);
+    if (top >= kInf) {
+        top = 0u;
+#pragma unroll 1
+        for (int i = 0; i < 4 * N; ++i) {
+            uint32_t x = 0u;   // (a register array takes no run-time index)
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (i == 4 * k) x = w[k].x;
+                if (i == 4 * k + 1) x = w[k].y;
+                if (i == 4 * k + 2) x = w[k].z;
+                if (i == 4 * k + 3) x = w[k].w;
+            }
+            const uint32_t lo = x & 0x7fffu, hi = (x >> 16) & 0x7fffu;
+            top = max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+        }
+    }
+    return __float_as_uint(unpack16<BF16>(top).x);
+}
+
 // One CTA per (sequence, page it may touch, KV head, keys or values): the page's
 // new tokens are read once into registers (NV 16-byte vectors a thread, PAGE * D
 // = 1024 NV), their largest magnitude gives the scale, then they are rounded
 // and written; earlier tokens of the page are read only when the scale grew.
+// Bound by memory: 64 registers a thread leave 8 CTAs of 16 KB (64-token pages, D =
+// 128) in flight on an SM, and the tokens are asked for before the page's id.
 template <int D, int PAGE, bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 5 : 8)
+    kv8_append_kernel(const AppendParams p) {
     constexpr int NV = PAGE * D / 8 / kAppendThreads;
     static_assert(NV >= 1, "a thread holds at least one vector");
-    constexpr int VPT = D / 8;   // vectors per token
+    constexpr int VPT = D / 8;                        // vectors per token
+    constexpr int STEP = kAppendThreads / VPT;        // tokens between a thread's vectors
     asm volatile("griddepcontrol.launch_dependents;");   // the attention may set up meanwhile
-    int64_t id = blockIdx.x;
-    const int which = static_cast<int>(id & 1);
+    int id = static_cast<int>(blockIdx.x);
+    const int which = id & 1;
     id >>= 1;
-    const int h = static_cast<int>(id % p.Hkv);
+    const int h = id % p.Hkv;
     id /= p.Hkv;
-    const int slot = static_cast<int>(id % p.n_slots);
-    const int b = static_cast<int>(id / p.n_slots);
+    const int slot = id % p.n_slots;
+    const int b = id / p.n_slots;
     const int len = p.lens[b];
     const int n = p.n_new ? p.n_new[b] : p.T;
     if (n == 0) return;
@@ -124,38 +160,24 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     const int t0 = pj * PAGE;
     if (t0 >= len) return;
     const int pid = p.table[static_cast<int64_t>(b) * p.max_pages + pj];
+    const int pos0 = t0 + static_cast<int>(threadIdx.x) / VPT;   // position of the first vector
+    const uint16_t* src = p.src[which] + b * p.sb + h * p.sh + (pos0 - start) * p.st +
+                          threadIdx.x % VPT * 8;
+    uint4 w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int pos = pos0 + i * STEP;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (pos >= start && pos < len) w[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * (STEP * p.st)));
+    }
     if (pid < 0 || pid >= p.n_pages) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
         return;
     }
-    const uint16_t* src = p.src[which] + b * p.sb + h * p.sh;
-    uint8_t* dst = p.pages[which] + (static_cast<int64_t>(pid) * p.Hkv + h) * (PAGE * D);
+    uint8_t* dst = p.pages[which] + (static_cast<int64_t>(pid) * p.Hkv + h) * (PAGE * D) + threadIdx.x * 8;
     float* scale = p.scales[which] + static_cast<int64_t>(pid) * p.Hkv + h;
     const float s_old = t0 < start ? *scale : 0.0f;
-
-    uint4 w[NV];
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * kAppendThreads;
-        const int pos = t0 + c / VPT;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pos >= start && pos < len)
-            w[i] = *reinterpret_cast<const uint4*>(src + (pos - start) * p.st + c % VPT * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16<BF16>(x[j]);
-            const float a = fabsf(f.x), c = fabsf(f.y);
-            amax = fmaxf(amax, a <= 3.4028235e38f ? a : 0.0f);   // finite ones only
-            amax = fmaxf(amax, c <= 3.4028235e38f ? c : 0.0f);
-        }
-    }
-    // magnitudes order like their bits
-    uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    uint32_t u = __reduce_max_sync(0xffffffffu, amax_bits<BF16>(w));
     __shared__ uint32_t s_max[kAppendThreads / 32];
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = u;
     __syncthreads();   // also: every thread has read the old scale
@@ -166,12 +188,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     e = max(e, e_old);
     if (threadIdx.x == 0) *scale = exp2i(e);
     const float inv = exp2i(-e);
-    const float redo = e_old - e < -100 ? 0.0f : exp2i(e_old - e);   // 448 * 2^-100 rounds to 0
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * kAppendThreads;
-        const int pos = t0 + c / VPT;
-        uint2* at = reinterpret_cast<uint2*>(dst + c * 8);
+        const int pos = pos0 + i * STEP;
         if (pos >= start && pos < len) {
             const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t r[4];
@@ -180,8 +199,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
                 const float2 f = unpack16<BF16>(x[j]);
                 r[j] = f32_to_e4m3x2(f.x * inv, f.y * inv);
             }
-            *at = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
-        } else if (pos < start && e != e_old) {
+            *reinterpret_cast<uint2*>(dst + i * (kAppendThreads * 8)) =
+                make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+        }
+    }
+    if (e != e_old) {   // the earlier tokens, to the larger scale
+        const float redo = e_old - e < -100 ? 0.0f : exp2i(e_old - e);   // 448 * 2^-100 rounds to 0
+#pragma unroll 1
+        for (int pos = pos0; pos < start && pos < t0 + PAGE; pos += STEP) {
+            uint2* at = reinterpret_cast<uint2*>(dst + (pos - pos0) / STEP * (kAppendThreads * 8));
             const uint2 o = *at;
             const uint32_t x[2] = {o.x, o.y};
             uint32_t r[4];
@@ -947,9 +973,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
             while (unit0 < g1 && s_pre[b + 1] == s_pre[b]);   // empty sequences
         }
         if (unit0 < g1) load_q(b, u);
-        // every warp's LSE of each row; this lane's columns: rows 2t, 2t + 1 of each 8
+        // Every warp's LSE of each row to shared memory; then lane i weighs row i of
+        // the unit (mod 8 NR), and this lane's columns take their rows' factors.
         float up[NR][2];   // brings O^T to real units, then to the warp's share of the row
-        float own[NR][2];
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -957,33 +983,35 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
                 float x = l[nt][e];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                own[nt][e] = x == 0.0f ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
+                if (g == 0)
+                    s_lse[(warp * NR + nt) * 8 + 2 * t + e] =
+                        x == 0.0f ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
                 up[nt][e] = x == 0.0f ? 0.0f : ex2_ftz(R[nt][e] - m[nt][e]) / x;
-                if (g == 0) s_lse[(warp * NR + nt) * 8 + 2 * t + e] = own[nt][e];
             }
         __syncthreads();
+        {
+            const int i = lane % (8 * NR);
+            float a[kWarps], M = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // lanes g take warps g and g + 8
-                const int at = nt * 8 + 2 * t + e;
-                const float a = s_lse[g * NR * 8 + at];
-                const float z = kWarps > 8 && g + 8 < kWarps ? s_lse[(g + 8) * NR * 8 + at] : -INFINITY;
-                float M = fmaxf(a, z);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                float sum = (a == -INFINITY ? 0.0f : ex2_ftz(a - M)) + (z == -INFINITY ? 0.0f : ex2_ftz(z - M));
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                up[nt][e] *= sum == 0.0f || own[nt][e] == -INFINITY ? 0.0f : ex2_ftz(own[nt][e] - M) / sum;
-                const int row = row0 + at;
-                if (warp == 0 && g == 0 && row < p.rows) {
-                    const float L = sum == 0.0f ? -INFINITY : M + lg2_approx(sum);
-                    if (whole) p.lse[head_row + row] = L * 0.6931471805599453f;
-                    else p.part_lse[static_cast<int64_t>(part) * (8 * NR) + at] = L;
-                }
+            for (int k = 0; k < kWarps; ++k) {
+                a[k] = s_lse[k * (8 * NR) + i];
+                M = fmaxf(M, a[k]);
             }
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sum += a[k] == -INFINITY ? 0.0f : ex2_ftz(a[k] - M);
+            const float own = s_lse[warp * (8 * NR) + i];
+            const float share = sum == 0.0f || own == -INFINITY ? 0.0f : ex2_ftz(own - M) / sum;
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    up[nt][e] *= __shfl_sync(0xffffffffu, share, nt * 8 + 2 * t + e);
+            if (warp == 0 && lane < 8 * NR && row0 + i < p.rows) {
+                const float L = sum == 0.0f ? -INFINITY : M + lg2_approx(sum);
+                if (whole) p.lse[head_row + row0 + i] = L * 0.6931471805599453f;
+                else p.part_lse[static_cast<int64_t>(part) * (8 * NR) + i] = L;
+            }
+        }
         // the warps' shares of O, 8 rows and 64 dimensions at a time: per lane the
         // next 8 of its dimensions
 #pragma unroll
@@ -1135,7 +1163,8 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnPara
     p.tile_shift = AttnCfg<D, NR>::kTile == 64 ? 6 : 5;
     p.min_share = kMinShare;
     const int smem = AttnCfg<D, NR>::smem_bytes(p.B);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(kern, AttnCfg<D, NR>::smem_bytes(kMaxBatch));
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, p.ctas, AttnCfg<D, NR>::kThreads, smem, stream, tmK, tmV, p);
     if (e != cudaSuccess) return e;
@@ -1214,13 +1243,20 @@ int check_cache(int B, int Hkv, int D, int page, int n_pages, int max_pages) {
     return ATTN_OK;
 }
 
+// SM count of the current device (0 without one), asked for once per device.
 int device_sms() {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 

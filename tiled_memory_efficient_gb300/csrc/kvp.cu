@@ -423,12 +423,11 @@ size_t lay_out(PageParams* p, void* ws, int n_seqs, int max_pages, int n_pages) 
 
 // Launches a planning kernel: `shared` when its working arrays fit shared memory.
 template <typename... Args>
-cudaError_t launch_plan(void (*shared)(Args...), void (*global)(Args...), const PageParams& p,
-                        cudaStream_t stream, Args... args) {
+cudaError_t launch_plan(SmemLimit& limit, void (*shared)(Args...), void (*global)(Args...),
+                        const PageParams& p, cudaStream_t stream, Args... args) {
     const size_t bytes = scratch_ints(p.n_seqs, p.n_pages) * sizeof(int);
     if (bytes > kSharedBytes) return launch_kernel(global, dim3(1), dim3(kThreads), 0, stream, args...);
-    const cudaError_t e = cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kSharedBytes));
+    const cudaError_t e = limit.raise(shared, static_cast<int>(kSharedBytes));
     if (e != cudaSuccess) return e;
     return launch_kernel(shared, dim3(1), dim3(kThreads), bytes, stream, args...);
 }
@@ -480,7 +479,8 @@ extern "C" int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, i
     // no position is past 2^30: larger ones mean all of them
     p.window = window > (1 << 30) ? 1 << 30 : window;
     p.sinks = sinks > (1 << 30) ? 1 << 30 : sinks;
-    return launch_plan(kvp_reserve_kernel<true>, kvp_reserve_kernel<false>, p,
+    static SmemLimit limit;
+    return launch_plan(limit, kvp_reserve_kernel<true>, kvp_reserve_kernel<false>, p,
                        static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
@@ -507,7 +507,8 @@ extern "C" int kvp_reassign(int* table, int* lens, int* refs, const int* parents
     p.dst = copy_dst;
     p.info = info;
     p.page = page;
-    return launch_plan(kvp_reassign_kernel<true>, kvp_reassign_kernel<false>, p,
+    static SmemLimit limit;
+    return launch_plan(limit, kvp_reassign_kernel<true>, kvp_reassign_kernel<false>, p,
                        static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
@@ -533,7 +534,8 @@ extern "C" int kvp_compact(const int* table, const int* refs, int* table_out, in
     p.info = info;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t n = static_cast<int64_t>(n_seqs) * max_pages;
-    cudaError_t e = launch_plan(kvp_compact_kernel<true>, kvp_compact_kernel<false>, p, st, p, n);
+    static SmemLimit limit;
+    cudaError_t e = launch_plan(limit, kvp_compact_kernel<true>, kvp_compact_kernel<false>, p, st, p, n);
     if (e == cudaSuccess && n > kRemapEntries)
         e = launch_dependent(kvp_remap_kernel, (n + 255) / 256, 256, 0, st, p, n);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
