@@ -9,7 +9,6 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import re
@@ -355,89 +354,61 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
     return out, lse
 
 
-class _on_device:
-    """Makes a device current for a call (nothing to do when it is)."""
-    __slots__ = ("index", "prev")
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        import torch
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.prev != self.index:
-            import torch
-            torch.cuda.set_device(self.prev)
+_BOUND = ("kv8_append", "kv8_attn", "kv8_attn_workspace_size", "kv8_copy_pages", "kvp_reserve",
+          "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
+          "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size")
+_bind = None
 
 
-def _call(fn: str, dev: int, *args):
-    """lib.fn(*args, current stream) with device `dev` current; raises on an error.
-    (The calls below take a few microseconds on the GPU for a decoding step, so
-    this side is kept short: one test per tensor, and only one that fails is
-    looked at again to say why.)"""
-    import torch
-    f = getattr(_lib or load(), fn)
-    try:
-        stream = torch._C._cuda_getCurrentRawStream(dev)   # what current_stream() wraps
-    except AttributeError:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev:
-        rc = f(*args, stream)
-    else:
-        with _on_device(dev):
-            rc = f(*args, stream)
-    if rc != ATTN_OK:
-        raise AttnError(fn, rc)
-
-
-def _fits(t, shape, dtype, dev) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+def _load_bind():
+    """The compiled part of this binding (csrc/bind.cpp): the checks, outputs and
+    workspaces of the calls below, which decoding steps make many of."""
+    global _bind
+    lib = load()
+    with _lock:
+        if _bind is None:
+            import importlib.util
+            path = os.path.join(PKG, "_build", "_bind.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: run __graft_entry__.build() first")
+            import torch  # noqa: F401  (its libraries, before the module that needs them)
+            spec = importlib.util.spec_from_file_location("_bind", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.init(*(ctypes.cast(getattr(lib, n), _vp).value for n in _BOUND))
+            _bind = mod
+    return _bind
 
 
 def _need(name, t, shape, dtype, dev):
     """Raises unless t is a contiguous tensor of that shape and dtype on CUDA device dev."""
-    if not _fits(t, shape, dtype, dev):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"CUDA device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _workspace(workspace, size: int, dev: int):
-    """The caller's workspace after a look at it, or a new one (None: none needed)."""
-    import torch
-    if workspace is None:
-        return torch.empty(size, device=dev, dtype=torch.uint8) if size > 0 else None
-    if workspace.get_device() != dev or not workspace.is_contiguous():
+def _need_workspace(t, dev):
+    if t is not None and (t.get_device() != dev or not t.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
-    return workspace
 
 
-@functools.lru_cache(maxsize=1024)
-def _size_on(dev: int, fn: str, *args) -> int:
-    """A workspace size (a function of the sizes and the device alone)."""
-    with _on_device(dev):
-        return getattr(load(), fn)(*args)
+def _refused(fn: str, rc: int, explain):
+    """Raises for a call that did not run: a status of the library, or arguments that
+    do not fit together, which `explain` raises for."""
+    if rc > 0:
+        raise AttnError(fn, rc)
+    explain()
+    raise ValueError(f"{fn}: arguments do not fit together")
 
 
-def _window_args(q, k, v, window, sinks, scale):
-    """Device, dtype code, sizes and clamped window of a sliding-window call."""
-    dev, dt = q.get_device(), q.dtype
-    if not (dev >= 0 and q.dim() == 4 and k.dim() == 4 and k.dtype is dt and v.dtype is dt
-            and v.shape == k.shape and k.shape[0] == q.shape[0] and k.shape[3] == q.shape[3]
-            and k.get_device() == dev and v.get_device() == dev and q.is_contiguous()
-            and k.is_contiguous() and v.is_contiguous()):
-        _check(q, k, v)
+def _explain_window(q, k, v):
+    """Device of a sliding-window call's q, k, v; raises when they do not fit."""
+    _check(q, k, v)
+    _dtype_code(q)
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
         raise ValueError(f"tensors on {q.device}, {k.device} and {v.device}: one device is needed")
-    B, Hq, Nq, D = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    # the C ABI takes 32-bit counts; either may exceed the keys
-    return (dev, _dtype_code(q), (B, Hq, Hkv, Nq, Nk, D), float(scale),
-            min(int(window), 0x7fffffff), min(int(sinks), 0x7fffffff))
+    return dev
 
 
 def attn_fwd_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None,
@@ -446,44 +417,40 @@ def attn_fwd_window(q, k, v, window: int, sinks: int = 0, scale: float | None = 
     p = i + Nk - Nq and sees keys j <= p with j > p - window or j < sinks.
     Returns (out, lse) as attn_fwd does; workspace (allocated here when not
     given) as in include/attn.h."""
-    import torch
-    dev, dt, sizes, scale, window, sinks = _window_args(q, k, v, window, sinks, scale)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need("out", out, q.shape, q.dtype, dev)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], device=dev, dtype=torch.float32)
-    else:
-        _need("lse", lse, q.shape[:3], torch.float32, dev)
-    ws = _workspace(workspace, _size_on(dev, "attn_fwd_window_workspace_size", *sizes, window, sinks,
-                                        dt), dev)
-    _call("attn_fwd_window", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-          lse.data_ptr(), _ptr(ws), _nbytes(ws), *sizes, scale, window, sinks, dt)
-    return out, lse
+    r = (_bind or _load_bind()).attn_fwd_window(q, k, v, window, sinks, scale, out, lse, workspace)
+    if type(r) is tuple:
+        return r
+
+    def explain():
+        import torch
+        dev = _explain_window(q, k, v)
+        if out is not None:
+            _need("out", out, q.shape, q.dtype, dev)
+        if lse is not None:
+            _need("lse", lse, q.shape[:3], torch.float32, dev)
+        _need_workspace(workspace, dev)
+    _refused("attn_fwd_window", r, explain)
 
 
 def attn_bwd_window(q, k, v, out, dout, lse, window: int, sinks: int = 0,
                     scale: float | None = None, dq=None, dk=None, dv=None, workspace=None):
     """dq, dk, dv of attn_fwd_window (dk, dv summed over each GQA group)."""
-    import torch
-    dev, dt, sizes, scale, window, sinks = _window_args(q, k, v, window, sinks, scale)
-    _need("out", out, q.shape, q.dtype, dev)
-    _need("dout", dout, q.shape, q.dtype, dev)
-    _need("lse", lse, q.shape[:3], torch.float32, dev)
-    grads = []
-    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if g is None:
-            g = torch.empty_like(like)
-        else:
-            _need(name, g, like.shape, like.dtype, dev)
-        grads.append(g)
-    ws = _workspace(workspace, max(16, _size_on(dev, "attn_bwd_window_workspace_size", *sizes, window,
-                                                sinks, dt)), dev)
-    _call("attn_bwd_window", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-          dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
-          grads[2].data_ptr(), ws.data_ptr(), _nbytes(ws), *sizes, scale, window, sinks, dt)
-    return tuple(grads)
+    r = (_bind or _load_bind()).attn_bwd_window(q, k, v, out, dout, lse, window, sinks, scale, dq, dk,
+                                                dv, workspace)
+    if type(r) is tuple:
+        return r
+
+    def explain():
+        import torch
+        dev = _explain_window(q, k, v)
+        _need("out", out, q.shape, q.dtype, dev)
+        _need("dout", dout, q.shape, q.dtype, dev)
+        _need("lse", lse, q.shape[:3], torch.float32, dev)
+        for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if g is not None:
+                _need(name, g, like.shape, like.dtype, dev)
+        _need_workspace(workspace, dev)
+    _refused("attn_bwd_window", r, explain)
 
 
 def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None = None,
@@ -536,10 +503,6 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
-
-
 def ffn_forward(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4096, out=None,
                 workspace=None):
     """y = act(x W1^T + b1) W2^T + b2 over x [T, d_model], `chunk` tokens at a
@@ -586,25 +549,26 @@ def ffn_check_chunking(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4
 
 # ------------------------------------------------------------------ paged 8-bit KV cache
 
-def _pools(k_pages, v_pages, k_scale, v_scale, dev):
-    """Looks a cache's pools over: [n_pages, Hkv, page, D], or with a leading layer
-    dimension, 8-bit; scales of all but the last two."""
+def _explain_pools(k_pages, v_pages, k_scale, v_scale, layers=False):
+    """Device and shape of a cache's pools; raises when they do not fit together."""
     import torch
-    shape, dt = k_pages.shape, k_pages.dtype
-    if not (len(shape) in (4, 5) and dt in (torch.float8_e4m3fn, torch.uint8, torch.int8)
-            and k_pages.get_device() == dev >= 0 and k_pages.is_contiguous()):
-        raise ValueError("k_pages must be a contiguous tensor of 8-bit values [n_pages, Hkv, page, D] "
-                         f"on CUDA device {dev}, not {dt} {tuple(shape)} on {k_pages.device}")
+    shape, dt, dev = k_pages.shape, k_pages.dtype, k_pages.get_device()
+    if not (len(shape) in ((4, 5) if layers else (4,)) and k_pages.is_contiguous() and dev >= 0
+            and dt in (torch.float8_e4m3fn, torch.uint8, torch.int8)):
+        raise ValueError("k_pages must be a contiguous CUDA tensor of 8-bit values [n_pages, Hkv, page, "
+                         f"D], not {dt} {tuple(shape)} on {k_pages.device}")
     _need("v_pages", v_pages, shape, dt, dev)
     _need("k_scale", k_scale, shape[:-2], torch.float32, dev)
     _need("v_scale", v_scale, shape[:-2], torch.float32, dev)
-    return shape
+    return dev, shape
 
 
-def _layer(shape):
-    if len(shape) != 4:
-        raise ValueError(f"the pools {tuple(shape)} must be one layer's [n_pages, Hkv, page, D]")
-    return shape
+def _explain_table(table, lens, B, dev):
+    import torch
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages]")
+    _need("table", table, (B, table.shape[1]), torch.int32, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
 
 
 def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None):
@@ -612,90 +576,70 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
     of 8 with dense rows) into the paged cache (include/kvcache.h).  lens [B] are
     the lengths after the call; n_new [B] how many of the T tokens each sequence
     takes (None: all T)."""
-    import torch
-    dev = k.get_device()
-    n_pages, Hkv, page, D = _layer(_pools(k_pages, v_pages, k_scale, v_scale, dev))
-    if not (k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and k.shape[1] == Hkv
-            and k.shape[3] == D and v.get_device() == dev):
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, {Hkv}, T, {D}] on "
-                         "one device")
-    B, _, T, _ = k.shape
-    sb, sh, st, sd = k.stride()
-    if v.stride() != (sb, sh, st, sd) or sd != 1:
-        # strides of dimensions of size 1 do not matter
+    rc = (_bind or _load_bind()).kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new)
+    if rc == ATTN_OK:
+        return
+
+    def explain():
+        import torch
+        dev, (_, Hkv, _, D) = _explain_pools(k_pages, v_pages, k_scale, v_scale)
+        _dtype_code(k)
+        if not (k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and k.shape[1] == Hkv
+                and k.shape[3] == D and k.get_device() == dev and v.get_device() == dev):
+            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, {Hkv}, T, {D}] on "
+                             f"CUDA device {dev}")
         strides = [tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride())) for t in (k, v)]
-        if strides[0] != strides[1] or sd != 1 or v.stride(3) != 1:
+        if strides[0] != strides[1] or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides and dense rows")
-    if B == 1:
-        sb = 0
-    if Hkv == 1:
-        sh = 0
-    if T == 1:
-        st = 0
-    if table.dim() != 2:
-        raise ValueError("table must be [B, max_pages]")
-    max_pages = table.shape[1]
-    _need("table", table, (B, max_pages), torch.int32, dev)
-    _need("lens", lens, (B,), torch.int32, dev)
-    if n_new is not None:
-        _need("n_new", n_new, (B,), torch.int32, dev)
-    _call("kv8_append", dev, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(n_new), B,
-          Hkv, T, D, page, n_pages, max_pages, sb, sh, st, _dtype_code(k))
+        _explain_table(table, lens, k.shape[0], dev)
+        if n_new is not None:
+            _need("n_new", n_new, (k.shape[0],), torch.int32, dev)
+    _refused("kv8_append", rc, explain)
 
 
 def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,
              window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None):
     """Attention of the newest Nq positions of each sequence, q [B, Hq, Nq, D], over
     the paged cache (include/kvcache.h); returns (out, lse)."""
-    import torch
-    dev = q.get_device()
-    n_pages, Hkv, page, D = _layer(_pools(k_pages, v_pages, k_scale, v_scale, dev))
-    if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous CUDA tensor [B, Hq, Nq, {D}]")
-    B, Hq, Nq, _ = q.shape
-    if table.dim() != 2:
-        raise ValueError("table must be [B, max_pages]")
-    max_pages = table.shape[1]
-    _need("table", table, (B, max_pages), torch.int32, dev)
-    _need("lens", lens, (B,), torch.int32, dev)
-    dt = _dtype_code(q)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need("out", out, q.shape, q.dtype, dev)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], device=dev, dtype=torch.float32)
-    else:
-        _need("lse", lse, q.shape[:3], torch.float32, dev)
-    ws = _workspace(workspace, max(16, _size_on(dev, "kv8_attn_workspace_size", B, Hq, Hkv, Nq, D)),
-                    dev)
-    _call("kv8_attn", dev, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-          v_scale.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          ws.data_ptr(), _nbytes(ws), B, Hq, Hkv, Nq, D, page, n_pages, max_pages,
-          1.0 / math.sqrt(D) if scale is None else float(scale), min(int(window), 0x7fffffff),
-          min(int(sinks), 0x7fffffff), dt)
-    return out, lse
+    r = (_bind or _load_bind()).kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale,
+                                         window, sinks, out, lse, workspace)
+    if type(r) is tuple:
+        return r
+
+    def explain():
+        import torch
+        dev, (_, _, _, D) = _explain_pools(k_pages, v_pages, k_scale, v_scale)
+        _dtype_code(q)
+        if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous() or q.get_device() != dev:
+            raise ValueError(f"q must be a contiguous tensor [B, Hq, Nq, {D}] on CUDA device {dev}")
+        _explain_table(table, lens, q.shape[0], dev)
+        if out is not None:
+            _need("out", out, q.shape, q.dtype, dev)
+        if lse is not None:
+            _need("lse", lse, q.shape[:3], torch.float32, dev)
+        _need_workspace(workspace, dev)
+    _refused("kv8_attn", r, explain)
 
 
 def kv8_copy_pages(k_pages, v_pages, k_scale, v_scale, src, dst, count, max_count: int | None = None):
     """Copies pages src[i] to dst[i] for i < min(count[0], max_count) in every layer
     of the pools ([n_layers, n_pages, Hkv, page, D], or without layers)."""
-    import torch
-    dev = k_pages.get_device()
-    shape = _pools(k_pages, v_pages, k_scale, v_scale, dev)
-    n_pages, Hkv, page, D = shape[-4:]
-    _need("src", src, src.shape, torch.int32, dev)
-    _need("dst", dst, dst.shape, torch.int32, dev)
-    if count.dtype is not torch.int32 or count.numel() < 1 or count.get_device() != dev:
-        raise ValueError(f"count must be an int32 tensor on CUDA device {dev}")
-    room = min(src.numel(), dst.numel())
-    max_count = room if max_count is None else int(max_count)
-    if max_count > room:
-        raise ValueError(f"max_count {max_count} is past the {room} listed pairs")
-    _call("kv8_copy_pages", dev, k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-          v_scale.data_ptr(), src.data_ptr(), dst.data_ptr(), count.data_ptr(), max_count,
-          shape[0] if len(shape) == 5 else 1, Hkv, page, D, n_pages)
+    rc = (_bind or _load_bind()).kv8_copy_pages(k_pages, v_pages, k_scale, v_scale, src, dst, count,
+                                                max_count)
+    if rc == ATTN_OK:
+        return
+
+    def explain():
+        import torch
+        dev, _ = _explain_pools(k_pages, v_pages, k_scale, v_scale, layers=True)
+        _need("src", src, src.shape, torch.int32, dev)
+        _need("dst", dst, dst.shape, torch.int32, dev)
+        if count.dtype is not torch.int32 or count.numel() < 1 or count.get_device() != dev:
+            raise ValueError(f"count must be an int32 tensor on CUDA device {dev}")
+        room = min(src.numel(), dst.numel())
+        if max_count is not None and max_count > room:
+            raise ValueError(f"max_count {max_count} is past the {room} listed pairs")
+    _refused("kv8_copy_pages", rc, explain)
 
 
 def kvp_workspace_size(n_seqs: int, max_pages: int, n_pages: int) -> int:
@@ -703,22 +647,23 @@ def kvp_workspace_size(n_seqs: int, max_pages: int, n_pages: int) -> int:
     return load().kvp_workspace_size(n_seqs, max_pages, n_pages)
 
 
-def _page_args(table, refs, info, workspace):
-    """Device, sizes and workspace of a bookkeeping call."""
+def _explain_book(table, refs, info, workspace, lists=(), **per_seq):
+    """Raises when a bookkeeping call's tensors do not fit together: per_seq are int32
+    [n_seqs], lists (name, tensor, least entries)."""
     import torch
     dev = table.get_device()
     if table.dim() != 2 or refs.dim() != 1 or dev < 0:
         raise ValueError("table must be a CUDA tensor [n_seqs, max_pages], refs [n_pages]")
-    n_seqs, max_pages = table.shape
-    n_pages = refs.shape[0]
     _need("table", table, table.shape, torch.int32, dev)
     _need("refs", refs, refs.shape, torch.int32, dev)
     _need("info", info, (4,), torch.int32, dev)
-    if workspace is None:
-        size = max(16, kvp_workspace_size(n_seqs, max_pages, n_pages))
-    else:
-        size = 0
-    return dev, n_seqs, max_pages, n_pages, _workspace(workspace, size, dev)
+    for name, t in per_seq.items():
+        _need(name, t, table.shape[:1], torch.int32, dev)
+    for name, t, least in lists:
+        _need(name, t, t.shape, torch.int32, dev)
+        if t.numel() < least:
+            raise ValueError(f"{name} needs {least} entries")
+    _need_workspace(workspace, dev)
 
 
 def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sinks: int = 0,
@@ -726,30 +671,23 @@ def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sink
     """Adds n_new [n_seqs] tokens to the sequences' lengths and pages for them to
     their tables; with a window first gives back the pages it has left behind
     (include/kvcache.h).  info [4] int32 receives (done, taken, given back, free)."""
-    import torch
-    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
-    _need("lens", lens, (n_seqs,), torch.int32, dev)
-    _need("n_new", n_new, (n_seqs,), torch.int32, dev)
-    _call("kvp_reserve", dev, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), n_new.data_ptr(),
-          n_seqs, max_pages, n_pages, int(page), min(int(window), 0x7fffffff),
-          min(int(sinks), 0x7fffffff), info.data_ptr(), ws.data_ptr(), _nbytes(ws))
+    rc = (_bind or _load_bind()).kvp_reserve(table, lens, refs, n_new, page, info, window, sinks, workspace)
+    if rc != ATTN_OK:
+        _refused("kvp_reserve", rc,
+                 lambda: _explain_book(table, refs, info, workspace, lens=lens, n_new=n_new))
 
 
 def kvp_reassign(table, lens, refs, parents, page: int, copy_src, copy_dst, info, workspace=None):
     """Sequence c becomes what parents[c] was (c: kept, -1: freed); the pairs of
     pages to copy go to copy_src / copy_dst, info [4] int32 receives (done, pairs,
     given back, free) (include/kvcache.h)."""
-    import torch
-    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
-    _need("lens", lens, (n_seqs,), torch.int32, dev)
-    _need("parents", parents, (n_seqs,), torch.int32, dev)
-    _need("copy_src", copy_src, copy_src.shape, torch.int32, dev)
-    _need("copy_dst", copy_dst, copy_dst.shape, torch.int32, dev)
-    if copy_src.numel() < n_seqs or copy_dst.numel() < n_seqs:
-        raise ValueError(f"copy_src and copy_dst need {n_seqs} entries")
-    _call("kvp_reassign", dev, table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
-          parents.data_ptr(), n_seqs, max_pages, n_pages, int(page), copy_src.data_ptr(),
-          copy_dst.data_ptr(), info.data_ptr(), ws.data_ptr(), _nbytes(ws))
+    rc = (_bind or _load_bind()).kvp_reassign(table, lens, refs, parents, page, copy_src, copy_dst, info,
+                                              workspace)
+    if rc != ATTN_OK:
+        n = table.shape[0]
+        _refused("kvp_reassign", rc, lambda: _explain_book(
+            table, refs, info, workspace, (("copy_src", copy_src, n), ("copy_dst", copy_dst, n)), lens=lens,
+            parents=parents))
 
 
 def kvp_compact(table, refs, move_src, move_dst, info, table_out=None, refs_out=None,
@@ -757,16 +695,15 @@ def kvp_compact(table, refs, move_src, move_dst, info, table_out=None, refs_out=
     """Renumbers the held pages to the front of the pool (in place without table_out
     and refs_out); the moves go to move_src / move_dst, info [4] int32 receives (1,
     moves, held, free) (include/kvcache.h)."""
-    import torch
-    dev, n_seqs, max_pages, n_pages, ws = _page_args(table, refs, info, workspace)
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
-    _need("table_out", table_out, table.shape, torch.int32, dev)
-    _need("refs_out", refs_out, refs.shape, torch.int32, dev)
-    _need("move_src", move_src, move_src.shape, torch.int32, dev)
-    _need("move_dst", move_dst, move_dst.shape, torch.int32, dev)
-    if min(move_src.numel(), move_dst.numel()) < n_pages // 2:
-        raise ValueError(f"move_src and move_dst need {n_pages // 2} entries")
-    _call("kvp_compact", dev, table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
-          refs_out.data_ptr(), n_seqs, max_pages, n_pages, move_src.data_ptr(),
-          move_dst.data_ptr(), info.data_ptr(), ws.data_ptr(), _nbytes(ws))
+    rc = (_bind or _load_bind()).kvp_compact(table, refs, move_src, move_dst, info, table_out, refs_out,
+                                             workspace)
+    if rc != ATTN_OK:
+        def explain():
+            import torch
+            n = refs.numel() // 2
+            _explain_book(table, refs, info, workspace, (("move_src", move_src, n), ("move_dst", move_dst, n)))
+            _need("table_out", table_out, table.shape, torch.int32, table.get_device())
+            _need("refs_out", refs_out, refs.shape, torch.int32, table.get_device())
+        _refused("kvp_compact", rc, explain)
