@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <functional>
@@ -949,9 +950,10 @@ namespace {
 // Query ranges of the sliding-window dK/dV.  A key tile past the sinks meets
 // about (window + 127) / 128 + 1 query tiles of each of its G heads; a sink tile
 // meets every later one, so its list is cut into ranges of about one other
-// tile's work (its CTAs would otherwise outlast the grid).  When the other
-// tiles alone leave SMs idle, they are cut too.  Ranges hold at least
-// kWindowMinTiles query tiles.
+// tile's work (its CTAs would otherwise outlast the grid).  The others are cut
+// into the number of ranges that gives the shortest grid: waves of CTAs, each of
+// its query tiles and kWindowCtaTiles more (set-up, the first loads, the
+// epilogue).  Ranges hold at least kWindowMinTiles query tiles.
 struct WindowBwdPlan {
     int64_t n_qtiles = 0, n_ktiles = 0;
     int sink_tiles = 0;
@@ -959,6 +961,7 @@ struct WindowBwdPlan {
     int keys[2] = {0, 0};
 };
 constexpr int64_t kWindowMinTiles = 4;
+constexpr int64_t kWindowCtaTiles = 3;
 
 WindowBwdPlan window_bwd_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks,
                               int sms) {
@@ -974,22 +977,30 @@ WindowBwdPlan window_bwd_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window
     int64_t per = (static_cast<int64_t>(window) + 127) / 128 + 1;
     if (per > w.n_qtiles) per = w.n_qtiles;
     per *= G;
-    const int64_t units = groups * (w.n_ktiles - w.sink_tiles);
-    if (units > 0 && units < sms) {
-        int64_t want = (sms + units - 1) / units;
-        if (want > per / kWindowMinTiles) want = per / kWindowMinTiles;
-        if (want > 32) want = 32;
-        if (want > 1) w.splits[1] = static_cast<int>(want);
-    }
-    if (w.sink_tiles > 0) {
-        int64_t target = (per + w.splits[1] - 1) / w.splits[1];
+    const int64_t tiles = w.n_ktiles - w.sink_tiles;
+    // ranges of a sink tile for others of `target` query tiles (many sink tiles
+    // fill the device by themselves)
+    auto sink_splits = [&](int64_t target) {
+        if (w.sink_tiles == 0) return int64_t{1};
         if (target < kWindowMinTiles) target = kWindowMinTiles;
         int64_t want = (G * w.n_qtiles + target - 1) / target;
-        // many sink tiles fill the device by themselves
         const int64_t most = (4LL * sms + groups * w.sink_tiles - 1) / (groups * w.sink_tiles);
         if (want > most) want = most;
-        if (want > 256) want = 256;
-        w.splits[0] = static_cast<int>(want);
+        return want > 256 ? int64_t{256} : want;
+    };
+    int64_t best = 0;
+    for (int64_t s = 1; s <= 32 && (s == 1 || per / s >= kWindowMinTiles); ++s) {
+        const int64_t each = (per + s - 1) / s, ss = sink_splits(each);
+        const int64_t ctas = groups * (tiles * s + w.sink_tiles * ss);
+        const int64_t longest = std::max(tiles > 0 ? each : 0, (G * w.n_qtiles + ss - 1) / ss);
+        const int64_t cost = (ctas + sms - 1) / sms * (longest + kWindowCtaTiles);
+        // more ranges also mean more partial sums: they have to save 5%
+        if (s == 1 || cost * 20 < best * 19) {
+            best = cost;
+            w.splits[0] = static_cast<int>(ss);
+            w.splits[1] = static_cast<int>(s);
+        }
+        if (ctas > 8LL * sms) break;   // waves no longer matter
     }
     return w;
 }

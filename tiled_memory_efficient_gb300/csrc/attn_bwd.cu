@@ -553,10 +553,16 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             bool fast = (row0 + q_first + 32 <= p.rows_per_group) && (wkey_last < p.Nk);
             // WIN: key position of the chunk's first query, the last sees 31 more
             const int kq_first = base + q_first + p.causal_off;
-            if (WIN)
-                fast = fast && !window_edge(wkey_last - 31, wkey_last, kq_first, kq_first + 31,
-                                            p.window, p.sinks);
-            else if (CAUSAL)
+            // A block behind every window: its queries all see the same keys, the
+            // sinks among them (live: this thread's key is one, or the block is
+            // an ordinary one).
+            bool live = true;
+            if (WIN) {
+                const bool past = wkey_last <= kq_first - p.window;
+                live = !past || key < p.sinks;
+                fast = fast && (past || !window_edge(wkey_last - 31, wkey_last, kq_first,
+                                                     kq_first + 31, p.window, p.sinks));
+            } else if (CAUSAL)
                 fast = fast && (base + q_first + 32 <= p.Nq) && (wkey_last <= base + q_first);
             const uint64_t sl22 = f2(sc, sc);
             tmem_wait_ld();
@@ -574,7 +580,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                         const int e = i + 2 * h;
                         const uint64_t x = ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
                                                  sl22, h ? f2(l4.z, l4.w) : f2(l4.x, l4.y));
-                        const float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
+                        float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
+                        if constexpr (WIN) {
+                            p0 = live ? p0 : 0.0f;
+                            p1 = live ? p1 : 0.0f;
+                        }
                         const uint64_t dd = fmul2(
                             f2(p0, p1),
                             fadd2(f2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),

@@ -383,13 +383,14 @@ struct AttnCfg {
     static constexpr int kWarps = attn_warps<D, NR>();
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = tile_tokens<D, NR>();
-    static constexpr int kStages = 24 * 1024 * 8 / kWarps / (2 * D * kTile);
+    // 192 KB of slots; 128 KB with more rows, whose combination takes more room
+    static constexpr int kStages = (NR == 1 ? 192 : 128) * 1024 / kWarps / (2 * D * kTile);
     static constexpr int kHalf = kTile * D;         // bytes of K (or V) of a tile
     static constexpr bool kQSmem = NR == 4;
     static constexpr int kSlot = 2 * kHalf;
     static constexpr int kRing = kWarps * kStages * kSlot;          // 192 KB
-    static constexpr int kMergeOff = kRing;                         // [warp][8 rows][64] fp32
-    static constexpr int kLseOff = kMergeOff + kWarps * 8 * 64 * 4;
+    static constexpr int kMergeOff = kRing;                         // [warp][8 NR rows][64] fp32
+    static constexpr int kLseOff = kMergeOff + kWarps * NR * 8 * 64 * 4;
     static constexpr int kInfoOff = kLseOff + kWarps * NR * 8 * 4;  // a slot each
     static constexpr int kQOff = kInfoOff + kWarps * kStages * static_cast<int>(sizeof(SlotInfo));
     static constexpr int kBarOff = kQOff + (kQSmem ? NR * 8 * D * 2 + NR * 8 * 4 : 0);
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     constexpr int MT = D / 16;         // 16-dimension tiles of O^T
     constexpr int VB = D / 8;          // bytes of a V row per lane (16 or 8)
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* s_merge = reinterpret_cast<float*>(smem + C::kMergeOff);   // [warp][8 rows][64]
+    float* s_merge = reinterpret_cast<float*>(smem + C::kMergeOff);   // [warp][8 NR rows][64]
     float* s_lse = reinterpret_cast<float*>(smem + C::kLseOff);       // [warp][8 NR rows]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -1012,42 +1013,39 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
                 else p.part_lse[static_cast<int64_t>(part) * (8 * NR) + i] = L;
             }
         }
-        // the warps' shares of O, 8 rows and 64 dimensions at a time: per lane the
-        // next 8 of its dimensions
+        // the warps' shares of O, 64 dimensions at a time: per lane the next 8 of its
+        // dimensions of rows 2t, 2t + 1 of each 8
 #pragma unroll
-        for (int nt = 0; nt < NR; ++nt) {
-            if (row0 + nt * 8 >= p.rows) break;
+        for (int half = 0; half < D / 64; ++half) {
+            if (half > 0) __syncthreads();   // the previous step's sums are made
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                if (nt + half > 0) __syncthreads();   // the previous step's sums are made
+            for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float(&x)[4] = o[nt][4 * half + i];
-                    float* at = s_merge + (warp * 8 + 2 * t) * 64 + 8 * g + 2 * i;
+                    float* at = s_merge + ((warp * NR + nt) * 8 + 2 * t) * 64 + 8 * g + 2 * i;
                     *reinterpret_cast<float2*>(at) = make_float2(x[0] * up[nt][0], x[2] * up[nt][0]);
                     *reinterpret_cast<float2*>(at + 64) = make_float2(x[1] * up[nt][1], x[3] * up[nt][1]);
                 }
-                __syncthreads();
-                // warp r < 8 takes row r, two columns a lane
-                const int row = row0 + nt * 8 + warp;
-                if (warp < 8 && row < p.rows) {
-                    float ox = 0.0f, oy = 0.0f;
+            __syncthreads();
+            // a row per warp and turn, two columns a lane: dimension VB g + 8 half + 2t
+            for (int r = warp; r < min(8 * NR, p.rows - row0); r += kWarps) {
+                float ox = 0.0f, oy = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < kWarps; ++k) {
-                        const float2 x =
-                            *reinterpret_cast<const float2*>(s_merge + (k * 8 + warp) * 64 + 2 * lane);
-                        ox += x.x;
-                        oy += x.y;
-                    }
-                    const int dim = VB * g + 8 * half + 2 * t;   // of column 2 lane
-                    if (whole)
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-                                                     (head_row + row) * D + dim) = pack2<BF16>(ox, oy);
-                    else
-                        *reinterpret_cast<float2*>(
-                            p.part_o + (static_cast<int64_t>(part) * (8 * NR) + nt * 8 + warp) * D + dim) =
-                            make_float2(ox, oy);
+                for (int k = 0; k < kWarps; ++k) {
+                    const float2 x =
+                        *reinterpret_cast<const float2*>(s_merge + (k * NR * 8 + r) * 64 + 2 * lane);
+                    ox += x.x;
+                    oy += x.y;
                 }
+                const int dim = VB * g + 8 * half + 2 * t;
+                if (whole)
+                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                 (head_row + row0 + r) * D + dim) = pack2<BF16>(ox, oy);
+                else
+                    *reinterpret_cast<float2*>(
+                        p.part_o + (static_cast<int64_t>(part) * (8 * NR) + r) * D + dim) =
+                        make_float2(ox, oy);
             }
         }
     }

@@ -21,8 +21,8 @@ constexpr int kWarps = kThreads / 32;
 // The planning's steps depend on one another through the pages' counts, the list of
 // free ids and a few numbers per sequence, and each step costs a round trip of the
 // memory those are in: they live in shared memory up to this many bytes (2 ints a
-// page, 5 a sequence), in the workspace past it.  reassign of 64 sequences over
-// 2049 pages: @SH us against @WS us.
+// page, 5 a sequence, reassign's rows beside them when they fit, too), in the
+// workspace past it.  reassign of 64 sequences over 2049 pages: @SH us against @WS us.
 constexpr size_t kSharedBytes = 200 * 1024;
 // Table entries that compact's planning CTA renumbers itself; more take a second
 // kernel.
@@ -222,10 +222,11 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
 }
 
 template <bool SHARED>
-__global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams p) {
+__global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams p, bool rows_shared) {
     asm volatile("griddepcontrol.launch_dependents;");   // the copies may set up meanwhile
     const Scratch<SHARED> m(p);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int* table2 = SHARED && rows_shared ? m.tail + p.n_seqs : p.table2;
     const int cap = p.max_pages * p.page;
     for (int c = tid; c < p.n_seqs; c += kThreads) {
         int q = p.arg[c];
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
             const int id = j < has ? p.table[from + j] : -1;
             if (in_pool(p, old)) atomicSub(m.count + old, 1);
             if (in_pool(p, id) && j != tail) atomicAdd(m.count + id, 1);
-            p.table2[row + j] = id;
+            table2[row + j] = id;
         }
     }
     __syncthreads();
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
         const int tail = m.tail[c], at = m.base[c];
         const int64_t row = static_cast<int64_t>(c) * p.max_pages;
         for (int j = lane; j < cols; j += 32) {
-            int id = p.table2[row + j];   // this lane wrote it
+            int id = table2[row + j];   // this lane wrote it
             if (j == tail) {
                 p.src[at] = id;
                 id = m.ids[at];
@@ -424,8 +425,8 @@ size_t lay_out(PageParams* p, void* ws, int n_seqs, int max_pages, int n_pages) 
 // Launches a planning kernel: `shared` when its working arrays fit shared memory.
 template <typename... Args>
 cudaError_t launch_plan(SmemLimit& limit, void (*shared)(Args...), void (*global)(Args...),
-                        const PageParams& p, cudaStream_t stream, Args... args) {
-    const size_t bytes = scratch_ints(p.n_seqs, p.n_pages) * sizeof(int);
+                        const PageParams& p, size_t more, cudaStream_t stream, Args... args) {
+    const size_t bytes = scratch_ints(p.n_seqs, p.n_pages) * sizeof(int) + more;
     if (bytes > kSharedBytes) return launch_kernel(global, dim3(1), dim3(kThreads), 0, stream, args...);
     const cudaError_t e = limit.raise(shared, static_cast<int>(kSharedBytes));
     if (e != cudaSuccess) return e;
@@ -480,7 +481,7 @@ extern "C" int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, i
     p.window = window > (1 << 30) ? 1 << 30 : window;
     p.sinks = sinks > (1 << 30) ? 1 << 30 : sinks;
     static SmemLimit limit;
-    return launch_plan(limit, kvp_reserve_kernel<true>, kvp_reserve_kernel<false>, p,
+    return launch_plan(limit, kvp_reserve_kernel<true>, kvp_reserve_kernel<false>, p, 0,
                        static_cast<cudaStream_t>(stream), p) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
@@ -507,9 +508,11 @@ extern "C" int kvp_reassign(int* table, int* lens, int* refs, const int* parents
     p.dst = copy_dst;
     p.info = info;
     p.page = page;
+    const size_t rows = static_cast<size_t>(n_seqs) * max_pages * sizeof(int);
+    const bool rows_shared = scratch_ints(n_seqs, n_pages) * sizeof(int) + rows <= kSharedBytes;
     static SmemLimit limit;
     return launch_plan(limit, kvp_reassign_kernel<true>, kvp_reassign_kernel<false>, p,
-                       static_cast<cudaStream_t>(stream), p) == cudaSuccess
+                       rows_shared ? rows : 0, static_cast<cudaStream_t>(stream), p, rows_shared) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
 }
@@ -535,7 +538,7 @@ extern "C" int kvp_compact(const int* table, const int* refs, int* table_out, in
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t n = static_cast<int64_t>(n_seqs) * max_pages;
     static SmemLimit limit;
-    cudaError_t e = launch_plan(limit, kvp_compact_kernel<true>, kvp_compact_kernel<false>, p, st, p, n);
+    cudaError_t e = launch_plan(limit, kvp_compact_kernel<true>, kvp_compact_kernel<false>, p, 0, st, p, n);
     if (e == cudaSuccess && n > kRemapEntries)
         e = launch_dependent(kvp_remap_kernel, (n + 255) / 256, 256, 0, st, p, n);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
