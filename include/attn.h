@@ -190,8 +190,8 @@ int attn_fwd_masked(const void* q, const void* k, const void* v, void* out, floa
  *
  * workspace: attn_fwd_window_workspace_size() bytes, 16-byte aligned (may be
  * NULL when that is 0): the fp16 copy of v that attn_fwd_ws also makes (bf16,
- * Nq > 256; only its visible tiles), and the partial results of a grid under
- * one wave, whose key tiles are cut into ranges and merged like
+ * grids of a wave or more; only its visible tiles), or the partial results of a
+ * grid under one wave, whose key tiles are cut into ranges and merged like
  * attn_fwd_splitkv's.  Other arguments, layouts and errors are attn_fwd's.
  * Like the causal forwards it multiplies hidden keys' values by zero, so a
  * value tile that holds an infinity or NaN spoils the rows that meet it.

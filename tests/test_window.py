@@ -64,9 +64,9 @@ def test_forward_refusals(lib, change, code):
 
 
 def test_workspace_is_checked_first(lib):
-    ws = lib.attn_fwd_window_workspace_size(1, 2, 2, 300, 300, 64, 16, 0, 1)
-    assert ws >= 2 * 300 * 64 * 2 + 2 * 3   # bf16: the fp16 copy of v and its flags
-    args = (1, 2, 2, 300, 300, 64, 0.1, 16, 0, 1, None)
+    ws = lib.attn_fwd_window_workspace_size(64, 32, 2, 300, 300, 64, 16, 0, 1)
+    assert ws >= 128 * 300 * 64 * 2 + 128 * 3   # bf16: the fp16 copy of v and its flags
+    args = (64, 32, 2, 300, 300, 64, 0.1, 16, 0, 1, None)
     assert lib.attn_fwd_window(*[P] * 5, 0, ws, *args) == 1
     assert lib.attn_fwd_window(*[P] * 5, P + 8, ws, *args) == 3
     assert lib.attn_fwd_window(*[P] * 5, P, ws - 1, *args) == 6

@@ -273,7 +273,6 @@ struct AttnParams {
     int B, Hkv, rows, n_rb;   // rows = G * Nq of a KV head, row blocks
     int Nq, page_shift, n_pages, max_pages;
     int window, sinks, ctas, tile_shift;
-    int min_share;     // tiles per CTA, at least
     float scale_log2;
 };
 
@@ -304,8 +303,8 @@ __device__ __forceinline__ int seq_tile(const Seq& s, int v) {   // tile v of th
 struct Shares {
     int n, q, rem;
     __device__ __forceinline__ Shares(int T, const AttnParams& p) {
-        n = min((T + p.min_share - 1) / p.min_share, p.ctas);
-        q = n > 0 ? T / n : 0;
+        n = min((T + kMinShare - 1) / kMinShare, p.ctas);
+        q = n > 0 ? static_cast<int>(static_cast<unsigned>(T) / static_cast<unsigned>(n)) : 0;
         rem = T - q * n;
     }
     __device__ __forceinline__ int begin(int c) const { return c * q + min(c, rem); }
@@ -481,20 +480,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     if (c >= sh.n) return;   // nothing in flight, no barrier left
     const int g0 = sh.begin(c), g1 = sh.begin(c + 1);
 
-    // (sequence, unit, tile) of a position in the concatenated lists
-    auto locate = [&](int x, int& b, int& u, int& v) {
-        int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before x and is not empty
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pre[mid] * U <= x) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-        const int n = s_pre[b + 1] - s_pre[b];
-        const int r = x - s_pre[b] * U;
-        u = r / n;
-        v = r - u * n;
-    };
+    // KV head of a unit (unit = head * n_rb + row block; one block, as a rule)
+    auto head_of = [&](int u_) { return p.n_rb == 1 ? u_ : u_ / p.n_rb; };
 
     // ---- the first unit, and Q of a unit as B fragments: lane (g, t) holds
     // dimensions 16 (t + 4 cc) .. + 15 of row g of each 8.  The raw rows are asked
@@ -504,16 +491,30 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     // largest exactly.  They stay in registers, or (kQSmem) warp w prepares the 8
     // rows w and leaves them in shared memory as [row tile][word pair][lane], and
     // the factors behind them.
-    int b, u, v;
-    locate(g0, b, u, v);
-    int unit0 = g0 - v;         // the unit's first tile in the concatenated lists
+    int b;   // the last sequence that starts at or before g0: not an empty one
+    if (few) {
+        const bool before = lane < p.B && s_pre[lane] * U <= g0;
+        b = 31 - __clz(__ballot_sync(0xffffffffu, before));
+    } else {
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_pre[mid] * U <= g0) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo;
+    }
+    const int n_first = s_pre[b + 1] - s_pre[b];
+    int u = static_cast<int>(static_cast<unsigned>(g0 - s_pre[b] * U) / static_cast<unsigned>(n_first));
+    const int v_first = g0 - s_pre[b] * U - u * n_first;
+    int unit0 = g0 - v_first;   // the unit's first tile in the concatenated lists
     constexpr int QN = C::kQSmem ? 1 : NR;
     uint32_t qf[QN][KC][8];
     float f_row[NR][2];   // softmax scale of this lane's score columns 2t, 2t + 1
     uint32_t* s_q = reinterpret_cast<uint32_t*>(smem + C::kQOff);
     float* s_f = reinterpret_cast<float*>(smem + C::kQOff + NR * 8 * D * 2);
     auto load_q = [&](int b_, int u_) {
-        const int h_ = u_ / p.n_rb;
+        const int h_ = head_of(u_);
         const int64_t head = (static_cast<int64_t>(b_) * p.Hkv + h_) * p.rows;
 #pragma unroll
         for (int nt = 0; nt < QN; ++nt) {
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
                     enter();
                 }
             } while (nv >= nn);
-            nh = nu / p.n_rb;
+            nh = head_of(nu);
         }
         ntok = (nv < n_sink ? nv : nv + n_skip) << p.tile_shift;
         if constexpr (ONE) {
@@ -695,8 +696,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
         const int first = g0 + warp + kWarps * lane;
         if (first < g1) {
             left = (g1 - first + kWarps * ST - 1) / (kWarps * ST);
-            locate(first, nb, nu, nv);
-            nh = nu / p.n_rb;
+            nb = b;
+            nu = u;
+            nv = v_first + first - g0;   // fetch carries it into later units
+            nh = head_of(nu);
             enter();
         }
         fetch();
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     uint32_t phase = 0;         // and its turn of the ring
     while (unit0 < g1) {
         const Seq s = seq_of(p, s_len[b]);
-        const int h = u / p.n_rb, row0 = (u - h * p.n_rb) * (8 * NR);
+        const int h = head_of(u), row0 = (u - h * p.n_rb) * (8 * NR);
         const int unit1 = unit0 + s.n, end = min(unit1, g1);
         const int64_t head_row = (static_cast<int64_t>(b) * p.Hkv + h) * p.rows;   // of q, out, lse
         make_q();
@@ -1159,7 +1162,6 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnPara
                         cudaStream_t stream) {
     auto kern = kv8_attn_kernel<D, BF16, NR, ONE>;
     p.tile_shift = AttnCfg<D, NR>::kTile == 64 ? 6 : 5;
-    p.min_share = kMinShare;
     const int smem = AttnCfg<D, NR>::smem_bytes(p.B);
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, AttnCfg<D, NR>::smem_bytes(kMaxBatch));
