@@ -75,7 +75,12 @@ int kv8_append(const void* k, const void* v, void* k_pages, void* v_pages, float
  * on the device from lens, so mixed lengths are balanced without the host.
  * The keys' part of the arithmetic is exact in fp16 (e4m3 fits), scores, softmax
  * statistics and sums are fp32, the softmax terms of the value product fp16.
- * B <= 1024.  workspace: kv8_attn_workspace_size() bytes.
+ * B <= 1024, and all sequences' table capacity times KV heads and passes under
+ * 2^31 tiles of 32 tokens (ATTN_ERR_UNSUPPORTED otherwise).  Rows past a
+ * sequence's end and keys that no query of the call sees may hold anything; a NaN
+ * or infinity in a value that one of several queries (Nq > 1) sees reaches the
+ * queries of the call that do not see it, too.
+ * workspace: kv8_attn_workspace_size() bytes.
  */
 int kv8_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
              const float* v_scale, const int* table, const int* lens, void* out, float* lse,
@@ -103,7 +108,9 @@ int kv8_copy_pages(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
  * adds them to lens and fills the table with free pages (refs 0), lowest id
  * first, sequences in order.  With window > 0 a sequence that takes tokens first
  * gives back the pages that no query from its first new position on can see
- * (all their positions >= sinks and <= lens - window, lens before the call).
+ * (all their positions >= sinks and <= lens - window, lens before the call; the
+ * search goes back to the columns an earlier call has emptied, so a cache keeps
+ * one window and one number of sinks).
  * When pages or table columns run out nothing changes and ATTN_ERR_POOL is
  * recorded.  info[4] (device): 1 done / 0 not, pages taken, pages given back,
  * pages still free.  workspace: kvp_workspace_size() bytes.

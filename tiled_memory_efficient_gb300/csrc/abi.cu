@@ -544,8 +544,13 @@ namespace {
 
 // Launch plan of the sliding-window forward.  A query block of more than 256
 // positions runs one query head per group: its Q tiles then never span two
-// heads, whose windows lie far apart.  A shorter one (a decode step, a draft)
-// flattens the group's heads onto its KV head like the other forwards.
+// heads, whose windows lie far apart (GQA 14:2, D = 64, window 2000 of 20000 keys:
+// 512 queries 19.7 us, with the group's heads flattened onto their KV head like in
+// the other forwards 21.2; 1024 29.2 against 33.1).  So does one of more than 16
+// while that fills no more than a wave: more, smaller units (64 queries 13.3
+// against 17.9).  A shorter one (a decode step, a draft) or a larger batch of
+// such blocks flattens the heads, which reads K and V once per group (16 queries:
+// 12.9 against 13.2).
 struct WindowPlan {
     bool per_head = false;
     int64_t groups = 0, pairs = 0, rows = 0;   // rows per group
@@ -556,7 +561,8 @@ struct WindowPlan {
 
 WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks, int sms) {
     WindowPlan w;
-    w.per_head = Nq > 256;
+    if (sms <= 0) sms = device_sms();
+    w.per_head = Nq > 256 || (Nq > 16 && static_cast<int64_t>(B) * Hq <= sms);
     w.groups = static_cast<int64_t>(B) * (w.per_head ? Hq : Hkv);
     w.rows = w.per_head ? Nq : static_cast<int64_t>(Hq / Hkv) * Nq;
     w.pairs = (w.rows + 255) / 256;
@@ -573,12 +579,12 @@ WindowPlan window_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window, int s
     if (tiles > key_tiles(Nk)) tiles = key_tiles(Nk);
     w.tps = static_cast<int>(tiles);
     const int64_t units = w.groups * w.pairs;
-    if (sms <= 0) sms = device_sms();
     if (sms <= 0 || units >= sms) return w;
     w.under_wave = true;
     // Under one wave: cut the list into as many ranges as fill the SMs, of at
-    // least kWindowRangeTiles key tiles each.
-    constexpr int64_t kWindowRangeTiles = 4;
+    // least kWindowRangeTiles key tiles each (one query, window 2000, D = 128:
+    // 2 12.8 us, 4 16.5, 8 23.6).
+    constexpr int64_t kWindowRangeTiles = 2;
     int64_t want = sms / units;
     if (want > tiles / kWindowRangeTiles) want = tiles / kWindowRangeTiles;
     if (want > kMaxSplits) want = kMaxSplits;

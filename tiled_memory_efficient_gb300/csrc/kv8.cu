@@ -256,7 +256,13 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 // the tokens of a V column may meet the product in any order that its other
 // operand shares, which is how 16-byte shared loads feed both (kTok below).
 
-constexpr int kMinShare = 4;      // tiles per CTA, at least
+// Warps per CTA: 12 of them with 2 slots each instead of 3 took 5.4 us against 4.8 (8
+// sequences of 256 tokens, D = 64) and 51.4 against 50.4 (64K tokens, D = 128).
+constexpr int kWarps = 8;
+constexpr int kAttnThreads = kWarps * 32;
+// Tiles per CTA, at least: 12 of them put 8 sequences of 256 tokens on 6 CTAs, several
+// units each, 13.4 us against 5.4.
+constexpr int kMinShare = 4;
 constexpr int kMaxBatch = 1024;   // sequences per call (their tile counts live in shared memory)
 
 struct AttnParams {
@@ -374,13 +380,9 @@ struct SlotInfo {
 // registers for more.
 template <int D, int NR>
 constexpr int tile_tokens() { return D == 64 && NR < 4 ? 64 : 32; }
-template <int D, int NR>
-constexpr int attn_warps() { return NR == 1 ? 12 : 8; }
 
 template <int D, int NR>
 struct AttnCfg {
-    static constexpr int kWarps = attn_warps<D, NR>();
-    static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = tile_tokens<D, NR>();
     // 192 KB of slots; 128 KB with more rows, whose combination takes more room
     static constexpr int kStages = (NR == 1 ? 192 : 128) * 1024 / kWarps / (2 * D * kTile);
@@ -401,11 +403,11 @@ struct AttnCfg {
 
 // ONE: a tile lies in one page (page >= the tile's tokens); else it takes 2 or 4 boxes.
 template <int D, bool BF16, int NR, bool ONE>
-__global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnParams p) {
     using C = AttnCfg<D, NR>;
-    constexpr int ST = C::kStages, kTile = C::kTile, kWarps = C::kWarps;
+    constexpr int ST = C::kStages, kTile = C::kTile;
     constexpr int NQ = kTile / 16;     // 16-token quarters of a tile (2 or 4)
     constexpr int KC = D / 64;         // 16-byte chunks of a K row per lane
     constexpr int MT = D / 16;         // 16-dimension tiles of O^T
@@ -433,12 +435,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     // a rule), whose writes it reads from here on; the merge may set up already.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    // Exclusive prefix sums of the sequences' tile counts: up to 32 sequences each
-    // warp makes them for itself (all write the same), more are made together.
+    // exclusive prefix sums of the sequences' tile counts
     int carry = 0;
-    const bool few = p.B <= 32;
-    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
-        const int b = few ? lane : b0 + static_cast<int>(threadIdx.x);
+    for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
         int len = 0;
         if (b < p.B) {
             len = p.lens[b];
@@ -452,28 +452,23 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
             const int y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += y;
         }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
         int before = carry, all = carry;
-        if (few) {
-            all = __shfl_sync(0xffffffffu, x, 31);
-        } else {
-            if (lane == 31) s_warp[warp] = x;
-            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                if (i < warp) before += s_warp[i];
-                all += s_warp[i];
-            }
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) before += s_warp[i];
+            all += s_warp[i];
         }
         if (b < p.B) {
             s_pre[b] = before + x - n;
             s_len[b] = len;
         }
         carry = all;
-        if (!few) __syncthreads();
+        if (b0 + kAttnThreads < p.B) __syncthreads();   // s_warp is written again
     }
-    if (lane == 0) s_pre[p.B] = carry;
-    if (few) __syncwarp();
-    else __syncthreads();
+    if (threadIdx.x == 0) s_pre[p.B] = carry;
+    __syncthreads();
     const int U = p.Hkv * p.n_rb;
     const Shares sh(carry * U, p);
     const int c = static_cast<int>(blockIdx.x);
@@ -491,18 +486,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NR>::kThreads, 1)
     // largest exactly.  They stay in registers, or (kQSmem) warp w prepares the 8
     // rows w and leaves them in shared memory as [row tile][word pair][lane], and
     // the factors behind them.
-    int b;   // the last sequence that starts at or before g0: not an empty one
-    if (few) {
-        const bool before = lane < p.B && s_pre[lane] * U <= g0;
-        b = 31 - __clz(__ballot_sync(0xffffffffu, before));
-    } else {
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pre[mid] * U <= g0) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
+    int b = 0;   // the last sequence that starts at or before g0: not an empty one
+    for (int hi = p.B - 1; b < hi;) {
+        const int mid = (b + hi + 1) >> 1;
+        if (s_pre[mid] * U <= g0) b = mid;
+        else hi = mid - 1;
     }
     const int n_first = s_pre[b + 1] - s_pre[b];
     int u = static_cast<int>(static_cast<unsigned>(g0 - s_pre[b] * U) / static_cast<unsigned>(n_first));
@@ -1166,7 +1154,7 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnPara
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, AttnCfg<D, NR>::smem_bytes(kMaxBatch));
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, p.ctas, AttnCfg<D, NR>::kThreads, smem, stream, tmK, tmV, p);
+    e = launch_dependent(kern, p.ctas, kAttnThreads, smem, stream, tmK, tmV, p);
     if (e != cudaSuccess) return e;
     const int rows = 8 * NR < p.rows ? 8 * NR : p.rows;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.Hkv * p.n_rb *
@@ -1344,7 +1332,7 @@ int check_kv8_attn(int B, int Hq, int Hkv, int Nq, int D) {
     if (B > kMaxBatch) return ATTN_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
     const int64_t units = static_cast<int64_t>(B) * Hkv * ((rows + 31) / 32);
-    if (rows > (1 << 30) || units > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (rows > (1 << 30) || units > (1 << 27)) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 }  // namespace
@@ -1377,8 +1365,8 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     if (!aligned(ptrs, 16) || !aligned(words, 4)) return ATTN_ERR_ALIGN;
     if (workspace_bytes < kv8_attn_workspace_size(B, Hq, Hkv, Nq, D)) return ATTN_ERR_WORKSPACE;
     // the kernels count tiles of all sequences' table capacity in 32 bits
-    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Hq / Hkv) * Nq + 31) / 32 + 1) *
-            ((static_cast<int64_t>(max_pages) * page + 31) / 32 + 1) > 0x7fffffffll)
+    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Hq / Hkv) * Nq + 31) / 32) *
+            ((static_cast<int64_t>(max_pages) * page + 31) / 32) > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
     AttnParams p{};
     rc = device_setup_public(&p.status);

@@ -22,10 +22,12 @@ constexpr int kWarps = kThreads / 32;
 // free ids and a few numbers per sequence, and each step costs a round trip of the
 // memory those are in: they live in shared memory up to this many bytes (2 ints a
 // page, 5 a sequence, reassign's rows beside them when they fit, too), in the
-// workspace past it.  reassign of 64 sequences over 2049 pages: @SH us against @WS us.
+// workspace past it.  A fork of 64 sequences over 2049 pages, its copies included:
+// 11.7 us against 14.5; of 96 over 19201 pages: 18.9 against 31.8.
 constexpr size_t kSharedBytes = 200 * 1024;
 // Table entries that compact's planning CTA renumbers itself; more take a second
-// kernel.
+// kernel (2304 entries 7.2 us against 8.3, 16K 19.1 against 19.5, 64K 91.7 against
+// 89.1).
 constexpr int64_t kRemapEntries = 16 * 1024;
 
 struct PageParams {
@@ -103,38 +105,68 @@ __device__ __forceinline__ bool in_pool(const PageParams& p, int id) {
     return id >= 0 && id < p.n_pages;
 }
 
+// Calls f(i, refs[i]) for every page, 8 loads of a thread in flight.
+template <typename F>
+__device__ __forceinline__ void for_pages(const PageParams& p, const int* refs, F&& f) {
+    for (int i0 = 0; i0 < p.n_pages; i0 += 8 * kThreads) {
+        int r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads + static_cast<int>(threadIdx.x);
+            r[k] = i < p.n_pages ? __ldcg(refs + i) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads + static_cast<int>(threadIdx.x);
+            if (i < p.n_pages) f(i, r[k]);
+        }
+    }
+}
+
 // Loads the counts; returns how many pages are free (after a barrier).
 template <bool SHARED>
 __device__ int load_counts(const PageParams& p, const Scratch<SHARED>& m, const int* refs) {
     int free = 0;
-    for (int i = threadIdx.x; i < p.n_pages; i += kThreads) {
-        const int r = refs[i];
+    for_pages(p, refs, [&](int i, int r) {
         m.count[i] = r;
         free += r == 0;
-    }
+    });
     int total;
     block_scan(free, &total);
     return total;
 }
 
-// Lists the free ids in order; returns how many there are.  4 pages a thread and step.
+// Writes the counts back.
 template <bool SHARED>
-__device__ int list_free(const PageParams& p, const Scratch<SHARED>& m) {
+__device__ void store_counts(const PageParams& p, const Scratch<SHARED>& m) {
+    if constexpr (SHARED) {
+        for (int i = threadIdx.x; i < p.n_pages; i += kThreads) p.refs[i] = m.count[i];
+    } else {
+        for_pages(p, m.count, [&](int i, int r) { p.refs[i] = r; });
+    }
+}
+
+// Lists the lowest `want` free ids in order; returns how many there are in all.  16
+// pages a thread and step (4 in shared memory, whose pools are smaller).
+template <bool SHARED>
+__device__ int list_free(const PageParams& p, const Scratch<SHARED>& m, int want) {
+    constexpr int K = SHARED ? 4 : 16;
     int n = 0;
-    for (int i0 = 0; i0 < p.n_pages; i0 += 4 * kThreads) {
-        const int i = i0 + 4 * static_cast<int>(threadIdx.x);
-        bool free[4];
-        int mine = 0;
+    for (int i0 = 0; i0 < p.n_pages; i0 += K * kThreads) {
+        const int i = i0 + K * static_cast<int>(threadIdx.x);
+        int r[K], mine = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            free[k] = i + k < p.n_pages && m.get(m.count + i + k) == 0;
-            mine += free[k];
-        }
+        for (int k = 0; k < K; ++k) r[k] = i + k < p.n_pages ? m.get(m.count + i + k) : 1;
+#pragma unroll
+        for (int k = 0; k < K; ++k) mine += r[k] == 0;
         int total;
         int at = n + block_scan(mine, &total);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (free[k]) m.ids[at++] = i + k;
+        for (int k = 0; k < K; ++k)
+            if (r[k] == 0) {
+                if (at < want) m.ids[at] = i + k;
+                ++at;
+            }
         n += total;
     }
     __syncthreads();
@@ -185,15 +217,23 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
         const int first = m.len[c] - p.window + 1;   // first position a new query sees
         return min(first > 0 ? first / p.page : 0, p.max_pages);
     };
-    if (p.window > 0) {
-        for (int c = warp; c < p.n_seqs; c += kWarps) {
-            const int* row = p.table + static_cast<int64_t>(c) * p.max_pages;
-            for (int j = j0 + lane; j < past(c); j += 32)
-                if (in_pool(p, row[j])) atomicSub(m.count + row[j], 1);
+    // Calls f(column, page) for those still held, from the newest down to the first
+    // 32 columns that an earlier call has dealt with.
+    auto leave = [&](int c, auto&& f) {
+        const int* row = p.table + static_cast<int64_t>(c) * p.max_pages;
+        for (int j1 = past(c); j1 > j0; j1 -= 32) {
+            const int j = j1 - 32 + lane;
+            const int id = j >= j0 ? row[j] : -1;
+            if (in_pool(p, id)) f(j, id);
+            if (__any_sync(0xffffffffu, !in_pool(p, id))) break;
         }
+    };
+    if (p.window > 0) {
+        for (int c = warp; c < p.n_seqs; c += kWarps)
+            leave(c, [&](int, int id) { atomicSub(m.count + id, 1); });
         __syncthreads();
     }
-    const int free = list_free(p, m);
+    const int free = list_free(p, m, need);
     const bool done = s_bad == 0 && need <= free;
     if (tid == 0) {
         p.info[0] = done;
@@ -205,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
     if (!done) return;
     for (int c = warp; c < p.n_seqs; c += kWarps) {
         int* row = p.table + static_cast<int64_t>(c) * p.max_pages;
-        for (int j = j0 + lane; j < past(c); j += 32) row[j] = -1;
+        leave(c, [&](int j, int) { row[j] = -1; });
         const int len = m.len[c], n = m.arg[c];
         if (n > 0) {
             const int first = ceil_div(len, p.page), want = ceil_div(len + n, p.page) - first;
@@ -218,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = m.get(m.count + i);
+    store_counts(p, m);
 }
 
 template <bool SHARED>
@@ -287,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
         }
     }
     __syncthreads();
-    const int free = list_free(p, m);
+    const int free = list_free(p, m, n_copy);
     const bool done = n_copy <= free;
     if (tid == 0) {
         p.info[0] = done;
@@ -317,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reassign_kernel(const PageParams
         if (lane == 0) p.lens[c] = q >= 0 ? m.len[q] : 0;
     }
     __syncthreads();
-    for (int i = tid; i < p.n_pages; i += kThreads) p.refs[i] = m.get(m.count + i);
+    store_counts(p, m);
 }
 
 // New ids of the held pages (ids: -1 not held, the page itself, or the free id it
@@ -328,11 +368,10 @@ __global__ void __launch_bounds__(kThreads) kvp_compact_kernel(const PageParams 
     const Scratch<SHARED> m(p);
     const int tid = threadIdx.x;
     int held = 0;
-    for (int i = tid; i < p.n_pages; i += kThreads) {
-        const int r = p.refs_in[i];
+    for_pages(p, p.refs_in, [&](int i, int r) {
         m.count[i] = r;
         held += r > 0;
-    }
+    });
     int total;
     block_scan(held, &total);
     held = total;
