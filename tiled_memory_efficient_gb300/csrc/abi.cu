@@ -1102,6 +1102,10 @@ extern "C" int attn_bwd_window(const void* q, const void* k, const void* v, cons
     p.causal_off = Nk - Nq;
     p.kv_div = p.G;
     p.n_sink_tiles = w.sink_tiles;
+    p.n_units = static_cast<int>(groups * (w.sink_tiles * static_cast<int64_t>(w.splits[0]) +
+                                           (w.n_ktiles - w.sink_tiles) * w.splits[1]));
+    p.ctas = device_sms();
+    if (p.ctas <= 0) return ATTN_ERR_CUDA;
     char* part = static_cast<char*>(workspace) + window_stats_bytes(w, B, Hq);
     for (int r = 0; r < 2; ++r) {
         const size_t bytes = window_range_bytes(w, r, B, Hkv, D);

@@ -292,47 +292,69 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     uint64_t* p_full = s_full + 2;     // [2] P^T_u and dS^T_u in TMEM (128 arrivals)
     uint64_t* acc_full = p_full + 2;   // last dV / dK product done
     uint64_t* mma_done = acc_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    uint64_t* kv_empty = mma_done + 1;  // WIN: K and V of the unit read for the last time
+    uint64_t* acc_empty = kv_empty + 1; // WIN: its dV and dK read (512 arrivals)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Heaviest first: under the causal mask low key tiles meet the most queries.
     // CTA (group, key tile kt, query range sp): consecutive CTAs share a key
     // tile; range sp takes query tiles [qi0, qi1).
-    // With a window the sink tiles' CTAs come first, then the others'.
-    const int n_sink_ctas = WIN ? p.n_groups * p.n_sink_tiles * p.wr[0].splits : 0;
-    const int region = WIN && static_cast<int>(blockIdx.x) >= n_sink_ctas ? 1 : 0;
-    const int kv_splits = WIN ? p.wr[region].splits : p.kv_splits;
-    const int cta = static_cast<int>(blockIdx.x) - (region ? n_sink_ctas : 0);
-    const int unit = cta / kv_splits;
-    const int sp = cta % kv_splits;
-    const int region_tiles = !WIN ? p.n_ktiles : region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
-    const int group = unit / region_tiles;
-    const int kt = unit % region_tiles + (region ? p.n_sink_tiles : 0);
-    const int key0 = kt * kRows;
+    // With a window the sink tiles' units come first, then the others', and a CTA
+    // takes every gridDim.x-th of them: its lists are short (a window's query
+    // tiles), so set-up, first loads and epilogue would be a quarter of a CTA's
+    // time if each unit had its own; here they run under the next unit's
+    // loads and first products.
+    int region = 0, kv_splits = 1, sp = 0, group = 0, kt = 0, key0 = 0;
     int qi0 = 0, qi1 = 0;          // list entries [qi0, qi1)
     int qa = 0, q_cnt = 1;         // WIN: first query tile, tiles per head
     int head_0 = 0, pos_0 = 0;     // head and position of the first row of entry qi0
-    if constexpr (WIN) {
-        // positions of a head that see some key of the tile
-        const int i_min = max(0, key0 - p.causal_off);
-        int64_t i_max = p.Nq - 1;
-        if (key0 >= p.sinks)
-            i_max = min(i_max, static_cast<int64_t>(key0) + kRows - 2 + p.window - p.causal_off);
-        qa = i_min / kRows;
-        q_cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
-        const int64_t total = static_cast<int64_t>(p.G) * q_cnt;
-        qi0 = static_cast<int>(total * sp / kv_splits);
-        qi1 = static_cast<int>(total * (sp + 1) / kv_splits);
-        head_0 = q_cnt > 0 ? qi0 / q_cnt : 0;
-        pos_0 = q_cnt > 0 ? (qa + qi0 % q_cnt) * kRows : 0;
-    } else {
-        qi0 = sp * p.qtiles_per_split;
-        qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
-        const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
-        head_0 = static_cast<int>(r0 / p.Nq);
-        pos_0 = static_cast<int>(r0 % p.Nq);
-    }
+    auto set_unit = [&](int idx) {
+        const int n_sink = WIN ? p.n_groups * p.n_sink_tiles * p.wr[0].splits : 0;
+        region = WIN && idx >= n_sink ? 1 : 0;
+        kv_splits = WIN ? p.wr[region].splits : p.kv_splits;
+        const int cta = idx - (region ? n_sink : 0);
+        const int unit = cta / kv_splits;
+        sp = cta % kv_splits;
+        const int tiles = !WIN ? p.n_ktiles : region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
+        group = unit / tiles;
+        kt = unit % tiles + (region ? p.n_sink_tiles : 0);
+        key0 = kt * kRows;
+        if constexpr (WIN) {
+            // positions of a head that see some key of the tile
+            const int i_min = max(0, key0 - p.causal_off);
+            int64_t i_max = p.Nq - 1;
+            if (key0 >= p.sinks)
+                i_max = min(i_max, static_cast<int64_t>(key0) + kRows - 2 + p.window - p.causal_off);
+            qa = i_min / kRows;
+            q_cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
+            const int64_t total = static_cast<int64_t>(p.G) * q_cnt;
+            qi0 = static_cast<int>(total * sp / kv_splits);
+            qi1 = static_cast<int>(total * (sp + 1) / kv_splits);
+            head_0 = q_cnt > 0 ? qi0 / q_cnt : 0;
+            pos_0 = q_cnt > 0 ? (qa + qi0 % q_cnt) * kRows : 0;
+        } else {
+            qi0 = sp * p.qtiles_per_split;
+            qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
+            const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
+            head_0 = static_cast<int>(r0 / p.Nq);
+            pos_0 = static_cast<int>(r0 % p.Nq);
+        }
+    };
+    if constexpr (!WIN) set_unit(static_cast<int>(blockIdx.x));
+    // Every role runs body(k) for the CTA's k-th unit.
+    auto for_units = [&](auto&& body) {
+        if constexpr (WIN) {
+            int k = 0;
+            for (int idx = static_cast<int>(blockIdx.x); idx < p.n_units; idx += static_cast<int>(gridDim.x), ++k) {
+                set_unit(idx);
+                body(k);
+            }
+        } else {
+            body(0);
+        }
+    };
     // head and position of the next entry's first row
     auto next_entry = [&](int& pos, int& head) {
         if constexpr (WIN) {
@@ -371,6 +393,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         }
         mbar_init(acc_full, 1);
         mbar_init(mma_done, 1);
+        mbar_init(kv_empty, 1);
+        mbar_init(acc_empty, 512);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -385,12 +409,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (lane == 0) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmDO);
+            int n = 0, units = 0;   // tiles and K/V pairs loaded
+            bool okp = true;
+            for_units([&](int k) {
+            if (WIN && okp && k > 0) okp = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status);
+            if (!okp) return;
             mbar_arrive_expect_tx(kv_full, 2 * TB);
             for (int kb = 0; kb < KB; ++kb) {
                 tma_load_3d(&tmK, kv_full, sK + kb * (kRows * 128), kb * 64, key0, group);
                 tma_load_3d(&tmV, kv_full, sV + kb * (kRows * 128), kb * 64, key0, group);
             }
-            int n = 0;
+            ++units;
             int head = head_0;
             for (int qi = qi0, pos = pos_0; qi < qi1; ++qi) {
                 if (!visit(qi, pos)) {
@@ -403,7 +432,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 if constexpr (WIN) next_entry(pos, head);
                 else pos = next_tile_pos(pos, p.Nq);
                 const int slot = n % QS;
-                if (!mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status)) break;
+                okp = mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status);
+                if (!okp) break;
                 mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
@@ -416,7 +446,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
                 ++n;
             }
-            mbar_wait_bounded(kv_full, 0, p.status);
+            });
+            mbar_wait_bounded(kv_full, (units - 1) & 1, p.status);
             for (int m = (n > QS ? n - QS : 0); m < n; ++m)
                 mbar_wait_bounded(&q_full[m % QS], (m / QS) & 1, p.status);
         }
@@ -448,6 +479,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                            idesc_s, kb > 0 ? 1u : 0u);
             mma_commit_elect(&s_full[u]);
         };
+        int nb = 0;   // tiles of the units before
+        for_units([&](int k) {
         int n_vis = 0;   // query tiles this key tile meets (the producer loads them in order)
         if constexpr (WIN) {
             n_vis = qi1 - qi0;
@@ -455,20 +488,26 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq))
                 n_vis += visit(qi, pos) ? 1 : 0;
         }
-        warp_wait(kv_full, 0, abort_flag, p.status);
+        warp_wait(kv_full, k & 1, abort_flag, p.status);
         if (n_vis > 0) {
-            warp_wait(&q_full[0], 0, abort_flag, p.status);
+            warp_wait(&q_full[nb % QS], (nb / QS) & 1, abort_flag, p.status);
             tc_fence_after();
-            issue_sdp(0, 0);
-            issue_sdp(0, 1);
+            issue_sdp(nb % QS, 0);
+            issue_sdp(nb % QS, 1);
         }
+        if (WIN && n_vis <= 1) mma_commit_elect(kv_empty);
+        // (a unit without tiles waits, too, so that no phase of acc_empty is skipped)
+        if (WIN && n_vis == 0 && k > 0) warp_wait(acc_empty, (k - 1) & 1, abort_flag, p.status);
         // A wait that times out sets the abort flag and later waits return at
         // once, so the loop runs to its end without blocking.
         for (int n = 0; n < n_vis; ++n) {
-            const int slot = n % QS, nslot = (n + 1) % QS;
+            const int slot = (nb + n) % QS, nslot = (nb + n + 1) % QS;
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                warp_wait(&p_full[u], n & 1, abort_flag, p.status);
+                warp_wait(&p_full[u], (nb + n) & 1, abort_flag, p.status);
+                // the first products overwrite the accumulators of the unit before
+                if (WIN && k > 0 && n == 0 && u == 0)
+                    warp_wait(acc_empty, (k - 1) & 1, abort_flag, p.status);
                 tc_fence_after();
                 const uint32_t acc = (n > 0 || u > 0) ? 1u : 0u;
                 // dV += P^T_u dO_u, dK += dS^T_u Q_u (K = the 64 queries of half u)
@@ -483,14 +522,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 if (u == 1) mma_commit_elect(&q_empty[slot]);
                 if (n + 1 < n_vis) {
                     if (u == 0) {
-                        warp_wait(&q_full[nslot], ((n + 1) / QS) & 1, abort_flag, p.status);
+                        warp_wait(&q_full[nslot], ((nb + n + 1) / QS) & 1, abort_flag, p.status);
                         tc_fence_after();
                     }
                     issue_sdp(nslot, u);
+                    if (WIN && u == 1 && n + 2 == n_vis) mma_commit_elect(kv_empty);
                 }
             }
         }
         mma_commit_elect(acc_full);
+        nb += n_vis;
+        });
         mma_commit_elect(mma_done);
         mbar_wait_bounded(mma_done, 0, p.status);
     } else {
@@ -498,16 +540,18 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         // 32(w%4) .. 32(w%4)+31, query half hq = (w/4)%2, chunk cc = w/8 of it.
         const int quad = warp & 3, hq = (warp >> 2) & 1, cc = warp >> 3;
         const int c = 2 * hq + cc;   // 32-query chunk of the tile
-        const int key = key0 + quad * 32 + lane;
         const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + lb + 128 * hq + 32 * cc, tDP = tS + 64;
         const float sl2 = p.scale_log2;
         // scale still to apply to the scores read below: an additive bias
         // leaves natural-log logits (log2 e), a boolean one raw scores
         const float sc = (MASK && p.mask_kind == 2) ? kLog2e : sl2;
+        int n = 0;   // tiles of all units so far
+        for_units([&](int k) {
+        const int key = key0 + quad * 32 + lane;
         const int64_t b_off = MASK ? static_cast<int64_t>(group / p.Hkv) * p.msb : 0;
         const int head0 = MASK ? (group % p.Hkv) * p.G : 0;
-        int n = 0;
+        const int n_before = n;
         int head = head_0;   // head within the group of the current tile's first row
         for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, next_entry(pos, head)) {
             if (!visit(qi, pos)) continue;
@@ -553,15 +597,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             bool fast = (row0 + q_first + 32 <= p.rows_per_group) && (wkey_last < p.Nk);
             // WIN: key position of the chunk's first query, the last sees 31 more
             const int kq_first = base + q_first + p.causal_off;
-            // A block behind every window: its queries all see the same keys, the
-            // sinks among them (live: this thread's key is one, or the block is
-            // an ordinary one).
+            // A block ahead of its queries or behind every window takes the unmasked
+            // path: no query sees its keys but, behind, the sinks among them (live:
+            // this thread's key counts).
             bool live = true;
             if (WIN) {
+                const bool ahead = wkey_last - 31 > kq_first + 31;
                 const bool past = wkey_last <= kq_first - p.window;
-                live = !past || key < p.sinks;
-                fast = fast && (past || !window_edge(wkey_last - 31, wkey_last, kq_first,
-                                                     kq_first + 31, p.window, p.sinks));
+                live = !ahead && (!past || key < p.sinks);
+                fast = fast && (ahead || past ||
+                                !window_edge(wkey_last - 31, wkey_last, kq_first, kq_first + 31,
+                                             p.window, p.sinks));
             } else if (CAUSAL)
                 fast = fast && (base + q_first + 32 <= p.Nq) && (wkey_last <= base + q_first);
             const uint64_t sl22 = f2(sc, sc);
@@ -634,13 +680,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int64_t grow = static_cast<int64_t>(group) * p.Nk + key;
         uint16_t* dvp = static_cast<uint16_t*>(p.dv) + grow * D + col0;
         uint16_t* dkp = static_cast<uint16_t*>(p.dk) + grow * D + col0;
-        if (n > 0) warp_wait(acc_full, 0, abort_flag, p.status);
+        if (WIN || n > n_before) warp_wait(acc_full, k & 1, abort_flag, p.status);
         tc_fence_after();
         // dV first, then dK, so only one accumulator chunk is live at a time.
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             uint32_t a[CW];
-            if (n > 0) {
+            if (n > n_before) {
                 const uint32_t src = tmem + lb + 256 + which * D + col0;
                 if constexpr (CW == 32) tmem_ld32(src, a);
                 else tmem_ld16(src, a);
@@ -679,6 +725,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                     dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
         }
+        if constexpr (WIN) {
+            tc_fence_before();
+            mbar_arrive(acc_empty);
+        }
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -1232,11 +1283,7 @@ cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
     constexpr int kv_bytes = dkdv_smem<D>();
     e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
     if (e != cudaSuccess) return e;
-    const long long ctas =
-        static_cast<long long>(p.n_groups) *
-        (static_cast<long long>(p.n_sink_tiles) * p.wr[0].splits +
-         static_cast<long long>(p.n_ktiles - p.n_sink_tiles) * p.wr[1].splits);
-    e = launch_dependent(kv, ctas, kKvThreads, kv_bytes, stream, tmQ, tmDO, tmK, tmV, p);
+    e = launch_dependent(kv, p.n_units < p.ctas ? p.n_units : p.ctas, kKvThreads, kv_bytes, stream, tmQ, tmDO, tmK, tmV, p);
     if (e != cudaSuccess) return e;
     int64_t n8[2];
     for (int r = 0; r < 2; ++r)

@@ -178,6 +178,8 @@ struct BwdParams {
         float* dv_part;
         float* dk_part;
     } wr[2];
+    int n_units;   // dK/dV: (key tile, query range) units of all groups
+    int ctas;      // CTAs of both persistent grids, at most (SMs of the device)
 };
 
 // Workspace bytes of the backward without the split of dK/dV (the per-row
