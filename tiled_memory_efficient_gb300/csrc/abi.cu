@@ -997,7 +997,7 @@ WindowBwdPlan window_bwd_plan(int B, int Hq, int Hkv, int Nq, int Nk, int window
         int64_t want = (G * w.n_qtiles + target - 1) / target;
         const int64_t most = (4LL * sms + groups * w.sink_tiles - 1) / (groups * w.sink_tiles);
         if (want > most) want = most;
-        return want > 256 ? int64_t{256} : want;
+        return want > 255 ? int64_t{255} : want;
     };
     int64_t best = 0;
     for (int64_t s = 1; s <= 32 && (s == 1 || per / s >= kWindowMinTiles); ++s) {

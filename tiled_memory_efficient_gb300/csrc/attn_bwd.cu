@@ -329,9 +329,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 i_max = min(i_max, static_cast<int64_t>(key0) + kRows - 2 + p.window - p.causal_off);
             qa = i_min / kRows;
             q_cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
-            const int64_t total = static_cast<int64_t>(p.G) * q_cnt;
-            qi0 = static_cast<int>(total * sp / kv_splits);
-            qi1 = static_cast<int>(total * (sp + 1) / kv_splits);
+            // 32 bits hold it: at most 2^31 / 128 tiles, 255 ranges
+            const unsigned total = static_cast<unsigned>(p.G) * q_cnt, ns = kv_splits;
+            qi0 = static_cast<int>(total * sp / ns);
+            qi1 = static_cast<int>(total * (sp + 1) / ns);
             head_0 = q_cnt > 0 ? qi0 / q_cnt : 0;
             pos_0 = q_cnt > 0 ? (qa + qi0 % q_cnt) * kRows : 0;
         } else {
@@ -1021,7 +1022,7 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         const int hq = warp >> 2, quad = warp & 3;   // column group, TMEM lane quadrant
         const int64_t row = row0 + quad * 32 + lane;
         const bool row_ok = row < p.rows_per_group;
-        const int pos = static_cast<int>(row % p.Nq);
+        const int pos = static_cast<int>(WIN ? row : row % p.Nq);   // WIN: one head per group
         const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + lb, tDP = tmem + lb + 128;
         const float sl2 = p.scale_log2;
@@ -1036,8 +1037,10 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         // which are never stored, so they need none.
         const int64_t wr0 = row0 + quad * 32;
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
-        const int warp_min_pos = (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
-        const int warp_max_pos = static_cast<int>(wr1 % p.Nq);   // WIN: one head per group
+        const int warp_min_pos = WIN ? static_cast<int>(wr0)
+                                 : (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq)
+                                                              : 0;
+        const int warp_max_pos = static_cast<int>(wr1);   // (WIN)
         // scale still to apply to the scores read below: an additive bias
         // leaves natural-log logits (log2 e), a boolean one raw scores
         const float sc = (MASK && p.mask_kind == 2) ? kLog2e : sl2;

@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     }
     int group, pair;
     int only = -1;   // >= 0: the one Q tile of the pair this CTA runs
+    // WIN with one query head per group: rows are positions, so that no 64-bit
+    // division stands before the CTA's first loads
+    const bool one_head = WIN && p.rows_per_group == p.Nq;
     if (WIN) {
         // Units of equal work but for the first positions of a head (shorter
         // lists): those last.  Consecutive CTAs share most of their key tiles.
@@ -347,17 +350,26 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     const int tps = split >= 0 ? p.tiles_per_split : 0x7fffffff - kt0;
     KeyList kl;
     if constexpr (WIN) {
-        const int64_t last = min(row_base + 2 * kRows, p.rows_per_group) - 1;
-        // a pair that spans heads holds position 0
-        const int64_t min_pos = row_base / p.Nq == last / p.Nq ? row_base % p.Nq : 0;
+        int64_t min_pos = row_base;
+        if (!one_head) {
+            const int64_t last = min(row_base + 2 * kRows, p.rows_per_group) - 1;
+            // a pair that spans heads holds position 0
+            min_pos = row_base / p.Nq == last / p.Nq ? row_base % p.Nq : 0;
+        }
         kl = key_list(min_pos + p.causal_off, p.window, p.sinks);
     }
+    // key tiles of the list that a Q tile needs
+    auto tiles_for = [&](int64_t row0) {
+        if (!one_head) return kv_tiles_for(row0, p, CAUSAL) - kl.skip;
+        const int r = static_cast<int>(row0), end = min(r + kRows, p.Nq);   // one past its last position
+        return r < p.Nq ? (min(end + p.causal_off, p.Nk) + kRows - 1) / kRows - kl.skip : 0;
+    };
     // key tile of this CTA's step j, and its K/V group (a window's units may be
     // query heads: FwdParams)
     auto ktile = [&](int j) { return WIN ? kl.tile(kt0 + j) : kt0 + j; };
     const int kv_group = WIN ? group / p.kv_div : group;
-    int n0 = tiles_in_range(kv_tiles_for(row_base, p, CAUSAL) - kl.skip, kt0, tps);
-    int n1 = tiles_in_range(kv_tiles_for(row_base + kRows, p, CAUSAL) - kl.skip, kt0, tps);
+    int n0 = tiles_in_range(tiles_for(row_base), kt0, tps);
+    int n1 = tiles_in_range(tiles_for(row_base + kRows), kt0, tps);
     if (only == 0) n1 = 0;
     if (only == 1) n0 = 0;
     int nmax = n0 > n1 ? n0 : n1;
@@ -638,13 +650,18 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         const int64_t row0 = row_base + t * kRows;
         const int64_t row = row0 + rl;
         const bool row_valid = row < p.rows_per_group;
-        const int pos = static_cast<int>(row % p.Nq);
+        const int pos = static_cast<int>(one_head ? row : row % p.Nq);
         const int64_t wr0 = row0 + quad * 32;
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
-        const int warp_min_pos =
-            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
-        const int warp_max_pos =   // for a window's lower edge
-            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
+        int warp_min_pos, warp_max_pos;   // the latter for a window's lower edge
+        if (one_head) {
+            warp_min_pos = static_cast<int>(wr0);
+            warp_max_pos = static_cast<int>(wr1);
+        } else {
+            const bool same = wr0 / p.Nq == wr1 / p.Nq;
+            warp_min_pos = same ? static_cast<int>(wr0 % p.Nq) : 0;
+            warp_max_pos = same ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
+        }
         // General bias (MK = 1): this row's bias row (query head hkv*G +
         // row/Nq of batch group/Hkv), staged one key tile ahead: this warp's
         // 32 rows x 64 keys, nvalid rows real.  A half-tile is staged when its
@@ -910,7 +927,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         const int64_t row0 = row_base + t * kRows;
         const int64_t row = row0 + quad * 32 + lane;
         const bool row_valid = row < p.rows_per_group;
-        const int pos = static_cast<int>(row % p.Nq);
+        const int pos = static_cast<int>(one_head ? row : row % p.Nq);
         // This row's bias: query head hkv*G + row/Nq of batch group/Hkv.
         const uint8_t* mrow = nullptr;
         if constexpr (MASK) {
@@ -923,10 +940,15 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
         // key tiles that reach past it (or past Nk).
         const int64_t wr0 = row0 + quad * 32;
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
-        const int warp_min_pos =
-            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
-        const int warp_max_pos =   // for a window's lower edge
-            (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
+        int warp_min_pos, warp_max_pos;   // the latter for a window's lower edge
+        if (one_head) {
+            warp_min_pos = static_cast<int>(wr0);
+            warp_max_pos = static_cast<int>(wr1);
+        } else {
+            const bool same = wr0 / p.Nq == wr1 / p.Nq;
+            warp_min_pos = same ? static_cast<int>(wr0 % p.Nq) : 0;
+            warp_max_pos = same ? static_cast<int>(wr1 % p.Nq) : p.Nq - 1;
+        }
         // Staged bias (kBiasSmem): this warp's 32 rows, nvalid of them real.
         // A key tile is staged when it lies inside [0, Nk) and the warp has a
         // real row; the ragged last tile reads its bias directly.

@@ -21,7 +21,7 @@ struct KeyList {
 __device__ __forceinline__ KeyList key_list(int64_t min_pos, int window, int sinks) {
     KeyList kl;
     const int64_t lo = min_pos - window + 1;   // first key inside a window
-    const int lo_tile = lo > 0 ? static_cast<int>(lo / 128) : 0;
+    const int lo_tile = lo > 0 ? static_cast<int>(static_cast<uint64_t>(lo) >> 7) : 0;
     kl.n_sink = min((sinks + 127) / 128, lo_tile);
     kl.skip = lo_tile - kl.n_sink;
     return kl;
