@@ -348,6 +348,8 @@ def _same(ref, table, lens, refs):
     (40, 6, 120, 64, 0, 0),
     (1, 1, 1, 128, 0, 0),
     (1100, 3, 2500, 32, 40, 1),     # more sequences and pages than threads of the planning CTA
+    (90, 200, 30000, 16, 400, 3),   # plans that outgrow shared memory, a table of two compaction CTAs
+    (700, 30, 9000, 16, 0, 0),
 ], ids=str)
 def test_bookkeeping_matches_lists(cuda_lib, n_seqs, max_pages, n_pages, page, window, sinks):
     """A random run of reserve, reassign and compact against Python lists; calls that
@@ -509,6 +511,36 @@ def test_a_decoding_run(cuda_lib, window, sinks, dtype):
     become([-1] * S)
     assert cache.refs.tolist() == [0] * 40 and cache.lens.tolist() == [0] * S
     assert bool((cache.table == -1).all())
+
+
+@pytest.mark.gpu
+def test_two_caches_on_two_streams(cuda_lib):
+    """Two decoding runs side by side give what each gives alone."""
+    g = torch.Generator().manual_seed(6)
+    data = [[[torch.randn(5, h, n, 64, generator=g).to(dt).cuda() for h in (2, 2, 8)] for n in (70, 1, 1, 2)]
+            for dt in (F16, BF16)]
+
+    def run(x, cache):
+        res = []
+        for k, v, q in x:
+            res += _step(cache, 1, [k], [v], [q[:, :, -2:].contiguous()], k.shape[2])[0]
+        cache.reassign(torch.tensor([1, 1, 0, -1, 4], dtype=torch.int32, device="cuda"))
+        cache.compact()
+        return res + [cache.table.clone(), cache.lens.clone(), cache.k_pages.view(torch.uint8)[:, :10].clone()]
+    make = lambda: PagedKVCache(1, 5, 2, 64, n_pages=60, page_size=16, max_pages=9)
+    want = [run(x, make()) for x in data]
+    caches = [make() for _ in data]
+    streams = [torch.cuda.Stream() for _ in data]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for s, x, c in zip(streams, data, caches):
+        with torch.cuda.stream(s):
+            got.append(run(x, c))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(t, u) for t, u in zip(a, b))
+    assert _lib.sync_status() == _lib.ATTN_OK
 
 
 @pytest.mark.gpu

@@ -113,6 +113,9 @@ CASES = [
     (1, 2, 2, 700, 700, 128, BF16, 333, 0),
     (2, 2, 1, 1, 1, 64, BF16, 1, 1),
     (1, 2, 2, 1100, 1100, 64, F16, 129, 129),
+    (4, 8, 8, 1000, 1000, 64, F16, 130, 4),         # more key tiles than CTAs: each takes several
+    (4, 8, 8, 300, 1500, 128, BF16, 200, 3),        # and most of them no query sees
+    (5, 8, 8, 700, 700, 128, F16, 700, 0),
 ]
 
 
@@ -215,6 +218,64 @@ def test_captured_and_replayed(cuda_lib):
     for a, b in zip(got, both()):
         assert torch.equal(a, b)
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("view", [False, True])
+def test_captured_backward_beside_an_older_graph(cuda_lib, view):
+    """Leaves that a graph outside the capture holds are refused, before anything of the
+    backward is launched, and captured once that graph is gone."""
+    x = inputs.make_custom(1, 2, 2, 200, 200, 64, F16, seed=30, with_grad=True)
+    leaves = [x[n].cuda().requires_grad_(True) for n in "qkv"]
+    do = x["do"].cuda()
+
+    def both():
+        q, k, v = (t[:, :] if view else t for t in leaves)
+        out = sdpa.window_attention(q, k, v, 40, 2)
+        return (out.detach(),) + torch.autograd.grad(out, leaves, do)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = both()
+    torch.cuda.current_stream().wait_stream(side)
+    older = sdpa.window_attention(*leaves, 40, 2)
+    with pytest.raises(RuntimeError, match="recorded outside the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            both()
+    del older
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    graph.replay()
+    for a, b in zip(held, want):
+        assert torch.equal(a, b)
+    assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(cuda_lib):
+    """Forward and backward of two problems side by side give what each gives alone."""
+    xs = [{n: t.cuda() for n, t in
+           inputs.make_custom(2, 8, 2, 900, 900, 64, dt, seed=s, with_grad=True).items()}
+          for s, dt in ((40, F16), (41, BF16))]
+
+    def both(x):
+        out, lse = _lib.attn_fwd_window(x["q"], x["k"], x["v"], 100, 3)
+        return (out, lse) + _lib.attn_bwd_window(x["q"], x["k"], x["v"], out, x["do"], lse, 100, 3)
+    want = [both(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = []
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(both(x))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(t, u) for t, u in zip(a, b))
 
 
 @pytest.mark.gpu

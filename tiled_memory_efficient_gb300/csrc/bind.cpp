@@ -13,9 +13,12 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <set>
+#include <vector>
 
 #include "../../include/attn.h"
 #include "../../include/kvcache.h"
@@ -415,6 +418,40 @@ PyObject* py_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// () -> ids of the streams, other than the current one, that the running backward pass
+// would hand gradients to from here on: those of the functions above the one being
+// evaluated that the pass will reach.  Called by that function's backward.
+PyObject* py_streams_above(PyObject*, PyObject* const*, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    using torch::autograd::Node;
+    std::set<int64_t> found;
+    std::set<const Node*> seen;
+    std::vector<std::shared_ptr<Node>> open;
+    if (auto node = torch::autograd::get_current_node()) open.push_back(std::move(node));
+    while (!open.empty()) {
+        const std::shared_ptr<Node> node = std::move(open.back());
+        open.pop_back();
+        for (uint32_t i = 0; i < node->num_outputs(); ++i) {
+            const auto& next = node->next_edge(i).function;
+            if (!next || !node->task_should_compute_output(i) || !seen.insert(next.get()).second)
+                continue;
+            if (const auto s = next->stream()) {
+                const int64_t here = c10::cuda::getCurrentCUDAStream(s->device_index()).id();
+                if (s->device_type() == at::kCUDA && s->id() != here) found.insert(s->id());
+            }
+            open.push_back(next);
+        }
+    }
+    PyObject* r = PyList_New(0);
+    for (const int64_t id : found) {
+        PyObject* x = r ? PyLong_FromLongLong(id) : nullptr;
+        if (!x || PyList_Append(r, x) != 0) Py_CLEAR(r);
+        Py_XDECREF(x);
+    }
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
 // (addresses of the C entry points, in Fns' order)
 PyObject* py_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* at[sizeof(Fns) / sizeof(void*)];
@@ -444,6 +481,7 @@ PyMethodDef methods[] = {METHOD("init", py_init),
                          METHOD("kvp_compact", py_compact),
                          METHOD("attn_fwd_window", py_fwd),
                          METHOD("attn_bwd_window", py_bwd),
+                         METHOD("streams_above", py_streams_above),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

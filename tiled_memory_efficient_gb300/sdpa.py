@@ -93,6 +93,8 @@ class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
+        if torch.cuda.is_current_stream_capturing():
+            _lib.check_captured_backward(dout.device)
         dq, dk, dv = _lib.attn_bwd_window(q, k, v, out, dout.contiguous(), lse, ctx.window,
                                           ctx.sinks, scale=ctx.scale)
         return dq, dk, dv, None, None, None
@@ -131,7 +133,11 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
     """Differentiable causal attention with a sliding window and sinks.  The Nq
     queries are the last Nq of the Nk positions; each sees the last `window`
     positions up to its own and the first `sinks` ones (Nq <= Nk, window >= 1,
-    sinks >= 0).  Layouts, dtypes and GQA as in ``attention``."""
+    sinks >= 0).  Layouts, dtypes and GQA as in ``attention``.
+
+    A backward pass captured into a CUDA graph raises while a graph recorded
+    outside the capture still holds the same leaves: drop that graph's outputs
+    first, or record it on the capturing stream."""
     _validate(q, k, v)
     if q.shape[2] > k.shape[2]:
         raise ValueError(f"{q.shape[2]} queries are more than the {k.shape[2]} positions")
