@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "bias.cuh"
@@ -264,10 +265,7 @@ struct BwdCfg {
 // its P^T / dS^T are in TMEM, then S^T / dP^T of half u of tile n+1 into the
 // same columns (the tensor pipe runs in order, so the products of tile n have
 // read them first).
-// WIN: the key tile meets query tiles [qa, qb] of each of its G heads (window and
-// sinks, BwdParams); entry it of that list is tile qa + it % (qb - qa + 1) of
-// head it / (qb - qa + 1).  Without it the list is the group's flattened tiles.
-template <int D, bool BF16, bool CAUSAL, bool MASK, bool WIN = false>
+template <int D, bool BF16, bool CAUSAL, bool MASK>
 __global__ void __launch_bounds__(kKvThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmDO,
@@ -292,82 +290,24 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     uint64_t* p_full = s_full + 2;     // [2] P^T_u and dS^T_u in TMEM (128 arrivals)
     uint64_t* acc_full = p_full + 2;   // last dV / dK product done
     uint64_t* mma_done = acc_full + 1;
-    uint64_t* kv_empty = mma_done + 1;  // WIN: K and V of the unit read for the last time
-    uint64_t* acc_empty = kv_empty + 1; // WIN: its dV and dK read (512 arrivals)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Heaviest first: under the causal mask low key tiles meet the most queries.
     // CTA (group, key tile kt, query range sp): consecutive CTAs share a key
     // tile; range sp takes query tiles [qi0, qi1).
-    // With a window the sink tiles' units come first, then the others', and a CTA
-    // takes every gridDim.x-th of them: its lists are short (a window's query
-    // tiles), so set-up, first loads and epilogue would be a quarter of a CTA's
-    // time if each unit had its own; here they run under the next unit's
-    // loads and first products.
-    int region = 0, kv_splits = 1, sp = 0, group = 0, kt = 0, key0 = 0;
-    int qi0 = 0, qi1 = 0;          // list entries [qi0, qi1)
-    int qa = 0, q_cnt = 1;         // WIN: first query tile, tiles per head
-    int head_0 = 0, pos_0 = 0;     // head and position of the first row of entry qi0
-    auto set_unit = [&](int idx) {
-        const int n_sink = WIN ? p.n_groups * p.n_sink_tiles * p.wr[0].splits : 0;
-        region = WIN && idx >= n_sink ? 1 : 0;
-        kv_splits = WIN ? p.wr[region].splits : p.kv_splits;
-        const int cta = idx - (region ? n_sink : 0);
-        const int unit = cta / kv_splits;
-        sp = cta % kv_splits;
-        const int tiles = !WIN ? p.n_ktiles : region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
-        group = unit / tiles;
-        kt = unit % tiles + (region ? p.n_sink_tiles : 0);
-        key0 = kt * kRows;
-        if constexpr (WIN) {
-            // positions of a head that see some key of the tile
-            const int i_min = max(0, key0 - p.causal_off);
-            int64_t i_max = p.Nq - 1;
-            if (key0 >= p.sinks)
-                i_max = min(i_max, static_cast<int64_t>(key0) + kRows - 2 + p.window - p.causal_off);
-            qa = i_min / kRows;
-            q_cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
-            // 32 bits hold it: at most 2^31 / 128 tiles, 255 ranges
-            const unsigned total = static_cast<unsigned>(p.G) * q_cnt, ns = kv_splits;
-            qi0 = static_cast<int>(total * sp / ns);
-            qi1 = static_cast<int>(total * (sp + 1) / ns);
-            head_0 = q_cnt > 0 ? qi0 / q_cnt : 0;
-            pos_0 = q_cnt > 0 ? (qa + qi0 % q_cnt) * kRows : 0;
-        } else {
-            qi0 = sp * p.qtiles_per_split;
-            qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
-            const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
-            head_0 = static_cast<int>(r0 / p.Nq);
-            pos_0 = static_cast<int>(r0 % p.Nq);
-        }
-    };
-    if constexpr (!WIN) set_unit(static_cast<int>(blockIdx.x));
-    // Every role runs body(k) for the CTA's k-th unit.
-    auto for_units = [&](auto&& body) {
-        if constexpr (WIN) {
-            int k = 0;
-            for (int idx = static_cast<int>(blockIdx.x); idx < p.n_units; idx += static_cast<int>(gridDim.x), ++k) {
-                set_unit(idx);
-                body(k);
-            }
-        } else {
-            body(0);
-        }
-    };
-    // head and position of the next entry's first row
-    auto next_entry = [&](int& pos, int& head) {
-        if constexpr (WIN) {
-            pos += kRows;
-            if (pos >= (qa + q_cnt) * kRows) {
-                pos = qa * kRows;
-                ++head;
-            }
-        } else {
-            next_tile(pos, head, p.Nq);
-        }
-    };
+    const int unit = static_cast<int>(blockIdx.x / p.kv_splits);
+    const int sp = static_cast<int>(blockIdx.x % p.kv_splits);
+    const int group = unit / p.n_ktiles;
+    const int kt = unit % p.n_ktiles;
+    const int key0 = kt * kRows;
+    const int qi0 = sp * p.qtiles_per_split;
+    const int qi1 = min(p.n_qtiles, qi0 + p.qtiles_per_split);
+    // head (within the group) and position of the first row of query tile qi0
+    const int64_t r0 = static_cast<int64_t>(qi0) * kRows;
+    const int head_0 = static_cast<int>(r0 / p.Nq);
+    const int pos_0 = static_cast<int>(r0 % p.Nq);
     // Query tile qi (first-row position pos) meets this key tile.
     // A boolean mask that depends on the key alone (one row of keep bytes per
     // KV group, as a padding mask is) may remove every key of this tile: then
@@ -382,7 +322,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
     bool any_kept = true;   // set after the set-up barrier
     auto visit = [&](int qi, int pos) {
-        return any_kept && (WIN || !CAUSAL || tile_max_pos_at(qi, pos, p) >= key0);
+        return any_kept && (!CAUSAL || tile_max_pos_at(qi, pos, p) >= key0);
     };
 
     if (threadIdx.x == 0) {
@@ -394,8 +334,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         }
         mbar_init(acc_full, 1);
         mbar_init(mma_done, 1);
-        mbar_init(kv_empty, 1);
-        mbar_init(acc_empty, 512);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -410,45 +348,29 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (lane == 0) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmDO);
-            int n = 0, units = 0;   // tiles and K/V pairs loaded
-            bool okp = true;
-            for_units([&](int k) {
-            if (WIN && okp && k > 0) okp = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status);
-            if (!okp) return;
             mbar_arrive_expect_tx(kv_full, 2 * TB);
             for (int kb = 0; kb < KB; ++kb) {
                 tma_load_3d(&tmK, kv_full, sK + kb * (kRows * 128), kb * 64, key0, group);
                 tma_load_3d(&tmV, kv_full, sV + kb * (kRows * 128), kb * 64, key0, group);
             }
-            ++units;
-            int head = head_0;
-            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi) {
-                if (!visit(qi, pos)) {
-                    pos = next_tile_pos(pos, p.Nq);
-                    continue;
-                }
-                // first row of the tile within its group (WIN: its head) and that group
-                const int row0 = WIN ? pos : qi * kRows;
-                const int q_group = WIN ? group * p.G + head : group;
-                if constexpr (WIN) next_entry(pos, head);
-                else pos = next_tile_pos(pos, p.Nq);
+            int n = 0;
+            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq)) {
+                if (!visit(qi, pos)) continue;
                 const int slot = n % QS;
-                okp = mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status);
-                if (!okp) break;
+                if (!mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status)) break;
                 mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
                 for (int kb = 0; kb < KB; ++kb) {
                     tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
-                                row0, q_group);
+                                qi * kRows, group);
                     tma_load_3d(&tmDO, &q_full[slot], sDO + slot * TB + kb * (kRows * 128),
-                                kb * 64, row0, q_group);
+                                kb * 64, qi * kRows, group);
                 }
-                const int64_t w0 = static_cast<int64_t>(q_group) * p.rows_pad + row0;
+                const int64_t w0 = static_cast<int64_t>(group) * p.rows_pad + qi * kRows;
                 bulk_load(sL + slot * kRows, p.nlse2 + w0, kRows * 4, &q_full[slot]);
                 bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
                 ++n;
             }
-            });
-            mbar_wait_bounded(kv_full, (units - 1) & 1, p.status);
+            mbar_wait_bounded(kv_full, 0, p.status);
             for (int m = (n > QS ? n - QS : 0); m < n; ++m)
                 mbar_wait_bounded(&q_full[m % QS], (m / QS) & 1, p.status);
         }
@@ -480,35 +402,23 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                            idesc_s, kb > 0 ? 1u : 0u);
             mma_commit_elect(&s_full[u]);
         };
-        int nb = 0;   // tiles of the units before
-        for_units([&](int k) {
         int n_vis = 0;   // query tiles this key tile meets (the producer loads them in order)
-        if constexpr (WIN) {
-            n_vis = qi1 - qi0;
-        } else {
-            for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq))
-                n_vis += visit(qi, pos) ? 1 : 0;
-        }
-        warp_wait(kv_full, k & 1, abort_flag, p.status);
+        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, pos = next_tile_pos(pos, p.Nq))
+            n_vis += visit(qi, pos) ? 1 : 0;
+        warp_wait(kv_full, 0, abort_flag, p.status);
         if (n_vis > 0) {
-            warp_wait(&q_full[nb % QS], (nb / QS) & 1, abort_flag, p.status);
+            warp_wait(&q_full[0], 0, abort_flag, p.status);
             tc_fence_after();
-            issue_sdp(nb % QS, 0);
-            issue_sdp(nb % QS, 1);
+            issue_sdp(0, 0);
+            issue_sdp(0, 1);
         }
-        if (WIN && n_vis <= 1) mma_commit_elect(kv_empty);
-        // (a unit without tiles waits, too, so that no phase of acc_empty is skipped)
-        if (WIN && n_vis == 0 && k > 0) warp_wait(acc_empty, (k - 1) & 1, abort_flag, p.status);
         // A wait that times out sets the abort flag and later waits return at
         // once, so the loop runs to its end without blocking.
         for (int n = 0; n < n_vis; ++n) {
-            const int slot = (nb + n) % QS, nslot = (nb + n + 1) % QS;
+            const int slot = n % QS, nslot = (n + 1) % QS;
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                warp_wait(&p_full[u], (nb + n) & 1, abort_flag, p.status);
-                // the first products overwrite the accumulators of the unit before
-                if (WIN && k > 0 && n == 0 && u == 0)
-                    warp_wait(acc_empty, (k - 1) & 1, abort_flag, p.status);
+                warp_wait(&p_full[u], n & 1, abort_flag, p.status);
                 tc_fence_after();
                 const uint32_t acc = (n > 0 || u > 0) ? 1u : 0u;
                 // dV += P^T_u dO_u, dK += dS^T_u Q_u (K = the 64 queries of half u)
@@ -523,17 +433,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 if (u == 1) mma_commit_elect(&q_empty[slot]);
                 if (n + 1 < n_vis) {
                     if (u == 0) {
-                        warp_wait(&q_full[nslot], ((nb + n + 1) / QS) & 1, abort_flag, p.status);
+                        warp_wait(&q_full[nslot], ((n + 1) / QS) & 1, abort_flag, p.status);
                         tc_fence_after();
                     }
                     issue_sdp(nslot, u);
-                    if (WIN && u == 1 && n + 2 == n_vis) mma_commit_elect(kv_empty);
                 }
             }
         }
         mma_commit_elect(acc_full);
-        nb += n_vis;
-        });
         mma_commit_elect(mma_done);
         mbar_wait_bounded(mma_done, 0, p.status);
     } else {
@@ -541,20 +448,18 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         // 32(w%4) .. 32(w%4)+31, query half hq = (w/4)%2, chunk cc = w/8 of it.
         const int quad = warp & 3, hq = (warp >> 2) & 1, cc = warp >> 3;
         const int c = 2 * hq + cc;   // 32-query chunk of the tile
+        const int key = key0 + quad * 32 + lane;
         const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + lb + 128 * hq + 32 * cc, tDP = tS + 64;
         const float sl2 = p.scale_log2;
         // scale still to apply to the scores read below: an additive bias
         // leaves natural-log logits (log2 e), a boolean one raw scores
         const float sc = (MASK && p.mask_kind == 2) ? kLog2e : sl2;
-        int n = 0;   // tiles of all units so far
-        for_units([&](int k) {
-        const int key = key0 + quad * 32 + lane;
         const int64_t b_off = MASK ? static_cast<int64_t>(group / p.Hkv) * p.msb : 0;
         const int head0 = MASK ? (group % p.Hkv) * p.G : 0;
-        const int n_before = n;
+        int n = 0;
         int head = head_0;   // head within the group of the current tile's first row
-        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, next_entry(pos, head)) {
+        for (int qi = qi0, pos = pos_0; qi < qi1; ++qi, next_tile(pos, head, p.Nq)) {
             if (!visit(qi, pos)) continue;
             const int slot = n % QS;
             // This chunk's bias column, requested before the waits for the
@@ -586,7 +491,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             uint32_t sv[32], dp[32];
             tmem_ld32(tS, sv);
             tmem_ld32(tDP, dp);
-            const int64_t row0 = WIN ? pos : static_cast<int64_t>(qi) * kRows;
+            const int64_t row0 = static_cast<int64_t>(qi) * kRows;
             const int base = pos;
             const float* L = sL + slot * kRows + c * 32;
             const float* Dl = sDl + slot * kRows + c * 32;
@@ -596,20 +501,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             const int wkey_last = key0 + quad * 32 + 31;
             const int q_first = c * 32;
             bool fast = (row0 + q_first + 32 <= p.rows_per_group) && (wkey_last < p.Nk);
-            // WIN: key position of the chunk's first query, the last sees 31 more
-            const int kq_first = base + q_first + p.causal_off;
-            // A block ahead of its queries or behind every window takes the unmasked
-            // path: no query sees its keys but, behind, the sinks among them (live:
-            // this thread's key counts).
-            bool live = true;
-            if (WIN) {
-                const bool ahead = wkey_last - 31 > kq_first + 31;
-                const bool past = wkey_last <= kq_first - p.window;
-                live = !ahead && (!past || key < p.sinks);
-                fast = fast && (ahead || past ||
-                                !window_edge(wkey_last - 31, wkey_last, kq_first, kq_first + 31,
-                                             p.window, p.sinks));
-            } else if (CAUSAL)
+            if (CAUSAL)
                 fast = fast && (base + q_first + 32 <= p.Nq) && (wkey_last <= base + q_first);
             const uint64_t sl22 = f2(sc, sc);
             tmem_wait_ld();
@@ -627,11 +519,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                         const int e = i + 2 * h;
                         const uint64_t x = ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
                                                  sl22, h ? f2(l4.z, l4.w) : f2(l4.x, l4.y));
-                        float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
-                        if constexpr (WIN) {
-                            p0 = live ? p0 : 0.0f;
-                            p1 = live ? p1 : 0.0f;
-                        }
+                        const float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
                         const uint64_t dd = fmul2(
                             f2(p0, p1),
                             fadd2(f2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
@@ -649,12 +537,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                     for (int u = 0; u < 2; ++u) {
                         const int q = q_first + i + u;
                         bool ok = (row0 + q < p.rows_per_group) && (key < p.Nk);
-                        if (WIN) {
-                            const int kq = base + q + p.causal_off;   // key position of the query
-                            ok = ok && window_sees(key, kq + 1, kq - p.window, p.sinks);
-                        } else if (CAUSAL) {
-                            ok = ok && key <= tile_pos(base, q, p.Nq);
-                        }
+                        if (CAUSAL) ok = ok && key <= tile_pos(base, q, p.Nq);
                         const float pr = ex2_ftz(fmaf(__uint_as_float(sv[i + u]), sc, L[i + u]));
                         pp[u] = ok ? pr : 0.0f;
                         dd[u] = ok ? pr * (__uint_as_float(dp[i + u]) + Dl[i + u]) : 0.0f;
@@ -681,13 +564,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int64_t grow = static_cast<int64_t>(group) * p.Nk + key;
         uint16_t* dvp = static_cast<uint16_t*>(p.dv) + grow * D + col0;
         uint16_t* dkp = static_cast<uint16_t*>(p.dk) + grow * D + col0;
-        if (WIN || n > n_before) warp_wait(acc_full, k & 1, abort_flag, p.status);
+        if (n > 0) warp_wait(acc_full, 0, abort_flag, p.status);
         tc_fence_after();
         // dV first, then dK, so only one accumulator chunk is live at a time.
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             uint32_t a[CW];
-            if (n > n_before) {
+            if (n > 0) {
                 const uint32_t src = tmem + lb + 256 + which * D + col0;
                 if constexpr (CW == 32) tmem_ld32(src, a);
                 else tmem_ld16(src, a);
@@ -697,18 +580,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
                 for (int i = 0; i < CW; ++i) a[i] = 0u;
             }
-            if (ok && key < p.Nk && kv_splits > 1) {
+            if (ok && key < p.Nk && p.kv_splits > 1) {
                 // this query range's fp32 partial sum (dK unscaled)
-                float* dst;
-                if constexpr (WIN) {
-                    const BwdParams::WindowRanges& w = p.wr[region];
-                    dst = (which ? w.dk_part : w.dv_part) +
-                          ((static_cast<int64_t>(sp) * p.n_groups + group) * w.keys + key - w.key0) * D +
-                          col0;
-                } else {
-                    dst = (which ? p.dk_part : p.dv_part) +
-                          (static_cast<int64_t>(sp) * p.n_groups * p.Nk + grow) * D + col0;
-                }
+                float* dst = (which ? p.dk_part : p.dv_part) +
+                             (static_cast<int64_t>(sp) * p.n_groups * p.Nk + grow) * D + col0;
 #pragma unroll
                 for (int i = 0; i < CW / 4; ++i)
                     reinterpret_cast<float4*>(dst)[i] =
@@ -726,11 +601,432 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                     dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
         }
-        if constexpr (WIN) {
-            tc_fence_before();
-            mbar_arrive(acc_empty);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kKvMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    // Launched as a programmatic dependent of the dQ kernel (whose results it
+    // does not read): it does not end before dQ has, so whatever follows in the
+    // stream sees both.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- dK/dV, sliding window
+// The same products and TMEM layout as bwd_dkdv_kernel.  What differs is that a key
+// tile meets a window's query tiles only (9 of each head at a window of 1024), so
+// whatever a CTA does once per key tile counts: with one CTA per key tile or, in turn,
+// one key tile after the other, the gap between two cost as much as 3 of those 9
+// tiles.  Here a CTA takes units (key tile, query range) in turn and its three roles
+// run through them without a break:
+//   - the MMA warp issues the first S^T, dP^T of the next unit before the last dV, dK of
+//     this one, as it does between two tiles of one unit;
+//   - the elementwise warps work on the next unit's first tile before they write this
+//     one's dV, dK, which the tensor core finishes meanwhile;
+//   - the producer works out the units (divisions) and leaves them in shared memory.
+// A query range meets each of its key's visible queries as one run, so a thread's mask
+// of a 32-query chunk is an interval of bits; chunks that all 32 keys of a warp see
+// take the path without a mask.
+struct WindowUnit {
+    int n;            // query tiles
+    int pos, head;    // the first one: its first row within its head, the head within the group
+    int qa, q_end;    // rows where a head's run of tiles starts and ends
+    int key0, group;
+    int region, sp;   // query range sp of BwdParams::wr[region]
+};
+constexpr int kUnitSlots = 4;   // a unit is read until its dV, dK are written, two units on
+
+__device__ __forceinline__ WindowUnit window_unit(const BwdParams& p, int idx) {
+    WindowUnit w;
+    const int n_sink = p.n_groups * p.n_sink_tiles * p.wr[0].splits;   // sink tiles' units first
+    w.region = idx >= n_sink ? 1 : 0;
+    const unsigned splits = p.wr[w.region].splits;
+    const unsigned at = idx - (w.region ? n_sink : 0);
+    const unsigned tiles = w.region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
+    const unsigned unit = at / splits;
+    w.sp = static_cast<int>(at % splits);
+    w.group = static_cast<int>(unit / tiles);
+    w.key0 = static_cast<int>(unit % tiles + (w.region ? p.n_sink_tiles : 0)) * kRows;
+    // positions of a head that see some key of the tile
+    const int i_min = max(0, w.key0 - p.causal_off);
+    int64_t i_max = p.Nq - 1;
+    if (w.key0 >= p.sinks)
+        i_max = min(i_max, static_cast<int64_t>(w.key0) + kRows - 2 + p.window - p.causal_off);
+    const int qa = i_min / kRows;
+    const int cnt = i_max >= i_min ? static_cast<int>(i_max) / kRows - qa + 1 : 0;
+    // 32 bits hold it: at most 2^31 / 128 tiles, 255 ranges
+    const unsigned total = static_cast<unsigned>(p.G) * cnt, sp = w.sp;
+    const int i0 = static_cast<int>(total * sp / splits);
+    w.n = static_cast<int>(total * (sp + 1) / splits) - i0;
+    w.head = cnt > 0 ? i0 / cnt : 0;
+    w.qa = qa * kRows;
+    w.q_end = (qa + cnt) * kRows;
+    w.pos = cnt > 0 ? w.qa + i0 % cnt * kRows : 0;
+    return w;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kKvThreads, 1)
+    bwd_window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmDO,
+                           const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+    using C = BwdCfg<D>;
+    constexpr int TB = C::kTileBytes, KB = C::kKB, QS = 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sK = smem;
+    uint8_t* sV = sK + TB;
+    uint8_t* sQ = sV + TB;             // [QS]
+    uint8_t* sDO = sQ + QS * TB;       // [QS]
+    float* sL = reinterpret_cast<float*>(sDO + QS * TB);  // [QS][128] -lse2 of the query tile
+    float* sDl = sL + QS * kRows;                          // [QS][128] -delta
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sDl + QS * kRows);
+    uint64_t* kv_full = bars;          // a unit's numbers, K and V
+    uint64_t* kv_empty = kv_full + 1;  // its numbers read (16 warps), K and V read for the last time
+    uint64_t* q_full = kv_empty + 1;   // [QS]
+    uint64_t* q_empty = q_full + QS;   // [QS]
+    uint64_t* s_full = q_empty + QS;   // [2] S^T_u and dP^T_u in TMEM
+    uint64_t* p_full = s_full + 2;     // [2] P^T_u and dS^T_u in TMEM (256 arrivals)
+    uint64_t* acc_full = p_full + 2;   // a unit's last dV / dK product done
+    uint64_t* acc_empty = acc_full + 1;   // its dV and dK read (512 arrivals)
+    uint64_t* mma_done = acc_empty + 1;
+    WindowUnit* units = reinterpret_cast<WindowUnit*>(mma_done + 1);   // [kUnitSlots]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + kUnitSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_units = (p.n_units - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    if (threadIdx.x == 0) {
+        mbar_init(kv_full, 1);
+        mbar_init(kv_empty, 1 + 16);
+        for (int i = 0; i < QS; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&s_full[u], 1);
+            mbar_init(&p_full[u], 256);
         }
-        });
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 512);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kKvMmaWarp) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == kKvProducerWarp) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmDO);
+            int n = 0, done = 0;   // tiles and units handed on
+            bool ok = true;
+            for (int k = 0; k < n_units && ok; ++k) {
+                const WindowUnit w = window_unit(p, static_cast<int>(blockIdx.x + k * gridDim.x));
+                if (k > 0) ok = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status);
+                if (!ok) break;
+                units[k % kUnitSlots] = w;
+                if (w.n > 0) {
+                    mbar_arrive_expect_tx(kv_full, 2 * TB);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        tma_load_3d(&tmK, kv_full, sK + kb * (kRows * 128), kb * 64, w.key0, w.group);
+                        tma_load_3d(&tmV, kv_full, sV + kb * (kRows * 128), kb * 64, w.key0, w.group);
+                    }
+                } else {
+                    mbar_arrive(kv_full);
+                }
+                ++done;
+                int pos = w.pos, q_group = w.group * p.G + w.head;
+                for (int i = 0; i < w.n; ++i) {
+                    const int slot = n % QS;
+                    ok = mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
+                                    pos, q_group);
+                        tma_load_3d(&tmDO, &q_full[slot], sDO + slot * TB + kb * (kRows * 128),
+                                    kb * 64, pos, q_group);
+                    }
+                    const int64_t w0 = static_cast<int64_t>(q_group) * p.rows_pad + pos;
+                    bulk_load(sL + slot * kRows, p.nlse2 + w0, kRows * 4, &q_full[slot]);
+                    bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
+                    ++n;
+                    pos += kRows;
+                    if (pos >= w.q_end) {
+                        pos = w.qa;
+                        ++q_group;
+                    }
+                }
+            }
+            if (done > 0) mbar_wait_bounded(kv_full, (done - 1) & 1, p.status);
+            for (int m = (n > QS ? n - QS : 0); m < n; ++m)
+                mbar_wait_bounded(&q_full[m % QS], (m / QS) & 1, p.status);
+        }
+    } else if (warp == kKvMmaWarp) {
+        constexpr uint32_t idesc_s = idesc_f16(kRows, 64, BF16, false);  // 128 keys x 64 queries
+        constexpr uint32_t idesc_g = idesc_f16(kRows, D, BF16, true);
+        constexpr uint64_t kStep = TB >> 4;
+        constexpr uint64_t kBlk = (kRows * 128) >> 4;
+        constexpr uint64_t kHalf = (64 * 128) >> 4;   // 64 rows of a tile (bwd_dkdv_kernel)
+        const uint64_t dK_ = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dV_ = smem_desc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dQk = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dDOk = smem_desc_sw128(smem_u32(sDO), 16, 1024);
+        const uint64_t dQm = smem_desc_sw128(smem_u32(sQ), kRows * 128, 1024);
+        const uint64_t dDOm = smem_desc_sw128(smem_u32(sDO), kRows * 128, 1024);
+        // S^T_u = K Q_u^T and dP^T_u = V dO_u^T of the tile in `slot`.
+        auto issue_sdp = [&](int slot, int u) {
+            const uint32_t d = tmem + 128 * u;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                mma_ss_k64(d, dK_ + kb * kBlk, dQk + slot * kStep + kb * kBlk + u * kHalf, idesc_s,
+                           kb > 0 ? 1u : 0u);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                mma_ss_k64(d + 64, dV_ + kb * kBlk, dDOk + slot * kStep + kb * kBlk + u * kHalf,
+                           idesc_s, kb > 0 ? 1u : 0u);
+            mma_commit_elect(&s_full[u]);
+        };
+        // Tiles of unit k once its K and V are there: 0 past the last unit, -1 after
+        // a wait that gave up.
+        auto tiles_of = [&](int k) {
+            if (k >= n_units) return 0;
+            if (!warp_wait(kv_full, k & 1, abort_flag, p.status)) return -1;
+            return *static_cast<const volatile int*>(&units[k % kUnitSlots].n);
+        };
+        int m = 0, full = 0;   // tiles, and units with tiles, so far
+        bool primed = false;   // the unit's first S^T, dP^T are issued
+        int nv = tiles_of(0);
+        // (a wait that gives up sets the abort flag, later waits return at once and
+        // the loops end without blocking)
+        for (int k = 0; k < n_units && nv >= 0;) {
+            if (nv == 0) {
+                mma_commit_elect(kv_empty);
+                nv = tiles_of(++k);
+                continue;
+            }
+            if (!primed) {
+                warp_wait(&q_full[m % QS], (m / QS) & 1, abort_flag, p.status);
+                tc_fence_after();
+                issue_sdp(m % QS, 0);
+                issue_sdp(m % QS, 1);
+                if (nv == 1) mma_commit_elect(kv_empty);
+            }
+            int nx = 0;   // tiles of the next unit
+            for (int n = 0; n < nv; ++n, ++m) {
+                const bool last = n + 1 == nv;
+                if (last) nx = tiles_of(k + 1);
+                const bool more = !last || nx > 0;
+                const int slot = m % QS, nslot = (m + 1) % QS;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    warp_wait(&p_full[u], m & 1, abort_flag, p.status);
+                    // the first products overwrite the accumulators of the unit before
+                    if (n == 0 && u == 0 && full > 0)
+                        warp_wait(acc_empty, (full - 1) & 1, abort_flag, p.status);
+                    tc_fence_after();
+                    const uint32_t acc = (n > 0 || u > 0) ? 1u : 0u;
+                    // dV += P^T_u dO_u, dK += dS^T_u Q_u (K = the 64 queries of half u)
+                    const uint32_t pu = tmem + 128 * u;
+                    mma_ts_k64_split(tmem + 256, pu, pu + 32, dDOm + slot * kStep + u * kHalf, idesc_g,
+                                     acc);
+                    if constexpr (BF16)   // dV += (low-order part of P^T_u) dO_u
+                        mma_ts_k64_split(tmem + 256, pu + 16, pu + 48, dDOm + slot * kStep + u * kHalf,
+                                         idesc_g, 1u);
+                    mma_ts_k64_split(tmem + 256 + D, pu + 64, pu + 96, dQm + slot * kStep + u * kHalf,
+                                     idesc_g, acc);
+                    if (u == 1) {
+                        mma_commit_elect(&q_empty[slot]);
+                        if (last) mma_commit_elect(acc_full);
+                    }
+                    if (more) {
+                        if (u == 0) {
+                            warp_wait(&q_full[nslot], ((m + 1) / QS) & 1, abort_flag, p.status);
+                            tc_fence_after();
+                        }
+                        issue_sdp(nslot, u);
+                        if (u == 1 && (last ? nx == 1 : n + 2 == nv)) mma_commit_elect(kv_empty);
+                    }
+                }
+            }
+            ++full;
+            ++k;
+            primed = nx > 0;
+            nv = nx;
+        }
+        mma_commit_elect(mma_done);
+        mbar_wait_bounded(mma_done, 0, p.status);
+    } else {
+        // One thread per key row and 32-query chunk, as in bwd_dkdv_kernel.
+        const int quad = warp & 3, hq = (warp >> 2) & 1, cc = warp >> 3;
+        const int c = 2 * hq + cc;   // 32-query chunk of the tile
+        const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tS = tmem + lb + 128 * hq + 32 * cc, tDP = tS + 64;
+        const uint64_t sl22 = f2(p.scale_log2, p.scale_log2);
+
+        // dV and scale * dK of this thread's key row, D/4 columns per warp.
+        int full = 0;   // units with tiles so far
+        auto write_unit = [&](const WindowUnit& w) {
+            constexpr int CW = D / 4;   // 32 (D = 128) or 16 (D = 64)
+            const int col0 = (hq + 2 * cc) * CW;
+            const int key = w.key0 + quad * 32 + lane;
+            const bool any = w.n > 0;
+            if (any) {
+                warp_wait(acc_full, full & 1, abort_flag, p.status);
+                ++full;
+            }
+            tc_fence_after();
+            const bool ok = *abort_flag == 0;
+            const BwdParams::WindowRanges& wr = p.wr[w.region];
+            const int64_t grow = static_cast<int64_t>(w.group) * p.Nk + key;
+            // dV first, then dK, so only one accumulator chunk is live at a time.
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                uint32_t a[CW];
+                if (any) {
+                    const uint32_t src = tmem + lb + 256 + which * D + col0;
+                    if constexpr (CW == 32) tmem_ld32(src, a);
+                    else tmem_ld16(src, a);
+                    tmem_wait_ld();
+                    reg_fence(a);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < CW; ++i) a[i] = 0u;
+                }
+                if (ok && key < p.Nk && wr.splits > 1) {
+                    // this query range's fp32 partial sum (dK unscaled)
+                    float* dst = (which ? wr.dk_part : wr.dv_part) +
+                                 ((static_cast<int64_t>(w.sp) * p.n_groups + w.group) * wr.keys + key -
+                                  wr.key0) * D + col0;
+#pragma unroll
+                    for (int i = 0; i < CW / 4; ++i)
+                        reinterpret_cast<float4*>(dst)[i] =
+                            make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+                                        __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]));
+                } else if (ok && key < p.Nk) {
+                    const float sc = which ? p.scale : 1.0f;
+                    uint32_t x[CW / 2];
+#pragma unroll
+                    for (int i = 0; i < CW / 2; ++i)
+                        x[i] = pack2<BF16>(__uint_as_float(a[2 * i]) * sc, __uint_as_float(a[2 * i + 1]) * sc);
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(which ? p.dk : p.dv) +
+                                                          grow * D + col0);
+#pragma unroll
+                    for (int i = 0; i < CW / 8; ++i)
+                        dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                mbar_arrive(acc_empty);
+            }
+        };
+
+        int n = 0;   // tiles so far
+        for (int k = 0; k <= n_units; ++k) {   // (the last turn only writes)
+            int tiles = 0, pos = 0, qa = 0, q_end = 0, key0 = 0;
+            if (k < n_units) {
+                if (!warp_wait(kv_full, k & 1, abort_flag, p.status)) break;
+                const WindowUnit& w = units[k % kUnitSlots];
+                tiles = w.n;
+                pos = w.pos;
+                qa = w.qa;
+                q_end = w.q_end;
+                key0 = w.key0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv_empty);
+            }
+            const int key = key0 + quad * 32 + lane;
+            int i = 0;
+            do {
+                if (i < tiles) {
+                    const int slot = n % QS;
+                    warp_wait(&q_full[slot], (n / QS) & 1, abort_flag, p.status);
+                    // Bit j: query j of the chunk sees this thread's key.  It does from the
+                    // key's own position on, to the window's end or, for a sink, for good.
+                    const int to_key = key - (pos + c * 32 + p.causal_off);   // query at the key
+                    const int end = min(key < p.sinks ? 32 : to_key + p.window, p.Nq - pos - c * 32);
+                    uint32_t vis = to_key >= 32 || end <= 0 || key >= p.Nk ? 0u : 0xffffffffu;
+                    if (to_key > 0) vis &= 0xffffffffu << (to_key & 31);
+                    if (end < 32) vis &= ~(0xffffffffu << (end & 31));
+                    if (end <= 0 || to_key >= 32) vis = 0u;
+                    const bool all = __all_sync(0xffffffffu, vis == 0xffffffffu);
+                    const bool none = __all_sync(0xffffffffu, vis == 0u);
+                    const float* L = sL + slot * kRows + c * 32;
+                    const float* Dl = sDl + slot * kRows + c * 32;
+                    warp_wait(&s_full[hq], n & 1, abort_flag, p.status);
+                    tc_fence_after();
+                    uint32_t sv[32], dp[32];
+                    tmem_ld32(tS, sv);
+                    tmem_ld32(tDP, dp);
+                    tmem_wait_ld();
+                    reg_fence(sv);
+                    reg_fence(dp);
+                    // The packed P^T / dS^T of this chunk go to the first 16 of its own
+                    // 32 columns, which are already read into registers (bf16: the
+                    // low-order parts of P^T to the other 16).
+                    auto math = [&](auto masked) {
+                        constexpr bool M = decltype(masked)::value;
+                        uint32_t pw[16], dw[16];
+                        uint32_t plw[BF16 ? 16 : 1];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 l4 = *reinterpret_cast<const float4*>(L + j);
+                            const float4 d4 = *reinterpret_cast<const float4*>(Dl + j);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int e = j + 2 * h;
+                                const uint64_t x =
+                                    ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl22,
+                                          h ? f2(l4.z, l4.w) : f2(l4.x, l4.y));
+                                float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
+                                const uint64_t dd = fmul2(
+                                    f2(p0, p1),
+                                    fadd2(f2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                          h ? f2(d4.z, d4.w) : f2(d4.x, d4.y)));
+                                float d0 = f2lo(dd), d1 = f2hi(dd);
+                                if constexpr (M) {
+                                    const bool s0 = (vis >> e) & 1u, s1 = (vis >> (e + 1)) & 1u;
+                                    p0 = s0 ? p0 : 0.0f;
+                                    p1 = s1 ? p1 : 0.0f;
+                                    d0 = s0 ? d0 : 0.0f;
+                                    d1 = s1 ? d1 : 0.0f;
+                                }
+                                pw[e >> 1] = pack2<BF16>(p0, p1);
+                                dw[e >> 1] = pack2<BF16>(d0, d1);
+                                if constexpr (BF16) plw[e >> 1] = bf16x2_residual(p0, p1, pw[e >> 1]);
+                            }
+                        }
+                        tmem_st16(tS, pw);
+                        tmem_st16(tDP, dw);
+                        if constexpr (BF16) tmem_st16(tS + 16, plw);
+                    };
+                    if (all) {
+                        math(std::false_type{});
+                    } else if (!none) {
+                        math(std::true_type{});
+                    } else {
+                        const uint32_t zero[16] = {};
+                        tmem_st16(tS, zero);
+                        tmem_st16(tDP, zero);
+                        if constexpr (BF16) tmem_st16(tS + 16, zero);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[hq]);
+                    ++n;
+                    pos += kRows;
+                    if (pos >= q_end) pos = qa;
+                }
+                if (i == 0 && k > 0) write_unit(units[(k - 1) % kUnitSlots]);
+            } while (++i < tiles);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1282,8 +1578,8 @@ cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
     e = launch_dependent(dq, static_cast<long long>(p.n_groups) * p.G * p.n_qtiles,
                          dq_threads<3, D>(), dq_bytes, stream, tmQ, tmDO, tmK, tmV, p);
     if (e != cudaSuccess) return e;
-    auto kv = bwd_dkdv_kernel<D, BF16, true, false, true>;
-    constexpr int kv_bytes = dkdv_smem<D>();
+    auto kv = bwd_window_dkdv_kernel<D, BF16>;
+    constexpr int kv_bytes = dkdv_smem<D>() + kUnitSlots * static_cast<int>(sizeof(WindowUnit));
     e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kv, p.n_units < p.ctas ? p.n_units : p.ctas, kKvThreads, kv_bytes, stream, tmQ, tmDO, tmK, tmV, p);
