@@ -151,6 +151,24 @@ int make_byte_map_public(CUtensorMap* map, const void* base, int D, int rows, in
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
+// 3-D map over a [groups][rows][D] 16-bit tensor for stores of 32 rows x D/4 columns from
+// dense rows of shared memory, swizzled over a row's 16-byte pieces.
+int make_patch_map_public(CUtensorMap* map, const void* base, bool bf16, int D, int64_t rows,
+                          int64_t groups) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                   static_cast<cuuint64_t>(rows) * D * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D / 4), 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                3, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
 int make_map_public(CUtensorMap* map, const void* base, bool bf16, int cols, int64_t rows,
                     int64_t groups) {
     return make_map(map, base, bf16, cols, rows, groups);

@@ -31,6 +31,11 @@
 #include "window.cuh"
 
 namespace tme {
+
+// abi.cu
+int make_patch_map_public(CUtensorMap* map, const void* base, bool bf16, int D, int64_t rows,
+                          int64_t groups);
+
 namespace {
 
 constexpr int kRows = 128;
@@ -621,11 +626,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 // one key tile after the other, the gap between two cost as much as 3 of those 9
 // tiles.  Here a CTA takes units (key tile, query range) in turn and its three roles
 // run through them without a break:
-//   - the MMA warp issues the first S^T, dP^T of the next unit before the last dV, dK of
-//     this one, as it does between two tiles of one unit;
+//   - the producer works out the units (divisions) and leaves them in shared memory; it
+//     asks the next unit's K and V into the second-level cache and loads its first
+//     query tile before this unit's K and V have been read for the last time;
 //   - the elementwise warps work on the next unit's first tile before they write this
-//     one's dV, dK, which the tensor core finishes meanwhile;
-//   - the producer works out the units (divisions) and leaves them in shared memory.
+//     one's dV, dK, which the tensor core finishes meanwhile; they give the
+//     accumulators back once those are in registers, and the tensor memory
+//     accelerator stores them (a row a thread, stored by the threads, met a line a
+//     lane: 5000 cycles for what takes 1000 now).
 // A query range meets each of its key's visible queries as one run, so a thread's mask
 // of a 32-query chunk is an interval of bits; chunks that all 32 keys of a warp see
 // take the path without a mask.
@@ -672,17 +680,20 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     bwd_window_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmDO,
                            const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+                           const __grid_constant__ CUtensorMap tmV,
+                           const __grid_constant__ CUtensorMap tmDK,
+                           const __grid_constant__ CUtensorMap tmDV, const BwdParams p) {
     using C = BwdCfg<D>;
     constexpr int TB = C::kTileBytes, KB = C::kKB, QS = 2;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* sK = smem;
+    constexpr int CW = D / 4;          // columns of dV, dK a warp writes: 32 (D = 128) or 16
+    constexpr int kPatch = 32 * CW * 2;
+    extern __shared__ __align__(1024) uint8_t smem_w[];
+    uint8_t* sK = smem_w;
     uint8_t* sV = sK + TB;
     uint8_t* sQ = sV + TB;             // [QS]
     uint8_t* sDO = sQ + QS * TB;       // [QS]
-    float* sL = reinterpret_cast<float*>(sDO + QS * TB);  // [QS][128] -lse2 of the query tile
+    uint8_t* sOut = sDO + QS * TB;     // [16 warps] 32 rows x CW columns, 16-bit
+    float* sL = reinterpret_cast<float*>(sOut + 16 * kPatch);  // [QS][128] -lse2 of the query tile
     float* sDl = sL + QS * kRows;                          // [QS][128] -delta
     uint64_t* bars = reinterpret_cast<uint64_t*>(sDl + QS * kRows);
     uint64_t* kv_full = bars;          // a unit's numbers, K and V
@@ -726,9 +737,27 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             tma_prefetch_desc(&tmDO);
             int n = 0, done = 0;   // tiles and units handed on
             bool ok = true;
-            for (int k = 0; k < n_units && ok; ++k) {
-                const WindowUnit w = window_unit(p, static_cast<int>(blockIdx.x + k * gridDim.x));
-                if (k > 0) ok = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status);
+            auto load_q = [&](int pos, int q_group) {
+                const int slot = n % QS;
+                ok = mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
+                                pos, q_group);
+                    tma_load_3d(&tmDO, &q_full[slot], sDO + slot * TB + kb * (kRows * 128),
+                                kb * 64, pos, q_group);
+                }
+                const int64_t w0 = static_cast<int64_t>(q_group) * p.rows_pad + pos;
+                bulk_load(sL + slot * kRows, p.nlse2 + w0, kRows * 4, &q_full[slot]);
+                bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
+                ++n;
+            };
+            WindowUnit w = window_unit(p, static_cast<int>(blockIdx.x));
+            for (int k = 0; k < n_units; ++k) {
+                int pos = w.pos, q_group = w.group * p.G + w.head;
+                if (w.n > 0) load_q(pos, q_group);
+                if (ok && k > 0) ok = mbar_wait(kv_empty, (k - 1) & 1, abort_flag, p.status);
                 if (!ok) break;
                 units[k % kUnitSlots] = w;
                 if (w.n > 0) {
@@ -741,28 +770,21 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                     mbar_arrive(kv_full);
                 }
                 ++done;
-                int pos = w.pos, q_group = w.group * p.G + w.head;
-                for (int i = 0; i < w.n; ++i) {
-                    const int slot = n % QS;
-                    ok = mbar_wait(&q_empty[slot], ((n / QS) & 1) ^ 1, abort_flag, p.status);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&q_full[slot], 2 * TB + 2 * kRows * 4);
-                    for (int kb = 0; kb < KB; ++kb) {
-                        tma_load_3d(&tmQ, &q_full[slot], sQ + slot * TB + kb * (kRows * 128), kb * 64,
-                                    pos, q_group);
-                        tma_load_3d(&tmDO, &q_full[slot], sDO + slot * TB + kb * (kRows * 128),
-                                    kb * 64, pos, q_group);
-                    }
-                    const int64_t w0 = static_cast<int64_t>(q_group) * p.rows_pad + pos;
-                    bulk_load(sL + slot * kRows, p.nlse2 + w0, kRows * 4, &q_full[slot]);
-                    bulk_load(sDl + slot * kRows, p.ndelta + w0, kRows * 4, &q_full[slot]);
-                    ++n;
+                for (int i = 1; i < w.n && ok; ++i) {
                     pos += kRows;
                     if (pos >= w.q_end) {
                         pos = w.qa;
                         ++q_group;
                     }
+                    load_q(pos, q_group);
                 }
+                if (!ok || k + 1 >= n_units) break;
+                w = window_unit(p, static_cast<int>(blockIdx.x + (k + 1) * gridDim.x));
+                if (w.n > 0)
+                    for (int kb = 0; kb < KB; ++kb) {
+                        tma_prefetch_3d(&tmK, kb * 64, w.key0, w.group);
+                        tma_prefetch_3d(&tmV, kb * 64, w.key0, w.group);
+                    }
             }
             if (done > 0) mbar_wait_bounded(kv_full, (done - 1) & 1, p.status);
             for (int m = (n > QS ? n - QS : 0); m < n; ++m)
@@ -793,36 +815,21 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                            idesc_s, kb > 0 ? 1u : 0u);
             mma_commit_elect(&s_full[u]);
         };
-        // Tiles of unit k once its K and V are there: 0 past the last unit, -1 after
-        // a wait that gave up.
-        auto tiles_of = [&](int k) {
-            if (k >= n_units) return 0;
-            if (!warp_wait(kv_full, k & 1, abort_flag, p.status)) return -1;
-            return *static_cast<const volatile int*>(&units[k % kUnitSlots].n);
-        };
         int m = 0, full = 0;   // tiles, and units with tiles, so far
-        bool primed = false;   // the unit's first S^T, dP^T are issued
-        int nv = tiles_of(0);
         // (a wait that gives up sets the abort flag, later waits return at once and
         // the loops end without blocking)
-        for (int k = 0; k < n_units && nv >= 0;) {
-            if (nv == 0) {
-                mma_commit_elect(kv_empty);
-                nv = tiles_of(++k);
-                continue;
-            }
-            if (!primed) {
+        for (int k = 0; k < n_units; ++k) {
+            if (!warp_wait(kv_full, k & 1, abort_flag, p.status)) break;
+            const int nv = *static_cast<const volatile int*>(&units[k % kUnitSlots].n);
+            if (nv > 0) {
                 warp_wait(&q_full[m % QS], (m / QS) & 1, abort_flag, p.status);
                 tc_fence_after();
                 issue_sdp(m % QS, 0);
                 issue_sdp(m % QS, 1);
-                if (nv == 1) mma_commit_elect(kv_empty);
             }
-            int nx = 0;   // tiles of the next unit
+            if (nv <= 1) mma_commit_elect(kv_empty);
             for (int n = 0; n < nv; ++n, ++m) {
                 const bool last = n + 1 == nv;
-                if (last) nx = tiles_of(k + 1);
-                const bool more = !last || nx > 0;
                 const int slot = m % QS, nslot = (m + 1) % QS;
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
@@ -845,20 +852,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                         mma_commit_elect(&q_empty[slot]);
                         if (last) mma_commit_elect(acc_full);
                     }
-                    if (more) {
+                    if (!last) {
                         if (u == 0) {
                             warp_wait(&q_full[nslot], ((m + 1) / QS) & 1, abort_flag, p.status);
                             tc_fence_after();
                         }
                         issue_sdp(nslot, u);
-                        if (u == 1 && (last ? nx == 1 : n + 2 == nv)) mma_commit_elect(kv_empty);
+                        if (u == 1 && n + 2 == nv) mma_commit_elect(kv_empty);
                     }
                 }
             }
-            ++full;
-            ++k;
-            primed = nx > 0;
-            nv = nx;
+            if (nv > 0) ++full;
         }
         mma_commit_elect(mma_done);
         mbar_wait_bounded(mma_done, 0, p.status);
@@ -870,61 +874,70 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const uint32_t tS = tmem + lb + 128 * hq + 32 * cc, tDP = tS + 64;
         const uint64_t sl22 = f2(p.scale_log2, p.scale_log2);
 
-        // dV and scale * dK of this thread's key row, D/4 columns per warp.
+        // dV and scale * dK of this thread's key row, CW columns per warp.
+        const uint32_t patch = smem_u32(sOut) + warp * kPatch;
         int full = 0;   // units with tiles so far
         auto write_unit = [&](const WindowUnit& w) {
-            constexpr int CW = D / 4;   // 32 (D = 128) or 16 (D = 64)
             const int col0 = (hq + 2 * cc) * CW;
-            const int key = w.key0 + quad * 32 + lane;
-            const bool any = w.n > 0;
-            if (any) {
+            const int key_first = w.key0 + quad * 32, key = key_first + lane;
+            uint32_t a[2][CW];
+            if (w.n > 0) {
                 warp_wait(acc_full, full & 1, abort_flag, p.status);
                 ++full;
+                tc_fence_after();
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    const uint32_t src = tmem + lb + 256 + which * D + col0;
+                    if constexpr (CW == 32) tmem_ld32(src, a[which]);
+                    else tmem_ld16(src, a[which]);
+                }
+                tmem_wait_ld();
+                reg_fence(a[0]);
+                reg_fence(a[1]);
+                tc_fence_before();
+                mbar_arrive(acc_empty);
+            } else {
+#pragma unroll
+                for (int i = 0; i < CW; ++i) a[0][i] = a[1][i] = 0u;
             }
-            tc_fence_after();
             const bool ok = *abort_flag == 0;
             const BwdParams::WindowRanges& wr = p.wr[w.region];
-            const int64_t grow = static_cast<int64_t>(w.group) * p.Nk + key;
-            // dV first, then dK, so only one accumulator chunk is live at a time.
-#pragma unroll 1
-            for (int which = 0; which < 2; ++which) {
-                uint32_t a[CW];
-                if (any) {
-                    const uint32_t src = tmem + lb + 256 + which * D + col0;
-                    if constexpr (CW == 32) tmem_ld32(src, a);
-                    else tmem_ld16(src, a);
-                    tmem_wait_ld();
-                    reg_fence(a);
-                } else {
+            const bool whole = wr.splits == 1;
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) a[i] = 0u;
-                }
-                if (ok && key < p.Nk && wr.splits > 1) {
+            for (int which = 0; which < 2; ++which) {
+                if (whole) {
+                    const float sc = which ? p.scale : 1.0f;
+                    if (lane == 0) tma_store_wait_read();   // of the patch's last values
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < CW / 8; ++i) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = pack2<BF16>(__uint_as_float(a[which][8 * i + 2 * j]) * sc,
+                                               __uint_as_float(a[which][8 * i + 2 * j + 1]) * sc);
+                        // 16-byte piece i of row `lane`, where the map's swizzle puts it
+                        const int at = CW == 32 ? i ^ ((lane >> 1) & 3) : i ^ ((lane >> 2) & 1);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         patch + lane * (CW * 2) + at * 16),
+                                     "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && ok && key_first < p.Nk)
+                        tma_store_3d(which ? &tmDK : &tmDV, patch, col0, key_first, w.group);
+                } else if (ok && key < p.Nk) {
                     // this query range's fp32 partial sum (dK unscaled)
                     float* dst = (which ? wr.dk_part : wr.dv_part) +
                                  ((static_cast<int64_t>(w.sp) * p.n_groups + w.group) * wr.keys + key -
                                   wr.key0) * D + col0;
 #pragma unroll
                     for (int i = 0; i < CW / 4; ++i)
-                        reinterpret_cast<float4*>(dst)[i] =
-                            make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
-                                        __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]));
-                } else if (ok && key < p.Nk) {
-                    const float sc = which ? p.scale : 1.0f;
-                    uint32_t x[CW / 2];
-#pragma unroll
-                    for (int i = 0; i < CW / 2; ++i)
-                        x[i] = pack2<BF16>(__uint_as_float(a[2 * i]) * sc, __uint_as_float(a[2 * i + 1]) * sc);
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(which ? p.dk : p.dv) +
-                                                          grow * D + col0);
-#pragma unroll
-                    for (int i = 0; i < CW / 8; ++i)
-                        dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        reinterpret_cast<float4*>(dst)[i] = make_float4(
+                            __uint_as_float(a[which][4 * i]), __uint_as_float(a[which][4 * i + 1]),
+                            __uint_as_float(a[which][4 * i + 2]), __uint_as_float(a[which][4 * i + 3]));
                 }
-            }
-            if (any) {
-                tc_fence_before();
-                mbar_arrive(acc_empty);
             }
         };
 
@@ -1027,6 +1040,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 if (i == 0 && k > 0) write_unit(units[(k - 1) % kUnitSlots]);
             } while (++i < tiles);
         }
+        if (lane == 0) tma_store_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -1483,6 +1497,12 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
 
 template <int D>
 constexpr int dkdv_smem() { return 2 * BwdCfg<D>::kTileBytes + 4 * BwdCfg<D>::kTileBytes + 2 * 2 * kRows * 4 + 256 + 1024; }
+// 6 tiles, 16 warps' patches of dV or dK, the query tiles' statistics, barriers and units
+template <int D>
+constexpr int window_dkdv_smem() {
+    return 6 * BwdCfg<D>::kTileBytes + kRows * D * 2 + 2 * 2 * kRows * 4 + 512;
+}
+static_assert(window_dkdv_smem<128>() <= 227 * 1024, "shared memory of a CTA");
 template <int D, bool STAGE>
 constexpr int dq_smem() {
     return (2 + dq_kstages<D, STAGE>() + kDqVStages) * BwdCfg<D>::kTileBytes +
@@ -1579,10 +1599,15 @@ cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
                          dq_threads<3, D>(), dq_bytes, stream, tmQ, tmDO, tmK, tmV, p);
     if (e != cudaSuccess) return e;
     auto kv = bwd_window_dkdv_kernel<D, BF16>;
-    constexpr int kv_bytes = dkdv_smem<D>() + kUnitSlots * static_cast<int>(sizeof(WindowUnit));
+    constexpr int kv_bytes = window_dkdv_smem<D>();
     e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_bytes);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kv, p.n_units < p.ctas ? p.n_units : p.ctas, kKvThreads, kv_bytes, stream, tmQ, tmDO, tmK, tmV, p);
+    CUtensorMap tmDK, tmDV;
+    if (make_patch_map_public(&tmDK, p.dk, BF16, D, p.Nk, p.n_groups) != 0 ||
+        make_patch_map_public(&tmDV, p.dv, BF16, D, p.Nk, p.n_groups) != 0)
+        return cudaErrorInvalidValue;
+    e = launch_dependent(kv, p.n_units < p.ctas ? p.n_units : p.ctas, kKvThreads, kv_bytes, stream, tmQ,
+                         tmDO, tmK, tmV, tmDK, tmDV, p);
     if (e != cudaSuccess) return e;
     int64_t n8[2];
     for (int r = 0; r < 2; ++r)
