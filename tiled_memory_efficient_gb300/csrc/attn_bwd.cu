@@ -1159,8 +1159,7 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
     // MK: 0 no mask, 1 a general bias, 2 a boolean mask that depends on the
     // key alone (the same keep bytes for every row: read directly, served to
     // the whole warp at once).
-    // 3 a sliding window with sinks (one query head per group).
-    constexpr bool MASK = MK == 1 || MK == 2, STAGE = MK == 1, WIN = MK == 3;
+    constexpr bool MASK = MK != 0, STAGE = MK == 1;
     // K lives from S_j to dQ_j, V only until dP_j: separate rings, K deeper.
     // A general mask stages each warp's next 32 x 64 bias block in shared
     // memory (8 warps x 4 KB); at D = 128 the K ring gives a stage for it.
@@ -1199,18 +1198,10 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
     const int qi = p.n_qtiles - 1 - static_cast<int>(blockIdx.x % p.n_qtiles);
     const int64_t row0 = static_cast<int64_t>(qi) * kRows;
     int nkv = (p.Nk + kRows - 1) / kRows;
-    KeyList kl;
-    if constexpr (WIN) {
-        kl = key_list(row0 + p.causal_off, p.window, p.sinks);
-        const int64_t keys =
-            min(min(row0 + kRows, p.rows_per_group) + p.causal_off, static_cast<int64_t>(p.Nk));
-        nkv = static_cast<int>((keys + kRows - 1) / kRows) - kl.skip;
-    } else if (CAUSAL) {
+    if (CAUSAL) {
         const int keys = min(tile_max_pos(row0, p) + 1, p.Nk);
         nkv = (keys + kRows - 1) / kRows;
     }
-    auto ktile = [&](int j) { return WIN ? kl.tile(j) : j; };
-    const int kv_group = WIN ? group / p.kv_div : group;
     // A boolean mask that depends on the key alone: the key tiles past its last
     // kept key contribute nothing to dQ (at least one tile is kept, so rows with
     // no kept key still end with dQ = 0).
@@ -1269,13 +1260,13 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
                 mbar_arrive_expect_tx(&k_full[ks], TB);
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(&tmK, &k_full[ks], sK + ks * TB + kb * (kRows * 128), kb * 64,
-                                ktile(j) * kRows, kv_group);
+                                j * kRows, group);
                 ++nk;
                 if (!mbar_wait(&v_empty[vs], ((j / VS) & 1) ^ 1, abort_flag, p.status)) break;
                 mbar_arrive_expect_tx(&v_full[vs], TB);
                 for (int kb = 0; kb < KB; ++kb)
                     tma_load_3d(&tmV, &v_full[vs], sV + vs * TB + kb * (kRows * 128), kb * 64,
-                                ktile(j) * kRows, kv_group);
+                                j * kRows, group);
                 ++nv;
             }
             mbar_wait_bounded(q_full, 0, p.status);
@@ -1332,25 +1323,20 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         const int hq = warp >> 2, quad = warp & 3;   // column group, TMEM lane quadrant
         const int64_t row = row0 + quad * 32 + lane;
         const bool row_ok = row < p.rows_per_group;
-        const int pos = static_cast<int>(WIN ? row : row % p.Nq);   // WIN: one head per group
+        const int pos = static_cast<int>(row % p.Nq);
         const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tS = tmem + lb, tDP = tmem + lb + 128;
         const float sl2 = p.scale_log2;
         warp_wait(q_full, 0, abort_flag, p.status);
         const float nl = sL[quad * 32 + lane];   // -lse2 of this row
         const float nd = sDl[quad * 32 + lane];  // -delta of this row
-        const int off = WIN ? p.causal_off : 0;
-        const int lim = CAUSAL ? min(p.Nk, pos + off + 1) : p.Nk;  // keys [0, lim) allowed
-        const int low = WIN ? pos + off - p.window : 0;            // WIN: above it, or sinks
+        const int lim = CAUSAL ? min(p.Nk, pos + 1) : p.Nk;  // keys [0, lim) allowed
         // Smallest position among this warp's rows: key tiles past it (or past
         // Nk) need the mask.  Rows past the group only feed their own dQ rows,
         // which are never stored, so they need none.
         const int64_t wr0 = row0 + quad * 32;
         const int64_t wr1 = min(wr0 + 31, p.rows_per_group - 1);
-        const int warp_min_pos = WIN ? static_cast<int>(wr0)
-                                 : (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq)
-                                                              : 0;
-        const int warp_max_pos = static_cast<int>(wr1);   // (WIN)
+        const int warp_min_pos = (wr0 / p.Nq == wr1 / p.Nq) ? static_cast<int>(wr0 % p.Nq) : 0;
         // scale still to apply to the scores read below: an additive bias
         // leaves natural-log logits (log2 e), a boolean one raw scores
         const float sc = (MASK && p.mask_kind == 2) ? kLog2e : sl2;
@@ -1380,14 +1366,10 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
         if constexpr (STAGE)
             if (nkv > 0 && staged(0)) prefetch(32 * CPW * hq);
         for (int j = 0; j < nkv; ++j) {
-            const int k0 = ktile(j) * kRows;
+            const int k0 = j * kRows;
             warp_wait(s_full, j & 1, abort_flag, p.status);
             tc_fence_after();
-            const bool need_mask =
-                (k0 + kRows > p.Nk) ||
-                (WIN ? window_edge(k0, k0 + kRows - 1, warp_min_pos + off, warp_max_pos + off,
-                                   p.window, p.sinks)
-                     : CAUSAL && k0 + kRows - 1 > warp_min_pos);
+            const bool need_mask = (k0 + kRows > p.Nk) || (CAUSAL && k0 + kRows - 1 > warp_min_pos);
             uint32_t sv[CPW][32], dp[CPW][32];
 #pragma unroll
             for (int cc = 0; cc < CPW; ++cc) {
@@ -1440,13 +1422,8 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
                     float p0 = ex2_ftz(f2lo(x)), p1 = ex2_ftz(f2hi(x));
                     if (need_mask) {
                         const int kk = k0 + c * 32 + i;
-                        if constexpr (WIN) {
-                            p0 = window_sees(kk, lim, low, p.sinks) ? p0 : 0.0f;
-                            p1 = window_sees(kk + 1, lim, low, p.sinks) ? p1 : 0.0f;
-                        } else {
-                            p0 = kk < lim ? p0 : 0.0f;
-                            p1 = kk + 1 < lim ? p1 : 0.0f;
-                        }
+                        p0 = kk < lim ? p0 : 0.0f;
+                        p1 = kk + 1 < lim ? p1 : 0.0f;
                     }
                     const uint64_t dd = fmul2(
                         f2(p0, p1),
@@ -1495,6 +1472,349 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
     }
 }
 
+// ---------------------------------------------------------------- dQ, sliding window
+// The same products and TMEM layout as bwd_dq_kernel with 16 elementwise warps.  A
+// query tile meets a window's key tiles only (10 at a window of 1024), and with a
+// CTA to each, set-up, first loads, a masked tile at either end and the epilogue took
+// a third of its time.  As in bwd_window_dkdv_kernel a CTA takes query tiles in turn
+// and its roles run through them without a break; the next one's first S and dP
+// are computed before this one's last dQ product.
+struct WindowRows {
+    int n;               // key tiles
+    int row0, head;      // first row within the query head, the head of all batches
+    int n_sink, skip;    // KeyList
+};
+
+__device__ __forceinline__ WindowRows window_rows(const BwdParams& p, int idx) {
+    WindowRows w;
+    w.head = static_cast<int>(static_cast<unsigned>(idx) / static_cast<unsigned>(p.n_qtiles));
+    w.row0 = (p.n_qtiles - 1 - (idx - w.head * p.n_qtiles)) * kRows;
+    const KeyList kl = key_list(w.row0 + p.causal_off, p.window, p.sinks);
+    const int keys = min(w.row0 + kRows, p.Nq) + p.causal_off;
+    w.n_sink = kl.n_sink;
+    w.skip = kl.skip;
+    w.n = (keys + kRows - 1) / kRows - kl.skip;   // at least 1: a query sees its own position
+    return w;
+}
+
+// Bits [0, n) of 32.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// One step of a transposition over lanes: lanes with bit b keep hi and trade lo for the
+// hi of the lane without it.
+__device__ __forceinline__ void trade_piece(uint32_t (&lo)[4], uint32_t (&hi)[4], int lane, int b) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo[e] : hi[e], b);
+        lo[e] = up ? got : lo[e];
+        hi[e] = up ? hi[e] : got;
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kKvThreads, 1)
+    bwd_window_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmDO,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+    using C = BwdCfg<D>;
+    constexpr int TB = C::kTileBytes, KB = C::kKB, VS = kDqVStages, KS = dq_kstages<D, false>();
+    extern __shared__ __align__(1024) uint8_t smem_w[];
+    uint8_t* sQ = smem_w;
+    uint8_t* sDO = sQ + TB;
+    uint8_t* sK = sDO + TB;           // [KS]
+    uint8_t* sV = sK + KS * TB;       // [VS]
+    float* sL = reinterpret_cast<float*>(sV + VS * TB);
+    float* sDl = sL + kRows;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sDl + kRows);
+    uint64_t* q_full = bars;          // a query tile's numbers, Q, dO and statistics
+    uint64_t* q_empty = q_full + 1;   // numbers and statistics read (16 warps), Q and dO, too
+    uint64_t* k_full = q_empty + 1;   // [KS]
+    uint64_t* k_empty = k_full + KS;  // [KS]
+    uint64_t* v_full = k_empty + KS;  // [VS]
+    uint64_t* v_empty = v_full + VS;  // [VS]
+    uint64_t* s_full = v_empty + VS;  // S and dP in TMEM
+    uint64_t* s_free = s_full + 1;    // S and dP read (512 arrivals)
+    uint64_t* p_full = s_free + 1;    // dS in TMEM (512 arrivals)
+    uint64_t* dq_done = p_full + 1;   // dQ += dS K done (dS columns free)
+    uint64_t* acc_full = dq_done + 1;    // a query tile's last dQ product done
+    uint64_t* acc_empty = acc_full + 1;  // its dQ read (512 arrivals)
+    uint64_t* mma_done = acc_empty + 1;
+    WindowRows* units = reinterpret_cast<WindowRows*>(mma_done + 1);   // [kUnitSlots]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + kUnitSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int total = p.n_groups * p.G * p.n_qtiles;
+    const int n_units = (total - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1 + 16);
+        for (int i = 0; i < KS; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+        for (int i = 0; i < VS; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 512);
+        mbar_init(p_full, 512);
+        mbar_init(dq_done, 1);
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 512);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kKvMmaWarp) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // Launched as a programmatic dependent of the statistics kernel; the dK/dV kernel
+    // may start on the SMs this grid leaves idle (bwd_dq_kernel).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    if (warp == kKvProducerWarp) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            int nk = 0, nv = 0, nq = 0;   // K tiles, V tiles, query tiles asked for
+            bool ok = true;
+            auto load_kv = [&](int key0, int kv_group) {
+                const int ks = nk % KS, vs = nv % VS;
+                ok = mbar_wait(&k_empty[ks], ((nk / KS) & 1) ^ 1, abort_flag, p.status);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&k_full[ks], TB);
+                for (int kb = 0; kb < KB; ++kb)
+                    tma_load_3d(&tmK, &k_full[ks], sK + ks * TB + kb * (kRows * 128), kb * 64, key0,
+                                kv_group);
+                ++nk;
+                ok = mbar_wait(&v_empty[vs], ((nv / VS) & 1) ^ 1, abort_flag, p.status);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&v_full[vs], TB);
+                for (int kb = 0; kb < KB; ++kb)
+                    tma_load_3d(&tmV, &v_full[vs], sV + vs * TB + kb * (kRows * 128), kb * 64, key0,
+                                kv_group);
+                ++nv;
+            };
+            WindowRows w = window_rows(p, static_cast<int>(blockIdx.x));
+            for (int k = 0; k < n_units; ++k) {
+                KeyList kl;
+                kl.n_sink = w.n_sink;
+                kl.skip = w.skip;
+                const int kv_group = w.head / p.kv_div;
+                load_kv(kl.tile(0) * kRows, kv_group);
+                if (ok && k > 0) ok = mbar_wait(q_empty, (k - 1) & 1, abort_flag, p.status);
+                if (!ok) break;
+                units[k % kUnitSlots] = w;
+                mbar_arrive_expect_tx(q_full, 2 * TB + 2 * kRows * 4);
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_load_3d(&tmQ, q_full, sQ + kb * (kRows * 128), kb * 64, w.row0, w.head);
+                    tma_load_3d(&tmDO, q_full, sDO + kb * (kRows * 128), kb * 64, w.row0, w.head);
+                }
+                const int64_t w0 = static_cast<int64_t>(w.head) * p.rows_pad + w.row0;
+                bulk_load(sL, p.nlse2 + w0, kRows * 4, q_full);
+                bulk_load(sDl, p.ndelta + w0, kRows * 4, q_full);
+                ++nq;
+                for (int j = 1; j < w.n && ok; ++j) load_kv(kl.tile(j) * kRows, kv_group);
+                if (!ok || k + 1 >= n_units) break;
+                w = window_rows(p, static_cast<int>(blockIdx.x + (k + 1) * gridDim.x));
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_prefetch_3d(&tmQ, kb * 64, w.row0, w.head);
+                    tma_prefetch_3d(&tmDO, kb * 64, w.row0, w.head);
+                }
+            }
+            if (nq > 0) mbar_wait_bounded(q_full, (nq - 1) & 1, p.status);
+            for (int m = (nk > KS ? nk - KS : 0); m < nk; ++m)
+                mbar_wait_bounded(&k_full[m % KS], (m / KS) & 1, p.status);
+            for (int m = (nv > VS ? nv - VS : 0); m < nv; ++m)
+                mbar_wait_bounded(&v_full[m % VS], (m / VS) & 1, p.status);
+        }
+    } else if (warp == kKvMmaWarp) {
+        constexpr uint32_t idesc_s = idesc_f16(kRows, kRows, BF16, false);
+        constexpr uint32_t idesc_g = idesc_f16(kRows, D, BF16, true);
+        constexpr uint64_t kStep = TB >> 4;
+        constexpr uint64_t kBlk = (kRows * 128) >> 4;
+        const uint64_t dQk = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dDOk = smem_desc_sw128(smem_u32(sDO), 16, 1024);
+        const uint64_t dKk = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dVk = smem_desc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dKm = smem_desc_sw128(smem_u32(sK), kRows * 128, 1024);
+        // S = Q K^T and dP = dO V^T of key tile m (of all query tiles), one commit for
+        // both; `last` of its query tile: Q and dO are free after it.
+        auto issue_s_dp = [&](int m, bool last) {
+            const int ks = m % KS, vs = m % VS;
+            warp_wait(&k_full[ks], (m / KS) & 1, abort_flag, p.status);
+            warp_wait(&v_full[vs], (m / VS) & 1, abort_flag, p.status);
+            tc_fence_after();
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                mma_ss_k64(tmem, dQk + kb * kBlk, dKk + ks * kStep + kb * kBlk, idesc_s,
+                           kb > 0 ? 1u : 0u);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                mma_ss_k64(tmem + 128, dDOk + kb * kBlk, dVk + vs * kStep + kb * kBlk, idesc_s,
+                           kb > 0 ? 1u : 0u);
+            mma_commit_elect(s_full);
+            mma_commit_elect(&v_empty[vs]);   // V is only read by dP
+            if (last) mma_commit_elect(q_empty);
+        };
+        // Key tiles of query tile k once its Q and dO are there; 0: none left, or a
+        // wait gave up.
+        auto tiles_of = [&](int k) {
+            if (k >= n_units || !warp_wait(q_full, k & 1, abort_flag, p.status)) return 0;
+            return *static_cast<const volatile int*>(&units[k % kUnitSlots].n);
+        };
+        int m = 0, n = tiles_of(0);
+        if (n > 0) issue_s_dp(0, n == 1);
+        for (int k = 0; n > 0; ++k) {
+            int next = 0;
+            for (int j = 0; j < n; ++j, ++m) {
+                const bool last = j + 1 == n;
+                warp_wait(s_free, m & 1, abort_flag, p.status);
+                if (last) next = tiles_of(k + 1);
+                if (!last || next > 0) issue_s_dp(m + 1, last ? next == 1 : j + 2 == n);
+                warp_wait(p_full, m & 1, abort_flag, p.status);
+                // the first product overwrites the dQ of the query tile before
+                if (j == 0 && k > 0) warp_wait(acc_empty, (k - 1) & 1, abort_flag, p.status);
+                tc_fence_after();
+                mma_ts_k128(tmem + 256, tmem + 384, dKm + (m % KS) * kStep, idesc_g, j > 0 ? 1u : 0u);
+                mma_commit_elect(dq_done);
+                mma_commit_elect(&k_empty[m % KS]);
+                if (last) mma_commit_elect(acc_full);
+            }
+            n = next;
+        }
+        mma_commit_elect(mma_done);
+        mbar_wait_bounded(mma_done, 0, p.status);
+    } else {
+        // One thread per query row and 32-key chunk hq of the tile.
+        const int hq = warp >> 2, quad = warp & 3;
+        const uint32_t lb = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tS = tmem + lb + 32 * hq, tDP = tS + 128, tDS = tmem + lb + 384 + 16 * hq;
+        const uint64_t sl22 = f2(p.scale_log2, p.scale_log2);
+
+        // dQ of this thread's row, 32 columns a warp (D = 64: half of the warps).  Four
+        // lanes trade their rows' 16-byte pieces, so that a store of the warp writes 8
+        // rows' 64 bytes, not 32 rows' 16.
+        auto write_rows = [&](const WindowRows& w, int k) {
+            warp_wait(acc_full, k & 1, abort_flag, p.status);
+            tc_fence_after();
+            uint32_t a[32];
+            tmem_ld32(tmem + lb + 256 + hq % (D / 32) * 32, a);
+            tmem_wait_ld();
+            reg_fence(a);
+            tc_fence_before();
+            mbar_arrive(acc_empty);
+            uint32_t x[4][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x[i >> 2][i & 3] = pack2<BF16>(__uint_as_float(a[2 * i]) * p.scale,
+                                               __uint_as_float(a[2 * i + 1]) * p.scale);
+            trade_piece(x[0], x[1], lane, 1);
+            trade_piece(x[2], x[3], lane, 1);
+            trade_piece(x[0], x[2], lane, 2);
+            trade_piece(x[1], x[3], lane, 2);
+            const bool ok = hq < D / 32 && *abort_flag == 0;
+            const int row = w.row0 + quad * 32 + (lane & ~3);   // piece lane & 3 of 4 rows
+            uint16_t* dst = static_cast<uint16_t*>(p.dq) +
+                            (static_cast<int64_t>(w.head) * p.Nq + row) * D + hq * 32 + (lane & 3) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (ok && row + i < p.Nq)
+                    *reinterpret_cast<uint4*>(dst + i * D) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        };
+
+        int m = 0;   // key tiles so far
+        for (int k = 0; k <= n_units; ++k) {   // (the last turn only writes)
+            WindowRows w{};
+            float nl = 0.0f, nd = 0.0f;   // -lse2 and -delta of this row
+            if (k < n_units) {
+                if (!warp_wait(q_full, k & 1, abort_flag, p.status)) break;
+                w = units[k % kUnitSlots];
+                nl = sL[quad * 32 + lane];
+                nd = sDl[quad * 32 + lane];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_empty);
+            }
+            const uint64_t nl2 = f2(nl, nl), nd2 = f2(nd, nd);
+            const int pos0 = w.row0 + quad * 32 + p.causal_off;      // of the warp's first row
+            const int pos1 = min(pos0 + 31, p.Nk - 1);               // and last
+            const int pos = pos0 + lane;
+            int j = 0;
+            do {
+                if (j < w.n) {
+                    const int key0 = (j < w.n_sink ? j : j + w.skip) * kRows + 32 * hq;
+                    // does every row see every key of the chunk, or none any?  (rows past the
+                    // last query are not written)
+                    const bool all = !window_edge(key0, key0 + 31, pos0, pos1, p.window, p.sinks);
+                    const bool none = key0 > pos1 || (key0 + 31 <= pos0 - p.window && key0 >= p.sinks);
+                    warp_wait(s_full, m & 1, abort_flag, p.status);
+                    tc_fence_after();
+                    uint32_t sv[32], dp[32];
+                    tmem_ld32(tS, sv);
+                    tmem_ld32(tDP, dp);
+                    tmem_wait_ld();
+                    reg_fence(sv);
+                    reg_fence(dp);
+                    // S and dP are in registers: the next ones may overwrite them
+                    tc_fence_before();
+                    mbar_arrive(s_free);
+                    // the dS columns still feed the product before
+                    if (m > 0) {
+                        warp_wait(dq_done, (m - 1) & 1, abort_flag, p.status);
+                        tc_fence_after();
+                    }
+                    auto math = [&](auto masked) {
+                        constexpr bool M = decltype(masked)::value;
+                        // Bit i: this row sees key key0 + i.
+                        const uint32_t vis =
+                            !M ? 0u
+                               : bits_below(pos + 1 - key0) & (~bits_below(pos - p.window + 1 - key0) |
+                                                               bits_below(p.sinks - key0));
+                        uint32_t dw[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const uint64_t x = ffma2(
+                                f2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), sl22, nl2);
+                            const uint64_t dd = fmul2(
+                                f2(ex2_ftz(f2lo(x)), ex2_ftz(f2hi(x))),
+                                fadd2(f2(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])), nd2));
+                            float d0 = f2lo(dd), d1 = f2hi(dd);
+                            if constexpr (M) {
+                                d0 = (vis >> i) & 1u ? d0 : 0.0f;
+                                d1 = (vis >> (i + 1)) & 1u ? d1 : 0.0f;
+                            }
+                            dw[i >> 1] = pack2<BF16>(d0, d1);
+                        }
+                        tmem_st16(tDS, dw);
+                    };
+                    if (all) {
+                        math(std::false_type{});
+                    } else if (!none) {
+                        math(std::true_type{});
+                    } else {
+                        const uint32_t zero[16] = {};
+                        tmem_st16(tDS, zero);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_full);
+                    ++m;
+                }
+                if (j == 0 && k > 0) write_rows(units[(k - 1) % kUnitSlots], k - 1);
+            } while (++j < w.n);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kKvMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 template <int D>
 constexpr int dkdv_smem() { return 2 * BwdCfg<D>::kTileBytes + 4 * BwdCfg<D>::kTileBytes + 2 * 2 * kRows * 4 + 256 + 1024; }
 // 6 tiles, 16 warps' patches of dV or dK, the query tiles' statistics, barriers and units
@@ -1502,7 +1822,12 @@ template <int D>
 constexpr int window_dkdv_smem() {
     return 6 * BwdCfg<D>::kTileBytes + kRows * D * 2 + 2 * 2 * kRows * 4 + 512;
 }
-static_assert(window_dkdv_smem<128>() <= 227 * 1024, "shared memory of a CTA");
+template <int D>
+constexpr int window_dq_smem() {
+    return (2 + dq_kstages<D, false>() + kDqVStages) * BwdCfg<D>::kTileBytes + 2 * kRows * 4 + 512;
+}
+static_assert(window_dkdv_smem<128>() <= 227 * 1024 && window_dq_smem<128>() <= 227 * 1024,
+              "shared memory of a CTA");
 template <int D, bool STAGE>
 constexpr int dq_smem() {
     return (2 + dq_kstages<D, STAGE>() + kDqVStages) * BwdCfg<D>::kTileBytes +
@@ -1591,12 +1916,13 @@ cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
                                   dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0,
                                   stream, p);
     if (e != cudaSuccess) return e;
-    auto dq = bwd_dq_kernel<D, BF16, true, 3>;
-    constexpr int dq_bytes = dq_smem<D, false>();
+    auto dq = bwd_window_dq_kernel<D, BF16>;
+    constexpr int dq_bytes = window_dq_smem<D>();
     e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_bytes);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(dq, static_cast<long long>(p.n_groups) * p.G * p.n_qtiles,
-                         dq_threads<3, D>(), dq_bytes, stream, tmQ, tmDO, tmK, tmV, p);
+    const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.G * p.n_qtiles;
+    e = launch_dependent(dq, tiles < p.ctas ? tiles : p.ctas, kKvThreads, dq_bytes, stream, tmQ, tmDO, tmK,
+                         tmV, p);
     if (e != cudaSuccess) return e;
     auto kv = bwd_window_dkdv_kernel<D, BF16>;
     constexpr int kv_bytes = window_dkdv_smem<D>();
