@@ -453,21 +453,12 @@ def attn_bwd_window(q, k, v, out, dout, lse, window: int, sinks: int = 0,
     _refused("attn_bwd_window", r, explain)
 
 
-def check_captured_backward(device):
-    """Raises when the backward pass being captured would hand a gradient to a stream
-    outside the capture.  A leaf's gradient is summed on the stream of the first live
-    graph that holds the leaf; when that graph was recorded outside the capture, the
-    capture would make an outside stream wait for it, which ends the capture and with
-    it the process.  Called from inside a backward, before it launches anything."""
-    import torch
-    for sid in (_bind or _load_bind()).streams_above():
-        if sid:
-            with torch.cuda.stream(torch.cuda.Stream(stream_id=sid, device_index=device.index,
-                                                     device_type=1)):
-                if torch.cuda.is_current_stream_capturing():
-                    continue   # a branch of this capture
-        raise RuntimeError("this backward pass is being captured, but a graph recorded outside the "
-                           "capture still holds one of its leaves: drop that graph first")
+def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None = None):
+    """attn_fwd_window as a differentiable function: its output alone."""
+    r = (_bind or _load_bind()).window_attention(q, k, v, window, sinks, scale)
+    if type(r) is not int:
+        return r
+    _refused("attn_fwd_window", r, lambda: _explain_window(q, k, v))
 
 
 def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None = None,

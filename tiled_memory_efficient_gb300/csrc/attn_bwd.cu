@@ -1497,11 +1497,6 @@ __device__ __forceinline__ WindowRows window_rows(const BwdParams& p, int idx) {
     return w;
 }
 
-// Bits [0, n) of 32.
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
 // One step of a transposition over lanes: lanes with bit b keep hi and trade lo for the
 // hi of the lane without it.
 __device__ __forceinline__ void trade_piece(uint32_t (&lo)[4], uint32_t (&hi)[4], int lane, int b) {

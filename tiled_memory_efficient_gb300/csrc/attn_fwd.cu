@@ -238,6 +238,20 @@ __device__ __forceinline__ void pack_p128(const uint32_t (&sr)[4][32], uint32_t 
     }
 }
 
+// Hides from a row at key position `pos` what it does not see of the 32 keys from key0
+// on; the warp's rows stand at [min_pos, max_pos].  Chunks that all of them see cost
+// a test, the others a bit a key.
+__device__ __forceinline__ void window_mask32(uint32_t (&s)[32], int key0, int pos, int min_pos,
+                                              int max_pos, const FwdParams& p) {
+    if (!window_edge(key0, key0 + 31, min_pos, max_pos, p.window, p.sinks)) return;
+    // (a row past the last query may stand past the last key: it is not written)
+    const uint32_t vis = bits_below(pos + 1 - key0) &
+                         (~bits_below(pos + 1 - p.window - key0) | bits_below(p.sinks - key0));
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (!((vis >> i) & 1u)) s[i] = __float_as_uint(-INFINITY);
+}
+
 template <int D, bool BF16, bool CAUSAL, int MK, bool VPRE>
 __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -802,18 +816,10 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 }
             }
             if constexpr (WIN) {
-                if (key0 + 64 > p.Nk ||
-                    window_edge(key0, key0 + 63, warp_min_pos + p.causal_off,
-                                warp_max_pos + p.causal_off, p.window, p.sinks)) {
-                    const int lim = min(p.Nk, pos + p.causal_off + 1);
-                    const int low = pos + p.causal_off - p.window;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!window_sees(key0 + c * 32 + i, lim, low, p.sinks))
-                                sr[c][i] = __float_as_uint(-INFINITY);
-                }
+                for (int c = 0; c < 2; ++c)
+                    window_mask32(sr[c], key0 + 32 * c, pos + p.causal_off,
+                                  warp_min_pos + p.causal_off, warp_max_pos + p.causal_off, p);
             } else if (j >= j_mask) {
                 // keys [0, lim) allowed
                 const int lim = CAUSAL ? min(p.Nk, pos + p.causal_off + 1) : p.Nk;
@@ -1007,6 +1013,30 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
                 }
                 tmem_wait_st();
             }
+            if constexpr (WIN) {
+                // What the mask hides in the tile, in place in TMEM, 32 keys at a time:
+                // with the tile's 128 scores in registers the masking code cost every
+                // tile (B=2 H=16 N=8192 bf16, window 1024: 189 us so, 178 here; window
+                // 4096: 400 and 355).
+                if (window_edge(key0, key0 + kRows - 1, warp_min_pos + p.causal_off,
+                                warp_max_pos + p.causal_off, p.window, p.sinks)) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const int k0 = key0 + 32 * c;
+                        if (!window_edge(k0, k0 + 31, warp_min_pos + p.causal_off,
+                                         warp_max_pos + p.causal_off, p.window, p.sinks))
+                            continue;
+                        uint32_t x[32];
+                        tmem_ld32(tS + c * 32, x);
+                        tmem_wait_ld();
+                        reg_fence(x);
+                        window_mask32(x, k0, pos + p.causal_off, warp_min_pos + p.causal_off,
+                                      warp_max_pos + p.causal_off, p);
+                        tmem_st32(tS + c * 32, x);
+                    }
+                    tmem_wait_st();
+                }
+            }
             uint32_t sr[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
@@ -1040,20 +1070,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
             const float sc = MASK ? 1.0f : sl2;   // scale still to apply to sr
             const bool need_mask =
                 (key0 + kRows > p.Nk) || (CAUSAL && key0 + kRows - 1 > warp_min_pos + p.causal_off);
-            if constexpr (WIN) {
-                if (key0 + kRows > p.Nk ||
-                    window_edge(key0, key0 + kRows - 1, warp_min_pos + p.causal_off,
-                                warp_max_pos + p.causal_off, p.window, p.sinks)) {
-                    const int lim = min(p.Nk, pos + p.causal_off + 1);
-                    const int low = pos + p.causal_off - p.window;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!window_sees(key0 + c * 32 + i, lim, low, p.sinks))
-                                sr[c][i] = __float_as_uint(-INFINITY);
-                }
-            } else if (need_mask) {
+            if (!WIN && need_mask) {
                 // keys [0, lim) allowed
                 const int lim = CAUSAL ? min(p.Nk, pos + p.causal_off + 1) : p.Nk;
 #pragma unroll

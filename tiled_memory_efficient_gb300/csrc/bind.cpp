@@ -10,10 +10,11 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -123,14 +124,16 @@ void* stream_of(int64_t dev) {
     return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
 }
 
-// The C call without the interpreter's lock: a launch waits when the device's queue is full.
+// The C calls run without the interpreter's lock: a launch waits when the device's queue
+// is full.
+struct Unlock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 int unlocked(F&& f) {
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = f();
-    Py_END_ALLOW_THREADS
-    return rc;
+    const Unlock here;
+    return f();
 }
 
 // The pools of a cache: [n_pages, Hkv, page, D], or with a leading layer dimension.
@@ -353,7 +356,11 @@ struct Window {
     int window = 0, sinks = 0;
     float scale = 0.0f;
     bool read(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* w, PyObject* s, PyObject* sc) {
-        q = tensor(q_), k = tensor(k_), v = tensor(v_);
+        return read(tensor(q_), tensor(k_), tensor(v_)) && count(w, &window) && count(s, &sinks) &&
+               scale_of(sc, D, &scale);
+    }
+    bool read(const Tensor& q_, const Tensor& k_, const Tensor& v_) {
+        q = q_, k = k_, v = v_;
         dev = cuda_of(q);
         if (dev < 0 || cuda_of(k) != dev || cuda_of(v) != dev || q.dim() != 4 || k.dim() != 4 ||
             !half(q) || k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type() ||
@@ -362,7 +369,20 @@ struct Window {
             !small(k.sizes()))
             return false;
         B = q.size(0), Hq = q.size(1), Nq = q.size(2), D = q.size(3), Hkv = k.size(1), Nk = k.size(2);
-        return count(w, &window) && count(s, &sinks) && scale_of(sc, D, &scale);
+        return true;
+    }
+    // Workspace bytes, and the calls themselves.
+    size_t fwd_size() const { return fn.fwd_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, code(q)); }
+    size_t bwd_size() const { return fn.bwd_size(B, Hq, Hkv, Nq, Nk, D, window, sinks, code(q)); }
+    int fwd(const Tensor& out, const Tensor& lse, const Tensor& ws) const {
+        return fn.fwd(ptr(q), ptr(k), ptr(v), ptr(out), as<float>(lse), ptr(ws), bytes(ws), B, Hq, Hkv,
+                      Nq, Nk, D, scale, window, sinks, code(q), stream_of(dev));
+    }
+    int bwd(const Tensor& out, const Tensor& dout, const Tensor& lse, const Tensor (&g)[3],
+            const Tensor& ws) const {
+        return fn.bwd(ptr(q), ptr(k), ptr(v), ptr(out), ptr(dout), as<float>(lse), ptr(g[0]),
+                      ptr(g[1]), ptr(g[2]), ptr(ws), bytes(ws), B, Hq, Hkv, Nq, Nk, D, scale, window,
+                      sinks, code(q), stream_of(dev));
     }
 };
 
@@ -375,14 +395,9 @@ PyObject* py_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor out, lse, ws;
     if (!given_or_new(a[6], &out, w.q.sizes(), w.q.scalar_type(), w.dev) ||
         !given_or_new(a[7], &lse, {w.B, w.Hq, w.Nq}, at::kFloat, w.dev) ||
-        !workspace(a[8], &ws,
-                   fn.fwd_size(w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.D, w.window, w.sinks, code(w.q)), w.dev))
+        !workspace(a[8], &ws, w.fwd_size(), w.dev))
         MISFIT();
-    const int rc = unlocked([&] {
-        return fn.fwd(ptr(w.q), ptr(w.k), ptr(w.v), ptr(out), as<float>(lse), ptr(ws), bytes(ws), w.B,
-                      w.Hq, w.Hkv, w.Nq, w.Nk, w.D, w.scale, w.window, w.sinks, code(w.q),
-                      stream_of(w.dev));
-    });
+    const int rc = unlocked([&] { return w.fwd(out, lse, ws); });
     return rc == ATTN_OK ? pair(out, lse) : PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
@@ -400,16 +415,11 @@ PyObject* py_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         MISFIT();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(w.dev));
     Tensor g[3], ws;
-    const size_t size =
-        fn.bwd_size(w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.D, w.window, w.sinks, code(w.q));
+    const size_t size = w.bwd_size();
     for (int i = 0; i < 3; ++i)
         if (!given_or_new(a[9 + i], &g[i], i == 0 ? w.q.sizes() : w.k.sizes(), type, w.dev)) MISFIT();
     if (!workspace(a[12], &ws, size > 0 ? size : 16, w.dev)) MISFIT();
-    const int rc = unlocked([&] {
-        return fn.bwd(ptr(w.q), ptr(w.k), ptr(w.v), ptr(out), ptr(dout), as<float>(lse), ptr(g[0]),
-                      ptr(g[1]), ptr(g[2]), ptr(ws), bytes(ws), w.B, w.Hq, w.Hkv, w.Nq, w.Nk, w.D,
-                      w.scale, w.window, w.sinks, code(w.q), stream_of(w.dev));
-    });
+    const int rc = unlocked([&] { return w.bwd(out, dout, lse, g, ws); });
     if (rc != ATTN_OK) return PyLong_FromLong(rc);
     PyObject* r = PyTuple_New(3);
     if (!r) return nullptr;
@@ -418,13 +428,15 @@ PyObject* py_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// () -> ids of the streams, other than the current one, that the running backward pass
-// would hand gradients to from here on: those of the functions above the one being
-// evaluated that the pass will reach.  Called by that function's backward.
-PyObject* py_streams_above(PyObject*, PyObject* const*, Py_ssize_t) {
-    HANDLE_TH_ERRORS
+// Refuses a captured backward pass that would hand a gradient to a stream outside the
+// capture: the capture would make that stream wait for it, which ends the capture
+// and with it the process.  A leaf's gradient is summed on the stream of the first
+// live graph that holds the leaf, so a graph recorded outside the capture is enough.
+// Looks at the functions above the one being evaluated that the pass will reach;
+// called by its backward before it launches anything.
+void check_captured_backward() {
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
     using torch::autograd::Node;
-    std::set<int64_t> found;
     std::set<const Node*> seen;
     std::vector<std::shared_ptr<Node>> open;
     if (auto node = torch::autograd::get_current_node()) open.push_back(std::move(node));
@@ -435,20 +447,95 @@ PyObject* py_streams_above(PyObject*, PyObject* const*, Py_ssize_t) {
             const auto& next = node->next_edge(i).function;
             if (!next || !node->task_should_compute_output(i) || !seen.insert(next.get()).second)
                 continue;
-            if (const auto s = next->stream()) {
-                const int64_t here = c10::cuda::getCurrentCUDAStream(s->device_index()).id();
-                if (s->device_type() == at::kCUDA && s->id() != here) found.insert(s->id());
-            }
             open.push_back(next);
+            const auto s = next->stream();
+            if (!s || s->device_type() != at::kCUDA ||
+                s->id() == c10::cuda::getCurrentCUDAStream(s->device_index()).id())
+                continue;
+            bool inside = s->id() != 0;   // a branch of this capture?  (0: the default stream)
+            if (inside) {
+                const c10::cuda::CUDAStreamGuard there(*s);
+                inside = c10::cuda::currentStreamCaptureStatusMayInitCtx() !=
+                         c10::cuda::CaptureStatus::None;
+            }
+            TORCH_CHECK(inside, "this backward pass is being captured, but a graph recorded outside the "
+                                "capture still holds one of its leaves: drop that graph first");
         }
     }
-    PyObject* r = PyList_New(0);
-    for (const int64_t id : found) {
-        PyObject* x = r ? PyLong_FromLongLong(id) : nullptr;
-        if (!x || PyList_Append(r, x) != 0) Py_CLEAR(r);
-        Py_XDECREF(x);
+}
+
+// A call that did not run: a status of the library, or kMisfit.
+struct Refused {
+    int rc;
+};
+
+// Sliding-window attention as a function of the autograd graph.  (In Python it took 235
+// us of host time a training pass: the engine's threads hand the interpreter's lock
+// to and fro.)
+struct WindowAttention : torch::autograd::Function<WindowAttention> {
+    using Context = torch::autograd::AutogradContext;
+    static Tensor forward(Context* ctx, const Tensor& q, const Tensor& k, const Tensor& v, int64_t window,
+                          int64_t sinks, double scale) {
+        Window w;
+        if (!w.read(q.contiguous(), k.contiguous(), v.contiguous())) throw Refused{kMisfit};
+        w.window = static_cast<int>(window), w.sinks = static_cast<int>(sinks);
+        w.scale = static_cast<float>(scale);
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(w.dev));
+        const Tensor out = empty(w.q.sizes(), w.q.scalar_type(), w.dev);
+        const Tensor lse = empty({w.B, w.Hq, w.Nq}, at::kFloat, w.dev);
+        Tensor ws;
+        if (const size_t size = w.fwd_size()) ws = empty({static_cast<int64_t>(size)}, at::kByte, w.dev);
+        if (const int rc = w.fwd(out, lse, ws)) throw Refused{rc};
+        ctx->save_for_backward({w.q, w.k, w.v, out, lse});
+        ctx->saved_data["window"] = window;
+        ctx->saved_data["sinks"] = sinks;
+        ctx->saved_data["scale"] = scale;
+        return out;
     }
-    return r;
+    static torch::autograd::variable_list backward(Context* ctx, torch::autograd::variable_list grads) {
+        check_captured_backward();
+        const auto saved = ctx->get_saved_variables();
+        Window w;
+        TORCH_CHECK(w.read(saved[0], saved[1], saved[2]), "attn_bwd_window: the saved tensors changed");
+        w.window = static_cast<int>(ctx->saved_data["window"].toInt());
+        w.sinks = static_cast<int>(ctx->saved_data["sinks"].toInt());
+        w.scale = static_cast<float>(ctx->saved_data["scale"].toDouble());
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(w.dev));
+        const Tensor dout = grads[0].contiguous();
+        const auto type = w.q.scalar_type();
+        TORCH_CHECK(fits(dout, w.dev, type, w.q.sizes()) && fits(saved[3], w.dev, type, w.q.sizes()) &&
+                        fits(saved[4], w.dev, at::kFloat, {w.B, w.Hq, w.Nq}),
+                    "attn_bwd_window: arguments do not fit together");
+        const Tensor g[3] = {empty(w.q.sizes(), type, w.dev), empty(w.k.sizes(), type, w.dev),
+                             empty(w.k.sizes(), type, w.dev)};
+        const Tensor ws = empty({static_cast<int64_t>(std::max<size_t>(w.bwd_size(), 16))}, at::kByte, w.dev);
+        const int rc = w.bwd(saved[3], dout, saved[4], g, ws);
+        TORCH_CHECK(rc == ATTN_OK, "attn_bwd_window failed with status ", rc);
+        return {g[0], g[1], g[2], Tensor(), Tensor(), Tensor()};
+    }
+};
+
+// (q, k, v, window, sinks, scale) -> out or rc; differentiable
+PyObject* py_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    int window, sinks;
+    float scale;
+    const Tensor q = n == 6 ? tensor(a[0]) : Tensor();
+    if (!q.defined() || q.dim() != 4 || !count(a[3], &window) || !count(a[4], &sinks) ||
+        !scale_of(a[5], q.size(3), &scale))
+        MISFIT();
+    const Tensor k = tensor(a[1]), v = tensor(a[2]);
+    if (!k.defined() || !v.defined()) MISFIT();
+    Tensor out;
+    const int rc = unlocked([&] {
+        try {
+            out = WindowAttention::apply(q, k, v, window, sinks, scale);
+        } catch (const Refused& r) {
+            return r.rc;
+        }
+        return static_cast<int>(ATTN_OK);
+    });
+    return rc == ATTN_OK ? THPVariable_Wrap(out) : PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
 
@@ -481,7 +568,7 @@ PyMethodDef methods[] = {METHOD("init", py_init),
                          METHOD("kvp_compact", py_compact),
                          METHOD("attn_fwd_window", py_fwd),
                          METHOD("attn_bwd_window", py_bwd),
-                         METHOD("streams_above", py_streams_above),
+                         METHOD("window_attention", py_window),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -35,9 +35,9 @@ __device__ __forceinline__ bool window_edge(int key0, int last, int min_pos, int
     return last > min_pos || (key0 <= max_pos - window && last >= sinks);
 }
 
-// Keys [0, lim) that lie above `low` (in the window) or below `sinks`.
-__device__ __forceinline__ bool window_sees(int key, int lim, int low, int sinks) {
-    return key < lim && (key > low || key < sinks);
+// Bits [0, n) of 32.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
 }  // namespace tme

@@ -81,25 +81,6 @@ class _TiledAttention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
-class _WindowAttention(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, v, window, sinks, scale):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        out, lse = _lib.attn_fwd_window(q, k, v, window, sinks, scale=scale)
-        ctx.save_for_backward(q, k, v, out, lse)
-        ctx.window, ctx.sinks, ctx.scale = window, sinks, scale
-        return out
-
-    @staticmethod
-    def backward(ctx, dout):
-        q, k, v, out, lse = ctx.saved_tensors
-        if torch.cuda.is_current_stream_capturing():
-            _lib.check_captured_backward(dout.device)
-        dq, dk, dv = _lib.attn_bwd_window(q, k, v, out, dout.contiguous(), lse, ctx.window,
-                                          ctx.sinks, scale=ctx.scale)
-        return dq, dk, dv, None, None, None
-
-
 def _validate(q, k, v):
     for name, t in (("query", q), ("key", k), ("value", v)):
         if not isinstance(t, torch.Tensor):
@@ -145,7 +126,7 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
         raise ValueError(f"window must be >= 1 and sinks >= 0, got {window} and {sinks}")
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    return _WindowAttention.apply(q, k, v, int(window), int(sinks), float(scale))
+    return _lib.window_attention(q, k, v, int(window), int(sinks), float(scale))
 
 
 def scaled_dot_product_attention(query, key, value, attn_mask=None, dropout_p=0.0,
