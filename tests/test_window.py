@@ -4,6 +4,7 @@ sdpa.window_attention) against the fp64 definition, and its refusals.
 Tolerances are those of the other forwards and backwards (tests/helpers.py):
 the kernels are the same but for the key tiles they visit and the mask of the
 edge tiles."""
+import numpy as np
 import pytest
 import torch
 
@@ -116,11 +117,28 @@ CASES = [
     (4, 8, 8, 1000, 1000, 64, F16, 130, 4),         # more key tiles than CTAs: each takes several
     (4, 8, 8, 300, 1500, 128, BF16, 200, 3),        # and most of them no query sees
     (5, 8, 8, 700, 700, 128, F16, 700, 0),
+    (5, 8, 8, 1000, 1000, 128, BF16, 200, 130),     # D = 128 in more than a wave of Q tile pairs
+    (6, 8, 4, 900, 2100, 128, F16, 300, 0),
+    (8, 8, 8, 1100, 1100, 128, F16, 64, 1),         # pairs with one Q tile, several a CTA
+    (3, 20, 4, 1025, 1025, 128, BF16, 129, 0),
 ]
 
 
 def _inputs(B, Hq, Hkv, Nq, Nk, D, dtype, window, sinks):
     return inputs.make_custom(B, Hq, Hkv, Nq, Nk, D, dtype, seed=7 * Nq + window, with_grad=True)
+
+
+def _assert_gradient(got, ref, dtype, what, name):
+    """The gradient before its store lies within TOL_BWD of the definition, as the other
+    backwards' do; the store rounds it by half a step more: |got - ref| <= |x - ref| +
+    |round(x) - x| <= TOL_BWD + step / 2.  (At 4 to 8 half a bf16 step is 2^-6 = 0.0156 of
+    the flat 0.02, which leaves 0.0044 for sums over a group of five heads.)"""
+    assert np.all(np.isfinite(got)), f"{what}: non-finite {name}"
+    err = np.abs(got - ref)
+    # a step of the binade above ref's, where x may lie
+    bound = helpers.TOL_BWD[dtype] + 0.5 * helpers.ulp(np.abs(ref) + helpers.TOL_BWD[dtype], dtype)
+    worst = np.unravel_index(np.argmax(err - bound), err.shape)
+    assert np.all(err <= bound), f"{what}: {name} off by {err[worst]:.3e} > {bound[worst]:.3e} at {ref[worst]:.3f}"
 
 
 @pytest.mark.gpu
@@ -137,8 +155,33 @@ def test_forward_and_backward_match_the_definition(cuda_lib, case):
     helpers.assert_fwd_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref[0], ref[1],
                              dtype, what)
     for name, g, r in zip(("dq", "dk", "dv"), grads, ref[2:]):
-        helpers.assert_close_elementwise(g.double().cpu().numpy(), r, helpers.TOL_BWD[dtype], dtype,
-                                         what, name)
+        _assert_gradient(g.double().cpu().numpy(), r, dtype, what, name)
+
+
+@pytest.mark.gpu
+def test_wide_bf16_values(cuda_lib):
+    """Value tiles past fp16's range stay bf16, and P beside them; the other heads' do not."""
+    B, H, N, D = 5, 8, 1000, 128
+    x = inputs.make_custom(B, H, H, N, N, D, BF16, seed=50)
+    v = x["v"].clone()
+    v[1, 3, 400:410] *= 2.0 ** 20
+    v[4, 7] *= 2.0 ** -12
+    q, k = x["q"].cuda(), x["k"].cuda()
+    out, lse = _lib.attn_fwd_window(q, k, v.cuda(), 150, 2)
+    assert _lib.sync_status() == _lib.ATTN_OK
+    plain, plain_lse = _lib.attn_fwd_window(q, k, x["v"].cuda(), 150, 2)
+    ro, rl = window_ref.attention(x["q"], x["k"], v, 150, 2)
+    assert torch.equal(lse, plain_lse)
+    out = out.double().cpu()
+    # bf16 P and output: 2^-9 of a term and of the result each (half a step of 8 bits), of
+    # at most the largest value in sight
+    for b, h in ((1, 3), (4, 7)):
+        size = float(v[b, h].double().abs().max())
+        assert float((out[b, h] - ro[b, h]).abs().max()) <= size * (2.0 ** -8 + 2.0 ** -8), (b, h)
+    out[1, 3] = out[4, 7] = 0
+    plain = plain.double().cpu()
+    plain[1, 3] = plain[4, 7] = 0
+    assert torch.equal(out, plain)
 
 
 @pytest.mark.gpu

@@ -652,11 +652,11 @@ __device__ __forceinline__ WindowUnit window_unit(const BwdParams& p, int idx) {
     w.region = idx >= n_sink ? 1 : 0;
     const unsigned splits = p.wr[w.region].splits;
     const unsigned at = idx - (w.region ? n_sink : 0);
-    const unsigned tiles = w.region ? p.n_ktiles - p.n_sink_tiles : p.n_sink_tiles;
-    const unsigned unit = at / splits;
+    const unsigned unit = at / splits, groups = p.n_groups;
     w.sp = static_cast<int>(at % splits);
-    w.group = static_cast<int>(unit / tiles);
-    w.key0 = static_cast<int>(unit % tiles + (w.region ? p.n_sink_tiles : 0)) * kRows;
+    // the same key tile of every group, then the next: the last ones meet fewer queries
+    w.group = static_cast<int>(unit % groups);
+    w.key0 = static_cast<int>(unit / groups + (w.region ? p.n_sink_tiles : 0)) * kRows;
     // positions of a head that see some key of the tile
     const int i_min = max(0, w.key0 - p.causal_off);
     int64_t i_max = p.Nq - 1;
@@ -1487,8 +1487,12 @@ struct WindowRows {
 
 __device__ __forceinline__ WindowRows window_rows(const BwdParams& p, int idx) {
     WindowRows w;
-    w.head = static_cast<int>(static_cast<unsigned>(idx) / static_cast<unsigned>(p.n_qtiles));
-    w.row0 = (p.n_qtiles - 1 - (idx - w.head * p.n_qtiles)) * kRows;
+    // The same tile of every head, then the one before it: the first positions of a head
+    // have shorter lists, and a CTA's turn with them comes last.
+    const int heads = p.n_groups * p.G;
+    const int from_end = static_cast<int>(static_cast<unsigned>(idx) / static_cast<unsigned>(heads));
+    w.head = idx - from_end * heads;
+    w.row0 = (p.n_qtiles - 1 - from_end) * kRows;
     const KeyList kl = key_list(w.row0 + p.causal_off, p.window, p.sinks);
     const int keys = min(w.row0 + kRows, p.Nq) + p.causal_off;
     w.n_sink = kl.n_sink;

@@ -1182,6 +1182,420 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     }
 }
 
+// ------------------------------------------------ sliding window, D = 128, long grids
+// The products, TMEM layout and softmax of attn_fwd_kernel at D = 128 (P over S, one MMA
+// issuer, one thread per row), for grids of a wave or more with one query head per group.  A
+// pair of Q tiles meets a window's key tiles only, so what a CTA does once per pair
+// counts: set-up, first loads, and each tile's epilogue with the other tile at work
+// took a third of the time.  A CTA takes pairs in turn (units) and its roles run
+// through them without a break, as in the backward's window kernels: the next pair's first
+// scores are computed before this pair's last product, and its first softmax runs
+// before this pair's output is written.  A key tile that lies before every window of the
+// second Q tile (the first one past the sinks, as a rule) is left out for it.
+// bf16: V comes from the workspace's fp16 copy unless one of the unit's value tiles
+// had to stay bf16 (vconv.cu).
+struct WindowPair {
+    int n0, n1;         // steps of the unit's key list that Q tile 0, 1 run to (n1 = 0: no rows)
+    int x1;             // a step that Q tile 1 leaves out (-1: none)
+    int row0, head;     // first row within the query head, the head of all batches
+    int n_sink, skip;   // KeyList
+    int v16;            // V is read as fp16
+};
+constexpr int kPairSlots = 4;   // a unit is read until its output is written
+
+__device__ __forceinline__ WindowPair window_pair(const FwdParams& p, int idx) {
+    WindowPair w;
+    // The same pair of every head, then the one before it: the first positions of a head
+    // have shorter lists, and a CTA's turn with them comes last.
+    const int from_end = static_cast<int>(static_cast<unsigned>(idx) / static_cast<unsigned>(p.n_groups));
+    w.head = idx - from_end * p.n_groups;
+    w.row0 = (p.n_pairs - 1 - from_end) * (2 * kRows);
+    const KeyList kl = key_list(w.row0 + p.causal_off, p.window, p.sinks);
+    w.n_sink = kl.n_sink;
+    w.skip = kl.skip;
+    auto steps = [&](int row0) {
+        return row0 < p.Nq ? (min(row0 + kRows, p.Nq) + p.causal_off + kRows - 1) / kRows - kl.skip : 0;
+    };
+    w.n0 = steps(w.row0);
+    w.n1 = steps(w.row0 + kRows);
+    // first tile of a window of Q tile 0 and of Q tile 1
+    const int lo0 = max(w.row0 + p.causal_off - p.window + 1, 0) / kRows;
+    const int lo1 = max(w.row0 + kRows + p.causal_off - p.window + 1, 0) / kRows;
+    w.x1 = lo1 > lo0 && (p.sinks + kRows - 1) / kRows <= lo0 ? kl.n_sink : -1;
+    w.v16 = 1;
+    return w;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(384, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmV16, const FwdParams p) {
+    constexpr int D = 128, KS = 2, VS = 3, KB = 2, TB = kRows * D * 2;
+    constexpr int kMmaWarp = 9, kProducerWarp = 11;   // 0-7 softmax; 8 and 10 only end
+    extern __shared__ __align__(1024) uint8_t smem_w[];
+    uint8_t* sQ = smem_w;                // [2]
+    uint8_t* sK = sQ + 2 * TB;           // [KS]
+    uint8_t* sV = sK + KS * TB;          // [VS]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + VS * TB);
+    uint64_t* q_full = bars;             // [2] a unit's numbers and Q tile t
+    uint64_t* q_empty = q_full + 2;      // [2] read: by tile t's 4 warps, by its last scores
+    uint64_t* k_full = q_empty + 2;      // [KS]
+    uint64_t* k_empty = k_full + KS;     // [KS][2]: tile t is done with the step's K (or left it out)
+    uint64_t* v_full = k_empty + 2 * KS; // [VS]
+    uint64_t* v_empty = v_full + VS;     // [VS][2]
+    uint64_t* s_full = v_empty + 2 * VS; // [2] S_t in TMEM
+    uint64_t* p_full = s_full + 2;       // [2] P_t in TMEM and O_t rescaled (128 arrivals)
+    uint64_t* o_full = p_full + 2;       // [2] a unit's last PV of tile t done
+    uint64_t* o_empty = o_full + 2;      // [2] its O_t read (128 arrivals)
+    uint64_t* mma_done = o_empty + 2;
+    WindowPair* units = reinterpret_cast<WindowPair*>(mma_done + 1);   // [kPairSlots]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + kPairSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int total = p.n_groups * p.n_pairs;
+    const int n_units = (total - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < KS; ++i) mbar_init(&k_full[i], 1);
+        for (int i = 0; i < 2 * KS; ++i) mbar_init(&k_empty[i], 1);
+        for (int i = 0; i < VS; ++i) mbar_init(&v_full[i], 1);
+        for (int i = 0; i < 2 * VS; ++i) mbar_init(&v_empty[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&q_empty[t], 1 + 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 128);
+            mbar_init(&o_full[t], 1);
+            mbar_init(&o_empty[t], 128);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            if constexpr (BF16) tma_prefetch_desc(&tmV16);
+            int nk = 0, nv = 0, nq[2] = {0, 0};   // K tiles, V tiles, units asked for
+            bool ok = true;
+            for (int k = 0; k < n_units && ok; ++k) {
+                WindowPair w = window_pair(p, static_cast<int>(blockIdx.x + k * gridDim.x));
+                const int kv_group = w.head / p.kv_div, steps = max(w.n0, w.n1);
+                KeyList kl;
+                kl.n_sink = w.n_sink;
+                kl.skip = w.skip;
+                for (int kb = 0; kb < KB; ++kb) {
+                    tma_prefetch_3d(&tmQ, kb * 64, w.row0, w.head);
+                    if (w.n1 > 0) tma_prefetch_3d(&tmQ, kb * 64, w.row0 + kRows, w.head);
+                }
+                if constexpr (BF16) {
+                    const uint8_t* fl = p.vflags + static_cast<int64_t>(kv_group) * p.n_ktiles;
+                    uint32_t wide = 0u;
+#pragma unroll 16
+                    for (int i = 0; i < steps; ++i) wide |= fl[kl.tile(i)];
+                    w.v16 = wide == 0u ? 1 : 0;
+                }
+                const CUtensorMap* mv = BF16 && w.v16 ? &tmV16 : &tmV;
+                auto load_kv = [&](int key0) {
+                    const int ks = nk % KS, vs = nv % VS;
+                    const uint32_t kph = ((nk / KS) & 1) ^ 1, vph = ((nv / VS) & 1) ^ 1;
+                    ok = mbar_wait(&k_empty[2 * ks], kph, abort_flag, p.status) &&
+                         mbar_wait(&k_empty[2 * ks + 1], kph, abort_flag, p.status);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(&k_full[ks], TB);
+                    for (int kb = 0; kb < KB; ++kb)
+                        tma_load_3d(&tmK, &k_full[ks], sK + ks * TB + kb * (kRows * 128), kb * 64, key0,
+                                    kv_group);
+                    ++nk;
+                    ok = mbar_wait(&v_empty[2 * vs], vph, abort_flag, p.status) &&
+                         mbar_wait(&v_empty[2 * vs + 1], vph, abort_flag, p.status);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(&v_full[vs], TB);
+                    for (int kb = 0; kb < KB; ++kb)
+                        tma_load_3d(mv, &v_full[vs], sV + vs * TB + kb * (kRows * 128), kb * 64, key0,
+                                    kv_group);
+                    ++nv;
+                };
+                load_kv(kl.tile(0) * kRows);
+                if (ok && k > 0) ok = mbar_wait(&q_empty[0], (k - 1) & 1, abort_flag, p.status);
+                if (!ok) break;
+                units[k % kPairSlots] = w;
+                mbar_arrive_expect_tx(&q_full[0], TB);
+                for (int kb = 0; kb < KB; ++kb)
+                    tma_load_3d(&tmQ, &q_full[0], sQ + kb * (kRows * 128), kb * 64, w.row0, w.head);
+                ++nq[0];
+                if (k > 0) ok = mbar_wait(&q_empty[1], (k - 1) & 1, abort_flag, p.status);
+                if (!ok) break;
+                if (w.n1 > 0) {
+                    mbar_arrive_expect_tx(&q_full[1], TB);
+                    for (int kb = 0; kb < KB; ++kb)
+                        tma_load_3d(&tmQ, &q_full[1], sQ + TB + kb * (kRows * 128), kb * 64,
+                                    w.row0 + kRows, w.head);
+                } else {
+                    mbar_arrive(&q_full[1]);
+                }
+                ++nq[1];
+                for (int j = 1; j < steps && ok; ++j) load_kv(kl.tile(j) * kRows);
+            }
+            // Never leave a copy in flight into shared memory we are about to give up.
+            if (nq[0] > 0) mbar_wait_bounded(&q_full[0], (nq[0] - 1) & 1, p.status);
+            if (nq[1] > 0) mbar_wait_bounded(&q_full[1], (nq[1] - 1) & 1, p.status);
+            for (int n = (nk > KS ? nk - KS : 0); n < nk; ++n)
+                mbar_wait_bounded(&k_full[n % KS], (n / KS) & 1, p.status);
+            for (int n = (nv > VS ? nv - VS : 0); n < nv; ++n)
+                mbar_wait_bounded(&v_full[n % VS], (n / VS) & 1, p.status);
+        }
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = idesc_f16(kRows, kRows, BF16, false);
+        constexpr uint32_t idesc_o = idesc_f16(kRows, D, BF16, true);
+        constexpr uint32_t idesc_o16 = idesc_f16(kRows, D, false, true);
+        constexpr uint64_t kStep = TB >> 4;
+        constexpr uint64_t kBlk = (kRows * 128) >> 4;
+        const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), kRows * 128, 1024);
+        // Steps are counted over all units (g).  S_t = Q_t K_g^T; `last` of the unit for tile t.
+        auto issue_s = [&](int t, int g, bool last) {
+            const int ks = g % KS;
+            warp_wait(&k_full[ks], (g / KS) & 1, abort_flag, p.status);
+            tc_fence_after();
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+                mma_ss_k64(tmem + t * kRows, dq0 + t * kStep + kb * kBlk, dk0 + ks * kStep + kb * kBlk,
+                           idesc_s, kb > 0 ? 1u : 0u);
+            mma_commit_elect(&s_full[t]);
+            mma_commit_elect(&k_empty[2 * ks + t]);
+            if (last) mma_commit_elect(&q_empty[t]);
+        };
+        int n_p[2] = {0, 0}, n_o[2] = {0, 0};   // steps and units run so far, per tile
+        // O_t (+)= P_t V_g; `first`, `last` of the unit for tile t.
+        auto issue_pv = [&](int t, int g, bool first, bool last, uint32_t idesc) {
+            const int vs = g % VS;
+            warp_wait(&v_full[vs], (g / VS) & 1, abort_flag, p.status);
+            warp_wait(&p_full[t], (t ? n_p[1] : n_p[0]) & 1, abort_flag, p.status);
+            const int units_before = t ? n_o[1] : n_o[0];
+            if (first && units_before > 0)   // it overwrites the O of the unit before
+                warp_wait(&o_empty[t], (units_before - 1) & 1, abort_flag, p.status);
+            tc_fence_after();
+            mma_ts_k128(tmem + 256 + t * D, tmem + t * kRows, dv0 + vs * kStep, idesc, first ? 0u : 1u);
+            mma_commit_elect(&v_empty[2 * vs + t]);
+            if (last) mma_commit_elect(&o_full[t]);
+            if (t) {
+                ++n_p[1];
+                n_o[1] += last ? 1 : 0;
+            } else {
+                ++n_p[0];
+                n_o[0] += last ? 1 : 0;
+            }
+        };
+        int g0 = 0;           // steps of the units before
+        bool ahead = false;   // S_0 of this unit's first step is issued
+        for (int k = 0; k < n_units; ++k) {
+            if (!warp_wait(&q_full[0], k & 1, abort_flag, p.status)) break;
+            const WindowPair w = units[k % kPairSlots];
+            const int steps = max(w.n0, w.n1);
+            const uint32_t idesc = BF16 && w.v16 ? idesc_o16 : idesc_o;
+            auto next1 = [&](int j) { return j + 1 == w.x1 ? j + 2 : j + 1; };   // tile 1's step after j
+            const int first1 = next1(-1);
+            if (!ahead) issue_s(0, g0, w.n0 == 1);
+            ahead = false;
+            warp_wait(&q_full[1], k & 1, abort_flag, p.status);
+            if (w.n1 > 0) issue_s(1, g0 + first1, next1(first1) >= w.n1);
+            else mma_commit_elect(&q_empty[1]);
+            for (int j = 0; j < steps; ++j) {
+                const int g = g0 + j, ks = g % KS, vs = g % VS;
+                if (j < w.n0) {
+                    issue_pv(0, g, j == 0, j + 1 == w.n0, idesc);
+                    if (j + 1 < w.n0) issue_s(0, g + 1, j + 2 == w.n0);
+                } else {
+                    mma_commit_elect(&k_empty[2 * ks]);
+                    mma_commit_elect(&v_empty[2 * vs]);
+                    // Tile 0 has no step here: its first scores of the next unit
+                    if (j + 1 == steps && k + 1 < n_units &&
+                        warp_wait(&q_full[0], (k + 1) & 1, abort_flag, p.status)) {
+                        const int n = *static_cast<const volatile int*>(&units[(k + 1) % kPairSlots].n0);
+                        issue_s(0, g + 1, n == 1);
+                        ahead = true;
+                    }
+                }
+                if (j < w.n1 && j != w.x1) {
+                    const int nx = next1(j);
+                    issue_pv(1, g, j == first1, nx >= w.n1, idesc);
+                    if (nx < w.n1) issue_s(1, g0 + nx, next1(nx) >= w.n1);
+                } else {
+                    mma_commit_elect(&k_empty[2 * ks + 1]);
+                    mma_commit_elect(&v_empty[2 * vs + 1]);
+                }
+            }
+            g0 += steps;
+        }
+        mma_commit_elect(mma_done);
+        mbar_wait_bounded(mma_done, 0, p.status);
+    } else if (warp < 8) {
+        // One thread per row of Q tile t.
+        const int t = warp >> 2, quad = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_base + t * kRows, tO = tmem + lane_base + 256 + t * D;
+        const float sl2 = p.scale_log2;
+        const uint64_t sl22 = f2(sl2, sl2);
+        int n = 0, n_out = 0;      // steps, and units written, so far
+        float inv_before = 0.0f;   // 1 / normaliser of the unit whose O is not written yet
+        int before = -1;           // and that unit (-1: none)
+        for (int k = 0; k <= n_units; ++k) {   // (the last turn only writes)
+            int n_t = 0, x = -1, n_sink = 0, skip = 0, row0 = 0, head = 0;
+            bool p_bf16 = false;
+            if (k < n_units) {
+                if (!warp_wait(&q_full[t], k & 1, abort_flag, p.status)) break;
+                const WindowPair& w = units[k % kPairSlots];
+                n_t = t ? w.n1 : w.n0;
+                x = t ? w.x1 : -1;
+                n_sink = w.n_sink;
+                skip = w.skip;
+                row0 = w.row0 + t * kRows + quad * 32;
+                head = w.head;
+                p_bf16 = BF16 && w.v16 == 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_empty[t]);
+            }
+            const int min_pos = row0 + p.causal_off, max_pos = min(min_pos + 31, p.Nk - 1);
+            float m = -INFINITY;  // running max (log2 domain, scaled) used for exponentiation
+            float l = 0.0f;       // running sum of p (gives the LSE)
+            float lres = 0.0f;    // running sum of the rounding residuals of the tile maxima
+            bool first = true;
+            int j = 0;
+            do {
+                if (j < n_t && j != x) {
+                    const int key0 = (j < n_sink ? j : j + skip) * kRows;
+                    warp_wait(&s_full[t], n & 1, abort_flag, p.status);
+                    tc_fence_after();
+                    // what the mask hides, in place in TMEM (attn_fwd_kernel)
+                    if (window_edge(key0, key0 + kRows - 1, min_pos, max_pos, p.window, p.sinks)) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            const int k0 = key0 + 32 * c;
+                            if (!window_edge(k0, k0 + 31, min_pos, max_pos, p.window, p.sinks)) continue;
+                            uint32_t y[32];
+                            tmem_ld32(tS + c * 32, y);
+                            tmem_wait_ld();
+                            reg_fence(y);
+                            window_mask32(y, k0, min_pos + lane, min_pos, max_pos, p);
+                            tmem_st32(tS + c * 32, y);
+                        }
+                        tmem_wait_st();
+                    }
+                    uint32_t sr[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) reg_fence(sr[c]);
+                    const float mx = row_max128(sr);
+                    const float m_new = fmaxf(m, mx * sl2);
+                    const bool need = m_new > m + kRescaleThreshold;
+                    const float alpha = need ? ex2_ftz(m - m_new) : 1.0f;   // (used when need)
+                    m = need ? m_new : m;
+                    const float m_sub = (m == -INFINITY) ? 0.0f : m;
+                    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+                    const uint64_t nm2 = f2(-m_sub, -m_sub);
+                    float rtop;
+                    if (BF16 && p_bf16) {
+                        rtop = round16_residual<true>(mx, sl2, -m_sub);
+                        pack_p128<true>(sr, tS, sl22, nm2, acc2);
+                    } else {
+                        rtop = round16_residual<false>(mx, sl2, -m_sub);
+                        pack_p128<false>(sr, tS, sl22, nm2, acc2);
+                    }
+                    const uint64_t a2 = fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3]));
+                    const float rs = f2lo(a2) + f2hi(a2);
+                    lres = lres * alpha + rtop;
+                    // The product before is complete: this S was committed after it.
+                    if (!first && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c * 32, o);
+                            tmem_wait_ld();
+                            reg_fence(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + c * 32, o);
+                        }
+                    }
+                    l = l * alpha + rs;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[t]);
+                    ++n;
+                    first = false;
+                }
+                if (before >= 0 && (!first || n_t == 0)) {
+                    // O of the unit before
+                    warp_wait(&o_full[t], n_out & 1, abort_flag, p.status);
+                    ++n_out;
+                    tc_fence_after();
+                    const WindowPair& w = units[before % kPairSlots];
+                    const int row = w.row0 + t * kRows + quad * 32 + lane;
+                    const int64_t grow = static_cast<int64_t>(w.head) * p.Nq + row;
+                    const bool write = *abort_flag == 0 && row < p.Nq;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c * 32, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+                        if (c == D / 32 - 1) {
+                            tc_fence_before();
+                            mbar_arrive(&o_empty[t]);
+                        }
+                        if (write) store_o32<D, BF16>(p, -1, grow, c, o, inv_before);
+                    }
+                    before = -1;
+                }
+            } while (++j < n_t);
+            if (n_t > 0) {
+                // O is normalised by the sum of p plus the residuals of the tile
+                // maxima; the LSE uses the sum of p alone.
+                const float l_out = l + lres;
+                inv_before = l_out > 0.0f ? 1.0f / l_out : 0.0f;
+                before = k;
+                const float m_sub = (m == -INFINITY) ? 0.0f : m;
+                if (row0 + lane < p.Nq && *abort_flag == 0)
+                    p.lse[static_cast<int64_t>(head) * p.Nq + row0 + lane] =
+                        l > 0.0f ? (m_sub + lg2_approx(l)) * kLn2 : -INFINITY;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool BF16>
+cudaError_t launch_window(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          const CUtensorMap& tmV16, const FwdParams& p, int ctas, cudaStream_t stream) {
+    auto kern = window_fwd_kernel<BF16>;
+    constexpr int smem = 7 * kRows * 128 * 2 + 512;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(384), smem, stream, tmQ, tmK, tmV,
+                         tmV16, p);
+}
+
 template <int D, bool BF16, bool CAUSAL, int MK, bool VPRE>
 cudaError_t launch_one(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmV16, const FwdParams& p, cudaStream_t stream) {
@@ -1201,6 +1615,13 @@ cudaError_t launch_one(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
 }
 
 }  // namespace
+
+cudaError_t launch_fwd_window_long(bool bf16, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                   const CUtensorMap& tmV, const FwdParams& p, int ctas,
+                                   cudaStream_t stream, const CUtensorMap* tmV16) {
+    return bf16 ? launch_window<true>(tmQ, tmK, tmV, *tmV16, p, ctas, stream)
+                : launch_window<false>(tmQ, tmK, tmV, tmV, p, ctas, stream);
+}
 
 cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const FwdParams& p,
@@ -1223,9 +1644,8 @@ cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
     if (tmV16 != nullptr) {
         if (!bf16 || (mk != 0 && mk != 3) || p.vflags == nullptr) return cudaErrorInvalidValue;
         if (mk == 3)
-            return D == 64    ? launch_one<64, true, true, 3, true>(tmQ, tmK, tmV, *tmV16, p, stream)
-                   : D == 128 ? launch_one<128, true, true, 3, true>(tmQ, tmK, tmV, *tmV16, p, stream)
-                              : cudaErrorInvalidValue;
+            return D == 64 ? launch_one<64, true, true, 3, true>(tmQ, tmK, tmV, *tmV16, p, stream)
+                           : cudaErrorInvalidValue;
         if (D == 64 && !causal) return launch_one<64, true, false, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);
         if (D == 64 && causal) return launch_one<64, true, true, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);
         if (D == 128 && !causal) return launch_one<128, true, false, 0, true>(tmQ, tmK, tmV, *tmV16, p, stream);

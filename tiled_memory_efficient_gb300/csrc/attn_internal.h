@@ -117,6 +117,12 @@ cudaError_t launch_fwd(int D, bool bf16, bool causal, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const FwdParams& p,
                        cudaStream_t stream, const CUtensorMap* tmV16 = nullptr);
 
+// A sliding window at D = 128 with one query head per group, `ctas` CTAs that take pairs of
+// Q tiles in turn (bf16: tmV16 and p.vflags are given).
+cudaError_t launch_fwd_window_long(bool bf16, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                   const CUtensorMap& tmV, const FwdParams& p, int ctas,
+                                   cudaStream_t stream, const CUtensorMap* tmV16);
+
 // Writes the fp16 copy of a bf16 value tensor [groups][Nk][D] and one flag
 // byte per (group, 128-key tile) (vconv.cu).  Key tiles [skip0, skip1) are left
 // out (those a sliding window never visits).
