@@ -622,9 +622,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 // ---------------------------------------------------------------- dK/dV, sliding window
 // The same products and TMEM layout as bwd_dkdv_kernel.  What differs is that a key
 // tile meets a window's query tiles only (9 of each head at a window of 1024), so
-// whatever a CTA does once per key tile counts: with one CTA per key tile or, in turn,
-// one key tile after the other, the gap between two cost as much as 3 of those 9
-// tiles.  Here a CTA takes units (key tile, query range) in turn and its three roles
+// whatever a CTA does once per key tile counts: with key tiles one after the other
+// the gap between two cost as much as 3 of those 9 tiles.  Here a CTA takes units (key tile, query range) in turn and its three roles
 // run through them without a break:
 //   - the producer works out the units (divisions) and leaves them in shared memory; it
 //     asks the next unit's K and V into the second-level cache and loads its first
@@ -637,6 +636,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 // A query range meets each of its key's visible queries as one run, so a thread's mask
 // of a 32-query chunk is an interval of bits; chunks that all 32 keys of a warp see
 // take the path without a mask.
+// Bound by the chain of a query half (its scores, 32 terms a thread, its products), which
+// runs beside the other half's: a query tile takes 4050 cycles, of which the tensor
+// core needs 3100, bf16's low-order product among them.  B=2 H=16 D=128 N=8192 bf16,
+// window 1024 and 4 sinks: 284 us (419 with a CTA to each key tile, 399 with key tiles in
+// turn), 911 TFLOP/s of the four products, the tensor pipe active 60% of the time.
 struct WindowUnit {
     int n;            // query tiles
     int pos, head;    // the first one: its first row within its head, the head within the group
@@ -1479,6 +1483,10 @@ __global__ void __launch_bounds__(dq_threads<MK, D>(), 1)
 // a third of its time.  As in bwd_window_dkdv_kernel a CTA takes query tiles in turn
 // and its roles run through them without a break; the next one's first S and dP
 // are computed before this one's last dQ product.
+// Bound by the tensor core and the chain of S, dP, dS beside it (a key tile takes 2050
+// cycles, its products 1540).  B=2 H=16 D=128 N=8192 bf16, window 1024 and 4 sinks: 169
+// us (226 with a CTA to each query tile), 1150 TFLOP/s of the three products, the tensor
+// pipe active 63% of the time.
 struct WindowRows {
     int n;               // key tiles
     int row0, head;      // first row within the query head, the head of all batches
@@ -1872,7 +1880,8 @@ cudaError_t launch_dq(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUte
     return launch_dependent(kern, ctas, dq_threads<MK, D>(), smem, stream, tmQ, tmDO, tmK, tmV, p);
 }
 
-// The same sums for a sliding window's backward: regions of keys with their own
+// The same sums for a sliding window's backward (bound by memory; the sink tile's ranges
+// of the case above: 10 us): regions of keys with their own
 // numbers of ranges (BwdParams::wr), n8[r] = 8-element runs of region r that
 // have partials.
 template <int D, bool BF16>
