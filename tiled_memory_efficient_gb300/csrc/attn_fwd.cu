@@ -324,9 +324,10 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
     const bool one_head = WIN && p.rows_per_group == p.Nq;
     if (WIN) {
         // Units of equal work but for the first positions of a head (shorter
-        // lists): those last.  Consecutive CTAs share most of their key tiles.
-        group = unit / p.n_pairs;
-        pair = p.n_pairs - 1 - unit % p.n_pairs;
+        // lists): those last.  CTAs that run together share most of their key tiles.
+        pair = unit / p.n_groups;
+        group = unit - pair * p.n_groups;
+        pair = p.n_pairs - 1 - pair;
     } else if (CAUSAL && p.Nq % (2 * kRows) == 0) {
         const int m = p.Nq / (2 * kRows);        // pairs per head (n_pairs = G * m)
         const int heads = p.n_groups * p.G;      // (group, head) combinations
