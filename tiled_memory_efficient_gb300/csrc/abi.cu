@@ -618,7 +618,7 @@ int check_window(int Nq, int Nk, int window, int sinks) {
 
 // Bytes of the fp16 copy of V and its flags (bf16, long query blocks).  The copy is a
 // kernel before the forward: it pays where every value tile serves several CTAs
-// (B=2 H=16 D=128 N=8192, window 1024: 193 us with it, 205 without), not in a grid
+// (B=2 H=16 D=128 N=8192, window 1024, a CTA per pair: 193 us with it, 205 without), not in a grid
 // under one wave (501 queries of 16 heads, window 2000: 31.5 us with, 29.1 without).
 size_t window_v_bytes(const WindowPlan& w, int B, int Hkv, int Nk, int D, int dtype) {
     if (dtype != ATTN_BF16 || !w.per_head || w.under_wave) return 0;
@@ -986,7 +986,8 @@ namespace {
 // tile's work (its CTAs would otherwise outlast the grid).  The others are cut
 // into the number of ranges that gives the shortest grid: waves of CTAs, each of
 // its query tiles and kWindowCtaTiles more (set-up, the first loads, the
-// epilogue).  Ranges hold at least kWindowMinTiles query tiles.
+// epilogue: 12:3 heads, B=2 N=3000 D=64, window 700, 118 us with 3 tiles for them, 126
+// with 1 or 2).  Ranges hold at least kWindowMinTiles query tiles.
 struct WindowBwdPlan {
     int64_t n_qtiles = 0, n_ktiles = 0;
     int sink_tiles = 0;
