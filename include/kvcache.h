@@ -55,11 +55,26 @@ extern "C" {
  * values exactly except those that become subnormal.  Values round to nearest
  * even; infinities are stored as the largest magnitude, NaN as NaN.  Rows past
  * the last token are left as they were.
+ *
+ * lens has to hold the tokens: after a kvp_reserve that found no room it does
+ * not, and the same n_new would be written over the newest ones.  Look at its
+ * info[0] first, or use kv8_append_step.
  */
 int kv8_append(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale,
                float* v_scale, const int* table, const int* lens, const int* n_new, int B,
                int Hkv, int T, int D, int page, int n_pages, int max_pages, long long stride_b,
                long long stride_h, long long stride_t, int dtype, void* stream);
+
+/*
+ * kv8_append for a step that no host looks at: granted (one int32 on the device,
+ * written by kvp_reserve_step; NULL: 1) is 0 when the step was given no room,
+ * and nothing is read or written then.
+ */
+int kv8_append_step(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale,
+                    float* v_scale, const int* table, const int* lens, const int* n_new,
+                    const int* granted, int B, int Hkv, int T, int D, int page, int n_pages,
+                    int max_pages, long long stride_b, long long stride_h, long long stride_t,
+                    int dtype, void* stream);
 
 /*
  * Attention of the newest Nq positions of every sequence over its cache:
@@ -118,6 +133,14 @@ int kv8_copy_pages(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
 int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, int n_seqs, int max_pages,
                 int n_pages, int page, int window, int sinks, int* info, void* workspace,
                 size_t workspace_bytes, void* stream);
+
+/*
+ * kvp_reserve that also writes info[0] to granted (one int32 on the device, or
+ * NULL), which no other call writes: the step's appends and attention read it.
+ */
+int kvp_reserve_step(int* table, int* lens, int* refs, const int* n_new, int n_seqs, int max_pages,
+                     int n_pages, int page, int window, int sinks, int* info, int* granted,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Gives every sequence the content of another, all at once: sequence c becomes

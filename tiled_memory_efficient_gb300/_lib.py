@@ -83,10 +83,12 @@ _SIGNATURES = {
     "ffn_check_chunking": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
                             ctypes.c_size_t, _i, _vp], _i),
     "kv8_append": ([_vp] * 9 + [_i] * 7 + [ctypes.c_longlong] * 3 + [_i, _vp], _i),
+    "kv8_append_step": ([_vp] * 10 + [_i] * 7 + [ctypes.c_longlong] * 3 + [_i, _vp], _i),
     "kv8_attn": ([_vp] * 10 + [ctypes.c_size_t] + [_i] * 8 + [ctypes.c_float, _i, _i, _i, _vp], _i),
     "kv8_attn_workspace_size": ([_i] * 5, ctypes.c_size_t),
     "kv8_copy_pages": ([_vp] * 7 + [_i] * 6 + [_vp], _i),
     "kvp_reserve": ([_vp] * 4 + [_i] * 6 + [_vp, _vp, ctypes.c_size_t, _vp], _i),
+    "kvp_reserve_step": ([_vp] * 4 + [_i] * 6 + [_vp] * 3 + [ctypes.c_size_t, _vp], _i),
     "kvp_reassign": ([_vp] * 4 + [_i] * 4 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
     "kvp_compact": ([_vp] * 4 + [_i] * 3 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
     "kvp_workspace_size": ([_i] * 3, ctypes.c_size_t),
@@ -354,8 +356,8 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
     return out, lse
 
 
-_BOUND = ("kv8_append", "kv8_attn", "kv8_attn_workspace_size", "kv8_copy_pages", "kvp_reserve",
-          "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
+_BOUND = ("kv8_append_step", "kv8_attn", "kv8_attn_workspace_size", "kv8_copy_pages",
+          "kvp_reserve_step", "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
           "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size")
 _bind = None
 
@@ -579,12 +581,20 @@ def _explain_table(table, lens, B, dev):
     _need("lens", lens, (B,), torch.int32, dev)
 
 
-def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None):
+def _need_word(name, t, dev):
+    import torch
+    if t is not None:
+        _need(name, t, (1,), torch.int32, dev)
+
+
+def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None, granted=None):
     """Quantises new keys and values [B, Hkv, T, D] (any strides that are multiples
     of 8 with dense rows) into the paged cache (include/kvcache.h).  lens [B] are
     the lengths after the call; n_new [B] how many of the T tokens each sequence
-    takes (None: all T)."""
-    rc = (_bind or _load_bind()).kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new)
+    takes (None: all T).  granted [1] (written by kvp_reserve): nothing is appended
+    where it is 0, since lens does not hold the tokens then."""
+    rc = (_bind or _load_bind()).kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new,
+                                            granted)
     if rc == ATTN_OK:
         return
 
@@ -602,6 +612,7 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
         _explain_table(table, lens, k.shape[0], dev)
         if n_new is not None:
             _need("n_new", n_new, (k.shape[0],), torch.int32, dev)
+        _need_word("granted", granted, dev)
     _refused("kv8_append", rc, explain)
 
 
@@ -675,14 +686,18 @@ def _explain_book(table, refs, info, workspace, lists=(), **per_seq):
 
 
 def kvp_reserve(table, lens, refs, n_new, page: int, info, window: int = 0, sinks: int = 0,
-                workspace=None):
+                workspace=None, granted=None):
     """Adds n_new [n_seqs] tokens to the sequences' lengths and pages for them to
     their tables; with a window first gives back the pages it has left behind
-    (include/kvcache.h).  info [4] int32 receives (done, taken, given back, free)."""
-    rc = (_bind or _load_bind()).kvp_reserve(table, lens, refs, n_new, page, info, window, sinks, workspace)
+    (include/kvcache.h).  info [4] int32 receives (done, taken, given back, free),
+    granted [1] int32, if given, done alone."""
+    rc = (_bind or _load_bind()).kvp_reserve(table, lens, refs, n_new, page, info, window, sinks, workspace,
+                                             granted)
     if rc != ATTN_OK:
-        _refused("kvp_reserve", rc,
-                 lambda: _explain_book(table, refs, info, workspace, lens=lens, n_new=n_new))
+        def explain():
+            _explain_book(table, refs, info, workspace, lens=lens, n_new=n_new)
+            _need_word("granted", granted, table.get_device())
+        _refused("kvp_reserve", rc, explain)
 
 
 def kvp_reassign(table, lens, refs, parents, page: int, copy_src, copy_dst, info, workspace=None):

@@ -28,11 +28,11 @@ namespace {
 
 // The C entry points, by address (init): this module does not link the library.
 struct Fns {
-    decltype(&kv8_append) append;
+    decltype(&kv8_append_step) append;
     decltype(&kv8_attn) attn;
     decltype(&kv8_attn_workspace_size) attn_size;
     decltype(&kv8_copy_pages) copy;
-    decltype(&kvp_reserve) reserve;
+    decltype(&kvp_reserve_step) reserve;
     decltype(&kvp_reassign) reassign;
     decltype(&kvp_compact) compact;
     decltype(&kvp_workspace_size) page_size;
@@ -171,10 +171,17 @@ bool small(at::IntArrayRef shape) {
 
 #define MISFIT() return PyLong_FromLong(kMisfit)
 
-// (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new | None) -> rc
+// An optional device word: undefined for None.
+bool word(PyObject* o, Tensor* out, int64_t dev) {
+    if (o == Py_None) return true;
+    *out = tensor(o);
+    return ints(*out, dev, {1});
+}
+
+// (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new | None, granted | None) -> rc
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) MISFIT();
+    if (n != 10) MISFIT();
     const Tensor k = tensor(a[0]), v = tensor(a[1]), table = tensor(a[6]), lens = tensor(a[7]);
     Pools p;
     if (!p.read(a + 2, false)) MISFIT();
@@ -192,16 +199,17 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
         !ints(lens, p.dev, {B}))
         MISFIT();
-    Tensor n_new;
+    Tensor n_new, granted;
     if (a[8] != Py_None) {
         n_new = tensor(a[8]);
         if (!ints(n_new, p.dev, {B})) MISFIT();
     }
+    if (!word(a[9], &granted, p.dev)) MISFIT();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
     return PyLong_FromLong(unlocked([&] {
         return fn.append(ptr(k), ptr(v), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
-                         as<int>(table), as<int>(lens), as<int>(n_new), B, p.heads, T, p.D, p.page,
-                         p.n_pages, table.size(1), st[0], st[1], st[2], code(k), stream_of(p.dev));
+                         as<int>(table), as<int>(lens), as<int>(n_new), as<int>(granted), B, p.heads, T,
+                         p.D, p.page, p.n_pages, table.size(1), st[0], st[1], st[2], code(k), stream_of(p.dev));
     }));
     END_HANDLE_TH_ERRORS
 }
@@ -290,22 +298,24 @@ struct Book {
     }
 };
 
-// (table, lens, refs, n_new, page, info, window, sinks, workspace | None) -> rc
+// (table, lens, refs, n_new, page, info, window, sinks, workspace | None, granted | None) -> rc
 PyObject* py_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) MISFIT();
+    if (n != 10) MISFIT();
     Book k;
     int page, window, sinks;
     if (!k.read(a[0], a[2], a[5], a[8]) || !count(a[4], &page) || !count(a[6], &window) ||
         !count(a[7], &sinks))
         MISFIT();
     const Tensor lens = tensor(a[1]), n_new = tensor(a[3]);
-    if (!ints(lens, k.dev, {k.n_seqs}) || !ints(n_new, k.dev, {k.n_seqs})) MISFIT();
+    Tensor granted;
+    if (!ints(lens, k.dev, {k.n_seqs}) || !ints(n_new, k.dev, {k.n_seqs}) || !word(a[9], &granted, k.dev))
+        MISFIT();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(k.dev));
     return PyLong_FromLong(unlocked([&] {
         return fn.reserve(as<int>(k.table), as<int>(lens), as<int>(k.refs), as<int>(n_new), k.n_seqs,
-                          k.max_pages, k.n_pages, page, window, sinks, as<int>(k.info), ptr(k.ws),
-                          bytes(k.ws), stream_of(k.dev));
+                          k.max_pages, k.n_pages, page, window, sinks, as<int>(k.info), as<int>(granted),
+                          ptr(k.ws), bytes(k.ws), stream_of(k.dev));
     }));
     END_HANDLE_TH_ERRORS
 }

@@ -89,6 +89,7 @@ struct AppendParams {
     const int* table;
     const int* lens;
     const int* n_new;
+    const int* granted;
     unsigned int* status;
     int64_t sb, sh, st;
     int B, Hkv, T, n_pages, max_pages, n_slots;
@@ -151,7 +152,8 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 5 : 8)
     const int b = id / p.n_slots;
     const int len = p.lens[b];
     const int n = p.n_new ? p.n_new[b] : p.T;
-    if (n == 0) return;
+    const int granted = p.granted ? *p.granted : 1;   // 0: lens does not hold the tokens
+    if (n == 0 || granted == 0) return;
     if (n < 0 || n > p.T || n > len || (len - 1) / PAGE >= p.max_pages) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
         return;
@@ -1282,6 +1284,16 @@ extern "C" int kv8_append(const void* k, const void* v, void* k_pages, void* v_p
                           const int* n_new, int B, int Hkv, int T, int D, int page, int n_pages,
                           int max_pages, long long stride_b, long long stride_h,
                           long long stride_t, int dtype, void* stream) {
+    return kv8_append_step(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new, nullptr, B,
+                           Hkv, T, D, page, n_pages, max_pages, stride_b, stride_h, stride_t, dtype,
+                           stream);
+}
+
+extern "C" int kv8_append_step(const void* k, const void* v, void* k_pages, void* v_pages,
+                               float* k_scale, float* v_scale, const int* table, const int* lens,
+                               const int* n_new, const int* granted, int B, int Hkv, int T, int D,
+                               int page, int n_pages, int max_pages, long long stride_b,
+                               long long stride_h, long long stride_t, int dtype, void* stream) {
     if (!k || !v || !k_pages || !v_pages || !k_scale || !v_scale || !table || !lens)
         return ATTN_ERR_INVALID;
     int rc = check_cache(B, Hkv, D, page, n_pages, max_pages);
@@ -1289,7 +1301,7 @@ extern "C" int kv8_append(const void* k, const void* v, void* k_pages, void* v_p
     if (T <= 0 || (dtype != ATTN_F16 && dtype != ATTN_BF16)) return ATTN_ERR_INVALID;
     if (stride_b < 0 || stride_h < 0 || stride_t < 0) return ATTN_ERR_INVALID;
     const void* ptrs[] = {k, v, k_pages, v_pages};
-    const void* words[] = {k_scale, v_scale, table, lens, n_new};
+    const void* words[] = {k_scale, v_scale, table, lens, n_new, granted};
     if (!aligned(ptrs, 16) || !aligned(words, 4)) return ATTN_ERR_ALIGN;
     if (stride_b % 8 || stride_h % 8 || stride_t % 8) return ATTN_ERR_ALIGN;
     const int64_t slots = (static_cast<int64_t>(T) + page - 2) / page + 1;
@@ -1306,6 +1318,7 @@ extern "C" int kv8_append(const void* k, const void* v, void* k_pages, void* v_p
     p.table = table;
     p.lens = lens;
     p.n_new = n_new;
+    p.granted = granted;
     p.sb = stride_b;
     p.sh = stride_h;
     p.st = stride_t;

@@ -40,6 +40,7 @@ struct PageParams {
     int* src;              // pairs to copy
     int* dst;
     int* info;
+    int* granted;          // reserve: info[0] again, or null
     unsigned int* status;
     int* scratch;          // workspace: scratch_ints() (when not in shared memory)
     int* ids;              // workspace: new id of each page (compact's second kernel)
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kThreads) kvp_reserve_kernel(const PageParams 
     const bool done = s_bad == 0 && need <= free;
     if (tid == 0) {
         p.info[0] = done;
+        if (p.granted) *p.granted = done;
         p.info[1] = done ? need : 0;
         p.info[2] = done ? free - before : 0;
         p.info[3] = done ? free - need : before;
@@ -502,11 +504,19 @@ extern "C" size_t kvp_workspace_size(int n_seqs, int max_pages, int n_pages) {
 extern "C" int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, int n_seqs,
                            int max_pages, int n_pages, int page, int window, int sinks, int* info,
                            void* workspace, size_t workspace_bytes, void* stream) {
+    return kvp_reserve_step(table, lens, refs, n_new, n_seqs, max_pages, n_pages, page, window, sinks,
+                            info, nullptr, workspace, workspace_bytes, stream);
+}
+
+extern "C" int kvp_reserve_step(int* table, int* lens, int* refs, const int* n_new, int n_seqs,
+                                int max_pages, int n_pages, int page, int window, int sinks,
+                                int* info, int* granted, void* workspace, size_t workspace_bytes,
+                                void* stream) {
     if (!table || !lens || !refs || !n_new || !info) return ATTN_ERR_INVALID;
     if (window < 0 || sinks < 0) return ATTN_ERR_INVALID;
     if (!page_ok(page)) return page <= 0 ? ATTN_ERR_INVALID : ATTN_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_pages) * page > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
-    const void* ptrs[] = {table, lens, refs, n_new, info};
+    const void* ptrs[] = {table, lens, refs, n_new, info, granted};
     for (const void* ptr : ptrs)
         if (!aligned4(ptr)) return ATTN_ERR_ALIGN;
     PageParams p{};
@@ -517,6 +527,7 @@ extern "C" int kvp_reserve(int* table, int* lens, int* refs, const int* n_new, i
     p.refs = refs;
     p.arg = n_new;
     p.info = info;
+    p.granted = granted;
     p.page = page;
     // no position is past 2^30: larger ones mean all of them
     p.window = window > (1 << 30) ? 1 << 30 : window;

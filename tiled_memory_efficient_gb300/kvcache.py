@@ -15,7 +15,8 @@ holder counts -- and offers the calls of a decoding loop over it::
 Nothing here reads device memory on the host: lengths and tables stay on the
 device, so a step captures into a CUDA graph.  ``sync_status()`` reports what a
 call could not do (a full pool: ATTN_ERR_POOL), ``info`` holds the last
-bookkeeping call's counts.
+bookkeeping call's counts.  After a ``reserve`` that found no room ``granted`` is 0
+and every ``append`` leaves the cache as it is, until a ``reserve`` succeeds.
 """
 from __future__ import annotations
 
@@ -58,6 +59,7 @@ class PagedKVCache:
         self.lens = torch.zeros(n_seqs, **i32)
         self.refs = torch.zeros(n_pages, **i32)
         self.info = torch.zeros(4, **i32)
+        self.granted = torch.ones(1, **i32)   # did the last reserve make room?
         self._count = self.info[1:2]
         # pairs of pages to copy: at most one a sequence, or half the pool
         pairs = max(n_seqs, n_pages // 2)
@@ -73,16 +75,19 @@ class PagedKVCache:
 
     def reserve(self, n_new):
         """Makes room for n_new tokens of every sequence (an int, or an int32 tensor
-        [n_seqs]; 0: the sequence rests) and adds them to the lengths."""
+        [n_seqs]; 0: the sequence rests) and adds them to the lengths; with too few
+        free pages it changes nothing but ``granted``."""
         _lib.kvp_reserve(self.table, self.lens, self.refs, self._counts(n_new), self.page_size,
-                         self.info, window=self.window, sinks=self.sinks, workspace=self._ws)
+                         self.info, window=self.window, sinks=self.sinks, workspace=self._ws,
+                         granted=self.granted)
 
     def append(self, layer: int, k, v, n_new=None):
         """Stores the keys and values [n_seqs, n_kv_heads, T, head_dim] of the tokens
-        that ``reserve`` made room for (n_new of the T each; None: all T)."""
+        that ``reserve`` made room for (n_new of the T each; None: all T); none when it
+        found no room."""
         _lib.kv8_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                         self.v_scale[layer], self.table, self.lens,
-                        n_new=None if n_new is None else self._counts(n_new))
+                        n_new=None if n_new is None else self._counts(n_new), granted=self.granted)
 
     def attend(self, layer: int, q, scale: float | None = None):
         """(out, lse) of the newest positions q [n_seqs, Hq, Nq, head_dim]."""
