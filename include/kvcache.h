@@ -95,6 +95,9 @@ int kv8_append_step(const void* k, const void* v, void* k_pages, void* v_pages, 
  * sequence's end and keys that no query of the call sees may hold anything; a NaN
  * or infinity in a value that one of several queries (Nq > 1) sees reaches the
  * queries of the call that do not see it, too.
+ * With a window kvp_reserve has given back what the tokens it made room for do not
+ * see: where a sequence took fewer than Nq of them, the first of the Nq queries may
+ * want such a page, which is recorded as a bad one (kv8_attn_step takes the counts).
  * workspace: kv8_attn_workspace_size() bytes.
  */
 int kv8_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
@@ -102,6 +105,22 @@ int kv8_attn(const void* q, const void* k_pages, const void* v_pages, const floa
              void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int D,
              int page, int n_pages, int max_pages, float scale, int window, int sinks, int dtype,
              void* stream);
+
+/*
+ * kv8_attn for the tokens of one step.  n_new [B] on the device (NULL: Nq each):
+ * the first n = n_new[b] queries are the sequence's n newest positions, as
+ * kv8_append takes the first n tokens: query i < n stands at lens[b] - n + i, the
+ * others see nothing (out = 0, lse = -inf).  A count outside [0, Nq] or past lens[b]
+ * is recorded like a bad length, and none of the sequence's queries sees anything.
+ * granted (one int32 on the device, written by kvp_reserve_step; NULL: 1): where it
+ * is 0 no query of the call sees anything.  Other arguments are kv8_attn's.
+ */
+int kv8_attn_step(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                  const float* v_scale, const int* table, const int* lens, const int* n_new,
+                  const int* granted, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int D, int page,
+                  int n_pages, int max_pages, float scale, int window, int sinks, int dtype,
+                  void* stream);
 
 /* Workspace bytes kv8_attn needs on the current device (partial results of the
  * shares that end inside a sequence); 0 for invalid sizes.  Host-only apart from

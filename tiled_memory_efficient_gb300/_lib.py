@@ -85,6 +85,7 @@ _SIGNATURES = {
     "kv8_append": ([_vp] * 9 + [_i] * 7 + [ctypes.c_longlong] * 3 + [_i, _vp], _i),
     "kv8_append_step": ([_vp] * 10 + [_i] * 7 + [ctypes.c_longlong] * 3 + [_i, _vp], _i),
     "kv8_attn": ([_vp] * 10 + [ctypes.c_size_t] + [_i] * 8 + [ctypes.c_float, _i, _i, _i, _vp], _i),
+    "kv8_attn_step": ([_vp] * 12 + [ctypes.c_size_t] + [_i] * 8 + [ctypes.c_float, _i, _i, _i, _vp], _i),
     "kv8_attn_workspace_size": ([_i] * 5, ctypes.c_size_t),
     "kv8_copy_pages": ([_vp] * 7 + [_i] * 6 + [_vp], _i),
     "kvp_reserve": ([_vp] * 4 + [_i] * 6 + [_vp, _vp, ctypes.c_size_t, _vp], _i),
@@ -356,7 +357,7 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
     return out, lse
 
 
-_BOUND = ("kv8_append_step", "kv8_attn", "kv8_attn_workspace_size", "kv8_copy_pages",
+_BOUND = ("kv8_append_step", "kv8_attn_step", "kv8_attn_workspace_size", "kv8_copy_pages",
           "kvp_reserve_step", "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
           "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size")
 _bind = None
@@ -617,11 +618,14 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
 
 
 def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,
-             window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None):
+             window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, n_new=None,
+             granted=None):
     """Attention of the newest Nq positions of each sequence, q [B, Hq, Nq, D], over
-    the paged cache (include/kvcache.h); returns (out, lse)."""
+    the paged cache (include/kvcache.h); returns (out, lse).  n_new [B]: only the
+    first n_new of a sequence's queries are its newest positions, the others get 0
+    and -inf, and so do all of them where granted [1] (written by kvp_reserve) is 0."""
     r = (_bind or _load_bind()).kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale,
-                                         window, sinks, out, lse, workspace)
+                                         window, sinks, out, lse, workspace, n_new, granted)
     if type(r) is tuple:
         return r
 
@@ -632,6 +636,9 @@ def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | 
         if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous() or q.get_device() != dev:
             raise ValueError(f"q must be a contiguous tensor [B, Hq, Nq, {D}] on CUDA device {dev}")
         _explain_table(table, lens, q.shape[0], dev)
+        if n_new is not None:
+            _need("n_new", n_new, (q.shape[0],), torch.int32, dev)
+        _need_word("granted", granted, dev)
         if out is not None:
             _need("out", out, q.shape, q.dtype, dev)
         if lse is not None:

@@ -29,7 +29,7 @@ namespace {
 // The C entry points, by address (init): this module does not link the library.
 struct Fns {
     decltype(&kv8_append_step) append;
-    decltype(&kv8_attn) attn;
+    decltype(&kv8_attn_step) attn;
     decltype(&kv8_attn_workspace_size) attn_size;
     decltype(&kv8_copy_pages) copy;
     decltype(&kvp_reserve_step) reserve;
@@ -225,10 +225,10 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
 }
 
 // (q, k_pages, v_pages, k_scale, v_scale, table, lens, scale | None, window, sinks,
-//  out | None, lse | None, workspace | None) -> (out, lse) or rc
+//  out | None, lse | None, workspace | None, n_new | None, granted | None) -> (out, lse) or rc
 PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 13) MISFIT();
+    if (n != 15) MISFIT();
     const Tensor q = tensor(a[0]), table = tensor(a[5]), lens = tensor(a[6]);
     Pools p;
     int window, sinks;
@@ -243,6 +243,12 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
         !ints(lens, p.dev, {B}))
         MISFIT();
+    Tensor n_new, granted;
+    if (a[13] != Py_None) {
+        n_new = tensor(a[13]);
+        if (!ints(n_new, p.dev, {B})) MISFIT();
+    }
+    if (!word(a[14], &granted, p.dev)) MISFIT();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
     Tensor out, lse, ws;
     const size_t size = fn.attn_size(B, Hq, p.heads, Nq, p.D);
@@ -252,8 +258,8 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         MISFIT();
     const int rc = unlocked([&] {
         return fn.attn(ptr(q), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
-                       as<int>(table), as<int>(lens), ptr(out), as<float>(lse), ptr(ws), bytes(ws), B,
-                       Hq, p.heads, Nq, p.D, p.page, p.n_pages, table.size(1), scale, window, sinks,
+                       as<int>(table), as<int>(lens), as<int>(n_new), as<int>(granted), ptr(out),
+                       as<float>(lse), ptr(ws), bytes(ws), B, Hq, p.heads, Nq, p.D, p.page, p.n_pages, table.size(1), scale, window, sinks,
                        code(q), stream_of(p.dev));
     });
     return rc == ATTN_OK ? pair(out, lse) : PyLong_FromLong(rc);

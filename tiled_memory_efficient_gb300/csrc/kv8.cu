@@ -279,6 +279,8 @@ struct AttnParams {
     const float* v_scale;
     const int* table;
     const int* lens;
+    const int* n_new;     // queries of a sequence that stand at a position (null: all Nq)
+    const int* granted;   // 0: none does (null: 1)
     void* out;
     float* lse;
     float* part_o;     // [2 * ctas][rows of a block][D]
@@ -292,21 +294,30 @@ struct AttnParams {
 
 // The visible tiles of a sequence.
 struct Seq {
-    int len, first;        // positions held; position of the first query (may be < 0)
+    int len, nq, first;    // positions held; queries; position of the first one (may be < 0)
     int lo;                // first position inside a window of some query
     int n_sink, skip, n;   // tiles [0, n_sink) and [n_sink + skip, ...), n in all
 };
-__device__ __forceinline__ Seq seq_of(const AttnParams& p, int len) {
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int len, int nq) {
     Seq s;
     const int up = (1 << p.tile_shift) - 1;
     s.len = min(max(len, 0), p.max_pages << p.page_shift);
-    s.first = s.len - p.Nq;
+    s.nq = nq;
+    s.first = s.len - nq;
     s.lo = p.window > 0 ? max(s.first - p.window + 1, 0) : 0;
     const int lo_tile = s.lo >> p.tile_shift;
     s.n_sink = min((p.sinks + up) >> p.tile_shift, lo_tile);
     s.skip = lo_tile - s.n_sink;
-    s.n = ((s.len + up) >> p.tile_shift) - s.skip;
+    s.n = nq > 0 ? ((s.len + up) >> p.tile_shift) - s.skip : 0;
     return s;
+}
+__device__ __forceinline__ bool step_granted(const AttnParams& p) { return !p.granted || *p.granted != 0; }
+// Queries of sequence b of that length; -1: a count that does not fit.
+__device__ __forceinline__ int queries_of(const AttnParams& p, bool granted, int b, int len) {
+    if (!granted) return 0;
+    if (!p.n_new) return p.Nq;
+    const int n = p.n_new[b];
+    return n < 0 || n > p.Nq || n > min(len, p.max_pages << p.page_shift) ? -1 : n;
 }
 __device__ __forceinline__ int seq_tile(const Seq& s, int v) {   // tile v of the list
     return v < s.n_sink ? v : v + s.skip;
@@ -404,8 +415,8 @@ struct AttnCfg {
     static constexpr int kQOff = kInfoOff + kWarps * kStages * static_cast<int>(sizeof(SlotInfo));
     static constexpr int kBarOff = kQOff + (kQSmem ? NR * 8 * D * 2 + NR * 8 * 4 : 0);
     static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kPreOff = kMiscOff + 8 * kWarps;                   // B + 1 ints, then B
-    static constexpr int smem_bytes(int B) { return kPreOff + (2 * B + 1) * 4; }
+    static constexpr int kPreOff = kMiscOff + 8 * kWarps;                   // B + 1 ints, then 2 B
+    static constexpr int smem_bytes(int B) { return kPreOff + (3 * B + 1) * 4; }
     static_assert(smem_bytes(kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -430,6 +441,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 4 * kWarps);   // [kWarps]
     int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
     int* s_len = s_pre + p.B + 1;                                     // [B]
+    int* s_nq = s_len + p.B;                                          // [B] queries
 
     if (lane == 0) {
         // a slot's phase: its copies' bytes, and its lane's small copies
@@ -444,16 +456,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     // exclusive prefix sums of the sequences' tile counts
+    const bool granted = step_granted(p);
     int carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        int len = 0;
+        int len = 0, nq = 0;
         if (b < p.B) {
             len = p.lens[b];
-            if (blockIdx.x == 0 && (len < 0 || len > p.max_pages << p.page_shift))
+            nq = queries_of(p, granted, b, len);
+            if (blockIdx.x == 0 && (len < 0 || len > p.max_pages << p.page_shift || nq < 0))
                 atomicOr(p.status, kStatusPage);
         }
-        const int n = b < p.B ? seq_of(p, len).n : 0;
+        const int n = b < p.B ? seq_of(p, len, nq).n : 0;
         int x = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -471,6 +485,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (b < p.B) {
             s_pre[b] = before + x - n;
             s_len[b] = len;
+            s_nq[b] = nq;
         }
         carry = all;
         if (b0 + kAttnThreads < p.B) __syncthreads();   // s_warp is written again
@@ -596,7 +611,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int ntok = 0, nseen = 0;                    // its first token; boxes some query sees
     int issued = 0;
     auto enter = [&]() {   // a new sequence
-        const Seq x = seq_of(p, s_len[nb]);
+        const Seq x = seq_of(p, s_len[nb], s_nq[nb]);
         nn = x.n;
         n_sink = x.n_sink;
         n_skip = x.skip;
@@ -724,7 +739,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int slot = 0;               // of that tile
     uint32_t phase = 0;         // and its turn of the ring
     while (unit0 < g1) {
-        const Seq s = seq_of(p, s_len[b]);
+        const Seq s = seq_of(p, s_len[b], s_nq[b]);
         const int h = head_of(u), row0 = (u - h * p.n_rb) * (8 * NR);
         const int unit1 = unit0 + s.n, end = min(unit1, g1);
         const int64_t head_row = (static_cast<int64_t>(b) * p.Hkv + h) * p.rows;   // of q, out, lse
@@ -817,7 +832,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             // scores in log2 units; edge tiles hide what a row does not see
-            const bool edge = bad != 0 || tok + kTile - 1 > s.first ||
+            const bool edge = bad != 0 || tok + kTile - 1 > s.first || s.nq < p.Nq ||
                               (p.window > 0 && tok <= s.len - 1 - p.window && tok + kTile > p.sinks);
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
@@ -834,7 +849,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int pos = s.first + (row0 + nt * 8 + 2 * t + (e & 1)) % p.Nq;
+                        const int i = (row0 + nt * 8 + 2 * t + (e & 1)) % p.Nq;
+                        const int pos = i < s.nq ? s.first + i : -1;
 #pragma unroll
                         for (int hf = 0; hf < NQ; ++hf) {
                             const int key = tok + hf * 16 + tok_a + 8 * (e >> 1);
@@ -987,6 +1003,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     s_lse[(warp * NR + nt) * 8 + 2 * t + e] =
                         x == 0.0f ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
                 up[nt][e] = x == 0.0f ? 0.0f : ex2_ftz(R[nt][e] - m[nt][e]) / x;
+                if (x == 0.0f) {   // a row that sees nothing: 0, beside a NaN of the others', too
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) o[nt][i][e] = o[nt][i][e + 2] = 0.0f;
+                }
             }
         __syncthreads();
         {
@@ -1074,10 +1094,10 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnPa
     // results after the wait below.
     // tiles of all sequences, and of those before b: each warp for itself, or
     // (many sequences) the CTA together
-    const bool alone = p.B <= 128;
+    const bool alone = p.B <= 128, granted = step_granted(p);
     int all = 0, before = 0;
     for (int i = alone ? lane : threadIdx.x; i < p.B; i += alone ? 32 : kThreads) {
-        const int n = seq_of(p, p.lens[i]).n;
+        const int len = p.lens[i], n = seq_of(p, len, queries_of(p, granted, i, len)).n;
         all += n;
         if (i < b) before += n;
     }
@@ -1099,7 +1119,7 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv8_merge_kernel(const AttnPa
     }
     const int row0 = u % p.n_rb * (8 * NR);
     const int r = static_cast<int>(blockIdx.x % chunks) * kMergeRows + warp;   // within the block
-    const int n = seq_of(p, p.lens[b]).n;
+    const int len = p.lens[b], n = seq_of(p, len, queries_of(p, granted, b, len)).n;
     const Shares sh(all * U, p);
     const int first = before * U + u * n;
     int c0 = 0, c1 = -1;   // the CTAs that hold part of the unit
@@ -1371,6 +1391,17 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
                         size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int D, int page,
                         int n_pages, int max_pages, float scale, int window, int sinks, int dtype,
                         void* stream) {
+    return kv8_attn_step(q, k_pages, v_pages, k_scale, v_scale, table, lens, nullptr, nullptr, out, lse,
+                         workspace, workspace_bytes, B, Hq, Hkv, Nq, D, page, n_pages, max_pages,
+                         scale, window, sinks, dtype, stream);
+}
+
+extern "C" int kv8_attn_step(const void* q, const void* k_pages, const void* v_pages,
+                             const float* k_scale, const float* v_scale, const int* table,
+                             const int* lens, const int* n_new, const int* granted, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                             int Hkv, int Nq, int D, int page, int n_pages, int max_pages,
+                             float scale, int window, int sinks, int dtype, void* stream) {
     if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !table || !lens || !out || !lse ||
         !workspace)
         return ATTN_ERR_INVALID;
@@ -1382,7 +1413,7 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     if (!(scale > 0.0f) || !std::isfinite(scale)) return ATTN_ERR_INVALID;
     if (window < 0 || sinks < 0) return ATTN_ERR_INVALID;
     const void* ptrs[] = {q, k_pages, v_pages, out, lse, workspace};
-    const void* words[] = {k_scale, v_scale, table, lens};
+    const void* words[] = {k_scale, v_scale, table, lens, n_new, granted};
     if (!aligned(ptrs, 16) || !aligned(words, 4)) return ATTN_ERR_ALIGN;
     if (workspace_bytes < kv8_attn_workspace_size(B, Hq, Hkv, Nq, D)) return ATTN_ERR_WORKSPACE;
     // the kernels count tiles of all sequences' table capacity in 32 bits
@@ -1406,6 +1437,8 @@ extern "C" int kv8_attn(const void* q, const void* k_pages, const void* v_pages,
     p.v_scale = v_scale;
     p.table = table;
     p.lens = lens;
+    p.n_new = n_new;
+    p.granted = granted;
     p.out = out;
     p.lse = lse;
     p.ctas = sms;

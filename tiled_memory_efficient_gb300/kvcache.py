@@ -8,7 +8,7 @@ holder counts -- and offers the calls of a decoding loop over it::
     cache.reserve(n_new)                     # room for this step's tokens, every layer
     for layer in range(24):
         cache.append(layer, k, v, n_new)     # this layer's new keys and values
-        out, lse = cache.attend(layer, q)    # the newest positions over the cache
+        out, lse = cache.attend(layer, q, n_new=n_new)   # the same tokens over the cache
     cache.reassign(parents)                  # fork, reorder or free sequences
     cache.compact()                          # held pages to the front of the pools
 
@@ -17,6 +17,9 @@ device, so a step captures into a CUDA graph.  ``sync_status()`` reports what a
 call could not do (a full pool: ATTN_ERR_POOL), ``info`` holds the last
 bookkeeping call's counts.  After a ``reserve`` that found no room ``granted`` is 0
 and every ``append`` leaves the cache as it is, until a ``reserve`` succeeds.
+
+A step may give each sequence its own number of tokens: ``n_new`` goes to all three
+calls, and both the keys and the queries of sequence b are the first n_new[b] rows.
 """
 from __future__ import annotations
 
@@ -89,11 +92,17 @@ class PagedKVCache:
                         self.v_scale[layer], self.table, self.lens,
                         n_new=None if n_new is None else self._counts(n_new), granted=self.granted)
 
-    def attend(self, layer: int, q, scale: float | None = None):
-        """(out, lse) of the newest positions q [n_seqs, Hq, Nq, head_dim]."""
+    def attend(self, layer: int, q, scale: float | None = None, n_new=None):
+        """(out, lse) of the newest positions q [n_seqs, Hq, Nq, head_dim].  n_new as in
+        ``append``: the first n_new rows of each sequence, the others (and all rows
+        of a step that found no room) get 0 and -inf.  None: all Nq rows are the
+        newest positions; with a window no more than the sequence's last ``reserve``
+        made room for, since older queries want pages that it gave back."""
         return _lib.kv8_attn(q, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                              self.v_scale[layer], self.table, self.lens, scale=scale,
-                             window=self.window, sinks=self.sinks)
+                             window=self.window, sinks=self.sinks,
+                             n_new=None if n_new is None else self._counts(n_new),
+                             granted=None if n_new is None else self.granted)
 
     def reassign(self, parents):
         """Sequence c becomes a copy-on-write child of parents[c] (int32 tensor
