@@ -1425,7 +1425,6 @@ __global__ void __launch_bounds__(384, 1)
                     if (j + 1 < w.n0) issue_s(0, g + 1, j + 2 == w.n0);
                 } else {
                     mma_commit_elect(&k_empty[2 * ks]);
-                    mma_commit_elect(&v_empty[2 * vs]);
                     // Tile 0 has no step here: its first scores of the next unit
                     if (j + 1 == steps && k + 1 < n_units &&
                         warp_wait(&q_full[0], (k + 1) & 1, abort_flag, p.status)) {
@@ -1437,6 +1436,9 @@ __global__ void __launch_bounds__(384, 1)
                 if (j < w.n1 && j != w.x1) {
                     const int nx = next1(j);
                     issue_pv(1, g, j == first1, nx >= w.n1, idesc);
+                    // For the idle tile 0: only now is the step's V known to have arrived.  A
+                    // release before that could let the barrier's phase pass twice unseen.
+                    if (j >= w.n0) mma_commit_elect(&v_empty[2 * vs]);
                     if (nx < w.n1) issue_s(1, g0 + nx, next1(nx) >= w.n1);
                 } else {
                     mma_commit_elect(&k_empty[2 * ks + 1]);
