@@ -350,10 +350,12 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* ou
                      void* stream);
 
 /*
- * Synchronises `stream`, then returns and clears the device status word of the
- * current device: ATTN_ERR_TIMEOUT if any kernel's bounded wait gave up since
- * the last call, else ATTN_ERR_PAGE or ATTN_ERR_POOL if a cache call (kvcache.h)
- * recorded one, ATTN_ERR_CUDA if the synchronisation failed, else ATTN_OK.
+ * Synchronises `stream`, then returns and clears one record of the current
+ * device's status word: ATTN_ERR_TIMEOUT if any kernel's bounded wait gave up
+ * since it was last returned, else ATTN_ERR_PAGE, else ATTN_ERR_POOL if a cache
+ * call (kvcache.h) recorded one, else ATTN_OK (ATTN_ERR_CUDA if the
+ * synchronisation failed).  Records of the other kinds are kept: the calls up to
+ * the first ATTN_OK name all of them.
  */
 int attn_sync_status(void* stream);
 

@@ -27,7 +27,8 @@
  * What the device finds wrong (a page id outside the pool where a token is
  * needed, a length past the table, a bad parent) is skipped, never read or
  * written, and recorded in the status word: attn_sync_status() then returns
- * ATTN_ERR_PAGE, or ATTN_ERR_POOL when a pool had too few free pages.
+ * ATTN_ERR_PAGE, or ATTN_ERR_POOL when a pool had too few free pages (one after
+ * the other when both happened).
  */
 #ifndef TME_KVCACHE_H
 #define TME_KVCACHE_H

@@ -179,3 +179,25 @@ def test_granted_of_the_wrong_kind_is_refused(cuda_lib):
         with pytest.raises(ValueError, match="granted"):
             _lib.kv8_append(k, v, *pools, cache.table, cache.lens, granted=bad)
     assert cache.lens.tolist() == [0, 0]
+
+
+# ------------------------------------------------------------------ GPU: the status word
+
+@pytest.mark.gpu
+def test_one_kind_of_error_does_not_hide_another(cuda_lib):
+    """A time-out, a bad length and a full pool in one go are returned one by one."""
+    assert _lib.sync_status() == _lib.ATTN_OK
+    cache = PagedKVCache(1, 1, 2, 64, n_pages=1, page_size=16)
+    k = torch.ones(1, 2, 20, 64, dtype=F16, device="cuda")
+    for timeout in (False, True):
+        cache.reserve(17)                                       # one page of 16
+        assert cache.granted.item() == 0
+        _lib.kv8_append(k, k, cache.k_pages[0], cache.v_pages[0], cache.k_scale[0], cache.v_scale[0], cache.table,
+                        cache.lens)                             # 20 tokens of a length of 0
+        if timeout:
+            stream = torch.cuda.current_stream().cuda_stream
+            assert cuda_lib.attn_selftest_timeout(1_000_000, stream) == _lib.ATTN_OK   # 1 ms
+            assert _lib.sync_status() == _lib.ATTN_ERR_TIMEOUT
+        assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+        assert _lib.sync_status() == _lib.ATTN_ERR_POOL
+        assert _lib.sync_status() == _lib.ATTN_OK

@@ -504,7 +504,8 @@ def attn_bwd(q, k, v, out, dout, lse, causal: bool = False, scale: float | None 
 
 
 def sync_status(device=None) -> int:
-    """Synchronise the current stream and return (and clear) the device status."""
+    """Synchronise the current stream and return (and clear) the most urgent kind of
+    error the device recorded: ATTN_ERR_TIMEOUT, _PAGE, _POOL, or ATTN_OK."""
     import torch
     dev = device if device is not None else torch.cuda.current_device()
     return load().attn_sync_status(_stream_handle(dev))

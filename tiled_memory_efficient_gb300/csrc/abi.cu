@@ -20,12 +20,14 @@ namespace tme {
 
 // One status word per device (a static device variable; nothing is allocated).
 __device__ unsigned int g_status;
+__device__ unsigned int g_reported;   // what attn_sync_status took from it last
 
 namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSplits = 256;  // key ranges of one split forward, at most
 std::mutex g_mu;
+std::mutex g_report_mu;          // g_reported is one caller's at a time
 unsigned int* g_status_ptr[kMaxDevices] = {};
 int g_cc_ok[kMaxDevices] = {};  // 0 unknown, 1 sm_103, -1 other
 
@@ -112,6 +114,17 @@ int check_shape(int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int 
     const int64_t pairs = (rows + 255) / 256;
     if (groups * pairs > 0x7fffffffll || groups > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
+}
+
+// Takes the most urgent bit out of the status word.  Atomic: kernels of other streams
+// may set bits meanwhile, which stay.
+__global__ void take_status_kernel(unsigned int* status) {
+    const unsigned int word = atomicOr(status, 0u);
+    const unsigned int bit = word & kStatusTimeout ? kStatusTimeout
+                             : word & kStatusPage  ? kStatusPage
+                                                   : word & kStatusPool;
+    atomicAnd(status, ~bit);
+    g_reported = bit;
 }
 
 __global__ void selftest_timeout_kernel(unsigned long long wait_ns, unsigned int* status) {
@@ -1153,15 +1166,17 @@ extern "C" int attn_sync_status(void* stream) {
     unsigned int word = 0;
     if (cudaMemcpy(&word, status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return ATTN_ERR_CUDA;
-    if (word != 0) {
-        const unsigned int zero = 0;
-        if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
-            return ATTN_ERR_CUDA;
-    }
-    return (word & kStatusTimeout) ? ATTN_ERR_TIMEOUT
-           : (word & kStatusPage)  ? ATTN_ERR_PAGE
-           : (word & kStatusPool)  ? ATTN_ERR_POOL
-                                   : ATTN_OK;
+    if (word == 0) return ATTN_OK;
+    std::lock_guard<std::mutex> lk(g_report_mu);
+    if (launch_kernel(take_status_kernel, dim3(1), dim3(1), 0, static_cast<cudaStream_t>(stream),
+                      status) != cudaSuccess ||
+        cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&word, g_reported, sizeof(word)) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return word == kStatusTimeout ? ATTN_ERR_TIMEOUT
+           : word == kStatusPage  ? ATTN_ERR_PAGE
+           : word == kStatusPool  ? ATTN_ERR_POOL
+                                  : ATTN_OK;
 }
 
 extern "C" int attn_selftest_timeout(unsigned long long wait_ns, void* stream) {
