@@ -15,6 +15,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -485,6 +487,18 @@ struct Refused {
     int rc;
 };
 
+// Gradients of a pass with create_graph: differentiating them raises.  They would be
+// constants to the second pass otherwise, whose result would lack their part.  The node
+// that raises leads where the one being evaluated does, so that a pass to any of its
+// inputs meets it.
+void refuse_second(const Tensor (&g)[3], const Tensor& dout) {
+    torch::autograd::edge_list to = torch::autograd::get_current_node()->next_edges();
+    to.push_back(torch::autograd::impl::gradient_edge(dout));
+    const auto node = std::make_shared<torch::autograd::Error>("window_attention has no second derivative",
+                                                               std::move(to));
+    for (const Tensor& t : g) torch::autograd::set_history(t, node);
+}
+
 // Sliding-window attention as a function of the autograd graph.  (In Python it took 235
 // us of host time a training pass: the engine's threads hand the interpreter's lock
 // to and fro.)
@@ -527,6 +541,7 @@ struct WindowAttention : torch::autograd::Function<WindowAttention> {
         const Tensor ws = empty({static_cast<int64_t>(std::max<size_t>(w.bwd_size(), 16))}, at::kByte, w.dev);
         const int rc = w.bwd(saved[3], dout, saved[4], g, ws);
         TORCH_CHECK(rc == ATTN_OK, "attn_bwd_window failed with status ", rc);
+        if (at::GradMode::is_enabled()) refuse_second(g, grads[0]);   // create_graph
         return {g[0], g[1], g[2], Tensor(), Tensor(), Tensor()};
     }
 };

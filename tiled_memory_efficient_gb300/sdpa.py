@@ -114,7 +114,8 @@ def window_attention(q, k, v, window: int, sinks: int = 0, scale: float | None =
     """Differentiable causal attention with a sliding window and sinks.  The Nq
     queries are the last Nq of the Nk positions; each sees the last `window`
     positions up to its own and the first `sinks` ones (Nq <= Nk, window >= 1,
-    sinks >= 0).  Layouts, dtypes and GQA as in ``attention``.
+    sinks >= 0).  Layouts, dtypes and GQA as in ``attention``.  It has no second
+    derivative: differentiating a gradient taken with create_graph raises.
 
     A backward pass captured into a CUDA graph raises while a graph recorded
     outside the capture still holds the same leaves: drop that graph's outputs
