@@ -40,3 +40,34 @@ def _check(call, dtype=F16):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_window_attention(cuda_lib, dtype):
     _check(lambda q, k, v: sdpa.window_attention(q, k, v, 40, 2), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention(cuda_lib, causal):
+    _check(lambda q, k, v: sdpa.attention(q, k, v, is_causal=causal))
+
+
+@pytest.mark.gpu
+def test_masked_attention(cuda_lib):
+    mask = torch.ones(1, 1, 150, 150, dtype=torch.bool, device="cuda").tril()
+    _check(lambda q, k, v: sdpa.attention(q, k, v, attn_mask=mask))
+
+
+@pytest.mark.gpu
+def test_views_of_one_projection(cuda_lib):
+    """Inputs that are not contiguous: the same gradients, and a second derivative raises."""
+    g = torch.Generator().manual_seed(61)
+    x = torch.randn(2, 100, 8, 64, generator=g).to(BF16).cuda().requires_grad_(True)
+    do = torch.randn(2, 4, 100, 64, generator=g).to(BF16).cuda()
+    for call in (lambda q, k, v: sdpa.attention(q, k, v, is_causal=True),
+                 lambda q, k, v: sdpa.window_attention(q, k, v, 30, 1)):
+        def once(x, **kw):
+            return torch.autograd.grad(call(*(t.transpose(1, 2) for t in x.split((4, 2, 2), 2))), x, do, **kw)[0]
+        parts = [t.transpose(1, 2).contiguous().detach().requires_grad_(True) for t in x.split((4, 2, 2), 2)]
+        want = torch.cat([t.transpose(1, 2) for t in torch.autograd.grad(call(*parts), parts, do)], 2)
+        assert torch.equal(once(x), want)
+        first = once(x, create_graph=True)
+        assert torch.equal(first, want)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            torch.autograd.grad(first.float().square().sum() + x.float().pow(3).sum(), x)

@@ -33,11 +33,31 @@ _SUPPORTED_D = (64, 128)
 _original_sdpa = None
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Gradients (the first n arguments) of a pass with create_graph: differentiating
+    them raises.  They would be constants to the second pass otherwise, whose result
+    would lack their part.  The other arguments are what they were made from, so that
+    a pass to any of it meets this function."""
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("attention has no second derivative")
+
+
+def _gradients(ctx_inputs, dout, *grads):
+    """The gradients a backward returns (ctx_inputs: the tensors it was saved with)."""
+    if not torch.is_grad_enabled():   # no create_graph
+        return grads
+    return _NoSecondDerivative.apply(len(grads), *grads, *ctx_inputs, dout)
+
+
 class _TiledAttentionMasked(torch.autograd.Function):
     """Attention with an attn_mask (the mask itself gets no gradient)."""
     @staticmethod
     def forward(ctx, q, k, v, mask, is_causal, scale):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         out, lse = _lib.attn_fwd(q, k, v, causal=is_causal, scale=scale, mask=mask)
         ctx.save_for_backward(q, k, v, out, lse, mask)
         ctx.is_causal = is_causal
@@ -49,13 +69,12 @@ class _TiledAttentionMasked(torch.autograd.Function):
         q, k, v, out, lse, mask = ctx.saved_tensors
         dq, dk, dv = _lib.attn_bwd(q, k, v, out, dout.contiguous(), lse, causal=ctx.is_causal,
                                    scale=ctx.scale, mask=mask)
-        return dq, dk, dv, None, None, None
+        return *_gradients((q, k, v), dout, dq, dk, dv), None, None, None
 
 
 class _TiledAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, is_causal, scale):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         B, Hq, Nq, D = q.shape
         Hkv, Nk = k.shape[1], k.shape[2]
         # Short query blocks against long keys (decode) leave most SMs idle
@@ -78,7 +97,7 @@ class _TiledAttention(torch.autograd.Function):
         q, k, v, out, lse = ctx.saved_tensors
         dq, dk, dv = _lib.attn_bwd(q, k, v, out, dout.contiguous(), lse,
                                    causal=ctx.is_causal, scale=ctx.scale)
-        return dq, dk, dv, None, None
+        return *_gradients((q, k, v), dout, dq, dk, dv), None, None
 
 
 def _validate(q, k, v):
@@ -101,10 +120,13 @@ def attention(q, k, v, is_causal: bool = False, scale: float | None = None, attn
     """Differentiable tiled attention.  q [B,Hq,Nq,D]; k, v [B,Hkv,Nk,D] with
     Hq a multiple of Hkv (query head h uses KV head h // (Hq//Hkv)); causal is
     top-left aligned; scale defaults to 1/sqrt(D).  attn_mask: bool (True
-    keeps a key) or additive, broadcastable to [B,Hq,Nq,Nk]."""
+    keeps a key) or additive, broadcastable to [B,Hq,Nq,Nk].  It has no second
+    derivative: differentiating a gradient taken with create_graph raises."""
     _validate(q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
+    # here and not inside the functions, whose saved tensors are then their inputs
+    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
     if attn_mask is not None:
         return _TiledAttentionMasked.apply(q, k, v, attn_mask, bool(is_causal), float(scale))
     return _TiledAttention.apply(q, k, v, bool(is_causal), float(scale))
