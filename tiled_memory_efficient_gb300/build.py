@@ -1,5 +1,6 @@
 """Builds the CUDA library libattn.so in-tree with nvcc (sm_103a only), and the
-compiled part of its Python binding (_bind.so) with the host compiler.
+compiled part of its Python binding (_bind.so) with the host compiler where torch is
+installed.
 
     python -m tiled_memory_efficient_gb300.build [--force]
 
@@ -39,9 +40,16 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h", "kvcache.h")]
-    files.append(BIND_SOURCE)
-    return max(os.path.getmtime(f) for f in files)
+    return max(os.path.getmtime(f) for f in files + _public_headers())
+
+
+def _public_headers() -> list:
+    return [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h", "kvcache.h")]
+
+
+def _have_torch() -> bool:
+    import importlib.util
+    return importlib.util.find_spec("torch") is not None
 
 
 def _bind_command(out: str) -> list:
@@ -60,45 +68,53 @@ def _bind_command(out: str) -> list:
             "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
-                         for f in (LIB, BIND)):
-        return LIB
-    cc = nvcc()
-    procs = []
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        log = open(os.path.join(BUILD, src.replace(".cu", ".log")), "w")
-        cmd = [cc, *ARCH, *FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((src, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
-        objs.append(obj)
-    tmp = os.path.join(BUILD, f"_bind.tmp{os.getpid()}.so")
-    log = open(os.path.join(BUILD, "bind.log"), "w")
-    procs.append(("bind.cpp", subprocess.Popen(_bind_command(tmp), stdout=log,
-                                               stderr=subprocess.STDOUT), log))
-    failed = []
-    for src, pr, log in procs:
-        rc = pr.wait()
-        log.close()
-        if rc != 0:
-            failed.append(src)
+def _start(src: str, cmd: list):
+    """A compiler process whose output goes to the log of `src`."""
+    log = open(os.path.join(BUILD, os.path.splitext(src)[0] + ".log"), "w")
+    with log:
+        return src, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)
+
+
+def _finish(procs: list) -> None:
+    failed = [src for src, pr in procs if pr.wait() != 0]
     if failed:
         msgs = []
         for src in failed:
             with open(os.path.join(BUILD, os.path.splitext(src)[0] + ".log")) as f:
                 msgs.append(f"--- {src}\n" + f.read()[-6000:])
         raise RuntimeError("compilation failed:\n" + "\n".join(msgs))
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is out of date: the library, which needs nvcc alone, and beside it the
+    compiled part of the Python binding where torch is installed."""
+    os.makedirs(BUILD, exist_ok=True)
+    stale = lambda f, newest: force or not os.path.exists(f) or os.path.getmtime(f) < newest
+    bind, tmp_bind = [], BIND + f".tmp{os.getpid()}"
+    if _have_torch() and stale(BIND, max(os.path.getmtime(f) for f in [BIND_SOURCE] + _public_headers())):
+        bind = [_start("bind.cpp", _bind_command(tmp_bind))]
+    try:
+        if stale(LIB, _deps_mtime()):
+            _build_library(verbose)
+    finally:
+        _finish(bind)
+    if bind:
+        os.replace(tmp_bind, BIND)
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
+    cc = nvcc()
+    objs = [os.path.join(BUILD, src.replace(".cu", ".o")) for src in SOURCES]
+    _finish([_start(src, [cc, *ARCH, *FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj])
+             for src, obj in zip(SOURCES, objs)])
     if verbose:
         for src in SOURCES:
             with open(os.path.join(BUILD, src.replace(".cu", ".log"))) as f:
                 print(f.read())
-    os.replace(tmp, BIND)
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
