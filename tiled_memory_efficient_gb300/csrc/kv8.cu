@@ -1003,15 +1003,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     s_lse[(warp * NR + nt) * 8 + 2 * t + e] =
                         x == 0.0f ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
                 up[nt][e] = x == 0.0f ? 0.0f : ex2_ftz(R[nt][e] - m[nt][e]) / x;
-                if (x == 0.0f) {   // a row that sees nothing: 0, beside a NaN of the others', too
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) o[nt][i][e] = o[nt][i][e + 2] = 0.0f;
-                }
             }
         __syncthreads();
+        float sum = 0.0f;   // of row lane % (8 NR): 0 when it sees nothing
         {
             const int i = lane % (8 * NR);
-            float a[kWarps], M = -INFINITY, sum = 0.0f;
+            float a[kWarps], M = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 a[k] = s_lse[k * (8 * NR) + i];
@@ -1057,6 +1054,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     ox += x.x;
                     oy += x.y;
                 }
+                // a row that sees nothing is 0 beside a NaN that others see, too
+                if (__shfl_sync(0xffffffffu, sum, r) == 0.0f) ox = oy = 0.0f;
                 const int dim = VB * g + 8 * half + 2 * t;
                 if (whole)
                     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
