@@ -1196,8 +1196,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MK, BF16, VPRE>::kThreads, 1)
 // bf16: V comes from the workspace's fp16 copy unless one of the unit's value tiles
 // had to stay bf16 (vconv.cu).
 // Bound by the chain of a tile (scores, 128 terms a thread, product), which two tiles run
-// half a period apart: a key tile takes 3000 cycles for both, their products 2050.  B=2
-// H=16 N=8192, window 1024: bf16 152 us, 17 of them V's copy (178 with a CTA to each
+// half a period apart: a key tile takes 3000 cycles for both, their products 2050.  In a
+// graph, B=2 H=16 N=8192, window 1024: bf16 152 us (157 for a single call), 17 of them V's copy (178 with a CTA to each
 // pair), fp16 132 (157), 976 TFLOP/s; window 256: 90 and 71 us (115, 100); window 4096:
 // 341 and 325 (355, 326).
 struct WindowPair {

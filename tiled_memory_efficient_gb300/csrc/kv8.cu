@@ -132,9 +132,12 @@ __device__ __forceinline__ uint32_t amax_bits(const uint4 (&w)[N]) {
 // new tokens are read once into registers (NV 16-byte vectors a thread, PAGE * D
 // = 1024 NV), their largest magnitude gives the scale, then they are rounded
 // and written; earlier tokens of the page are read only when the scale grew.
-// Bound by memory (2 x 8190 tokens, 8 KV heads, D = 128: 101 MB in 15.7 us, 6.4 TB/s;
-// one token a sequence: 4.4 us, a launch): 64 registers a thread leave 8 CTAs of 16 KB (64-token pages, D =
-// 128) in flight on an SM, and the tokens are asked for before the page's id.
+// A single token a sequence is bound by a launch (3.7 us in a graph), a prompt by the CTAs'
+// turns: 2 x 8190 tokens, 8 KV heads, D = 128 read 67 MB and write 34 in 16.4 us cold, of
+// which 31 are still in the second-level cache at the end; DRAM is 54% busy and the issue
+// slots 57%.  3.4 waves of CTAs load, meet a barrier and store, with nothing between a
+// CTA's stores and the next one's loads.  64 registers a thread leave 8 CTAs of 16 KB (64-token
+// pages, D = 128) in flight on an SM, and the tokens are asked for before the page's id.
 template <int D, int PAGE, bool BF16>
 __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 5 : 8)
     kv8_append_kernel(const AppendParams p) {
@@ -261,8 +264,13 @@ cudaError_t launch_append(bool bf16, const AppendParams& p, cudaStream_t stream)
 //
 // Bound by memory where caches are long: 32 sequences of 200 to 32768 tokens, 8 KV
 // heads, D = 128 stream 962 MB in 154 us, 6.2 TB/s, 92% of a plain copy's rate; 8 of 64K
-// tokens, 2 KV heads, D = 64, 134 MB in 31 us with the merge.  Short ones by latency: 8 of
-// 256 tokens take 4.9 us, launch, the chain of lengths, page ids and tiles, and merge.
+// tokens, 2 KV heads, D = 64, 134 MB in 31 us with the merge, calls in a graph.  Short ones by
+// latency: 8 of 256 tokens take 4.9 us in a graph, launch, the chain of lengths, page ids and
+// tiles, and merge.  With 32 query rows the same chain is three times as long (4 drafts of 7
+// heads, 516 visible tokens: 17 us): a unit's end brings 8 warps' 32 rows together through
+// shared memory, twice where a share of 4 tiles crosses into the next head, and all of that
+// code runs once, so that warps stand 3.6 of 14 cycles per instruction waiting for
+// instructions, 3.1 at barriers and 3.0 for shared memory.
 
 // Warps per CTA: 12 of them with 2 slots each instead of 3 took 5.4 us against 4.8 (8
 // sequences of 256 tokens, D = 64) and 51.4 against 50.4 (64K tokens, D = 128).
@@ -1204,8 +1212,8 @@ struct CopyParams {
 
 // CTAs take (pair, layer, keys or values) items in turn, as many as the device
 // holds: the count of pairs is only known there.  4 vectors in flight a thread.
-// Bound by memory: 166 MB read and written in 24.2 us, the compaction's plan before it
-// included.
+// Bound by memory: a compaction's 59 MB are read and written in 19.6 us cold, 6.0 TB/s (40
+// of the written MB are still in the second-level cache then); its plan takes 7.5 us before.
 constexpr int kCopyThreads = 256, kCopyCtasPerSm = 8;
 __global__ void __launch_bounds__(kCopyThreads) kv8_copy_kernel(const CopyParams p) {
     // Launched as a programmatic dependent of the kernel that lists the pairs.

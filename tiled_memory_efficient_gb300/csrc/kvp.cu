@@ -17,7 +17,7 @@ int device_setup_public(unsigned int** status);   // abi.cu
 namespace {
 
 // The planning kernels run as one CTA: they are chains of a few scans, bound by latency
-// (reserve: 3.9 us at 512 pages, 40 us at 65537 pages).
+// (reserve: 3.9 us at 512 pages, 40 us at 65537 pages; times in this file are in a graph).
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 // The planning's steps depend on one another through the pages' counts, the list of
