@@ -261,8 +261,8 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = unlocked([&] {
         return fn.attn(ptr(q), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
                        as<int>(table), as<int>(lens), as<int>(n_new), as<int>(granted), ptr(out),
-                       as<float>(lse), ptr(ws), bytes(ws), B, Hq, p.heads, Nq, p.D, p.page, p.n_pages, table.size(1), scale, window, sinks,
-                       code(q), stream_of(p.dev));
+                       as<float>(lse), ptr(ws), bytes(ws), B, Hq, p.heads, Nq, p.D, p.page, p.n_pages,
+                       table.size(1), scale, window, sinks, code(q), stream_of(p.dev));
     });
     return rc == ATTN_OK ? pair(out, lse) : PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS

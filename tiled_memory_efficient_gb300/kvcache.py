@@ -106,7 +106,8 @@ class PagedKVCache:
 
     def reassign(self, parents):
         """Sequence c becomes a copy-on-write child of parents[c] (int32 tensor
-        [n_seqs]; c: kept, -1: freed), all at once, in every layer."""
+        [n_seqs]; c: kept, -1: freed), all at once, in every layer.  With too few free
+        pages every sequence keeps its own content (``info[0]`` is 0 then)."""
         _lib.kvp_reassign(self.table, self.lens, self.refs, parents, self.page_size, self._src,
                           self._dst, self.info, workspace=self._ws)
         self._copy(self.table.shape[0])
