@@ -229,3 +229,49 @@ def test_a_captured_step_follows_the_counts(cuda_lib):
         assert torch.equal(out, wo) and torch.equal(lse, wl)
     assert _lib.sync_status() == _lib.ATTN_OK
     assert torch.equal(held.table, eager.table) and torch.equal(held.lens, eager.lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,Nq,dtype", [(64, 1, 1, F16), (64, 3, 5, BF16), (64, 7, 4, F16), (128, 1, 1, BF16),
+                                          (128, 3, 4, F16), (128, 8, 4, BF16)])
+def test_the_largest_batch(cuda_lib, D, G, Nq, dtype):
+    """1024 sequences, whose lengths and counts live in shared memory."""
+    g = torch.Generator().manual_seed(D + G)
+    lens = torch.randint(0, 60, (1024,), generator=g).tolist()
+    n_new = [min(n, int(torch.randint(0, Nq + 1, (1,), generator=g))) for n in lens]
+    cache = _cache(lens, 1, D, 16, 20, 2, Nq, seed=5)
+    _hide(cache, n_new, 16, 20, 2)
+    q = torch.randn(1024, G, Nq, D, generator=g).to(dtype)
+    out, lse = _lib.kv8_attn(q.cuda(), *(t.cuda() for t in cache), window=20, sinks=2, n_new=_i32(*n_new))
+    assert _lib.sync_status() == _lib.ATTN_OK
+    out, lse = out.cpu(), lse.cpu()
+    some = [c for c in range(1024) if c % 37 == 0 or c > 1015]
+    pick = torch.tensor(some)
+    _check(q[pick], cache[:4] + (cache[4][pick], cache[5][pick]), [n_new[c] for c in some], 20, 2, out[pick], lse[pick],
+           f"1024 sequences D={D}")
+    for c in range(1024):
+        assert bool((out[c, :, n_new[c]:] == 0).all()) and bool((lse[c, :, n_new[c]:] == float("-inf")).all())
+
+
+@pytest.mark.gpu
+def test_pools_past_32_bits(cuda_lib):
+    """Pages whose bytes start past 2^31: append, attention and copies against a small pool
+    that holds the same pages, byte for byte and bit for bit."""
+    Hkv, page, D, n_pages = 8, 64, 128, 40000
+    ids = [39999, 1, 38000, 39000, 20000, 39998, 5, 37777]
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(2, Hkv, 300, D, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(2, 32, 3, D, generator=g).to(BF16).cuda()
+    res = []
+    for n, at in ((n_pages, ids), (len(ids), list(range(len(ids))))):
+        pools = [torch.zeros(n, Hkv, page, D, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+        scales = [torch.ones(n, Hkv, device="cuda") for _ in range(2)]
+        table = _i32(*at[:3], -1, -1, *at[3:]).view(2, 5)
+        _lib.kv8_append(k, v, *pools, *scales, table, _i32(130, 300), n_new=_i32(130, 300))
+        out = _lib.kv8_attn(q, *pools, *scales, table, _i32(130, 300), n_new=_i32(3, 1))
+        _lib.kv8_copy_pages(*pools, *scales, _i32(at[0]), _i32(at[2]), _i32(1))
+        assert _lib.sync_status() == _lib.ATTN_OK
+        res.append([*out, *(p.view(torch.uint8)[at].clone() for p in pools), *(s[at].clone() for s in scales)])
+        del pools, scales
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert bool(res[0][2][0].any()) and torch.equal(res[0][2][0], res[0][2][2])
