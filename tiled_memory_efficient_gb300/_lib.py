@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/attn.h, ffn.h and kvcache.h (argument
+"""ctypes binding of the C ABI in include/attn.h, ffn.h, kvcache.h and rope.h (argument
 marshalling only).
 
 Every step of the computation runs in libattn.so's CUDA kernels; torch is used
@@ -18,7 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libattn.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = [os.path.join(INCLUDE, "attn.h"), os.path.join(INCLUDE, "ffn.h"),
-           os.path.join(INCLUDE, "kvcache.h")]
+           os.path.join(INCLUDE, "kvcache.h"), os.path.join(INCLUDE, "rope.h")]
 
 ATTN_OK = 0
 ATTN_ERR_INVALID = 1
@@ -93,6 +93,8 @@ _SIGNATURES = {
     "kvp_reassign": ([_vp] * 4 + [_i] * 4 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
     "kvp_compact": ([_vp] * 4 + [_i] * 3 + [_vp] * 4 + [ctypes.c_size_t, _vp], _i),
     "kvp_workspace_size": ([_i] * 3, ctypes.c_size_t),
+    "rope_apply": ([_vp] * 6 + [_i] * 8 + [ctypes.c_float, _i, _vp, _i, _vp], _i),
+    "kv8_append_rope": ([_vp] * 13 + [_i, _i, ctypes.c_float] + [_i] * 8 + [_vp, _i, _vp], _i),
     "attn_selftest_timeout": ([ctypes.c_ulonglong, _vp], _i),
     "attn_strerror": ([_i], ctypes.c_char_p),
     "attn_version": ([], _i),
@@ -106,11 +108,11 @@ class AttnError(RuntimeError):
 
 
 def declared_functions() -> list:
-    """Names of the functions include/attn.h, ffn.h and kvcache.h declare."""
+    """Names of the functions include/attn.h, ffn.h, kvcache.h and rope.h declare."""
     names = set()
     for h in HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
-        names.update(re.findall(r"\b((?:attn|ffn|kv8|kvp)_[a-z0-9_]+)\s*\(", text))
+        names.update(re.findall(r"\b((?:attn|ffn|kv8|kvp|rope)_[a-z0-9_]+)\s*\(", text))
     return sorted(names)
 
 
@@ -359,7 +361,8 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
 
 _BOUND = ("kv8_append_step", "kv8_attn_step", "kv8_attn_workspace_size", "kv8_copy_pages",
           "kvp_reserve_step", "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
-          "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size")
+          "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size",
+          "rope_apply", "kv8_append_rope")
 _bind = None
 
 
@@ -559,6 +562,73 @@ def ffn_check_chunking(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4
     return y, rc == ATTN_OK
 
 
+# ------------------------------------------------------------------ rotary positions
+
+def _explain_result(name, out, like):
+    """Raises when `out` cannot take the rows of `like`."""
+    import torch
+    if out is None:
+        return
+    if out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
+        raise ValueError(f"{name} must be a {like.dtype} tensor {tuple(like.shape)} on {like.device}")
+    if torch.is_grad_enabled() and (out.requires_grad or like.requires_grad):
+        raise ValueError(f"{name} is written to behind autograd's back: use the differentiable call")
+    raise ValueError(f"{name} needs dense, 16-byte aligned rows that do not overlap")
+
+
+def _explain_rope(q, k, positions):
+    import torch
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+            raise ValueError(f"{name} must be a CUDA tensor [B, H, N, D]")
+        _dtype_code(t)
+    if k is not None and (k.dtype is not q.dtype or k.device != q.device or k.shape[0] != q.shape[0]
+                          or k.shape[2:] != q.shape[2:]):
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must share dtype, device, B, N and D")
+    if positions is not None:
+        B, _, N, _ = q.shape
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 \
+                or positions.device != q.device or tuple(positions.shape) not in ((N,), (B, N)):
+            raise ValueError(f"positions must be an int32 tensor [{N}] or [{B}, {N}] on {q.device}")
+
+
+def _need_head_dim(rope, q):
+    if q.dim() != 4 or q.shape[3] != rope.head_dim:
+        raise ValueError(f"rows {tuple(q.shape)} are not [B, H, N, {rope.head_dim}]")
+
+
+def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, transposed: bool = False):
+    """q [B, Hq, N, D] and k [B, Hk, N, D] (k None: q alone) turned to positions (int32
+    [N] or [B, N]; None: start + n) by a rope.Rope (include/rope.h): the pair, or q
+    alone.  q_out and k_out may be q and k.  transposed turns back, times the amplitude.
+    Not differentiable: see rotary."""
+    _need_head_dim(rope, q)
+    r = (_bind or _load_bind()).rope(q, k, positions, start, rope.turns(q.device), rope.rotary_dim,
+                                     rope.interleaved, rope.amplitude, q_out, k_out, int(transposed))
+    if type(r) is not int:
+        return r
+
+    def explain():
+        _explain_rope(q, k, positions)
+        if k is None and k_out is not None:
+            raise ValueError("k_out without k")
+        _explain_result("q_out", q_out, q)
+        _explain_result("k_out", k_out, k)
+    _refused("rope_apply", r, explain)
+
+
+def rotary(q, k, rope, positions=None, start: int = 0):
+    """rope as a differentiable function of q and k."""
+    _need_head_dim(rope, q)
+    r = (_bind or _load_bind()).rotary(q, k, positions, start, rope.turns(q.device), rope.rotary_dim,
+                                       rope.interleaved, rope.amplitude)
+    if type(r) is not int:
+        return r
+    _refused("rope_apply", r, lambda: _explain_rope(q, k, positions))
+
+
 # ------------------------------------------------------------------ paged 8-bit KV cache
 
 def _explain_pools(k_pages, v_pages, k_scale, v_scale, layers=False):
@@ -589,16 +659,32 @@ def _need_word(name, t, dev):
         _need(name, t, (1,), torch.int32, dev)
 
 
-def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None, granted=None):
+def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None, granted=None, rope=None,
+               q=None, q_out=None):
     """Quantises new keys and values [B, Hkv, T, D] (any strides that are multiples
     of 8 with dense rows) into the paged cache (include/kvcache.h).  lens [B] are
     the lengths after the call; n_new [B] how many of the T tokens each sequence
     takes (None: all T).  granted [1] (written by kvp_reserve): nothing is appended
-    where it is 0, since lens does not hold the tokens then."""
-    rc = (_bind or _load_bind()).kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new,
-                                            granted)
-    if rc == ATTN_OK:
-        return
+    where it is 0, since lens does not hold the tokens then.
+
+    With rope (a rope.Rope) the keys are turned to the positions they take
+    (include/rope.h), and with q [B, Hq, T, D] the step's queries as well: they are
+    returned, in q_out if given (it may be q)."""
+    bind = _bind or _load_bind()
+    if rope is None:
+        if q is not None or q_out is not None:
+            raise ValueError("queries are only turned with rope")
+        rc = bind.kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new, granted)
+        if rc == ATTN_OK:
+            return None
+    else:
+        if rope.head_dim != k.shape[-1]:
+            raise ValueError(f"the rotation is for head dim {rope.head_dim}, not {k.shape[-1]}")
+        rc = bind.kv8_append_rope(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new, granted,
+                                  rope.turns(k.device), rope.rotary_dim, rope.interleaved, rope.amplitude, q,
+                                  q_out)
+        if type(rc) is not int:
+            return rc
 
     def explain():
         import torch
@@ -615,7 +701,16 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
         if n_new is not None:
             _need("n_new", n_new, (k.shape[0],), torch.int32, dev)
         _need_word("granted", granted, dev)
-    _refused("kv8_append", rc, explain)
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+        else:
+            if not (q.dim() == 4 and q.dtype is k.dtype and q.shape[0] == k.shape[0]
+                    and q.shape[2:] == k.shape[2:] and q.get_device() == dev):
+                raise ValueError(f"q {tuple(q.shape)} must be a {k.dtype} tensor [{k.shape[0]}, Hq, "
+                                 f"{k.shape[2]}, {D}] on CUDA device {dev}")
+            _explain_result("q_out", q_out, q)
+    _refused("kv8_append" if rope is None else "kv8_append_rope", rc, explain)
 
 
 def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,

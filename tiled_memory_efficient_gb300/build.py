@@ -23,8 +23,8 @@ BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["abi.cu", "attn_fwd.cu", "attn_bwd.cu", "bwd_noalloc.cu", "splitkv.cu", "ffn.cu",
-           "vconv.cu", "kv8.cu", "kvp.cu"]
-HEADERS = ["ptx.cuh", "attn_internal.h", "bias.cuh", "window.cuh"]
+           "vconv.cu", "kv8.cu", "kvp.cu", "rope.cu"]
+HEADERS = ["ptx.cuh", "attn_internal.h", "bias.cuh", "window.cuh", "kv8.cuh", "rope.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -44,7 +44,7 @@ def _deps_mtime() -> float:
 
 
 def _public_headers() -> list:
-    return [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h", "kvcache.h")]
+    return [os.path.join(INCLUDE, h) for h in ("attn.h", "ffn.h", "kvcache.h", "rope.h")]
 
 
 def _have_torch() -> bool:

@@ -1,5 +1,5 @@
-// bind.cpp -- Python binding of the sliding-window and cache calls (include/attn.h,
-// kvcache.h): argument checks, output and workspace tensors, the current stream.
+// bind.cpp -- Python binding of the sliding-window, cache and rotary calls (include/attn.h,
+// kvcache.h, rope.h): argument checks, output and workspace tensors, the current stream.
 //
 // A decoding step's kernels take a few microseconds, less than the same checks
 // and allocations take in Python (append: 10.9 us of host time a call there, 3.8 us
@@ -20,11 +20,13 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <set>
 #include <vector>
 
 #include "../../include/attn.h"
 #include "../../include/kvcache.h"
+#include "../../include/rope.h"
 
 namespace {
 
@@ -42,6 +44,8 @@ struct Fns {
     decltype(&attn_fwd_window_workspace_size) fwd_size;
     decltype(&attn_bwd_window) bwd;
     decltype(&attn_bwd_window_workspace_size) bwd_size;
+    decltype(&rope_apply) rope;
+    decltype(&kv8_append_rope) append_rope;
 } fn;
 
 using at::Tensor;
@@ -76,6 +80,18 @@ bool count(PyObject* o, int* out) {
            : overflow < 0 || v < -0x7fffffff ? -0x7fffffff
                                              : static_cast<int>(v);
     return true;
+}
+
+// An integer that 32 bits hold.
+bool whole(PyObject* o, int* out) {
+    int overflow = 0;
+    const long long v = PyLong_AsLongLongAndOverflow(o, &overflow);
+    if (v == -1 && !overflow && PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    *out = static_cast<int>(v);
+    return !overflow && v == *out;
 }
 
 // The softmax scale: None is 1/sqrt(D).
@@ -180,39 +196,132 @@ bool word(PyObject* o, Tensor* out, int64_t dev) {
     return ints(*out, dev, {1});
 }
 
-// (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new | None, granted | None) -> rc
+// What both appends take: (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new | None,
+// granted | None).
+struct Append {
+    Pools p;
+    Tensor k, v, table, lens, n_new, granted;
+    int64_t B = 0, T = 0, st[3] = {};
+    bool read(PyObject* const* a) {
+        k = tensor(a[0]), v = tensor(a[1]), table = tensor(a[6]), lens = tensor(a[7]);
+        if (!p.read(a + 2, false)) return false;
+        if (cuda_of(k) != p.dev || cuda_of(v) != p.dev || k.dim() != 4 || !half(k) ||
+            v.scalar_type() != k.scalar_type() || v.sizes() != k.sizes() || !small(k.sizes()))
+            return false;
+        B = k.size(0), T = k.size(2);
+        if (k.size(1) != p.heads || k.size(3) != p.D) return false;
+        for (int i = 0; i < 3; ++i) {   // strides of dimensions of size 1 do not matter
+            st[i] = k.size(i) == 1 ? 0 : k.stride(i);
+            if (k.size(i) != 1 && v.stride(i) != st[i]) return false;
+        }
+        if (k.stride(3) != 1 || v.stride(3) != 1) return false;
+        if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
+            !ints(lens, p.dev, {B}))
+            return false;
+        if (a[8] != Py_None) {
+            n_new = tensor(a[8]);
+            if (!ints(n_new, p.dev, {B})) return false;
+        }
+        return word(a[9], &granted, p.dev);
+    }
+};
+
+// (Append) -> rc
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 10) MISFIT();
-    const Tensor k = tensor(a[0]), v = tensor(a[1]), table = tensor(a[6]), lens = tensor(a[7]);
-    Pools p;
-    if (!p.read(a + 2, false)) MISFIT();
-    if (cuda_of(k) != p.dev || cuda_of(v) != p.dev || k.dim() != 4 || !half(k) ||
-        v.scalar_type() != k.scalar_type() || v.sizes() != k.sizes() || !small(k.sizes()))
-        MISFIT();
-    const int64_t B = k.size(0), H = k.size(1), T = k.size(2);
-    if (H != p.heads || k.size(3) != p.D) MISFIT();
-    int64_t st[3];
-    for (int i = 0; i < 3; ++i) {   // strides of dimensions of size 1 do not matter
-        st[i] = k.size(i) == 1 ? 0 : k.stride(i);
-        if (k.size(i) != 1 && v.stride(i) != st[i]) MISFIT();
-    }
-    if (k.stride(3) != 1 || v.stride(3) != 1) MISFIT();
-    if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
-        !ints(lens, p.dev, {B}))
-        MISFIT();
-    Tensor n_new, granted;
-    if (a[8] != Py_None) {
-        n_new = tensor(a[8]);
-        if (!ints(n_new, p.dev, {B})) MISFIT();
-    }
-    if (!word(a[9], &granted, p.dev)) MISFIT();
+    Append x;
+    if (n != 10 || !x.read(a)) MISFIT();
+    const Pools& p = x.p;
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
     return PyLong_FromLong(unlocked([&] {
-        return fn.append(ptr(k), ptr(v), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
-                         as<int>(table), as<int>(lens), as<int>(n_new), as<int>(granted), B, p.heads, T,
-                         p.D, p.page, p.n_pages, table.size(1), st[0], st[1], st[2], code(k), stream_of(p.dev));
+        return fn.append(ptr(x.k), ptr(x.v), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
+                         as<int>(x.table), as<int>(x.lens), as<int>(x.n_new), as<int>(x.granted), x.B, p.heads,
+                         x.T, p.D, p.page, p.n_pages, x.table.size(1), x.st[0], x.st[1], x.st[2], code(x.k),
+                         stream_of(p.dev));
     }));
+    END_HANDLE_TH_ERRORS
+}
+
+// A rotation: its frequencies on a device and what the C calls take beside them.
+struct Turns {
+    Tensor turns;
+    int rot = 0, interleaved = 0;
+    float amp = 1.0f;
+    // (turns, rot, interleaved, amplitude)
+    bool read(PyObject* const* a, int64_t dev) {
+        turns = tensor(a[0]);
+        float x;
+        if (!whole(a[1], &rot) || !whole(a[2], &interleaved) || a[3] == Py_None || !scale_of(a[3], 1, &x))
+            return false;
+        amp = x;
+        return rot > 0 && fits(turns, dev, at::kLong, {rot / 2});
+    }
+    const unsigned long long* at() const { return as<unsigned long long>(turns); }
+};
+
+// Whether the C calls can read rows where they lie; strides of dimensions of size 1 do not matter.
+bool in_place(const Tensor& t) {
+    if (t.stride(3) != 1 || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16) return false;
+    for (int i = 0; i < 3; ++i)
+        if (t.size(i) != 1 && t.stride(i) % 8) return false;
+    return true;
+}
+void strides_of(const Tensor& t, long long* st) {
+    for (int i = 0; i < 3; ++i) st[i] = t.size(i) == 1 ? 0 : t.stride(i);
+}
+Tensor readable(const Tensor& t) { return in_place(t) ? t : t.clone(at::MemoryFormat::Contiguous); }
+
+// A given result for `like`: rows that no two elements share, of a tensor that no graph follows
+// (its version is counted on, as any call that writes to it does).
+bool result_for(const Tensor& out, const Tensor& like) {
+    if (!like.defined() || cuda_of(out) != cuda_of(like) || out.scalar_type() != like.scalar_type() ||
+        out.sizes() != like.sizes() || !in_place(out))
+        return false;
+    for (int i = 0; i < 3; ++i)
+        if (out.size(i) != 1 && out.stride(i) == 0) return false;
+    if (at::GradMode::is_enabled() && (out.requires_grad() || like.requires_grad())) return false;
+    if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+    return true;
+}
+
+// (Append, turns, rot, interleaved, amplitude, q | None, q_out | None) -> q_out, None or rc
+PyObject* py_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Append x;
+    Turns r;
+    if (n != 16 || !x.read(a) || !r.read(a + 10, x.p.dev)) MISFIT();
+    const Pools& p = x.p;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
+    long long st[9] = {x.st[0], x.st[1], x.st[2]};
+    Tensor q, out;
+    if (a[14] != Py_None) {
+        q = tensor(a[14]);
+        if (cuda_of(q) != p.dev || q.dim() != 4 || q.scalar_type() != x.k.scalar_type() || q.size(0) != x.B ||
+            q.size(2) != x.T || q.size(3) != p.D || !small(q.sizes()))
+            MISFIT();
+        if (a[15] == Py_None) {
+            q = readable(q);
+            out = empty(q.sizes(), q.scalar_type(), p.dev);
+        } else {
+            out = tensor(a[15]);
+            if (!result_for(out, q)) MISFIT();
+            if (out.data_ptr() != q.data_ptr()) q = readable(q);
+        }
+        strides_of(q, st + 3);
+        strides_of(out, st + 6);
+    } else if (a[15] != Py_None) {
+        MISFIT();
+    }
+    const int rc = unlocked([&] {
+        return fn.append_rope(ptr(x.k), ptr(x.v), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
+                              as<int>(x.table), as<int>(x.lens), as<int>(x.n_new), as<int>(x.granted), ptr(q),
+                              ptr(out), r.at(), r.rot, r.interleaved, r.amp, x.B, q.defined() ? q.size(1) : 0,
+                              p.heads, x.T, p.D, p.page, p.n_pages, x.table.size(1), st, code(x.k),
+                              stream_of(p.dev));
+    });
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    if (!out.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
 
@@ -570,6 +679,151 @@ PyObject* py_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Rotary positions of q and, if there is one, k.
+struct RopeCall {
+    Tensor q, k, positions;
+    Turns r;
+    int start = 0, transposed = 0;
+    bool read(const Tensor& q_, const Tensor& k_, const Tensor& positions_) {
+        q = q_, k = k_, positions = positions_;
+        const int64_t dev = cuda_of(q);
+        if (dev < 0 || q.dim() != 4 || !half(q) || !small(q.sizes())) return false;
+        if (k.defined() && (cuda_of(k) != dev || k.dim() != 4 || k.scalar_type() != q.scalar_type() ||
+                            k.size(0) != q.size(0) || k.size(2) != q.size(2) || k.size(3) != q.size(3) ||
+                            !small(k.sizes())))
+            return false;
+        if (positions.defined()) {   // [N] or [B, N]
+            const int64_t d = positions.dim();
+            if (cuda_of(positions) != dev || positions.scalar_type() != at::kInt || (d != 1 && d != 2) ||
+                positions.size(d - 1) != q.size(2) || (d == 2 && positions.size(0) != q.size(0)))
+                return false;
+        }
+        return true;
+    }
+    int64_t dev() const { return q.get_device(); }
+    // q_out and k_out are given, or made here: contiguous, as the attention takes them.
+    int run(Tensor* q_out, Tensor* k_out) const {
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev()));
+        const Tensor x = q_out->defined() && q_out->data_ptr() == q.data_ptr() ? q : readable(q);
+        const Tensor y = !k.defined() || (k_out->defined() && k_out->data_ptr() == k.data_ptr()) ? k : readable(k);
+        if (!q_out->defined()) *q_out = empty(q.sizes(), q.scalar_type(), dev());
+        if (k.defined() && !k_out->defined()) *k_out = empty(k.sizes(), k.scalar_type(), dev());
+        long long st[14] = {};
+        strides_of(x, st);
+        strides_of(*q_out, st + 6);
+        if (k.defined()) {
+            strides_of(y, st + 3);
+            strides_of(*k_out, st + 9);
+        }
+        if (positions.defined()) {
+            st[12] = positions.dim() == 2 ? positions.stride(0) : 0;
+            st[13] = positions.stride(positions.dim() - 1);
+        }
+        return fn.rope(ptr(x), ptr(y), ptr(*q_out), ptr(*k_out), r.at(), as<int>(positions), start, x.size(0),
+                       x.size(1), k.defined() ? k.size(1) : 0, x.size(2), x.size(3), r.rot, r.interleaved, r.amp,
+                       transposed, st, code(x), stream_of(dev()));
+    }
+};
+
+// The rotation as a function of the autograd graph.  It is linear in its rows: the gradient is
+// the transposed rotation of theirs, as a function of the graph again.
+struct Rotary : torch::autograd::Function<Rotary> {
+    using Context = torch::autograd::AutogradContext;
+    using Maybe = std::optional<Tensor>;   // (an argument that is an undefined tensor is an error there)
+    static Maybe maybe(const Tensor& t) { return t.defined() ? Maybe(t) : std::nullopt; }
+    static torch::autograd::variable_list forward(Context* ctx, const Tensor& q, const Maybe& k_,
+                                                  const Maybe& positions_, const Tensor& turns, int64_t start,
+                                                  int64_t rot, int64_t interleaved, double amp, int64_t transposed) {
+        RopeCall c;
+        const Tensor k = k_.value_or(Tensor()), positions = positions_.value_or(Tensor());
+        if (!c.read(q, k, positions)) throw Refused{kMisfit};
+        c.r.turns = turns, c.r.rot = static_cast<int>(rot), c.r.interleaved = static_cast<int>(interleaved);
+        c.r.amp = static_cast<float>(amp);
+        c.start = static_cast<int>(start), c.transposed = static_cast<int>(transposed);
+        Tensor q_out, k_out;
+        if (const int rc = c.run(&q_out, &k_out)) throw Refused{rc};
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({positions, turns});
+        ctx->saved_data["start"] = start;
+        ctx->saved_data["rot"] = rot;
+        ctx->saved_data["interleaved"] = interleaved;
+        ctx->saved_data["amp"] = amp;
+        ctx->saved_data["transposed"] = transposed;
+        if (!k.defined()) return {q_out};
+        return {q_out, k_out};
+    }
+    static torch::autograd::variable_list backward(Context* ctx, torch::autograd::variable_list grads) {
+        check_captured_backward();
+        const auto saved = ctx->get_saved_variables();
+        torch::autograd::variable_list out(9);
+        const bool two = grads.size() > 1 && grads[1].defined();
+        if (!grads[0].defined() && !two) return out;
+        // the first of them that there is takes q's place
+        const int first = grads[0].defined() ? 0 : 1;
+        try {
+            auto g = apply(grads[first], first == 0 && two ? Maybe(grads[1]) : Maybe(), maybe(saved[0]), saved[1],
+                           ctx->saved_data["start"].toInt(), ctx->saved_data["rot"].toInt(),
+                           ctx->saved_data["interleaved"].toInt(), ctx->saved_data["amp"].toDouble(),
+                           1 - ctx->saved_data["transposed"].toInt());
+            out[first] = g[0];
+            if (g.size() > 1) out[1] = g[1];
+        } catch (const Refused& r) {
+            TORCH_CHECK(false, "rope_apply failed with status ", r.rc);
+        }
+        return out;
+    }
+};
+
+// Wraps q' and, if there is one, k'.
+PyObject* rotated(const Tensor& q, const Tensor& k) { return k.defined() ? pair(q, k) : THPVariable_Wrap(q); }
+
+// (q, k | None, positions | None, start, turns, rot, interleaved, amplitude) -> q', (q', k') or rc;
+// differentiable
+PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    RopeCall c;
+    if (n != 8 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
+        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a + 4, c.dev()))
+        MISFIT();
+    Tensor q_out, k_out;
+    const bool graph = at::GradMode::is_enabled() &&
+                       (c.q.requires_grad() || (c.k.defined() && c.k.requires_grad()));
+    const int rc = unlocked([&] {
+        if (!graph) return c.run(&q_out, &k_out);
+        try {
+            auto r = Rotary::apply(c.q, Rotary::maybe(c.k), Rotary::maybe(c.positions), c.r.turns, c.start, c.r.rot, c.r.interleaved, c.r.amp, 0);
+            q_out = r[0];
+            if (r.size() > 1) k_out = r[1];
+        } catch (const Refused& r) {
+            return r.rc;
+        }
+        return static_cast<int>(ATTN_OK);
+    });
+    return rc == ATTN_OK ? rotated(q_out, k_out) : PyLong_FromLong(rc);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k | None, positions | None, start, turns, rot, interleaved, amplitude, q_out | None,
+//  k_out | None, transposed) -> q', (q', k') or rc
+PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    RopeCall c;
+    if (n != 11 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
+        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a + 4, c.dev()) ||
+        !whole(a[10], &c.transposed))
+        MISFIT();
+    Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+        if (a[8 + i] == Py_None) continue;
+        const Tensor& like = i == 0 ? c.q : c.k;
+        out[i] = tensor(a[8 + i]);
+        if (!result_for(out[i], like)) MISFIT();
+    }
+    const int rc = unlocked([&] { return c.run(&out[0], &out[1]); });
+    return rc == ATTN_OK ? rotated(out[0], out[1]) : PyLong_FromLong(rc);
+    END_HANDLE_TH_ERRORS
+}
+
 // (addresses of the C entry points, in Fns' order)
 PyObject* py_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* at[sizeof(Fns) / sizeof(void*)];
@@ -600,6 +854,9 @@ PyMethodDef methods[] = {METHOD("init", py_init),
                          METHOD("attn_fwd_window", py_fwd),
                          METHOD("attn_bwd_window", py_bwd),
                          METHOD("window_attention", py_window),
+                         METHOD("rope", py_rope),
+                         METHOD("rotary", py_rotary),
+                         METHOD("kv8_append_rope", py_append_rope),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

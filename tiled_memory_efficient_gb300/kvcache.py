@@ -84,13 +84,16 @@ class PagedKVCache:
                          self.info, window=self.window, sinks=self.sinks, workspace=self._ws,
                          granted=self.granted)
 
-    def append(self, layer: int, k, v, n_new=None):
+    def append(self, layer: int, k, v, n_new=None, rope=None, q=None):
         """Stores the keys and values [n_seqs, n_kv_heads, T, head_dim] of the tokens
         that ``reserve`` made room for (n_new of the T each; None: all T); none when it
-        found no room."""
-        _lib.kv8_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
-                        self.v_scale[layer], self.table, self.lens,
-                        n_new=None if n_new is None else self._counts(n_new), granted=self.granted)
+        found no room.  With rope (a ``rope.Rope``) the keys are turned to their positions
+        on the way, and the step's queries q [n_seqs, Hq, T, head_dim], if given, as
+        well: they are returned, rows from n_new on as 0."""
+        return _lib.kv8_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
+                               self.v_scale[layer], self.table, self.lens,
+                               n_new=None if n_new is None else self._counts(n_new), granted=self.granted,
+                               rope=rope, q=q)
 
     def attend(self, layer: int, q, scale: float | None = None, n_new=None):
         """(out, lse) of the newest positions q [n_seqs, Hq, Nq, head_dim].  n_new as in
