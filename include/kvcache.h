@@ -129,6 +129,52 @@ int kv8_attn_step(const void* q, const void* k_pages, const void* v_pages, const
 size_t kv8_attn_workspace_size(int B, int Hq, int Hkv, int Nq, int D);
 
 /*
+ * Which sequences begin with the same pages, as kvp_reassign leaves them: fills plan
+ * (kvp_plan_words(n_seqs) int32 on the device) for kv8_attn_shared.  Sequences whose
+ * first pages are the same, in whole runs of 128 positions, form a group; where some of
+ * them share more than the others, each joins the group that leaves it the least to
+ * read.  A group is kept when reading its prefix once saves min_saved
+ * positions or more (members less one, times the prefix; below about KVP_MIN_SAVED the
+ * plain attention is the faster one).  table [n_seqs, max_pages] and lens are not changed.  n_seqs <= 1024.
+ *
+ * The plan stays right while every sequence keeps the pages it begins with: appends, kvp_reserve
+ * without a window and kvp_compact keep them; after kvp_reassign it is made anew.  (Work
+ * grows with n_seqs^2 times the prefix's runs: it is for a fork, not for every step.)
+ */
+#define KVP_MIN_SAVED 8192
+
+int kvp_find_shared(const int* table, const int* lens, int n_seqs, int max_pages, int page,
+                    int min_saved, int* plan, void* stream);
+
+/* int32 words of a plan; 0 for invalid counts.  Host-only. */
+size_t kvp_plan_words(int n_seqs);
+
+/*
+ * kv8_attn_step, without a window, for sequences that share prefixes: the prefix of a
+ * group is read once for all rows of its sequences (which then meet it as one matrix on
+ * the tensor cores), the rest as there, and the two parts are merged by their LSEs in
+ * fp32.  plan is kvp_find_shared's for the same table; something else than a plan for B
+ * sequences is recorded like a bad page, and every sequence then reads for itself.
+ * n_new and granted as in kv8_attn_step, other arguments and limits as in kv8_attn; up to 2^20
+ * rows (G Nq) of a KV head.
+ *
+ * Within a group's prefix the values of 128 positions meet the product at one power of two, the
+ * largest of their pages' scales and of those before: where scales differ by more than 2^15 the
+ * smaller ones' values lose bits that stand 2^-33 below the larger's magnitude.  A
+ * NaN or infinity in a value of the prefix reaches all rows of the group's
+ * sequences, those before its position too.
+ * workspace: kv8_attn_shared_workspace_size() bytes.
+ */
+int kv8_attn_shared(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                    const float* v_scale, const int* table, const int* lens, const int* n_new,
+                    const int* granted, const int* plan, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int D, int page,
+                    int n_pages, int max_pages, float scale, int dtype, void* stream);
+
+/* Workspace bytes of kv8_attn_shared on the current device; 0 for invalid sizes. */
+size_t kv8_attn_shared_workspace_size(int B, int Hq, int Hkv, int Nq, int D);
+
+/*
  * Copies pages src[i] to dst[i], keys, values and scales, for i < min(*count,
  * max_count), in each of n_layers pools that follow one another ([n_layers,
  * n_pages, ...]).  src, dst and count are device arrays; no dst may be a src or

@@ -1,0 +1,418 @@
+"""Attention over the paged 8-bit cache for sequences that share prefixes: the plan against a model of it,
+the attention against each sequence's definition alone (tests/kv8_ref.py), with the tolerances of the
+other forwards (tests/helpers.py): scores of exact keys, softmax terms in fp16 (2^-11 of themselves), sums
+and the merge of prefix and rest in fp32, as there."""
+import random
+
+import pytest
+import torch
+
+from tests import helpers, kv8_ref
+from tiled_memory_efficient_gb300 import _lib
+
+F16, BF16, F8 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
+P = 256  # a fake, 16-byte-aligned "device" address: validation fails before any use
+RUN = 128    # positions that are shared or not together
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    return _lib.load()
+
+
+CALL = dict(q=P, kp=P, vp=P, ks=P, vs=P, table=P, lens=P, n_new=P, granted=P, plan=P, out=P, lse=P, ws=P, n=1 << 40, B=2,
+            Hq=4, Hkv=2, Nq=1, D=64, page=64, n_pages=10, max_pages=5, scale=0.1, dtype=0)
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"q": 0}, 1), ({"plan": 0}, 1), ({"ws": 0}, 1), ({"Hq": 3}, 1), ({"B": 0}, 1), ({"scale": 0.0}, 1), ({"dtype": 3}, 1),
+    ({"D": 96}, 2), ({"page": 48}, 2), ({"B": 1025}, 2), ({"kp": P + 8}, 3), ({"plan": P + 2}, 3), ({"n_new": P + 1}, 3),
+    ({"n": 16}, 6),
+])
+def test_attention_refusals(lib, change, code):
+    assert lib.kv8_attn_shared(*{**CALL, **change}.values(), None) == code
+
+
+FIND = dict(table=P, lens=P, n=4, max_pages=5, page=64, least=0, plan=P)
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"table": 0}, 1), ({"plan": 0}, 1), ({"n": 0}, 1), ({"least": -1}, 1), ({"max_pages": 0}, 1), ({"n": 1025}, 2),
+    ({"page": 20}, 2), ({"lens": P + 2}, 3), ({"max_pages": 1 << 28}, 2),
+])
+def test_plan_refusals(lib, change, code):
+    assert lib.kvp_find_shared(*{**FIND, **change}.values(), None) == code
+
+
+def test_plan_sizes(lib):
+    assert lib.kvp_plan_words(0) == 0 and lib.kvp_plan_words(1025) == 0 and lib.kvp_plan_words(3) >= 4 + 3 * 7
+    assert lib.kv8_attn_shared_workspace_size(2, 4, 2, 1, 96) == 0
+    assert lib.kv8_attn_shared_workspace_size(2, 4, 2, 1, 64) > lib.kv8_attn_workspace_size(2, 4, 2, 1, 64)
+
+
+# ------------------------------------------------------------------ the plan
+
+def _plan_model(table, lens, page, least):
+    """{first sequence: (members, runs)} of the groups that are kept."""
+    B, cols = len(lens), RUN // page
+    full = [min(max(n, 0), len(table[0]) * page) // RUN for n in lens]
+    depth = []
+    for b in range(B):
+        best = (0.0, 0)
+        for i in range(full[b]):
+            c = (i + 1) * cols - 1
+            r = sum(table[k][c] == table[b][c] and full[k] > i for k in range(B)) if table[b][c] >= 0 else 0
+            if r > 1:
+                best = max(best, ((i + 1) * (r - 1) / r, i + 1))
+        depth.append(best[1])
+    groups = {}
+    for b in range(B):
+        d = depth[b]
+        if d == 0:
+            continue
+        key = (d, table[b][d * cols - 1])
+        first = next(k for k in range(B) if depth[k] == d and table[k][d * cols - 1] == key[1])
+        if table[first][:d * cols] == table[b][:d * cols]:
+            groups.setdefault(first, ([], d))[0].append(b)
+    return {f: (m, d) for f, (m, d) in groups.items() if len(m) > 1 and (len(m) - 1) * d * RUN >= least}
+
+
+def _read_plan(plan, B):
+    w = plan.tolist()
+    at = lambda a: w[4 + a * B: 4 + (a + 1) * B]
+    groups = {}
+    for g in range(w[1]):
+        m = at(3)[at(0)[g]: at(0)[g] + at(1)[g]]
+        groups[m[0]] = (m, at(2)[g])
+        for rank, b in enumerate(m):
+            assert at(4)[b] == g and at(5)[b] == rank and at(6)[b] == at(2)[g] * RUN
+    held = {b for m, _ in groups.values() for b in m}
+    assert all(at(4)[b] == -1 and at(6)[b] == 0 for b in range(B) if b not in held)
+    return groups
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(8))
+def test_plans_match_the_model(cuda_lib, seed):
+    """Random forks of forks: nested prefixes, lengths inside them, empty sequences."""
+    rng = random.Random(seed)
+    page, B = rng.choice([16, 32, 64, 128]), rng.choice([2, 7, 33, 60])
+    most = rng.choice([4, 20]) * RUN // page
+    ids = iter(range(1, 10 ** 6))
+    rows, lens = [], []
+    for b in range(B):
+        if rows and rng.random() < 0.8:
+            k = rng.randrange(len(rows))
+            keep = rng.randint(0, lens[k] // page)
+            row = rows[k][:keep]
+        else:
+            row = []
+        n = rng.choice([0, len(row) * page + rng.randint(0, most * page)]) if rng.random() < 0.15 else \
+            min(len(row) * page + rng.randint(1, most * page // 2), most * page)
+        while len(row) * page < n:
+            row.append(next(ids))
+        rows.append(row[: -(-n // page)])
+        lens.append(n)
+    width = max(max(map(len, rows)), 1)
+    table = [r + [-1] * (width - len(r)) for r in rows]
+    lens = [min(n, width * page) for n in lens]
+    for least in (0, 600):
+        plan = _lib.kvp_find_shared(_i32(table), _i32(lens), page, least)
+        assert _read_plan(plan, B) == _plan_model(table, lens, page, least)
+    again = _lib.kvp_find_shared(_i32(table), _i32(lens), page, least, plan=torch.zeros_like(plan))
+    assert torch.equal(plan, again)
+
+
+@pytest.mark.gpu
+def test_pages_in_another_order_are_not_a_prefix(cuda_lib):
+    """Tables that meet in a page without the same beginning share nothing."""
+    table = [[5, 6, 7, 8], [6, 5, 7, 8], [5, 6, 7, 9]]
+    plan = _lib.kvp_find_shared(_i32(table), _i32([512, 512, 512]), 128, 0)
+    assert _read_plan(plan, 3) == _plan_model(table, [512] * 3, 128, 0)
+    for m, d in _read_plan(plan, 3).values():
+        assert all(table[b][:d] == table[m[0]][:d] for b in m)
+
+
+@pytest.mark.gpu
+def test_the_largest_plan(cuda_lib):
+    """1024 sequences in 300 groups."""
+    g = torch.Generator().manual_seed(1)
+    of = torch.randint(0, 300, (1024,), generator=g)
+    table = torch.stack([of * 2, of * 2 + 1, 1000 + torch.arange(1024)], 1).int()
+    lens = torch.full((1024,), 300, dtype=torch.int32)
+    plan = _lib.kvp_find_shared(table.cuda(), lens.cuda(), 128, 0)
+    assert _read_plan(plan, 1024) == _plan_model(table.tolist(), lens.tolist(), 128, 0)
+
+
+# ------------------------------------------------------------------ the attention
+
+def _batch(groups, tails, alone, Hkv, D, page, seed, spread=3):
+    """A cache of sequences that share: groups = [(positions, members)], members interleaved; tails: own
+    positions of each member in turn; alone: lengths of sequences that share nothing.  Scales of
+    2^-spread .. 2^spread."""
+    g = torch.Generator().manual_seed(seed)
+    rng = random.Random(seed)
+    order = [i for i, (_, m) in enumerate(groups) for _ in range(m)] + [-1] * len(alone)
+    rng.shuffle(order)
+    heads = [-(-n // page) for n, _ in groups]
+    lens, rows, next_page, alone, tails = [], [], 0, list(alone), list(tails)
+    shared = []
+    for h in heads:
+        shared.append(list(range(next_page, next_page + h)))
+        next_page += h
+    k = 0
+    for i in order:
+        if i < 0:
+            n, row = alone.pop(), []
+        else:
+            t = tails[k % len(tails)]
+            k += 1
+            # a member's own positions begin on a page of its own
+            row, n = list(shared[i]), len(shared[i]) * page + t
+        while len(row) * page < n:
+            row.append(next_page)
+            next_page += 1
+        rows.append(row)
+        lens.append(n)
+    width = max(map(len, rows)) + 1
+    n_pages = next_page + 2
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    table = torch.tensor([[perm[i] for i in r] + [-1] * (width - len(r)) for r in rows], dtype=torch.int32)
+    pools = []
+    for amp in (0.5, 1.0):
+        x = torch.randn(n_pages, Hkv, page, D, generator=g)
+        e = torch.randint(-spread, spread + 1, (n_pages, Hkv), generator=g)
+        s = torch.ldexp(torch.ones(n_pages, Hkv), e)
+        pools += [(x * amp / s[:, :, None, None]).clamp(-448, 448).to(F8), s]
+    return pools[0], pools[2], pools[1], pools[3], table, torch.tensor(lens, dtype=torch.int32)
+
+
+def _check(q, cache, n_new, out, lse, what, some=None):
+    out, lse = out.double().cpu(), lse.double().cpu()
+    for b in range(q.shape[0]) if some is None else some:
+        n = q.shape[2] if n_new is None else n_new[b]
+        assert bool((out[b, :, n:] == 0).all()) and bool((lse[b, :, n:] == float("-inf")).all()), (what, b)
+        if n:
+            one = cache[:4] + (cache[4][b:b + 1], cache[5][b:b + 1])
+            ro, rl = kv8_ref.attention(q[b:b + 1, :, :n], *one)
+            helpers.assert_fwd_close(out[b, :, :n].numpy(), lse[b, :, :n].numpy(), ro[0].numpy(), rl[0].numpy(), q.dtype,
+                                     f"{what} sequence {b}")
+
+
+CASES = [
+    # Hq, Hkv, Nq, D, page, groups, tails, alone, dtype
+    (1, 1, 1, 64, 64, [(128, 2)], [1, 1], [], F16),
+    (1, 1, 1, 128, 128, [(128, 2)], [1, 5], [], BF16),
+    (4, 2, 1, 64, 16, [(300, 3)], [7, 130, 64], [50], F16),             # 256 of 304 positions are shared
+    (14, 2, 1, 64, 32, [(1000, 5)], [1, 40, 300], [], BF16),
+    (8, 2, 1, 128, 64, [(640, 9), (128, 2)], [3, 99, 0], [1, 700], F16),  # members without own positions
+    (16, 4, 3, 128, 16, [(500, 6), (260, 4)], [3, 50, 2, 1], [9], BF16),  # queries that stand in the prefix
+    (8, 1, 1, 64, 64, [(2048, 20)], [10, 60], [], F16),                 # 160 rows: a second Q tile
+    (8, 1, 2, 128, 128, [(1408, 21)], [2, 77], [300], BF16),            # 336 rows: a second row block
+    (32, 8, 1, 128, 32, [(384, 40)], [20, 33], [], F16),
+    (7, 1, 5, 64, 16, [(256, 4), (384, 4), (128, 3)], [5, 6, 40], [], BF16),
+    (2, 2, 1, 64, 128, [(12800, 3)], [4000, 1], [], F16),               # own positions over many CTAs
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attention_matches_the_definition(cuda_lib, case):
+    Hq, Hkv, Nq, D, page, groups, tails, alone, dtype = case
+    cache = _batch(groups, tails, alone, Hkv, D, page, seed=Hq + D)
+    B = cache[5].numel()
+    q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+    found = _read_plan(plan, B)
+    assert sorted((d * RUN, len(m)) for m, d in found.values()) == sorted(
+        (-(-n // page) * page // RUN * RUN, m) for n, m in groups)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
+    assert _lib.sync_status() == _lib.ATTN_OK
+    _check(q, cache, None, out, lse, f"shared {case}")
+    again = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    # a plan without groups is the plain call, bit for bit
+    none = _lib.kvp_find_shared(dev[4], dev[5], page, (1 << 31) - 1)
+    assert _read_plan(none, B) == {}
+    a, b = _lib.kv8_attn_shared(q.cuda(), *dev, none), _lib.kv8_attn(q.cuda(), *dev)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,Nq,D,page,dtype", [(8, 2, 4, 64, 16, F16), (6, 1, 3, 128, 64, BF16)])
+def test_ragged_steps(cuda_lib, Hq, Hkv, Nq, D, page, dtype):
+    """Counts of 0 to Nq, more queries than own positions, and a step without room."""
+    cache = _batch([(700, 6), (256, 3)], [Nq, 40, 1, 100], [5, 0], Hkv, D, page, seed=3)
+    B, rng = cache[5].numel(), random.Random(5)
+    n_new = [min(rng.randint(0, Nq), int(n)) for n in cache[5]]
+    q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(2)).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new), granted=_i32([1]))
+    assert _lib.sync_status() == _lib.ATTN_OK
+    _check(q, cache, n_new, out, lse, f"shared ragged D={D}")
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new), granted=_i32([0]))
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all()) and _lib.sync_status() == _lib.ATTN_OK
+    # a count that does not fit: that sequence sees nothing, the others what they saw
+    good = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new))
+    victim = _read_plan(plan, B).popitem()[1][0][1]
+    bad = [Nq + 1 if b == victim else n for b, n in enumerate(n_new)]
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(bad))
+    assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+    assert bool((out[victim] == 0).all()) and bool((lse[victim] == float("-inf")).all())
+    for b in range(B):
+        if b != victim and n_new[b]:
+            helpers.assert_fwd_close(*(x[b, :, :n_new[b]].double().cpu().numpy() for x in (out, lse, *good)), q.dtype,
+                                     "shared, bad count")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,page,dtype", [(64, 16, F16), (128, 32, BF16)])
+def test_pages_of_very_different_scales(cuda_lib, D, page, dtype):
+    """Scales of 2^-9 to 2^9 beside each other, and positions far apart in size."""
+    cache = _batch([(1200, 5)], [30, 200], [], 2, D, page, seed=9, spread=9)
+    q = torch.randn(5, 8, 1, D, generator=torch.Generator().manual_seed(4)).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
+    _check(q, cache, None, out, lse, f"shared, scales D={D}")
+    # queries whose largest value is far from 1 (bf16 reaches further than the fp16 products)
+    q = q * 2.0 ** (-10 if dtype is F16 else 30)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, scale=D ** -0.5 * 2.0 ** (10 if dtype is F16 else -30))
+    _check_scaled(q, cache, out, lse, D, dtype)
+    assert _lib.sync_status() == _lib.ATTN_OK
+
+
+def _check_scaled(q, cache, out, lse, D, dtype):
+    scale = D ** -0.5 * 2.0 ** (10 if dtype is F16 else -30)
+    ro, rl = kv8_ref.attention(q, *cache, scale=scale)
+    helpers.assert_fwd_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), ro.numpy(), rl.numpy(), dtype,
+                             f"shared, scaled queries D={D}")
+
+
+@pytest.mark.gpu
+def test_bad_pages_and_plans_are_recorded(cuda_lib):
+    cache = _batch([(512, 4)], [20, 60], [77], 2, 64, 32, seed=11)
+    q = torch.randn(5, 4, 1, 64, generator=torch.Generator().manual_seed(2)).to(F16)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], 32, 0)
+    first = _read_plan(plan, 5).popitem()[1][0][0]
+    # pages of the prefix outside the pool: their positions are not seen
+    table = cache[4].clone()
+    for col, pid in ((3, -1), (9, 10 ** 6)):
+        table[first, col] = pid
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev[:4], table.cuda(), dev[5], plan)
+    assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+    for b in range(5):
+        if int(cache[5][b]) < 512:
+            keep = list(range(int(cache[5][b])))
+        else:
+            keep = [t for t in range(int(cache[5][b])) if t // 32 not in (3, 9)]
+        k, v = (kv8_ref.dense(p, s, cache[4][b], int(cache[5][b]))[:, keep] for p, s in ((cache[0], cache[2]), (cache[1], cache[3])))
+        s = (q[b].double().view(2, 2, 64) @ k.transpose(1, 2)) / 8.0
+        ref = torch.softmax(s, -1) @ v
+        helpers.assert_fwd_close(out[b].double().cpu().numpy(), lse[b].double().cpu().numpy(), ref.view(4, 1, 64).numpy(),
+                                 torch.logsumexp(s, -1).view(4, 1).numpy(), F16, f"bad pages, sequence {b}")
+    # what is not a plan: recorded, and every sequence reads for itself
+    want = _lib.kv8_attn(q.cuda(), *dev)
+    other = _lib.kvp_find_shared(dev[4][:4].contiguous(), dev[5][:4].contiguous(), 32, 0)
+    for junk in (torch.zeros_like(plan), torch.full_like(plan, 10 ** 9), torch.cat([other, other])[: plan.numel()]):
+        out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, junk)
+        assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(ValueError, match="plan"):
+        _lib.kv8_attn_shared(q.cuda(), *dev, plan[:-1])
+    with pytest.raises(ValueError, match="plan"):
+        _lib.kv8_attn_shared(q.cuda(), *dev, None)
+    with pytest.raises(ValueError, match="lens"):
+        _lib.kvp_find_shared(dev[4], dev[5].long(), 32)
+    with pytest.raises(_lib.AttnError):
+        _lib.kvp_find_shared(dev[4], dev[5], 48)
+    assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_special_values(cuda_lib):
+    """A NaN key or value of the prefix reaches the group's rows; one behind every row's end does not."""
+    cache = _batch([(256, 3)], [10, 20], [64], 1, 64, 32, seed=13)
+    q = torch.randn(4, 2, 1, 64, generator=torch.Generator().manual_seed(2)).to(F16)
+    plan = _lib.kvp_find_shared(cache[4].cuda(), cache[5].cuda(), 32, 0)
+    group = _read_plan(plan, 4).popitem()[1][0]
+    alone = [b for b in range(4) if b not in group]
+    clean = _lib.kv8_attn_shared(q.cuda(), *(t.cuda() for t in cache), plan)
+    for w in (0, 1):
+        pools = [t.clone() for t in cache]
+        pools[w].view(torch.uint8)[int(cache[4][group[0], 2]), 0, 5, 7] = 0x7F
+        out, lse = _lib.kv8_attn_shared(q.cuda(), *(t.cuda() for t in pools), plan)
+        assert bool(torch.isnan(out[group, :, :, 7]).all()) and torch.equal(out[alone], clean[0][alone])
+        assert bool(torch.isnan(lse[group]).all() if w == 0 else torch.isfinite(lse[group]).all())
+    # garbage past the ends
+    pools = [t.clone() for t in cache]
+    for b in range(4):
+        n = int(cache[5][b])
+        if n % 32:
+            for w in (0, 1):
+                pools[w].view(torch.uint8)[int(cache[4][b, n // 32]), :, n % 32:] = 0x7F
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *(t.cuda() for t in pools), plan)
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.gpu
+def test_captured_and_side_by_side(cuda_lib):
+    """Replayed on other queries and lengths, the workspace kept; two calls on two streams at once."""
+    cache = _batch([(1024, 7)], [40, 90], [10], 2, 128, 64, seed=17)
+    dev = [t.cuda() for t in cache]
+    g = torch.Generator().manual_seed(3)
+    qs = [torch.randn(8, 8, 1, 128, generator=g).to(BF16).cuda() for _ in range(4)]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], 64, 0)
+    want = [_lib.kv8_attn_shared(q, *dev, plan) for q in qs]
+    ws = torch.empty(_lib.load().kv8_attn_shared_workspace_size(8, 8, 2, 1, 128), dtype=torch.uint8, device="cuda")
+    buf = qs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = _lib.kv8_attn_shared(buf, *dev, plan, workspace=ws)
+        second = _lib.kv8_attn_shared(buf, *dev, plan, workspace=ws)
+    for q, (o, l) in zip(qs, want):
+        buf.copy_(q)
+        graph.replay()
+        for x in (held, second):
+            assert torch.equal(x[0], o) and torch.equal(x[1], l)
+    dev[5] -= 3
+    graph.replay()
+    short = _lib.kv8_attn_shared(buf, *dev, plan)
+    assert torch.equal(held[0], short[0]) and not torch.equal(held[0], want[3][0])
+    dev[5] += 3
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(_lib.kv8_attn_shared(qs[i % 4], *dev, plan))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 4][0]) and torch.equal(l, want[i % 4][1])
+    assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,Nq,dtype", [(64, 3, 1, F16), (128, 1, 2, BF16)])
+def test_the_largest_batch(cuda_lib, D, G, Nq, dtype):
+    """1024 sequences: one large group, many small ones, some alone."""
+    cache = _batch([(384, 500)] + [(128, 2)] * 200, [5, 17, 40], [30] * 124, 1, D, 128, seed=19)
+    q = torch.randn(1024, G, Nq, D, generator=torch.Generator().manual_seed(4)).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], 128, 0)
+    assert len(_read_plan(plan, 1024)) == 201
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
+    assert _lib.sync_status() == _lib.ATTN_OK
+    _check(q, cache, None, out, lse, f"shared, 1024 sequences D={D}", some=range(0, 1024, 41))
+    a, b = _lib.kv8_attn(q.cuda(), *dev)
+    helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (out, lse, a, b)), dtype, f"shared against plain D={D}")

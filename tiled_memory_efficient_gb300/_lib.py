@@ -95,6 +95,10 @@ _SIGNATURES = {
     "kvp_workspace_size": ([_i] * 3, ctypes.c_size_t),
     "rope_apply": ([_vp] * 6 + [_i] * 8 + [ctypes.c_float, _i, _vp, _i, _vp], _i),
     "kv8_append_rope": ([_vp] * 13 + [_i, _i, ctypes.c_float] + [_i] * 8 + [_vp, _i, _vp], _i),
+    "kv8_attn_shared": ([_vp] * 13 + [ctypes.c_size_t] + [_i] * 8 + [ctypes.c_float, _i, _vp], _i),
+    "kv8_attn_shared_workspace_size": ([_i] * 5, ctypes.c_size_t),
+    "kvp_find_shared": ([_vp] * 2 + [_i] * 4 + [_vp, _vp], _i),
+    "kvp_plan_words": ([_i], ctypes.c_size_t),
     "attn_selftest_timeout": ([ctypes.c_ulonglong, _vp], _i),
     "attn_strerror": ([_i], ctypes.c_char_p),
     "attn_version": ([], _i),
@@ -362,7 +366,8 @@ def attn_fwd_splitkv(q, k, v, causal=False, scale: float | None = None, splits: 
 _BOUND = ("kv8_append_step", "kv8_attn_step", "kv8_attn_workspace_size", "kv8_copy_pages",
           "kvp_reserve_step", "kvp_reassign", "kvp_compact", "kvp_workspace_size", "attn_fwd_window",
           "attn_fwd_window_workspace_size", "attn_bwd_window", "attn_bwd_window_workspace_size",
-          "rope_apply", "kv8_append_rope")
+          "rope_apply", "kv8_append_rope", "kv8_attn_shared", "kv8_attn_shared_workspace_size",
+          "kvp_find_shared", "kvp_plan_words")
 _bind = None
 
 
@@ -713,6 +718,26 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
     _refused("kv8_append" if rope is None else "kv8_append_rope", rc, explain)
 
 
+def _explain_cache_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, out, lse, workspace, n_new,
+                        granted):
+    """Device of a cache attention's arguments; raises when they do not fit together."""
+    import torch
+    dev, (_, _, _, D) = _explain_pools(k_pages, v_pages, k_scale, v_scale)
+    _dtype_code(q)
+    if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous() or q.get_device() != dev:
+        raise ValueError(f"q must be a contiguous tensor [B, Hq, Nq, {D}] on CUDA device {dev}")
+    _explain_table(table, lens, q.shape[0], dev)
+    if n_new is not None:
+        _need("n_new", n_new, (q.shape[0],), torch.int32, dev)
+    _need_word("granted", granted, dev)
+    if out is not None:
+        _need("out", out, q.shape, q.dtype, dev)
+    if lse is not None:
+        _need("lse", lse, q.shape[:3], torch.float32, dev)
+    _need_workspace(workspace, dev)
+    return dev
+
+
 def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | None = None,
              window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, n_new=None,
              granted=None):
@@ -726,21 +751,54 @@ def kv8_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale: float | 
         return r
 
     def explain():
-        import torch
-        dev, (_, _, _, D) = _explain_pools(k_pages, v_pages, k_scale, v_scale)
-        _dtype_code(q)
-        if q.dim() != 4 or q.shape[3] != D or not q.is_contiguous() or q.get_device() != dev:
-            raise ValueError(f"q must be a contiguous tensor [B, Hq, Nq, {D}] on CUDA device {dev}")
-        _explain_table(table, lens, q.shape[0], dev)
-        if n_new is not None:
-            _need("n_new", n_new, (q.shape[0],), torch.int32, dev)
-        _need_word("granted", granted, dev)
-        if out is not None:
-            _need("out", out, q.shape, q.dtype, dev)
-        if lse is not None:
-            _need("lse", lse, q.shape[:3], torch.float32, dev)
-        _need_workspace(workspace, dev)
+        _explain_cache_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, out, lse, workspace, n_new,
+                            granted)
     _refused("kv8_attn", r, explain)
+
+
+def kv8_attn_shared(q, k_pages, v_pages, k_scale, v_scale, table, lens, plan, scale: float | None = None,
+                    out=None, lse=None, workspace=None, n_new=None, granted=None):
+    """kv8_attn, without a window, for sequences that begin with the same pages: plan
+    (kvp_find_shared's for this table) says which, and their common prefix is read once
+    for all of them (include/kvcache.h).  n_new and granted as in kv8_attn."""
+    r = (_bind or _load_bind()).kv8_attn_shared(q, k_pages, v_pages, k_scale, v_scale, table, lens, scale,
+                                                plan, out, lse, workspace, n_new, granted)
+    if type(r) is tuple:
+        return r
+
+    def explain():
+        import torch
+        dev = _explain_cache_attn(q, k_pages, v_pages, k_scale, v_scale, table, lens, out, lse, workspace,
+                                  n_new, granted)
+        words = load().kvp_plan_words(q.shape[0])
+        if not isinstance(plan, torch.Tensor):
+            raise ValueError("plan must be what kvp_find_shared returned")
+        _need("plan", plan, (words,), torch.int32, dev)
+    _refused("kv8_attn_shared", r, explain)
+
+
+# Positions that a group has to save by reading its prefix once (include/kvcache.h, KVP_MIN_SAVED).
+MIN_SAVED = 8192
+
+
+def kvp_find_shared(table, lens, page: int, min_saved: int = MIN_SAVED, plan=None):
+    """Which sequences begin with the same pages: the plan of kv8_attn_shared (int32, written
+    to plan if given).  Made after a fork and kept until the next one
+    (include/kvcache.h)."""
+    r = (_bind or _load_bind()).kvp_find_shared(table, lens, page, min_saved, plan)
+    if type(r) is not int:
+        return r
+
+    def explain():
+        import torch
+        if not table.is_cuda or table.dim() != 2:
+            raise ValueError("table must be a CUDA tensor [B, max_pages]")
+        dev = table.get_device()
+        _need("table", table, table.shape, torch.int32, dev)
+        _need("lens", lens, table.shape[:1], torch.int32, dev)
+        if plan is not None:
+            _need("plan", plan, (load().kvp_plan_words(table.shape[0]),), torch.int32, dev)
+    _refused("kvp_find_shared", r, explain)
 
 
 def kv8_copy_pages(k_pages, v_pages, k_scale, v_scale, src, dst, count, max_count: int | None = None):

@@ -23,8 +23,9 @@ BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["abi.cu", "attn_fwd.cu", "attn_bwd.cu", "bwd_noalloc.cu", "splitkv.cu", "ffn.cu",
-           "vconv.cu", "kv8.cu", "kvp.cu", "rope.cu"]
-HEADERS = ["ptx.cuh", "attn_internal.h", "bias.cuh", "window.cuh", "kv8.cuh", "rope.cuh"]
+           "vconv.cu", "kv8.cu", "kvp.cu", "rope.cu", "kv8_shared.cu",
+           "kv8_shared_attn.cu"]
+HEADERS = ["ptx.cuh", "attn_internal.h", "bias.cuh", "window.cuh", "kv8.cuh", "kv8_attn.cuh", "rope.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

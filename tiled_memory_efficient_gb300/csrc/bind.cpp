@@ -46,6 +46,10 @@ struct Fns {
     decltype(&attn_bwd_window_workspace_size) bwd_size;
     decltype(&rope_apply) rope;
     decltype(&kv8_append_rope) append_rope;
+    decltype(&kv8_attn_shared) attn_shared;
+    decltype(&kv8_attn_shared_workspace_size) attn_shared_size;
+    decltype(&kvp_find_shared) find_shared;
+    decltype(&kvp_plan_words) plan_words;
 } fn;
 
 using at::Tensor;
@@ -335,45 +339,97 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
     return r;
 }
 
+// What both attentions take: (q, k_pages, v_pages, k_scale, v_scale, table, lens, scale | None), and
+// elsewhere n_new | None, granted | None.
+struct CacheAttn {
+    Pools p;
+    Tensor q, table, lens, n_new, granted, out, lse, ws;
+    int64_t B = 0, Hq = 0, Nq = 0;
+    float scale = 0.0f;
+    bool read(PyObject* const* a, PyObject* counts, PyObject* grant) {
+        q = tensor(a[0]), table = tensor(a[5]), lens = tensor(a[6]);
+        if (!p.read(a + 1, false) || !scale_of(a[7], p.D, &scale)) return false;
+        if (cuda_of(q) != p.dev || q.dim() != 4 || !half(q) || q.size(3) != p.D ||
+            !q.is_contiguous() || !small(q.sizes()))
+            return false;
+        B = q.size(0), Hq = q.size(1), Nq = q.size(2);
+        if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
+            !ints(lens, p.dev, {B}))
+            return false;
+        if (counts != Py_None) {
+            n_new = tensor(counts);
+            if (!ints(n_new, p.dev, {B})) return false;
+        }
+        return word(grant, &granted, p.dev);
+    }
+    // (out | None, lse | None, workspace | None), the last of `size` bytes
+    bool results(PyObject* const* a, size_t size) {
+        return given_or_new(a[0], &out, q.sizes(), q.scalar_type(), p.dev) &&
+               given_or_new(a[1], &lse, {B, Hq, Nq}, at::kFloat, p.dev) &&
+               workspace(a[2], &ws, size > 0 ? size : 16, p.dev);
+    }
+};
+
 // (q, k_pages, v_pages, k_scale, v_scale, table, lens, scale | None, window, sinks,
 //  out | None, lse | None, workspace | None, n_new | None, granted | None) -> (out, lse) or rc
 PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 15) MISFIT();
-    const Tensor q = tensor(a[0]), table = tensor(a[5]), lens = tensor(a[6]);
-    Pools p;
+    CacheAttn x;
     int window, sinks;
-    float scale;
-    if (!p.read(a + 1, false) || !count(a[8], &window) || !count(a[9], &sinks) ||
-        !scale_of(a[7], p.D, &scale))
-        MISFIT();
-    if (cuda_of(q) != p.dev || q.dim() != 4 || !half(q) || q.size(3) != p.D ||
-        !q.is_contiguous() || !small(q.sizes()))
-        MISFIT();
-    const int64_t B = q.size(0), Hq = q.size(1), Nq = q.size(2);
-    if (!table.defined() || table.dim() != 2 || !ints(table, p.dev, {B, table.size(1)}) ||
-        !ints(lens, p.dev, {B}))
-        MISFIT();
-    Tensor n_new, granted;
-    if (a[13] != Py_None) {
-        n_new = tensor(a[13]);
-        if (!ints(n_new, p.dev, {B})) MISFIT();
-    }
-    if (!word(a[14], &granted, p.dev)) MISFIT();
+    if (n != 15 || !count(a[8], &window) || !count(a[9], &sinks) || !x.read(a, a[13], a[14])) MISFIT();
+    const Pools& p = x.p;
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
-    Tensor out, lse, ws;
-    const size_t size = fn.attn_size(B, Hq, p.heads, Nq, p.D);
-    if (!given_or_new(a[10], &out, q.sizes(), q.scalar_type(), p.dev) ||
-        !given_or_new(a[11], &lse, {B, Hq, Nq}, at::kFloat, p.dev) ||
-        !workspace(a[12], &ws, size > 0 ? size : 16, p.dev))
-        MISFIT();
+    if (!x.results(a + 10, fn.attn_size(x.B, x.Hq, p.heads, x.Nq, p.D))) MISFIT();
     const int rc = unlocked([&] {
-        return fn.attn(ptr(q), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
-                       as<int>(table), as<int>(lens), as<int>(n_new), as<int>(granted), ptr(out),
-                       as<float>(lse), ptr(ws), bytes(ws), B, Hq, p.heads, Nq, p.D, p.page, p.n_pages,
-                       table.size(1), scale, window, sinks, code(q), stream_of(p.dev));
+        return fn.attn(ptr(x.q), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs),
+                       as<int>(x.table), as<int>(x.lens), as<int>(x.n_new), as<int>(x.granted), ptr(x.out),
+                       as<float>(x.lse), ptr(x.ws), bytes(x.ws), x.B, x.Hq, p.heads, x.Nq, p.D, p.page, p.n_pages,
+                       x.table.size(1), x.scale, window, sinks, code(x.q), stream_of(p.dev));
     });
-    return rc == ATTN_OK ? pair(out, lse) : PyLong_FromLong(rc);
+    return rc == ATTN_OK ? pair(x.out, x.lse) : PyLong_FromLong(rc);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k_pages, v_pages, k_scale, v_scale, table, lens, scale | None, plan, out | None, lse | None,
+//  workspace | None, n_new | None, granted | None) -> (out, lse) or rc
+PyObject* py_attn_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    CacheAttn x;
+    if (n != 14 || !x.read(a, a[12], a[13])) MISFIT();
+    const Pools& p = x.p;
+    const Tensor plan = tensor(a[8]);
+    if (x.B > 0x7fffffff || !ints(plan, p.dev, {static_cast<int64_t>(fn.plan_words(static_cast<int>(x.B)))})) MISFIT();
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
+    if (!x.results(a + 9, fn.attn_shared_size(x.B, x.Hq, p.heads, x.Nq, p.D))) MISFIT();
+    const int rc = unlocked([&] {
+        return fn.attn_shared(ptr(x.q), ptr(p.k), ptr(p.v), as<float>(p.ks), as<float>(p.vs), as<int>(x.table),
+                              as<int>(x.lens), as<int>(x.n_new), as<int>(x.granted), as<int>(plan), ptr(x.out),
+                              as<float>(x.lse), ptr(x.ws), bytes(x.ws), x.B, x.Hq, p.heads, x.Nq, p.D, p.page,
+                              p.n_pages, x.table.size(1), x.scale, code(x.q), stream_of(p.dev));
+    });
+    return rc == ATTN_OK ? pair(x.out, x.lse) : PyLong_FromLong(rc);
+    END_HANDLE_TH_ERRORS
+}
+
+// (table, lens, page, min_saved, plan | None) -> plan or rc
+PyObject* py_find_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 5) MISFIT();
+    const Tensor table = tensor(a[0]), lens = tensor(a[1]);
+    const int64_t dev = cuda_of(table);
+    int page, least;
+    if (dev < 0 || table.dim() != 2 || !ints(table, dev, table.sizes()) || !small(table.sizes()) ||
+        !ints(lens, dev, {table.size(0)}) || !whole(a[2], &page) || !whole(a[3], &least))
+        MISFIT();
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    Tensor plan;
+    const int B = static_cast<int>(table.size(0));
+    if (!given_or_new(a[4], &plan, {static_cast<int64_t>(fn.plan_words(B))}, at::kInt, dev)) MISFIT();
+    const int rc = unlocked([&] {
+        return fn.find_shared(as<int>(table), as<int>(lens), B, static_cast<int>(table.size(1)), page, least,
+                              as<int>(plan), stream_of(dev));
+    });
+    return rc == ATTN_OK ? THPVariable_Wrap(plan) : PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
 
@@ -857,6 +913,8 @@ PyMethodDef methods[] = {METHOD("init", py_init),
                          METHOD("rope", py_rope),
                          METHOD("rotary", py_rotary),
                          METHOD("kv8_append_rope", py_append_rope),
+                         METHOD("kv8_attn_shared", py_attn_shared),
+                         METHOD("kvp_find_shared", py_find_shared),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

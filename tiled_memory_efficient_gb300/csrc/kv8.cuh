@@ -15,6 +15,19 @@ namespace tme {
 // abi.cu
 int device_setup_public(unsigned int** status);
 
+struct AttnParams;
+
+// kv8.cu: checks a cache attention's arguments (the workspace for `needed` bytes) and fills its
+// parameters.
+int attn_params(AttnParams* p, const void* q, const void* k_pages, const void* v_pages,
+                const float* k_scale, const float* v_scale, const int* table, const int* lens,
+                const int* n_new, const int* granted, void* out, float* lse, void* workspace,
+                size_t workspace_bytes, size_t needed, int B, int Hq, int Hkv, int Nq, int D, int page,
+                int n_pages, int max_pages, float scale, int window, int sinks, int dtype);
+// kv8_shared_attn.cu: the attention behind a shared prefix, without the merge.
+int attn_launch_shared(const AttnParams& p, const void* k_pages, const void* v_pages, int D, int page, bool bf16,
+                       cudaStream_t stream);
+
 namespace {
 
 // ------------------------------------------------------------------ e4m3
@@ -93,6 +106,112 @@ __device__ __forceinline__ void raise_tokens(uint8_t* at, int pos, int end, int 
     }
 }
 
+// ------------------------------------------------------------------ attention
+
+// Tiles per CTA, at least: 12 of them put 8 sequences of 256 tokens on 6 CTAs, several
+// units each, 13.4 us against 5.4.
+constexpr int kMinShare = 4;
+constexpr int kMaxBatch = 1024;   // sequences per call (their tile counts live in shared memory)
+
+}  // namespace
+
+struct AttnParams {
+    const void* q;
+    const float* k_scale;
+    const float* v_scale;
+    const int* table;
+    const int* lens;
+    const int* n_new;     // queries of a sequence that stand at a position (null: all Nq)
+    const int* granted;   // 0: none does (null: 1)
+    void* out;
+    float* lse;
+    float* part_o;     // [2 * ctas][rows of a block][D]
+    float* part_lse;   // [2 * ctas][rows of a block], log2 domain
+    // attention over a shared prefix (null: none): the plan, and the rows of sequences that
+    // share, over the positions after their prefix
+    const int* plan;
+    float* own_o;      // [B, Hq, Nq][D]
+    float* own_lse;    // [B, Hq, Nq], log2 domain
+    unsigned int* status;
+    int B, Hkv, rows, n_rb;   // rows = G * Nq of a KV head, row blocks
+    int Nq, page_shift, n_pages, max_pages;
+    int window, sinks, ctas, tile_shift;
+    float scale_log2;
+};
+
+namespace {
+
+// The visible tiles of a sequence.
+struct Seq {
+    int len, nq, first;    // positions held; queries; position of the first one (may be < 0)
+    int lo;                // first position inside a window of some query, or past the shared prefix
+    int n_sink, skip, n;   // tiles [0, n_sink) and [n_sink + skip, ...), n in all
+};
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int len, int nq, int start = 0) {
+    Seq s;
+    const int up = (1 << p.tile_shift) - 1;
+    s.len = min(max(len, 0), p.max_pages << p.page_shift);
+    s.nq = nq;
+    s.first = s.len - nq;
+    s.lo = p.window > 0 ? max(s.first - p.window + 1, 0) : start;
+    const int lo_tile = s.lo >> p.tile_shift;
+    s.n_sink = min((p.sinks + up) >> p.tile_shift, lo_tile);
+    s.skip = lo_tile - s.n_sink;
+    s.n = nq > 0 ? max(((s.len + up) >> p.tile_shift) - s.skip, 0) : 0;
+    return s;
+}
+__device__ __forceinline__ bool step_granted(const AttnParams& p) { return !p.granted || *p.granted != 0; }
+// Queries of sequence b of that length; -1: a count that does not fit.
+__device__ __forceinline__ int queries_of(const AttnParams& p, bool granted, int b, int len) {
+    if (!granted) return 0;
+    if (!p.n_new) return p.Nq;
+    const int n = p.n_new[b];
+    return n < 0 || n > p.Nq || n > min(len, p.max_pages << p.page_shift) ? -1 : n;
+}
+__device__ __forceinline__ int seq_tile(const Seq& s, int v) {   // tile v of the list
+    return v < s.n_sink ? v : v + s.skip;
+}
+
+// Shares: the T tiles are cut into n runs of q or q + 1 tiles (the first rem of them).
+// T < 2^31 (checked on the host).
+struct Shares {
+    int n, q, rem;
+    __device__ __forceinline__ Shares(int T, int ctas, int least = kMinShare) {
+        n = min((T + least - 1) / least, ctas);
+        q = n > 0 ? static_cast<int>(static_cast<unsigned>(T) / static_cast<unsigned>(n)) : 0;
+        rem = T - q * n;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int owner(int x) const {   // CTA that holds tile x
+        const int big = rem * (q + 1);
+        return x < big ? x / (q + 1) : rem + (x - big) / q;
+    }
+};
+
+// What kvp_find_shared leaves: a header, then arrays of n_seqs words.  Group g are the
+// sequences members[first[g] .. + count[g]), in ascending order; the first `blocks[g]` runs of
+// kShareBlock positions of all of them lie in the pages of the first one's table row.
+constexpr int kShareBlock = 128;
+constexpr int kPlanMagic = 0x5a4e0001;
+struct Plan {
+    const int* w;
+    int n;
+    __device__ __forceinline__ Plan(const int* words, int n_seqs) : w(words), n(n_seqs) {}
+    // Whether it is a plan for as many sequences at all.
+    __device__ __forceinline__ bool ok() const { return w[0] == kPlanMagic && w[2] == n; }
+    __device__ __forceinline__ int groups() const { return min(max(w[1], 0), n); }
+    __device__ __forceinline__ int at(int array, int i) const { return w[4 + array * n + i]; }
+    __device__ __forceinline__ int first(int g) const { return min(max(at(0, g), 0), n); }
+    __device__ __forceinline__ int count(int g) const { return min(max(at(1, g), 0), n - first(g)); }
+    __device__ __forceinline__ int blocks(int g) const { return max(at(2, g), 0); }
+    __device__ __forceinline__ int member(int i) const { return min(max(at(3, i), 0), n - 1); }
+    __device__ __forceinline__ int group(int b) const { return min(at(4, b), n - 1); }   // -1: none
+    __device__ __forceinline__ int rank(int b) const { return at(5, b); }
+    // positions that sequence b shares (a multiple of kShareBlock)
+    __device__ __forceinline__ int start(int b) const { return max(at(6, b), 0) & ~(kShareBlock - 1); }
+};
+constexpr int kPlanArrays = 7, kPlanScratch = 3;
+
 // ------------------------------------------------------------------ host
 
 template <int N>
@@ -102,10 +221,10 @@ bool aligned(const void* const (&ptrs)[N], uintptr_t bytes) {
     return true;
 }
 
-bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
 // Sizes of a cache that every call shares.
-int check_cache(int B, int Hkv, int D, int page, int n_pages, int max_pages) {
+inline int check_cache(int B, int Hkv, int D, int page, int n_pages, int max_pages) {
     if (B <= 0 || Hkv <= 0 || D <= 0 || page <= 0 || n_pages <= 0 || max_pages <= 0)
         return ATTN_ERR_INVALID;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
@@ -117,7 +236,7 @@ int check_cache(int B, int Hkv, int D, int page, int n_pages, int max_pages) {
 }
 
 // SM count of the current device (0 without one), asked for once per device.
-int device_sms() {
+inline int device_sms() {
     static std::atomic<int> known[64];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -131,6 +250,16 @@ int device_sms() {
     }
     if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
+}
+
+inline size_t pad256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// 8-row tiles of a row block: 1, 2 or 4.
+inline int row_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+inline size_t part_bytes(int64_t rows, int D, int ctas) {
+    const size_t n = 2 * static_cast<size_t>(ctas) * 8 * row_tiles(rows);
+    return pad256(n * D * sizeof(float)) + pad256(n * sizeof(float));
 }
 
 }  // namespace

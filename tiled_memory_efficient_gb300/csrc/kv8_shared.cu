@@ -1,0 +1,1104 @@
+// kv8_shared.cu -- attention over the paged 8-bit cache for sequences that share a
+// prefix (include/kvcache.h): which sequences those are, the prefix's attention for
+// all of them at once, and the merge with what each sees of its own.
+//
+// softmax(q K^T) V over positions [0, len) is the sum over [0, s) and [s, len), each
+// with its own maximum and sum, weighted by exp(LSE - LSE of both).  The part [s, len) is
+// kv8_attn's; over [0, s) the rows of a group's sequences (G Nq each of a KV head) stand together as
+// one matrix, so its keys and values are read once for all of them and the two products
+// become matrix products with 128 rows or more: work for tcgen05, bound by it and by the
+// exponentials where the single sequence's attention is bound by memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/kvcache.h"
+#include "attn_internal.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
+
+namespace tme {
+namespace {
+
+// ------------------------------------------------------------------ the prefix's attention
+
+constexpr int kPreRows = 128;       // rows of a Q tile, keys of a K/V tile
+constexpr int kPreMinShare = 2;     // tiles per CTA, at least
+constexpr float kPreThreshold = 8.0f;   // powers of two the largest score may outgrow its reference by
+
+struct PreParams {
+    AttnParams a;
+    const uint8_t* k_pages;
+    const uint8_t* v_pages;
+    float* row_o;      // [B, Hq, Nq][D]: units that lie in one CTA
+    float* row_lse;    // [B, Hq, Nq], log2 domain
+    float* part_o;     // [2 * ctas][rows of a block][D]: the others
+    float* part_lse;
+};
+
+// What the producer leaves beside a raw tile: the exponents of its pages' scales, and which
+// pages hold nothing readable.
+struct RawInfo {
+    int ke[8], ve[8];
+    int bad, pad[3];
+};
+// What the converters leave for the softmax: keys are 2^e of this times their fp16 values,
+// the accumulator's values 2^ev.
+struct TileInfo {
+    float kf;
+    int ev, bad, pad;
+};
+
+// QT: Q tiles of a CTA (128 rows each).
+template <int D, int QT>
+struct PreCfg {
+    static constexpr int kTile16 = kPreRows * D * 2;    // 128 x D, fp16
+    static constexpr int kRaw = kPreRows * D;           // 128 x D, e4m3
+    // K and V take turns; shared memory is full at D = 128 with two Q tiles
+    static constexpr int kRawSlots = D == 64 ? 8 : QT == 1 ? 4 : 2;
+    static constexpr int kKOff = QT * kTile16;
+    static constexpr int kVOff = kKOff + 2 * kTile16;
+    static constexpr int kRawOff = kVOff + 2 * kTile16;
+    static constexpr int kRawInfoOff = kRawOff + kRawSlots * kRaw;
+    static constexpr int kTileInfoOff = kRawInfoOff + kRawSlots / 2 * static_cast<int>(sizeof(RawInfo));
+    static constexpr int kBarOff = kTileInfoOff + 4 * static_cast<int>(sizeof(TileInfo));
+    static constexpr int kBars = 2 * kRawSlots + 8 + 4 + 2 + 2 + QT * 2 + 1;
+    static constexpr int kMiscOff = kBarOff + kBars * 8;
+    static constexpr int kSmem = kMiscOff + 16 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int kSoftmaxWarps = 4 * QT, kConvWarp = kSoftmaxWarps, kMmaWarp = kConvWarp + 4,
+                         kProducerWarp = kMmaWarp + 1, kThreads = (kProducerWarp + 1) * 32;
+    static constexpr int kRowBlock = QT * kPreRows;
+};
+
+// Tiles, units and rows of a group.
+struct Group {
+    int blocks, n_rb, units;
+    int64_t rows;
+    __device__ __forceinline__ int tiles() const { return units * blocks; }
+};
+__device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan, int g, int row_block) {
+    Group x;
+    x.blocks = min(plan.blocks(g), (p.max_pages << p.page_shift) / kShareBlock);
+    x.rows = static_cast<int64_t>(plan.count(g)) * p.rows;
+    x.n_rb = static_cast<int>((x.rows + row_block - 1) / row_block);
+    x.units = p.Hkv * x.n_rb;
+    return x;
+}
+// Tiles of all groups; each warp for itself.
+__device__ __forceinline__ int all_tiles(const AttnParams& p, const Plan& plan, int groups, int row_block,
+                                         int before = -1, int* first = nullptr) {
+    const int lane = threadIdx.x & 31;
+    int all = 0, lead = 0;
+    for (int g = lane; g < groups; g += 32) {
+        const int n = group_of(p, plan, g, row_block).tiles();
+        all += n;
+        if (g < before) lead += n;
+    }
+    if (first) *first = __reduce_add_sync(0xffffffffu, lead);
+    return __reduce_add_sync(0xffffffffu, all);
+}
+
+// A CTA's share of the tiles, part by part (a part: consecutive tiles of one unit).  Every role
+// walks it for itself.
+struct Walk {
+    Group x;
+    int g, u, v;      // group, unit within it, first tile of the part within the unit
+    int left;         // tiles of the share from the part on
+    __device__ __forceinline__ int tiles() const { return min(x.blocks - v, left); }
+    __device__ __forceinline__ void next(const AttnParams& p, const Plan& plan, int groups, int row_block) {
+        left -= tiles();
+        v = 0;
+        if (left > 0 && ++u == x.units) {
+            u = 0;
+            do ++g, x = group_of(p, plan, g, row_block);
+            while (x.tiles() == 0 && g + 1 < groups);
+            if (x.tiles() == 0) left = 0;   // (a plan that changed meanwhile: no endless walk)
+        }
+    }
+    __device__ __forceinline__ int head() const { return u / x.n_rb; }
+    __device__ __forceinline__ int64_t row0(int row_block) const {
+        return static_cast<int64_t>(u - head() * x.n_rb) * row_block;
+    }
+};
+// The share of CTA c that starts at tile g0 and ends at g1 (g0 < g1).
+__device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block, int g0,
+                                          int g1) {
+    const int lane = threadIdx.x & 31;
+    Walk w{};
+    int carry = 0;
+    for (int base = 0; base < groups; base += 32) {
+        const int g = base + lane;
+        const int n = g < groups ? group_of(p, plan, g, row_block).tiles() : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, carry + sum > g0);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            const int before = carry + __shfl_sync(0xffffffffu, sum - n, at);
+            w.g = base + at;
+            w.x = group_of(p, plan, w.g, row_block);
+            const int off = g0 - before;
+            w.u = off / w.x.blocks;
+            w.v = off - w.u * w.x.blocks;
+            break;
+        }
+        carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    w.left = g1 - g0;
+    return w;
+}
+
+// 16 e4m3 values as fp16, times 2^d (d <= 0, as two fp16 in `factor`; 1: not multiplied).
+__device__ __forceinline__ void convert16(const uint4& x, uint32_t factor, bool scaled, uint4* lo, uint4* hi) {
+    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = e4m3x2_to_f16x2(in[i]);
+        r[2 * i + 1] = e4m3x2_hi_to_f16x2(in[i]);
+    }
+    if (scaled) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(factor));
+    }
+    *lo = make_uint4(r[0], r[1], r[2], r[3]);
+    *hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// 2^d as two fp16 values; 0 below the smallest one (the values it would scale are under 2^-33
+// of the largest that the tile can hold).
+__device__ __forceinline__ uint32_t pow2_f16x2(int d) {
+    const uint32_t h = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+    return h | (h << 16);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& x) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128v(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// One CTA per SM, each an equal share of all groups' (KV head, row block, tile of 128 keys): the
+// roles are those of the dense forward, but the keys and values arrive as e4m3 pages in a
+// ring of raw tiles (one bulk copy a page) and four warps rewrite them as fp16 operands (exact; a page
+// whose scale is below the tile's largest is moved by that power of two, exact down to 2^-15 of
+// it), swizzled as TMA would have written them.  The value scale that the accumulator stands at
+// only grows within a unit, by whole tiles, and joins the softmax's rescale.  A part of a unit ends in fp32
+// rows with their LSE, for kv8_shared_merge_kernel.
+//   warps 0 .. 4 QT - 1   softmax, a thread per row: two passes over S in TMEM (maximum, then
+//                         exponentials), P over S as fp16
+//   then 4 warps          converters
+//   then 1 warp           tcgen05.mma issue: QT = 2 PV_0, S_0', PV_1, S_1', so that one tile's softmax
+//                         runs beside the other's products; QT = 1 two S buffers, S' before PV
+//   then 1 warp           producer: page ids, scales, bulk copies
+template <int D, bool BF16, int QT>
+__global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
+    kv8_prefix_kernel(const __grid_constant__ PreParams p) {
+    using C = PreCfg<D, QT>;
+    constexpr int RS = C::kRawSlots, NI = RS / 2, RB = C::kRowBlock;
+    constexpr int kOCol = 256;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    RawInfo* raw_info = reinterpret_cast<RawInfo*>(smem + C::kRawInfoOff);      // [NI]
+    volatile TileInfo* tile_info = reinterpret_cast<TileInfo*>(smem + C::kTileInfoOff);   // [4]
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);       // [RS]
+    uint64_t* raw_empty = raw_full + RS;     // [RS]
+    uint64_t* k_full = raw_empty + RS;       // [2] the fp16 tile is written
+    uint64_t* k_empty = k_full + 2;          // [2]
+    uint64_t* v_full = k_empty + 2;          // [2]
+    uint64_t* v_empty = v_full + 2;          // [2]
+    uint64_t* info_full = v_empty + 2;       // [4] tile_info
+    uint64_t* s_full = info_full + 4;        // [2] QT = 2: of tile t; QT = 1: of S buffer x & 1
+    uint64_t* pv_done = s_full + 2;          // [2] PV of tile t done
+    uint64_t* p_full = pv_done + 2;          // [QT]
+    uint64_t* q_full = p_full + QT;          // [QT]
+    uint64_t* mma_done = q_full + QT;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const AttnParams& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // As the attention behind it: reads from here on what earlier kernels wrote; that one may
+    // set up and start (it reads nothing of this one's).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const Plan plan(a.plan, a.B);
+    const bool granted = step_granted(a);
+    if (!plan.ok()) {   // the sequences are then each for itself
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusPage);
+        return;
+    }
+    const int groups = granted ? plan.groups() : 0;
+    const int T = all_tiles(a, plan, groups, RB);
+    const Shares sh(T, a.ctas, kPreMinShare);
+    const int cta = static_cast<int>(blockIdx.x);
+    if (cta >= sh.n) return;   // nothing to wait for
+    const int g0 = sh.begin(cta), g1 = sh.begin(cta + 1);
+    Walk w = walk_from(a, plan, groups, RB, g0, g1);
+    auto next = [&](Walk& x) { x.next(a, plan, groups, RB); };
+    auto active = [&](const Walk& x, int t) { return x.row0(RB) + t * kPreRows < x.x.rows; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RS; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 4);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&pv_done[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&info_full[i], 1);
+        for (int t = 0; t < QT; ++t) {
+            mbar_init(&p_full[t], kPreRows);
+            mbar_init(&q_full[t], kPreRows);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // Every wait is bounded: one that gives up sets the abort flag, at which all others return
+    // at once, so each role's loops run to their end (or leave) without blocking.
+    if (warp < C::kSoftmaxWarps) {
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2, quad = warp & 3;
+        const int rl = quad * 32 + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tO = tmem + lane_base + kOCol + t * D;
+        const uint32_t sQ = smem_u32(smem + t * C::kTile16);
+        // this thread's row of the part: whether it exists, its position (-1: sees nothing), its
+        // place among all rows, its scores' factor
+        bool exists = false;
+        int pos = -1;
+        int64_t row_id = 0;
+        float f_row = 0.0f;
+        // Q of a part's tile t: each thread its own row, bf16 brought into fp16's range by a power of
+        // two first (as in kv8_attn).  S of the part before has been computed.
+        auto load_q = [&](const Walk& x) {
+            const int64_t r = x.row0(RB) + t * kPreRows + rl;
+            exists = r < x.x.rows;
+            pos = -1;
+            uint32_t q[D / 2];
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) q[i] = 0u;
+            int shift = 0;
+            if (exists) {
+                const int m = static_cast<int>(r / a.rows), rr = static_cast<int>(r - static_cast<int64_t>(m) * a.rows);
+                const int b = plan.member(plan.first(x.g) + m);
+                const int len = a.lens[b], nq = queries_of(a, granted, b, len);
+                const int i = rr % a.Nq;
+                if (i < nq) pos = min(max(len, 0), a.max_pages << a.page_shift) - nq + i;
+                row_id = (static_cast<int64_t>(b) * a.Hkv + x.head()) * a.rows + rr;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row_id * D);
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 v = src[k];
+                    q[4 * k] = v.x, q[4 * k + 1] = v.y, q[4 * k + 2] = v.z, q[4 * k + 3] = v.w;
+                }
+                if constexpr (BF16) {
+                    uint32_t ex = 0u;   // largest finite exponent field
+#pragma unroll
+                    for (int k = 0; k < D / 2; ++k) {
+                        const uint32_t lo = (q[k] >> 7) & 0xffu, hi = (q[k] >> 23) & 0xffu;
+                        ex = max(ex, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
+                    }
+                    shift = ex == 0u ? 0 : min(14 + 127 - static_cast<int>(ex), 126);
+                    const float up = exp2i(shift);
+#pragma unroll
+                    for (int k = 0; k < D / 2; ++k) {
+                        const float2 v = unpack16<true>(q[k]);
+                        q[k] = pack2<false>(v.x * up, v.y * up);
+                    }
+                }
+            }
+            f_row = a.scale_log2 * exp2i(-shift);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                sts128(sQ + (k >> 3) * (kPreRows * 128) + rl * 128 + (((k & 7) ^ (rl & 7)) << 4),
+                       make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]));
+            fence_proxy_async_smem();
+            mbar_arrive(&q_full[t]);
+        };
+        int x = 0;          // tile of the share
+        uint32_t ns = 0;    // tiles of this Q tile so far
+        bool ok = true;
+        if (active(w, t)) load_q(w);
+        while (w.left > 0 && ok) {
+            const int n = w.tiles();
+            if (!active(w, t)) {
+                x += n;
+                next(w);
+                if (w.left > 0 && active(w, t)) load_q(w);
+                continue;
+            }
+            const bool mine = exists;
+            const int my_pos = pos;
+            const int64_t my_row = row_id;
+            const float my_f = f_row;
+            const bool live = __any_sync(0xffffffffu, my_pos >= 0);
+            const int min_pos = __reduce_min_sync(0xffffffffu, mine ? my_pos : 0x7fffffff);
+            float m = -INFINITY, l = 0.0f;
+            int ev = 0;
+            for (int j = 0; j < n && ok; ++j, ++x, ++ns) {
+                const uint32_t buf = QT == 1 ? (ns & 1u) : static_cast<uint32_t>(t);
+                const uint32_t tS = tmem + lane_base + buf * 128;
+                ok = warp_wait(&info_full[x & 3], (x >> 2) & 1, abort_flag, a.status);
+                ok = ok && warp_wait(&s_full[buf], QT == 1 ? (ns >> 1) & 1u : ns & 1u, abort_flag, a.status);
+                if (!ok) break;
+                tc_fence_after();
+                const float f = my_f * tile_info[x & 3].kf;
+                const int ev_now = tile_info[x & 3].ev, bad = tile_info[x & 3].bad;
+                // QT = 1: S of this tile went out ahead of the last PV.  A warp that arrived for this tile
+                // while another has yet to for the last one would complete that phase in its place; and O is
+                // not to be touched before that PV is done.
+                auto last_pv = [&]() {
+                    if (QT == 1 && j > 0) ok = warp_wait(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status);
+                    return ok;
+                };
+                if (!live) {   // a warp with no row that sees anything keeps the counts
+                    if (!last_pv()) break;
+                    mbar_arrive(&p_full[t]);
+                    continue;
+                }
+                const int key0 = (w.v + j) * kPreRows;
+                const bool edge = bad != 0 || key0 + kPreRows - 1 > min_pos;
+                auto hide = [&](uint32_t (&s)[32], int k0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int k = k0 + i;
+                        if (key0 + k > my_pos || ((bad >> (k >> a.page_shift)) & 1)) s[i] = __float_as_uint(-INFINITY);
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    uint32_t s0[32], s1[32];
+                    tmem_ld64(tS + c * 32, s0, s1);
+                    tmem_wait_ld();
+                    reg_fence(s0);
+                    reg_fence(s1);
+                    if (edge) {
+                        hide(s0, c * 32);
+                        hide(s1, c * 32 + 32);
+                    }
+                    float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        b0 = fmax3(b0, __uint_as_float(s0[i]), __uint_as_float(s1[i]));
+                        b1 = fmax3(b1, __uint_as_float(s0[i + 1]), __uint_as_float(s1[i + 1]));
+                        b2 = fmax3(b2, __uint_as_float(s0[i + 2]), __uint_as_float(s1[i + 2]));
+                        b3 = fmax3(b3, __uint_as_float(s0[i + 3]), __uint_as_float(s1[i + 3]));
+                    }
+                    mx = fmax3(mx, fmaxf(b0, b1), fmaxf(b2, b3));
+                }
+                const float m_new = fmaxf(m, mx * f);
+                const bool need = m_new > m + kPreThreshold;
+                const float al = need ? ex2_ftz(m - m_new) : 1.0f;   // from -inf: 0
+                m = need ? m_new : m;
+                const float m_sub = m == -INFINITY ? 0.0f : m;
+                const uint64_t f2s = f2(f, f), nm2 = f2(-m_sub, -m_sub);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t s[32], pk[16];
+                    tmem_ld32(tS + c * 32, s);
+                    tmem_wait_ld();
+                    reg_fence(s);
+                    if (edge) hide(s, c * 32);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        pk[i >> 1] = softmax_pair<false>(s[i], s[i + 1], f2s, nm2, acc[(i >> 1) & 3]);
+                    tmem_st16(tS + c * 16, pk);
+                }
+                const uint64_t a2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                l = l * al + (f2lo(a2) + f2hi(a2));
+                const int up = j > 0 ? ev_now - ev : 0;   // the value scale grew by 2^up
+                ev = ev_now;
+                if (!last_pv()) break;
+                if (j > 0 && __any_sync(0xffffffffu, need || up > 0)) {
+                    tc_fence_after();
+                    const float o_al = al * exp2i(-min(up, 126));
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c * 32, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * o_al);
+                        tmem_st32(tO + c * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            // where this part's rows go
+            const int done = (g1 - g0) - w.left;   // tiles before the part
+            const bool whole = w.v == 0 && n == w.x.blocks;
+            const int part = 2 * cta + (done == 0 ? 0 : 1);
+            next(w);
+            if (w.left > 0 && active(w, t)) load_q(w);
+            ok = warp_wait(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const bool empty = !live || l == 0.0f;   // (a NaN is not)
+            const float inv = empty ? 0.0f : 1.0f / l, scale = exp2i(ev);
+            const int64_t at = whole ? my_row : static_cast<int64_t>(part) * RB + t * kPreRows + rl;
+            float* dst = (whole ? p.row_o : p.part_o) + at * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+                tmem_wait_ld();
+                reg_fence(o);
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            y[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[8 * i + k]) * inv * scale);
+                        st_global_v8(dst + c * 32 + 8 * i, y);
+                    }
+                }
+            }
+            if (mine) (whole ? p.row_lse : p.part_lse)[at] = empty ? -INFINITY : m + lg2_approx(l);
+            tc_fence_before();
+        }
+    } else if (warp < C::kMmaWarp) {
+        // ------------------------------------------------------------ converters
+        const int ct = threadIdx.x - C::kConvWarp * 32;
+        const int ppt_log = 7 - a.page_shift;   // pages of a tile: 2^ppt_log
+        constexpr int CPR = D / 16;             // 16-value chunks of a row
+        int x = 0;
+        bool ok = true;
+        while (w.left > 0 && ok) {
+            const int n = w.tiles();
+            int ev = -1000;   // value scale of the accumulator: none yet
+            for (int j = 0; j < n && ok; ++j, ++x) {
+                const int sk = (2 * x) % RS, sv = sk + 1;
+                const uint32_t turn = static_cast<uint32_t>(x / NI) & 1u;
+                const RawInfo* in = raw_info + x % NI;
+                ok = warp_wait(&raw_full[sk], turn, abort_flag, a.status);
+                if (ok && x >= 2) ok = warp_wait(&k_empty[x & 1], ((x - 2) >> 1) & 1, abort_flag, a.status);
+                if (!ok) break;
+                const int bad = in->bad;
+                int ke = -1000, ve = -1000, ke_min = 1000, ve_min = 1000;
+                for (int i = 0; i < 1 << ppt_log; ++i) {
+                    if ((bad >> i) & 1) continue;
+                    ke = max(ke, in->ke[i]), ke_min = min(ke_min, in->ke[i]);
+                    ve = max(ve, in->ve[i]), ve_min = min(ve_min, in->ve[i]);
+                }
+                if (ke == -1000) ke = ke_min = 0;
+                ev = max(ev, ve);
+                const int ev_now = ev == -1000 ? 0 : ev;
+                if (ct == 0) {
+                    tile_info[x & 3].kf = exp2i(ke);
+                    tile_info[x & 3].ev = ev_now;
+                    tile_info[x & 3].bad = bad;
+                    mbar_arrive(&info_full[x & 3]);
+                }
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    if (which == 1) {
+                        ok = warp_wait(&raw_full[sv], turn, abort_flag, a.status);
+                        if (ok && x >= 2) ok = warp_wait(&v_empty[x & 1], ((x - 2) >> 1) & 1, abort_flag, a.status);
+                        if (!ok) break;
+                    }
+                    const uint32_t src = smem_u32(smem + C::kRawOff + (which == 0 ? sk : sv) * C::kRaw);
+                    const uint32_t dst = smem_u32(smem + (which == 0 ? C::kKOff : C::kVOff) + (x & 1) * C::kTile16);
+                    const int top = which == 0 ? ke : ev_now;
+                    const bool scaled = which == 0 ? ke_min < ke : ve_min < ev_now;
+#pragma unroll 4
+                    for (int i = ct; i < kPreRows * CPR; i += 128) {
+                        const int r = i / CPR, c = i % CPR, pg = r >> a.page_shift;
+                        uint4 lo, hi;
+                        uint32_t factor = 0u;
+                        if (scaled) factor = pow2_f16x2((which == 0 ? in->ke[pg] : in->ve[pg]) - top);
+                        convert16(lds128v(src + i * 16), factor, scaled, &lo, &hi);
+                        if ((bad >> pg) & 1) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                        // 16-byte units 2 (c & 3) and the next of column block c / 4; the second block's
+                        // lanes write theirs the other way round, so that 8 lanes meet every bank once
+                        const uint32_t row = dst + (c >> 2) * (kPreRows * 128) + r * 128;
+                        const int u0 = 2 * (c & 3), swap = (c >> 2) & 1;
+                        sts128(row + (((u0 + swap) ^ (r & 7)) << 4), swap ? hi : lo);
+                        sts128(row + (((u0 + 1 - swap) ^ (r & 7)) << 4), swap ? lo : hi);
+                    }
+                    // the tensor core reads these bytes after the arrival below
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[which == 0 ? sk : sv]);
+                        mbar_arrive(which == 0 ? &k_full[x & 1] : &v_full[x & 1]);
+                    }
+                }
+            }
+            next(w);
+        }
+    } else if (warp == C::kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue
+        constexpr uint32_t idesc_s = idesc_f16(kPreRows, kPreRows, false, false);
+        constexpr uint32_t idesc_o = idesc_f16(kPreRows, D, false, true);
+        constexpr uint64_t kTileStep = C::kTile16 >> 4, kBlk = (kPreRows * 128) >> 4;
+        const uint64_t dq0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + C::kVOff), kPreRows * 128, 1024);
+        uint32_t ns[2] = {0u, 0u}, np[2] = {0u, 0u}, nq[2] = {0u, 0u};
+        auto issue_s = [&](int t, int x, bool last) {
+            const int st = x & 1;
+            warp_wait(&k_full[st], (x >> 1) & 1, abort_flag, a.status);
+            tc_fence_after();
+            const uint32_t buf = QT == 1 ? (ns[t] & 1u) : static_cast<uint32_t>(t);
+#pragma unroll
+            for (int kb = 0; kb < D / 64; ++kb)
+                mma_ss_k64(tmem + buf * 128, dq0 + t * kTileStep + kb * kBlk, dk0 + st * kTileStep + kb * kBlk,
+                           idesc_s, kb > 0 ? 1u : 0u);
+            mma_commit_elect(&s_full[buf]);
+            if (last) mma_commit_elect(&k_empty[st]);
+            ++ns[t];
+        };
+        auto issue_pv = [&](int t, int x, bool first, bool last) {
+            const int st = x & 1;
+            warp_wait(&v_full[st], (x >> 1) & 1, abort_flag, a.status);
+            warp_wait(&p_full[t], np[t] & 1u, abort_flag, a.status);
+            tc_fence_after();
+            const uint32_t buf = QT == 1 ? (np[t] & 1u) : static_cast<uint32_t>(t);
+            mma_ts_k128(tmem + kOCol + t * D, tmem + buf * 128, dv0 + st * kTileStep, idesc_o, first ? 0u : 1u);
+            mma_commit_elect(&pv_done[t]);
+            if (last) mma_commit_elect(&v_empty[st]);
+            ++np[t];
+        };
+        int x = 0;
+        while (w.left > 0 && __all_sync(0xffffffffu, *abort_flag == 0)) {
+            const int n = w.tiles();
+            const bool two = QT == 2 && active(w, 1);   // (tile 0 always has rows)
+            warp_wait(&q_full[0], nq[0]++ & 1u, abort_flag, a.status);
+            issue_s(0, x, !two);
+            if (two) {
+                warp_wait(&q_full[QT - 1], nq[1]++ & 1u, abort_flag, a.status);
+                issue_s(QT - 1, x, true);
+            }
+            for (int j = 0; j < n; ++j) {
+                if (QT == 1) {
+                    if (j + 1 < n) issue_s(0, x + j + 1, true);
+                    issue_pv(0, x + j, j == 0, true);
+                } else {
+                    issue_pv(0, x + j, j == 0, !two);
+                    if (j + 1 < n) issue_s(0, x + j + 1, !two);
+                    if (two) {
+                        issue_pv(QT - 1, x + j, j == 0, true);
+                        if (j + 1 < n) issue_s(QT - 1, x + j + 1, true);
+                    }
+                }
+            }
+            x += n;
+            next(w);
+        }
+        mma_commit_elect(mma_done);
+        mbar_wait_bounded(mma_done, 0, a.status);
+    } else {
+        // ------------------------------------------------------------ producer
+        const int ppt = 1 << (7 - a.page_shift), page_bytes = D << a.page_shift;
+        // a lane per page of the tile: its id two tiles ahead, its scales one
+        Walk ahead = w;
+        int vv = 0;   // tile of `ahead`'s part
+        struct Page {
+            int pid, h;
+            float ks, vs;
+        };
+        const int64_t stride = a.max_pages;
+        auto fetch = [&]() {
+            Page r{-1, 0, 1.0f, 1.0f};
+            if (ahead.left <= 0) return r;
+            if (lane < ppt) {
+                const int b = plan.member(plan.first(ahead.g));   // the group's first sequence
+                r.pid = a.table[b * stride + ((ahead.v + vv) * ppt + lane)];
+            }
+            r.h = ahead.head();
+            if (++vv == ahead.tiles()) {
+                vv = 0;
+                next(ahead);
+            }
+            return r;
+        };
+        auto scales = [&](Page& r) {
+            if (r.pid >= 0 && r.pid < a.n_pages) {
+                const int64_t at = static_cast<int64_t>(r.pid) * a.Hkv + r.h;
+                r.ks = a.k_scale[at];
+                r.vs = a.v_scale[at];
+            }
+        };
+        Page now = fetch(), soon = fetch();
+        scales(now);
+        const int total = g1 - g0;
+        int x = 0;
+        for (; x < total; ++x) {
+            const Page later = fetch();
+            scales(soon);
+            const int sk = (2 * x) % RS, sv = sk + 1;
+            bool ok = true;
+            if (x >= NI) {
+                const uint32_t turn = static_cast<uint32_t>(x / NI - 1) & 1u;
+                ok = warp_wait(&raw_empty[sk], turn, abort_flag, a.status) &&
+                     warp_wait(&raw_empty[sv], turn, abort_flag, a.status);
+            }
+            if (!ok) break;
+            const bool good = lane < ppt && now.pid >= 0 && now.pid < a.n_pages;
+            const unsigned all_good = __ballot_sync(0xffffffffu, good);
+            const unsigned bad = ((1u << ppt) - 1u) & ~all_good;
+            RawInfo* in = raw_info + x % NI;
+            if (lane < ppt) {
+                in->ke[lane] = scale_exp(now.ks);
+                in->ve[lane] = scale_exp(now.vs);
+            }
+            if (lane == 0) in->bad = static_cast<int>(bad);
+            if (bad && lane == 0) atomicOr(a.status, kStatusPage);
+            __syncwarp();
+            const uint32_t bytes = static_cast<uint32_t>(__popc(all_good)) * page_bytes;
+            if (lane == 0) {   // releases the stores above, too
+                mbar_arrive_expect_tx(&raw_full[sk], bytes);
+                mbar_arrive_expect_tx(&raw_full[sv], bytes);
+            }
+            __syncwarp();
+            if (good) {
+                const int64_t at = (static_cast<int64_t>(now.pid) * a.Hkv + now.h) * page_bytes;
+                bulk_load(smem + C::kRawOff + sk * C::kRaw + lane * page_bytes, p.k_pages + at, page_bytes, &raw_full[sk]);
+                bulk_load(smem + C::kRawOff + sv * C::kRaw + lane * page_bytes, p.v_pages + at, page_bytes, &raw_full[sv]);
+            }
+            now = soon;
+            soon = later;
+        }
+        // No copy may still be on its way into shared memory that the CTA gives up.
+        __syncwarp();
+        if (lane == 0)
+            for (int y = max(x - NI, 0); y < x; ++y) {
+                mbar_wait_bounded(&raw_full[(2 * y) % RS], static_cast<uint32_t>(y / NI) & 1u, a.status);
+                mbar_wait_bounded(&raw_full[(2 * y) % RS + 1], static_cast<uint32_t>(y / NI) & 1u, a.status);
+            }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ merge
+
+// A warp per row: the row's results over the prefix and over its own positions, each whole or in
+// the parts that several CTAs left.  Rows of sequences that share nothing and lie in
+// one CTA are written already.
+constexpr int kMergeWarps = 4;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    kv8_shared_merge_kernel(const __grid_constant__ PreParams p, int row_block, int row8) {
+    constexpr int V = D / 32;
+    const AttnParams& a = p.a;
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");   // the next kernel may set up
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    const bool real = row < static_cast<int64_t>(a.B) * a.Hkv * a.rows;
+    const int u = real ? static_cast<int>(row / a.rows) : 0;   // (sequence, KV head)
+    const int b = u / a.Hkv, h = u - b * a.Hkv, rr = static_cast<int>(row - static_cast<int64_t>(u) * a.rows);
+    const Plan plan(a.plan, a.B);
+    const bool granted = step_granted(a), planned = plan.ok();
+    // own positions: the tiles of all sequences, and of those before b
+    int all = 0, before = 0, n = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int len = a.lens[i];
+        const int k = seq_of(a, len, queries_of(a, granted, i, len), planned ? plan.start(i) : 0).n;
+        all += k;
+        if (i < b) before += k;
+        if (i == b) n = k;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+    n = __reduce_add_sync(0xffffffffu, n);
+    const int U = a.Hkv * a.n_rb;
+    int c0 = 0, c1 = -1, second = 0, r_own = 0;
+    if (n > 0) {
+        const Shares sh(all * U, a.ctas);
+        const int first = before * U + (h * a.n_rb + rr / row8) * n;
+        c0 = sh.owner(first);
+        c1 = sh.owner(first + n - 1);
+        second = first > sh.begin(c0) ? 1 : 0;
+        r_own = rr % row8;
+    }
+    // the prefix
+    const int groups = planned && granted ? plan.groups() : 0;
+    const int g = real && groups > 0 ? plan.group(b) : -1;
+    int d0 = 0, d1 = -1, second_pre = 0, r_pre = 0;
+    int lead = 0;
+    const int T = all_tiles(a, plan, groups, row_block, g, &lead);
+    if (g >= 0 && g < groups) {
+        const Group x = group_of(a, plan, g, row_block);
+        const int64_t r = static_cast<int64_t>(plan.rank(b)) * a.rows + rr;
+        if (x.blocks > 0 && r >= 0 && r < x.rows) {
+            const Shares sh(T, a.ctas, kPreMinShare);
+            const int first = lead + (h * x.n_rb + static_cast<int>(r / row_block)) * x.blocks;
+            d0 = sh.owner(first);
+            d1 = sh.owner(first + x.blocks - 1);
+            second_pre = first > sh.begin(d0) ? 1 : 0;
+            r_pre = static_cast<int>(r % row_block);
+        }
+    }
+    const bool shares = planned && plan.start(b) > 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // in every thread: this grid ends after those
+    if (!real || (!shares && n > 0 && c0 == c1)) return;
+    // results [0, n_own) are over its own positions, the others over the prefix
+    const int n_own = c1 - c0 + 1, n_all = n_own + (d1 - d0 + 1);
+    auto at_own = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? second : 0)) * row8 + r_own; };
+    auto at_pre = [&](int k) {
+        return static_cast<int64_t>(2 * (d0 + k) + (k == 0 ? second_pre : 0)) * row_block + r_pre;
+    };
+    auto lse_of = [&](int k) {
+        if (k < n_own) return n_own == 1 && shares ? a.own_lse[row] : a.part_lse[at_own(k)];
+        return d0 == d1 ? p.row_lse[row] : p.part_lse[at_pre(k - n_own)];
+    };
+    auto o_of = [&](int k) {
+        if (k < n_own) return n_own == 1 && shares ? a.own_o + row * D : a.part_o + at_own(k) * D;
+        return d0 == d1 ? p.row_o + row * D : p.part_o + at_pre(k - n_own) * D;
+    };
+    float M = -INFINITY, sum = 0.0f, acc[V] = {};
+    for (int base = 0; base < n_all; base += 32) {
+        const int cnt = min(32, n_all - base);
+        const float L = lane < cnt ? lse_of(base + lane) : -INFINITY;
+        float M1 = fmaxf(M, L);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, d));
+        const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - M1);
+        const float w = L == -INFINITY ? 0.0f : ex2_ftz(L - M1);
+        M = M1;
+        sum *= al;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= al;
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* src = o_of(base + k) + lane * V;
+            float x[V];
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[0] = y.x, x[1] = y.y;
+            }
+            sum += wk;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, x[i], acc[i]);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t*>(out + i) =
+            sum == 0.0f ? 0u : pack2<BF16>(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + lg2_approx(sum)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ the plan
+
+struct FindParams {
+    const int* table;
+    const int* lens;
+    int* plan;
+    int B, max_pages, page_shift, min_saved;
+};
+constexpr int kFindThreads = 128;
+
+// Columns of a run of kShareBlock positions.
+__device__ __forceinline__ int block_cols(const FindParams& p) { return kShareBlock >> p.page_shift; }
+// Runs that a sequence's length and table hold in full.
+__device__ __forceinline__ int full_blocks(const FindParams& p, int len) {
+    return min(max(len, 0), p.max_pages << p.page_shift) / kShareBlock;
+}
+
+// How far sequence b should share, a CTA each: of the depths at which its last page is also the one of
+// r - 1 others', that which leaves it the least to read, depth (r - 1) / r saved.  (Pages
+// of a sequence that several hold are those of its whole beginning; the next kernel looks.)
+__global__ void __launch_bounds__(kFindThreads) kvp_depth_kernel(const FindParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float s_gain[kFindThreads / 32];
+    __shared__ int s_at[kFindThreads / 32];
+    const int b = static_cast<int>(blockIdx.x), cols = block_cols(p);
+    const int n = full_blocks(p, p.lens[b]);
+    const int64_t stride = p.max_pages;
+    float gain = 0.0f;
+    int at = -1;
+    for (int base = 0; base < n; base += kFindThreads) {
+        const int i = base + static_cast<int>(threadIdx.x);
+        int r = 0;
+        if (i < n) {
+            const int c = (i + 1) * cols - 1, pid = p.table[b * stride + c];
+            if (pid >= 0)
+                for (int k = 0; k < p.B; ++k)
+                    if (p.table[k * stride + c] == pid && full_blocks(p, p.lens[k]) > i) ++r;
+        }
+        const float x = r > 1 ? static_cast<float>(i + 1) * static_cast<float>(r - 1) / static_cast<float>(r) : 0.0f;
+        if (x > gain) gain = x, at = i;
+        if (!__syncthreads_or(r > 1)) break;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, gain, d);
+        const int y = __shfl_xor_sync(0xffffffffu, at, d);
+        if (x > gain || (x == gain && y > at)) gain = x, at = y;
+    }
+    if ((threadIdx.x & 31) == 0) s_gain[threadIdx.x >> 5] = gain, s_at[threadIdx.x >> 5] = at;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < kFindThreads / 32; ++k)
+            if (s_gain[k] > gain || (s_gain[k] == gain && s_at[k] > at)) gain = s_gain[k], at = s_at[k];
+        int* scratch = p.plan + 4 + kPlanArrays * p.B;
+        scratch[b] = at + 1;                                                          // depth, 0: none
+        scratch[p.B + b] = at >= 0 ? p.table[b * stride + (at + 1) * cols - 1] : -1;   // its last page
+    }
+}
+
+// Whose group: the first sequence of the same depth and last page, if all pages before are
+// its, too (-1: none).
+__global__ void __launch_bounds__(kFindThreads) kvp_leader_kernel(const FindParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ int s_first;
+    const int b = static_cast<int>(blockIdx.x);
+    int* scratch = p.plan + 4 + kPlanArrays * p.B;
+    const int depth = scratch[b], key = scratch[p.B + b];
+    if (threadIdx.x == 0) s_first = b;
+    __syncthreads();
+    if (depth > 0)
+        for (int k = threadIdx.x; k < b; k += kFindThreads)
+            if (scratch[k] == depth && scratch[p.B + k] == key) atomicMin(&s_first, k);
+    __syncthreads();
+    const int first = s_first, cols = depth * block_cols(p);
+    const int64_t stride = p.max_pages;
+    int same = depth > 0;
+    if (first != b)
+        for (int c = threadIdx.x; c < cols; c += kFindThreads)
+            if (p.table[b * stride + c] != p.table[first * stride + c]) same = 0;
+    same = __syncthreads_and(same);
+    if (threadIdx.x == 0) scratch[2 * p.B + b] = same ? first : -1;
+}
+
+// The plan, one CTA: groups of two or more that save enough, in the order of their first sequences.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams p) {
+    __shared__ int s_leader[kMaxBatch], s_count[kMaxBatch], s_group[kMaxBatch], s_off[kMaxBatch];
+    __shared__ int s_warp[2][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = static_cast<int>(threadIdx.x), lane = b & 31, warp = b >> 5;
+    const int* scratch = p.plan + 4 + kPlanArrays * p.B;
+    const int depth = b < p.B ? scratch[b] : 0, leader = b < p.B ? scratch[2 * p.B + b] : -1;
+    s_leader[b] = leader;
+    s_count[b] = 0;
+    __syncthreads();
+    if (leader >= 0) atomicAdd(&s_count[leader], 1);
+    __syncthreads();
+    // leaders of groups that stay
+    const int64_t saved = static_cast<int64_t>(s_count[b] - 1) * depth * kShareBlock;
+    const bool stays = leader == b && s_count[b] > 1 && saved >= p.min_saved;
+    int g = stays ? 1 : 0, off = stays ? s_count[b] : 0;   // prefix sums over the sequences
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, g, d), y = __shfl_up_sync(0xffffffffu, off, d);
+        if (lane >= d) g += x, off += y;
+    }
+    if (lane == 31) s_warp[0][warp] = g, s_warp[1][warp] = off;
+    __syncthreads();
+    int groups = 0, members = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+        if (i < warp) g += s_warp[0][i], off += s_warp[1][i];
+        groups += s_warp[0][i];
+        members += s_warp[1][i];
+    }
+    s_group[b] = stays ? g - 1 : -1;
+    s_off[b] = stays ? off - s_count[b] : 0;
+    __syncthreads();
+    auto put = [&](int array, int i, int x) { p.plan[4 + array * p.B + i] = x; };
+    if (stays) {
+        put(0, g - 1, off - s_count[b]);
+        put(1, g - 1, s_count[b]);
+        put(2, g - 1, depth);
+    }
+    if (b >= groups && b < p.B) {   // entries of no group
+        put(0, b, 0);
+        put(1, b, 0);
+        put(2, b, 0);
+    }
+    if (b >= members && b < p.B) put(3, b, 0);
+    if (b < p.B) {
+        const int mine = leader >= 0 ? s_group[leader] : -1;
+        int rank = 0;
+        if (mine >= 0) {
+            for (int k = 0; k < b; ++k) rank += s_leader[k] == leader;
+            put(3, s_off[leader] + rank, b);
+        }
+        put(4, b, mine);
+        put(5, b, rank);
+        put(6, b, mine >= 0 ? depth * kShareBlock : 0);
+    }
+    if (b == 0) {
+        p.plan[1] = groups;
+        p.plan[2] = p.B;
+        p.plan[3] = 0;
+        p.plan[0] = kPlanMagic;
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows of a CTA of the prefix kernel: one Q tile where all the batch's rows of a KV head fit it.
+int prefix_tiles(int B, int64_t rows) { return B * rows <= kPreRows ? 1 : 2; }
+
+struct SharedSizes {
+    size_t own_part, own_o, own_lse, row_o, row_lse, part_o, part_lse;
+    size_t total() const { return own_part + own_o + own_lse + row_o + row_lse + part_o + part_lse; }
+};
+SharedSizes shared_sizes(int B, int Hq, int Hkv, int Nq, int D, int sms) {
+    const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
+    const size_t all = static_cast<size_t>(B) * Hq * Nq;
+    const size_t parts = 2 * static_cast<size_t>(sms) * prefix_tiles(B, rows) * kPreRows;
+    return {part_bytes(rows, D, sms),          pad256(all * D * sizeof(float)), pad256(all * sizeof(float)),
+            pad256(all * D * sizeof(float)),   pad256(all * sizeof(float)),
+            pad256(parts * D * sizeof(float)), pad256(parts * sizeof(float))};
+}
+
+template <int D, bool BF16, int QT>
+cudaError_t launch_prefix(const PreParams& p, cudaStream_t stream) {
+    auto kern = kv8_prefix_kernel<D, BF16, QT>;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(kern, PreCfg<D, QT>::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, p.a.ctas, PreCfg<D, QT>::kThreads, PreCfg<D, QT>::kSmem, stream, p);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_shared_merge(const PreParams& p, int row_block, int row8, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(p.a.B) * p.a.Hkv * p.a.rows;
+    return launch_dependent(kv8_shared_merge_kernel<D, BF16>, (rows + kMergeWarps - 1) / kMergeWarps,
+                            kMergeWarps * 32, 0, stream, p, row_block, row8);
+}
+
+}  // namespace
+}  // namespace tme
+
+using namespace tme;
+
+extern "C" size_t kvp_plan_words(int n_seqs) {
+    if (n_seqs <= 0 || n_seqs > kMaxBatch) return 0;
+    return 4 + static_cast<size_t>(kPlanArrays + kPlanScratch) * n_seqs;
+}
+
+extern "C" int kvp_find_shared(const int* table, const int* lens, int n_seqs, int max_pages, int page,
+                               int min_saved, int* plan, void* stream) {
+    if (!table || !lens || !plan || n_seqs <= 0 || max_pages <= 0 || page <= 0 || min_saved < 0)
+        return ATTN_ERR_INVALID;
+    if (n_seqs > kMaxBatch) return ATTN_ERR_UNSUPPORTED;
+    int rc = check_cache(n_seqs, 1, 64, page, 1, max_pages);
+    if (rc != ATTN_OK) return rc;
+    const void* words[] = {table, lens, plan};
+    if (!aligned(words, 4)) return ATTN_ERR_ALIGN;
+    unsigned int* status;
+    if ((rc = device_setup_public(&status)) != ATTN_OK) return rc;
+    const int shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+    const FindParams p{table, lens, plan, n_seqs, max_pages, shift, min_saved};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_kernel(kvp_depth_kernel, dim3(n_seqs), dim3(kFindThreads), 0, st, p);
+    if (e == cudaSuccess) e = launch_dependent(kvp_leader_kernel, n_seqs, kFindThreads, 0, st, p);
+    if (e == cudaSuccess) e = launch_dependent(kvp_plan_kernel, 1, kPlanThreads, 0, st, p);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" size_t kv8_attn_shared_workspace_size(int B, int Hq, int Hkv, int Nq, int D) {
+    if (kv8_attn_workspace_size(B, Hq, Hkv, Nq, D) == 0) return 0;
+    const int sms = device_sms();
+    return shared_sizes(B, Hq, Hkv, Nq, D, sms > 0 ? sms : 1).total();
+}
+
+extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v_pages,
+                               const float* k_scale, const float* v_scale, const int* table,
+                               const int* lens, const int* n_new, const int* granted, const int* plan,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, int B,
+                               int Hq, int Hkv, int Nq, int D, int page, int n_pages, int max_pages,
+                               float scale, int dtype, void* stream) {
+    if (!plan) return ATTN_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(plan) & 3) return ATTN_ERR_ALIGN;
+    PreParams p{};
+    int rc = attn_params(&p.a, q, k_pages, v_pages, k_scale, v_scale, table, lens, n_new, granted, out, lse,
+                         workspace, workspace_bytes, kv8_attn_shared_workspace_size(B, Hq, Hkv, Nq, D), B,
+                         Hq, Hkv, Nq, D, page, n_pages, max_pages, scale, 0, 0, dtype);
+    if (rc != ATTN_OK) return rc;
+    const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
+    const int qt = prefix_tiles(B, rows), row_block = qt * kPreRows;
+    // tiles of all groups, and rows, are counted in 32 bits; B / 2 groups at most
+    const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
+    if (rows > 1 << 20 || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + 1) > 0x7fffffffll ||
+        (static_cast<int64_t>(B) * Hkv * rows + kMergeWarps - 1) / kMergeWarps > 0x7fffffffll)
+        return ATTN_ERR_UNSUPPORTED;
+    const SharedSizes z = shared_sizes(B, Hq, Hkv, Nq, D, p.a.ctas);
+    char* at = static_cast<char*>(workspace) + z.own_part;
+    auto take = [&](size_t bytes) {
+        float* r = reinterpret_cast<float*>(at);
+        at += bytes;
+        return r;
+    };
+    p.a.plan = plan;
+    p.a.own_o = take(z.own_o);
+    p.a.own_lse = take(z.own_lse);
+    p.row_o = take(z.row_o);
+    p.row_lse = take(z.row_lse);
+    p.part_o = take(z.part_o);
+    p.part_lse = take(z.part_lse);
+    p.k_pages = static_cast<const uint8_t*>(k_pages);
+    p.v_pages = static_cast<const uint8_t*>(v_pages);
+    const bool bf16 = dtype == ATTN_BF16;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaErrorInvalidValue;
+#define TME_PREFIX(d, b, n) \
+    if (D == d && bf16 == b && qt == n) e = launch_prefix<d, b, n>(p, st);
+    TME_PREFIX(64, false, 1)
+    TME_PREFIX(64, false, 2)
+    TME_PREFIX(64, true, 1)
+    TME_PREFIX(64, true, 2)
+    TME_PREFIX(128, false, 1)
+    TME_PREFIX(128, false, 2)
+    TME_PREFIX(128, true, 1)
+    TME_PREFIX(128, true, 2)
+#undef TME_PREFIX
+    if (e != cudaSuccess) return ATTN_ERR_CUDA;
+    rc = attn_launch_shared(p.a, k_pages, v_pages, D, page, bf16, st);
+    if (rc != ATTN_OK) return rc;
+    const int row8 = 8 * row_tiles(rows);
+    e = D == 64 ? (bf16 ? launch_shared_merge<64, true>(p, row_block, row8, st)
+                        : launch_shared_merge<64, false>(p, row_block, row8, st))
+                : (bf16 ? launch_shared_merge<128, true>(p, row_block, row8, st)
+                        : launch_shared_merge<128, false>(p, row_block, row8, st));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
