@@ -238,11 +238,10 @@ def test_attention_matches_the_definition(cuda_lib, case):
     _check(q, cache, None, out, lse, f"shared {case}")
     again = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
-    # a plan without groups is the plain call, bit for bit
+    # without groups every sequence reads for itself
     none = _lib.kvp_find_shared(dev[4], dev[5], page, (1 << 31) - 1)
     assert _read_plan(none, B) == {}
-    a, b = _lib.kv8_attn_shared(q.cuda(), *dev, none), _lib.kv8_attn(q.cuda(), *dev)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    _check(q, cache, None, *_lib.kv8_attn_shared(q.cuda(), *dev, none), f"shared without groups {case}")
     assert _lib.sync_status() == _lib.ATTN_OK
 
 
@@ -322,7 +321,8 @@ def test_bad_pages_and_plans_are_recorded(cuda_lib):
         helpers.assert_fwd_close(out[b].double().cpu().numpy(), lse[b].double().cpu().numpy(), ref.view(4, 1, 64).numpy(),
                                  torch.logsumexp(s, -1).view(4, 1).numpy(), F16, f"bad pages, sequence {b}")
     # what is not a plan: recorded, and every sequence reads for itself
-    want = _lib.kv8_attn(q.cuda(), *dev)
+    none = _lib.kvp_find_shared(dev[4], dev[5], 32, (1 << 31) - 1)
+    want = _lib.kv8_attn_shared(q.cuda(), *dev, none)
     other = _lib.kvp_find_shared(dev[4][:4].contiguous(), dev[5][:4].contiguous(), 32, 0)
     for junk in (torch.zeros_like(plan), torch.full_like(plan, 10 ** 9), torch.cat([other, other])[: plan.numel()]):
         out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, junk)

@@ -188,6 +188,14 @@ struct Shares {
     }
 };
 
+// Behind a shared prefix each warp of the attention has a share (up to 16 query rows; with
+// more the CTA has), of this many tiles at least.
+constexpr int kAttnWarps = 8, kWarpMinShare = 2;
+inline __host__ __device__ int own_workers(int ctas, int rows) { return rows <= 16 ? ctas * kAttnWarps : ctas; }
+__device__ __forceinline__ Shares own_shares(const AttnParams& p, int T) {
+    return Shares(T, own_workers(p.ctas, p.rows), p.rows <= 16 ? kWarpMinShare : kMinShare);
+}
+
 // What kvp_find_shared leaves: a header, then arrays of n_seqs words.  Group g are the
 // sequences members[first[g] .. + count[g]), in ascending order; the first `blocks[g]` runs of
 // kShareBlock positions of all of them lie in the pages of the first one's table row.

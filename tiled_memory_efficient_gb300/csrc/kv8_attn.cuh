@@ -57,7 +57,7 @@ namespace {
 
 // Warps per CTA: 12 of them with 2 slots each instead of 3 took 5.4 us against 4.8 (8
 // sequences of 256 tokens, D = 64) and 51.4 against 50.4 (64K tokens, D = 128).
-constexpr int kWarps = 8;
+constexpr int kWarps = kAttnWarps;
 constexpr int kAttnThreads = kWarps * 32;
 // Token that row m of a 16-token product tile stands for (both halves of 8
 // alike).  The 16-byte shared loads of K (lanes g = m, chunk t) and of V (lanes
@@ -142,13 +142,18 @@ struct AttnCfg {
 
 // ONE: a tile lies in one page (page >= the tile's tokens); else it takes 2 or 4 boxes.
 // SHARED: behind a shared prefix's attention (kv8_shared.cu): a sequence's tiles start after its prefix,
-// and its rows go to own_o and own_lse in fp32, for the merge with the prefix's.
+// and its rows go to own_o and own_lse in fp32, for the merge with the prefix's.  What is left behind
+// a prefix is short, a few tiles a unit, and the end of a unit that 8 warps share costs more than its
+// tiles: up to 16 query rows each warp therefore takes a share of its own, whose units it
+// ends by itself (128 sequences of 1 to 1000 positions, 8 KV heads, D = 128: 77 us so, 36 alone).
 template <int D, bool BF16, int NR, bool ONE, bool SHARED>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnParams p) {
     using C = AttnCfg<D, NR>;
+    constexpr bool ALONE = SHARED && NR < 4;   // every warp has a share of its own (below)
     constexpr int ST = C::kStages, kTile = C::kTile;
+    constexpr int STEP = ALONE ? 1 : kWarps;   // tiles from one of a warp's to its next
     constexpr int NQ = kTile / 16;     // 16-token quarters of a tile (2 or 4)
     constexpr int KC = D / 64;         // 16-byte chunks of a K row per lane
     constexpr int MT = D / 16;         // 16-dimension tiles of O^T
@@ -226,8 +231,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (threadIdx.x == 0) s_pre[p.B] = carry;
     __syncthreads();
     const int U = p.Hkv * p.n_rb;
-    const Shares sh(carry * U, p.ctas);
-    const int c = static_cast<int>(blockIdx.x);
+    const Shares sh = ALONE ? own_shares(p, carry * U) : Shares(carry * U, p.ctas);
+    // (consecutive shares of warps on different SMs)
+    const int c = static_cast<int>(blockIdx.x) + (ALONE ? warp * p.ctas : 0);
     if (c >= sh.n) {   // nothing in flight, no barrier left
         if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
@@ -436,13 +442,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         cp_async_arrive(&full[lane]);
         ++issued;
-        nv += kWarps * ST;
+        nv += STEP * ST;
         fetch();
     };
     if (lane < ST) {
-        const int first = g0 + warp + kWarps * lane;
+        const int first = g0 + (ALONE ? 0 : warp) + STEP * lane;
         if (first < g1) {
-            left = (g1 - first + kWarps * ST - 1) / (kWarps * ST);
+            left = (g1 - first + STEP * ST - 1) / (STEP * ST);
             nb = b;
             nu = u;
             nv = v_first + first - g0;   // fetch carries it into later units
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int tok_v0 = tok8<D>(2 * t), tok_v1 = tok8<D>(2 * t + 1);
 
     // ---- the share, unit by unit
-    int mine = g0 + warp;       // this warp's next tile
+    int mine = g0 + (ALONE ? 0 : warp);   // this warp's next tile
     int slot = 0;               // of that tile
     uint32_t phase = 0;         // and its turn of the ring
     while (unit0 < g1) {
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
         }
 
-        for (; mine < end; mine += kWarps) {
+        for (; mine < end; mine += STEP) {
             const int tok = seq_tile(s, mine - unit0) * kTile;
             warp_wait(&full[slot], phase, abort_flag, p.status);
             const uint32_t sk = smem_u32(ring + slot * C::kSlot), sv = sk + C::kHalf;
@@ -726,6 +732,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             while (unit0 < g1 && s_pre[b + 1] == s_pre[b]);   // empty sequences
         }
         if (unit0 < g1) load_q(b, u);
+        if constexpr (ALONE) {
+            // this warp alone: lane (g, t) holds dimensions VB g .. + VB - 1 of rows 2t, 2t + 1 of each 8
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[nt][e];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    const int i = nt * 8 + 2 * t + e;
+                    if (row0 + i >= p.rows) continue;
+                    const bool empty = x == 0.0f;   // sees nothing: 0, beside a NaN that others see, too
+                    const float L = empty ? -INFINITY : m[nt][e] + lg2_approx(x);   // a NaN stays one
+                    const float f = empty ? 0.0f : ex2_ftz(R[nt][e] - m[nt][e]) / x;
+                    const int64_t row = head_row + row0 + i, at = static_cast<int64_t>(part) * (8 * NR) + i;
+                    if (g == 0) {
+                        if (!whole) p.part_lse[at] = L;
+                        else if (joins) p.own_lse[row] = L;
+                        else p.lse[row] = L * 0.6931471805599453f;
+                    }
+                    float y[VB];
+#pragma unroll
+                    for (int k = 0; k < VB / 2; ++k) {
+                        y[2 * k] = empty ? 0.0f : o[nt][k][e] * f;
+                        y[2 * k + 1] = empty ? 0.0f : o[nt][k][e + 2] * f;
+                    }
+                    if (whole && !joins) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + VB * g);
+#pragma unroll
+                        for (int k = 0; k < VB / 8; ++k)
+                            dst[k] = make_uint4(pack2<BF16>(y[8 * k], y[8 * k + 1]), pack2<BF16>(y[8 * k + 2], y[8 * k + 3]),
+                                                pack2<BF16>(y[8 * k + 4], y[8 * k + 5]),
+                                                pack2<BF16>(y[8 * k + 6], y[8 * k + 7]));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>((whole ? p.own_o + row * D : p.part_o + at * D) + VB * g);
+#pragma unroll
+                        for (int k = 0; k < VB / 4; ++k)
+                            dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    }
+                }
+        } else {
         // Every warp's LSE of each row to shared memory; then lane i weighs row i of
         // the unit (mod 8 NR), and this lane's columns take their rows' factors.
         float up[NR][2];   // brings O^T to real units, then to the warp's share of the row
@@ -805,6 +852,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         p.part_o + (static_cast<int64_t>(part) * (8 * NR) + r) * D + dim) =
                         make_float2(ox, oy);
             }
+        }
         }
     }
     // After a wait that gave up, copies may still be on their way into this

@@ -38,18 +38,15 @@ struct PreParams {
     float* part_lse;
 };
 
-// What the producer leaves beside a raw tile: the exponents of its pages' scales, and which
-// pages hold nothing readable.
-struct RawInfo {
-    int ke[8], ve[8];
-    int bad, pad[3];
-};
-// What the converters leave for the softmax: keys are 2^e of this times their fp16 values,
-// the accumulator's values 2^ev.
+// What the producer leaves beside a raw tile: keys are kf times their fp16 values, the accumulator's
+// values 2^ev; bad: pages (bits) that hold nothing readable; scaled: whether some page's keys (1) or
+// values (2) are moved by a power of two on their way to fp16, and by which (two fp16 each).
 struct TileInfo {
     float kf;
-    int ev, bad, pad;
+    int ev, bad, scaled;
+    uint32_t factor[2][8];
 };
+constexpr int kInfos = 8;   // of them: the softmax may be four tiles behind the producer
 
 // QT: Q tiles of a CTA (128 rows each).
 template <int D, int QT>
@@ -61,10 +58,9 @@ struct PreCfg {
     static constexpr int kKOff = QT * kTile16;
     static constexpr int kVOff = kKOff + 2 * kTile16;
     static constexpr int kRawOff = kVOff + 2 * kTile16;
-    static constexpr int kRawInfoOff = kRawOff + kRawSlots * kRaw;
-    static constexpr int kTileInfoOff = kRawInfoOff + kRawSlots / 2 * static_cast<int>(sizeof(RawInfo));
-    static constexpr int kBarOff = kTileInfoOff + 4 * static_cast<int>(sizeof(TileInfo));
-    static constexpr int kBars = 2 * kRawSlots + 8 + 4 + 2 + 2 + QT * 2 + 1;
+    static constexpr int kInfoOff = kRawOff + kRawSlots * kRaw;
+    static constexpr int kBarOff = kInfoOff + kInfos * static_cast<int>(sizeof(TileInfo));
+    static constexpr int kBars = 2 * kRawSlots + 8 + kInfos + 2 + 2 + QT * 2 + 1;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -75,15 +71,14 @@ struct PreCfg {
 
 // Tiles, units and rows of a group.
 struct Group {
-    int blocks, n_rb, units;
-    int64_t rows;
+    int blocks, n_rb, units, rows;
     __device__ __forceinline__ int tiles() const { return units * blocks; }
 };
 __device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan, int g, int row_block) {
     Group x;
     x.blocks = min(plan.blocks(g), (p.max_pages << p.page_shift) / kShareBlock);
-    x.rows = static_cast<int64_t>(plan.count(g)) * p.rows;
-    x.n_rb = static_cast<int>((x.rows + row_block - 1) / row_block);
+    x.rows = plan.count(g) * p.rows;   // at most 2^30 (checked on the host)
+    x.n_rb = (x.rows + row_block - 1) / row_block;
     x.units = p.Hkv * x.n_rb;
     return x;
 }
@@ -119,9 +114,7 @@ struct Walk {
         }
     }
     __device__ __forceinline__ int head() const { return u / x.n_rb; }
-    __device__ __forceinline__ int64_t row0(int row_block) const {
-        return static_cast<int64_t>(u - head() * x.n_rb) * row_block;
-    }
+    __device__ __forceinline__ int row0(int row_block) const { return (u - head() * x.n_rb) * row_block; }
 };
 // The share of CTA c that starts at tile g0 and ends at g1 (g0 < g1).
 __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block, int g0,
@@ -178,9 +171,9 @@ __device__ __forceinline__ uint32_t pow2_f16x2(int d) {
     return h | (h << 16);
 }
 
+// (no "memory": what reads it is behind a fence, and other loads may pass)
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& x) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
 }
 __device__ __forceinline__ uint4 lds128v(uint32_t a) {
     uint4 r;
@@ -206,20 +199,20 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
     kv8_prefix_kernel(const __grid_constant__ PreParams p) {
     using C = PreCfg<D, QT>;
     constexpr int RS = C::kRawSlots, NI = RS / 2, RB = C::kRowBlock;
+    static_assert(kInfos >= NI + 3, "a tile's info outlives its softmax");
     constexpr int kOCol = 256;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    RawInfo* raw_info = reinterpret_cast<RawInfo*>(smem + C::kRawInfoOff);      // [NI]
-    volatile TileInfo* tile_info = reinterpret_cast<TileInfo*>(smem + C::kTileInfoOff);   // [4]
+    TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kInfoOff);          // [kInfos]
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);       // [RS]
     uint64_t* raw_empty = raw_full + RS;     // [RS]
     uint64_t* k_full = raw_empty + RS;       // [2] the fp16 tile is written
     uint64_t* k_empty = k_full + 2;          // [2]
     uint64_t* v_full = k_empty + 2;          // [2]
     uint64_t* v_empty = v_full + 2;          // [2]
-    uint64_t* info_full = v_empty + 2;       // [4] tile_info
-    uint64_t* s_full = info_full + 4;        // [2] QT = 2: of tile t; QT = 1: of S buffer x & 1
+    uint64_t* info_full = v_empty + 2;       // [kInfos]
+    uint64_t* s_full = info_full + kInfos;        // [2] QT = 2: of tile t; QT = 1: of S buffer x & 1
     uint64_t* pv_done = s_full + 2;          // [2] PV of tile t done
     uint64_t* p_full = pv_done + 2;          // [QT]
     uint64_t* q_full = p_full + QT;          // [QT]
@@ -262,7 +255,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&pv_done[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&info_full[i], 1);
+        for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
         for (int t = 0; t < QT; ++t) {
             mbar_init(&p_full[t], kPreRows);
             mbar_init(&q_full[t], kPreRows);
@@ -290,84 +283,125 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         // place among all rows, its scores' factor
         bool exists = false;
         int pos = -1;
-        int64_t row_id = 0;
+        int row_id = 0;
         float f_row = 0.0f;
         // Q of a part's tile t: each thread its own row, bf16 brought into fp16's range by a power of
         // two first (as in kv8_attn).  S of the part before has been computed.
         auto load_q = [&](const Walk& x) {
-            const int64_t r = x.row0(RB) + t * kPreRows + rl;
+            const int r = x.row0(RB) + t * kPreRows + rl;
             exists = r < x.x.rows;
             pos = -1;
-            uint32_t q[D / 2];
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) q[i] = 0u;
-            int shift = 0;
+            const uint4* src = nullptr;
             if (exists) {
-                const int m = static_cast<int>(r / a.rows), rr = static_cast<int>(r - static_cast<int64_t>(m) * a.rows);
+                const int m = r / a.rows, rr = r - m * a.rows;
                 const int b = plan.member(plan.first(x.g) + m);
                 const int len = a.lens[b], nq = queries_of(a, granted, b, len);
                 const int i = rr % a.Nq;
                 if (i < nq) pos = min(max(len, 0), a.max_pages << a.page_shift) - nq + i;
-                row_id = (static_cast<int64_t>(b) * a.Hkv + x.head()) * a.rows + rr;
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row_id * D);
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
+                row_id = (b * a.Hkv + x.head()) * a.rows + rr;
+                src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(row_id) * D);
+            }
+            int shift = 0;
+            if constexpr (BF16) {
+                uint32_t ex = 0u;   // largest finite exponent field
+#pragma unroll 4
+                for (int k = 0; k < D / 8 && exists; ++k) {
                     const uint4 v = src[k];
-                    q[4 * k] = v.x, q[4 * k + 1] = v.y, q[4 * k + 2] = v.z, q[4 * k + 3] = v.w;
-                }
-                if constexpr (BF16) {
-                    uint32_t ex = 0u;   // largest finite exponent field
+                    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int k = 0; k < D / 2; ++k) {
-                        const uint32_t lo = (q[k] >> 7) & 0xffu, hi = (q[k] >> 23) & 0xffu;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = (q[e] >> 7) & 0xffu, hi = (q[e] >> 23) & 0xffu;
                         ex = max(ex, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
                     }
-                    shift = ex == 0u ? 0 : min(14 + 127 - static_cast<int>(ex), 126);
-                    const float up = exp2i(shift);
-#pragma unroll
-                    for (int k = 0; k < D / 2; ++k) {
-                        const float2 v = unpack16<true>(q[k]);
-                        q[k] = pack2<false>(v.x * up, v.y * up);
-                    }
                 }
+                shift = ex == 0u ? 0 : min(14 + 127 - static_cast<int>(ex), 126);
             }
+            const float up = exp2i(shift);
             f_row = a.scale_log2 * exp2i(-shift);
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (exists) v = src[k];
+                if constexpr (BF16) {
+                    uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k)
-                sts128(sQ + (k >> 3) * (kPreRows * 128) + rl * 128 + (((k & 7) ^ (rl & 7)) << 4),
-                       make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = unpack16<true>(q[e]);
+                        q[e] = pack2<false>(y.x * up, y.y * up);
+                    }
+                    v = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+                sts128(sQ + (k >> 3) * (kPreRows * 128) + rl * 128 + (((k & 7) ^ (rl & 7)) << 4), v);
+            }
             fence_proxy_async_smem();
             mbar_arrive(&q_full[t]);
         };
         int x = 0;          // tile of the share
         uint32_t ns = 0;    // tiles of this Q tile so far
         bool ok = true;
-        if (active(w, t)) load_q(w);
-        while (w.left > 0 && ok) {
+        // the part whose rows are still to be written (its Q tile's next rows are loaded first)
+        bool pending = false, mine = false, live = false, whole = false;
+        int my_row = 0, part = 0, ev = 0;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+        for (;;) {
+            const bool more = w.left > 0, act = more && active(w, t);
+            if (act) load_q(w);
+            if (pending) {
+                ok = warp_wait(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status);
+                if (!ok) break;
+                tc_fence_after();
+                const bool empty = !live || l == 0.0f;   // (a NaN is not)
+                const float inv = empty ? 0.0f : 1.0f / l, scale = exp2i(ev);
+                const int at = whole ? my_row : part * RB + t * kPreRows + rl;
+                float* dst = (whole ? p.row_o : p.part_o) + static_cast<int64_t>(at) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c * 32, o);
+                    tmem_wait_ld();
+                    reg_fence(o);
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                y[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[8 * i + k]) * inv * scale);
+                            st_global_v8(dst + c * 32 + 8 * i, y);
+                        }
+                    }
+                }
+                if (mine) (whole ? p.row_lse : p.part_lse)[at] = empty ? -INFINITY : m + lg2_approx(l);
+                tc_fence_before();
+                pending = false;
+            }
+            if (!more) break;
             const int n = w.tiles();
-            if (!active(w, t)) {
+            if (!act) {
                 x += n;
                 next(w);
-                if (w.left > 0 && active(w, t)) load_q(w);
                 continue;
             }
-            const bool mine = exists;
+            mine = exists;
+            my_row = row_id;
             const int my_pos = pos;
-            const int64_t my_row = row_id;
             const float my_f = f_row;
-            const bool live = __any_sync(0xffffffffu, my_pos >= 0);
+            live = __any_sync(0xffffffffu, my_pos >= 0);
             const int min_pos = __reduce_min_sync(0xffffffffu, mine ? my_pos : 0x7fffffff);
-            float m = -INFINITY, l = 0.0f;
-            int ev = 0;
+            m = -INFINITY, l = 0.0f;
+            ev = 0;
+#pragma unroll 1
             for (int j = 0; j < n && ok; ++j, ++x, ++ns) {
                 const uint32_t buf = QT == 1 ? (ns & 1u) : static_cast<uint32_t>(t);
                 const uint32_t tS = tmem + lane_base + buf * 128;
-                ok = warp_wait(&info_full[x & 3], (x >> 2) & 1, abort_flag, a.status);
+                ok = warp_wait(&info_full[x % kInfos], (x / kInfos) & 1, abort_flag, a.status);
                 ok = ok && warp_wait(&s_full[buf], QT == 1 ? (ns >> 1) & 1u : ns & 1u, abort_flag, a.status);
                 if (!ok) break;
                 tc_fence_after();
-                const float f = my_f * tile_info[x & 3].kf;
-                const int ev_now = tile_info[x & 3].ev, bad = tile_info[x & 3].bad;
+                const volatile TileInfo* in = infos + x % kInfos;
+                const float f = my_f * in->kf;
+                const int ev_now = in->ev, bad = in->bad;
                 // QT = 1: S of this tile went out ahead of the last PV.  A warp that arrived for this tile
                 // while another has yet to for the last one would complete that phase in its place; and O is
                 // not to be touched before that PV is done.
@@ -381,35 +415,41 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                     continue;
                 }
                 const int key0 = (w.v + j) * kPreRows;
-                const bool edge = bad != 0 || key0 + kPreRows - 1 > min_pos;
-                auto hide = [&](uint32_t (&s)[32], int k0) {
+                if (bad != 0 || key0 + kPreRows - 1 > min_pos) {
+                    // what the rows do not see, in place in TMEM, 32 keys at a time (tiles that hold the
+                    // queries' own positions, and bad pages, are rare: not in the other tiles' code)
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        tmem_ld32(tS + c * 32, s);
+                        tmem_wait_ld();
+                        reg_fence(s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int k = k0 + i;
-                        if (key0 + k > my_pos || ((bad >> (k >> a.page_shift)) & 1)) s[i] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 32; ++i) {
+                            const int k = c * 32 + i;
+                            if (key0 + k > my_pos || ((bad >> (k >> a.page_shift)) & 1)) s[i] = __float_as_uint(-INFINITY);
+                        }
+                        tmem_st32(tS + c * 32, s);
                     }
-                };
+                    tmem_wait_st();
+                }
+                // Two passes over S, 32 keys at a time, in loops: the four roles run different code on each SM
+                // sub-partition, and what is unrolled waits for its instructions
                 float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
                     uint32_t s0[32], s1[32];
-                    tmem_ld64(tS + c * 32, s0, s1);
+                    tmem_ld64(tS + c, s0, s1);
                     tmem_wait_ld();
                     reg_fence(s0);
                     reg_fence(s1);
-                    if (edge) {
-                        hide(s0, c * 32);
-                        hide(s1, c * 32 + 32);
-                    }
-                    float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+                    float b0 = mx, b1 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
+                    for (int i = 0; i < 32; i += 2) {
                         b0 = fmax3(b0, __uint_as_float(s0[i]), __uint_as_float(s1[i]));
                         b1 = fmax3(b1, __uint_as_float(s0[i + 1]), __uint_as_float(s1[i + 1]));
-                        b2 = fmax3(b2, __uint_as_float(s0[i + 2]), __uint_as_float(s1[i + 2]));
-                        b3 = fmax3(b3, __uint_as_float(s0[i + 3]), __uint_as_float(s1[i + 3]));
                     }
-                    mx = fmax3(mx, fmaxf(b0, b1), fmaxf(b2, b3));
+                    mx = fmaxf(b0, b1);
                 }
                 const float m_new = fmaxf(m, mx * f);
                 const bool need = m_new > m + kPreThreshold;
@@ -418,16 +458,16 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                 const float m_sub = m == -INFINITY ? 0.0f : m;
                 const uint64_t f2s = f2(f, f), nm2 = f2(-m_sub, -m_sub);
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t s[32], pk[16];
-                    tmem_ld32(tS + c * 32, s);
+                    uint32_t now[32], pk[16];
+                    tmem_ld32(tS + c * 32, now);
                     tmem_wait_ld();
-                    reg_fence(s);
-                    if (edge) hide(s, c * 32);
+                    reg_fence(now);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2)
-                        pk[i >> 1] = softmax_pair<false>(s[i], s[i + 1], f2s, nm2, acc[(i >> 1) & 3]);
+                        pk[i >> 1] = softmax_pair<false>(now[i], now[i + 1], f2s, nm2, acc[(i >> 1) & 3]);
+                    // (columns 16 c .. + 15: of scores that are read)
                     tmem_st16(tS + c * 16, pk);
                 }
                 const uint64_t a2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
@@ -438,7 +478,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                 if (j > 0 && __any_sync(0xffffffffu, need || up > 0)) {
                     tc_fence_after();
                     const float o_al = al * exp2i(-min(up, 126));
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(tO + c * 32, o);
@@ -455,107 +495,70 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
             }
             if (!ok) break;
             // where this part's rows go
-            const int done = (g1 - g0) - w.left;   // tiles before the part
-            const bool whole = w.v == 0 && n == w.x.blocks;
-            const int part = 2 * cta + (done == 0 ? 0 : 1);
+            whole = w.v == 0 && n == w.x.blocks;
+            part = 2 * cta + (w.left == g1 - g0 ? 0 : 1);
+            pending = true;
             next(w);
-            if (w.left > 0 && active(w, t)) load_q(w);
-            ok = warp_wait(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const bool empty = !live || l == 0.0f;   // (a NaN is not)
-            const float inv = empty ? 0.0f : 1.0f / l, scale = exp2i(ev);
-            const int64_t at = whole ? my_row : static_cast<int64_t>(part) * RB + t * kPreRows + rl;
-            float* dst = (whole ? p.row_o : p.part_o) + at * D;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + c * 32, o);
-                tmem_wait_ld();
-                reg_fence(o);
-                if (mine) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            y[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[8 * i + k]) * inv * scale);
-                        st_global_v8(dst + c * 32 + 8 * i, y);
-                    }
-                }
-            }
-            if (mine) (whole ? p.row_lse : p.part_lse)[at] = empty ? -INFINITY : m + lg2_approx(l);
-            tc_fence_before();
         }
     } else if (warp < C::kMmaWarp) {
         // ------------------------------------------------------------ converters
         const int ct = threadIdx.x - C::kConvWarp * 32;
-        const int ppt_log = 7 - a.page_shift;   // pages of a tile: 2^ppt_log
-        constexpr int CPR = D / 16;             // 16-value chunks of a row
-        int x = 0;
+        constexpr int KB = D / 64;                // column blocks of an fp16 tile
+        const int total = g1 - g0;
+        // 8 lanes hold chunks 0 .. 3 of a column block in two neighbouring rows (D = 128: of block a in the even
+        // row and of the other one in the odd row, a in turn), so that both their loads and their stores,
+        // units 2 j and 2 j + 1 of the row's swizzled 128 bytes, meet every bank once.
+        const int cj = ct & 3, cs = (ct >> 2) & 1, cr = 2 * (ct >> 3) + cs;   // row modulo 32
+        const uint32_t lo_at = cr * 128 + (((2 * cj) ^ (cr & 7)) << 4);
+        const uint32_t hi_at = cr * 128 + (((2 * cj + 1) ^ (cr & 7)) << 4);
         bool ok = true;
-        while (w.left > 0 && ok) {
-            const int n = w.tiles();
-            int ev = -1000;   // value scale of the accumulator: none yet
-            for (int j = 0; j < n && ok; ++j, ++x) {
-                const int sk = (2 * x) % RS, sv = sk + 1;
-                const uint32_t turn = static_cast<uint32_t>(x / NI) & 1u;
-                const RawInfo* in = raw_info + x % NI;
-                ok = warp_wait(&raw_full[sk], turn, abort_flag, a.status);
-                if (ok && x >= 2) ok = warp_wait(&k_empty[x & 1], ((x - 2) >> 1) & 1, abort_flag, a.status);
+        for (int x = 0; x < total && ok; ++x) {
+            const TileInfo* in = infos + x % kInfos;
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                const int slot = (2 * x) % RS + which;
+                ok = warp_wait(&raw_full[slot], static_cast<uint32_t>(x / NI) & 1u, abort_flag, a.status);
+                uint64_t* empty = which == 0 ? &k_empty[x & 1] : &v_empty[x & 1];
+                if (ok && x >= 2) ok = warp_wait(empty, ((x - 2) >> 1) & 1, abort_flag, a.status);
                 if (!ok) break;
+                const uint32_t src = smem_u32(smem + C::kRawOff + slot * C::kRaw) + cr * D + cj * 16;
+                const uint32_t dst = smem_u32(smem + (which == 0 ? C::kKOff : C::kVOff) + (x & 1) * C::kTile16);
                 const int bad = in->bad;
-                int ke = -1000, ve = -1000, ke_min = 1000, ve_min = 1000;
-                for (int i = 0; i < 1 << ppt_log; ++i) {
-                    if ((bad >> i) & 1) continue;
-                    ke = max(ke, in->ke[i]), ke_min = min(ke_min, in->ke[i]);
-                    ve = max(ve, in->ve[i]), ve_min = min(ve_min, in->ve[i]);
-                }
-                if (ke == -1000) ke = ke_min = 0;
-                ev = max(ev, ve);
-                const int ev_now = ev == -1000 ? 0 : ev;
-                if (ct == 0) {
-                    tile_info[x & 3].kf = exp2i(ke);
-                    tile_info[x & 3].ev = ev_now;
-                    tile_info[x & 3].bad = bad;
-                    mbar_arrive(&info_full[x & 3]);
-                }
+                const bool scaled = (in->scaled >> which) & 1;
+                // 32 rows a turn, asked for a turn ahead
+                uint4 raw[KB], ahead[KB];
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    if (which == 1) {
-                        ok = warp_wait(&raw_full[sv], turn, abort_flag, a.status);
-                        if (ok && x >= 2) ok = warp_wait(&v_empty[x & 1], ((x - 2) >> 1) & 1, abort_flag, a.status);
-                        if (!ok) break;
+                for (int e = 0; e < KB; ++e) raw[e] = lds128v(src + (KB == 1 ? 0 : cs ^ e) * 64);
+#pragma unroll 1
+                for (int i = 0; i < kPreRows; i += 32) {
+                    if (i + 32 < kPreRows) {
+#pragma unroll
+                        for (int e = 0; e < KB; ++e)
+                            ahead[e] = lds128v(src + (i + 32) * D + (KB == 1 ? 0 : cs ^ e) * 64);
                     }
-                    const uint32_t src = smem_u32(smem + C::kRawOff + (which == 0 ? sk : sv) * C::kRaw);
-                    const uint32_t dst = smem_u32(smem + (which == 0 ? C::kKOff : C::kVOff) + (x & 1) * C::kTile16);
-                    const int top = which == 0 ? ke : ev_now;
-                    const bool scaled = which == 0 ? ke_min < ke : ve_min < ev_now;
-#pragma unroll 4
-                    for (int i = ct; i < kPreRows * CPR; i += 128) {
-                        const int r = i / CPR, c = i % CPR, pg = r >> a.page_shift;
+                    const int pg = (i + cr) >> a.page_shift;
+                    uint32_t factor = 0u;
+                    if (scaled) factor = in->factor[which][pg];
+                    const bool drop = (bad >> pg) & 1;
+#pragma unroll
+                    for (int e = 0; e < KB; ++e) {
                         uint4 lo, hi;
-                        uint32_t factor = 0u;
-                        if (scaled) factor = pow2_f16x2((which == 0 ? in->ke[pg] : in->ve[pg]) - top);
-                        convert16(lds128v(src + i * 16), factor, scaled, &lo, &hi);
-                        if ((bad >> pg) & 1) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-                        // 16-byte units 2 (c & 3) and the next of column block c / 4; the second block's
-                        // lanes write theirs the other way round, so that 8 lanes meet every bank once
-                        const uint32_t row = dst + (c >> 2) * (kPreRows * 128) + r * 128;
-                        const int u0 = 2 * (c & 3), swap = (c >> 2) & 1;
-                        sts128(row + (((u0 + swap) ^ (r & 7)) << 4), swap ? hi : lo);
-                        sts128(row + (((u0 + 1 - swap) ^ (r & 7)) << 4), swap ? lo : hi);
+                        convert16(raw[e], factor, scaled, &lo, &hi);
+                        if (drop) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t to = dst + (KB == 1 ? 0 : cs ^ e) * (kPreRows * 128) + i * 128;
+                        sts128(to + lo_at, lo);
+                        sts128(to + hi_at, hi);
+                        raw[e] = ahead[e];
                     }
-                    // the tensor core reads these bytes after the arrival below
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&raw_empty[which == 0 ? sk : sv]);
-                        mbar_arrive(which == 0 ? &k_full[x & 1] : &v_full[x & 1]);
-                    }
+                }
+                // the tensor core reads these bytes after the arrival below
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&raw_empty[slot]);
+                    mbar_arrive(which == 0 ? &k_full[x & 1] : &v_full[x & 1]);
                 }
             }
-            next(w);
         }
     } else if (warp == C::kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
@@ -618,28 +621,35 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         }
         mma_commit_elect(mma_done);
         mbar_wait_bounded(mma_done, 0, a.status);
-    } else {
+    } else if (warp == C::kProducerWarp) {
         // ------------------------------------------------------------ producer
         const int ppt = 1 << (7 - a.page_shift), page_bytes = D << a.page_shift;
         // a lane per page of the tile: its id two tiles ahead, its scales one
         Walk ahead = w;
         int vv = 0;   // tile of `ahead`'s part
+        // the table row of the group's first sequence (looked up when the group changes: two loads that wait for
+        // each other)
+        auto row_of_group = [&]() { return a.table + static_cast<int64_t>(plan.member(plan.first(ahead.g))) * a.max_pages; };
+        const int* row = row_of_group();
         struct Page {
             int pid, h;
+            bool fresh;   // the first tile of a part
             float ks, vs;
         };
-        const int64_t stride = a.max_pages;
+        int head = ahead.head();
         auto fetch = [&]() {
-            Page r{-1, 0, 1.0f, 1.0f};
+            Page r{-1, 0, vv == 0, 1.0f, 1.0f};
             if (ahead.left <= 0) return r;
-            if (lane < ppt) {
-                const int b = plan.member(plan.first(ahead.g));   // the group's first sequence
-                r.pid = a.table[b * stride + ((ahead.v + vv) * ppt + lane)];
-            }
-            r.h = ahead.head();
+            if (lane < ppt) r.pid = row[(ahead.v + vv) * ppt + lane];
+            r.h = head;
             if (++vv == ahead.tiles()) {
                 vv = 0;
+                const int g = ahead.g;
                 next(ahead);
+                if (ahead.left > 0) {
+                    head = ahead.head();
+                    if (ahead.g != g) row = row_of_group();
+                }
             }
             return r;
         };
@@ -653,50 +663,64 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         Page now = fetch(), soon = fetch();
         scales(now);
         const int total = g1 - g0;
-        int x = 0;
-        for (; x < total; ++x) {
+        int issued = 0;   // raw tiles, K and V in turn
+        int ev = -1000;   // value scale of the accumulator: none yet
+        for (int x = 0; x < total; ++x) {
             const Page later = fetch();
             scales(soon);
-            const int sk = (2 * x) % RS, sv = sk + 1;
-            bool ok = true;
-            if (x >= NI) {
-                const uint32_t turn = static_cast<uint32_t>(x / NI - 1) & 1u;
-                ok = warp_wait(&raw_empty[sk], turn, abort_flag, a.status) &&
-                     warp_wait(&raw_empty[sv], turn, abort_flag, a.status);
-            }
-            if (!ok) break;
             const bool good = lane < ppt && now.pid >= 0 && now.pid < a.n_pages;
             const unsigned all_good = __ballot_sync(0xffffffffu, good);
             const unsigned bad = ((1u << ppt) - 1u) & ~all_good;
-            RawInfo* in = raw_info + x % NI;
-            if (lane < ppt) {
-                in->ke[lane] = scale_exp(now.ks);
-                in->ve[lane] = scale_exp(now.vs);
-            }
-            if (lane == 0) in->bad = static_cast<int>(bad);
-            if (bad && lane == 0) atomicOr(a.status, kStatusPage);
-            __syncwarp();
             const uint32_t bytes = static_cast<uint32_t>(__popc(all_good)) * page_bytes;
-            if (lane == 0) {   // releases the stores above, too
-                mbar_arrive_expect_tx(&raw_full[sk], bytes);
-                mbar_arrive_expect_tx(&raw_full[sv], bytes);
+            const int64_t at = (static_cast<int64_t>(now.pid) * a.Hkv + now.h) * page_bytes;
+            bool ok = true;
+#pragma unroll 1
+            for (int which = 0; which < 2; ++which) {
+                const int slot = (2 * x) % RS + which;
+                if (x >= NI)
+                    ok = warp_wait(&raw_empty[slot], static_cast<uint32_t>(x / NI - 1) & 1u, abort_flag, a.status);
+                if (!ok) break;
+                if (which == 0) {
+                    // the keys' largest scale; the values', of the unit's part so far
+                    const int ke = good ? scale_exp(now.ks) : -1000, ve = good ? scale_exp(now.vs) : -1000;
+                    int top = __reduce_max_sync(0xffffffffu, ke);
+                    if (now.fresh) ev = -1000;
+                    ev = max(ev, __reduce_max_sync(0xffffffffu, ve));
+                    const int ev_now = ev == -1000 ? 0 : ev;
+                    if (top == -1000) top = 0;
+                    TileInfo* in = infos + x % kInfos;
+                    if (lane < ppt) {
+                        in->factor[0][lane] = good ? pow2_f16x2(ke - top) : 0u;
+                        in->factor[1][lane] = good ? pow2_f16x2(ve - ev_now) : 0u;
+                    }
+                    const int scaled = (__any_sync(0xffffffffu, good && ke != top) ? 1 : 0) |
+                                       (__any_sync(0xffffffffu, good && ve != ev_now) ? 2 : 0);
+                    if (lane == 0) {
+                        in->kf = exp2i(top);
+                        in->ev = ev_now;
+                        in->bad = static_cast<int>(bad);
+                        in->scaled = scaled;
+                        if (bad) atomicOr(a.status, kStatusPage);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&info_full[x % kInfos]);
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], bytes);   // releases the stores above, too
+                __syncwarp();
+                if (good)
+                    bulk_load(smem + C::kRawOff + slot * C::kRaw + lane * page_bytes,
+                              (which == 0 ? p.k_pages : p.v_pages) + at, page_bytes, &raw_full[slot]);
+                ++issued;
             }
-            __syncwarp();
-            if (good) {
-                const int64_t at = (static_cast<int64_t>(now.pid) * a.Hkv + now.h) * page_bytes;
-                bulk_load(smem + C::kRawOff + sk * C::kRaw + lane * page_bytes, p.k_pages + at, page_bytes, &raw_full[sk]);
-                bulk_load(smem + C::kRawOff + sv * C::kRaw + lane * page_bytes, p.v_pages + at, page_bytes, &raw_full[sv]);
-            }
+            if (!ok) break;
             now = soon;
             soon = later;
         }
         // No copy may still be on its way into shared memory that the CTA gives up.
         __syncwarp();
         if (lane == 0)
-            for (int y = max(x - NI, 0); y < x; ++y) {
-                mbar_wait_bounded(&raw_full[(2 * y) % RS], static_cast<uint32_t>(y / NI) & 1u, a.status);
-                mbar_wait_bounded(&raw_full[(2 * y) % RS + 1], static_cast<uint32_t>(y / NI) & 1u, a.status);
-            }
+            for (int y = max(issued - RS, 0); y < issued; ++y)
+                mbar_wait_bounded(&raw_full[y % RS], static_cast<uint32_t>(y / RS) & 1u, a.status);
         __syncwarp();
     }
     tc_fence_before();
@@ -717,7 +741,6 @@ constexpr int kMergeWarps = 4;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     kv8_shared_merge_kernel(const __grid_constant__ PreParams p, int row_block, int row8) {
-    constexpr int V = D / 32;
     const AttnParams& a = p.a;
     const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");   // the next kernel may set up
@@ -742,7 +765,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int U = a.Hkv * a.n_rb;
     int c0 = 0, c1 = -1, second = 0, r_own = 0;
     if (n > 0) {
-        const Shares sh(all * U, a.ctas);
+        const Shares sh = own_shares(a, all * U);
         const int first = before * U + (h * a.n_rb + rr / row8) * n;
         c0 = sh.owner(first);
         c1 = sh.owner(first + n - 1);
@@ -770,56 +793,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const bool shares = planned && plan.start(b) > 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // in every thread: this grid ends after those
     if (!real || (!shares && n > 0 && c0 == c1)) return;
-    // results [0, n_own) are over its own positions, the others over the prefix
+    // Results [0, n_own) are over its own positions, the others over the prefix.  Where result k stands,
+    // in rows of its buffer (without branches: the loads of several are to be in flight at once).
     const int n_own = c1 - c0 + 1, n_all = n_own + (d1 - d0 + 1);
-    auto at_own = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? second : 0)) * row8 + r_own; };
-    auto at_pre = [&](int k) {
-        return static_cast<int64_t>(2 * (d0 + k) + (k == 0 ? second_pre : 0)) * row_block + r_pre;
+    const bool own_whole = n_own == 1 && shares, pre_whole = d0 == d1;
+    const float* o_own = own_whole ? a.own_o : a.part_o;
+    const float* o_pre = pre_whole ? p.row_o : p.part_o;
+    const float* l_own = own_whole ? a.own_lse : a.part_lse;
+    const float* l_pre = pre_whole ? p.row_lse : p.part_lse;
+    const int64_t own0 = own_whole ? row : static_cast<int64_t>(2 * c0) * row8 + r_own;
+    const int64_t pre0 = pre_whole ? row : static_cast<int64_t>(2 * d0) * row_block + r_pre;
+    const int own_add = own_whole ? 0 : second * row8, pre_add = pre_whole ? 0 : second_pre * row_block;
+    auto at_of = [&](int k) {
+        const int i = k < n_own ? k : k - n_own;
+        const int step = 2 * (k < n_own ? row8 : row_block), add = i == 0 ? (k < n_own ? own_add : pre_add) : 0;
+        return (k < n_own ? own0 : pre0) + static_cast<int64_t>(i) * step + add;
     };
-    auto lse_of = [&](int k) {
-        if (k < n_own) return n_own == 1 && shares ? a.own_lse[row] : a.part_lse[at_own(k)];
-        return d0 == d1 ? p.row_lse[row] : p.part_lse[at_pre(k - n_own)];
-    };
-    auto o_of = [&](int k) {
-        if (k < n_own) return n_own == 1 && shares ? a.own_o + row * D : a.part_o + at_own(k) * D;
-        return d0 == d1 ? p.row_o + row * D : p.part_o + at_pre(k - n_own) * D;
-    };
-    float M = -INFINITY, sum = 0.0f, acc[V] = {};
+    constexpr int LPR = D / 4, PER = 32 / LPR;   // lanes of a row, four dimensions each; results side by side
+    const int sub = lane / LPR, col = lane % LPR * 4;
+    float M = -INFINITY, sum = 0.0f, acc[4] = {};
     for (int base = 0; base < n_all; base += 32) {
         const int cnt = min(32, n_all - base);
-        const float L = lane < cnt ? lse_of(base + lane) : -INFINITY;
+        const int kl = base + min(lane, cnt - 1);
+        const float x_lse = (kl < n_own ? l_own : l_pre)[at_of(kl)];
+        const float L = lane < cnt ? x_lse : -INFINITY;
         float M1 = fmaxf(M, L);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, d));
         const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - M1);
-        const float w = L == -INFINITY ? 0.0f : ex2_ftz(L - M1);
+        const float w = L == -INFINITY ? 0.0f : ex2_ftz(L - M1);   // (0 for lanes past the last result)
         M = M1;
-        sum *= al;
+        float all_w = w;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] *= al;
+        for (int d = 16; d > 0; d >>= 1) all_w += __shfl_xor_sync(0xffffffffu, all_w, d);
+        sum = sum * al + all_w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] *= al;
 #pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* src = o_of(base + k) + lane * V;
-            float x[V];
-            if constexpr (V == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(src);
-                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(src);
-                x[0] = y.x, x[1] = y.y;
+        for (int k = 0; k < cnt; k += PER) {
+            const float wk = __shfl_sync(0xffffffffu, w, (k + sub) & 31);
+            const int ki = base + min(k + sub, cnt - 1);
+            const float4 y = *reinterpret_cast<const float4*>((ki < n_own ? o_own : o_pre) + at_of(ki) * D + col);
+            if (k + sub < cnt) {
+                acc[0] = fmaf(wk, y.x, acc[0]);
+                acc[1] = fmaf(wk, y.y, acc[1]);
+                acc[2] = fmaf(wk, y.z, acc[2]);
+                acc[3] = fmaf(wk, y.w, acc[3]);
             }
-            sum += wk;
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, x[i], acc[i]);
         }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + row * D + lane * V;
+    if constexpr (PER == 2) {
 #pragma unroll
-    for (int i = 0; i < V; i += 2)
-        *reinterpret_cast<uint32_t*>(out + i) =
-            sum == 0.0f ? 0u : pack2<BF16>(acc[i] * inv, acc[i + 1] * inv);
+        for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (sub == 0)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + col) =
+            sum == 0.0f ? make_uint2(0u, 0u)
+                        : make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
     if (lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (M + lg2_approx(sum)) * 0.6931471805599453f;
 }
 
@@ -985,7 +1016,7 @@ SharedSizes shared_sizes(int B, int Hq, int Hkv, int Nq, int D, int sms) {
     const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
     const size_t all = static_cast<size_t>(B) * Hq * Nq;
     const size_t parts = 2 * static_cast<size_t>(sms) * prefix_tiles(B, rows) * kPreRows;
-    return {part_bytes(rows, D, sms),          pad256(all * D * sizeof(float)), pad256(all * sizeof(float)),
+    return {part_bytes(rows, D, own_workers(sms, static_cast<int>(rows))), pad256(all * D * sizeof(float)), pad256(all * sizeof(float)),
             pad256(all * D * sizeof(float)),   pad256(all * sizeof(float)),
             pad256(parts * D * sizeof(float)), pad256(parts * sizeof(float))};
 }
@@ -1059,11 +1090,14 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     const int qt = prefix_tiles(B, rows), row_block = qt * kPreRows;
     // tiles of all groups, and rows, are counted in 32 bits; B / 2 groups at most
     const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
-    if (rows > 1 << 20 || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + 1) > 0x7fffffffll ||
+    if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + 1) > 0x7fffffffll ||
         (static_cast<int64_t>(B) * Hkv * rows + kMergeWarps - 1) / kMergeWarps > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
     const SharedSizes z = shared_sizes(B, Hq, Hkv, Nq, D, p.a.ctas);
     char* at = static_cast<char*>(workspace) + z.own_part;
+    // (as many parts as there are shares)
+    p.a.part_lse = reinterpret_cast<float*>(at - pad256(2 * static_cast<size_t>(own_workers(p.a.ctas, p.a.rows)) * 8 *
+                                                        row_tiles(rows) * sizeof(float)));
     auto take = [&](size_t bytes) {
         float* r = reinterpret_cast<float*>(at);
         at += bytes;
