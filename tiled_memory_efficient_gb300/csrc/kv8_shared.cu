@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kPreRows = 128;       // rows of a Q tile, keys of a K/V tile
 constexpr int kPreMinShare = 2;     // tiles per CTA, at least
-constexpr float kPreThreshold = 8.0f;   // powers of two the largest score may outgrow its reference by
+constexpr float kPreThreshold = 8.0f;   // powers of two a score may outgrow the reference by
 
 struct PreParams {
     AttnParams a;
@@ -82,17 +82,19 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan,
     x.units = p.Hkv * x.n_rb;
     return x;
 }
-// Tiles of all groups; each warp for itself.
+// Tiles of all groups, and (`before`) of those before one; each warp for itself.  (Cutting every unit into
+// equal pieces, one for a CTA, so that none ends one unit and begins another, measured no better: 16 units of
+// 128 tiles in 144 pieces 50 us, in 152 shares 45 to 55 us.)
 __device__ __forceinline__ int all_tiles(const AttnParams& p, const Plan& plan, int groups, int row_block,
-                                         int before = -1, int* first = nullptr) {
+                                         int before = 0, int* lead = nullptr) {
     const int lane = threadIdx.x & 31;
-    int all = 0, lead = 0;
+    int all = 0, first = 0;
     for (int g = lane; g < groups; g += 32) {
         const int n = group_of(p, plan, g, row_block).tiles();
         all += n;
-        if (g < before) lead += n;
+        if (g < before) first += n;
     }
-    if (first) *first = __reduce_add_sync(0xffffffffu, lead);
+    if (lead) *lead = __reduce_add_sync(0xffffffffu, first);
     return __reduce_add_sync(0xffffffffu, all);
 }
 
@@ -116,7 +118,7 @@ struct Walk {
     __device__ __forceinline__ int head() const { return u / x.n_rb; }
     __device__ __forceinline__ int row0(int row_block) const { return (u - head() * x.n_rb) * row_block; }
 };
-// The share of CTA c that starts at tile g0 and ends at g1 (g0 < g1).
+// The share of a CTA that starts at tile g0 and ends at g1 (g0 < g1).
 __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block, int g0,
                                           int g1) {
     const int lane = threadIdx.x & 31;
@@ -134,10 +136,9 @@ __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan,
         const unsigned past = __ballot_sync(0xffffffffu, carry + sum > g0);
         if (past) {
             const int at = __ffs(past) - 1;
-            const int before = carry + __shfl_sync(0xffffffffu, sum - n, at);
+            const int off = g0 - carry - __shfl_sync(0xffffffffu, sum - n, at);
             w.g = base + at;
             w.x = group_of(p, plan, w.g, row_block);
-            const int off = g0 - before;
             w.u = off / w.x.blocks;
             w.v = off - w.u * w.x.blocks;
             break;
@@ -237,8 +238,8 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
     const Shares sh(T, a.ctas, kPreMinShare);
     const int cta = static_cast<int>(blockIdx.x);
     if (cta >= sh.n) return;   // nothing to wait for
-    const int g0 = sh.begin(cta), g1 = sh.begin(cta + 1);
-    Walk w = walk_from(a, plan, groups, RB, g0, g1);
+    const int g0 = sh.begin(cta), total = sh.begin(cta + 1) - g0;
+    Walk w = walk_from(a, plan, groups, RB, g0, g0 + total);
     auto next = [&](Walk& x) { x.next(a, plan, groups, RB); };
     auto active = [&](const Walk& x, int t) { return x.row0(RB) + t * kPreRows < x.x.rows; };
 
@@ -301,16 +302,18 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                 row_id = (b * a.Hkv + x.head()) * a.rows + rr;
                 src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(row_id) * D);
             }
+            uint4 q[D / 8];   // the whole row at once: one trip to memory
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) q[k] = exists ? src[k] : make_uint4(0u, 0u, 0u, 0u);
             int shift = 0;
             if constexpr (BF16) {
                 uint32_t ex = 0u;   // largest finite exponent field
-#pragma unroll 4
-                for (int k = 0; k < D / 8 && exists; ++k) {
-                    const uint4 v = src[k];
-                    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint32_t y[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t lo = (q[e] >> 7) & 0xffu, hi = (q[e] >> 23) & 0xffu;
+                        const uint32_t lo = (y[e] >> 7) & 0xffu, hi = (y[e] >> 23) & 0xffu;
                         ex = max(ex, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
                     }
                 }
@@ -318,20 +321,18 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
             }
             const float up = exp2i(shift);
             f_row = a.scale_log2 * exp2i(-shift);
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (exists) v = src[k];
                 if constexpr (BF16) {
-                    uint32_t q[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t y[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 y = unpack16<true>(q[e]);
-                        q[e] = pack2<false>(y.x * up, y.y * up);
+                        const float2 v = unpack16<true>(y[e]);
+                        y[e] = pack2<false>(v.x * up, v.y * up);
                     }
-                    v = make_uint4(q[0], q[1], q[2], q[3]);
+                    q[k] = make_uint4(y[0], y[1], y[2], y[3]);
                 }
-                sts128(sQ + (k >> 3) * (kPreRows * 128) + rl * 128 + (((k & 7) ^ (rl & 7)) << 4), v);
+                sts128(sQ + (k >> 3) * (kPreRows * 128) + rl * 128 + (((k & 7) ^ (rl & 7)) << 4), q[k]);
             }
             fence_proxy_async_smem();
             mbar_arrive(&q_full[t]);
@@ -433,30 +434,11 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                     }
                     tmem_wait_st();
                 }
-                // Two passes over S, 32 keys at a time, in loops: the four roles run different code on each SM
-                // sub-partition, and what is unrolled waits for its instructions
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t s0[32], s1[32];
-                    tmem_ld64(tS + c, s0, s1);
-                    tmem_wait_ld();
-                    reg_fence(s0);
-                    reg_fence(s1);
-                    float b0 = mx, b1 = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        b0 = fmax3(b0, __uint_as_float(s0[i]), __uint_as_float(s1[i]));
-                        b1 = fmax3(b1, __uint_as_float(s0[i + 1]), __uint_as_float(s1[i + 1]));
-                    }
-                    mx = fmaxf(b0, b1);
-                }
-                const float m_new = fmaxf(m, mx * f);
-                const bool need = m_new > m + kPreThreshold;
-                const float al = need ? ex2_ftz(m - m_new) : 1.0f;   // from -inf: 0
-                m = need ? m_new : m;
-                const float m_sub = m == -INFINITY ? 0.0f : m;
-                const uint64_t f2s = f2(f, f), nm2 = f2(-m_sub, -m_sub);
+                // One pass over S, 32 keys at a time, in a loop: the four roles run different code on each SM
+                // sub-partition, and what is unrolled waits for its instructions.  The reference m moves,
+                // by whole powers of two, where a score outgrows it by more than 2^kPreThreshold:
+                // the terms of the keys before are then moved by as much, exactly.
+                float al = 1.0f;   // what the sum, and O, are moved by
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -464,6 +446,40 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                     tmem_ld32(tS + c * 32, now);
                     tmem_wait_ld();
                     reg_fence(now);
+                    float y0 = __uint_as_float(now[0]), y1 = __uint_as_float(now[1]);
+                    float y2 = __uint_as_float(now[2]), y3 = __uint_as_float(now[3]);
+#pragma unroll
+                    for (int i = 4; i < 28; i += 8) {
+                        y0 = fmax3(y0, __uint_as_float(now[i]), __uint_as_float(now[i + 1]));
+                        y1 = fmax3(y1, __uint_as_float(now[i + 2]), __uint_as_float(now[i + 3]));
+                        y2 = fmax3(y2, __uint_as_float(now[i + 4]), __uint_as_float(now[i + 5]));
+                        y3 = fmax3(y3, __uint_as_float(now[i + 6]), __uint_as_float(now[i + 7]));
+                    }
+                    y0 = fmax3(y0, __uint_as_float(now[28]), __uint_as_float(now[29]));
+                    y1 = fmax3(y1, __uint_as_float(now[30]), __uint_as_float(now[31]));
+                    const float m_new = ceilf(fmaxf(m, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)) * f));
+                    const bool need = m_new > m + kPreThreshold;
+                    if (__any_sync(0xffffffffu, need)) {
+                        // (from -inf: every term so far is 0)
+                        const int d = need ? static_cast<int>(fmaxf(m - m_new, -1000.0f)) : 0;
+                        const float by = need ? ex2_ftz(m - m_new) : 1.0f;
+                        al *= by;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i] = fmul2(acc[i], f2(by, by));
+                        m = need ? m_new : m;
+                        const uint32_t by16 = pow2_f16x2(d);
+                        tmem_wait_st();
+                        for (int e = 0; e < c; ++e) {
+                            tmem_ld16(tS + e * 16, pk);
+                            tmem_wait_ld();
+                            reg_fence(pk);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(pk[i]) : "r"(by16));
+                            tmem_st16(tS + e * 16, pk);
+                        }
+                    }
+                    const float m_sub = m == -INFINITY ? 0.0f : m;
+                    const uint64_t f2s = f2(f, f), nm2 = f2(-m_sub, -m_sub);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2)
                         pk[i >> 1] = softmax_pair<false>(now[i], now[i + 1], f2s, nm2, acc[(i >> 1) & 3]);
@@ -475,7 +491,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                 const int up = j > 0 ? ev_now - ev : 0;   // the value scale grew by 2^up
                 ev = ev_now;
                 if (!last_pv()) break;
-                if (j > 0 && __any_sync(0xffffffffu, need || up > 0)) {
+                if (j > 0 && __any_sync(0xffffffffu, al != 1.0f || up > 0)) {
                     tc_fence_after();
                     const float o_al = al * exp2i(-min(up, 126));
 #pragma unroll 1
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
             if (!ok) break;
             // where this part's rows go
             whole = w.v == 0 && n == w.x.blocks;
-            part = 2 * cta + (w.left == g1 - g0 ? 0 : 1);
+            part = 2 * cta + (w.left == total ? 0 : 1);
             pending = true;
             next(w);
         }
@@ -504,7 +520,6 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         // ------------------------------------------------------------ converters
         const int ct = threadIdx.x - C::kConvWarp * 32;
         constexpr int KB = D / 64;                // column blocks of an fp16 tile
-        const int total = g1 - g0;
         // 8 lanes hold chunks 0 .. 3 of a column block in two neighbouring rows (D = 128: of block a in the even
         // row and of the other one in the odd row, a in turn), so that both their loads and their stores,
         // units 2 j and 2 j + 1 of the row's swizzled 128 bytes, meet every bank once.
@@ -662,7 +677,6 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         };
         Page now = fetch(), soon = fetch();
         scales(now);
-        const int total = g1 - g0;
         int issued = 0;   // raw tiles, K and V in turn
         int ev = -1000;   // value scale of the accumulator: none yet
         for (int x = 0; x < total; ++x) {
@@ -793,58 +807,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const bool shares = planned && plan.start(b) > 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // in every thread: this grid ends after those
     if (!real || (!shares && n > 0 && c0 == c1)) return;
-    // Results [0, n_own) are over its own positions, the others over the prefix.  Where result k stands,
-    // in rows of its buffer (without branches: the loads of several are to be in flight at once).
-    const int n_own = c1 - c0 + 1, n_all = n_own + (d1 - d0 + 1);
-    const bool own_whole = n_own == 1 && shares, pre_whole = d0 == d1;
-    const float* o_own = own_whole ? a.own_o : a.part_o;
-    const float* o_pre = pre_whole ? p.row_o : p.part_o;
-    const float* l_own = own_whole ? a.own_lse : a.part_lse;
-    const float* l_pre = pre_whole ? p.row_lse : p.part_lse;
-    const int64_t own0 = own_whole ? row : static_cast<int64_t>(2 * c0) * row8 + r_own;
-    const int64_t pre0 = pre_whole ? row : static_cast<int64_t>(2 * d0) * row_block + r_pre;
-    const int own_add = own_whole ? 0 : second * row8, pre_add = pre_whole ? 0 : second_pre * row_block;
-    auto at_of = [&](int k) {
-        const int i = k < n_own ? k : k - n_own;
-        const int step = 2 * (k < n_own ? row8 : row_block), add = i == 0 ? (k < n_own ? own_add : pre_add) : 0;
-        return (k < n_own ? own0 : pre0) + static_cast<int64_t>(i) * step + add;
-    };
+    // Two runs of results, over its own positions and over the prefix: each `n` rows of a buffer, `step`
+    // apart, the first one `add` further on.  Eight of a run are in flight at once, and the code is kept
+    // small: it runs once, and a warp waits longer for instructions than for their data.
+    const bool own_whole = c0 == c1 && shares, pre_whole = d0 == d1;
     constexpr int LPR = D / 4, PER = 32 / LPR;   // lanes of a row, four dimensions each; results side by side
     const int sub = lane / LPR, col = lane % LPR * 4;
     float M = -INFINITY, sum = 0.0f, acc[4] = {};
-    for (int base = 0; base < n_all; base += 32) {
-        const int cnt = min(32, n_all - base);
-        const int kl = base + min(lane, cnt - 1);
-        const float x_lse = (kl < n_own ? l_own : l_pre)[at_of(kl)];
-        const float L = lane < cnt ? x_lse : -INFINITY;
-        float M1 = fmaxf(M, L);
+#pragma unroll 1
+    for (int run = 0; run < 2; ++run) {
+        const bool own = run == 0, whole = own ? own_whole : pre_whole;
+        const int n_run = own ? c1 - c0 + 1 : d1 - d0 + 1, step = 2 * (own ? row8 : row_block);
+        const int add = whole ? 0 : own ? second * row8 : second_pre * row_block;
+        const int64_t at = whole ? row : own ? static_cast<int64_t>(c0) * step + r_own : static_cast<int64_t>(d0) * step + r_pre;
+        const float* l = (own ? (whole ? a.own_lse : a.part_lse) : (whole ? p.row_lse : p.part_lse)) + at;
+        const float* o = (own ? (whole ? a.own_o : a.part_o) : (whole ? p.row_o : p.part_o)) + at * D + col;
+#pragma unroll 1
+        for (int k = sub; k < n_run; k += 8 * PER) {
+            float L[8], top = M;
+            float4 y[8];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, d));
-        const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - M1);
-        const float w = L == -INFINITY ? 0.0f : ex2_ftz(L - M1);   // (0 for lanes past the last result)
-        M = M1;
-        float all_w = w;
+            for (int u = 0; u < 8; ++u) {
+                const int i = k + u * PER, off = i * step + (i == 0 ? add : 0);
+                L[u] = -INFINITY;
+                y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < n_run) {
+                    L[u] = l[off];
+                    y[u] = *reinterpret_cast<const float4*>(o + static_cast<int64_t>(off) * D);
+                }
+            }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) all_w += __shfl_xor_sync(0xffffffffu, all_w, d);
-        sum = sum * al + all_w;
+            for (int u = 0; u < 8; ++u) top = fmaxf(top, L[u]);
+            const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - top);
+            M = top;
+            sum *= al;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= al;
-#pragma unroll 8
-        for (int k = 0; k < cnt; k += PER) {
-            const float wk = __shfl_sync(0xffffffffu, w, (k + sub) & 31);
-            const int ki = base + min(k + sub, cnt - 1);
-            const float4 y = *reinterpret_cast<const float4*>((ki < n_own ? o_own : o_pre) + at_of(ki) * D + col);
-            if (k + sub < cnt) {
-                acc[0] = fmaf(wk, y.x, acc[0]);
-                acc[1] = fmaf(wk, y.y, acc[1]);
-                acc[2] = fmaf(wk, y.z, acc[2]);
-                acc[3] = fmaf(wk, y.w, acc[3]);
+            for (int i = 0; i < 4; ++i) acc[i] *= al;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float w = L[u] == -INFINITY ? 0.0f : ex2_ftz(L[u] - M);
+                sum += w;
+                acc[0] = fmaf(w, y[u].x, acc[0]);
+                acc[1] = fmaf(w, y[u].y, acc[1]);
+                acc[2] = fmaf(w, y[u].z, acc[2]);
+                acc[3] = fmaf(w, y[u].w, acc[3]);
             }
         }
     }
-    if constexpr (PER == 2) {
+    if constexpr (PER == 2) {   // the two halves' sums
+        const float other = __shfl_xor_sync(0xffffffffu, M, 16), top = fmaxf(M, other);
+        const float al = M == -INFINITY ? 0.0f : ex2_ftz(M - top);
+        M = top;
+        sum *= al;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+        for (int i = 0; i < 4; ++i) {
+            acc[i] *= al;
+            acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (sub == 0)
