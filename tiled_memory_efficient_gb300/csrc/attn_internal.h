@@ -40,14 +40,13 @@ struct SmemLimit {
 // the grid may start before that kernel has ended, and waits for it on the
 // device (griddepcontrol.wait) where it needs its results.
 template <typename Kern, typename... Args>
-inline cudaError_t launch_dependent(Kern kern, long long ctas, int threads, int smem,
-                             cudaStream_t stream, Args... args) {
+inline cudaError_t launch_dependent(Kern kern, dim3 grid, dim3 block, int smem, cudaStream_t stream, Args... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;

@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/rope.h"
 #include "attn_internal.h"
@@ -16,6 +17,15 @@ namespace {
 
 // ------------------------------------------------------------------ queries and keys
 
+// New tokens of sequence b of that length (T at most, the table holds `most` positions): -1 for a
+// count that does not fit, 0 without room.
+__device__ __forceinline__ int tokens_of(const int* granted, const int* n_new, int b, int T, int len, int most) {
+    if (granted && *granted == 0) return 0;
+    const int n = n_new ? n_new[b] : T;
+    if (n == 0) return 0;
+    return n < 0 || n > T || n > len || len > most ? -1 : n;
+}
+
 struct RopeParams {
     RopeView f;
     const uint16_t* x[2];   // q, k
@@ -24,21 +34,36 @@ struct RopeParams {
     const int* pos;
     int64_t pos_b, pos_n;
     int start, B, N, Hq, heads;
-    int item_shift, chunk;        // 16-dimension items of a row; heads a thread takes
-    int total;                    // threads of a block row that have work
+    // positions of a cache's newest tokens instead (lens null: none)
+    const int* lens;
+    const int* n_new;
+    const int* granted;
+    int most;                     // positions that the table holds
+    int tok_shift;                // tokens of a CTA
+    int per_thread;               // heads a thread takes, kRopeBatch at most
 };
 
-constexpr int kRopeThreads = 256;
+// CTAs of two warps, each for itself at its barrier: rows of 2 x 8192 tokens with 32 heads of 128 take
+// 43 us a pass with 64 threads, 44 with 128 and 47 with 256.
+constexpr int kRopeThreads = 64;
 
-// A thread takes 16 dimensions of one token and `chunk` heads, so that one set of
-// sines serves them all; neighbouring threads take neighbouring items of a token.
-template <bool BF16, int MODE>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    const int id = static_cast<int>(blockIdx.x) * kRopeThreads + static_cast<int>(threadIdx.x);
-    if (id >= p.total) return;
-    const int items = 1 << p.item_shift, item = id & (items - 1), tok = id >> p.item_shift;
-    const int b = tok / p.N, n = tok - b * p.N;
-    const int h0 = static_cast<int>(blockIdx.y) * p.chunk;
+// Bound by memory: every value is read and written once.  A CTA takes a few tokens and a range of heads;
+// a thread 16 dimensions (an item) of one token and up to four of the heads, all of which it asks for
+// before the CTA makes its sines, each once.  (Each thread making the sines of its own item for all
+// heads that it takes: 16384 tokens of 16 heads of 64 in 15.5 us against 13.2, 64 tokens of 40 heads
+// of 128 in 3.6 against 2.6.)  2 x 8192 tokens, 32 heads of 128: 268 MB in 43 us, 6.2 TB/s.
+template <int D, bool BF16, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int items = D / 16, kItemShift = D == 128 ? 3 : 2;
+    __shared__ __align__(16) float s_cos[kRopeThreads * 8], s_sin[kRopeThreads * 8];   // [token][place of pair]
+    const int item = static_cast<int>(threadIdx.x) & (items - 1);
+    const int tl = (static_cast<int>(threadIdx.x) >> kItemShift) & ((1 << p.tok_shift) - 1);
+    const int hg = static_cast<int>(threadIdx.x) >> (kItemShift + p.tok_shift);   // the thread's first head
+    const int step = kRopeThreads >> (kItemShift + p.tok_shift);
+    const int tok = (static_cast<int>(blockIdx.x) << p.tok_shift) + tl;
+    const bool inside = tok < p.B * p.N;
+    const int b = inside ? tok / p.N : 0, n = inside ? tok - b * p.N : 0;
+    const int first = static_cast<int>(blockIdx.y) * p.per_thread * step;
     RopeRows t;
     t.x0 = p.x[0] + b * p.xs[0][0] + n * p.xs[0][2];
     t.x1 = p.x[1] + b * p.xs[1][0] + n * p.xs[1][2];
@@ -46,23 +71,91 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     t.y1 = p.y[1] + b * p.ys[1][0] + n * p.ys[1][2];
     t.xh0 = p.xs[0][1], t.xh1 = p.xs[1][1], t.yh0 = p.ys[0][1], t.yh1 = p.ys[1][1];
     t.first = p.Hq;
-    const int pos = p.pos ? p.pos[b * p.pos_b + n * p.pos_n] : p.start + n;
-    rope_item<BF16, MODE>(p.f, t, item, items, pos, h0, min(h0 + p.chunk, p.heads), true);
-}
-
-template <bool BF16>
-cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-    const dim3 grid((p.total + kRopeThreads - 1) / kRopeThreads, (p.heads + p.chunk - 1) / p.chunk);
-    const dim3 block(kRopeThreads);
-    switch (p.f.mode) {
-        case kRopeHalf: return launch_kernel(rope_kernel<BF16, kRopeHalf>, grid, block, 0, stream, p);
-        case kRopeInter: return launch_kernel(rope_kernel<BF16, kRopeInter>, grid, block, 0, stream, p);
-        default: return launch_kernel(rope_kernel<BF16, kRopeScalar>, grid, block, 0, stream, p);
+    int pos;
+    bool live = true;
+    if (p.lens) {
+        const int len = p.lens[b], fresh = tokens_of(p.granted, p.n_new, b, p.N, len, p.most);
+        live = n < fresh;
+        pos = len - fresh + n;
+    } else {
+        pos = p.pos ? p.pos[b * p.pos_b + n * p.pos_n] : p.start + n;
     }
+    // Pairs in eights, an item's, whose first fours come before all second fours: a token's items
+    // read whole lines.
+    auto place = [&](int pair) { return tl * (D / 2) + ((pair >> 2) & 1) * (D / 4) + (pair >> 3) * 4 + (pair & 3); };
+    auto sines = [&](float (&c)[8], float (&s)[8]) {
+        for (int pair = hg * items + item; 2 * pair < p.f.rot; pair += step * items) {
+            const float2 cs = rope_cs(p.f.turns, pair, pos, p.f.amp);
+            s_cos[place(pair)] = cs.x;
+            s_sin[place(pair)] = cs.y * p.f.sign;
+        }
+        __syncthreads();
+        if constexpr (MODE == kRopeScalar) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {   // (places past the last pair: read, not used)
+                const int at = place(item_pair<MODE>(item, items, j));
+                c[j] = s_cos[at];
+                s[j] = s_sin[at];
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const float4 cc = *reinterpret_cast<const float4*>(s_cos + place(8 * item + 4 * g));
+                const float4 ss = *reinterpret_cast<const float4*>(s_sin + place(8 * item + 4 * g));
+                c[4 * g] = cc.x, c[4 * g + 1] = cc.y, c[4 * g + 2] = cc.z, c[4 * g + 3] = cc.w;
+                s[4 * g] = ss.x, s[4 * g + 1] = ss.y, s[4 * g + 2] = ss.z, s[4 * g + 3] = ss.w;
+            }
+        }
+    };
+    const int end = inside ? min(first + p.per_thread * step, p.heads) : 0;
+    rope_item<BF16, MODE>(p.f, t, item, items, first + hg, step, end, live, sines);
+    // behind an append's prompts: it started before they were done, and ends only after them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Heads a thread takes of `heads`, given the threads that one head needs: as many as leave
-// the device its threads, at least two.
+// Tokens and heads of a CTA: heads a thread as many as leave every SM two CTAs; tokens so that the heads
+// fill the CTAs and the sines are few (a sine costs about as much as two thirds of an item).
+struct RopeSplit {
+    int tok_shift, per_thread;
+    int64_t x, y;
+};
+RopeSplit split_rope(int64_t tokens, int heads, int D, int rot) {
+    const int item_shift = D == 128 ? 3 : 2;
+    RopeSplit best{};
+    for (int k = kRopeBatch; k >= 1; k >>= 1) {
+        double least = 0.0;
+        for (int ts = 0; kRopeThreads >> (item_shift + ts); ++ts) {
+            const int per = (kRopeThreads >> (item_shift + ts)) * k;   // heads of a CTA
+            const int64_t x = (tokens + (int64_t(1) << ts) - 1) >> ts, y = (heads + per - 1) / per;
+            const int sines = ((rot / 2 << ts) + kRopeThreads - 1) / kRopeThreads;   // a thread
+            const double cost = static_cast<double>(x) * static_cast<double>(y) * (3 * k + 2 * sines);
+            if (least > 0.0 && cost >= least) continue;
+            least = cost;
+            best = {ts, k, x, y};
+        }
+        if (best.x * best.y >= 2 * device_sms()) break;
+    }
+    return best;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_rope(RopeParams p, cudaStream_t stream) {
+    const RopeSplit s = split_rope(static_cast<int64_t>(p.B) * p.N, p.heads, D, p.f.rot);
+    p.tok_shift = s.tok_shift;
+    p.per_thread = s.per_thread;
+    const dim3 grid(static_cast<unsigned>(s.x), static_cast<unsigned>(s.y)), block(kRopeThreads);
+    void (*kern)(RopeParams) = p.f.mode == kRopeHalf    ? rope_kernel<D, BF16, kRopeHalf>
+                               : p.f.mode == kRopeInter ? rope_kernel<D, BF16, kRopeInter>
+                                                        : rope_kernel<D, BF16, kRopeScalar>;
+    return p.lens ? launch_dependent(kern, grid, block, 0, stream, p) : launch_kernel(kern, grid, block, 0, stream, p);
+}
+cudaError_t launch_rope(const RopeParams& p, int D, bool bf16, cudaStream_t stream) {
+    if (D == 128) return bf16 ? launch_rope<128, true>(p, stream) : launch_rope<128, false>(p, stream);
+    return bf16 ? launch_rope<64, true>(p, stream) : launch_rope<64, false>(p, stream);
+}
+
+// Heads a thread of a step's queries takes of `heads`, given the threads that one head needs: as many as
+// leave the device its threads, at least two.
 int heads_per_thread(int64_t threads, int heads) {
     const int64_t want = static_cast<int64_t>(device_sms() > 0 ? device_sms() : 1) * 1024;
     int64_t parts = (want + threads - 1) / threads;
@@ -107,52 +200,319 @@ struct AppendRopeParams {
     const int* granted;
     unsigned int* status;
     int64_t sb, sh, st, qb, qh, qt, ob, oh, ot;
-    int B, Hq, Hkv, T, n_pages, max_pages, n_slots;
-    int page_ctas;    // CTAs of pages; the others turn queries
+    int B, Hq, Hkv, T, n_pages, max_pages, n_slots, page_shift;
+    int heads;        // of a page that a CTA takes in turn (prompts)
+    int page_ctas;    // CTAs of pages; the others turn queries (steps)
     int q_threads;    // threads that one head's queries need
     int q_chunk;      // heads a thread of those takes
 };
 
-// New tokens of sequence b (-1: a count that does not fit; 0 without room).
-template <int PAGE>
-__device__ __forceinline__ int tokens_of(const AppendRopeParams& p, int b, int len) {
-    if (p.granted && *p.granted == 0) return 0;
-    const int n = p.n_new ? p.n_new[b] : p.T;
-    if (n == 0) return 0;
-    return n < 0 || n > p.T || n > len || (len - 1) / PAGE >= p.max_pages ? -1 : n;
-}
-
-template <int D, int PAGE>
-struct AppendRopeCfg {
-    static constexpr int kThreads = PAGE * D / 8 < 256 ? PAGE * D / 8 : 256;
-    static constexpr int NV = PAGE * D / 8 / kThreads;   // 16-byte vectors a thread holds
-    static constexpr int VPT = D / 8;                    // vectors per token
-    static constexpr int STEP = kThreads / VPT;          // tokens between a thread's vectors
+// The tokens that slot `slot` of sequence b's new ones has on its page.
+struct PageTokens {
+    int n, start, t0, lo, hi, pid;   // new tokens; position of the first; of the page's first; new ones on it
+    int64_t head;                    // (page, head) of head 0
+    __device__ __forceinline__ bool find(const AppendRopeParams& p, int b, int slot, bool report) {
+        const int len = p.lens[b];
+        n = tokens_of(p.granted, p.n_new, b, p.T, len, p.max_pages << p.page_shift);
+        if (n <= 0) {
+            if (n < 0 && report) atomicOr(p.status, kStatusPage);
+            return false;
+        }
+        start = len - n;
+        const int col = (start >> p.page_shift) + slot;
+        t0 = col << p.page_shift;
+        if (t0 >= len) return false;
+        lo = max(start, t0);
+        hi = min(len, t0 + (1 << p.page_shift));
+        pid = p.table[static_cast<int64_t>(b) * p.max_pages + col];
+        if (pid < 0 || pid >= p.n_pages) {
+            if (report) atomicOr(p.status, kStatusPage);
+            return false;
+        }
+        head = static_cast<int64_t>(pid) * p.Hkv;
+        return true;
+    }
 };
 
-// One CTA per (sequence, page it may touch, KV head, keys or values) as in the plain
-// append: the page's new tokens in registers (fp32, since turned keys are rounded
-// once), their largest magnitude gives the scale, then the e4m3 bytes.  A thread's vectors are
-// STEP tokens apart: it makes the sines of its first one and of STEP positions, and turns from
-// one to the next by these (4 multiply-adds a pair; at most 7 steps, each off by 2^-23).  A pair's other
-// half comes from another lane of the token.
-template <int D, int PAGE, bool BF16>
-__global__ void __launch_bounds__(AppendRopeCfg<D, PAGE>::kThreads)
-    kv8_append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
-    using C = AppendRopeCfg<D, PAGE>;
-    constexpr int NV = C::NV, VPT = C::VPT, STEP = C::STEP;
+// The other half of each of a vector's pairs: dimensions d0 .. d0 + 7 of the row at `row` hold x (words w), and
+// neighbouring lanes the row's other vectors (every lane of the warp takes part).
+template <bool BF16>
+__device__ __forceinline__ void other_halves(const RopeView& f, const uint4& w, const float (&x)[8], int d0,
+                                             const uint16_t* row, bool fresh, float (&o)[8]) {
+    const int half = f.rot >> 1;
+    if (f.mode == kRopeHalf) {
+        const int away = d0 < f.rot ? (d0 < half ? half / 8 : -(half / 8)) : 0;
+        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 e = rope_unpack<BF16>(__shfl_sync(0xffffffffu, y[j], (threadIdx.x + away) & 31));
+            o[2 * j] = e.x;
+            o[2 * j + 1] = e.y;
+        }
+    } else if (f.mode == kRopeInter) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = x[j ^ 1];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int d = d0 + j;
+            o[j] = fresh && d < f.rot ? rope_load<BF16>(row + (d < half ? d + half : d - half)) : 0.0f;
+        }
+    }
+}
+// Pair of dimension d, and whether it is the pair's first half.
+__device__ __forceinline__ int pair_of(const RopeView& f, int d) {
+    return f.mode == kRopeInter ? d >> 1 : d < f.rot >> 1 ? d : d - (f.rot >> 1);
+}
+__device__ __forceinline__ bool first_of(const RopeView& f, int d) {
+    return f.mode == kRopeInter ? !(d & 1) : d < f.rot >> 1;
+}
+__device__ __forceinline__ float finite_max(float top, const float (&y)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fabsf(y[j]);
+        top = fmaxf(top, a < INFINITY ? a : 0.0f);   // false for a NaN, too
+    }
+    return top;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&y)[8]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 e = rope_unpack<BF16>(x[j]);
+        y[2 * j] = e.x;
+        y[2 * j + 1] = e.y;
+    }
+}
+__device__ __forceinline__ uint2 quantise8(const float (&y)[8], float inv) {
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = f32_to_e4m3x2(y[2 * j] * inv, y[2 * j + 1] * inv);
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+
+// Prompts: one CTA per (sequence, page it may touch, keys or values), `heads` KV heads in turn.  A thread
+// holds two rows' items (rope_item's, the two halves of each pair in one thread), and asks for the next
+// head's before this one's scale is known.  The page's sines are made once for all of the CTA's heads:
+// each pair's exactly at every eighth token, the others by turning those by one token up to four times (off
+// by less than 2^-21; all made exactly, a prompt's append took 42 us instead of 20 with the layout it had).
+template <int D>
+constexpr int prompt_threads(int page) { return page * (D / 32); }
+// CTAs of an SM up to which a page's heads are cut: 4 and 8 give 66.3 us, 12 67.0, 24 71.7 (the sines are made
+// once a CTA) for 2 x 8190 tokens, 8 KV heads, 32 query heads, D = 128.
+constexpr int kPromptCtas = 4;
+constexpr int kPromptThreads = 512;   // at most: pages of 128 tokens, D = 128
+
+// Largest finite magnitude of a thread's values: an infinity sends it to the slow look.
+__device__ __forceinline__ float item_max(const float (&y)[2][16]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(y[i][j]));   // (a NaN is passed over)
+    if (top < INFINITY) return top;
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(y[i][j]) < INFINITY ? fabsf(y[i][j]) : 0.0f);
+    return top;
+}
+
+template <int D, bool BF16, int MODE>
+__global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+    constexpr int items = D / 16;
+    extern __shared__ __align__(16) float s_cos[];   // [token][pitch] of the page, then the sines
+    __shared__ uint32_t s_max[2][kPromptThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;");   // what is behind may set up meanwhile
+    int id = static_cast<int>(blockIdx.x);
+    const int which = id & 1;
+    id >>= 1;
+    const int parts = (p.Hkv + p.heads - 1) / p.heads, part = id % parts;
+    id /= parts;
+    const int b = id / p.n_slots;
+    PageTokens t;
+    if (!t.find(p, b, id - b * p.n_slots, threadIdx.x == 0)) return;
+    const int h0 = part * p.heads, h1 = min(h0 + p.heads, p.Hkv);
+    const int page = 1 << p.page_shift, step = page >> 1;   // the thread's rows: tok and tok + step
+    const int tok = static_cast<int>(threadIdx.x) / items, item = static_cast<int>(threadIdx.x) % items;
+    const int half = p.f.rot >> 1;
+    const bool keys = which == 0;
+    // whether the item turns, and its two vectors (MODE 2: of the values)
+    const bool turns = keys && (MODE == kRopeScalar ? item < half : 8 * item < half);
+    const bool whole = MODE != kRopeHalf || 8 * item < half;
+    const int d0 = MODE != kRopeHalf ? 16 * item : whole ? 8 * item : p.f.rot + 16 * (item - (p.f.rot >> 4));
+    const int d1 = MODE != kRopeHalf || !whole ? d0 + 8 : d0 + half;
+    auto pair_of = [&](int j) { return MODE == kRopeScalar ? item + j * items : 8 * item + j; };
+    // MODE 2, keys: a pair's dimensions (two that stay past the turned ones)
+    auto first = [&](int j) { const int i = pair_of(j); return i < half ? i : 2 * i; };
+    auto second = [&](int j) { const int i = pair_of(j); return i < half ? i + half : 2 * i + 1; };
+    const uint16_t* src = p.src[which] + b * p.sb + (t.t0 + tok - t.start) * p.st;
+    bool fresh[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) fresh[i] = t.t0 + tok + i * step >= t.lo && t.t0 + tok + i * step < t.hi;
+    uint4 next[2][2];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            next[i][0] = next[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (!fresh[i]) continue;
+            const uint16_t* row = src + h * p.sh + i * step * p.st;
+            if (MODE == kRopeScalar && keys) {
+                uint32_t w[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[0][j] = row[first(2 * j)] | static_cast<uint32_t>(row[first(2 * j + 1)]) << 16;
+                    w[1][j] = row[second(2 * j)] | static_cast<uint32_t>(row[second(2 * j + 1)]) << 16;
+                }
+                next[i][0] = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+                next[i][1] = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+            } else {
+                next[i][0] = __ldcs(reinterpret_cast<const uint4*>(row + d0));
+                next[i][1] = __ldcs(reinterpret_cast<const uint4*>(row + d1));
+            }
+        }
+    };
+    load(h0);
+    // Pairs of a token's row of sines: in eights (an item's), whose first fours come before all second
+    // fours, so that a token's items read whole lines; past the last pair a turn by nothing.
+    const int pitch = (half + 7) & ~7;
+    auto place = [&](int pair) { return ((pair >> 2) & 1) * (pitch >> 1) + (pair >> 3) * 4 + (pair & 3); };
+    float* s_sin = s_cos + (pitch << p.page_shift);
+    if (keys) {
+        for (int i = threadIdx.x; i < pitch * (page / 8); i += blockDim.x) {
+            const int run = i / pitch, pair = i - run * pitch;
+            float2 mid = make_float2(1.0f, 0.0f), one = mid;
+            if (pair < half) {
+                mid = rope_cs(p.f.turns, pair, t.t0 + run * 8 + 4, p.f.amp);
+                one = rope_cs(p.f.turns, pair, 1, 1.0f);
+            }
+            const int at = run * 8 * pitch + place(pair);
+            float2 up = mid, down = mid;
+            s_cos[at + 4 * pitch] = mid.x;
+            s_sin[at + 4 * pitch] = mid.y;
+#pragma unroll
+            for (int k = 1; k <= 4; ++k) {
+                down = make_float2(down.x * one.x + down.y * one.y, down.y * one.x - down.x * one.y);
+                s_cos[at + (4 - k) * pitch] = down.x;
+                s_sin[at + (4 - k) * pitch] = down.y;
+                if (k == 4) break;
+                up = make_float2(up.x * one.x - up.y * one.y, up.y * one.x + up.x * one.y);
+                s_cos[at + (4 + k) * pitch] = up.x;
+                s_sin[at + (4 + k) * pitch] = up.y;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+        float y[2][16];   // the items' first vectors, then their second ones
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w[8] = {next[i][0].x, next[i][0].y, next[i][0].z, next[i][0].w,
+                                   next[i][1].x, next[i][1].y, next[i][1].z, next[i][1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 e = rope_unpack<BF16>(w[j]);
+                y[i][2 * j] = e.x;
+                y[i][2 * j + 1] = e.y;
+            }
+        }
+        if (h + 1 < h1) load(h + 1);
+        if (turns) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = (tok + i * step) * pitch;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float c[4], s[4];
+                    if constexpr (MODE == kRopeScalar) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = row + place(min(pair_of(4 * g + j), half - 1));
+                            c[j] = s_cos[at];
+                            s[j] = s_sin[at];
+                        }
+                    } else {
+                        const float4 cc = *reinterpret_cast<const float4*>(s_cos + row + g * (pitch >> 1) + 4 * item);
+                        const float4 ss = *reinterpret_cast<const float4*>(s_sin + row + g * (pitch >> 1) + 4 * item);
+                        c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+                        s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float& a = MODE == kRopeInter ? y[i][8 * g + 2 * j] : y[i][4 * g + j];
+                        float& e = MODE == kRopeInter ? y[i][8 * g + 2 * j + 1] : y[i][8 + 4 * g + j];
+                        if (MODE != kRopeHalf && pair_of(4 * g + j) >= half) continue;   // (0 * inf is none)
+                        const float x = a;
+                        a = x * c[j] - e * s[j];
+                        e = e * c[j] + x * s[j];
+                    }
+                }
+            }
+        }
+        uint8_t* dst = p.pages[which] + (((t.head + h) << p.page_shift) + tok) * D;
+        float* scale = p.scales[which] + t.head + h;
+        const float s_old = t.t0 < t.start ? *scale : 0.0f;
+        // largest finite magnitude: positive floats order like their bits
+        uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(item_max(y)));
+        if ((threadIdx.x & 31) == 0) s_max[h & 1][threadIdx.x >> 5] = u;
+        __syncthreads();   // also: every thread has read the old scale
+        for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) u = max(u, s_max[h & 1][i]);
+        int e = amax_exp(__uint_as_float(u));
+        const int e_old = t.t0 < t.start ? scale_exp(s_old) : e;
+        e = max(e, e_old);
+        if (threadIdx.x == 0) *scale = exp2i(e);
+        const float inv = exp2i(-e);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!fresh[i]) continue;
+            uint32_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = f32_to_e4m3x2(y[i][2 * j] * inv, y[i][2 * j + 1] * inv);
+            uint8_t* row = dst + i * step * D;
+            if (MODE == kRopeScalar && keys) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    row[first(j)] = static_cast<uint8_t>(r[j >> 1] >> (8 * (j & 1)));
+                    row[second(j)] = static_cast<uint8_t>(r[4 + (j >> 1)] >> (8 * (j & 1)));
+                }
+            } else {
+                *reinterpret_cast<uint2*>(row + d0) = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+                *reinterpret_cast<uint2*>(row + d1) = make_uint2(r[4] | (r[5] << 16), r[6] | (r[7] << 16));
+            }
+        }
+        if (e != e_old)   // (each vector of an old token is one thread's, whoever's its new values are)
+            for (int i = 0; i < 2; ++i) {
+                const int pos = t.t0 + tok + i * step;
+                raise_tokens<0, 1>(dst + i * step * D + 16 * item, pos, min(t.lo, pos + 1), e_old, e);
+                raise_tokens<0, 1>(dst + i * step * D + 16 * item + 8, pos, min(t.lo, pos + 1), e_old, e);
+            }
+    }
+}
+
+// Steps of a few tokens: one warp per (sequence, page, KV head, keys or values), whose new tokens it
+// holds whole; the CTAs behind those turn the queries.  A step is bound by its launch and two trips to memory.
+constexpr int kStepThreads = 128;
+template <int D>
+constexpr int step_tokens() { return 4 * (32 / (D / 8)); }   // tokens a warp holds: four turns of it
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kStepThreads) kv8_step_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+    constexpr int VPT = D / 8, TPI = 32 / VPT, items = D / 16;
     asm volatile("griddepcontrol.launch_dependents;");   // the attention may set up meanwhile
     if (static_cast<int>(blockIdx.x) >= p.page_ctas) {
         // queries
-        constexpr int items = D / 16;
-        const int64_t id = static_cast<int64_t>(blockIdx.x - p.page_ctas) * C::kThreads + threadIdx.x;
+        const int64_t id = static_cast<int64_t>(blockIdx.x - p.page_ctas) * kStepThreads + threadIdx.x;
         const int part = static_cast<int>(id / p.q_threads);
         if (part * p.q_chunk >= p.Hq) return;
         const int item = static_cast<int>(id) & (items - 1);   // (q_threads is a multiple of items)
         const int tok = static_cast<int>(id - static_cast<int64_t>(part) * p.q_threads) / items;
         const int h0 = part * p.q_chunk, h1 = min(h0 + p.q_chunk, p.Hq);
         const int b = tok / p.T, t = tok - b * p.T;
-        const int len = p.lens[b], n = tokens_of<PAGE>(p, b, len);
+        const int len = p.lens[b];
+        const int n = tokens_of(p.granted, p.n_new, b, p.T, len, p.max_pages << p.page_shift);
         RopeRows r;
         r.x0 = r.x1 = p.q + b * p.qb + t * p.qt;
         r.y0 = r.y1 = p.q_out + b * p.ob + t * p.ot;
@@ -160,183 +520,112 @@ __global__ void __launch_bounds__(AppendRopeCfg<D, PAGE>::kThreads)
         r.yh0 = r.yh1 = p.oh;
         r.first = p.Hq;
         const bool live = t < n;
-        if (p.f.mode == kRopeHalf) rope_item<BF16, kRopeHalf>(p.f, r, item, items, len - n + t, h0, h1, live);
-        else if (p.f.mode == kRopeInter) rope_item<BF16, kRopeInter>(p.f, r, item, items, len - n + t, h0, h1, live);
-        else rope_item<BF16, kRopeScalar>(p.f, r, item, items, len - n + t, h0, h1, live);
+        const int pos = len - n + t;
+        auto turn = [&](auto mode) {
+            constexpr int MODE = decltype(mode)::value;
+            rope_item<BF16, MODE>(p.f, r, item, items, h0, 1, h1, live, [&](float (&c)[8], float (&s)[8]) {
+                if (live) item_sines<MODE>(p.f, item, items, pos, c, s);
+            });
+        };
+        if (p.f.mode == kRopeHalf) turn(std::integral_constant<int, kRopeHalf>());
+        else if (p.f.mode == kRopeInter) turn(std::integral_constant<int, kRopeInter>());
+        else turn(std::integral_constant<int, kRopeScalar>());
         return;
     }
-    int id = static_cast<int>(blockIdx.x);
+    int id = static_cast<int>(blockIdx.x) * (kStepThreads / 32) + static_cast<int>(threadIdx.x >> 5);
     const int which = id & 1;
     id >>= 1;
     const int h = id % p.Hkv;
     id /= p.Hkv;
-    const int slot = id % p.n_slots;
-    const int b = id / p.n_slots;
-    const int len = p.lens[b];
-    const int n = tokens_of<PAGE>(p, b, len);
-    if (n == 0) return;
-    if (n < 0) {
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
-        return;
-    }
-    const int start = len - n;
-    const int pj = start / PAGE + slot;
-    const int t0 = pj * PAGE;
-    if (t0 >= len) return;
-    const int pid = p.table[static_cast<int64_t>(b) * p.max_pages + pj];
-    const int pos0 = t0 + static_cast<int>(threadIdx.x) / VPT;   // position of the first vector
-    const int d0 = static_cast<int>(threadIdx.x) % VPT * 8;
-    const uint16_t* row = p.src[which] + b * p.sb + h * p.sh;
-    uint4 w[NV];
+    const int b = id / p.n_slots, lane = threadIdx.x & 31;
+    PageTokens t;
+    if (b >= p.B || !t.find(p, b, id - b * p.n_slots, lane == 0)) return;
+    const int tok = lane / VPT, d0 = lane % VPT * 8;
+    const uint16_t* src = p.src[which] + b * p.sb + h * p.sh;
+    uint8_t* page = p.pages[which] + ((t.head + h) << p.page_shift) * D + d0;
+    float* scale = p.scales[which] + t.head + h;
+    const float s_old = t.t0 < t.start ? *scale : 0.0f;
+    uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int pos = pos0 + i * STEP;
+    for (int i = 0; i < 4; ++i) {
+        const int pos = t.lo + i * TPI + tok;
         w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (pos >= start && pos < len)
-            w[i] = __ldcs(reinterpret_cast<const uint4*>(row + (pos - start) * p.st + d0));
+        if (pos < t.hi) w[i] = *reinterpret_cast<const uint4*>(src + (pos - t.start) * p.st + d0);
     }
-    if (pid < 0 || pid >= p.n_pages) {
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusPage);
-        return;
-    }
-    float y[NV][8];
+    float y[4][8], top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 e = rope_unpack<BF16>(x[j]);
-            y[i][2 * j] = e.x;
-            y[i][2 * j + 1] = e.y;
-        }
-    }
-    if (which == 0) {
-        const int half = p.f.rot >> 1, mode = p.f.mode;
-        // this vector's dimensions: which turn (bits), their pairs' cosines and the
-        // sines that the other half of the pair takes, now and over STEP positions
-        const int turn = d0 >= p.f.rot ? 0 : (p.f.rot - d0 >= 8 ? 0xff : (1 << (p.f.rot - d0)) - 1);
-        float c[8], s[8], cd[8], sd[8];
-        const int first = start > pos0 ? (start - pos0 + STEP - 1) / STEP : 0;   // first new vector
-        const int pos1 = pos0 + first * STEP, end = min(len, t0 + PAGE);
-        if (turn != 0 && pos1 < end) {
-            const bool more = pos1 + STEP < end;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d = d0 + j;
-                if (mode == kRopeInter && (j & 1)) {   // the same pair's other half
-                    c[j] = c[j - 1], s[j] = -s[j - 1];
-                    cd[j] = cd[j - 1], sd[j] = -sd[j - 1];
-                    continue;
-                }
-                c[j] = cd[j] = 1.0f;
-                s[j] = sd[j] = 0.0f;
-                if (d >= p.f.rot) continue;
-                const bool low = mode == kRopeInter || d < half;
-                const int i = mode == kRopeInter ? d >> 1 : low ? d : d - half;
-                const float2 cs = rope_cs(p.f.turns, i, pos1, p.f.amp);
-                c[j] = cs.x, s[j] = low ? -cs.y : cs.y;
-                if (more) {
-                    const float2 dd = rope_cs(p.f.turns, i, STEP, 1.0f);
-                    cd[j] = dd.x, sd[j] = low ? -dd.y : dd.y;
-                }
-            }
-        }
-        const int away = mode == kRopeHalf && d0 < p.f.rot ? (d0 < half ? half / 8 : -(half / 8)) : 0;
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int pos = pos0 + i * STEP;
-            const bool fresh = pos >= start && pos < len;
-            float o[8];   // the pairs' other halves
-            if (mode == kRopeHalf) {   // (every lane takes part)
-                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 e = rope_unpack<BF16>(__shfl_sync(0xffffffffu, x[j], lane + away));
-                    o[2 * j] = e.x;
-                    o[2 * j + 1] = e.y;
-                }
-            } else if (mode == kRopeInter) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = y[i][j ^ 1];
-            } else {
+    for (int i = 0; i < 4; ++i) {
+        unpack8<BF16>(w[i], y[i]);
+        const int pos = t.lo + i * TPI + tok;
+        if (which == 0 && t.lo + i * TPI < t.hi) {   // (the same in all lanes)
+            float o[8];
+            other_halves<BF16>(p.f, w[i], y[i], d0, src + (pos - t.start) * p.st, pos < t.hi, o);
+            if (d0 < p.f.rot && pos < t.hi) {
+                float2 cs = make_float2(1.0f, 0.0f);
+                float r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int d = d0 + j;
-                    o[j] = fresh && d < p.f.rot
-                               ? rope_load<BF16>(row + (pos - start) * p.st + (d < half ? d + half : d - half))
-                               : 0.0f;
+                    if ((p.f.mode != kRopeInter || !(j & 1)) && d0 + j < p.f.rot)
+                        cs = rope_cs(p.f.turns, pair_of(p.f, d0 + j), pos, p.f.amp);
+                    r[j] = fmaf(first_of(p.f, d0 + j) ? -o[j] : o[j], cs.y, y[i][j] * cs.x);
                 }
-            }
-            if (!fresh || turn == 0) continue;
-            float r[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = fmaf(o[j], s[j], y[i][j] * c[j]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if ((turn >> j) & 1) y[i][j] = r[j];
-            if (i + 1 < NV) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float cn = fmaf(-s[j], sd[j], c[j] * cd[j]);
-                    s[j] = fmaf(s[j], cd[j], c[j] * sd[j]);
-                    c[j] = cn;
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (d0 + j < p.f.rot) y[i][j] = r[j];
             }
         }
+        top = finite_max(top, y[i]);
     }
-    uint8_t* dst = p.pages[which] + (static_cast<int64_t>(pid) * p.Hkv + h) * (PAGE * D) + threadIdx.x * 8;
-    float* scale = p.scales[which] + static_cast<int64_t>(pid) * p.Hkv + h;
-    const float s_old = t0 < start ? *scale : 0.0f;
-    // largest finite magnitude: positive floats order like their bits
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = fabsf(y[i][j]);
-            top = fmaxf(top, a < INFINITY ? a : 0.0f);   // false for a NaN, too
-        }
-    uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    __shared__ uint32_t s_max[C::kThreads / 32];
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = u;
-    __syncthreads();   // also: every thread has read the old scale
-#pragma unroll
-    for (int i = 0; i < C::kThreads / 32; ++i) u = max(u, s_max[i]);
-    int e = amax_exp(__uint_as_float(u));
-    const int e_old = t0 < start ? scale_exp(s_old) : e;
+    int e = amax_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+    const int e_old = t.t0 < t.start ? scale_exp(s_old) : e;
     e = max(e, e_old);
-    if (threadIdx.x == 0) *scale = exp2i(e);
+    __syncwarp();   // every lane has read the old scale
+    if (lane == 0) *scale = exp2i(e);
     const float inv = exp2i(-e);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int pos = pos0 + i * STEP;
-        if (pos >= start && pos < len) {
-            uint32_t r[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = f32_to_e4m3x2(y[i][2 * j] * inv, y[i][2 * j + 1] * inv);
-            *reinterpret_cast<uint2*>(dst + i * (C::kThreads * 8)) =
-                make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int pos = t.lo + i * TPI + tok;
+        if (pos < t.hi) *reinterpret_cast<uint2*>(page + (pos - t.t0) * D) = quantise8(y[i], inv);
     }
-    if (e != e_old) raise_tokens<C::kThreads * 8, STEP>(dst, pos0, min(start, t0 + PAGE), e_old, e);
+    if (e != e_old) raise_tokens<TPI * D, TPI>(page + tok * D, t.t0 + tok, t.lo, e_old, e);
 }
 
-template <int D, int PAGE>
-cudaError_t launch_append_rope(bool bf16, AppendRopeParams p, cudaStream_t stream) {
-    using C = AppendRopeCfg<D, PAGE>;
-    int64_t ctas = static_cast<int64_t>(p.B) * p.n_slots * p.Hkv * 2;
+template <int D, bool BF16>
+cudaError_t launch_step(AppendRopeParams p, cudaStream_t stream) {
+    constexpr int kWarps = kStepThreads / 32;
+    int64_t ctas = (static_cast<int64_t>(p.B) * p.n_slots * p.Hkv * 2 + kWarps - 1) / kWarps;
     p.page_ctas = static_cast<int>(ctas);
     if (p.q) {
         p.q_threads = p.B * p.T * (D / 16);
         p.q_chunk = heads_per_thread(p.q_threads, p.Hq);
         const int64_t parts = (p.Hq + p.q_chunk - 1) / p.q_chunk;
-        ctas += (parts * p.q_threads + C::kThreads - 1) / C::kThreads;
+        ctas += (parts * p.q_threads + kStepThreads - 1) / kStepThreads;
     }
-    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(ctas)), block(C::kThreads);
-    return bf16 ? launch_kernel(kv8_append_rope_kernel<D, PAGE, true>, grid, block, 0, stream, p)
-                : launch_kernel(kv8_append_rope_kernel<D, PAGE, false>, grid, block, 0, stream, p);
+    return launch_kernel(kv8_step_rope_kernel<D, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(kStepThreads), 0, stream, p);
+}
+
+template <int D, bool BF16, int MODE>
+cudaError_t launch_prompt(AppendRopeParams p, cudaStream_t stream) {
+    auto kern = kv8_append_rope_kernel<D, BF16, MODE>;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(kern, 128 * D * static_cast<int>(sizeof(float)));
+    if (e != cudaSuccess) return e;
+    // heads in turn as long as every SM still has some CTAs
+    const int64_t pages = static_cast<int64_t>(p.B) * p.n_slots * 2;
+    const int64_t most = (static_cast<int64_t>(device_sms()) * kPromptCtas + pages - 1) / pages;   // CTAs of a page
+    p.heads = most >= p.Hkv ? 1 : static_cast<int>((p.Hkv + most - 1) / most);
+    const int64_t ctas = pages * ((p.Hkv + p.heads - 1) / p.heads);
+    const int pitch = (p.f.rot / 2 + 7) & ~7;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(prompt_threads<D>(1 << p.page_shift)),
+                         (sizeof(float) * 2 * pitch) << p.page_shift, stream, p);
+}
+template <int D, bool BF16>
+cudaError_t launch_prompt(const AppendRopeParams& p, cudaStream_t stream) {
+    switch (p.f.mode) {
+        case kRopeHalf: return launch_prompt<D, BF16, kRopeHalf>(p, stream);
+        case kRopeInter: return launch_prompt<D, BF16, kRopeInter>(p, stream);
+        default: return launch_prompt<D, BF16, kRopeScalar>(p, stream);
+    }
 }
 
 }  // namespace
@@ -391,11 +680,7 @@ extern "C" int rope_apply(const void* q, const void* k, void* q_out, void* k_out
     p.N = N;
     p.Hq = Hq;
     p.heads = Hq + Hk;
-    p.item_shift = D == 128 ? 3 : 2;
-    p.total = (B * N) << p.item_shift;
-    p.chunk = heads_per_thread(p.total, p.heads);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == ATTN_BF16 ? launch_rope<true>(p, st) : launch_rope<false>(p, st);
+    const cudaError_t e = launch_rope(p, D, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -452,19 +737,34 @@ extern "C" int kv8_append_rope(const void* k, const void* v, void* k_pages, void
     p.n_pages = n_pages;
     p.max_pages = max_pages;
     p.n_slots = static_cast<int>(slots);
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     const bool bf16 = dtype == ATTN_BF16;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
-#define TME_APPEND(d, pg) \
-    if (D == d && page == pg) e = launch_append_rope<d, pg>(bf16, p, st);
-    TME_APPEND(64, 16)
-    TME_APPEND(64, 32)
-    TME_APPEND(64, 64)
-    TME_APPEND(64, 128)
-    TME_APPEND(128, 16)
-    TME_APPEND(128, 32)
-    TME_APPEND(128, 64)
-    TME_APPEND(128, 128)
-#undef TME_APPEND
+    if (T <= (D == 64 ? step_tokens<64>() : step_tokens<128>())) {
+        e = D == 64 ? (bf16 ? launch_step<64, true>(p, st) : launch_step<64, false>(p, st))
+                    : (bf16 ? launch_step<128, true>(p, st) : launch_step<128, false>(p, st));
+        return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    }
+    e = D == 64 ? (bf16 ? launch_prompt<64, true>(p, st) : launch_prompt<64, false>(p, st))
+                : (bf16 ? launch_prompt<128, true>(p, st) : launch_prompt<128, false>(p, st));
+    if (e == cudaSuccess && q) {   // a kernel of their own, that starts in the pages' tail
+        RopeParams r{};
+        r.f = p.f;
+        for (int w = 0; w < 2; ++w) {
+            r.x[w] = p.q;
+            r.y[w] = p.q_out;
+            r.xs[w][0] = p.qb, r.xs[w][1] = p.qh, r.xs[w][2] = p.qt;
+            r.ys[w][0] = p.ob, r.ys[w][1] = p.oh, r.ys[w][2] = p.ot;
+        }
+        r.lens = lens;
+        r.n_new = n_new;
+        r.granted = granted;
+        r.most = max_pages << p.page_shift;
+        r.B = B;
+        r.N = T;
+        r.Hq = r.heads = Hq;
+        e = launch_rope(r, D, bf16, st);
+    }
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

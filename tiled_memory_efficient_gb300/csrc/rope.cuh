@@ -80,41 +80,49 @@ struct RopeRows {
 
 constexpr int kRopeBatch = 4;   // heads in flight a thread
 
-// 16 of the D dimensions of one token's heads [h0, h1), whose sines are made once for all of
-// them.  `live` false: they become zeros.  What a rotation in place leaves alone is
-// not touched.
+// Pair p of 8 of item `item`: MODE 0 and 1 hold neighbours, MODE 2 every items-th.
+template <int MODE>
+__device__ __forceinline__ int item_pair(int item, int items, int p) {
+    return MODE == kRopeScalar ? item + p * items : 8 * item + p;
+}
 
-template <bool BF16, int MODE>
-__device__ __forceinline__ void rope_item(const RopeView& f, const RopeRows& t, int item, int items, int pos,
-                                          int h0, int h1, bool live) {
-    const int half = f.rot >> 1;
-    float c[8], s[8];
-    // pair p of the item; rows of 8 pairs: MODE 0 and 1 hold neighbours, MODE 2 every items-th
-    auto pair_of = [&](int p) { return MODE == kRopeScalar ? item + p * items : 8 * item + p; };
-    if (live) {
+// The sines of an item's 8 pairs, made where they are used.
+template <int MODE>
+__device__ __forceinline__ void item_sines(const RopeView& f, int item, int items, int pos, float (&c)[8], float (&s)[8]) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            c[p] = 1.0f, s[p] = 0.0f;
-            if (pair_of(p) < half) {
-                const float2 cs = rope_cs(f.turns, pair_of(p), pos, f.amp);
-                c[p] = cs.x, s[p] = cs.y * f.sign;
-            }
+    for (int p = 0; p < 8; ++p) {
+        c[p] = 1.0f, s[p] = 0.0f;
+        const int pair = item_pair<MODE>(item, items, p);
+        if (2 * pair < f.rot) {
+            const float2 cs = rope_cs(f.turns, pair, pos, f.amp);
+            c[p] = cs.x, s[p] = cs.y * f.sign;
         }
     }
+}
+
+// 16 of the D dimensions of one token's heads h0, h0 + step, ... below h1, with the sines that
+// sines(c, s) gives, called once by every thread while the first heads are on their way.  `live`
+// false: they become zeros.  What a rotation in place leaves alone is not touched.
+template <bool BF16, int MODE, typename Sines>
+__device__ __forceinline__ void rope_item(const RopeView& f, const RopeRows& t, int item, int items, int h0,
+                                          int step, int h1, bool live, Sines sines) {
+    const int half = f.rot >> 1;
+    float c[8], s[8];
     if constexpr (MODE == kRopeScalar) {
-        for (int h = h0; h < h1; ++h) {
+        sines(c, s);
+        for (int h = h0; h < h1; h += step) {
             const uint16_t* x = t.in(h);
             uint16_t* y = t.out(h);
             float a[8], b[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p) {   // (pairs past the rotated ones: two dimensions that stay)
-                const int i = pair_of(p), d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
+                const int i = item_pair<MODE>(item, items, p), d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
                 a[p] = live ? rope_load<BF16>(x + d0) : 0.0f;
                 b[p] = live ? rope_load<BF16>(x + d1) : 0.0f;
             }
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const int i = pair_of(p), d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
+                const int i = item_pair<MODE>(item, items, p), d0 = i < half ? i : 2 * i, d1 = i < half ? i + half : 2 * i + 1;
                 const bool turn = live && i < half;
                 if (!turn && live && x == y) continue;
                 y[d0] = rope_round<BF16>(turn ? a[p] * c[p] - b[p] * s[p] : a[p]);
@@ -126,21 +134,26 @@ __device__ __forceinline__ void rope_item(const RopeView& f, const RopeRows& t, 
         const bool turns = MODE == kRopeInter ? 16 * item < f.rot : 8 * item < half;
         const int d0 = MODE == kRopeInter ? 16 * item : turns ? 8 * item : f.rot + 16 * (item - (f.rot >> 4));
         const int d1 = MODE == kRopeInter ? d0 + 8 : turns ? d0 + half : d0 + 8;
-        for (int h = h0; h < h1; h += kRopeBatch) {
-            uint4 va[kRopeBatch], vb[kRopeBatch];
+        uint4 va[kRopeBatch], vb[kRopeBatch];
+        auto load = [&](int h) {
 #pragma unroll
             for (int u = 0; u < kRopeBatch; ++u) {
                 va[u] = vb[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (h + u < h1 && live) {
-                    const uint16_t* x = t.in(h + u);
+                if (h + u * step < h1 && live) {
+                    const uint16_t* x = t.in(h + u * step);
                     va[u] = *reinterpret_cast<const uint4*>(x + d0);
                     vb[u] = *reinterpret_cast<const uint4*>(x + d1);
                 }
             }
+        };
+        load(h0);
+        sines(c, s);
+        for (int h = h0; h < h1; h += kRopeBatch * step) {
+            if (h != h0) load(h);
 #pragma unroll
             for (int u = 0; u < kRopeBatch; ++u) {
-                if (h + u >= h1) continue;
-                uint16_t* y = t.out(h + u);
+                if (h + u * step >= h1) continue;
+                uint16_t* y = t.out(h + u * step);
                 uint32_t a[4] = {va[u].x, va[u].y, va[u].z, va[u].w};
                 uint32_t b[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
                 if (live && turns) {
@@ -156,7 +169,7 @@ __device__ __forceinline__ void rope_item(const RopeView& f, const RopeRows& t, 
                                 b[j] = pack2<BF16>(o.x * c[4 + j] - o.y * s[4 + j], o.y * c[4 + j] + o.x * s[4 + j]);
                         }
                     }
-                } else if (live && y == t.in(h + u)) {
+                } else if (live && y == t.in(h + u * step)) {
                     continue;   // in place, and nothing turns
                 }
                 *reinterpret_cast<uint4*>(y + d0) = make_uint4(a[0], a[1], a[2], a[3]);
