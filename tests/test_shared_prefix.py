@@ -9,6 +9,8 @@ import torch
 
 from tests import helpers, kv8_ref
 from tiled_memory_efficient_gb300 import _lib
+from tiled_memory_efficient_gb300.kvcache import PagedKVCache
+from tiled_memory_efficient_gb300.rope import Rope
 
 F16, BF16, F8 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
 P = 256  # a fake, 16-byte-aligned "device" address: validation fails before any use
@@ -416,3 +418,98 @@ def test_the_largest_batch(cuda_lib, D, G, Nq, dtype):
     _check(q, cache, None, out, lse, f"shared, 1024 sequences D={D}", some=range(0, 1024, 41))
     a, b = _lib.kv8_attn(q.cuda(), *dev)
     helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (out, lse, a, b)), dtype, f"shared against plain D={D}")
+
+
+# ------------------------------------------------------------------ the cache that shares
+
+def test_a_cache_with_a_window_does_not_share():
+    with pytest.raises(ValueError, match="window"):
+        PagedKVCache(1, 2, 1, 64, n_pages=4, window=8, share=True, device="cpu")
+
+
+@pytest.mark.gpu
+def test_only_a_sharing_cache_looks_for_prefixes(cuda_lib):
+    with pytest.raises(ValueError, match="share"):
+        PagedKVCache(1, 2, 1, 64, n_pages=4).find_shared()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,page,rot,inter,dtype", [(64, 32, 64, False, F16), (128, 64, 32, True, BF16)])
+def test_a_run_of_samples(cuda_lib, D, page, rot, inter, dtype):
+    """A prompt with rotated keys, its fork into samples, steps that are captured as one graph, a second
+    fork (beams change, one ends, another prompt comes in) that the same graph follows, and a
+    compaction: each step's attention against the definition over the cache's own content, the rotated
+    rows against the rotation alone."""
+    S, Hq, Hkv, L, prompt, T = 10, 4, 2, 2, 1100, 2
+    rope, g, rng = Rope(D, rot, interleaved=inter), torch.Generator().manual_seed(D), random.Random(7)
+    cache = PagedKVCache(L, S, Hkv, D, n_pages=3 * prompt // page + 8 * S, page_size=page, max_pages=prompt // page + 8,
+                         share=True)
+
+    def rows(h, n):
+        return torch.randn(S, h, n, D, generator=g).to(dtype).cuda()
+
+    def step(x, n):
+        cache.reserve(n)
+        res = []
+        for i in range(L):
+            q = cache.append(i, x[i][1], x[i][2], n, rope=rope, q=x[i][0])
+            res.append((q,) + cache.attend(i, q, n_new=n))
+        return res
+
+    def check(x, n, res, what):
+        assert _lib.sync_status() == _lib.ATTN_OK
+        n_new, lens = n.tolist(), cache.lens.tolist()
+        at = (cache.lens - n)[:, None] + torch.arange(x[0][0].shape[2], dtype=torch.int32, device="cuda")[None]
+        for i in range(L):
+            q, out, lse = res[i]
+            want = rope(x[i][0], positions=at)
+            held = [t[i].cpu() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+            for b, k in enumerate(n_new):
+                assert torch.equal(q[b, :, :k], want[b, :, :k]) and not q[b, :, k:].any()
+            _check(q.cpu(), (*held, cache.table.cpu(), cache.lens.cpu()), n_new, out, lse, f"{what} layer {i}", some=(
+                0, 3, 4, 9))
+
+    def fork(parents):
+        cache.reassign(_i32(parents))
+        assert _lib.sync_status() == _lib.ATTN_OK
+        return sorted((d * RUN, len(m)) for m, d in _read_plan(cache.plan, S).values())
+
+    assert _read_plan(cache.plan, S) == {}
+    first = [(rows(Hq, prompt), rows(Hkv, prompt), rows(Hkv, prompt)) for _ in range(L)]
+    n = _i32([prompt] + [0] * (S - 1))
+    cache.reserve(n)
+    for i, (q, k, v) in enumerate(first):
+        cache.append(i, k, v, n, rope=rope)
+    assert fork([0] * S) == [(prompt // RUN * RUN, S)]
+    bufs = [(rows(Hq, T), rows(Hkv, T), rows(Hkv, T)) for _ in range(L)]
+    counts = _i32([1, 2] * (S // 2))
+    check(bufs, counts, step(bufs, counts), "eager")
+    book = [t.clone() for t in (cache.table, cache.lens, cache.refs, cache.info, cache.granted)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step(bufs, counts)
+
+    def replay(what):
+        for x in bufs:
+            for t in x:
+                t.copy_(torch.randn(t.shape, generator=g).to(dtype))
+        counts.copy_(torch.tensor([rng.randint(0, T) for _ in range(S)]))
+        graph.replay()
+        check(bufs, counts, res, what)
+
+    assert all(torch.equal(a, b) for a, b in zip(book, (cache.table, cache.lens, cache.refs, cache.info, cache.granted)))
+    for k in range(3):
+        replay(f"replay {k}")
+    assert fork([0, 0, 0, 3, 3, 3, 3, 3, 3, -1]) == [(prompt // RUN * RUN, S - 1)]
+    replay("second fork")
+    n = _i32([0] * (S - 1) + [prompt])
+    cache.reserve(n)
+    for i, (q, k, v) in enumerate(first):
+        cache.append(i, k, v, n, rope=rope)
+    replay("another prompt beside the group")
+    cache.compact()
+    replay("compacted")
+    assert fork([0] * 5 + [9] * 5) == []                # 4 * 1024 positions saved by each: too few
+    replay("no group")
+    fork([-1] * S)
+    assert not cache.refs.any() and _read_plan(cache.plan, S) == {}

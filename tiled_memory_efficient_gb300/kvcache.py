@@ -20,6 +20,15 @@ and every ``append`` leaves the cache as it is, until a ``reserve`` succeeds.
 
 A step may give each sequence its own number of tokens: ``n_new`` goes to all three
 calls, and both the keys and the queries of sequence b are the first n_new[b] rows.
+
+With a ``rope.Rope`` the append also turns the keys, and the step's queries, to the
+positions that ``reserve`` gave them::
+
+    q = cache.append(layer, k, v, n_new, rope=rope, q=q)
+
+``share=True`` is for sequences that begin alike (samples or beams of one prompt, many
+questions about one text).  One sequence takes the prompt, ``reassign`` forks it, and
+``attend`` then reads the common pages once for all of them.
 """
 from __future__ import annotations
 
@@ -36,18 +45,22 @@ class PagedKVCache:
     page_size is 16, 32, 64 or 128 tokens; max_pages (default: all n_pages) the
     most pages one sequence can hold.  With window > 0 queries see the last
     `window` positions and the first `sinks`, and ``reserve`` gives back pages
-    the window has left behind.
+    the window has left behind.  share (without a window): ``reassign`` looks which
+    sequences begin with the same pages, and ``attend`` reads those once for all of
+    them; whoever writes `table` by hand calls ``find_shared`` afterwards.
     """
 
     def __init__(self, n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, n_pages: int,
                  page_size: int = 64, max_pages: int | None = None, window: int = 0, sinks: int = 0,
-                 device="cuda"):
+                 device="cuda", share: bool = False):
         if head_dim not in (64, 128):
             raise NotImplementedError(f"head dim {head_dim} is not one of (64, 128)")
         if page_size not in (16, 32, 64, 128):
             raise NotImplementedError(f"page size {page_size} is not one of (16, 32, 64, 128)")
         if min(n_layers, n_seqs, n_kv_heads, n_pages) < 1 or window < 0 or sinks < 0:
             raise ValueError("sizes must be positive, window and sinks not negative")
+        if share and window:
+            raise ValueError("a cache with a window does not share the reading of prefixes")
         max_pages = n_pages if max_pages is None else max_pages
         if max_pages < 1:
             raise ValueError("max_pages must be positive")
@@ -70,6 +83,9 @@ class PagedKVCache:
         self._ws = torch.empty(_lib.kvp_workspace_size(n_seqs, max_pages, n_pages), device=device,
                                dtype=torch.uint8)
         self._all = torch.empty(n_seqs, **i32)
+        self.plan = None   # which sequences share a prefix
+        if share:
+            self.plan = _lib.kvp_find_shared(self.table, self.lens, page_size)
 
     def _counts(self, n):
         if isinstance(n, int):
@@ -101,6 +117,11 @@ class PagedKVCache:
         of a step that found no room) get 0 and -inf.  None: all Nq rows are the
         newest positions; with a window no more than the sequence's last ``reserve``
         made room for, since older queries want pages that it gave back."""
+        if self.plan is not None:
+            return _lib.kv8_attn_shared(q, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
+                                        self.v_scale[layer], self.table, self.lens, self.plan, scale=scale,
+                                        n_new=None if n_new is None else self._counts(n_new),
+                                        granted=None if n_new is None else self.granted)
         return _lib.kv8_attn(q, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                              self.v_scale[layer], self.table, self.lens, scale=scale,
                              window=self.window, sinks=self.sinks,
@@ -114,6 +135,14 @@ class PagedKVCache:
         _lib.kvp_reassign(self.table, self.lens, self.refs, parents, self.page_size, self._src,
                           self._dst, self.info, workspace=self._ws)
         self._copy(self.table.shape[0])
+        if self.plan is not None:
+            self.find_shared()
+
+    def find_shared(self):
+        """With share: looks anew which sequences begin with the same pages."""
+        if self.plan is None:
+            raise ValueError("the cache was made without share")
+        _lib.kvp_find_shared(self.table, self.lens, self.page_size, plan=self.plan)
 
     def compact(self):
         """Moves the held pages of every layer to the front of the pools."""
