@@ -134,15 +134,14 @@ size_t kv8_attn_workspace_size(int B, int Hq, int Hkv, int Nq, int D);
  * first pages are the same, in whole runs of 128 positions, form a group; where some of
  * them share more than the others, each joins the group that leaves it the least to
  * read.  A group is kept when reading its prefix once saves min_saved
- * positions or more (members less one, times the prefix; below about KVP_MIN_SAVED the
- * plain attention is the faster one).  table [n_seqs, max_pages] and lens are not changed.  n_seqs <= 1024.
+ * positions or more (members less one, times the prefix).  min_saved -1 leaves it to the attention, which
+ * follows the plan where its groups save 128 MB of keys and values in all, and otherwise
+ * reads every sequence for itself.  table [n_seqs, max_pages] and lens are not changed.  n_seqs <= 1024.
  *
  * The plan stays right while every sequence keeps the pages it begins with: appends, kvp_reserve
  * without a window and kvp_compact keep them; after kvp_reassign it is made anew.  (Work
  * grows with n_seqs^2 times the prefix's runs: it is for a fork, not for every step.)
  */
-#define KVP_MIN_SAVED 8192
-
 int kvp_find_shared(const int* table, const int* lens, int n_seqs, int max_pages, int page,
                     int min_saved, int* plan, void* stream);
 

@@ -41,7 +41,7 @@ FIND = dict(table=P, lens=P, n=4, max_pages=5, page=64, least=0, plan=P)
 
 
 @pytest.mark.parametrize("change,code", [
-    ({"table": 0}, 1), ({"plan": 0}, 1), ({"n": 0}, 1), ({"least": -1}, 1), ({"max_pages": 0}, 1), ({"n": 1025}, 2),
+    ({"table": 0}, 1), ({"plan": 0}, 1), ({"n": 0}, 1), ({"least": -2}, 1), ({"max_pages": 0}, 1), ({"n": 1025}, 2),
     ({"page": 20}, 2), ({"lens": P + 2}, 3), ({"max_pages": 1 << 28}, 2),
 ])
 def test_plan_refusals(lib, change, code):
@@ -420,6 +420,33 @@ def test_the_largest_batch(cuda_lib, D, G, Nq, dtype):
     helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (out, lse, a, b)), dtype, f"shared against plain D={D}")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("members,worth", [(32, False), (34, True)])
+def test_the_attention_decides(cuda_lib, members, worth):
+    """A plan that leaves the choice is followed from 128 MB of keys and values saved on: 32 or 34
+    sequences with 2048 positions of 2 KB in common."""
+    Hkv, D, page = 8, 128, 64
+    cache = [t.cuda() for t in _batch([(2048, members)], [70, 3], [300], Hkv, D, page, seed=5)]
+    B = cache[5].numel()
+    q = torch.randn(B, 2 * Hkv, 1, D, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    by = {least: _lib.kvp_find_shared(cache[4], cache[5], page, least) for least in (-1, 0, (1 << 31) - 1)}
+    assert by[-1].tolist()[:4] == [by[0].tolist()[0], 1, B, (members - 1) * 2048 // RUN]
+    assert _read_plan(by[-1], B) == _read_plan(by[0], B) and len(_read_plan(by[0], B)) == 1
+    res = {least: _lib.kv8_attn_shared(q, *cache, plan) for least, plan in by.items()}
+    same = {least: all(torch.equal(a, b) for a, b in zip(res[least], res[-1])) for least in by}
+    assert same == {-1: True, 0: worth, (1 << 31) - 1: not worth}
+    assert (members - 1) * 2048 * 2 * Hkv * D // (128 << 20) == int(worth) and _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_small_groups_are_left_alone(cuda_lib):
+    """A plan that leaves the choice: no group of fewer than 8192 positions saved."""
+    _, _, _, _, table, lens = _batch([(1024, 9), (1024, 8), (4096, 3)], [5], [], 1, 64, 64, seed=2)
+    plan = _lib.kvp_find_shared(table.cuda(), lens.cuda(), 64)
+    assert sorted((d * RUN, len(m)) for m, d in _read_plan(plan, 20).values()) == [(1024, 9), (4096, 3)]
+    assert plan[3].item() == (8 * 1024 + 2 * 4096) // RUN
+
+
 # ------------------------------------------------------------------ the cache that shares
 
 def test_a_cache_with_a_window_does_not_share():
@@ -443,7 +470,7 @@ def test_a_run_of_samples(cuda_lib, D, page, rot, inter, dtype):
     S, Hq, Hkv, L, prompt, T = 10, 4, 2, 2, 1100, 2
     rope, g, rng = Rope(D, rot, interleaved=inter), torch.Generator().manual_seed(D), random.Random(7)
     cache = PagedKVCache(L, S, Hkv, D, n_pages=3 * prompt // page + 8 * S, page_size=page, max_pages=prompt // page + 8,
-                         share=True)
+                         share=True, min_saved=8192)
 
     def rows(h, n):
         return torch.randn(S, h, n, D, generator=g).to(dtype).cuda()

@@ -581,8 +581,10 @@ def _explain_result(name, out, like):
     raise ValueError(f"{name} needs dense, 16-byte aligned rows that do not overlap")
 
 
-def _explain_rope(q, k, positions):
+def _explain_rope(q, k, positions, rope):
     import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != rope.head_dim:
+        raise ValueError(f"rows {tuple(getattr(q, 'shape', ()))} are not [B, H, N, {rope.head_dim}]")
     for name, t in (("q", q), ("k", k)):
         if t is None:
             continue
@@ -599,24 +601,17 @@ def _explain_rope(q, k, positions):
             raise ValueError(f"positions must be an int32 tensor [{N}] or [{B}, {N}] on {q.device}")
 
 
-def _need_head_dim(rope, q):
-    if q.dim() != 4 or q.shape[3] != rope.head_dim:
-        raise ValueError(f"rows {tuple(q.shape)} are not [B, H, N, {rope.head_dim}]")
-
-
 def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, transposed: bool = False):
     """q [B, Hq, N, D] and k [B, Hk, N, D] (k None: q alone) turned to positions (int32
     [N] or [B, N]; None: start + n) by a rope.Rope (include/rope.h): the pair, or q
     alone.  q_out and k_out may be q and k.  transposed turns back, times the amplitude.
     Not differentiable: see rotary."""
-    _need_head_dim(rope, q)
-    r = (_bind or _load_bind()).rope(q, k, positions, start, rope.turns(q.device), rope.rotary_dim,
-                                     rope.interleaved, rope.amplitude, q_out, k_out, int(transposed))
+    r = (_bind or _load_bind()).rope(q, k, positions, start, rope.for_rows(q), q_out, k_out, int(transposed))
     if type(r) is not int:
         return r
 
     def explain():
-        _explain_rope(q, k, positions)
+        _explain_rope(q, k, positions, rope)
         if k is None and k_out is not None:
             raise ValueError("k_out without k")
         _explain_result("q_out", q_out, q)
@@ -626,12 +621,10 @@ def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, tra
 
 def rotary(q, k, rope, positions=None, start: int = 0):
     """rope as a differentiable function of q and k."""
-    _need_head_dim(rope, q)
-    r = (_bind or _load_bind()).rotary(q, k, positions, start, rope.turns(q.device), rope.rotary_dim,
-                                       rope.interleaved, rope.amplitude)
+    r = (_bind or _load_bind()).rotary(q, k, positions, start, rope.for_rows(q))
     if type(r) is not int:
         return r
-    _refused("rope_apply", r, lambda: _explain_rope(q, k, positions))
+    _refused("rope_apply", r, lambda: _explain_rope(q, k, positions, rope))
 
 
 # ------------------------------------------------------------------ paged 8-bit KV cache
@@ -683,16 +676,15 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
         if rc == ATTN_OK:
             return None
     else:
-        if rope.head_dim != k.shape[-1]:
-            raise ValueError(f"the rotation is for head dim {rope.head_dim}, not {k.shape[-1]}")
         rc = bind.kv8_append_rope(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new, granted,
-                                  rope.turns(k.device), rope.rotary_dim, rope.interleaved, rope.amplitude, q,
-                                  q_out)
+                                  rope.for_rows(k), q, q_out)
         if type(rc) is not int:
             return rc
 
     def explain():
         import torch
+        if rope is not None and rope.head_dim != k.shape[-1]:
+            raise ValueError(f"the rotation is for head dim {rope.head_dim}, not {k.shape[-1]}")
         dev, (_, Hkv, _, D) = _explain_pools(k_pages, v_pages, k_scale, v_scale)
         _dtype_code(k)
         if not (k.dim() == 4 and v.shape == k.shape and v.dtype is k.dtype and k.shape[1] == Hkv
@@ -777,14 +769,11 @@ def kv8_attn_shared(q, k_pages, v_pages, k_scale, v_scale, table, lens, plan, sc
     _refused("kv8_attn_shared", r, explain)
 
 
-# Positions that a group has to save by reading its prefix once (include/kvcache.h, KVP_MIN_SAVED).
-MIN_SAVED = 8192
-
-
-def kvp_find_shared(table, lens, page: int, min_saved: int = MIN_SAVED, plan=None):
+def kvp_find_shared(table, lens, page: int, min_saved: int = -1, plan=None):
     """Which sequences begin with the same pages: the plan of kv8_attn_shared (int32, written
-    to plan if given).  Made after a fork and kept until the next one
-    (include/kvcache.h)."""
+    to plan if given).  Made after a fork and kept until the next one.  min_saved: positions that
+    a group has to save (-1: as far as the attention finds it worth while;
+    include/kvcache.h)."""
     r = (_bind or _load_bind()).kvp_find_shared(table, lens, page, min_saved, plan)
     if type(r) is not int:
         return r

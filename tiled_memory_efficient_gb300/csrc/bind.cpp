@@ -251,14 +251,17 @@ struct Turns {
     Tensor turns;
     int rot = 0, interleaved = 0;
     float amp = 1.0f;
-    // (turns, rot, interleaved, amplitude)
-    bool read(PyObject* const* a, int64_t dev) {
+    // One tuple: (turns, rot, interleaved, amplitude, head dim)
+    bool read(PyObject* o, int64_t dev, int64_t D) {
+        if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) return false;
+        PyObject* a[5];
+        for (int i = 0; i < 5; ++i) a[i] = PyTuple_GET_ITEM(o, i);
         turns = tensor(a[0]);
-        float x;
-        if (!whole(a[1], &rot) || !whole(a[2], &interleaved) || a[3] == Py_None || !scale_of(a[3], 1, &x))
+        int dim;
+        if (!whole(a[1], &rot) || !whole(a[2], &interleaved) || a[3] == Py_None || !scale_of(a[3], 1, &amp) ||
+            !whole(a[4], &dim))
             return false;
-        amp = x;
-        return rot > 0 && fits(turns, dev, at::kLong, {rot / 2});
+        return dim == D && rot > 0 && fits(turns, dev, at::kLong, {rot / 2});
     }
     const unsigned long long* at() const { return as<unsigned long long>(turns); }
 };
@@ -288,32 +291,32 @@ bool result_for(const Tensor& out, const Tensor& like) {
     return true;
 }
 
-// (Append, turns, rot, interleaved, amplitude, q | None, q_out | None) -> q_out, None or rc
+// (Append, Turns, q | None, q_out | None) -> q_out, None or rc
 PyObject* py_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Append x;
     Turns r;
-    if (n != 16 || !x.read(a) || !r.read(a + 10, x.p.dev)) MISFIT();
+    if (n != 13 || !x.read(a) || !r.read(a[10], x.p.dev, x.p.D)) MISFIT();
     const Pools& p = x.p;
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(p.dev));
     long long st[9] = {x.st[0], x.st[1], x.st[2]};
     Tensor q, out;
-    if (a[14] != Py_None) {
-        q = tensor(a[14]);
+    if (a[11] != Py_None) {
+        q = tensor(a[11]);
         if (cuda_of(q) != p.dev || q.dim() != 4 || q.scalar_type() != x.k.scalar_type() || q.size(0) != x.B ||
             q.size(2) != x.T || q.size(3) != p.D || !small(q.sizes()))
             MISFIT();
-        if (a[15] == Py_None) {
+        if (a[12] == Py_None) {
             q = readable(q);
             out = empty(q.sizes(), q.scalar_type(), p.dev);
         } else {
-            out = tensor(a[15]);
+            out = tensor(a[12]);
             if (!result_for(out, q)) MISFIT();
             if (out.data_ptr() != q.data_ptr()) q = readable(q);
         }
         strides_of(q, st + 3);
         strides_of(out, st + 6);
-    } else if (a[15] != Py_None) {
+    } else if (a[12] != Py_None) {
         MISFIT();
     }
     const int rc = unlocked([&] {
@@ -833,13 +836,13 @@ struct Rotary : torch::autograd::Function<Rotary> {
 // Wraps q' and, if there is one, k'.
 PyObject* rotated(const Tensor& q, const Tensor& k) { return k.defined() ? pair(q, k) : THPVariable_Wrap(q); }
 
-// (q, k | None, positions | None, start, turns, rot, interleaved, amplitude) -> q', (q', k') or rc;
+// (q, k | None, positions | None, start, Turns) -> q', (q', k') or rc;
 // differentiable
 PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     RopeCall c;
-    if (n != 8 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
-        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a + 4, c.dev()))
+    if (n != 5 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
+        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a[4], c.dev(), c.q.size(3)))
         MISFIT();
     Tensor q_out, k_out;
     const bool graph = at::GradMode::is_enabled() &&
@@ -847,7 +850,8 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = unlocked([&] {
         if (!graph) return c.run(&q_out, &k_out);
         try {
-            auto r = Rotary::apply(c.q, Rotary::maybe(c.k), Rotary::maybe(c.positions), c.r.turns, c.start, c.r.rot, c.r.interleaved, c.r.amp, 0);
+            auto r = Rotary::apply(c.q, Rotary::maybe(c.k), Rotary::maybe(c.positions), c.r.turns, c.start, c.r.rot,
+                                   c.r.interleaved, c.r.amp, 0);
             q_out = r[0];
             if (r.size() > 1) k_out = r[1];
         } catch (const Refused& r) {
@@ -859,20 +863,19 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (q, k | None, positions | None, start, turns, rot, interleaved, amplitude, q_out | None,
-//  k_out | None, transposed) -> q', (q', k') or rc
+// (q, k | None, positions | None, start, Turns, q_out | None, k_out | None, transposed) -> q', (q', k') or rc
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     RopeCall c;
-    if (n != 11 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
-        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a + 4, c.dev()) ||
-        !whole(a[10], &c.transposed))
+    if (n != 8 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
+        !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a[4], c.dev(), c.q.size(3)) ||
+        !whole(a[7], &c.transposed))
         MISFIT();
     Tensor out[2];
     for (int i = 0; i < 2; ++i) {
-        if (a[8 + i] == Py_None) continue;
+        if (a[5 + i] == Py_None) continue;
         const Tensor& like = i == 0 ? c.q : c.k;
-        out[i] = tensor(a[8 + i]);
+        out[i] = tensor(a[5 + i]);
         if (!result_for(out[i], like)) MISFIT();
     }
     const int rc = unlocked([&] { return c.run(&out[0], &out[1]); });

@@ -130,6 +130,7 @@ struct AttnParams {
     // attention over a shared prefix (null: none): the plan, and the rows of sequences that
     // share, over the positions after their prefix
     const int* plan;
+    int least_runs;    // runs that a plan's groups have to save in all
     float* own_o;      // [B, Hq, Nq][D]
     float* own_lse;    // [B, Hq, Nq], log2 domain
     unsigned int* status;
@@ -196,7 +197,7 @@ __device__ __forceinline__ Shares own_shares(const AttnParams& p, int T) {
     return Shares(T, own_workers(p.ctas, p.rows), p.rows <= 16 ? kWarpMinShare : kMinShare);
 }
 
-// What kvp_find_shared leaves: a header, then arrays of n_seqs words.  Group g are the
+// What kvp_find_shared leaves: a header (magic, groups, n_seqs, runs that all of them save), then arrays of n_seqs words.  Group g are the
 // sequences members[first[g] .. + count[g]), in ascending order; the first `blocks[g]` runs of
 // kShareBlock positions of all of them lie in the pages of the first one's table row.
 constexpr int kShareBlock = 128;
@@ -205,8 +206,9 @@ struct Plan {
     const int* w;
     int n;
     __device__ __forceinline__ Plan(const int* words, int n_seqs) : w(words), n(n_seqs) {}
-    // Whether it is a plan for as many sequences at all.
+    // Whether it is a plan for as many sequences at all, and whether it is worth while.
     __device__ __forceinline__ bool ok() const { return w[0] == kPlanMagic && w[2] == n; }
+    __device__ __forceinline__ bool ok(int least_runs) const { return ok() && w[3] >= least_runs; }
     __device__ __forceinline__ int groups() const { return min(max(w[1], 0), n); }
     __device__ __forceinline__ int at(int array, int i) const { return w[4 + array * n + i]; }
     __device__ __forceinline__ int first(int g) const { return min(max(at(0, g), 0), n); }

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if constexpr (SHARED) {
                 const Plan plan(p.plan, p.B);
                 start = plan.start(b);   // (asked for beside the header)
-                if (!plan.ok()) start = 0;
+                if (!plan.ok(p.least_runs)) start = 0;
             }
             if (blockIdx.x == 0 && (len < 0 || len > p.max_pages << p.page_shift || nq < 0))
                 atomicOr(p.status, kStatusPage);

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusPage);
         return;
     }
-    const int groups = granted ? plan.groups() : 0;
+    const int groups = granted && plan.ok(a.least_runs) ? plan.groups() : 0;
     const int T = all_tiles(a, plan, groups, RB);
     const Shares sh(T, a.ctas, kPreMinShare);
     const int cta = static_cast<int>(blockIdx.x);
@@ -747,23 +747,24 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
 
 // ------------------------------------------------------------------ merge
 
-// A warp per row: the row's results over the prefix and over its own positions, each whole or in
-// the parts that several CTAs left.  Rows of sequences that share nothing and lie in
+// A warp per row, or (WPR) a CTA's four: the row's results over the prefix and over its own positions, each
+// whole or in the parts that several CTAs left.  Rows of sequences that share nothing and lie in
 // one CTA are written already.
 constexpr int kMergeWarps = 4;
+constexpr int kMergeRowsAlone = 8;   // rows per SM up to which a CTA takes one
 
-template <int D, bool BF16>
+template <int D, bool BF16, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     kv8_shared_merge_kernel(const __grid_constant__ PreParams p, int row_block, int row8) {
     const AttnParams& a = p.a;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;");   // the next kernel may set up
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    const int64_t row = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp : blockIdx.x;
     const bool real = row < static_cast<int64_t>(a.B) * a.Hkv * a.rows;
     const int u = real ? static_cast<int>(row / a.rows) : 0;   // (sequence, KV head)
     const int b = u / a.Hkv, h = u - b * a.Hkv, rr = static_cast<int>(row - static_cast<int64_t>(u) * a.rows);
     const Plan plan(a.plan, a.B);
-    const bool granted = step_granted(a), planned = plan.ok();
+    const bool granted = step_granted(a), planned = plan.ok(a.least_runs);
     // own positions: the tiles of all sequences, and of those before b
     int all = 0, before = 0, n = 0;
     for (int i = lane; i < a.B; i += 32) {
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         const float* l = (own ? (whole ? a.own_lse : a.part_lse) : (whole ? p.row_lse : p.part_lse)) + at;
         const float* o = (own ? (whole ? a.own_o : a.part_o) : (whole ? p.row_o : p.part_o)) + at * D + col;
 #pragma unroll 1
-        for (int k = sub; k < n_run; k += 8 * PER) {
+        for (int k = sub + (WPR > 1 ? warp * 8 * PER : 0); k < n_run; k += WPR * 8 * PER) {
             float L[8], top = M;
             float4 y[8];
 #pragma unroll
@@ -866,6 +867,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
             acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
         }
     }
+    if constexpr (WPR > 1) {   // the warps' sums
+        __shared__ float s_m[WPR], s_sum[WPR];
+        __shared__ __align__(16) float s_acc[WPR][D];
+        if (lane == 0) s_m[warp] = M, s_sum[warp] = sum;
+        if (sub == 0) *reinterpret_cast<float4*>(&s_acc[warp][col]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < WPR; ++w) M = fmaxf(M, s_m[w]);
+        sum = acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+        for (int w = 0; w < WPR; ++w) {
+            const float al = s_m[w] == -INFINITY ? 0.0f : ex2_ftz(s_m[w] - M);
+            const float4 y = *reinterpret_cast<const float4*>(&s_acc[w][col]);
+            sum = fmaf(s_sum[w], al, sum);
+            acc[0] = fmaf(y.x, al, acc[0]);
+            acc[1] = fmaf(y.y, al, acc[1]);
+            acc[2] = fmaf(y.z, al, acc[2]);
+            acc[3] = fmaf(y.w, al, acc[3]);
+        }
+    }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (sub == 0)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + col) =
@@ -898,8 +918,11 @@ __global__ void __launch_bounds__(kFindThreads) kvp_depth_kernel(const FindParam
     asm volatile("griddepcontrol.launch_dependents;");
     __shared__ float s_gain[kFindThreads / 32];
     __shared__ int s_at[kFindThreads / 32];
+    __shared__ int s_full[kMaxBatch];
     const int b = static_cast<int>(blockIdx.x), cols = block_cols(p);
-    const int n = full_blocks(p, p.lens[b]);
+    for (int k = threadIdx.x; k < p.B; k += kFindThreads) s_full[k] = full_blocks(p, p.lens[k]);
+    __syncthreads();
+    const int n = s_full[b];
     const int64_t stride = p.max_pages;
     float gain = 0.0f;
     int at = -1;
@@ -908,9 +931,16 @@ __global__ void __launch_bounds__(kFindThreads) kvp_depth_kernel(const FindParam
         int r = 0;
         if (i < n) {
             const int c = (i + 1) * cols - 1, pid = p.table[b * stride + c];
-            if (pid >= 0)
-                for (int k = 0; k < p.B; ++k)
-                    if (p.table[k * stride + c] == pid && full_blocks(p, p.lens[k]) > i) ++r;
+            const int* other = p.table + c;
+#pragma unroll 1
+            for (int k0 = 0; k0 < p.B; k0 += 16) {   // sixteen in flight
+                int x[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) x[u] = k0 + u < p.B ? other[(k0 + u) * stride] : -1;
+#pragma unroll
+                for (int u = 0; u < 16; ++u) r += k0 + u < p.B && x[u] == pid && s_full[min(k0 + u, kMaxBatch - 1)] > i;
+            }
+            if (pid < 0) r = 0;
         }
         const float x = r > 1 ? static_cast<float>(i + 1) * static_cast<float>(r - 1) / static_cast<float>(r) : 0.0f;
         if (x > gain) gain = x, at = i;
@@ -960,21 +990,26 @@ __global__ void __launch_bounds__(kFindThreads) kvp_leader_kernel(const FindPara
 
 // The plan, one CTA: groups of two or more that save enough, in the order of their first sequences.
 constexpr int kPlanThreads = 1024;
+// Of a plan that leaves the choice to the attention: what a group saves, in positions.
+constexpr int kGroupMinSaved = 8192;
 __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams p) {
     __shared__ int s_leader[kMaxBatch], s_count[kMaxBatch], s_group[kMaxBatch], s_off[kMaxBatch];
     __shared__ int s_warp[2][32];
+    __shared__ unsigned long long s_saved;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = static_cast<int>(threadIdx.x), lane = b & 31, warp = b >> 5;
     const int* scratch = p.plan + 4 + kPlanArrays * p.B;
     const int depth = b < p.B ? scratch[b] : 0, leader = b < p.B ? scratch[2 * p.B + b] : -1;
     s_leader[b] = leader;
     s_count[b] = 0;
+    if (b == 0) s_saved = 0;
     __syncthreads();
     if (leader >= 0) atomicAdd(&s_count[leader], 1);
     __syncthreads();
     // leaders of groups that stay
     const int64_t saved = static_cast<int64_t>(s_count[b] - 1) * depth * kShareBlock;
-    const bool stays = leader == b && s_count[b] > 1 && saved >= p.min_saved;
+    const bool stays = leader == b && s_count[b] > 1 && saved >= (p.min_saved < 0 ? kGroupMinSaved : p.min_saved);
+    if (stays) atomicAdd(&s_saved, static_cast<unsigned long long>(saved / kShareBlock));   // (integers: any order)
     int g = stays ? 1 : 0, off = stays ? s_count[b] : 0;   // prefix sums over the sequences
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -1018,12 +1053,18 @@ __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams
     if (b == 0) {
         p.plan[1] = groups;
         p.plan[2] = p.B;
-        p.plan[3] = 0;
+        p.plan[3] = p.min_saved < 0 ? static_cast<int>(min(s_saved, 0x7ffffffeull)) : 0x7fffffff;   // by hand: always
         p.plan[0] = kPlanMagic;
     }
 }
 
 // ------------------------------------------------------------------ host
+
+// Keys and values that a plan's groups save by reading prefixes once, from which on it is followed where it leaves
+// that to the attention.  Every sequence for itself against the prefixes once, us: 128 sequences of 512
+// shared positions, 8 KV heads of 128 (133 MB) 34 and 38, of 1024 (266 MB) 48 and 39; 32 sequences of 2048
+// (130 MB) 26 and 25; 128 sequences of 2048, 2 KV heads of 64 (67 MB) 21 and 23, of 4096 (133 MB) 29 and 24.
+constexpr int64_t kWorthBytes = 128ll << 20;
 
 // Rows of a CTA of the prefix kernel: one Q tile where all the batch's rows of a KV head fit it.
 int prefix_tiles(int B, int64_t rows) { return B * rows <= kPreRows ? 1 : 2; }
@@ -1053,8 +1094,15 @@ cudaError_t launch_prefix(const PreParams& p, cudaStream_t stream) {
 template <int D, bool BF16>
 cudaError_t launch_shared_merge(const PreParams& p, int row_block, int row8, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.a.B) * p.a.Hkv * p.a.rows;
-    return launch_dependent(kv8_shared_merge_kernel<D, BF16>, (rows + kMergeWarps - 1) / kMergeWarps,
-                            kMergeWarps * 32, 0, stream, p, row_block, row8);
+    // Few rows have many parts, which four warps take together: 896 rows (64 samples under 32K positions) 36.3 us
+    // the whole call and 33.7, two sequences of 64K for themselves 39 and 22; 2304 rows with a warp each 40,
+    // with four 47 (few parts, and four times the CTAs).
+    if (rows <= static_cast<int64_t>(kMergeRowsAlone) * p.a.ctas)
+        return launch_dependent(kv8_shared_merge_kernel<D, BF16, kMergeWarps>, static_cast<unsigned>(rows),
+                                kMergeWarps * 32, 0, stream, p, row_block, row8);
+    return launch_dependent(kv8_shared_merge_kernel<D, BF16, 1>,
+                            static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0,
+                            stream, p, row_block, row8);
 }
 
 }  // namespace
@@ -1069,7 +1117,7 @@ extern "C" size_t kvp_plan_words(int n_seqs) {
 
 extern "C" int kvp_find_shared(const int* table, const int* lens, int n_seqs, int max_pages, int page,
                                int min_saved, int* plan, void* stream) {
-    if (!table || !lens || !plan || n_seqs <= 0 || max_pages <= 0 || page <= 0 || min_saved < 0)
+    if (!table || !lens || !plan || n_seqs <= 0 || max_pages <= 0 || page <= 0 || min_saved < -1)
         return ATTN_ERR_INVALID;
     if (n_seqs > kMaxBatch) return ATTN_ERR_UNSUPPORTED;
     int rc = check_cache(n_seqs, 1, 64, page, 1, max_pages);
@@ -1124,6 +1172,8 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
         return r;
     };
     p.a.plan = plan;
+    const int64_t run_bytes = 2ll * Hkv * D * kShareBlock, least = (kWorthBytes + run_bytes - 1) / run_bytes;
+    p.a.least_runs = static_cast<int>(least);
     p.a.own_o = take(z.own_o);
     p.a.own_lse = take(z.own_lse);
     p.row_o = take(z.row_o);

@@ -47,12 +47,13 @@ class PagedKVCache:
     `window` positions and the first `sinks`, and ``reserve`` gives back pages
     the window has left behind.  share (without a window): ``reassign`` looks which
     sequences begin with the same pages, and ``attend`` reads those once for all of
-    them; whoever writes `table` by hand calls ``find_shared`` afterwards.
+    them where that saves enough (128 MB of keys and values; or min_saved positions, for
+    each group).  Whoever writes `table` by hand calls ``find_shared`` afterwards.
     """
 
     def __init__(self, n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, n_pages: int,
                  page_size: int = 64, max_pages: int | None = None, window: int = 0, sinks: int = 0,
-                 device="cuda", share: bool = False):
+                 device="cuda", share: bool = False, min_saved: int = -1):
         if head_dim not in (64, 128):
             raise NotImplementedError(f"head dim {head_dim} is not one of (64, 128)")
         if page_size not in (16, 32, 64, 128):
@@ -85,7 +86,8 @@ class PagedKVCache:
         self._all = torch.empty(n_seqs, **i32)
         self.plan = None   # which sequences share a prefix
         if share:
-            self.plan = _lib.kvp_find_shared(self.table, self.lens, page_size)
+            self.min_saved = min_saved
+            self.plan = _lib.kvp_find_shared(self.table, self.lens, page_size, min_saved)
 
     def _counts(self, n):
         if isinstance(n, int):
@@ -142,7 +144,7 @@ class PagedKVCache:
         """With share: looks anew which sequences begin with the same pages."""
         if self.plan is None:
             raise ValueError("the cache was made without share")
-        _lib.kvp_find_shared(self.table, self.lens, self.page_size, plan=self.plan)
+        _lib.kvp_find_shared(self.table, self.lens, self.page_size, self.min_saved, plan=self.plan)
 
     def compact(self):
         """Moves the held pages of every layer to the front of the pools."""

@@ -118,19 +118,28 @@ class Rope:
         # as fractions of a turn, 64 bits (the signed view of an unsigned word)
         words = [round(Fraction(f) * _PER_TURN * 2 ** 64) % 2 ** 64 for f in freqs]
         self._words = [w - 2 ** 64 if w >= 2 ** 63 else w for w in words]
-        self._turns = {}
+        self._turns = {}   # by device index (-1: the CPU)
 
     def turns(self, device):
         """The frequencies as the kernels take them (int64 [rotary_dim / 2]) on a device.  The
         first call on each device copies them there: make it before a stream capture."""
         import torch
         device = torch.device(device)
-        index = torch.cuda.current_device() if device.type == "cuda" and device.index is None else device.index
-        t = self._turns.get((device.type, index))
-        if t is None:
-            t = self._turns[(device.type, index)] = torch.tensor(self._words, dtype=torch.int64, device=device)
-        return t
+        index = -1 if device.type != "cuda" else torch.cuda.current_device() if device.index is None else device.index
+        if index not in self._turns:
+            t = torch.tensor(self._words, dtype=torch.int64, device=device)
+            self._turns[index] = (t, self.rotary_dim, self.interleaved, self.amplitude, self.head_dim)
+        return self._turns[index][0]
+
+    def for_rows(self, x):
+        """What the calls take for rows x: the frequencies on its device, and the numbers."""
+        a = self._turns.get(x.get_device())
+        if a is None:
+            self.turns(x.device)
+            a = self._turns[x.get_device()]
+        return a
 
     def __call__(self, q, k=None, positions=None, start: int = 0):
         """q, or (q, k), turned to positions (int32 [N] or [B, N]; None: start + n)."""
-        return _lib.rotary(q, k, self, positions, start)
+        r = (_lib._bind or _lib._load_bind()).rotary(q, k, positions, start, self.for_rows(q))
+        return r if type(r) is not int else _lib.rotary(q, k, self, positions, start)
