@@ -69,10 +69,21 @@ struct PreCfg {
     static constexpr int kRowBlock = QT * kPreRows;
 };
 
-// Tiles, units and rows of a group.
+// Tiles, units and rows of a group.  The shares are cut from its units' steps: to begin a unit (its queries
+// on their way, the rows of the one before written) takes about as long as kUnitSteps tiles, so that a CTA
+// which ends one unit and begins another has as many tiles less: four groups of 12 sequences with three
+// queries under 5008 positions (4 KV heads, D = 128) 36.5 us instead of 39.9 with equal tiles, 64 samples
+// under 32K positions (2 KV heads, D = 64) 32.9 instead of 33.8; 2 to 6 steps measure alike.
+constexpr int kUnitSteps = 3;
 struct Group {
     int blocks, n_rb, units, rows;
-    __device__ __forceinline__ int tiles() const { return units * blocks; }
+    __device__ __forceinline__ int unit_steps() const { return blocks > 0 ? blocks + kUnitSteps : 0; }
+    __device__ __forceinline__ int steps() const { return units * unit_steps(); }
+    // tiles before step s of the group
+    __device__ __forceinline__ int tiles_before(int s) const {
+        const int u = s / unit_steps();
+        return u * blocks + max(s - u * unit_steps() - kUnitSteps, 0);
+    }
 };
 __device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan, int g, int row_block) {
     Group x;
@@ -82,15 +93,13 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan,
     x.units = p.Hkv * x.n_rb;
     return x;
 }
-// Tiles of all groups, and (`before`) of those before one; each warp for itself.  (Cutting every unit into
-// equal pieces, one for a CTA, so that none ends one unit and begins another, measured no better: 16 units of
-// 128 tiles in 144 pieces 50 us, in 152 shares 45 to 55 us.)
-__device__ __forceinline__ int all_tiles(const AttnParams& p, const Plan& plan, int groups, int row_block,
+// Steps of all groups, and (`before`) of those before one; each warp for itself.
+__device__ __forceinline__ int all_steps(const AttnParams& p, const Plan& plan, int groups, int row_block,
                                          int before = 0, int* lead = nullptr) {
     const int lane = threadIdx.x & 31;
     int all = 0, first = 0;
     for (int g = lane; g < groups; g += 32) {
-        const int n = group_of(p, plan, g, row_block).tiles();
+        const int n = group_of(p, plan, g, row_block).steps();
         all += n;
         if (g < before) first += n;
     }
@@ -111,41 +120,48 @@ struct Walk {
         if (left > 0 && ++u == x.units) {
             u = 0;
             do ++g, x = group_of(p, plan, g, row_block);
-            while (x.tiles() == 0 && g + 1 < groups);
-            if (x.tiles() == 0) left = 0;   // (a plan that changed meanwhile: no endless walk)
+            while (x.steps() == 0 && g + 1 < groups);
+            if (x.steps() == 0) left = 0;   // (a plan that changed meanwhile: no endless walk)
         }
     }
     __device__ __forceinline__ int head() const { return u / x.n_rb; }
     __device__ __forceinline__ int row0(int row_block) const { return (u - head() * x.n_rb) * row_block; }
 };
-// The share of a CTA that starts at tile g0 and ends at g1 (g0 < g1).
+// The share of a CTA that starts at step g0 and ends at g1 (g0 < g1): its first tile, and how many.
 __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block, int g0,
                                           int g1) {
     const int lane = threadIdx.x & 31;
     Walk w{};
-    int carry = 0;
+    int carry = 0, tiles = 0;
+    bool found = false;
     for (int base = 0; base < groups; base += 32) {
         const int g = base + lane;
-        const int n = g < groups ? group_of(p, plan, g, row_block).tiles() : 0;
+        Group x{};
+        if (g < groups) x = group_of(p, plan, g, row_block);
+        const int n = x.steps();
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, d);
             if (lane >= d) sum += y;
         }
+        const int begin = carry + sum - n;   // of the lane's group
+        const int lo = max(g0, begin), hi = min(g1, carry + sum);
+        if (lo < hi) tiles += x.tiles_before(hi - begin) - x.tiles_before(lo - begin);
         const unsigned past = __ballot_sync(0xffffffffu, carry + sum > g0);
-        if (past) {
+        if (past && !found) {
             const int at = __ffs(past) - 1;
-            const int off = g0 - carry - __shfl_sync(0xffffffffu, sum - n, at);
+            const int off = g0 - __shfl_sync(0xffffffffu, begin, at);
             w.g = base + at;
             w.x = group_of(p, plan, w.g, row_block);
-            w.u = off / w.x.blocks;
-            w.v = off - w.u * w.x.blocks;
-            break;
+            w.u = off / w.x.unit_steps();
+            w.v = max(off - w.u * w.x.unit_steps() - kUnitSteps, 0);
+            found = true;
         }
         carry += __shfl_sync(0xffffffffu, sum, 31);
+        if (carry >= g1) break;
     }
-    w.left = g1 - g0;
+    w.left = __reduce_add_sync(0xffffffffu, tiles);
     return w;
 }
 
@@ -234,12 +250,13 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         return;
     }
     const int groups = granted && plan.ok(a.least_runs) ? plan.groups() : 0;
-    const int T = all_tiles(a, plan, groups, RB);
+    const int T = all_steps(a, plan, groups, RB);
     const Shares sh(T, a.ctas, kPreMinShare);
     const int cta = static_cast<int>(blockIdx.x);
     if (cta >= sh.n) return;   // nothing to wait for
-    const int g0 = sh.begin(cta), total = sh.begin(cta + 1) - g0;
-    Walk w = walk_from(a, plan, groups, RB, g0, g0 + total);
+    Walk w = walk_from(a, plan, groups, RB, sh.begin(cta), sh.begin(cta + 1));
+    const int total = w.left;
+    if (total <= 0) return;    // (the steps before a unit's first tile)
     auto next = [&](Walk& x) { x.next(a, plan, groups, RB); };
     auto active = [&](const Walk& x, int t) { return x.row0(RB) + t * kPreRows < x.x.rows; };
 
@@ -792,15 +809,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int g = real && groups > 0 ? plan.group(b) : -1;
     int d0 = 0, d1 = -1, second_pre = 0, r_pre = 0;
     int lead = 0;
-    const int T = all_tiles(a, plan, groups, row_block, g, &lead);
+    const int T = all_steps(a, plan, groups, row_block, g, &lead);
     if (g >= 0 && g < groups) {
         const Group x = group_of(a, plan, g, row_block);
         const int64_t r = static_cast<int64_t>(plan.rank(b)) * a.rows + rr;
         if (x.blocks > 0 && r >= 0 && r < x.rows) {
             const Shares sh(T, a.ctas, kPreMinShare);
-            const int first = lead + (h * x.n_rb + static_cast<int>(r / row_block)) * x.blocks;
-            d0 = sh.owner(first);
-            d1 = sh.owner(first + x.blocks - 1);
+            const int first = lead + (h * x.n_rb + static_cast<int>(r / row_block)) * x.unit_steps();
+            d0 = sh.owner(first + kUnitSteps);
+            d1 = sh.owner(first + kUnitSteps + x.blocks - 1);
             second_pre = first > sh.begin(d0) ? 1 : 0;
             r_pre = static_cast<int>(r % row_block);
         }
@@ -1156,9 +1173,9 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     if (rc != ATTN_OK) return rc;
     const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
     const int qt = prefix_tiles(B, rows), row_block = qt * kPreRows;
-    // tiles of all groups, and rows, are counted in 32 bits; B / 2 groups at most
+    // steps of all groups, and rows, are counted in 32 bits; B / 2 groups at most
     const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
-    if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + 1) > 0x7fffffffll ||
+    if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + kUnitSteps + 1) > 0x7fffffffll ||
         (static_cast<int64_t>(B) * Hkv * rows + kMergeWarps - 1) / kMergeWarps > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
     const SharedSizes z = shared_sizes(B, Hq, Hkv, Nq, D, p.a.ctas);
