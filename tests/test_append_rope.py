@@ -39,7 +39,7 @@ CALL = dict(k=P, v=P, kp=P, vp=P, ks=P, vs=P, table=P, lens=P, n_new=P, granted=
     ({"k": 0}, 1), ({"table": 0}, 1), ({"qo": 0}, 1), ({"q": 0}, 1), ({"Hq": 0}, 1), ({"turns": 0}, 1), ({"T": 0}, 1),
     ({"st": None}, 1), ({"rot": 65}, 1), ({"rot": 66}, 1), ({"inter": -1}, 1), ({"amp": -1.0}, 1), ({"dtype": 7}, 1),
     ({"D": 96}, 2), ({"page": 24}, 2), ({"B": 1 << 14, "T": 1 << 14, "page": 128, "max_pages": 1 << 10}, 2),
-    ({"q": P + 8}, 3), ({"granted": P + 2}, 3), ({"turns": P + 4}, 3), ({"vp": P + 4}, 3),
+    ({"T": (1 << 31) - 100}, 2), ({"q": P + 8}, 3), ({"granted": P + 2}, 3), ({"turns": P + 4}, 3), ({"vp": P + 4}, 3),
     ({"st": _strides(512, 256, 68, *ROWS, *ROWS)}, 3), ({"st": _strides(*ROWS, *ROWS, 512, 256, -64)}, 1),
     ({"qo": P, "st": _strides(*ROWS, *ROWS, 512, 128, 64)}, 1),
 ])

@@ -356,3 +356,21 @@ def test_rotated_training_step(cuda_lib):
     # rotated rows are rounded to bf16 twice over: a relative 2^-8 of each score's factors
     for a, b in zip(*res):
         assert float((a.double() - b.double()).norm() / b.double().norm()) < 4 * 2.0 ** -8
+
+
+@pytest.mark.gpu
+def test_a_first_use_is_not_captured(cuda_lib):
+    """The frequencies are copied to a device once: refused inside a capture, which goes on."""
+    rope, q = Rope(64), _rows((1, 2, 5, 64), F16, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="first use"):
+            rope(q)
+        twice = q * 2
+    graph.replay()
+    rope.turns("cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = rope(q)
+    graph.replay()
+    assert torch.equal(y, rope(q)) and torch.equal(twice, q * 2)

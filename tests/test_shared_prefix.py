@@ -447,6 +447,36 @@ def test_small_groups_are_left_alone(cuda_lib):
     assert plan[3].item() == (8 * 1024 + 2 * 4096) // RUN
 
 
+@pytest.mark.gpu
+def test_pools_past_32_bits(cuda_lib):
+    """Pages whose bytes start past 2^32: rotated prompts and steps, the plan and the attention against a
+    small pool that holds the same pages, byte for byte and bit for bit."""
+    Hkv, page, D, n_pages = 8, 64, 128, 70000
+    ids = [69999, 1, 68000, 69000, 20000, 69998, 5, 67777]
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(2, Hkv, 300, D, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.randn(2, 32, 3, D, generator=g).to(BF16).cuda()
+    rope, res = Rope(D), []
+    for n, at in ((n_pages, ids), (len(ids), list(range(len(ids))))):
+        pools = [torch.zeros(n, Hkv, page, D, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+        scales = [torch.ones(n, Hkv, device="cuda") for _ in range(2)]
+        # the second sequence's first four pages are the first one's, which has 297 positions of its own
+        table = _i32([*at[:6], *at[:4], *at[6:8]]).view(2, 6)
+        _lib.kv8_append(k, v, *pools, *scales, table, _i32([297, 0]), n_new=_i32([297, 0]), rope=rope)
+        _lib.kv8_append(k[:, :, :44].contiguous(), v[:, :, :44].contiguous(), *pools, *scales, table, _i32([297, 300]),
+                        n_new=_i32([0, 44]), rope=rope)
+        turned = _lib.kv8_append(k[:, :, :3], v[:, :, :3], *pools, *scales, table, _i32([300, 301]),
+                                 n_new=_i32([3, 1]), rope=rope, q=q)
+        plan = _lib.kvp_find_shared(table, _i32([300, 301]), page, 0)
+        assert _read_plan(plan, 2) == {0: ([0, 1], 2)}
+        out = _lib.kv8_attn_shared(turned, *pools, *scales, table, _i32([300, 301]), plan, n_new=_i32([3, 1]))
+        assert _lib.sync_status() == _lib.ATTN_OK
+        res.append([turned, *out, *(p.view(torch.uint8)[at].clone() for p in pools), *(s[at].clone() for s in scales)])
+        del pools, scales
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert bool(res[0][1][1, :, 0].any()) and bool(res[0][3].any())
+
+
 # ------------------------------------------------------------------ the cache that shares
 
 def test_a_cache_with_a_window_does_not_share():

@@ -612,7 +612,8 @@ cudaError_t launch_prompt(AppendRopeParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // heads in turn as long as every SM still has some CTAs
     const int64_t pages = static_cast<int64_t>(p.B) * p.n_slots * 2;
-    const int64_t most = (static_cast<int64_t>(device_sms()) * kPromptCtas + pages - 1) / pages;   // CTAs of a page
+    int64_t most = (static_cast<int64_t>(device_sms()) * kPromptCtas + pages - 1) / pages;   // CTAs of a page
+    if (most < 1) most = 1;
     p.heads = most >= p.Hkv ? 1 : static_cast<int>((p.Hkv + most - 1) / most);
     const int64_t ctas = pages * ((p.Hkv + p.heads - 1) / p.heads);
     const int pitch = (p.f.rot / 2 + 7) & ~7;
@@ -704,6 +705,8 @@ extern "C" int kv8_append_rope(const void* k, const void* v, void* k_pages, void
     const void* ptrs[] = {k, v, k_pages, v_pages, q, q_out};
     const void* words[] = {k_scale, v_scale, table, lens, n_new, granted};
     if (!aligned(ptrs, 16) || !aligned(words, 4)) return ATTN_ERR_ALIGN;
+    // positions past the last one that a sequence's pages could take are 32-bit, too
+    if (static_cast<int64_t>(T) + static_cast<int64_t>(max_pages) * page + 2 * page > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     const int64_t slots = (static_cast<int64_t>(T) + page - 2) / page + 1;
     if (slots * B * Hkv * 2 > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     // the queries' CTAs come on top, fewer than one per 16 of their rows
