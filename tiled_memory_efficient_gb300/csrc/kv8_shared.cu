@@ -205,8 +205,7 @@ __device__ __forceinline__ uint4 lds128v(uint32_t a) {
 // it), swizzled as TMA would have written them.  The value scale that the accumulator stands at
 // only grows within a unit, by whole tiles, and joins the softmax's rescale.  A part of a unit ends in fp32
 // rows with their LSE, for kv8_shared_merge_kernel.
-//   warps 0 .. 4 QT - 1   softmax, a thread per row: two passes over S in TMEM (maximum, then
-//                         exponentials), P over S as fp16
+//   warps 0 .. 4 QT - 1   softmax, a thread per row: one pass over S in TMEM, P over S as fp16
 //   then 4 warps          converters
 //   then 1 warp           tcgen05.mma issue: QT = 2 PV_0, S_0', PV_1, S_1', so that one tile's softmax
 //                         runs beside the other's products; QT = 1 two S buffers, S' before PV
