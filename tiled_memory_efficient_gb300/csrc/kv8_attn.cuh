@@ -166,11 +166,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * ST;   // this warp's slots
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff) + warp;
     int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 4 * kWarps);   // [kWarps]
+    int* s_held = reinterpret_cast<int*>(smem + C::kLseOff);          // ALONE (it has no use for s_lse): [kWarps]
     int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
     int* s_len = s_pre + p.B + 1;                                     // [B]
     int* s_nq = s_len + p.B;                                          // [B] queries
     int* s_start = s_nq + p.B;                                        // SHARED: [B] positions of the prefix
     auto start_of = [&](int b_) { return SHARED ? s_start[b_] : 0; };
+    // ALONE (up to 16 queries): beside them how many sequences before hold tiles
+    auto queries = [&](int b_) { return ALONE ? (s_nq[b_] & 255) - 1 : s_nq[b_]; };
 
     if (lane == 0) {
         // a slot's phase: its copies' bytes, and its lane's small copies
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     // exclusive prefix sums of the sequences' tile counts
     const bool granted = step_granted(p);
-    int carry = 0;
+    int carry = 0, held = 0;   // tiles, ALONE: sequences with any
     for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
         int len = 0, nq = 0, start = 0;
@@ -212,6 +215,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (lane >= d) x += y;
         }
         if (lane == 31) s_warp[warp] = x;
+        int z = 0;   // ALONE: sequences before in the turn that hold tiles
+        if constexpr (ALONE) {
+            const unsigned any = __ballot_sync(0xffffffffu, n > 0);
+            z = __popc(any & ((1u << lane) - 1u));
+            if (lane == 0) s_held[warp] = __popc(any);
+        }
         __syncthreads();
         int before = carry, all = carry;
 #pragma unroll
@@ -219,10 +228,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (i < warp) before += s_warp[i];
             all += s_warp[i];
         }
+        if constexpr (ALONE) {
+            z += held;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                if (i < warp) z += s_held[i];
+                held += s_held[i];
+            }
+        }
         if (b < p.B) {
             s_pre[b] = before + x - n;
             s_len[b] = len;
-            s_nq[b] = nq;
+            s_nq[b] = ALONE ? (nq + 1) | (z << 8) : nq;
             if constexpr (SHARED) s_start[b] = start;
         }
         carry = all;
@@ -231,14 +248,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (threadIdx.x == 0) s_pre[p.B] = carry;
     __syncthreads();
     const int U = p.Hkv * p.n_rb;
-    const Shares sh = ALONE ? own_shares(p, carry * U) : Shares(carry * U, p.ctas);
+    const Shares sh = ALONE ? own_shares(p, (carry + kOwnSteps * held) * U) : Shares(carry * U, p.ctas);
     // (consecutive shares of warps on different SMs)
     const int c = static_cast<int>(blockIdx.x) + (ALONE ? warp * p.ctas : 0);
-    if (c >= sh.n) {   // nothing in flight, no barrier left
+    // ALONE: the tile that step x of the concatenated units leads to; its sequence, KV head and place in its
+    // list.  Two probes a lane (at most 1024 sequences).
+    auto tile_at = [&](int x, int* b_, int* u_, int* v_) {
+        auto steps = [&](int i) { return (s_pre[i] + kOwnSteps * (s_nq[i] >> 8)) * U; };
+        const int gap = (p.B + 31) >> 5, i = lane * gap;
+        const int base = (__popc(__ballot_sync(0xffffffffu, i < p.B && steps(min(i, p.B - 1)) <= x)) - 1) * gap;
+        const int k = base + lane;
+        *b_ = base - 1 +
+              __popc(__ballot_sync(0xffffffffu, lane < gap && k < p.B && steps(min(k, p.B - 1)) <= x));
+        const int n = s_pre[*b_ + 1] - s_pre[*b_], off = x - steps(*b_);
+        *u_ = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(n + kOwnSteps));
+        *v_ = max(off - *u_ * (n + kOwnSteps) - kOwnSteps, 0);
+        return s_pre[*b_] * U + *u_ * n + *v_;
+    };
+    int g0 = 0, g1 = 0, b = 0, u = 0, v_first = 0;
+    if (c < sh.n) {
+        g0 = sh.begin(c), g1 = sh.begin(c + 1);
+        if constexpr (ALONE) {
+            int b1, u1, v1;
+            g1 = c + 1 < sh.n ? tile_at(g1, &b1, &u1, &v1) : carry * U;
+            g0 = tile_at(g0, &b, &u, &v_first);
+        }
+    }
+    if (g0 >= g1) {   // nothing in flight, no barrier left
         if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    const int g0 = sh.begin(c), g1 = sh.begin(c + 1);
 
     // KV head of a unit (unit = head * n_rb + row block; one block, as a rule)
     auto head_of = [&](int u_) { return p.n_rb == 1 ? u_ : u_ / p.n_rb; };
@@ -251,15 +290,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // largest exactly.  They stay in registers, or (kQSmem) warp w prepares the 8
     // rows w and leaves them in shared memory as [row tile][word pair][lane], and
     // the factors behind them.
-    int b = 0;   // the last sequence that starts at or before g0: not an empty one
-    for (int hi = p.B - 1; b < hi;) {
-        const int mid = (b + hi + 1) >> 1;
-        if (s_pre[mid] * U <= g0) b = mid;
-        else hi = mid - 1;
+    if constexpr (!ALONE) {
+        // the last sequence that starts at or before g0: not an empty one
+        for (int hi = p.B - 1; b < hi;) {
+            const int mid = (b + hi + 1) >> 1;
+            if (s_pre[mid] * U <= g0) b = mid;
+            else hi = mid - 1;
+        }
+        const int n_first = s_pre[b + 1] - s_pre[b];
+        u = static_cast<int>(static_cast<unsigned>(g0 - s_pre[b] * U) / static_cast<unsigned>(n_first));
+        v_first = g0 - s_pre[b] * U - u * n_first;
     }
-    const int n_first = s_pre[b + 1] - s_pre[b];
-    int u = static_cast<int>(static_cast<unsigned>(g0 - s_pre[b] * U) / static_cast<unsigned>(n_first));
-    const int v_first = g0 - s_pre[b] * U - u * n_first;
     int unit0 = g0 - v_first;   // the unit's first tile in the concatenated lists
     constexpr int QN = C::kQSmem ? 1 : NR;
     uint32_t qf[QN][KC][8];
@@ -353,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int ntok = 0, nseen = 0;                    // its first token; boxes some query sees
     int issued = 0;
     auto enter = [&]() {   // a new sequence
-        const Seq x = seq_of(p, s_len[nb], s_nq[nb], start_of(nb));
+        const Seq x = seq_of(p, s_len[nb], queries(nb), start_of(nb));
         nn = x.n;
         n_sink = x.n_sink;
         n_skip = x.skip;
@@ -481,7 +522,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int slot = 0;               // of that tile
     uint32_t phase = 0;         // and its turn of the ring
     while (unit0 < g1) {
-        const Seq s = seq_of(p, s_len[b], s_nq[b], start_of(b));
+        const Seq s = seq_of(p, s_len[b], queries(b), start_of(b));
         const bool joins = start_of(b) > 0;   // the rows join a shared prefix's
         const int h = head_of(u), row0 = (u - h * p.n_rb) * (8 * NR);
         const int unit1 = unit0 + s.n, end = min(unit1, g1);

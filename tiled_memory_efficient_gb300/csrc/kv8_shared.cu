@@ -782,12 +782,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const Plan plan(a.plan, a.B);
     const bool granted = step_granted(a), planned = plan.ok(a.least_runs);
     // own positions: the tiles of all sequences, and of those before b
-    int all = 0, before = 0, n = 0;
+    int all = 0, before = 0, n = 0;   // (of units: their first steps, too)
+    const int K = own_steps(a.rows);
     for (int i = lane; i < a.B; i += 32) {
         const int len = a.lens[i];
         const int k = seq_of(a, len, queries_of(a, granted, i, len), planned ? plan.start(i) : 0).n;
-        all += k;
-        if (i < b) before += k;
+        const int steps = k > 0 ? k + K : 0;
+        all += steps;
+        if (i < b) before += steps;
         if (i == b) n = k;
     }
     all = __reduce_add_sync(0xffffffffu, all);
@@ -797,9 +799,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     int c0 = 0, c1 = -1, second = 0, r_own = 0;
     if (n > 0) {
         const Shares sh = own_shares(a, all * U);
-        const int first = before * U + (h * a.n_rb + rr / row8) * n;
-        c0 = sh.owner(first);
-        c1 = sh.owner(first + n - 1);
+        const int first = before * U + (h * a.n_rb + rr / row8) * (n + K);
+        c0 = sh.owner(first + K);
+        c1 = sh.owner(first + K + n - 1);
         second = first > sh.begin(c0) ? 1 : 0;
         r_own = rr % row8;
     }
@@ -1174,6 +1176,8 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     const int qt = prefix_tiles(B, rows), row_block = qt * kPreRows;
     // steps of all groups, and rows, are counted in 32 bits; B / 2 groups at most
     const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
+    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(max_pages) * page + 31) / 32 + kOwnSteps) > 0x7fffffffll)
+        return ATTN_ERR_UNSUPPORTED;
     if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + kUnitSteps + 1) > 0x7fffffffll ||
         (static_cast<int64_t>(B) * Hkv * rows + kMergeWarps - 1) / kMergeWarps > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
