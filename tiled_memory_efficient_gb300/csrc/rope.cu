@@ -293,16 +293,26 @@ __device__ __forceinline__ uint2 quantise8(const float (&y)[8], float inv) {
 }
 
 // Prompts: one CTA per (sequence, page it may touch, keys or values), `heads` KV heads in turn.  A thread
-// holds two rows' items (rope_item's, the two halves of each pair in one thread), and asks for the next
-// head's before this one's scale is known.  The page's sines are made once for all of the CTA's heads:
+// holds two rows' items (rope_item's, the two halves of each pair in one thread); the next two heads' are
+// on their way to shared memory meanwhile.  The page's sines are made once for all of the CTA's heads:
 // each pair's exactly at every eighth token, the others by turning those by one token up to four times (off
-// by less than 2^-21; all made exactly, a prompt's append took 42 us instead of 20 with the layout it had).
+// by less than 2^-21).  2 x 8190 tokens, 8 KV heads, D = 128, 67 MB read and 34 written: 20.3 us (21.9
+// with one head ahead in registers, 23.1 with four ahead; in 64 registers a thread 21.4), bound by each
+// head's chain of turn, maximum, barrier, scale and store in three CTAs an SM; the plain append, without
+// sines, takes 15.6.
 template <int D>
 constexpr int prompt_threads(int page) { return page * (D / 32); }
-// CTAs of an SM up to which a page's heads are cut: 4 and 8 give 66.3 us, 12 67.0, 24 71.7 (the sines are made
-// once a CTA) for 2 x 8190 tokens, 8 KV heads, 32 query heads, D = 128.
+// CTAs of an SM up to which a page's heads are cut (the sines are made once a CTA): 8 take 21.6 us there.
 constexpr int kPromptCtas = 4;
 constexpr int kPromptThreads = 512;   // at most: pages of 128 tokens, D = 128
+constexpr int kPromptAhead = 2;       // heads on their way, a power of two
+
+// 16 bytes global -> shared, asynchronously; 0 instead if not `real`.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(real ? 16 : 0)
+                 : "memory");
+}
 
 // Largest finite magnitude of a thread's values: an infinity sends it to the slow look.
 __device__ __forceinline__ float item_max(const float (&y)[2][16]) {
@@ -352,34 +362,28 @@ __global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ A
     bool fresh[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) fresh[i] = t.t0 + tok + i * step >= t.lo && t.t0 + tok + i * step < t.hi;
-    uint4 next[2][2];
-    auto load = [&](int h) {
+    // A thread's vectors of a head travel into shared memory that it alone reads (0 where a token is not new);
+    // MODE 2's keys are read element by element where they are used.
+    const bool copies = MODE != kRopeScalar || !keys;
+    const int pitch = (half + 7) & ~7;
+    float* s_sin = s_cos + (pitch << p.page_shift);
+    uint4* s_raw = reinterpret_cast<uint4*>(s_sin + (pitch << p.page_shift)) + threadIdx.x;
+    auto ask = [&](int h) {
+        if (copies && h < h1) {
+            uint4* to = s_raw + (h & (kPromptAhead - 1)) * 4 * blockDim.x;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            next[i][0] = next[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (!fresh[i]) continue;
-            const uint16_t* row = src + h * p.sh + i * step * p.st;
-            if (MODE == kRopeScalar && keys) {
-                uint32_t w[2][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[0][j] = row[first(2 * j)] | static_cast<uint32_t>(row[first(2 * j + 1)]) << 16;
-                    w[1][j] = row[second(2 * j)] | static_cast<uint32_t>(row[second(2 * j + 1)]) << 16;
-                }
-                next[i][0] = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
-                next[i][1] = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
-            } else {
-                next[i][0] = __ldcs(reinterpret_cast<const uint4*>(row + d0));
-                next[i][1] = __ldcs(reinterpret_cast<const uint4*>(row + d1));
+            for (int i = 0; i < 2; ++i) {
+                const uint16_t* row = fresh[i] ? src + h * p.sh + i * step * p.st : p.src[which];
+                copy16(to + (2 * i) * blockDim.x, row + (fresh[i] ? d0 : 0), fresh[i]);
+                copy16(to + (2 * i + 1) * blockDim.x, row + (fresh[i] ? d1 : 0), fresh[i]);
             }
         }
+        cp_async_commit();
     };
-    load(h0);
+    for (int i = 0; i < kPromptAhead; ++i) ask(h0 + i);
     // Pairs of a token's row of sines: in eights (an item's), whose first fours come before all second
     // fours, so that a token's items read whole lines; past the last pair a turn by nothing.
-    const int pitch = (half + 7) & ~7;
     auto place = [&](int pair) { return ((pair >> 2) & 1) * (pitch >> 1) + (pair >> 3) * 4 + (pair & 3); };
-    float* s_sin = s_cos + (pitch << p.page_shift);
     if (keys) {
         for (int i = threadIdx.x; i < pitch * (page / 8); i += blockDim.x) {
             const int run = i / pitch, pair = i - run * pitch;
@@ -407,11 +411,24 @@ __global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ A
     }
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kPromptAhead - 1) : "memory");   // this head's are there
         float y[2][16];   // the items' first vectors, then their second ones
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t w[8] = {next[i][0].x, next[i][0].y, next[i][0].z, next[i][0].w,
-                                   next[i][1].x, next[i][1].y, next[i][1].z, next[i][1].w};
+            uint32_t w[8];
+            if (copies) {
+                const uint4* from = s_raw + ((h & (kPromptAhead - 1)) * 4 + 2 * i) * blockDim.x;
+                const uint4 lo = from[0], hi = from[blockDim.x];
+                w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+                w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+            } else {
+                const uint16_t* row = src + h * p.sh + i * step * p.st;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = fresh[i] ? row[first(2 * j)] | static_cast<uint32_t>(row[first(2 * j + 1)]) << 16 : 0u;
+                    w[4 + j] = fresh[i] ? row[second(2 * j)] | static_cast<uint32_t>(row[second(2 * j + 1)]) << 16 : 0u;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 e = rope_unpack<BF16>(w[j]);
@@ -419,7 +436,7 @@ __global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ A
                 y[i][2 * j + 1] = e.y;
             }
         }
-        if (h + 1 < h1) load(h + 1);
+        ask(h + kPromptAhead);
         if (turns) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -608,7 +625,8 @@ template <int D, bool BF16, int MODE>
 cudaError_t launch_prompt(AppendRopeParams p, cudaStream_t stream) {
     auto kern = kv8_append_rope_kernel<D, BF16, MODE>;
     static SmemLimit limit;
-    const cudaError_t e = limit.raise(kern, 128 * D * static_cast<int>(sizeof(float)));
+    // a page's cosines and sines, and the heads ahead: at most
+    const cudaError_t e = limit.raise(kern, 128 * D * static_cast<int>(sizeof(float)) + kPromptAhead * 64 * prompt_threads<D>(128));
     if (e != cudaSuccess) return e;
     // heads in turn as long as every SM still has some CTAs
     const int64_t pages = static_cast<int64_t>(p.B) * p.n_slots * 2;
@@ -617,8 +635,9 @@ cudaError_t launch_prompt(AppendRopeParams p, cudaStream_t stream) {
     p.heads = most >= p.Hkv ? 1 : static_cast<int>((p.Hkv + most - 1) / most);
     const int64_t ctas = pages * ((p.Hkv + p.heads - 1) / p.heads);
     const int pitch = (p.f.rot / 2 + 7) & ~7;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(prompt_threads<D>(1 << p.page_shift)),
-                         (sizeof(float) * 2 * pitch) << p.page_shift, stream, p);
+    const int threads = prompt_threads<D>(1 << p.page_shift);
+    const size_t smem = ((sizeof(float) * 2 * pitch) << p.page_shift) + kPromptAhead * 64 * threads;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, stream, p);
 }
 template <int D, bool BF16>
 cudaError_t launch_prompt(const AppendRopeParams& p, cudaStream_t stream) {
