@@ -570,3 +570,43 @@ def test_a_run_of_samples(cuda_lib, D, page, rot, inter, dtype):
     replay("no group")
     fork([-1] * S)
     assert not cache.refs.any() and _read_plan(cache.plan, S) == {}
+
+
+@pytest.mark.gpu
+def test_a_captured_fork(cuda_lib):
+    """reassign with its search for prefixes captured, and steps without counts behind it; a cache of one
+    sequence shares with nobody."""
+    S, Hq, Hkv, D, page, prompt = 9, 3, 1, 64, 16, 1050
+    g = torch.Generator().manual_seed(2)
+    cache = PagedKVCache(1, S, Hkv, D, n_pages=3 * prompt // page + 2 * S, page_size=page, max_pages=prompt // page + 3,
+                         share=True, min_saved=1024)
+    k, v = (torch.randn(S, Hkv, prompt, D, generator=g).to(F16).cuda() for _ in range(2))
+    q = torch.randn(S, Hq, 1, D, generator=g).to(F16).cuda()
+    n, parents = _i32([prompt, prompt] + [0] * (S - 2)), _i32(range(S))
+    cache.reserve(n)
+    cache.append(0, k, v, n)
+    cache.reassign(parents)                     # (the calls' first use is not captured)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.reassign(parents)
+    for fork, want in (([0] * 4 + [1] * 5, [(1024, 4), (1024, 5)]), ([0] * 2 + [8] * 7, [(1024, 2), (1024, 7)]),
+                       ([8] * S, [(1024, S)])):
+        parents.copy_(torch.tensor(fork))
+        graph.replay()
+        assert sorted((d * RUN, len(m)) for m, d in _read_plan(cache.plan, S).values()) == want
+        cache.reserve(1)
+        cache.append(0, k[:, :, :1].contiguous(), v[:, :, :1].contiguous())
+        out, lse = cache.attend(0, q)
+        assert _lib.sync_status() == _lib.ATTN_OK
+        held = [t[0].cpu() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+        _check(q.cpu(), (*held, cache.table.cpu(), cache.lens.cpu()), None, out, lse, f"fork {fork}", some=(0, 4, 8))
+    alone = PagedKVCache(1, 1, Hkv, D, n_pages=70, page_size=page, share=True, min_saved=0)
+    alone.reserve(prompt)
+    alone.append(0, k[:1], v[:1])
+    alone.find_shared()
+    assert _read_plan(alone.plan, 1) == {}
+    out, lse = alone.attend(0, q[:1])
+    want = _lib.kv8_attn(q[:1], alone.k_pages[0], alone.v_pages[0], alone.k_scale[0], alone.v_scale[0], alone.table,
+                         alone.lens)
+    helpers.assert_fwd_close(*(t.double().cpu().numpy() for t in (out, lse, *want)), F16, "one sequence")
+    assert _lib.sync_status() == _lib.ATTN_OK
