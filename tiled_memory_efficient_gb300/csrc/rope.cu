@@ -56,6 +56,10 @@ template <int D, bool BF16, int MODE>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int items = D / 16, kItemShift = D == 128 ? 3 : 2;
     __shared__ __align__(16) float s_cos[kRopeThreads * 8], s_sin[kRopeThreads * 8];   // [token][place of pair]
+    // What was before is complete from here on; what is behind may set up.  (Behind an append's prompts, which
+    // did the same before they let this one start: they are waited for at the end.)
+    if (!p.lens) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int item = static_cast<int>(threadIdx.x) & (items - 1);
     const int tl = (static_cast<int>(threadIdx.x) >> kItemShift) & ((1 << p.tok_shift) - 1);
     const int hg = static_cast<int>(threadIdx.x) >> (kItemShift + p.tok_shift);   // the thread's first head
@@ -109,8 +113,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
     };
     const int end = inside ? min(first + p.per_thread * step, p.heads) : 0;
     rope_item<BF16, MODE>(p.f, t, item, items, first + hg, step, end, live, sines);
-    // behind an append's prompts: it started before they were done, and ends only after them
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.lens) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Tokens and heads of a CTA: heads a thread as many as leave every SM two CTAs; tokens so that the heads
@@ -147,7 +150,7 @@ cudaError_t launch_rope(RopeParams p, cudaStream_t stream) {
     void (*kern)(RopeParams) = p.f.mode == kRopeHalf    ? rope_kernel<D, BF16, kRopeHalf>
                                : p.f.mode == kRopeInter ? rope_kernel<D, BF16, kRopeInter>
                                                         : rope_kernel<D, BF16, kRopeScalar>;
-    return p.lens ? launch_dependent(kern, grid, block, 0, stream, p) : launch_kernel(kern, grid, block, 0, stream, p);
+    return launch_dependent(kern, grid, block, 0, stream, p);
 }
 cudaError_t launch_rope(const RopeParams& p, int D, bool bf16, cudaStream_t stream) {
     if (D == 128) return bf16 ? launch_rope<128, true>(p, stream) : launch_rope<128, false>(p, stream);
@@ -335,6 +338,7 @@ __global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ A
     constexpr int items = D / 16;
     extern __shared__ __align__(16) float s_cos[];   // [token][pitch] of the page, then the sines
     __shared__ uint32_t s_max[2][kPromptThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");   // what is behind may set up meanwhile
     int id = static_cast<int>(blockIdx.x);
     const int which = id & 1;
@@ -518,6 +522,7 @@ constexpr int step_tokens() { return 4 * (32 / (D / 8)); }   // tokens a warp ho
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kStepThreads) kv8_step_rope_kernel(const __grid_constant__ AppendRopeParams p) {
     constexpr int VPT = D / 8, TPI = 32 / VPT, items = D / 16;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");   // the attention may set up meanwhile
     if (static_cast<int>(blockIdx.x) >= p.page_ctas) {
         // queries
@@ -618,7 +623,7 @@ cudaError_t launch_step(AppendRopeParams p, cudaStream_t stream) {
         const int64_t parts = (p.Hq + p.q_chunk - 1) / p.q_chunk;
         ctas += (parts * p.q_threads + kStepThreads - 1) / kStepThreads;
     }
-    return launch_kernel(kv8_step_rope_kernel<D, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(kStepThreads), 0, stream, p);
+    return launch_dependent(kv8_step_rope_kernel<D, BF16>, dim3(static_cast<unsigned>(ctas)), dim3(kStepThreads), 0, stream, p);
 }
 
 template <int D, bool BF16, int MODE>
@@ -637,7 +642,7 @@ cudaError_t launch_prompt(AppendRopeParams p, cudaStream_t stream) {
     const int pitch = (p.f.rot / 2 + 7) & ~7;
     const int threads = prompt_threads<D>(1 << p.page_shift);
     const size_t smem = ((sizeof(float) * 2 * pitch) << p.page_shift) + kPromptAhead * 64 * threads;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem, stream, p);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), static_cast<int>(smem), stream, p);
 }
 template <int D, bool BF16>
 cudaError_t launch_prompt(const AppendRopeParams& p, cudaStream_t stream) {
