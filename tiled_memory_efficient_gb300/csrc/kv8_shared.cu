@@ -93,13 +93,14 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, const Plan& plan,
     x.units = p.Hkv * x.n_rb;
     return x;
 }
-// Steps of all groups, and (`before`) of those before one; each warp for itself.
+// Steps of all groups, and (`before`) of those before one; each warp for itself.  `mine`: group `lane`, asked for
+// with the header.
 __device__ __forceinline__ int all_steps(const AttnParams& p, const Plan& plan, int groups, int row_block,
-                                         int before = 0, int* lead = nullptr) {
+                                         const Group& mine, int before = 0, int* lead = nullptr) {
     const int lane = threadIdx.x & 31;
     int all = 0, first = 0;
     for (int g = lane; g < groups; g += 32) {
-        const int n = group_of(p, plan, g, row_block).steps();
+        const int n = (g == lane ? mine : group_of(p, plan, g, row_block)).steps();
         all += n;
         if (g < before) first += n;
     }
@@ -128,8 +129,8 @@ struct Walk {
     __device__ __forceinline__ int row0(int row_block) const { return (u - head() * x.n_rb) * row_block; }
 };
 // The share of a CTA that starts at step g0 and ends at g1 (g0 < g1): its first tile, and how many.
-__device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block, int g0,
-                                          int g1) {
+__device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan, int groups, int row_block,
+                                          const Group& mine, int g0, int g1) {
     const int lane = threadIdx.x & 31;
     Walk w{};
     int carry = 0, tiles = 0;
@@ -137,7 +138,7 @@ __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan,
     for (int base = 0; base < groups; base += 32) {
         const int g = base + lane;
         Group x{};
-        if (g < groups) x = group_of(p, plan, g, row_block);
+        if (g < groups) x = base == 0 ? mine : group_of(p, plan, g, row_block);
         const int n = x.steps();
         int sum = n;
 #pragma unroll
@@ -153,7 +154,10 @@ __device__ __forceinline__ Walk walk_from(const AttnParams& p, const Plan& plan,
             const int at = __ffs(past) - 1;
             const int off = g0 - __shfl_sync(0xffffffffu, begin, at);
             w.g = base + at;
-            w.x = group_of(p, plan, w.g, row_block);
+            w.x.blocks = __shfl_sync(0xffffffffu, x.blocks, at);
+            w.x.n_rb = __shfl_sync(0xffffffffu, x.n_rb, at);
+            w.x.units = __shfl_sync(0xffffffffu, x.units, at);
+            w.x.rows = __shfl_sync(0xffffffffu, x.rows, at);
             w.u = off / w.x.unit_steps();
             w.v = max(off - w.u * w.x.unit_steps() - kUnitSteps, 0);
             found = true;
@@ -243,23 +247,24 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const Plan plan(a.plan, a.B);
+    const Group mine = group_of(a, plan, min(lane, a.B - 1), RB);   // (asked for beside the header)
     const bool granted = step_granted(a);
     if (!plan.ok()) {   // the sequences are then each for itself
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusPage);
         return;
     }
     const int groups = granted && plan.ok(a.least_runs) ? plan.groups() : 0;
-    const int T = all_steps(a, plan, groups, RB);
+    const int T = all_steps(a, plan, groups, RB, mine);
     const Shares sh(T, a.ctas, kPreMinShare);
     const int cta = static_cast<int>(blockIdx.x);
     if (cta >= sh.n) return;   // nothing to wait for
-    Walk w = walk_from(a, plan, groups, RB, sh.begin(cta), sh.begin(cta + 1));
+    Walk w = walk_from(a, plan, groups, RB, mine, sh.begin(cta), sh.begin(cta + 1));
     const int total = w.left;
     if (total <= 0) return;    // (the steps before a unit's first tile)
     auto next = [&](Walk& x) { x.next(a, plan, groups, RB); };
     auto active = [&](const Walk& x, int t) { return x.row0(RB) + t * kPreRows < x.x.rows; };
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == C::kConvWarp * 32) {
         for (int i = 0; i < RS; ++i) {
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], 4);
@@ -282,15 +287,20 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    // Each role looks up what it can before the barriers and TMEM are there, and comes here once.
+    uint32_t tmem = 0;
+    auto ready = [&]() {
+        tc_fence_before();
+        asm volatile("bar.sync 0;" ::: "memory");
+        tc_fence_after();
+        tmem = *tmem_slot;
+    };
 
     // Every wait is bounded: one that gives up sets the abort flag, at which all others return
     // at once, so each role's loops run to their end (or leave) without blocking.
     if (warp < C::kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax
+        ready();
         const int t = warp >> 2, quad = warp & 3;
         const int rl = quad * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
@@ -534,6 +544,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         }
     } else if (warp < C::kMmaWarp) {
         // ------------------------------------------------------------ converters
+        ready();
         const int ct = threadIdx.x - C::kConvWarp * 32;
         constexpr int KB = D / 64;                // column blocks of an fp16 tile
         // 8 lanes hold chunks 0 .. 3 of a column block in two neighbouring rows (D = 128: of block a in the even
@@ -593,6 +604,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         }
     } else if (warp == C::kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
+        ready();
         constexpr uint32_t idesc_s = idesc_f16(kPreRows, kPreRows, false, false);
         constexpr uint32_t idesc_o = idesc_f16(kPreRows, D, false, true);
         constexpr uint64_t kTileStep = C::kTile16 >> 4, kBlk = (kPreRows * 128) >> 4;
@@ -693,6 +705,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
         };
         Page now = fetch(), soon = fetch();
         scales(now);
+        ready();
         int issued = 0;   // raw tiles, K and V in turn
         int ev = -1000;   // value scale of the accumulator: none yet
         for (int x = 0; x < total; ++x) {
@@ -780,6 +793,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int u = real ? static_cast<int>(row / a.rows) : 0;   // (sequence, KV head)
     const int b = u / a.Hkv, h = u - b * a.Hkv, rr = static_cast<int>(row - static_cast<int64_t>(u) * a.rows);
     const Plan plan(a.plan, a.B);
+    const Group mine = group_of(a, plan, min(lane, a.B - 1), row_block);
     const bool granted = step_granted(a), planned = plan.ok(a.least_runs);
     // own positions: the tiles of all sequences, and of those before b
     int all = 0, before = 0, n = 0;   // (of units: their first steps, too)
@@ -810,7 +824,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int g = real && groups > 0 ? plan.group(b) : -1;
     int d0 = 0, d1 = -1, second_pre = 0, r_pre = 0;
     int lead = 0;
-    const int T = all_steps(a, plan, groups, row_block, g, &lead);
+    const int T = all_steps(a, plan, groups, row_block, mine, g, &lead);
     if (g >= 0 && g < groups) {
         const Group x = group_of(a, plan, g, row_block);
         const int64_t r = static_cast<int64_t>(plan.rank(b)) * a.rows + rr;
