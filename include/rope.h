@@ -52,7 +52,8 @@ int rope_apply(const void* q, const void* k, void* q_out, void* k_out,
  * into q_out (which may be q); rows from n_new[b] on, and all rows of a sequence whose
  * count does not fit or of a step without room, become 0.
  *
- * strides (host): batch, head and row strides of k and v (both), of q and of q_out.
+ * strides (host): batch, head and row strides of k and v (both), of q and of q_out.  T and the
+ * positions of a table row together stay below 2^31.
  */
 int kv8_append_rope(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale,
                     float* v_scale, const int* table, const int* lens, const int* n_new,
