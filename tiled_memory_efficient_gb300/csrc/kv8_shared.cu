@@ -214,6 +214,11 @@ __device__ __forceinline__ uint4 lds128v(uint32_t a) {
 //   then 1 warp           tcgen05.mma issue: QT = 2 PV_0, S_0', PV_1, S_1', so that one tile's softmax
 //                         runs beside the other's products; QT = 1 two S buffers, S' before PV
 //   then 1 warp           producer: page ids, scales, bulk copies
+// Bound by a tile's chain, scores, softmax, product, of which two are in flight: at D = 128 3750 cycles a step of
+// 128 keys and 256 rows, where the products take 2048 (D = 64: 3300 and 1024), and by both ends of a part: 6 to 9
+// us until the first scores, 3 to 4 for its rows.  128 sequences, 32:8 heads, D = 128 under 16K positions 38 us,
+// the tensor pipe 31% and issue slots 41% busy; 64 samples, 14:2 heads, D = 64 under 32K 17 to 20 us.  Two Q
+// tiles a CTA (QT) take those 51.5 us instead of 62.5 with one, and 25 instead of 29, in an earlier state of both.
 template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
     kv8_prefix_kernel(const __grid_constant__ PreParams p) {
@@ -778,7 +783,8 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
 
 // A warp per row, or (WPR) a CTA's four: the row's results over the prefix and over its own positions, each
 // whole or in the parts that several CTAs left.  Rows of sequences that share nothing and lie in
-// one CTA are written already.
+// one CTA are written already.  It finds its parts beside the kernels before it; behind them a row is two trips to
+// memory: 2.5 us for 896 rows of some 40 parts, 5 for 4096 rows of 10 (22 MB from L2).
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRowsAlone = 8;   // rows per SM up to which a CTA takes one
 
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         const bool own = run == 0, whole = own ? own_whole : pre_whole;
         const int n_run = own ? c1 - c0 + 1 : d1 - d0 + 1, step = 2 * (own ? row8 : row_block);
         const int add = whole ? 0 : own ? second * row8 : second_pre * row_block;
-        const int64_t at = whole ? row : own ? static_cast<int64_t>(c0) * step + r_own : static_cast<int64_t>(d0) * step + r_pre;
+        const int64_t at = whole ? row : static_cast<int64_t>(own ? c0 : d0) * step + (own ? r_own : r_pre);
         const float* l = (own ? (whole ? a.own_lse : a.part_lse) : (whole ? p.row_lse : p.part_lse)) + at;
         const float* o = (own ? (whole ? a.own_o : a.part_o) : (whole ? p.row_o : p.part_o)) + at * D + col;
 #pragma unroll 1
@@ -1109,7 +1115,8 @@ SharedSizes shared_sizes(int B, int Hq, int Hkv, int Nq, int D, int sms) {
     const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;
     const size_t all = static_cast<size_t>(B) * Hq * Nq;
     const size_t parts = 2 * static_cast<size_t>(sms) * prefix_tiles(B, rows) * kPreRows;
-    return {part_bytes(rows, D, own_workers(sms, static_cast<int>(rows))), pad256(all * D * sizeof(float)), pad256(all * sizeof(float)),
+    return {part_bytes(rows, D, own_workers(sms, static_cast<int>(rows))),
+            pad256(all * D * sizeof(float)),   pad256(all * sizeof(float)),
             pad256(all * D * sizeof(float)),   pad256(all * sizeof(float)),
             pad256(parts * D * sizeof(float)), pad256(parts * sizeof(float))};
 }
@@ -1192,7 +1199,8 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
     if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(max_pages) * page + 31) / 32 + kOwnSteps) > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
-    if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * (static_cast<int64_t>(max_pages) * page / kShareBlock + kUnitSteps + 1) > 0x7fffffffll ||
+    const int64_t unit = static_cast<int64_t>(max_pages) * page / kShareBlock + kUnitSteps + 1;
+    if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * unit > 0x7fffffffll ||
         (static_cast<int64_t>(B) * Hkv * rows + kMergeWarps - 1) / kMergeWarps > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
     const SharedSizes z = shared_sizes(B, Hq, Hkv, Nq, D, p.a.ctas);
