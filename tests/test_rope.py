@@ -154,6 +154,13 @@ CASES = [
     (64, 14, True, None, 2, 3, 2, 11, 500000, "bhnd", F16),
     (64, 62, True, None, 1, 1, 6, 5, 3, "odd", BF16),
     (128, 128, False, None, 1, 1, 1, 3000, 0, "bhnd", F16),      # one head: a thread takes one
+    # long enough for four heads a thread, none of the sizes a multiple of what a CTA takes
+    (128, 128, False, None, 2, 30, 11, 331, 50000, "bnhd", BF16),
+    (64, 64, False, None, 1, 33, 5, 601, 50000, "bhnd", F16),
+    (64, 20, False, None, 1, 33, 5, 601, 50000, "bnhd", BF16),
+    (128, 30, True, None, 3, 13, 3, 251, 50000, "bhnd", F16),
+    (64, 64, True, None, 1, 2, 1, 9001, 0, "bnhd", BF16),
+    (128, 64, False, None, 1, 130, 7, 9, 100, "bhnd", F16),
 ]
 
 
