@@ -75,6 +75,11 @@ CASES = [
     (128, 2, False, [9], [40], 1, 1, 40, 32, "bhnd", F16),
     (64, 16, False, [3, 3, 3, 3], [4, 0, 2, 5], 4, 2, 5, 16, "bhnd", F16),
     (64, 64, False, [120], [140], 2, 2, 140, 128, "bhnd", F16),
+    # prompts long enough for a CTA to take several of a page's heads, the last one fewer
+    (64, 64, False, [3, 0], [1290, 1300], 7, 7, 1300, 16, "bnhd", BF16),
+    (128, 40, True, [17, 5], [700, 690], 7, 7, 700, 16, "bhnd", F16),
+    (64, 20, False, [9, 1], [1300, 1], 3, 3, 1300, 16, "bnhd", F16),
+    (128, 128, False, [1000, 60], [2600, 2590], 2, 5, 2600, 64, "bnhd", F16),
 ]
 
 

@@ -477,6 +477,23 @@ def test_pools_past_32_bits(cuda_lib):
     assert bool(res[0][1][1, :, 0].any()) and bool(res[0][3].any())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,Nq,D,page,dtype", [(4, 2, 1, 64, 16, F16), (3, 3, 2, 128, 32, BF16), (20, 1, 1, 64, 64, F16)])
+def test_many_short_ends(cuda_lib, Hq, Hkv, Nq, D, page, dtype):
+    """Dozens of sequences with no, one or a few positions of their own, where a warp's share begins, ends and
+    lies inside the steps that a unit starts with."""
+    for seed, tails in enumerate(([0, 1, 33, 0, 64, 2, 129], [0] * 20 + [700], [1], [31, 0, 0, 0, 32])):
+        cache = _batch([(256, 50), (128, 21)], tails, [0, 5, 0, 300], Hkv, D, page, seed=seed)
+        B = cache[5].numel()
+        q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(seed)).to(dtype)
+        n_new = [min(Nq, int(n)) for n in cache[5]]
+        dev = [t.cuda() for t in cache]
+        plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+        out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new))
+        assert _lib.sync_status() == _lib.ATTN_OK
+        _check(q, cache, n_new, out, lse, f"short ends {seed} D={D}")
+
+
 # ------------------------------------------------------------------ the cache that shares
 
 def test_a_cache_with_a_window_does_not_share():
