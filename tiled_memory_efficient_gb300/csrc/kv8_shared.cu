@@ -217,7 +217,7 @@ __device__ __forceinline__ uint4 lds128v(uint32_t a) {
 // Bound by a tile's chain, scores, softmax, product, of which two are in flight: at D = 128 3750 cycles a step of
 // 128 keys and 256 rows, where the products take 2048 (D = 64: 3300 and 1024), and by both ends of a part: 6 to 9
 // us until the first scores, 3 to 4 for its rows.  128 sequences, 32:8 heads, D = 128 under 16K positions 38 us,
-// the tensor pipe 31% and issue slots 41% busy; 64 samples, 14:2 heads, D = 64 under 32K 17 to 20 us.  Two Q
+// the tensor pipe 32% and issue slots 42% busy; 64 samples, 14:2 heads, D = 64 under 32K 17 to 20 us.  Two Q
 // tiles a CTA (QT) take those 51.5 us instead of 62.5 with one, and 25 instead of 29, in an earlier state of both.
 template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
