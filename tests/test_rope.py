@@ -9,6 +9,7 @@ import torch
 
 from tests import rope_ref
 from tiled_memory_efficient_gb300 import _lib, sdpa
+from tiled_memory_efficient_gb300.kvcache import PagedKVCache
 from tiled_memory_efficient_gb300.rope import Rope, frequencies
 
 F16, BF16 = torch.float16, torch.bfloat16
@@ -381,3 +382,35 @@ def test_a_first_use_is_not_captured(cuda_lib):
         y = rope(q)
     graph.replay()
     assert torch.equal(y, rope(q)) and torch.equal(twice, q * 2)
+
+
+def test_frequencies_are_ordinary_tensors():
+    """Whatever mode the first use runs in, the kept frequencies can be saved for a backward pass."""
+    rope = Rope(64)
+    with torch.inference_mode():
+        words = rope.turns("cpu")
+        assert torch.equal(Rope(64).turns("cpu"), words)
+    assert not words.is_inference() and not rope.for_rows(torch.zeros(1, 1, 1, 64))[0].is_inference()
+
+
+@pytest.mark.gpu
+def test_a_first_use_under_inference_mode(cuda_lib):
+    """Evaluation first, training afterwards: the rotation's gradient is what it is without the former."""
+    q, k = _rows((1, 2, 5, 64), F16, 1), _rows((1, 2, 5, 64), F16, 2)
+    g = _rows((1, 2, 5, 64), F16, 3)
+    want = _lib.rope(g, None, Rope(64), transposed=True)
+    cache = PagedKVCache(1, 1, 2, 64, n_pages=2, page_size=16)
+    for first in ("rows", "append"):
+        rope = Rope(64)
+        with torch.inference_mode():
+            if first == "rows":
+                seen = rope(q, k)[0]
+            else:
+                cache.reserve(5)
+                seen = cache.append(0, k, k, rope=rope, q=q)
+        leaf = q.clone().requires_grad_(True)
+        y = rope(leaf)
+        assert torch.equal(y.detach(), rope(q)) and torch.equal(rope(q), Rope(64)(q)) and seen.is_inference()
+        (d,) = torch.autograd.grad(y, leaf, g)
+        assert torch.equal(d, want)
+    assert _lib.sync_status() == _lib.ATTN_OK

@@ -129,7 +129,8 @@ class Rope:
         if index not in self._turns:
             if index >= 0 and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a rotation's first use on a device cannot be captured: call turns(device) before")
-            t = torch.tensor(self._words, dtype=torch.int64, device=device)
+            with torch.inference_mode(False):   # kept for training, too: a backward pass saves it
+                t = torch.tensor(self._words, dtype=torch.int64, device=device)
             self._turns[index] = (t, self.rotary_dim, self.interleaved, self.amplitude, self.head_dim)
         return self._turns[index][0]
 
