@@ -627,3 +627,36 @@ def test_a_captured_fork(cuda_lib):
                          alone.lens)
     helpers.assert_fwd_close(*(t.double().cpu().numpy() for t in (out, lse, *want)), F16, "one sequence")
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,page,dtype,size,scale", [(64, 16, BF16, 2.0 ** -9, None), (128, 64, BF16, 2.0 ** -9, None),
+                                                     (64, 32, F16, 1.0, 1e-8), (128, 128, F16, 2.0 ** -14, 1e-20)])
+def test_keys_of_zeros_under_tiny_queries(cuda_lib, D, page, dtype, size, scale):
+    """A tile whose keys are all 0 has the smallest scale: its scores' factor is below fp32's range, and what
+    the queries that stand in it do not see is hidden all the same."""
+    cache = _batch([(256, 3)], [0, 2, 40], [], 1, D, page, seed=3)
+    zeros = sorted({int(r[c]) for r in cache[4] for c in range(RUN // page, 2 * RUN // page)})
+    cache[0].view(torch.uint8)[zeros] = 0
+    cache[2][zeros] = 2.0 ** -126
+    q = (torch.randn(3, 2, 4, D, generator=torch.Generator().manual_seed(1)) * size).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+    assert len(_read_plan(plan, 3)) == 1
+    ref = kv8_ref.attention(q, *cache, scale=scale)
+    for out, lse in (_lib.kv8_attn_shared(q.cuda(), *dev, plan, scale=scale), _lib.kv8_attn(q.cuda(), *dev, scale=scale)):
+        assert _lib.sync_status() == _lib.ATTN_OK
+        helpers.assert_fwd_close(*(t.double().cpu().numpy() for t in (out, lse, *ref)), dtype, f"zero keys D={D}")
+    # pages of the tile that hold nothing readable, for rows of which some see nothing at all
+    bad = dev[4].clone()
+    bad[:, RUN // page] = -1
+    n_new = _i32([4, 0, 1])
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev[:4], bad, dev[5], plan, scale=scale, n_new=n_new)
+    assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+    want = _lib.kv8_attn(q.cuda(), *dev[:4], bad, dev[5], scale=scale, n_new=n_new)
+    assert _lib.sync_status() == _lib.ATTN_ERR_PAGE
+    for b, n in enumerate((4, 0, 1)):
+        assert not out[b, :, n:].any() and bool((lse[b, :, n:] == float("-inf")).all())
+        if n:
+            helpers.assert_fwd_close(*(t[b, :, :n].double().cpu().numpy() for t in (out, lse, *want)), dtype,
+                                     f"zero keys, bad page D={D}")

@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const volatile TileInfo* in = infos + x % kInfos;
-                const float f = my_f * in->kf;
+                // (not 0, where both factors are tiny: what is hidden below is -inf times it; the scores,
+                // at most 2^32, are nothing beside 1 there)
+                const float f = fmaxf(my_f * in->kf, 0x1p-126f);
                 const int ev_now = in->ev, bad = in->bad;
                 // QT = 1: S of this tile went out ahead of the last PV.  A warp that arrived for this tile
                 // while another has yet to for the last one would complete that phase in its place; and O is
