@@ -414,3 +414,23 @@ def test_a_first_use_under_inference_mode(cuda_lib):
         (d,) = torch.autograd.grad(y, leaf, g)
         assert torch.equal(d, want)
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_forward_mode_is_refused(cuda_lib):
+    """A dual number's tangent does not vanish in silence: with or without gradients, of q or of k."""
+    from torch.autograd import forward_ad
+    rope, q, t = Rope(64), _rows((1, 2, 5, 64), F16, 1), _rows((1, 2, 5, 64), F16, 2)
+    want = rope(q)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(q, t)
+        for call in (lambda: rope(dual), lambda: rope(q, dual), lambda: _lib.rotary(dual, q, rope),
+                     lambda: rope(dual, q.clone().requires_grad_(True))):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        assert torch.equal(rope(q), want)
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(rope, (q,), (t,))
+    assert torch.equal(rope(q), want) and _lib.sync_status() == _lib.ATTN_OK

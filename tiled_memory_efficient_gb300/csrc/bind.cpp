@@ -836,6 +836,13 @@ struct Rotary : torch::autograd::Function<Rotary> {
 // Wraps q' and, if there is one, k'.
 PyObject* rotated(const Tensor& q, const Tensor& k) { return k.defined() ? pair(q, k) : THPVariable_Wrap(q); }
 
+// A forward-mode dual number requires no gradient, and its tangent would be lost: refused, as the other
+// differentiable calls refuse it.
+void no_tangent(const Tensor& t) {
+    TORCH_CHECK_NOT_IMPLEMENTED(!t.defined() || !t._fw_grad(0).defined(),
+                                "rotary positions have no forward-mode derivative");
+}
+
 // (q, k | None, positions | None, start, Turns) -> q', (q', k') or rc;
 // differentiable
 PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -844,6 +851,8 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 5 || (a[1] != Py_None && !tensor(a[1]).defined()) || (a[2] != Py_None && !tensor(a[2]).defined()) ||
         !c.read(tensor(a[0]), tensor(a[1]), tensor(a[2])) || !whole(a[3], &c.start) || !c.r.read(a[4], c.dev(), c.q.size(3)))
         MISFIT();
+    no_tangent(c.q);
+    no_tangent(c.k);
     Tensor q_out, k_out;
     const bool graph = at::GradMode::is_enabled() &&
                        (c.q.requires_grad() || (c.k.defined() && c.k.requires_grad()));
