@@ -292,3 +292,29 @@ def test_a_decoding_loop(cuda_lib):
             # e4m3: each key and value off by up to 2^-4 of itself (rms 2^-5.2): 4% on either side
             rel = (got[c, :, : n_new[c]] - ref).norm() / ref.norm()
             assert float(rel) < 0.12, (step, c, float(rel))
+
+
+@pytest.mark.gpu
+def test_queries_that_autograd_follows_are_refused(cuda_lib):
+    """Turned queries have no gradient: a q with one is refused, and nothing is appended; under no_grad it is
+    taken, and keys and values may require gradients."""
+    from torch.autograd import forward_ad
+    rope, q, k = Rope(64), _rows((1, 4, 3, 64), F16, 1), _rows((1, 2, 3, 64), F16, 2)
+    cache = PagedKVCache(1, 1, 2, 64, n_pages=1, page_size=16)
+    cache.reserve(3)
+    leaf = q.clone().requires_grad_(True)
+    for out in (None, torch.empty_like(q)):
+        args = (k, k, cache.k_pages[0], cache.v_pages[0], cache.k_scale[0], cache.v_scale[0], cache.table, cache.lens)
+        with pytest.raises(ValueError, match="autograd"):
+            _lib.kv8_append(*args, rope=rope, q=leaf, q_out=out)
+        with forward_ad.dual_level(), torch.no_grad(), pytest.raises(ValueError, match="autograd"):
+            _lib.kv8_append(*args, rope=rope, q=forward_ad.make_dual(q, q), q_out=out)
+    with pytest.raises(ValueError, match="autograd"):
+        cache.append(0, k, k, rope=rope, q=leaf)
+    assert not cache.k_pages.view(torch.uint8).any() and not cache.v_pages.view(torch.uint8).any()
+    with torch.no_grad():
+        got = cache.append(0, k, k, rope=rope, q=leaf)
+    assert torch.equal(got, rope(q)) and cache.k_pages.view(torch.uint8).any()
+    other = k.clone().requires_grad_(True)
+    assert torch.equal(cache.append(0, other, other, rope=rope, q=q), got)
+    assert _lib.sync_status() == _lib.ATTN_OK

@@ -569,14 +569,20 @@ def ffn_check_chunking(x, w1, b1, w2, b2, act: str = "gelu_tanh", chunk: int = 4
 
 # ------------------------------------------------------------------ rotary positions
 
+def _followed(t):
+    """Whether a graph follows a tensor, or a forward-mode derivative does."""
+    import torch
+    from torch.autograd import forward_ad
+    return (torch.is_grad_enabled() and t.requires_grad) or forward_ad.unpack_dual(t).tangent is not None
+
+
 def _explain_result(name, out, like):
     """Raises when `out` cannot take the rows of `like`."""
-    import torch
     if out is None:
         return
     if out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
         raise ValueError(f"{name} must be a {like.dtype} tensor {tuple(like.shape)} on {like.device}")
-    if torch.is_grad_enabled() and (out.requires_grad or like.requires_grad):
+    if _followed(out) or _followed(like):
         raise ValueError(f"{name} is written to behind autograd's back: use the differentiable call")
     raise ValueError(f"{name} needs dense, 16-byte aligned rows that do not overlap")
 
@@ -667,7 +673,8 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
 
     With rope (a rope.Rope) the keys are turned to the positions they take
     (include/rope.h), and with q [B, Hq, T, D] the step's queries as well: they are
-    returned, in q_out if given (it may be q)."""
+    returned, in q_out if given (it may be q).  Nothing here is differentiable: a q that
+    autograd follows is refused."""
     bind = _bind or _load_bind()
     if rope is None:
         if q is not None or q_out is not None:
@@ -706,6 +713,9 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
                     and q.shape[2:] == k.shape[2:] and q.get_device() == dev):
                 raise ValueError(f"q {tuple(q.shape)} must be a {k.dtype} tensor [{k.shape[0]}, Hq, "
                                  f"{k.shape[2]}, {D}] on CUDA device {dev}")
+            if q_out is None and _followed(q):
+                raise ValueError("q is turned behind autograd's back: call append under torch.no_grad(), or turn q by "
+                                 "the rotation itself")
             _explain_result("q_out", q_out, q)
     _refused("kv8_append" if rope is None else "kv8_append_rope", rc, explain)
 

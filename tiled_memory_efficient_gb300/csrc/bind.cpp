@@ -278,6 +278,11 @@ void strides_of(const Tensor& t, long long* st) {
 }
 Tensor readable(const Tensor& t) { return in_place(t) ? t : t.clone(at::MemoryFormat::Contiguous); }
 
+// Whether a graph follows a tensor, or a forward-mode derivative does.
+bool followed(const Tensor& t) {
+    return (at::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(0).defined();
+}
+
 // A given result for `like`: rows that no two elements share, of a tensor that no graph follows
 // (its version is counted on, as any call that writes to it does).
 bool result_for(const Tensor& out, const Tensor& like) {
@@ -286,7 +291,7 @@ bool result_for(const Tensor& out, const Tensor& like) {
         return false;
     for (int i = 0; i < 3; ++i)
         if (out.size(i) != 1 && out.stride(i) == 0) return false;
-    if (at::GradMode::is_enabled() && (out.requires_grad() || like.requires_grad())) return false;
+    if (followed(out) || followed(like)) return false;
     if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
     return true;
 }
@@ -307,6 +312,7 @@ PyObject* py_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q.size(2) != x.T || q.size(3) != p.D || !small(q.sizes()))
             MISFIT();
         if (a[12] == Py_None) {
+            if (followed(q)) MISFIT();   // (the turned queries would lead nowhere)
             q = readable(q);
             out = empty(q.sizes(), q.scalar_type(), p.dev);
         } else {

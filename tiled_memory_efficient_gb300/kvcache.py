@@ -107,7 +107,8 @@ class PagedKVCache:
         that ``reserve`` made room for (n_new of the T each; None: all T); none when it
         found no room.  With rope (a ``rope.Rope``) the keys are turned to their positions
         on the way, and the step's queries q [n_seqs, Hq, T, head_dim], if given, as
-        well: they are returned, rows from n_new on as 0."""
+        well: they are returned, rows from n_new on as 0.  (Without a gradient: a q that
+        autograd follows is refused.)"""
         return _lib.kv8_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                                self.v_scale[layer], self.table, self.lens,
                                n_new=None if n_new is None else self._counts(n_new), granted=self.granted,
