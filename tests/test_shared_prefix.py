@@ -660,3 +660,37 @@ def test_keys_of_zeros_under_tiny_queries(cuda_lib, D, page, dtype, size, scale)
         if n:
             helpers.assert_fwd_close(*(t[b, :, :n].double().cpu().numpy() for t in (out, lse, *want)), dtype,
                                      f"zero keys, bad page D={D}")
+
+
+@pytest.mark.gpu
+def test_more_rows_than_the_shared_attention_takes(cuda_lib, monkeypatch):
+    """Prompts past its rows, or past the workspace it may ask for, are read by every sequence for itself."""
+    from tiled_memory_efficient_gb300 import kvcache
+    Hq, n = 64, 16400                         # 1.05 million rows of the one KV head
+    cache = PagedKVCache(1, 1, 1, 64, n_pages=-(-n // 128), page_size=128, share=True, min_saved=0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(1, 1, n, 64, generator=g, device="cuda").to(BF16) for _ in range(2))
+    cache.reserve(n)
+    cache.append(0, k, v)
+    pools = [t[0] for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)] + [cache.table, cache.lens]
+    q = torch.randn(1, Hq, n, 64, generator=g, device="cuda").to(BF16)
+    want = _lib.kv8_attn(q, *pools)
+    for n_new in (None, n):
+        assert all(torch.equal(a, b) for a, b in zip(cache.attend(0, q, n_new=n_new), want))
+    assert _lib.sync_status() == _lib.ATTN_OK
+    # the workspace: rows in fp32 twice, as long as they fit the limit
+    q = q[:, :, -64:].contiguous()
+    sizes = []
+    for limit in (8 * q.numel(), 8 * q.numel() - 1):
+        monkeypatch.setattr(kvcache, "_SHARED_BYTES", limit)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out, lse = cache.attend(0, q)
+        sizes.append(torch.cuda.max_memory_allocated() - before - out.numel() * 2 - lse.numel() * 4)
+        helpers.assert_fwd_close(*(t.double().cpu().numpy() for t in (out, lse, want[0][:, :, -64:], want[1][:, :, -64:])),
+                                 BF16, "a prompt's last queries")
+    # what either call's own workspace takes, in the allocator's steps (512 bytes, 2 MB for larger blocks)
+    most = [f(1, Hq, 1, 64, 64) for f in (cuda_lib.kv8_attn_shared_workspace_size, cuda_lib.kv8_attn_workspace_size)]
+    assert 8 * q.numel() <= sizes[0] and all(a <= b + (2 << 20) for a, b in zip(sizes, most))
+    assert most[1] + (2 << 20) < most[0] and _lib.sync_status() == _lib.ATTN_OK

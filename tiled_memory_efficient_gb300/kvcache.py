@@ -38,6 +38,12 @@ from . import _lib
 
 __all__ = ["PagedKVCache"]
 
+# Attention over a shared prefix keeps all query rows in fp32 twice, and takes 2^20 rows a KV head.  A call whose
+# rows would take more is kv8_attn's.  (16 sequences of 2048 queries, 32:8 heads, D = 128, 1.1 GB: 18.3 ms where
+# 16384 positions are shared and 45.5 with every sequence for itself; 11.8 and 10.9 where it is 256.)
+_SHARED_BYTES = 4 << 30
+_SHARED_ROWS = 1 << 20
+
 
 class PagedKVCache:
     """Keys and values of n_seqs sequences in n_layers layers.
@@ -48,7 +54,9 @@ class PagedKVCache:
     the window has left behind.  share (without a window): ``reassign`` looks which
     sequences begin with the same pages, and ``attend`` reads those once for all of
     them where that saves enough (128 MB of keys and values; or min_saved positions, for
-    each group).  Whoever writes `table` by hand calls ``find_shared`` afterwards.
+    each group).  Whoever writes `table` by hand calls ``find_shared`` afterwards.  Such an ``attend``
+    asks for 8 bytes of workspace per value of q, and for parts of up to 40 MB beside; with
+    over 4 GB of them, or more than 2^20 queries a KV head (its query heads'), it reads every sequence for itself.
     """
 
     def __init__(self, n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, n_pages: int,
@@ -120,7 +128,7 @@ class PagedKVCache:
         of a step that found no room) get 0 and -inf.  None: all Nq rows are the
         newest positions; with a window no more than the sequence's last ``reserve``
         made room for, since older queries want pages that it gave back."""
-        if self.plan is not None:
+        if self.plan is not None and not self._too_many(q):
             return _lib.kv8_attn_shared(q, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                                         self.v_scale[layer], self.table, self.lens, self.plan, scale=scale,
                                         n_new=None if n_new is None else self._counts(n_new),
@@ -130,6 +138,10 @@ class PagedKVCache:
                              window=self.window, sinks=self.sinks,
                              n_new=None if n_new is None else self._counts(n_new),
                              granted=None if n_new is None else self.granted)
+
+    def _too_many(self, q):
+        return q.dim() == 4 and (8 * q.numel() > _SHARED_BYTES or
+                                 q.shape[1] * q.shape[2] > _SHARED_ROWS * self.k_scale.shape[2])
 
     def reassign(self, parents):
         """Sequence c becomes a copy-on-write child of parents[c] (int32 tensor
