@@ -694,3 +694,71 @@ def test_more_rows_than_the_shared_attention_takes(cuda_lib, monkeypatch):
     most = [f(1, Hq, 1, 64, 64) for f in (cuda_lib.kv8_attn_shared_workspace_size, cuda_lib.kv8_attn_workspace_size)]
     assert 8 * q.numel() <= sizes[0] and all(a <= b + (2 << 20) for a, b in zip(sizes, most))
     assert most[1] + (2 << 20) < most[0] and _lib.sync_status() == _lib.ATTN_OK
+
+
+QUESTIONS = [
+    # Hq, Hkv, Nq, D, page, groups, tails, alone, dtype: queries in several tiles of the prefix, members' rows over
+    # several blocks of 256, sequences shorter than their queries
+    (4, 2, 70, 64, 32, [(256, 3)], [3, 90, 200], [100], F16),
+    (7, 1, 40, 128, 16, [(384, 5), (128, 2)], [0, 41, 7], [39], BF16),
+    (2, 1, 300, 128, 64, [(512, 4)], [10, 310, 0], [400, 120], BF16),
+    (14, 2, 129, 64, 64, [(256, 2), (1024, 3)], [1, 150], [], F16),
+    (1, 1, 700, 64, 128, [(640, 3)], [0, 300], [], F16),
+    (8, 2, 17, 128, 128, [(1280, 30)], [17, 20, 300], [5], BF16),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", QUESTIONS, ids=str)
+def test_questions_behind_a_prefix(cuda_lib, case):
+    """Many queries a sequence: all of them, and a number for each sequence."""
+    Hq, Hkv, Nq, D, page, groups, tails, alone, dtype = case
+    cache = _batch(groups, tails, alone, Hkv, D, page, seed=Nq)
+    B, rng = cache[5].numel(), random.Random(Nq)
+    q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    dev = [t.cuda() for t in cache]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+    assert len(_read_plan(plan, B)) == len(groups)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan)
+    assert _lib.sync_status() == _lib.ATTN_OK
+    for b in range(B):   # all Nq rows: those before a sequence's first position see nothing
+        n = min(Nq, int(cache[5][b]))
+        assert not out[b, :, : Nq - n].any() and bool((lse[b, :, : Nq - n] == float("-inf")).all())
+        one = cache[:4] + (cache[4][b:b + 1], cache[5][b:b + 1])
+        ref = kv8_ref.attention(q[b:b + 1, :, Nq - n:], *one)
+        helpers.assert_fwd_close(*(t[b, :, Nq - n:].double().cpu().numpy() for t in (out, lse)), *(t[0].numpy() for t in ref),
+                                 dtype, f"questions {case} sequence {b}")
+    n_new = [min(rng.choice([0, 1, rng.randint(1, Nq), Nq]), int(n)) for n in cache[5]]
+    held = q.cuda()
+    held[0, :, n_new[0]:] = float("nan")         # rows past a count may hold anything
+    res = [_lib.kv8_attn_shared(held, *dev, plan, n_new=_i32(n_new)) for _ in range(2)]
+    assert _lib.sync_status() == _lib.ATTN_OK and all(torch.equal(a, b) for a, b in zip(*res))
+    _check(q, cache, n_new, *res[0], f"questions, counts {case}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,page,dtype", [(64, 16, F16), (128, 64, BF16)])
+def test_questions_about_one_text(cuda_lib, D, page, dtype):
+    """A sharing cache from its first prompt on: the text attends before any fork, each sequence's question of its own
+    length behind it, then drafts."""
+    S, Hq, Hkv, text = 6, 4, 2, 900
+    rope, g = Rope(D), torch.Generator().manual_seed(D)
+    cache = PagedKVCache(1, S, Hkv, D, n_pages=S * 300 // page + 2 * text // page, page_size=page, max_pages=1400 // page,
+                         share=True, min_saved=0)
+
+    def turn(counts, T):
+        q, k, v = (torch.randn(S, h, T, D, generator=g).to(dtype).cuda() for h in (Hq, Hkv, Hkv))
+        n = _i32(counts)
+        cache.reserve(n)
+        q = cache.append(0, k, v, n, rope=rope, q=q)
+        out, lse = cache.attend(0, q, n_new=n)
+        assert _lib.sync_status() == _lib.ATTN_OK
+        held = [t[0].cpu() for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+        _check(q.cpu(), (*held, cache.table.cpu(), cache.lens.cpu()), counts, out, lse, f"questions D={D} T={T}")
+
+    turn([text] + [0] * (S - 1), text)
+    cache.reassign(_i32([0] * S))
+    assert sorted((d * RUN, len(m)) for m, d in _read_plan(cache.plan, S).values()) == [(text // RUN * RUN, S)]
+    turn([200, 1, 77, 130, 0, 199], 200)
+    turn([1, 5, 0, 3, 2, 4], 5)
+    turn([0, 0, 0, 0, 90, 20], 90)
