@@ -318,3 +318,38 @@ def test_queries_that_autograd_follows_are_refused(cuda_lib):
     other = k.clone().requires_grad_(True)
     assert torch.equal(cache.append(0, other, other, rope=rope, q=q), got)
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+# What the sines and the arithmetic leave of a turned key: a sine made for its position is off by 2^-23.3 (its angle) and
+# 2^-23 (rope_ref.ARITH); a prompt's are one turn of such a pair by another, so twice that and the products' 2^-23, 2^-20.5
+# in all; amplitude, products and sum of the key 4 units of 2^-24 more: 2^-20 of A (|a| + |b|).
+EXACT = 2.0 ** -20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rot,inter,T,page,dtype", [
+    (128, 128, False, 600, 64, BF16), (128, 128, False, 600, 128, F16), (64, 64, False, 900, 16, F16), (64, 64, True, 500, 32, BF16),
+    (128, 32, True, 300, 64, F16), (128, 126, False, 400, 128, F16), (64, 20, False, 500, 16, BF16), (128, 40, False, 200, 16, F16),
+    (128, 128, False, 8, 64, F16), (64, 64, True, 16, 16, F16)])
+def test_codes_of_turned_keys(cuda_lib, D, rot, inter, T, page, dtype):
+    """Every key's code lies between those of the exact key less and plus what the arithmetic may add: prompts from far
+    positions on and steps, each page's tokens."""
+    rope, H, old = Rope(D, rot, interleaved=inter, base=300.0, amplitude=1.25), 3, [70003, 0]
+    k = _rows((2, H, T, D), dtype, T + D)
+    pools, table = _cache(old, [T, T], H, D, page, seed=T)
+    lens = [n + T for n in old]
+    dev = [t.cuda() for t in pools]
+    _lib.kv8_append(k, k, dev[0], dev[2], dev[1], dev[3], table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), rope=rope)
+    assert _lib.sync_status() == _lib.ATTN_OK
+    positions = torch.tensor(old)[:, None] + torch.arange(T)[None]
+    x = rope_ref.rotate(k.cpu(), rope.inv_freq, positions, rope.amplitude, inter)
+    off = rope.amplitude * EXACT * rope_ref.partner(k.cpu(), rot, inter)
+    pid = table.long().gather(1, positions // page)                      # [2, T]
+    s = dev[1].cpu().double()[pid].transpose(1, 2)[..., None]           # [2, H, T, 1]
+    got = dev[0].cpu().double()[pid[:, :, None], torch.arange(H)[None, None], (positions % page)[:, :, None]].transpose(1, 2)
+    code = lambda y: y.clamp(-448, 448).float().to(F8).double()
+    # (fp64 to fp32 rounds once more, by 2^-24 of the value: the bounds are moved by as much; what stays is exact,
+    # 16 bits that often lie between two codes)
+    lo, hi = ((x + sign * torch.where(off > 0, off + x.abs() * 2.0 ** -23, 0.0)) / s for sign in (-1, 1))
+    assert bool((code(lo) <= got).all()) and bool((got <= code(hi)).all())
+    assert float((code(lo) != code(hi)).double().mean()) < 1e-3   # (the bounds are sharp)

@@ -298,11 +298,13 @@ __device__ __forceinline__ uint2 quantise8(const float (&y)[8], float inv) {
 // Prompts: one CTA per (sequence, page it may touch, keys or values), `heads` KV heads in turn.  A thread
 // holds two rows' items (rope_item's, the two halves of each pair in one thread); the next two heads' are
 // on their way to shared memory meanwhile.  The page's sines are made once for all of the CTA's heads:
-// each pair's exactly at every eighth token, the others by turning those by one token up to four times (off
-// by less than 2^-21).  2 x 8190 tokens, 8 KV heads, D = 128, 67 MB read and 34 written: 20.3 us (21.9
-// with one head ahead in registers, 23.1 with four ahead; in 64 registers a thread 21.4), bound by each
-// head's chain of turn, maximum, barrier, scale and store in three CTAs an SM; the plain append, without
-// sines, takes 15.6.
+// each pair's for its position at every fourth token, the three beside it by one turn of that by the angle of
+// one or two tokens.  They are then off by 2^-21.8 at most (2^-24.3 rms, over 2^24 random frequencies and
+// positions), where every one made for its position is by 2^-23.0 (2^-24.9), at 24.4 us instead of what follows.  2 x
+// 8190 tokens, 8 KV heads, D = 128, 67 MB read and 34 written: 21.8 us (one head ahead in registers takes 1.6
+// longer, four ahead 2.8; in 64 registers a thread 1.1), bound by each head's chain of turn, maximum, barrier,
+// scale and store in three CTAs an SM; the plain append, without sines, takes 14.8.  Pairs that no vector holds
+// whole (kRopeScalar) are read and written by the element: 48.2 with 40 of the dimensions turning.
 template <int D>
 constexpr int prompt_threads(int page) { return page * (D / 32); }
 // CTAs of an SM up to which a page's heads are cut (the sines are made once a CTA): 8 take 21.6 us there.
@@ -389,26 +391,20 @@ __global__ void __maxnreg__(80) kv8_append_rope_kernel(const __grid_constant__ A
     // fours, so that a token's items read whole lines; past the last pair a turn by nothing.
     auto place = [&](int pair) { return ((pair >> 2) & 1) * (pitch >> 1) + (pair >> 3) * 4 + (pair & 3); };
     if (keys) {
-        for (int i = threadIdx.x; i < pitch * (page / 8); i += blockDim.x) {
-            const int run = i / pitch, pair = i - run * pitch;
-            float2 mid = make_float2(1.0f, 0.0f), one = mid;
-            if (pair < half) {
-                mid = rope_cs(p.f.turns, pair, t.t0 + run * 8 + 4, p.f.amp);
-                one = rope_cs(p.f.turns, pair, 1, 1.0f);
-            }
-            const int at = run * 8 * pitch + place(pair);
-            float2 up = mid, down = mid;
-            s_cos[at + 4 * pitch] = mid.x;
-            s_sin[at + 4 * pitch] = mid.y;
-#pragma unroll
-            for (int k = 1; k <= 4; ++k) {
-                down = make_float2(down.x * one.x + down.y * one.y, down.y * one.x - down.x * one.y);
-                s_cos[at + (4 - k) * pitch] = down.x;
-                s_sin[at + (4 - k) * pitch] = down.y;
-                if (k == 4) break;
-                up = make_float2(up.x * one.x - up.y * one.y, up.y * one.x + up.x * one.y);
-                s_cos[at + (4 + k) * pitch] = up.x;
-                s_sin[at + (4 + k) * pitch] = up.y;
+        // a thread one pair (there are as many threads, at least) at every so many fours of tokens
+        const int shift = pitch > 32 ? 6 : pitch > 16 ? 5 : pitch > 8 ? 4 : 3;
+        const int pair = static_cast<int>(threadIdx.x) & ((1 << shift) - 1);
+        if (pair < pitch) {
+            const unsigned long long turn = pair < half ? __ldg(p.f.turns + pair) : 0ull;
+            const float amp = pair < half ? p.f.amp : 1.0f;
+            const float2 one = rope_cs(turn, 1.0f), two = rope_cs(2 * turn, 1.0f);
+            for (int x = 4 * (static_cast<int>(threadIdx.x) >> shift); x < page; x += 4 * (static_cast<int>(blockDim.x) >> shift)) {
+                const float2 m = rope_cs(rope_phase(turn, t.t0 + x + 2), amp);
+                float *c = s_cos + x * pitch + place(pair), *s = s_sin + x * pitch + place(pair);
+                c[0] = m.x * two.x + m.y * two.y, s[0] = m.y * two.x - m.x * two.y;
+                c[pitch] = m.x * one.x + m.y * one.y, s[pitch] = m.y * one.x - m.x * one.y;
+                c[2 * pitch] = m.x, s[2 * pitch] = m.y;
+                c[3 * pitch] = m.x * one.x - m.y * one.y, s[3 * pitch] = m.y * one.x + m.x * one.y;
             }
         }
         __syncthreads();

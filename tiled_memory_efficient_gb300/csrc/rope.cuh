@@ -32,14 +32,19 @@ struct RopeView {
     float sign;   // -1: the transposed rotation
 };
 
-// (cosine, sine) * scale of pair i at position pos.
-__device__ __forceinline__ float2 rope_cs(const unsigned long long* turns, int i, int pos, float amp) {
-    const unsigned long long phase =
-        static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(turns + i);
+// (cosine, sine) * scale of an angle, a 64-bit fraction of a turn.
+__device__ __forceinline__ float2 rope_cs(unsigned long long phase, float amp) {
     const int top = static_cast<int>(static_cast<uint32_t>((phase + 0x80000000ull) >> 32));
     float s, c;
     sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
     return make_float2(c * amp, s * amp);
+}
+// The angle of frequency `turn` at position pos, and what pair i turns by there.
+__device__ __forceinline__ unsigned long long rope_phase(unsigned long long turn, int pos) {
+    return static_cast<unsigned long long>(static_cast<long long>(pos)) * turn;
+}
+__device__ __forceinline__ float2 rope_cs(const unsigned long long* turns, int i, int pos, float amp) {
+    return rope_cs(rope_phase(__ldg(turns + i), pos), amp);
 }
 
 template <bool BF16>
