@@ -434,3 +434,21 @@ def test_forward_mode_is_refused(cuda_lib):
     with pytest.raises(RuntimeError):
         torch.func.jvp(rope, (q,), (t,))
     assert torch.equal(rope(q), want) and _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_one_row_of_positions_for_a_batch(cuda_lib):
+    """[1, N], as models hold them: what [N] gives, forward, backward and of any strides."""
+    rope, q, g = Rope(64), _rows((3, 2, 7, 64), BF16, 1).requires_grad_(True), _rows((3, 2, 7, 64), BF16, 2)
+    pos = torch.randint(0, 9999, (7,), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    want = rope(q, positions=pos)
+    (dq,) = torch.autograd.grad(want, q, g)
+    rows = torch.stack([pos, pos + 1], 1)   # every second element, and a batch stride that is nobody's
+    for one in (pos[None], pos[None].expand(3, 7), rows[None, :, 0], rows.t()[:1]):
+        got = rope(q, positions=one)
+        assert torch.equal(got, want) and torch.equal(torch.autograd.grad(got, q, g)[0], dq)
+        assert torch.equal(_lib.rope(q.detach(), None, rope, one), want)
+    for bad in (pos[None, None], pos[None].expand(2, 7), pos[None, :6], pos[:1].expand(3, 1)):
+        with pytest.raises(ValueError, match="positions"):
+            rope(q, positions=bad)
+    assert _lib.sync_status() == _lib.ATTN_OK

@@ -603,13 +603,13 @@ def _explain_rope(q, k, positions, rope):
     if positions is not None:
         B, _, N, _ = q.shape
         if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 \
-                or positions.device != q.device or tuple(positions.shape) not in ((N,), (B, N)):
-            raise ValueError(f"positions must be an int32 tensor [{N}] or [{B}, {N}] on {q.device}")
+                or positions.device != q.device or tuple(positions.shape) not in ((N,), (1, N), (B, N)):
+            raise ValueError(f"positions must be an int32 tensor [{N}], [1, {N}] or [{B}, {N}] on {q.device}")
 
 
 def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, transposed: bool = False):
     """q [B, Hq, N, D] and k [B, Hk, N, D] (k None: q alone) turned to positions (int32
-    [N] or [B, N]; None: start + n) by a rope.Rope (include/rope.h): the pair, or q
+    [N], [1, N] or [B, N]; None: start + n) by a rope.Rope (include/rope.h): the pair, or q
     alone.  q_out and k_out may be q and k.  transposed turns back, times the amplitude.
     Not differentiable: see rotary."""
     r = (_bind or _load_bind()).rope(q, k, positions, start, rope.for_rows(q), q_out, k_out, int(transposed))

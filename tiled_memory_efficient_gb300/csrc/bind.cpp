@@ -757,10 +757,10 @@ struct RopeCall {
                             k.size(0) != q.size(0) || k.size(2) != q.size(2) || k.size(3) != q.size(3) ||
                             !small(k.sizes())))
             return false;
-        if (positions.defined()) {   // [N] or [B, N]
+        if (positions.defined()) {   // [N], [1, N] or [B, N]
             const int64_t d = positions.dim();
             if (cuda_of(positions) != dev || positions.scalar_type() != at::kInt || (d != 1 && d != 2) ||
-                positions.size(d - 1) != q.size(2) || (d == 2 && positions.size(0) != q.size(0)))
+                positions.size(d - 1) != q.size(2) || (d == 2 && positions.size(0) != 1 && positions.size(0) != q.size(0)))
                 return false;
         }
         return true;
@@ -781,7 +781,7 @@ struct RopeCall {
             strides_of(*k_out, st + 9);
         }
         if (positions.defined()) {
-            st[12] = positions.dim() == 2 ? positions.stride(0) : 0;
+            st[12] = positions.dim() == 2 && positions.size(0) > 1 ? positions.stride(0) : 0;
             st[13] = positions.stride(positions.dim() - 1);
         }
         return fn.rope(ptr(x), ptr(y), ptr(*q_out), ptr(*k_out), r.at(), as<int>(positions), start, x.size(0),

@@ -143,6 +143,6 @@ class Rope:
         return a
 
     def __call__(self, q, k=None, positions=None, start: int = 0):
-        """q, or (q, k), turned to positions (int32 [N] or [B, N]; None: start + n)."""
+        """q, or (q, k), turned to positions (int32 [N], [1, N] or [B, N]; None: start + n)."""
         r = (_lib._bind or _lib._load_bind()).rotary(q, k, positions, start, self.for_rows(q))
         return r if type(r) is not int else _lib.rotary(q, k, self, positions, start)
