@@ -135,9 +135,9 @@ struct AttnCfg {
     static constexpr int kQOff = kInfoOff + kWarps * kStages * static_cast<int>(sizeof(SlotInfo));
     static constexpr int kBarOff = kQOff + (kQSmem ? NR * 8 * D * 2 + NR * 8 * 4 : 0);
     static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kPreOff = kMiscOff + 8 * kWarps;                   // B + 1 ints, then 3 B
-    static constexpr int smem_bytes(int B) { return kPreOff + (4 * B + 1) * 4; }
-    static_assert(smem_bytes(kMaxBatch) <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int kPreOff = kMiscOff + 8 * kWarps;                   // B + 1 ints, then 2 B or (SHARED) 3 B
+    static constexpr int smem_bytes(int B, bool shared) { return kPreOff + ((shared ? 4 : 3) * B + 1) * 4; }
+    static_assert(smem_bytes(kMaxBatch, true) <= 227 * 1024, "shared memory of a CTA");
 };
 
 // ONE: a tile lies in one page (page >= the tile's tokens); else it takes 2 or 4 boxes.
@@ -916,9 +916,9 @@ cudaError_t launch_attn(const CUtensorMap& tmK, const CUtensorMap& tmV, const At
                         cudaStream_t stream) {
     auto kern = kv8_attn_kernel<D, BF16, NR, ONE, SHARED>;
     static SmemLimit limit;
-    const cudaError_t e = limit.raise(kern, AttnCfg<D, NR>::smem_bytes(kMaxBatch));
+    const cudaError_t e = limit.raise(kern, AttnCfg<D, NR>::smem_bytes(kMaxBatch, SHARED));
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, p.ctas, kAttnThreads, AttnCfg<D, NR>::smem_bytes(p.B), stream, tmK, tmV, p);
+    return launch_dependent(kern, p.ctas, kAttnThreads, AttnCfg<D, NR>::smem_bytes(p.B, SHARED), stream, tmK, tmV, p);
 }
 
 // The attention alone; its merge is the caller's.
