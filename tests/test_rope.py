@@ -452,3 +452,36 @@ def test_one_row_of_positions_for_a_batch(cuda_lib):
         with pytest.raises(ValueError, match="positions"):
             rope(q, positions=bad)
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_results_that_overlap_are_refused(cuda_lib):
+    """Results in each other's place, in another operand's, or with rows over rows: refused, and no version counted on;
+    slices of one tensor that lie side by side are taken."""
+    rope, q, k = Rope(64), _rows((2, 4, 6, 64), F16, 1), _rows((2, 4, 6, 64), F16, 2)
+    spare, want = torch.empty_like(q), rope(q, k)
+    flat = torch.zeros(2 * 4 * 6 * 64, dtype=F16, device="cuda")
+    for bad, what in ((dict(q_out=k), "k does"), (dict(k_out=q), "q does"), (dict(q_out=spare, k_out=spare), "k_out does"),
+                      (dict(q_out=spare, k_out=k[:, :2]), "k_out must"), (dict(q_out=k, k_out=q), "k does"),
+                      (dict(q_out=flat.as_strided(q.shape, (1536, 384, 32, 1))), "overlap"),
+                      (dict(k_out=flat.as_strided(q.shape, (384, 384, 64, 1))), "overlap")):
+        keep = [(t, t.clone(), t._version) for t in (q, k, spare, flat)]
+        with pytest.raises(ValueError, match=what):
+            _lib.rope(q, k, rope, **bad)
+        assert all(torch.equal(t.view(torch.uint8), c.view(torch.uint8)) and t._version == n for t, c, n in keep)
+    with pytest.raises(ValueError, match="k does"):
+        _lib.rope(q, q, rope, q_out=q, k_out=q)
+    wide = torch.cat([q, k], 3)                        # [.., 128]: two slices, reaching over each other
+    a, b = wide[..., :64], wide[..., 64:]
+    n = wide._version
+    got = _lib.rope(a, b, rope, q_out=a, k_out=b)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(wide, torch.cat(want, 3)) and wide._version > n
+    cache = PagedKVCache(1, 2, 4, 64, n_pages=2, page_size=16)
+    cache.reserve(6)
+    pools = [t[0] for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)]
+    for out, what in ((k, "k does"), (flat.as_strided(q.shape, (1536, 384, 32, 1)), "overlap")):
+        with pytest.raises(ValueError, match=what):
+            _lib.kv8_append(k, k, *pools, cache.table, cache.lens, rope=rope, q=q, q_out=out)
+    assert not cache.k_pages.view(torch.uint8).any()
+    assert torch.equal(_lib.kv8_append(k, k, *pools, cache.table, cache.lens, rope=rope, q=q, q_out=spare), want[0])
+    assert _lib.sync_status() == _lib.ATTN_OK

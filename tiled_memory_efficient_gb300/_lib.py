@@ -576,15 +576,23 @@ def _followed(t):
     return (torch.is_grad_enabled() and t.requires_grad) or forward_ad.unpack_dual(t).tangent is not None
 
 
-def _explain_result(name, out, like):
-    """Raises when `out` cannot take the rows of `like`."""
+def _explain_result(name, out, like, **others):
+    """Raises when `out` cannot take the rows of `like`, or begins where one of the others does."""
     if out is None:
         return
     if out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
         raise ValueError(f"{name} must be a {like.dtype} tensor {tuple(like.shape)} on {like.device}")
     if _followed(out) or _followed(like):
         raise ValueError(f"{name} is written to behind autograd's back: use the differentiable call")
-    raise ValueError(f"{name} needs dense, 16-byte aligned rows that do not overlap")
+    steps = sorted((s, n) for s, n in zip(out.stride()[:3], out.shape) if n > 1)
+    reach, apart = out.shape[3], out.stride(3) == 1 and out.data_ptr() % 16 == 0
+    for s, n in steps:
+        apart, reach = apart and s % 8 == 0 and s >= reach, reach + (n - 1) * s
+    if not apart:
+        raise ValueError(f"{name} needs dense, 16-byte aligned rows that do not overlap")
+    for other, t in others.items():
+        if t is not None and t.data_ptr() == out.data_ptr():
+            raise ValueError(f"{name} begins where {other} does")
 
 
 def _explain_rope(q, k, positions, rope):
@@ -610,7 +618,7 @@ def _explain_rope(q, k, positions, rope):
 def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, transposed: bool = False):
     """q [B, Hq, N, D] and k [B, Hk, N, D] (k None: q alone) turned to positions (int32
     [N], [1, N] or [B, N]; None: start + n) by a rope.Rope (include/rope.h): the pair, or q
-    alone.  q_out and k_out may be q and k.  transposed turns back, times the amplitude.
+    alone.  q_out and k_out may be q and k, and overlap nothing else.  transposed turns back, times the amplitude.
     Not differentiable: see rotary."""
     r = (_bind or _load_bind()).rope(q, k, positions, start, rope.for_rows(q), q_out, k_out, int(transposed))
     if type(r) is not int:
@@ -620,8 +628,8 @@ def rope(q, k, rope, positions=None, start: int = 0, q_out=None, k_out=None, tra
         _explain_rope(q, k, positions, rope)
         if k is None and k_out is not None:
             raise ValueError("k_out without k")
-        _explain_result("q_out", q_out, q)
-        _explain_result("k_out", k_out, k)
+        _explain_result("q_out", q_out, q, k=k, k_out=k_out)
+        _explain_result("k_out", k_out, k, q=q)
     _refused("rope_apply", r, explain)
 
 
@@ -716,7 +724,7 @@ def kv8_append(k, v, k_pages, v_pages, k_scale, v_scale, table, lens, n_new=None
             if q_out is None and _followed(q):
                 raise ValueError("q is turned behind autograd's back: call append under torch.no_grad(), or turn q by "
                                  "the rotation itself")
-            _explain_result("q_out", q_out, q)
+            _explain_result("q_out", q_out, q, k=k, v=v)
     _refused("kv8_append" if rope is None else "kv8_append_rope", rc, explain)
 
 

@@ -19,6 +19,7 @@
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <optional>
 #include <set>
@@ -283,17 +284,29 @@ bool followed(const Tensor& t) {
     return (at::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(0).defined();
 }
 
-// A given result for `like`: rows that no two elements share, of a tensor that no graph follows
-// (its version is counted on, as any call that writes to it does).
+// A given result for `like`: rows that no two elements share, of a tensor that no graph follows.
 bool result_for(const Tensor& out, const Tensor& like) {
     if (!like.defined() || cuda_of(out) != cuda_of(like) || out.scalar_type() != like.scalar_type() ||
         out.sizes() != like.sizes() || !in_place(out))
         return false;
-    for (int i = 0; i < 3; ++i)
-        if (out.size(i) != 1 && out.stride(i) == 0) return false;
-    if (followed(out) || followed(like)) return false;
+    // dimension by dimension, the nearest first: each steps over all that the ones before it reach
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return out.stride(a) < out.stride(b); });
+    int64_t reach = out.size(3);
+    for (int i : order) {
+        if (out.size(i) == 1) continue;
+        if (out.stride(i) < reach) return false;
+        reach += (out.size(i) - 1) * out.stride(i);
+    }
+    return !followed(out) && !followed(like);
+}
+// Two tensors that begin at the same place: a result is not to be another operand.
+bool same_place(const Tensor& a, const Tensor& b) {
+    return a.defined() && b.defined() && a.data_ptr() == b.data_ptr();
+}
+// A given result was written to: its version is counted on, as any call that writes to it does.
+void written(const Tensor& out) {
     if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
-    return true;
 }
 
 // (Append, Turns, q | None, q_out | None) -> q_out, None or rc
@@ -317,7 +330,7 @@ PyObject* py_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
             out = empty(q.sizes(), q.scalar_type(), p.dev);
         } else {
             out = tensor(a[12]);
-            if (!result_for(out, q)) MISFIT();
+            if (!result_for(out, q) || same_place(out, x.k) || same_place(out, x.v)) MISFIT();
             if (out.data_ptr() != q.data_ptr()) q = readable(q);
         }
         strides_of(q, st + 3);
@@ -334,6 +347,7 @@ PyObject* py_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
     if (rc != ATTN_OK) return PyLong_FromLong(rc);
     if (!out.defined()) Py_RETURN_NONE;
+    if (a[12] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -893,7 +907,10 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out[i] = tensor(a[5 + i]);
         if (!result_for(out[i], like)) MISFIT();
     }
+    if (same_place(out[0], c.k) || same_place(out[1], c.q) || same_place(out[0], out[1])) MISFIT();
     const int rc = unlocked([&] { return c.run(&out[0], &out[1]); });
+    for (int i = 0; i < 2 && rc == ATTN_OK; ++i)
+        if (a[5 + i] != Py_None) written(out[i]);
     return rc == ATTN_OK ? rotated(out[0], out[1]) : PyLong_FromLong(rc);
     END_HANDLE_TH_ERRORS
 }
