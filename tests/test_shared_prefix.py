@@ -762,3 +762,31 @@ def test_questions_about_one_text(cuda_lib, D, page, dtype):
     turn([200, 1, 77, 130, 0, 199], 200)
     turn([1, 5, 0, 3, 2, 4], 5)
     turn([0, 0, 0, 0, 90, 20], 90)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,Nq,members,followed", [
+    (8, 8, 64, 1, 7, False), (8, 8, 64, 1, 8, True), (16, 8, 64, 5, 5, False), (16, 8, 64, 5, 6, True), (32, 8, 64, 5, 2, True),
+    (8, 8, 128, 1, 2, False), (8, 8, 128, 1, 3, True), (24, 8, 128, 6, 2, True)])
+def test_groups_too_small_to_follow(cuda_lib, Hq, Hkv, D, Nq, members, followed):
+    """A plan that leaves the choice: groups whose rows cost more together than apart are read apart, beside a large one
+    that is followed; a plan made by hand follows all of them."""
+    page, big, small, n = 128, 40, 2, 4096 * 1024 // (Hkv * D)
+    cache = [t.cuda() for t in _batch([(n, big)] + [(8192, members)] * small, [70, 3, 200], [300], Hkv, D, page, seed=members)]
+    B = cache[5].numel()
+    q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    by = {least: _lib.kvp_find_shared(cache[4], cache[5], page, least) for least in (-1, 0, (members - 1) * 8192 + 1, (1 << 31) - 1)}
+    assert [len(_read_plan(p, B)) for p in by.values()] == [1 + small, 1 + small, 1, 0]
+    assert _read_plan(by[-1], B) == _read_plan(by[0], B) and (big - 1) * n * 2 * Hkv * D > 128 << 20
+    own, hand, large, none = (_lib.kv8_attn_shared(q, *cache, plan) for plan in by.values())
+    assert all(torch.equal(a, b) for a, b in zip(own, hand if followed else large))
+    assert not all(torch.equal(a, b) for a, b in zip(own, large if followed else hand))
+    for res in (hand, large, none):
+        helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (*own, *res)), BF16, f"small groups D={D} Nq={Nq}")
+    assert _lib.sync_status() == _lib.ATTN_OK
+    # nothing but small ones
+    cache = [t.cuda() for t in _batch([(8192, members)] * small, [70, 3, 200], [300], Hkv, D, page, seed=members)]
+    q = q[: cache[5].numel()].contiguous()
+    own = _lib.kv8_attn_shared(q, *cache, _lib.kvp_find_shared(cache[4], cache[5], page))
+    helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (*own, *_lib.kv8_attn(q, *cache))), BF16, "small groups alone")
+    assert _lib.sync_status() == _lib.ATTN_OK

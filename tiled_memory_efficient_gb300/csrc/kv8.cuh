@@ -130,7 +130,8 @@ struct AttnParams {
     // attention over a shared prefix (null: none): the plan, and the rows of sequences that
     // share, over the positions after their prefix
     const int* plan;
-    int least_runs;    // runs that a plan's groups have to save in all
+    int least_runs;    // runs that a plan's groups have to save in all,
+    int least_members; // and sequences that each of them has to have, where the plan leaves the choice
     float* own_o;      // [B, Hq, Nq][D]
     float* own_lse;    // [B, Hq, Nq], log2 domain
     unsigned int* status;
@@ -202,15 +203,17 @@ __device__ __forceinline__ Shares own_shares(const AttnParams& p, int T) {
     return Shares(T, own_workers(p.ctas, p.rows), p.rows <= 16 ? kWarpMinShare : kMinShare);
 }
 
-// What kvp_find_shared leaves: a header (magic, groups, n_seqs, runs that all of them save), then arrays of n_seqs words.  Group g are the
-// sequences members[first[g] .. + count[g]), in ascending order; the first `blocks[g]` runs of
-// kShareBlock positions of all of them lie in the pages of the first one's table row.
+// What kvp_find_shared leaves: a header (magic, groups, n_seqs, runs that all of them save or kPlanAlways), then
+// arrays of n_seqs words.  Group g are the sequences members[first[g] .. + count[g]), in ascending order; the first
+// `blocks[g]` runs of kShareBlock positions of all of them lie in the pages of the first one's table row.
 constexpr int kShareBlock = 128;
-constexpr int kPlanMagic = 0x5a4e0001;
+constexpr int kPlanMagic = 0x5a4e0002;
+constexpr int kPlanAlways = 0x7fffffff;   // a plan that is followed whatever it saves
 struct Plan {
     const int* w;
-    int n;
-    __device__ __forceinline__ Plan(const int* words, int n_seqs) : w(words), n(n_seqs) {}
+    int n, least;   // sequences; members of a group that is followed
+    __device__ __forceinline__ Plan(const int* words, int n_seqs, int least_members)
+        : w(words), n(n_seqs), least(words[3] == kPlanAlways ? 0 : least_members) {}
     // Whether it is a plan for as many sequences at all, and whether it is worth while.
     __device__ __forceinline__ bool ok() const { return w[0] == kPlanMagic && w[2] == n; }
     __device__ __forceinline__ bool ok(int least_runs) const { return ok() && w[3] >= least_runs; }
@@ -218,14 +221,16 @@ struct Plan {
     __device__ __forceinline__ int at(int array, int i) const { return w[4 + array * n + i]; }
     __device__ __forceinline__ int first(int g) const { return min(max(at(0, g), 0), n); }
     __device__ __forceinline__ int count(int g) const { return min(max(at(1, g), 0), n - first(g)); }
-    __device__ __forceinline__ int blocks(int g) const { return max(at(2, g), 0); }
+    __device__ __forceinline__ int blocks(int g) const { return at(1, g) >= least ? max(at(2, g), 0) : 0; }
     __device__ __forceinline__ int member(int i) const { return min(max(at(3, i), 0), n - 1); }
     __device__ __forceinline__ int group(int b) const { return min(at(4, b), n - 1); }   // -1: none
     __device__ __forceinline__ int rank(int b) const { return at(5, b); }
-    // positions that sequence b shares (a multiple of kShareBlock)
-    __device__ __forceinline__ int start(int b) const { return max(at(6, b), 0) & ~(kShareBlock - 1); }
+    // positions that sequence b shares (a multiple of kShareBlock), with how many others and itself
+    __device__ __forceinline__ int start(int b) const {
+        return at(7, b) >= least ? max(at(6, b), 0) & ~(kShareBlock - 1) : 0;
+    }
 };
-constexpr int kPlanArrays = 7, kPlanScratch = 3;
+constexpr int kPlanArrays = 8, kPlanScratch = 3;
 
 // ------------------------------------------------------------------ host
 

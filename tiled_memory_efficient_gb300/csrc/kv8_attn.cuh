@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             len = p.lens[b];
             nq = queries_of(p, granted, b, len);
             if constexpr (SHARED) {
-                const Plan plan(p.plan, p.B);
+                const Plan plan(p.plan, p.B, p.least_members);
                 start = plan.start(b);   // (asked for beside the header)
                 if (!plan.ok(p.least_runs)) start = 0;
             }

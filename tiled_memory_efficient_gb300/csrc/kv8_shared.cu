@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
     // set up and start (it reads nothing of this one's).
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const Plan plan(a.plan, a.B);
+    const Plan plan(a.plan, a.B, a.least_members);
     const Group mine = group_of(a, plan, min(lane, a.B - 1), RB);   // (asked for beside the header)
     const bool granted = step_granted(a);
     if (!plan.ok()) {   // the sequences are then each for itself
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const bool real = row < static_cast<int64_t>(a.B) * a.Hkv * a.rows;
     const int u = real ? static_cast<int>(row / a.rows) : 0;   // (sequence, KV head)
     const int b = u / a.Hkv, h = u - b * a.Hkv, rr = static_cast<int>(row - static_cast<int64_t>(u) * a.rows);
-    const Plan plan(a.plan, a.B);
+    const Plan plan(a.plan, a.B, a.least_members);
     const Group mine = group_of(a, plan, min(lane, a.B - 1), row_block);
     const bool granted = step_granted(a), planned = plan.ok(a.least_runs);
     // own positions: the tiles of all sequences, and of those before b
@@ -1030,7 +1030,11 @@ __global__ void __launch_bounds__(kFindThreads) kvp_leader_kernel(const FindPara
 
 // The plan, one CTA: groups of two or more that save enough, in the order of their first sequences.
 constexpr int kPlanThreads = 1024;
-// Of a plan that leaves the choice to the attention: what a group saves, in positions.
+// Of a plan that leaves the choice to the attention: what a group saves, in positions.  (It is made before the heads are
+// known, and takes out what does not matter: beside 64 sequences under 8192 positions, 16 groups of 8 under 512, 1024 and
+// 2048 more left for themselves and read once, us: 14:2 heads of 64 29.4 and 29.0, 31.0 and 29.7, 34.9 and 31.7;
+// 32:8 of 128 65 and 63, 79 and 69, 110 and 83.  Of 4 under 1024, 2048 and 4096: 29.4 and 28.8, 31.4 and 30.1,
+// 35.3 and 36.7; 61 and 59, 76 and 73, 112 and 99.)
 constexpr int kGroupMinSaved = 8192;
 __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams p) {
     __shared__ int s_leader[kMaxBatch], s_count[kMaxBatch], s_group[kMaxBatch], s_off[kMaxBatch];
@@ -1089,11 +1093,12 @@ __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams
         put(4, b, mine);
         put(5, b, rank);
         put(6, b, mine >= 0 ? depth * kShareBlock : 0);
+        put(7, b, mine >= 0 ? s_count[leader] : 0);
     }
     if (b == 0) {
         p.plan[1] = groups;
         p.plan[2] = p.B;
-        p.plan[3] = p.min_saved < 0 ? static_cast<int>(min(s_saved, 0x7ffffffeull)) : 0x7fffffff;   // by hand: always
+        p.plan[3] = p.min_saved < 0 ? static_cast<int>(min(s_saved, 0x7ffffffeull)) : kPlanAlways;
         p.plan[0] = kPlanMagic;
     }
 }
@@ -1105,6 +1110,14 @@ __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams
 // shared positions, 8 KV heads of 128 (133 MB) 34 and 38, of 1024 (266 MB) 48 and 39; 32 sequences of 2048
 // (130 MB) 26 and 25; 128 sequences of 2048, 2 KV heads of 64 (67 MB) 21 and 23, of 4096 (133 MB) 29 and 24.
 constexpr int64_t kWorthBytes = 128ll << 20;
+// And the sequences that a group has to have there.  A run of 128 positions of a KV head takes an SM about 1.9 us
+// here, for two rows as for 256, and each sequence for itself 0.3 to 0.4 us (D = 64, up to 16 rows, in part from L2) or
+// 0.6 to 0.8 (D = 128).  Groups under 16384 positions, for themselves and read once, us: 14:2 heads of 64, 12 of 4 35 and
+// 49, 8 of 6 35 and 39, 6 of 8 35 and 35, two queries 9 of 5 43 and 45, 8 of 6 45 and 43; 32:8 of 128, 24 of 2 254 and
+// 323, 16 of 3 250 and 225, four queries 256 and 334, 256 and 235.  With more rows each sequence for itself
+// takes longer, most of all beside short ones (five queries, 16 groups of 2 beside 64 sequences with 200 positions of
+// their own: 14:2 of 64 453 and 106, 32:8 of 128 1449 and 344): any group is followed.
+int least_members(int D, int64_t rows) { return rows > 16 ? 2 : D == 128 ? 3 : rows > 8 ? 6 : 8; }
 
 // Rows of a CTA of the prefix kernel: one Q tile where all the batch's rows of a KV head fit it.
 int prefix_tiles(int B, int64_t rows) { return B * rows <= kPreRows ? 1 : 2; }
@@ -1218,6 +1231,7 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     p.a.plan = plan;
     const int64_t run_bytes = 2ll * Hkv * D * kShareBlock, least = (kWorthBytes + run_bytes - 1) / run_bytes;
     p.a.least_runs = static_cast<int>(least);
+    p.a.least_members = least_members(D, rows);
     p.a.own_o = take(z.own_o);
     p.a.own_lse = take(z.own_lse);
     p.row_o = take(z.row_o);
