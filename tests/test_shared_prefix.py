@@ -790,3 +790,41 @@ def test_groups_too_small_to_follow(cuda_lib, Hq, Hkv, D, Nq, members, followed)
     own = _lib.kv8_attn_shared(q, *cache, _lib.kvp_find_shared(cache[4], cache[5], page))
     helpers.assert_fwd_close(*(x.double().cpu().numpy() for x in (*own, *_lib.kv8_attn(q, *cache))), BF16, "small groups alone")
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,Nq,D,page,dtype", [(20, 1, 1, 64, 16, F16), (8, 1, 5, 64, 64, BF16), (8, 2, 6, 128, 32, F16),
+                                                    (34, 2, 1, 128, 128, BF16), (6, 2, 23, 64, 32, F16)])
+def test_short_ends_of_many_rows(cuda_lib, Hq, Hkv, Nq, D, page, dtype):
+    """More than 16 rows a KV head: runs of short ends beside long sequences that share nothing, where a CTA's share begins,
+    ends and lies inside the steps that a unit starts with; empty sequences first, last and between."""
+    for seed, (tails, alone) in enumerate(([[1, 33, 0, 64, 129], [0, 5, 0, 3000, 2500]], [[0] * 9 + [700], [0, 0, 0]],
+                                           [[1], [4100]], [[31, 0, 0, 0, 200], [17, 1900, 0, 40]])):
+        cache = _batch([(256, 30), (128, 11)], tails, alone, Hkv, D, page, seed=seed + Nq)
+        B = cache[5].numel()
+        q = torch.randn(B, Hq, Nq, D, generator=torch.Generator().manual_seed(seed)).to(dtype)
+        n_new = [min(Nq, int(n)) for n in cache[5]]
+        dev = [t.cuda() for t in cache]
+        plan = _lib.kvp_find_shared(dev[4], dev[5], page, 0)
+        out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new))
+        assert _lib.sync_status() == _lib.ATTN_OK
+        _check(q, cache, n_new, out, lse, f"short ends, many rows {seed} D={D}")
+        again = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new))
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.gpu
+def test_the_largest_batch_of_many_rows(cuda_lib):
+    """1024 sequences of 24 rows: the count of sequences before and the queries share a word."""
+    cache = _batch([(128, 700), (256, 200)], [0, 5, 40], [30, 0, 200, 0] * 31, 1, 64, 128, seed=23)
+    q = torch.randn(1024, 8, 3, 64, generator=torch.Generator().manual_seed(4)).to(F16)
+    dev = [t.cuda() for t in cache]
+    n_new = [min(3, int(n)) for n in cache[5]]
+    plan = _lib.kvp_find_shared(dev[4], dev[5], 128, 0)
+    out, lse = _lib.kv8_attn_shared(q.cuda(), *dev, plan, n_new=_i32(n_new))
+    assert _lib.sync_status() == _lib.ATTN_OK
+    _check(q, cache, n_new, out, lse, "shared, 1024 sequences of many rows", some=range(0, 1024, 41))
+    a, b = _lib.kv8_attn(q.cuda(), *dev, n_new=_i32(n_new))
+    for i, n in enumerate(n_new):
+        if n:
+            helpers.assert_fwd_close(*(x[i, :, :n].double().cpu().numpy() for x in (out, lse, a, b)), F16, "shared against plain")

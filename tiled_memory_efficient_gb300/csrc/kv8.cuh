@@ -195,9 +195,12 @@ struct Shares {
 // Its units (a sequence's tiles of one KV head) begin with kOwnSteps steps beside their tiles: the queries
 // and the rows of the unit before take about as long, and a short sequence brings a run of such units
 // (128 sequences with 1 to 1000 positions of their own, 8 KV heads of 128: the whole call 87 us, 94.7
-// with equal tiles; 1 step 89.6, 2 to 4 alike).
-constexpr int kAttnWarps = 8, kWarpMinShare = 2, kOwnSteps = 3;
-inline __host__ __device__ int own_steps(int rows) { return rows <= 16 ? kOwnSteps : 0; }
+// with equal tiles; 1 step 89.6, 2 to 4 alike).  With more than 16 rows a CTA's eight warps end a unit
+// together, which takes as long as some 32 tiles: 64 sequences of 20 to 1000 positions behind 8192, five queries, 32:8
+// heads of 128, the whole call 125 us, 225 with equal tiles; with 200 positions each beside 32 sequences of 16384
+// that share nothing 369 and 1341 (kv8_attn 563), 14:2 of 64 142 and 456 (203); 16 steps 495 and 170, 64 394 and 152.
+constexpr int kAttnWarps = 8, kWarpMinShare = 2, kOwnSteps = 3, kOwnStepsCta = 32;
+inline __host__ __device__ int own_steps(int rows) { return rows <= 16 ? kOwnSteps : kOwnStepsCta; }
 inline __host__ __device__ int own_workers(int ctas, int rows) { return rows <= 16 ? ctas * kAttnWarps : ctas; }
 __device__ __forceinline__ Shares own_shares(const AttnParams& p, int T) {
     return Shares(T, own_workers(p.ctas, p.rows), p.rows <= 16 ? kWarpMinShare : kMinShare);

@@ -166,14 +166,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * ST;   // this warp's slots
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff) + warp;
     int* s_warp = reinterpret_cast<int*>(smem + C::kMiscOff + 4 * kWarps);   // [kWarps]
-    int* s_held = reinterpret_cast<int*>(smem + C::kLseOff);          // ALONE (it has no use for s_lse): [kWarps]
+    int* s_held = reinterpret_cast<int*>(smem + C::kLseOff);          // SHARED (before s_lse is used): [kWarps]
     int* s_pre = reinterpret_cast<int*>(smem + C::kPreOff);           // [B + 1] tiles before
     int* s_len = s_pre + p.B + 1;                                     // [B]
     int* s_nq = s_len + p.B;                                          // [B] queries
     int* s_start = s_nq + p.B;                                        // SHARED: [B] positions of the prefix
     auto start_of = [&](int b_) { return SHARED ? s_start[b_] : 0; };
-    // ALONE (up to 16 queries): beside them how many sequences before hold tiles
-    auto queries = [&](int b_) { return ALONE ? (s_nq[b_] & 255) - 1 : s_nq[b_]; };
+    // SHARED (up to 2^20 queries, 1024 sequences): beside them how many sequences before hold tiles
+    constexpr int kNqBits = 21;
+    static_assert(kMaxBatch <= 1 << (31 - kNqBits), "a word holds both");
+    auto queries = [&](int b_) { return SHARED ? (s_nq[b_] & ((1 << kNqBits) - 1)) - 1 : s_nq[b_]; };
 
     if (lane == 0) {
         // a slot's phase: its copies' bytes, and its lane's small copies
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     // exclusive prefix sums of the sequences' tile counts
     const bool granted = step_granted(p);
-    int carry = 0, held = 0;   // tiles, ALONE: sequences with any
+    int carry = 0, held = 0;   // tiles, SHARED: sequences with any
     for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
         int len = 0, nq = 0, start = 0;
@@ -215,8 +217,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (lane >= d) x += y;
         }
         if (lane == 31) s_warp[warp] = x;
-        int z = 0;   // ALONE: sequences before in the turn that hold tiles
-        if constexpr (ALONE) {
+        int z = 0;   // SHARED: sequences before in the turn that hold tiles
+        if constexpr (SHARED) {
             const unsigned any = __ballot_sync(0xffffffffu, n > 0);
             z = __popc(any & ((1u << lane) - 1u));
             if (lane == 0) s_held[warp] = __popc(any);
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (i < warp) before += s_warp[i];
             all += s_warp[i];
         }
-        if constexpr (ALONE) {
+        if constexpr (SHARED) {
             z += held;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (b < p.B) {
             s_pre[b] = before + x - n;
             s_len[b] = len;
-            s_nq[b] = ALONE ? (nq + 1) | (z << 8) : nq;
+            s_nq[b] = SHARED ? (nq + 1) | (z << kNqBits) : nq;
             if constexpr (SHARED) s_start[b] = start;
         }
         carry = all;
@@ -248,27 +250,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (threadIdx.x == 0) s_pre[p.B] = carry;
     __syncthreads();
     const int U = p.Hkv * p.n_rb;
-    const Shares sh = ALONE ? own_shares(p, (carry + kOwnSteps * held) * U) : Shares(carry * U, p.ctas);
+    constexpr int K = ALONE ? kOwnSteps : kOwnStepsCta;   // SHARED: a unit's steps beside its tiles
+    const Shares sh = SHARED ? own_shares(p, (carry + K * held) * U) : Shares(carry * U, p.ctas);
     // (consecutive shares of warps on different SMs)
     const int c = static_cast<int>(blockIdx.x) + (ALONE ? warp * p.ctas : 0);
-    // ALONE: the tile that step x of the concatenated units leads to; its sequence, KV head and place in its
+    // SHARED: the tile that step x of the concatenated units leads to; its sequence, KV head and place in its
     // list.  Two probes a lane (at most 1024 sequences).
     auto tile_at = [&](int x, int* b_, int* u_, int* v_) {
-        auto steps = [&](int i) { return (s_pre[i] + kOwnSteps * (s_nq[i] >> 8)) * U; };
+        auto steps = [&](int i) { return (s_pre[i] + K * (s_nq[i] >> kNqBits)) * U; };
         const int gap = (p.B + 31) >> 5, i = lane * gap;
         const int base = (__popc(__ballot_sync(0xffffffffu, i < p.B && steps(min(i, p.B - 1)) <= x)) - 1) * gap;
         const int k = base + lane;
         *b_ = base - 1 +
               __popc(__ballot_sync(0xffffffffu, lane < gap && k < p.B && steps(min(k, p.B - 1)) <= x));
         const int n = s_pre[*b_ + 1] - s_pre[*b_], off = x - steps(*b_);
-        *u_ = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(n + kOwnSteps));
-        *v_ = max(off - *u_ * (n + kOwnSteps) - kOwnSteps, 0);
+        *u_ = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(n + K));
+        *v_ = max(off - *u_ * (n + K) - K, 0);
         return s_pre[*b_] * U + *u_ * n + *v_;
     };
     int g0 = 0, g1 = 0, b = 0, u = 0, v_first = 0;
     if (c < sh.n) {
         g0 = sh.begin(c), g1 = sh.begin(c + 1);
-        if constexpr (ALONE) {
+        if constexpr (SHARED) {
             int b1, u1, v1;
             g1 = c + 1 < sh.n ? tile_at(g1, &b1, &u1, &v1) : carry * U;
             g0 = tile_at(g0, &b, &u, &v_first);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // largest exactly.  They stay in registers, or (kQSmem) warp w prepares the 8
     // rows w and leaves them in shared memory as [row tile][word pair][lane], and
     // the factors behind them.
-    if constexpr (!ALONE) {
+    if constexpr (!SHARED) {
         // the last sequence that starts at or before g0: not an empty one
         for (int hi = p.B - 1; b < hi;) {
             const int mid = (b + hi + 1) >> 1;

@@ -1114,9 +1114,8 @@ constexpr int64_t kWorthBytes = 128ll << 20;
 // here, for two rows as for 256, and each sequence for itself 0.3 to 0.4 us (D = 64, up to 16 rows, in part from L2) or
 // 0.6 to 0.8 (D = 128).  Groups under 16384 positions, for themselves and read once, us: 14:2 heads of 64, 12 of 4 35 and
 // 49, 8 of 6 35 and 39, 6 of 8 35 and 35, two queries 9 of 5 43 and 45, 8 of 6 45 and 43; 32:8 of 128, 24 of 2 254 and
-// 323, 16 of 3 250 and 225, four queries 256 and 334, 256 and 235.  With more rows each sequence for itself
-// takes longer, most of all beside short ones (five queries, 16 groups of 2 beside 64 sequences with 200 positions of
-// their own: 14:2 of 64 453 and 106, 32:8 of 128 1449 and 344): any group is followed.
+// 323, 16 of 3 250 and 225, four queries 256 and 334, 256 and 235.  With more rows each sequence for itself takes
+// longer: five queries, 48 of 2 283 and 170, 790 and 683 (three, 14:2 heads of 64, 149 and 157): any group is followed.
 int least_members(int D, int64_t rows) { return rows > 16 ? 2 : D == 128 ? 3 : rows > 8 ? 6 : 8; }
 
 // Rows of a CTA of the prefix kernel: one Q tile where all the batch's rows of a KV head fit it.
@@ -1212,7 +1211,8 @@ extern "C" int kv8_attn_shared(const void* q, const void* k_pages, const void* v
     const int qt = prefix_tiles(B, rows), row_block = qt * kPreRows;
     // steps of all groups, and rows, are counted in 32 bits; B / 2 groups at most
     const int64_t blocks = (static_cast<int64_t>(B) * rows + row_block - 1) / row_block + B / 2;
-    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(max_pages) * page + 31) / 32 + kOwnSteps) > 0x7fffffffll)
+    if (static_cast<int64_t>(B) * Hkv * ((rows + 31) / 32) *
+            ((static_cast<int64_t>(max_pages) * page + 31) / 32 + own_steps(p.a.rows)) > 0x7fffffffll)
         return ATTN_ERR_UNSUPPORTED;
     const int64_t unit = static_cast<int64_t>(max_pages) * page / kShareBlock + kUnitSteps + 1;
     if (rows > 1 << 20 || static_cast<int64_t>(B) * Hq * Nq > 0x7fffffffll || blocks * Hkv * unit > 0x7fffffffll ||
