@@ -828,3 +828,33 @@ def test_the_largest_batch_of_many_rows(cuda_lib):
     for i, n in enumerate(n_new):
         if n:
             helpers.assert_fwd_close(*(x[i, :, :n].double().cpu().numpy() for x in (out, lse, a, b)), F16, "shared against plain")
+
+
+@pytest.mark.gpu
+def test_a_cache_too_small_to_share(cuda_lib):
+    """Where no plan can be followed, attention is the plain one and a fork looks for no prefixes; a number of positions
+    asks for them all the same, and so does a larger table."""
+    S, Hkv, D, page = 8, 2, 64, 32
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn(S, Hkv, 520, D, generator=g).to(F16).cuda()
+    q = torch.randn(S, 4, 1, D, generator=g).to(F16).cuda()
+    per_page = (S - 1) * page * 2 * Hkv * D
+    for max_pages, least, shares in ((20, -1, False), (20, 0, True), (-(-(128 << 20) // per_page), -1, True),
+                                     (-(-(128 << 20) // per_page) - 1, -1, False)):
+        cache = PagedKVCache(1, S, Hkv, D, n_pages=200, page_size=page, max_pages=max_pages, share=True, min_saved=least)
+        n = _i32([512] + [0] * (S - 1))
+        cache.reserve(n)
+        cache.append(0, k, k, n)
+        cache.reassign(_i32([0] * S))
+        assert len(_read_plan(cache.plan, S)) == (1 if least == 0 else 0)   # (7 * 512 positions are too few by itself)
+        cache.plan.fill_(7)                    # no plan: a call that reads it says so
+        cache.reserve(3)
+        cache.append(0, k[:, :, 512:515].contiguous(), k[:, :, 512:515].contiguous())
+        out, lse = cache.attend(0, q)
+        assert _lib.sync_status() == (_lib.ATTN_ERR_PAGE if shares else _lib.ATTN_OK)
+        pools = [t[0] for t in (cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale)] + [cache.table, cache.lens]
+        want = _lib.kv8_attn(q, *pools)
+        if not shares:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        cache.find_shared()
+        assert _lib.sync_status() == _lib.ATTN_OK and cache.plan[0] != 7

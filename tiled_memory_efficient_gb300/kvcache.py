@@ -43,6 +43,9 @@ __all__ = ["PagedKVCache"]
 # 16384 positions are shared and 45.5 with every sequence for itself; 11.8 and 10.9 where it is 256.)
 _SHARED_BYTES = 4 << 30
 _SHARED_ROWS = 1 << 20
+# What prefixes have to save in keys and values before attention with a plan that leaves the choice follows it.  (8 beams
+# under 4096 positions, 14:2 heads, D = 64: 13.3 us with a plan that is not followed, 12 by kv8_attn.)
+_WORTH_BYTES = 128 << 20
 
 
 class PagedKVCache:
@@ -57,6 +60,8 @@ class PagedKVCache:
     each group).  Whoever writes `table` by hand calls ``find_shared`` afterwards.  Such an ``attend``
     asks for 8 bytes of workspace per value of q, and for parts of up to 40 MB beside; with
     over 4 GB of them, or more than 2^20 queries a KV head (its query heads'), it reads every sequence for itself.
+    So does a cache that can never save 128 MB: n_seqs - 1 tables of max_pages pages hold less (give max_pages, where
+    sequences cannot take the whole pool), and min_saved is -1.
     """
 
     def __init__(self, n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, n_pages: int,
@@ -95,6 +100,9 @@ class PagedKVCache:
         self.plan = None   # which sequences share a prefix
         if share:
             self.min_saved = min_saved
+            # whether a plan of this cache can ever be followed
+            self._worth = min_saved >= 0 or \
+                (n_seqs - 1) * max_pages * page_size * 2 * n_kv_heads * head_dim >= _WORTH_BYTES
             self.plan = _lib.kvp_find_shared(self.table, self.lens, page_size, min_saved)
 
     def _counts(self, n):
@@ -128,7 +136,7 @@ class PagedKVCache:
         of a step that found no room) get 0 and -inf.  None: all Nq rows are the
         newest positions; with a window no more than the sequence's last ``reserve``
         made room for, since older queries want pages that it gave back."""
-        if self.plan is not None and not self._too_many(q):
+        if self.plan is not None and self._worth and not self._too_many(q):
             return _lib.kv8_attn_shared(q, self.k_pages[layer], self.v_pages[layer], self.k_scale[layer],
                                         self.v_scale[layer], self.table, self.lens, self.plan, scale=scale,
                                         n_new=None if n_new is None else self._counts(n_new),
@@ -150,7 +158,7 @@ class PagedKVCache:
         _lib.kvp_reassign(self.table, self.lens, self.refs, parents, self.page_size, self._src,
                           self._dst, self.info, workspace=self._ws)
         self._copy(self.table.shape[0])
-        if self.plan is not None:
+        if self.plan is not None and self._worth:
             self.find_shared()
 
     def find_shared(self):
