@@ -133,10 +133,12 @@ size_t kv8_attn_workspace_size(int B, int Hq, int Hkv, int Nq, int D);
  * (kvp_plan_words(n_seqs) int32 on the device) for kv8_attn_shared.  Sequences whose
  * first pages are the same, in whole runs of 128 positions, form a group; where some of
  * them share more than the others, each joins the group that leaves it the least to
- * read.  A group is kept when reading its prefix once saves min_saved
- * positions or more (members less one, times the prefix).  min_saved -1 leaves it to the attention, which
- * follows the plan where its groups save 128 MB of keys and values in all, and otherwise
- * reads every sequence for itself.  table [n_seqs, max_pages] and lens are not changed.  n_seqs <= 1024.
+ * read.  A group is kept when reading its prefix once saves min_saved positions or more
+ * (members less one, times the prefix), and the attention follows all that are kept.  min_saved -1
+ * keeps those that save 8192, and leaves the rest to the attention: it follows the plan where its groups save
+ * 128 MB of keys and values in all, and of these the ones with enough members for the call's rows (D = 64: 8, 6 with
+ * 9 to 16 query rows of a KV head; D = 128: 3; any with more rows); other sequences read for
+ * themselves.  table [n_seqs, max_pages] and lens are not changed.  n_seqs <= 1024.
  *
  * The plan stays right while every sequence keeps the pages it begins with: appends, kvp_reserve
  * without a window and kvp_compact keep them; after kvp_reassign it is made anew.  (Work
@@ -162,7 +164,8 @@ size_t kvp_plan_words(int n_seqs);
  * smaller ones' values lose bits that stand 2^-33 below the larger's magnitude.  A
  * NaN or infinity in a value of the prefix reaches all rows of the group's
  * sequences, those before its position too.
- * workspace: kv8_attn_shared_workspace_size() bytes.
+ * workspace: kv8_attn_shared_workspace_size() bytes: all rows in fp32 twice (8 bytes per value of q), whether they
+ * share or not, and up to 40 MB of parts.
  */
 int kv8_attn_shared(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                     const float* v_scale, const int* table, const int* lens, const int* n_new,

@@ -35,7 +35,8 @@ extern "C" {
  * strides (host): 14 element counts, the batch, head and row strides of q, k, q_out and
  * k_out, then ps_b and ps_n; those of the 16-bit tensors are multiples of 8 and their pointers
  * 16-byte aligned.  Rows are dense.  A result may be its input (the same pointer and
- * strides); any other overlap is the caller's mistake.
+ * strides); any other overlap is the caller's mistake.  Up to 2^27 tokens (B N) and 65535 heads (Hq + Hk);
+ * positions counted from start end below 2^31.
  */
 int rope_apply(const void* q, const void* k, void* q_out, void* k_out,
                const unsigned long long* turns, const int* positions, int start, int B, int Hq,
@@ -53,7 +54,7 @@ int rope_apply(const void* q, const void* k, void* q_out, void* k_out,
  * count does not fit or of a step without room, become 0.
  *
  * strides (host): batch, head and row strides of k and v (both), of q and of q_out.  T and the
- * positions of a table row together stay below 2^31.
+ * positions of a table row together stay below 2^31; with q, up to 2^27 tokens (B T) and 65535 query heads.
  */
 int kv8_append_rope(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scale,
                     float* v_scale, const int* table, const int* lens, const int* n_new,

@@ -54,14 +54,18 @@ class PagedKVCache:
     page_size is 16, 32, 64 or 128 tokens; max_pages (default: all n_pages) the
     most pages one sequence can hold.  With window > 0 queries see the last
     `window` positions and the first `sinks`, and ``reserve`` gives back pages
-    the window has left behind.  share (without a window): ``reassign`` looks which
-    sequences begin with the same pages, and ``attend`` reads those once for all of
-    them where that saves enough (128 MB of keys and values; or min_saved positions, for
-    each group).  Whoever writes `table` by hand calls ``find_shared`` afterwards.  Such an ``attend``
-    asks for 8 bytes of workspace per value of q, and for parts of up to 40 MB beside; with
-    over 4 GB of them, or more than 2^20 queries a KV head (its query heads'), it reads every sequence for itself.
-    So does a cache that can never save 128 MB: n_seqs - 1 tables of max_pages pages hold less (give max_pages, where
-    sequences cannot take the whole pool), and min_saved is -1.
+    the window has left behind.
+
+    share (without a window): ``reassign`` looks which sequences begin with the same
+    pages, and ``attend`` reads those once for all of them where that saves enough (128 MB of
+    keys and values, in groups of enough sequences (include/kvcache.h); or min_saved
+    positions, for each group).  A NaN or infinity among a prefix's values then reaches every
+    query of the sequences that share it, those before its position too.  Whoever writes `table`
+    by hand calls ``find_shared`` afterwards.  Such an ``attend`` asks for 8 bytes of workspace per
+    value of q, and for parts of up to 40 MB beside; with over 4 GB of them, or more than 2^20
+    queries a KV head (its query heads'), it reads every sequence for itself.  So does a
+    cache that can never save 128 MB: n_seqs - 1 tables of max_pages pages hold less (give
+    max_pages, where sequences cannot take the whole pool), and min_saved is -1.
     """
 
     def __init__(self, n_layers: int, n_seqs: int, n_kv_heads: int, head_dim: int, n_pages: int,
