@@ -224,13 +224,14 @@ struct Plan {
     __device__ __forceinline__ int at(int array, int i) const { return w[4 + array * n + i]; }
     __device__ __forceinline__ int first(int g) const { return min(max(at(0, g), 0), n); }
     __device__ __forceinline__ int count(int g) const { return min(max(at(1, g), 0), n - first(g)); }
-    __device__ __forceinline__ int blocks(int g) const { return at(1, g) >= least ? max(at(2, g), 0) : 0; }
+    // (masks, no branches: a load behind one would wait for what decides it)
+    __device__ __forceinline__ int blocks(int g) const { return max(at(2, g), 0) & -static_cast<int>(at(1, g) >= least); }
     __device__ __forceinline__ int member(int i) const { return min(max(at(3, i), 0), n - 1); }
     __device__ __forceinline__ int group(int b) const { return min(at(4, b), n - 1); }   // -1: none
     __device__ __forceinline__ int rank(int b) const { return at(5, b); }
     // positions that sequence b shares (a multiple of kShareBlock), with how many others and itself
     __device__ __forceinline__ int start(int b) const {
-        return at(7, b) >= least ? max(at(6, b), 0) & ~(kShareBlock - 1) : 0;
+        return max(at(6, b), 0) & ~(kShareBlock - 1) & -static_cast<int>(at(7, b) >= least);
     }
 };
 constexpr int kPlanArrays = 8, kPlanScratch = 3;
