@@ -216,8 +216,9 @@ __device__ __forceinline__ uint4 lds128v(uint32_t a) {
 //   then 1 warp           producer: page ids, scales, bulk copies
 // Bound by a tile's chain, scores, softmax, product, of which two are in flight: at D = 128 3750 cycles a step of
 // 128 keys and 256 rows, where the products take 2048 (D = 64: 3300 and 1024), and by both ends of a part: 6 to 9
-// us until the first scores, 3 to 4 for its rows.  128 sequences, 32:8 heads, D = 128 under 16K positions 38 us,
-// the tensor pipe 32% and issue slots 42% busy; 64 samples, 14:2 heads, D = 64 under 32K 17 to 20 us.  Two Q
+// us until the first scores, 3 to 4 for its rows.  128 sequences, 32:8 heads, D = 128 under 16K positions 42 us behind
+// the call before (46 by itself, the tensor pipe 30% and issue slots 42% busy); 64 samples, 14:2 heads, D = 64 under
+// 32K 20 us (24, 15% and 35%).  Two Q
 // tiles a CTA (QT) take those 51.5 us instead of 62.5 with one, and 25 instead of 29, in an earlier state of both.
 template <int D, bool BF16, int QT>
 __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(PreCfg<D, QT>::kThreads, 1)
 // A warp per row, or (WPR) a CTA's four: the row's results over the prefix and over its own positions, each
 // whole or in the parts that several CTAs left.  Rows of sequences that share nothing and lie in
 // one CTA are written already.  It finds its parts beside the kernels before it; behind them a row is two trips to
-// memory: 2.5 us for 896 rows of some 40 parts, 5 for 4096 rows of 10 (22 MB from L2).
+// memory: 4 to 6 us for 896 rows of some 40 parts, 13 for 4096 rows of 10 (25 MB), whose last CTAs find room late.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRowsAlone = 8;   // rows per SM up to which a CTA takes one
 
@@ -1109,6 +1110,8 @@ __global__ void __launch_bounds__(kPlanThreads) kvp_plan_kernel(const FindParams
 // that to the attention.  Every sequence for itself against the prefixes once, us: 128 sequences of 512
 // shared positions, 8 KV heads of 128 (133 MB) 34 and 38, of 1024 (266 MB) 48 and 39; 32 sequences of 2048
 // (130 MB) 26 and 25; 128 sequences of 2048, 2 KV heads of 64 (67 MB) 21 and 23, of 4096 (133 MB) 29 and 24.
+// (With many rows less is worth while: 16 sequences with 64 queries behind 4096 positions, 32:8 heads of 128, 126 MB, 413
+// and 186, behind 256, 8 MB, 122 and 131; there a plan made with a number of positions asks for it.)
 constexpr int64_t kWorthBytes = 128ll << 20;
 // And the sequences that a group has to have there.  A run of 128 positions of a KV head takes an SM about 1.9 us
 // here, for two rows as for 256, and each sequence for itself 0.3 to 0.4 us (D = 64, up to 16 rows, in part from L2) or

@@ -39,8 +39,8 @@ from . import _lib
 __all__ = ["PagedKVCache"]
 
 # Attention over a shared prefix keeps all query rows in fp32 twice, and takes 2^20 rows a KV head.  A call whose
-# rows would take more is kv8_attn's.  (16 sequences of 2048 queries, 32:8 heads, D = 128, 1.1 GB: 18.3 ms where
-# 16384 positions are shared and 45.5 with every sequence for itself; 11.8 and 10.9 where it is 256.)
+# rows would take more is kv8_attn's.  (16 sequences of 2048 queries, 32:8 heads, D = 128, 1.1 GB: 17.0 ms where
+# 16384 positions are shared and 45.5 with every sequence for itself; 10.4 and 10.9 where it is 256.)
 _SHARED_BYTES = 4 << 30
 _SHARED_ROWS = 1 << 20
 # What prefixes have to save in keys and values before attention with a plan that leaves the choice follows it.  (8 beams
