@@ -485,3 +485,39 @@ def test_results_that_overlap_are_refused(cuda_lib):
     assert not cache.k_pages.view(torch.uint8).any()
     assert torch.equal(_lib.kv8_append(k, k, *pools, cache.table, cache.lens, rope=rope, q=q, q_out=spare), want[0])
     assert _lib.sync_status() == _lib.ATTN_OK
+
+
+def test_a_first_use_inside_a_function_transform_is_refused():
+    """What is made there ends with the transform: it is not kept, and the rotation goes on working."""
+    from torch._subclasses import FakeTensorMode
+    rope = Rope(64)
+
+    def f(x):
+        rope.turns("cpu")
+        return x.sum()
+    with pytest.raises(RuntimeError, match="function transform"):
+        torch.func.grad(f)(torch.ones(3))
+    with FakeTensorMode(), pytest.raises(RuntimeError, match="function transform"):
+        rope.turns("cpu")
+    words = rope.turns("cpu")
+    assert type(words) is torch.Tensor and words.data_ptr() and torch.equal(words, Rope(64).turns("cpu"))
+    assert torch.equal(torch.func.grad(f)(torch.ones(3)), torch.ones(3))
+
+
+@pytest.mark.gpu
+def test_function_transforms_are_refused(cuda_lib):
+    """torch.func's transforms raise, whether they come first or not, and leave the rotation as it was."""
+    q = _rows((1, 2, 5, 64), F16, 1)
+    want = Rope(64)(q)
+    for used in (False, True):
+        rope = Rope(64)
+        if used:
+            rope(q)
+        for transform in (lambda: torch.func.grad(lambda x: rope(x).float().sum())(q), lambda: torch.func.vjp(rope, q),
+                          lambda: torch.func.jvp(rope, (q,), (q,)), lambda: torch.func.vmap(lambda x: rope(x[None])[0])(q)):
+            with pytest.raises(RuntimeError):
+                transform()
+        leaf = q.clone().requires_grad_(True)
+        y = rope(leaf)
+        assert torch.equal(y.detach(), want) and torch.autograd.grad(y, leaf, q)[0].shape == q.shape
+    assert _lib.sync_status() == _lib.ATTN_OK

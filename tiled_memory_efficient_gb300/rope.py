@@ -131,6 +131,13 @@ class Rope:
                 raise RuntimeError("a rotation's first use on a device cannot be captured: call turns(device) before")
             with torch.inference_mode(False):   # kept for training, too: a backward pass saves it
                 t = torch.tensor(self._words, dtype=torch.int64, device=device)
+            try:   # inside a function transform it is a wrapper that ends with it: not to be kept
+                plain = type(t) is torch.Tensor and t.data_ptr() != 0
+            except RuntimeError:
+                plain = False
+            if not plain:
+                raise RuntimeError("a rotation's first use on a device cannot be inside a function transform: call "
+                                   "turns(device) before")
             self._turns[index] = (t, self.rotary_dim, self.interleaved, self.amplitude, self.head_dim)
         return self._turns[index][0]
 
